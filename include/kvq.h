@@ -60,7 +60,8 @@ enum {
     KVQ_DEV_BAD_PAGE = 2u,   /* a position past the page table, or a page id outside
                                 the pool                                               */
     KVQ_DEV_TIMEOUT = 4u,    /* a bounded device wait expired                          */
-    KVQ_DEV_BAD_FORMAT = 8u  /* a per-sequence format the kernel in use cannot read    */
+    KVQ_DEV_BAD_FORMAT = 8u, /* a per-sequence format the kernel in use cannot read    */
+    KVQ_DEV_NO_PAGE = 16u    /* kvq_resize_pages: no free page, or no room in a table  */
 };
 
 typedef enum kvq_format {
@@ -71,7 +72,7 @@ typedef enum kvq_format {
     KVQ_FMT_TQ3 = 5          /* rotated tier, 3-bit codes (8 levels) + fp32 radius      */
 } kvq_format;
 
-/* element type of a projection weight matrix */
+/* element type of a projection weight matrix, and of the rows that kvq_append_mla takes */
 typedef enum kvq_weight_type {
     KVQ_WEIGHT_F32 = 0,      /* fp32                                                   */
     KVQ_WEIGHT_BF16 = 1      /* bfloat16 (the upper half of an fp32 pattern; widened
@@ -416,6 +417,159 @@ int kvq_mla_decode(const kvq_mla_problem* p, float* out, float* lse, void* works
  */
 int kvq_mla_decode_noalloc(const kvq_mla_problem* p, float* out, float* lse,
                            uint32_t* dev_status, kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Serving drafted tokens over a paged MLA cache.  One step of a speculative decode is
+ *     kvq_resize_pages (pages and pool rows for the drafted tokens), kvq_append_mla (their
+ *     rows), kvq_mla_tree_decode (attention of the drafted tree), and after the
+ *     verification kvq_accept_mla (the accepted path moves to the front of the draft) and,
+ *     with the next step's lengths, kvq_resize_pages again.
+ * Every quantity that varies from step to step (lengths, counts, masks, paths) is read
+ * from device memory, so a captured graph of the step can be replayed.
+ * ------------------------------------------------------------------------------------ */
+
+/*
+ * Block tables and the slot map of a step, from the sequences' lengths.  Sequence s holds
+ * n_held[s] pages (block_table[s][0 .. n_held[s] - 1]); it keeps its first keep_len[s] rows and
+ * gains n_new[s] rows, for which it needs ceil((keep_len[s] + n_new[s]) / page_size) pages.
+ *   1. Pages beyond the need go back to the free list (a stack, free_list[0 .. *n_free - 1]), the
+ *      last sequence's last page first; their table entries become -1.
+ *   2. Missing pages are popped from the top of the list (those just returned included), in
+ *      sequence order, first page first.  A sequence whose pages the list cannot all supply
+ *      is refused, and so is every later one that needs a page.
+ * Resizing back to the former need undoes a step: list and tables are as they were.
+ *   seq_len[s]   keep_len[s] + n_new[s]; a refused sequence min(keep_len[s], n_held[s] * page_size)
+ *   tok_start    [n_seq + 1] prefix sums of n_new: the new tokens' packed order (values past
+ *                INT32_MAX are stored as INT32_MAX)
+ *   slot_map[i]  pool row of packed token i; -1 for the tokens of a refused sequence and for
+ *                i >= tok_start[n_seq]  (the input of kvq_append_mla)
+ *   tok_pos[i]   position of packed token i in its sequence, -1 where slot_map[i] is
+ * Refused, keeping its pages, its table row and n_held: a sequence without pages
+ * (KVQ_DEV_NO_PAGE), with a need above max_pages (KVQ_DEV_NO_PAGE), whose tokens end behind
+ * max_tokens or whose length passes INT32_MAX (KVQ_DEV_BAD_INDEX), or with keep_len beyond its
+ * pages (KVQ_DEV_BAD_PAGE).  Negative lengths count as 0, *n_free and n_held outside their
+ * arrays are clamped (KVQ_DEV_BAD_INDEX); a page id outside [0, n_pages) gets slot -1
+ * (KVQ_DEV_BAD_PAGE).  List entries at and above the new top that no page was pushed to stay as
+ * they were.  The page ids of list and tables are distinct: the caller sees to that.
+ */
+typedef struct kvq_page_plan {
+    int32_t n_seq;                  /* 0 .. 65535                                       */
+    int32_t max_pages, page_size;
+    int32_t n_pages;                /* pages of the pool = entries of free_list          */
+    int32_t max_tokens;             /* entries of slot_map and tok_pos                   */
+    const int32_t* keep_len;        /* device [n_seq]                                   */
+    const int32_t* n_new;           /* device [n_seq]                                   */
+    int32_t* block_table;           /* device [n_seq][max_pages], updated                */
+    int32_t* n_held;                /* device [n_seq], updated                          */
+    int32_t* free_list;             /* device [n_pages], updated                        */
+    int32_t* n_free;                /* device [1], updated                              */
+    int32_t* seq_len;               /* device [n_seq]; not keep_len or n_new             */
+    int32_t* tok_start;             /* device [n_seq + 1]                               */
+    int32_t* slot_map;              /* device [max_tokens]                              */
+    int32_t* tok_pos;               /* device [max_tokens] or NULL                      */
+} kvq_page_plan;
+
+int kvq_resize_pages(const kvq_page_plan* p, uint32_t* dev_status, kvq_stream_t stream);
+
+/*
+ * Paged append of MLA rows: row r, encoded as kvq_encode_mla encodes it (the same bytes),
+ * goes to pool row slot[r] of the cache planes.  A negative slot skips the row (padding, or
+ * a refused sequence); a slot of n_rows or more skips it and sets KVQ_DEV_BAD_PAGE.
+ * Non-negative slots must differ from one another.
+ *   c_lat   device [rows] x ldx of x_type (kvq_weight_type; bfloat16 is widened exactly)
+ *   k_rope  device [rows] x ldr of x_type
+ *   slot    device i32 [rows]
+ *   cache   the planes of tier fmt (KVQ_FMT_FP8 / TQ3 / TQ4 / TQ6), written
+ * 16-byte aligned rows (base and row stride) and code planes (KVQ_EALIGN otherwise).  Errors:
+ * KVQ_EFORMAT for another fmt; KVQ_EINVAL for rows < 0, a short stride, another x_type or a
+ * NULL pointer.  rows == 0 is a no-op.  One kernel launch.
+ */
+int kvq_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t ldr, int x_type,
+                   int64_t rows, const int32_t* slot, int fmt, const uint32_t* sign_bits,
+                   const kvq_mla_cache* cache, uint32_t* dev_status, kvq_stream_t stream);
+
+/*
+ * Absorbed-MLA attention of drafted trees.  The last n = n_node[s] of the L = seq_len[s] rows
+ * of sequence s are the rows of its drafted nodes (n is clamped to [0, min(n_q, L)]): node j's
+ * row is L - n + j.  Node j sees every row before them, t < L - n, and of the nodes' rows those
+ * with their bit set,
+ *     t = L - n + k  with bit k of mask[s][j]      (mask NULL: k <= j, a chain).
+ * Per node and head, as in kvq_mla_decode:
+ *     s_t = sm_scale * (q_lat . c_t + q_rope . k_rope_t),  out = sum_t softmax(s)_t c_t,
+ *     lse = log sum_t exp(s_t).
+ * A node with nothing to see, and every node j >= n (padding), gets out = 0 and lse = -inf;
+ * the q rows of padding are not used.  A page that is missing or outside the pool sets
+ * KVQ_DEV_BAD_PAGE and its rows are skipped.  The rows of a page past L may hold anything.
+ * Queries and outputs are bfloat16; scores, softmax and sums are fp32, and so is lse.
+ */
+typedef struct kvq_mla_tree_problem {
+    int32_t n_seq, n_q, n_heads;    /* n_q: nodes a sequence at most, 1 .. 64            */
+    int32_t d_lat, d_rope;          /* must be 512 and 64                               */
+    int32_t fmt;                    /* KVQ_FMT_FP8 / TQ3 / TQ4 / TQ6                     */
+    int32_t max_seq_len;            /* host bound on every seq_len (clamped to it)       */
+    const int32_t* seq_len;         /* device [n_seq]: rows held, the nodes' included    */
+    const int32_t* n_node;          /* device [n_seq] (clamped as above) or NULL: n_q     */
+    const uint64_t* mask;           /* device [n_seq][n_q] or NULL                      */
+    const int32_t* block_table;     /* device [n_seq][max_pages] pool page ids, or NULL */
+    int32_t max_pages, page_size;
+    int64_t seq_stride_rows;        /* no block table: seq i row t = pool row i*stride+t */
+    kvq_mla_cache cache;            /* the planes of tier fmt                           */
+    const uint32_t* signs;          /* device [16]: rotation signs (rotated tiers)       */
+    const void* q_lat;              /* device bf16 [n_seq][n_q][n_heads] rows of ldq_lat  */
+    const void* q_rope;             /* device bf16 [n_seq][n_q][n_heads] rows of ldq_rope */
+    int64_t ldq_lat, ldq_rope;      /* elements from one row to the next: multiples of 8 */
+    float sm_scale;                 /* finite                                           */
+    int32_t impl;                   /* 0: library chooses; 1: packed; 2: per query       */
+} kvq_mla_tree_problem;
+
+/*
+ * The form that runs: 1, packed — every (node, head) row of a sequence shares one pass over
+ * its cache, 64 rows a tile on the tensor cores (fp8 rows; contiguous sequences, or pages of a
+ * multiple of 8 rows); 2 — kvq_mla_decode over the rows before the draft, query by query, then
+ * the drafted rows joined to it (every tier and page size).  impl 0 takes 1 where it can read
+ * the problem.  A negated status for an invalid problem (-KVQ_EFORMAT for impl 1 on another
+ * tier, -KVQ_EINVAL for impl 1 on other page sizes).
+ */
+int kvq_mla_tree_decode_kernel(const kvq_mla_tree_problem* p);
+
+/* Bytes of workspace kvq_mla_tree_decode needs for this problem (0 if invalid). */
+size_t kvq_mla_tree_decode_workspace(const kvq_mla_tree_problem* p);
+
+/*
+ *   out        device bf16 [n_seq][n_q][n_heads][512], 16-byte aligned
+ *   lse        device fp32 [n_seq][n_q][n_heads] or NULL (natural log)
+ *   workspace  device, >= kvq_mla_tree_decode_workspace(p) bytes, 256-byte aligned
+ *   dev_status device u32 or NULL
+ */
+int kvq_mla_tree_decode(const kvq_mla_tree_problem* p, void* out, float* lse, void* workspace,
+                        size_t ws_bytes, uint32_t* dev_status, kvq_stream_t stream);
+
+/*
+ * After the verification of a draft: the accepted nodes' rows move to the front of the draft.
+ * With L, n as in kvq_mla_tree_decode and the accepted path path[s][0 .. n_acc[s] - 1] (node
+ * numbers, ascending, as a path from the root has them), row L - n + path[s][k] is copied to
+ * row L - n + k, every plane, byte for byte, as if all were read before any is written; then
+ *     new_len[s] = L - n + n_acc[s].
+ * n_acc is clamped to [0, n]; a path entry that is not larger than the one before it, or not a
+ * node (0 .. n - 1), ends the path before it (KVQ_DEV_BAD_INDEX).  A row on a missing page is
+ * not moved (KVQ_DEV_BAD_PAGE).  Rows behind new_len that no row moved to keep their bytes.
+ * new_len may be seq_len itself.
+ */
+typedef struct kvq_mla_accept_desc {
+    int32_t n_seq, n_q;             /* n_q: nodes a sequence at most, 1 .. 64            */
+    int32_t fmt;
+    const int32_t* seq_len;         /* device [n_seq]                                   */
+    const int32_t* n_node;          /* device [n_seq] or NULL: n_q                      */
+    const int32_t* path;            /* device [n_seq][n_q]                              */
+    const int32_t* n_acc;           /* device [n_seq]                                   */
+    int32_t* new_len;               /* device [n_seq]                                   */
+    const int32_t* block_table;     /* as in kvq_mla_tree_problem                       */
+    int32_t max_pages, page_size;
+    int64_t seq_stride_rows;
+    kvq_mla_cache cache;            /* the planes of tier fmt, written                   */
+} kvq_mla_accept_desc;
+
+int kvq_accept_mla(const kvq_mla_accept_desc* d, uint32_t* dev_status, kvq_stream_t stream);
 
 /*
  * q4_0 paged decode attention, grouped-query, head_dim 256 — Strata PR #2533, the qsa

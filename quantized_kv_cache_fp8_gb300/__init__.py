@@ -22,7 +22,11 @@ __all__ = [
     "MlaProblem", "Q4Problem", "make_q4_problem", "kvq_q4_decode", "kvq_q4_decode_workspace",
     "FMT_FP8", "FMT_TQ4", "FMT_Q4_0", "FMT_TQ6", "FMT_TQ3", "TQ_FMT", "kvq_encode_tq", "kvq_encode_mla",
     "kvq_tq_codebook", "DEV_BAD_INDEX", "DEV_BAD_PAGE", "DEV_TIMEOUT",
-    "DEV_BAD_FORMAT",
+    "DEV_BAD_FORMAT", "DEV_NO_PAGE",
+    "PagePlan", "make_page_plan", "kvq_resize_pages", "kvq_append_mla",
+    "TreeProblem", "make_tree_problem", "kvq_mla_tree_decode", "kvq_mla_tree_decode_workspace",
+    "kvq_mla_tree_decode_kernel", "TREE_PACKED", "TREE_PER_QUERY",
+    "AcceptDesc", "make_accept", "kvq_accept_mla",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -33,7 +37,8 @@ WEIGHT_F32, WEIGHT_BF16 = 0, 1
 TQ_FMT = {3: FMT_TQ3, 4: FMT_TQ4, 6: FMT_TQ6}     # rotated tier of each code width
 IMPL_AUTO, IMPL_SIMT, IMPL_TC, IMPL_MMA, IMPL_TC16, IMPL_TCF8 = 0, 1, 2, 3, 4, 5
 IMPL_BY_FMT = 6   # kvq_mla_decode_kernel only: fp8 sequences on IMPL_TCF8, TQ4 ones on IMPL_TC
-DEV_BAD_INDEX, DEV_BAD_PAGE, DEV_TIMEOUT, DEV_BAD_FORMAT = 1, 2, 4, 8
+TREE_PACKED, TREE_PER_QUERY = 1, 2       # forms of kvq_mla_tree_decode
+DEV_BAD_INDEX, DEV_BAD_PAGE, DEV_TIMEOUT, DEV_BAD_FORMAT, DEV_NO_PAGE = 1, 2, 4, 8, 16
 STATUS = {0: "KVQ_OK", 1: "KVQ_EINVAL", 2: "KVQ_ENOTPOW2", 3: "KVQ_EFORMAT", 4: "KVQ_EALIGN",
           5: "KVQ_EWORKSPACE", 6: "KVQ_ECUDA", 7: "KVQ_EFAULT_INJECTED", 8: "KVQ_EMISMATCH",
           9: "KVQ_EIO"}
@@ -46,7 +51,9 @@ EXPORTS = ["kvq_version", "kvq_status_string", "kvq_last_error", "kvq_set_fault"
            "kvq_gather", "kvq_mla_decode_workspace", "kvq_mla_decode_kernel", "kvq_mla_decode",
            "kvq_mla_decode_noalloc", "kvq_q4_decode_workspace", "kvq_q4_decode",
            "kvq_cache_probe", "kvq_cache_save", "kvq_cache_save_f32", "kvq_cache_append",
-           "kvq_cache_load_workspace", "kvq_cache_load"]
+           "kvq_cache_load_workspace", "kvq_cache_load",
+           "kvq_resize_pages", "kvq_append_mla", "kvq_mla_tree_decode_kernel",
+           "kvq_mla_tree_decode_workspace", "kvq_mla_tree_decode", "kvq_accept_mla"]
 
 
 class KvqError(RuntimeError):
@@ -91,6 +98,29 @@ class Q4Problem(C.Structure):
                 ("max_pages", _i32), ("page_size", _i32), ("n_cells", _i64),
                 ("k_pool", _p), ("v_pool", _p), ("q", _p), ("gate", _p),
                 ("sm_scale", _f32), ("split_rows", _i32)]
+
+
+class PagePlan(C.Structure):
+    _fields_ = [("n_seq", _i32), ("max_pages", _i32), ("page_size", _i32), ("n_pages", _i32),
+                ("max_tokens", _i32), ("keep_len", _p), ("n_new", _p), ("block_table", _p),
+                ("n_held", _p), ("free_list", _p), ("n_free", _p), ("seq_len", _p),
+                ("tok_start", _p), ("slot_map", _p), ("tok_pos", _p)]
+
+
+class TreeProblem(C.Structure):
+    _fields_ = [("n_seq", _i32), ("n_q", _i32), ("n_heads", _i32), ("d_lat", _i32),
+                ("d_rope", _i32), ("fmt", _i32), ("max_seq_len", _i32), ("seq_len", _p),
+                ("n_node", _p), ("mask", _p), ("block_table", _p), ("max_pages", _i32),
+                ("page_size", _i32), ("seq_stride_rows", _i64), ("cache", MlaCache),
+                ("signs", _p), ("q_lat", _p), ("q_rope", _p), ("ldq_lat", _i64),
+                ("ldq_rope", _i64), ("sm_scale", _f32), ("impl", _i32)]
+
+
+class AcceptDesc(C.Structure):
+    _fields_ = [("n_seq", _i32), ("n_q", _i32), ("fmt", _i32), ("seq_len", _p), ("n_node", _p),
+                ("path", _p), ("n_acc", _p), ("new_len", _p), ("block_table", _p),
+                ("max_pages", _i32), ("page_size", _i32), ("seq_stride_rows", _i64),
+                ("cache", MlaCache)]
 
 
 class CacheInfo(C.Structure):
@@ -167,6 +197,18 @@ def _declare(L):
     L.kvq_cache_load.restype = C.c_int
     L.kvq_cache_load.argtypes = [C.c_char_p, C.c_int32, _p, C.POINTER(MlaCache), _i64,
                                  C.POINTER(_i64), _p, C.c_size_t, _p]
+    L.kvq_resize_pages.restype = C.c_int
+    L.kvq_resize_pages.argtypes = [C.POINTER(PagePlan), _p, _p]
+    L.kvq_append_mla.restype = C.c_int
+    L.kvq_append_mla.argtypes = [_p, _i64, _p, _i64, C.c_int, _i64, _p, C.c_int, _p, C.POINTER(MlaCache), _p, _p]
+    L.kvq_mla_tree_decode_kernel.restype = C.c_int
+    L.kvq_mla_tree_decode_kernel.argtypes = [C.POINTER(TreeProblem)]
+    L.kvq_mla_tree_decode_workspace.restype = C.c_size_t
+    L.kvq_mla_tree_decode_workspace.argtypes = [C.POINTER(TreeProblem)]
+    L.kvq_mla_tree_decode.restype = C.c_int
+    L.kvq_mla_tree_decode.argtypes = [C.POINTER(TreeProblem), _p, _p, _p, C.c_size_t, _p, _p]
+    L.kvq_accept_mla.restype = C.c_int
+    L.kvq_accept_mla.argtypes = [C.POINTER(AcceptDesc), _p, _p]
     L.kvq_q4_decode_workspace.restype = C.c_size_t
     L.kvq_q4_decode_workspace.argtypes = [C.POINTER(Q4Problem)]
     L.kvq_q4_decode.restype = C.c_int
@@ -386,6 +428,153 @@ def kvq_q4_decode(p: Q4Problem, out, lse=None, workspace=None, dev_status=None,
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().kvq_q4_decode(C.byref(p), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
                                _ptr(dev_status), _stream(stream)))
+
+
+# --- drafted tokens over a paged MLA cache ------------------------------------------------
+
+def _want(name, t, dtype, *shape):
+    """A contiguous tensor of `dtype` (a name) and `shape` (None: any size), or None."""
+    if t is None:
+        return
+    if str(t.dtype) != "torch." + dtype or not t.is_contiguous() or t.dim() != len(shape) or \
+            any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, "
+                         f"is {t.dtype} {list(t.shape)}")
+
+
+def make_page_plan(*, keep_len, n_new, block_table, n_held, free_list, n_free, page_size, seq_len,
+                   tok_start, slot_map, tok_pos=None) -> PagePlan:
+    """Fill a kvq_page_plan from int32 tensors: block_table [n_seq, max_pages], free_list
+    [n_pages], n_free [1], tok_start [n_seq + 1], slot_map (and tok_pos) [max_tokens], the
+    others [n_seq].  The returned object keeps a reference to every tensor it carries."""
+    n = keep_len.shape[0]
+    for name, t, shape in (("keep_len", keep_len, (n,)), ("n_new", n_new, (n,)),
+                           ("block_table", block_table, (n, None)), ("n_held", n_held, (n,)),
+                           ("free_list", free_list, (None,)), ("n_free", n_free, (1,)),
+                           ("seq_len", seq_len, (n,)), ("tok_start", tok_start, (n + 1,)),
+                           ("slot_map", slot_map, (None,)), ("tok_pos", tok_pos, slot_map.shape)):
+        _want(name, t, "int32", *shape)
+    p = PagePlan()
+    p.n_seq, p.max_pages, p.page_size = n, block_table.shape[1], int(page_size)
+    p.n_pages, p.max_tokens = free_list.shape[0], slot_map.shape[0]
+    p.keep_len, p.n_new, p.block_table, p.n_held = _ptr(keep_len), _ptr(n_new), _ptr(block_table), _ptr(n_held)
+    p.free_list, p.n_free, p.seq_len = _ptr(free_list), _ptr(n_free), _ptr(seq_len)
+    p.tok_start, p.slot_map, p.tok_pos = _ptr(tok_start), _ptr(slot_map), _ptr(tok_pos)
+    p._keep = [keep_len, n_new, block_table, n_held, free_list, n_free, seq_len, tok_start, slot_map, tok_pos]
+    return p
+
+
+def kvq_resize_pages(p: PagePlan, dev_status=None, stream=None) -> None:
+    _check(lib().kvq_resize_pages(C.byref(p), _ptr(dev_status), _stream(stream)))
+
+
+def _mla_planes(planes, fmt):
+    row = {FMT_FP8: 512, FMT_TQ4: 256, FMT_TQ6: 384, FMT_TQ3: 192}.get(int(fmt))
+    n = planes["lat"].shape[0]
+    _want("lat", planes["lat"], "uint8", n, row)
+    _want("lat_scale", planes["lat_scale"], "float32", n)
+    _want("rope", planes["rope"], "uint8", n, 64)
+    _want("rope_scale", planes["rope_scale"], "float32", n)
+    return _cache(planes)
+
+
+def kvq_append_mla(c_lat, k_rope, slot_map, fmt, sign_bits, planes: dict, dev_status=None,
+                   stream=None) -> None:
+    """Encode rows c_lat [rows, 512] and k_rope [rows, 64] (both float32 or both bfloat16, rows
+    possibly strided) into the cache planes of tier `fmt` at pool rows slot_map int32 [rows]
+    (negative: skipped)."""
+    rows = c_lat.shape[0]
+    kind = {"torch.float32": WEIGHT_F32, "torch.bfloat16": WEIGHT_BF16}.get(str(c_lat.dtype))
+    if kind is None or k_rope.dtype != c_lat.dtype or tuple(c_lat.shape) != (rows, 512) or \
+            tuple(k_rope.shape) != (rows, 64) or (rows and (c_lat.stride(1) != 1 or k_rope.stride(1) != 1)):
+        raise ValueError("c_lat, k_rope must be [rows, 512] and [rows, 64], both float32 or both bfloat16")
+    _want("slot_map", slot_map, "int32", rows)
+    c = _mla_planes(planes, fmt)
+    _check(lib().kvq_append_mla(_ptr(c_lat), c_lat.stride(0), _ptr(k_rope), k_rope.stride(0), kind, rows,
+                                _ptr(slot_map), int(fmt), _ptr(sign_bits), C.byref(c), _ptr(dev_status),
+                                _stream(stream)))
+
+
+def _row_stride(name, q, width):
+    """Elements between the rows of q [n_seq, n_q, heads, width], which must be evenly spaced."""
+    n, nq, h, w = q.shape
+    ld = q.stride(2) if h > 1 else q.stride(1) if nq > 1 else q.stride(0) if n > 1 else w
+    even = (w == width and q.stride(3) == 1 and (h == 1 or q.stride(2) == ld)
+            and (nq == 1 or q.stride(1) == ld * h) and (n == 1 or q.stride(0) == ld * h * nq))
+    if str(q.dtype) != "torch.bfloat16" or not even:
+        raise ValueError(f"{name} must be bfloat16 [n_seq, n_q, heads, {width}] with evenly spaced rows")
+    return ld
+
+
+def make_tree_problem(*, seq_len, q_lat, q_rope, sm_scale, max_seq_len, fmt, cache, signs=None, n_node=None,
+                      mask=None, block_table=None, page_size=0, seq_stride_rows=0, impl=0) -> TreeProblem:
+    """Fill a kvq_mla_tree_problem from torch tensors: q_lat [n_seq, n_q, H, 512] and q_rope
+    [n_seq, n_q, H, 64] bfloat16, mask int64 [n_seq, n_q] (bit k of an entry: sees node k), cache the
+    planes of tier `fmt`.  The returned object keeps a reference to every tensor it carries."""
+    n_seq, n_q, H, DL = q_lat.shape
+    if tuple(q_rope.shape[:3]) != (n_seq, n_q, H):
+        raise ValueError("q_rope must have the rows of q_lat")
+    _want("seq_len", seq_len, "int32", n_seq)
+    _want("n_node", n_node, "int32", n_seq)
+    _want("mask", mask, "int64", n_seq, n_q)
+    _want("block_table", block_table, "int32", n_seq, None)
+    p = TreeProblem()
+    p.n_seq, p.n_q, p.n_heads, p.d_lat, p.d_rope = n_seq, n_q, H, DL, q_rope.shape[-1]
+    p.fmt, p.max_seq_len = int(fmt), int(max_seq_len)
+    p.seq_len, p.n_node, p.mask = _ptr(seq_len), _ptr(n_node), _ptr(mask)
+    if block_table is not None:
+        p.block_table, p.max_pages, p.page_size = _ptr(block_table), block_table.shape[1], int(page_size)
+    p.seq_stride_rows = int(seq_stride_rows)
+    p.cache, p.signs = _mla_planes(cache, fmt), _ptr(signs)
+    p.q_lat, p.q_rope = _ptr(q_lat), _ptr(q_rope)
+    p.ldq_lat, p.ldq_rope = _row_stride("q_lat", q_lat, 512), _row_stride("q_rope", q_rope, 64)
+    p.sm_scale, p.impl = float(sm_scale), int(impl)
+    p._keep = [seq_len, n_node, mask, block_table, cache, signs, q_lat, q_rope]
+    return p
+
+
+def kvq_mla_tree_decode_workspace(p: TreeProblem) -> int:
+    return lib().kvq_mla_tree_decode_workspace(C.byref(p))
+
+
+def kvq_mla_tree_decode_kernel(p: TreeProblem) -> int:
+    """The form kvq_mla_tree_decode runs for p: TREE_PACKED or TREE_PER_QUERY."""
+    r = lib().kvq_mla_tree_decode_kernel(C.byref(p))
+    if r < 0:
+        _check(-r)
+    return r
+
+
+def kvq_mla_tree_decode(p: TreeProblem, out, lse=None, workspace=None, dev_status=None, stream=None) -> None:
+    _want("out", out, "bfloat16", p.n_seq, p.n_q, p.n_heads, 512)
+    _want("lse", lse, "float32", p.n_seq, p.n_q, p.n_heads)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(lib().kvq_mla_tree_decode(C.byref(p), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
+                                     _ptr(dev_status), _stream(stream)))
+
+
+def make_accept(*, seq_len, path, n_acc, new_len, fmt, cache, n_node=None, block_table=None, page_size=0,
+                seq_stride_rows=0) -> AcceptDesc:
+    """Fill a kvq_mla_accept_desc from int32 tensors: path [n_seq, n_q], the others [n_seq].  The
+    returned object keeps a reference to every tensor it carries."""
+    n_seq, n_q = path.shape
+    for name, t, shape in (("seq_len", seq_len, (n_seq,)), ("path", path, (n_seq, n_q)),
+                           ("n_acc", n_acc, (n_seq,)), ("new_len", new_len, (n_seq,)),
+                           ("n_node", n_node, (n_seq,)), ("block_table", block_table, (n_seq, None))):
+        _want(name, t, "int32", *shape)
+    d = AcceptDesc()
+    d.n_seq, d.n_q, d.fmt = n_seq, n_q, int(fmt)
+    d.seq_len, d.n_node, d.path = _ptr(seq_len), _ptr(n_node), _ptr(path)
+    d.n_acc, d.new_len = _ptr(n_acc), _ptr(new_len)
+    if block_table is not None:
+        d.block_table, d.max_pages, d.page_size = _ptr(block_table), block_table.shape[1], int(page_size)
+    d.seq_stride_rows, d.cache = int(seq_stride_rows), _mla_planes(cache, fmt)
+    d._keep = [seq_len, n_node, path, n_acc, new_len, block_table, cache]
+    return d
+
+
+def kvq_accept_mla(d: AcceptDesc, dev_status=None, stream=None) -> None:
+    _check(lib().kvq_accept_mla(C.byref(d), _ptr(dev_status), _stream(stream)))
 
 
 # --- cache files ------------------------------------------------------------------------

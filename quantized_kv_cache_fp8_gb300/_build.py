@@ -29,6 +29,9 @@ UNITS = {
     "kvq_noalloc.cu": [],
     "kvq_q4_decode.cu": [],
     "kvq_persist.cu": [],
+    "kvq_pages.cu": [],
+    "kvq_tree.cu": [],
+    "kvq_tree_packed.cu": [],
 }
 
 

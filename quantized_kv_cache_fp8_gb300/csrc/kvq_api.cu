@@ -209,6 +209,31 @@ int kvq_encode_mla(const float* c_lat, int64_t ldx, const float* k_rope, int64_t
                                               lat_scale, rope, ldc, rope_scale, (cudaStream_t)stream), E);
 }
 
+int kvq_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t ldr, int x_type,
+                   int64_t rows, const int32_t* slot, int fmt, const uint32_t* sign_bits,
+                   const kvq_mla_cache* cache, uint32_t* dev_status, kvq_stream_t stream)
+{
+    const char* E = "kvq_append_mla";
+    if (int st = injected(E)) return st;
+    if (fmt != KVQ_FMT_FP8 && !kvq::rotated_format(fmt)) return fail(KVQ_EFORMAT, "%s: fmt %d", E, fmt);
+    if (rows < 0) return fail(KVQ_EINVAL, "%s: rows < 0", E);
+    if (x_type != KVQ_WEIGHT_F32 && x_type != KVQ_WEIGHT_BF16) return fail(KVQ_EINVAL, "%s: x_type %d", E, x_type);
+    if (ldx < kvq::kDLat || ldr < kvq::kDRope) return fail(KVQ_EINVAL, "%s: a row stride is smaller than its row", E);
+    if (rows == 0) return KVQ_OK;
+    const bool rot = fmt != KVQ_FMT_FP8;
+    if (!c_lat || !k_rope || !slot || !cache || !cache->lat || !cache->lat_scale || !cache->rope ||
+        !cache->rope_scale || cache->n_rows < 0 || (rot && !sign_bits))
+        return fail(KVQ_EINVAL, "%s: NULL pointer", E);
+    const int64_t per16 = x_type == KVQ_WEIGHT_BF16 ? 8 : 4;      // elements in 16 bytes
+    if (!aligned(c_lat, 16) || !aligned(k_rope, 16) || ldx % per16 != 0 || ldr % per16 != 0)
+        return fail(KVQ_EALIGN, "%s: input rows not 16-byte aligned", E);
+    if (!aligned(cache->lat, 16) || !aligned(cache->rope, 16) || !aligned(cache->lat_scale, 4) ||
+        !aligned(cache->rope_scale, 4) || !aligned(slot, 4) || (rot && !aligned(sign_bits, 4)))
+        return fail(KVQ_EALIGN, "%s: cache planes, slots or signs misaligned", E);
+    return cuda_status(kvq::launch_append_mla(c_lat, ldx, k_rope, ldr, x_type == KVQ_WEIGHT_BF16, rows, slot, fmt,
+                                              sign_bits, *cache, dev_status, (cudaStream_t)stream), E);
+}
+
 int kvq_append_q4(const float* k, const float* v, int n_seq, const int32_t* pos0, int n_tok,
                   int n_heads, int head_dim, const int32_t* page_table, int max_pages,
                   int page_size, int64_t n_cells, uint8_t* k_pool, uint8_t* v_pool,

@@ -8,6 +8,7 @@
 // All kernels are memory-streaming: one warp per row, coalesced loads of the fp32
 // input, shuffles for the Walsh-Hadamard butterflies and the row reductions, and
 // 16-byte stores of the packed output staged through shared memory.
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
@@ -46,13 +47,42 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
     return lo | (hi << 16);
 }
 
+// Where row r of an encoder's input goes: to row r (RowSame), or to the pool row of a slot
+// map (RowSlot: negative slots and slots past the pool get no row, -1).
+struct RowSame {
+    __device__ __forceinline__ int64_t operator()(int64_t r) const { return r; }
+};
+struct RowSlot {
+    const int32_t* slot;
+    int64_t n_rows;
+    uint32_t* status;
+    __device__ __forceinline__ int64_t operator()(int64_t r) const
+    {
+        const int64_t o = __ldg(slot + r);
+        if (o < n_rows) return o < 0 ? -1 : o;
+        if (status) atomicOr(status, (unsigned)KVQ_DEV_BAD_PAGE);
+        return -1;
+    }
+};
+
+// elements 4 i .. 4 i + 3 of a row (16-byte aligned fp32, or 8-byte aligned bfloat16 widened
+// exactly), read once
+__device__ __forceinline__ float4 load_f4(const float* x, int i) { return __ldcs(reinterpret_cast<const float4*>(x) + i); }
+__device__ __forceinline__ float4 load_f4(const __nv_bfloat16* x, int i)
+{
+    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(x) + i);
+    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u),
+                       __uint_as_float(w.y << 16), __uint_as_float(w.y & 0xFFFF0000u));
+}
+
 // LANES lanes per row (1 <= LANES <= 32, power of two), VPL float4 per lane:
 // dim = 4 * VPL * LANES.  Requires 16-byte aligned x rows and 4-byte aligned code rows.
 // Warp `warp` of `n_warps` takes every n_warps-th group of 32 / LANES rows.
-template <int LANES, int VPL>
-__device__ __forceinline__ void encode_fp8_vec_rows(const float* __restrict__ x, int64_t rows, int64_t ldx,
+template <int LANES, int VPL, typename X = float, typename Rows = RowSame>
+__device__ __forceinline__ void encode_fp8_vec_rows(const X* __restrict__ x, int64_t rows, int64_t ldx,
                                                     uint8_t* __restrict__ codes, int64_t ldc,
-                                                    float* __restrict__ scales, int64_t warp, int64_t n_warps)
+                                                    float* __restrict__ scales, int64_t warp, int64_t n_warps,
+                                                    Rows row_of = Rows())
 {
     constexpr int kRowsPerWarp = 32 / LANES;
     const int lane = threadIdx.x & 31;
@@ -60,24 +90,24 @@ __device__ __forceinline__ void encode_fp8_vec_rows(const float* __restrict__ x,
     const int l = lane % LANES;
     for (int64_t r0 = warp * kRowsPerWarp; r0 < rows; r0 += n_warps * kRowsPerWarp) {
         const int64_t r = r0 + sub;
-        const bool valid = r < rows;
+        const int64_t o = r < rows ? row_of(r) : -1;
+        const bool valid = o >= 0;
         float4 v[VPL];
         float amax = 0.0f;
         if (valid) {
-            const float4* xr = reinterpret_cast<const float4*>(x + r * ldx);
 #pragma unroll
             for (int k = 0; k < VPL; ++k) {
-                v[k] = __ldcs(xr + k * LANES + l);
+                v[k] = load_f4(x + r * ldx, k * LANES + l);
                 amax = fmaxf(amax, fmaxf(fmaxf(fabsf(v[k].x), fabsf(v[k].y)),
                                          fmaxf(fabsf(v[k].z), fabsf(v[k].w))));
             }
         }
 #pragma unroll
-        for (int o = LANES / 2; o >= 1; o >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, o));
+        for (int m = LANES / 2; m >= 1; m >>= 1)
+            amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
         if (!valid) continue;
         const float s = __fdiv_rn(amax, 448.0f);
-        uint32_t* cr = reinterpret_cast<uint32_t*>(codes + r * ldc);
+        uint32_t* cr = reinterpret_cast<uint32_t*>(codes + o * ldc);
 #pragma unroll
         for (int k = 0; k < VPL; ++k) {
             uint32_t w = 0;
@@ -86,7 +116,7 @@ __device__ __forceinline__ void encode_fp8_vec_rows(const float* __restrict__ x,
                            __fdiv_rn(v[k].z, s), __fdiv_rn(v[k].w, s));
             cr[k * LANES + l] = w;
         }
-        if (l == 0) scales[r] = s;
+        if (l == 0) scales[o] = s;
     }
 }
 
@@ -349,12 +379,12 @@ __device__ __forceinline__ const float* tq512_thresholds()
 
 // Rows warp, warp + n_warps, ... of the grid's warps; every thread of the CTA calls it
 // (the bucket table is built by the CTA)
-template <int BITS>
-__device__ __forceinline__ void encode_tq512_rows(const float* __restrict__ x, int64_t rows, int64_t ldx,
+template <int BITS, typename X = float, typename Rows = RowSame>
+__device__ __forceinline__ void encode_tq512_rows(const X* __restrict__ x, int64_t rows, int64_t ldx,
                                                   const uint32_t* __restrict__ sign_bits,
                                                   uint8_t* __restrict__ packed, int64_t ldp,
                                                   float* __restrict__ radius, bool vec_store,
-                                                  int64_t warp, int64_t n_warps)
+                                                  int64_t warp, int64_t n_warps, Rows row_of = Rows())
 {
     using G = Tq512Grid<BITS>;
     constexpr int kNThr = (1 << BITS) - 1;
@@ -369,9 +399,8 @@ __device__ __forceinline__ void encode_tq512_rows(const float* __restrict__ x, i
     // the first row's loads are issued before the bucket table is built
     float4 nx[4];
     if (warp < rows) {
-        const float4* src = reinterpret_cast<const float4*>(x + warp * ldx) + 4 * lane;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) nx[q] = __ldcs(src + q);
+        for (int q = 0; q < 4; ++q) nx[q] = load_f4(x + warp * ldx, 4 * lane + q);
     }
     for (int b = threadIdx.x; b < G::n; b += blockDim.x) {
         const float lo = ((float)b - G::off - 0.5f) / G::scale;
@@ -396,10 +425,11 @@ __device__ __forceinline__ void encode_tq512_rows(const float* __restrict__ x, i
             v[4 * q] = nx[q].x; v[4 * q + 1] = nx[q].y; v[4 * q + 2] = nx[q].z; v[4 * q + 3] = nx[q].w;
         }
         if (r + n_warps < rows) {
-            const float4* src = reinterpret_cast<const float4*>(x + (r + n_warps) * ldx) + 4 * lane;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) nx[q] = __ldcs(src + q);
+            for (int q = 0; q < 4; ++q) nx[q] = load_f4(x + (r + n_warps) * ldx, 4 * lane + q);
         }
+        const int64_t ro = row_of(r);
+        if (ro < 0) continue;                              // (the whole warp: one row)
 #pragma unroll
         for (int j = 0; j < 16; ++j)                       // s_i x_i: flip the sign bit
             v[j] = __uint_as_float(__float_as_uint(v[j]) ^ (((neg16 >> j) & 1u) << 31));
@@ -539,14 +569,14 @@ __device__ __forceinline__ void encode_tq512_rows(const float* __restrict__ x, i
             }
         }
         __syncwarp();
-        uint8_t* pr = packed + r * ldp;
+        uint8_t* pr = packed + ro * ldp;
         if (vec_store) {
             if (lane < kRowBytes / 16) reinterpret_cast<uint4*>(pr)[lane] = reinterpret_cast<const uint4*>(out)[lane];
         } else {
             for (int q = lane; q < kRowBytes; q += 32) pr[q] = out[q];
         }
         __syncwarp();
-        if (lane == 0) radius[r] = rad;
+        if (lane == 0) radius[ro] = rad;
     }
 }
 
@@ -583,6 +613,29 @@ encode_mla_kernel(const float* __restrict__ c_lat, int64_t ldx, const float* __r
             encode_fp8_vec_rows<32, 4>(c_lat, rows, ldx, lat, ldl, lat_scale, warp, n_warps);
         else
             encode_tq512_rows<BITS>(c_lat, rows, ldx, sign_bits, lat, ldl, lat_scale, vec_store, warp, n_warps);
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// The same at the pool rows of a slot map (the paged append): row r's planes go to row
+// slot[r] of the cache, fp32 or bfloat16 rows.
+// ------------------------------------------------------------------------------------
+template <int BITS, typename X>
+__global__ void __launch_bounds__(kCodecThreads)
+append_mla_kernel(const X* __restrict__ c_lat, int64_t ldx, const X* __restrict__ k_rope, int64_t ldr, int64_t rows,
+                  RowSlot row_of, const uint32_t* __restrict__ sign_bits, uint8_t* __restrict__ lat,
+                  float* __restrict__ lat_scale, uint8_t* __restrict__ rope, float* __restrict__ rope_scale)
+{
+    const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+    const int64_t n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    if (blockIdx.y == 1) {
+        encode_fp8_vec_rows<4, 4>(k_rope, rows, ldr, rope, (int64_t)64, rope_scale, warp, n_warps, row_of);
+    } else {
+        if constexpr (BITS == 8)
+            encode_fp8_vec_rows<32, 4>(c_lat, rows, ldx, lat, (int64_t)512, lat_scale, warp, n_warps, row_of);
+        else
+            encode_tq512_rows<BITS>(c_lat, rows, ldx, sign_bits, lat, (int64_t)64 * BITS, lat_scale, true, warp,
+                                    n_warps, row_of);
     }
 }
 
@@ -1322,6 +1375,53 @@ cudaError_t launch_encode_mla(const float* c_lat, int64_t ldx, const float* k_ro
         case 6: return launch_encode_mla_fused<6>(c_lat, ldx, k_rope, ldr, rows, sign_bits, lat, ldl, lat_scale, rope, ldc, rope_scale, vec, s);
         default: return cudaErrorInvalidValue;
     }
+}
+
+namespace {
+
+template <int BITS, typename X>
+cudaError_t launch_append_mla_as(const void* c_lat, int64_t ldx, const void* k_rope, int64_t ldr, int64_t rows,
+                                 const RowSlot& row_of, const uint32_t* sign_bits, const kvq_mla_cache& c, cudaStream_t s)
+{
+    // as launch_encode_mla_fused: one wave of the rotated encoder, 16 CTAs an SM of the fp8 one
+    int n = 16;
+    if constexpr (BITS != 8) {
+        static std::atomic<int> per_sm{0};
+        n = per_sm.load();
+        if (n <= 0) {
+            if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, append_mla_kernel<BITS, X>, kCodecThreads, 0) !=
+                    cudaSuccess || n <= 0) {
+                (void)cudaGetLastError();
+                n = 1;
+            }
+            per_sm.store(n);
+        }
+    }
+    const int64_t g = std::max<int64_t>(1, std::min<int64_t>((rows + kCodecWarps - 1) / kCodecWarps, (int64_t)sm_count() * n));
+    append_mla_kernel<BITS, X><<<dim3((unsigned)g, 2), kCodecThreads, 0, s>>>(
+        static_cast<const X*>(c_lat), ldx, static_cast<const X*>(k_rope), ldr, rows, row_of, sign_bits,
+        const_cast<uint8_t*>(c.lat), const_cast<float*>(c.lat_scale), const_cast<uint8_t*>(c.rope),
+        const_cast<float*>(c.rope_scale));
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t ldr, bool bf16, int64_t rows,
+                              const int32_t* slot, int fmt, const uint32_t* sign_bits, const kvq_mla_cache& c,
+                              uint32_t* dev_status, cudaStream_t s)
+{
+    const RowSlot row_of{slot, c.n_rows, dev_status};
+#define KVQ_APPEND(B)                                                                                             \
+    return bf16 ? launch_append_mla_as<B, __nv_bfloat16>(c_lat, ldx, k_rope, ldr, rows, row_of, sign_bits, c, s) \
+                : launch_append_mla_as<B, float>(c_lat, ldx, k_rope, ldr, rows, row_of, sign_bits, c, s)
+    switch (fmt == KVQ_FMT_FP8 ? 8 : rotated_bits(fmt)) {
+        case 8: KVQ_APPEND(8);
+        case 6: KVQ_APPEND(6);
+        case 4: KVQ_APPEND(4);
+        default: KVQ_APPEND(3);
+    }
+#undef KVQ_APPEND
 }
 
 void tq_codebook_values(int bits, float* centroids, float* thresholds)

@@ -185,6 +185,10 @@ cudaError_t launch_encode_mla(const float* c_lat, int64_t ldx, const float* k_ro
                               int64_t rows, int fmt, const uint32_t* sign_bits, uint8_t* lat,
                               int64_t ldl, float* lat_scale, uint8_t* rope, int64_t ldc,
                               float* rope_scale, cudaStream_t s);
+// the same at the pool rows slot[r] of a cache, fp32 or bfloat16 rows
+cudaError_t launch_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t ldr, bool bf16, int64_t rows,
+                              const int32_t* slot, int fmt, const uint32_t* sign_bits, const kvq_mla_cache& c,
+                              uint32_t* dev_status, cudaStream_t s);
 // the stored codebook of width b (2^b centroids, 2^b - 1 thresholds), host side
 void tq_codebook_values(int bits, float* centroids, float* thresholds);
 cudaError_t launch_append_q4(const float* k, const float* v, int n_seq, const int32_t* pos0,
@@ -244,5 +248,26 @@ struct Q4Plan {
 bool plan_q4_decode(const kvq_q4_problem& p, Q4Plan& plan);
 cudaError_t launch_q4_decode(const kvq_q4_problem& p, const Q4Plan& plan, float* out, float* lse,
                              void* ws, uint32_t* dev_status, cudaStream_t s);
+
+// ---- drafted trees (kvq_tree.cu, kvq_tree_packed.cu) -------------------------------------
+// (L, n) of sequence s: the rows it holds and its drafted nodes
+__device__ __forceinline__ int2 tree_seq_shape(const kvq_mla_tree_problem& p, int s)
+{
+    const int L = min(max(p.seq_len[s], 0), p.max_seq_len);
+    return make_int2(L, min(max(p.n_node ? p.n_node[s] : p.n_q, 0), min(p.n_q, L)));
+}
+
+// the drafted rows (bit k: node k's) that node j of sequence s sees, j < n <= 64
+__device__ __forceinline__ uint64_t tree_visible(const kvq_mla_tree_problem& p, int s, int j, int n)
+{
+    const uint64_t see = p.mask ? p.mask[(int64_t)s * p.n_q + j] : ~0ull >> (63 - j);
+    return n < 64 ? see & ((1ull << n) - 1) : see;
+}
+
+// the packed form: whether it can read the rows' layout (fp8 rows), its workspace, its launches
+bool tree_packed_reads(const kvq_mla_tree_problem& p);
+size_t tree_packed_workspace(const kvq_mla_tree_problem& p);
+cudaError_t launch_tree_packed(const kvq_mla_tree_problem& p, void* out, float* lse, void* ws,
+                               uint32_t* dev_status, cudaStream_t s);
 
 }  // namespace kvq
