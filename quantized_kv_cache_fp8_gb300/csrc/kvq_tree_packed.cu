@@ -1,6 +1,1091 @@
+// kvq_tree_packed.cu — attention of drafted trees over the fp8 tier with every (node, head) row
+// of a sequence packed into tiles of NR = 64 (or 32) rows that share one pass over the cache
+// (tcgen05 kind::f8f6f4; no code is converted).
+//
+// Per tile of 128 cache rows (M) and NR query rows (N), all operands e4m3:
+//   S^T[rows x 2 NR] = C_tile[rows x 576] . Qd^T        Qd: two digits of every query row
+//   O^T[dims x NR]  += V_tile^T[dims x rows] . Wd^T      Wd: two digits of every weight
+// Each 128-dim block of the latent codes is one [128 rows x 128 B] box, 128B-swizzled, read
+// K-major by the scores and MN-major by the context, so one copy serves both.  The scales
+// of a row stay outside: the softmax applies them to the scores in fp32 and folds the
+// latent's into the weights.
+//
+// Digits.  An e4m3 rounding keeps 4 significant bits, so q = 2^-sigma (Qd_0 + Qd_1 / 16) holds
+// the 8 bits of a bfloat16 exactly (down to 2^-21 of the row's largest element), and w = Wd_0 +
+// Wd_1 carries a weight to 2^-8 of its value, or to 2^-10 absolute where the second digit is
+// subnormal, on a scale that keeps the largest weight of a row between 2^kBase and 2^8.  The
+// outputs are rounded to bfloat16 (2^-8), so more digits would not show.  With NR = 32 the digits
+// of a weight have N columns of their own (the second one in units of 2^-4); with NR = 64 tensor
+// memory has no room for that and they are summed along K.
+//
+// Softmax: two running maxima per row, m_s over the scores (for the normalizer) and m_u over
+// u = s + log2(latent scale) (for the weights 2^(u - m_u + kBase)); either moves only when a
+// tile exceeds it by more than 2^kLazy, so that O is rescaled rarely.
+//
+// Work: the tiles of every (sequence, row tile) unit laid end to end on one line, cut into
+// equal stretches, one per CTA and SM; the cuts come from the lengths on the device, so ragged
+// batches are balanced and a captured call follows new lengths.  A unit inside one stretch
+// is written out directly; one that a cut crosses leaves partials (m, l, o) that
+// tree_combine_kernel joins (at most two per CTA).
+//
+// Every wait is bounded as in the other tensor-core kernels; a CTA that gives up poisons
+// the rows of its stretch.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include <algorithm>
+#include <atomic>
+#include <climits>
+#include <cstring>
+
 #include "kvq_internal.cuh"
+#include "kvq_sm100.cuh"
+#include "kvq_tc_common.cuh"
+
 namespace kvq {
-bool tree_packed_reads(const kvq_mla_tree_problem&) { return false; }
-size_t tree_packed_workspace(const kvq_mla_tree_problem&) { return 0; }
-cudaError_t launch_tree_packed(const kvq_mla_tree_problem&, void*, float*, void*, uint32_t*, cudaStream_t) { return cudaErrorNotSupported; }
+
+using namespace sm100;
+
+namespace {
+
+using namespace tc;
+
+constexpr int kRT = 128;                     // cache rows per tile
+constexpr int kBox = kRT * 128;              // [128 rows x 128 dims] codes
+constexpr int kRopeBox = kRT * 64;
+constexpr int kStages = 2;
+constexpr int kSmx = 16;                     // softmax warps: lane quarter w % 4, query rows NR / 4 (w / 4) ..
+constexpr int kWarpLoad = kSmx;
+constexpr int kWarpS = kSmx + 1;             // score MMAs (and tensor memory)
+constexpr int kWarpC = kSmx + 2;             // context MMAs
+constexpr int kThreads = 32 * (kSmx + 3);
+constexpr int kBoxes = 5;                    // four latent blocks and the rope key
+constexpr int kPieces = 8;                   // 16-byte pieces of a latent that each quarter of the warps clears
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 4.0f, kBase = 4.0f;  // kLazy + kBase <= 8: weights stay below 2^8 < 448
+constexpr float kNoMax = -1e30f;             // a maximum over nothing: finite, below any score
+constexpr uint64_t kTimeoutNs = kDefaultWaitNs;   // drains
+constexpr uint32_t kColO = 256;              // tensor memory: O^T of dims 128 m .. at 256 + 64 m
+
+template <int NR>
+struct Cfg {
+    static constexpr int kNS = 2 * NR;                       // score columns: digit 0 rows, digit 1 rows
+    static constexpr int kGR = NR / 4;                       // query rows per softmax warp
+    static constexpr int kWImgs = NR / 32;                   // [128 rows x 64 B] weight images
+    static constexpr int kRS = NR == 64 ? 1 : 2;             // rope key stages (64: shared memory is full)
+    static constexpr uint32_t kColSL = 0, kColSR = kNS;      // latent and rope scores
+    static constexpr int kQBlk = kNS * 128;
+    static constexpr int kQRope = 4 * kQBlk;
+    static constexpr int kQBytes = kQRope + kNS * 64;
+    static constexpr int kOffRope = kStages * 4 * kBox;
+    static constexpr int kOffQ = kOffRope + kRS * kRopeBox;
+    static constexpr int kOffW = kOffQ + kQBytes;
+    static constexpr int kOffRed = kOffW + kWImgs * kRT * 64;   // [4][NR] f32
+    static constexpr int kOffM = kOffRed + 4 * NR * 4;          // m_s, m_u, al_s, al_u, query scale: [NR] each
+    static constexpr int kOffBar = kOffM + 5 * NR * 4;
+    // full[2][4], empty[2][4], rope full[2], empty[2], s_full, s_empty, p_full, o_done, q_full, drain_s, drain_c
+    static constexpr int kNumBars = 2 * kStages * 4 + 2 * 2 + 7;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;     // tmem base, abort flag, start of the stretch
+    static constexpr int kSmem = kOffMisc + 32;
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(kOffQ % 1024 == 0 && kQBlk % 1024 == 0 && kOffW % 1024 == 0 && kOffBar % 16 == 0, "swizzle atoms");
+    static_assert(kColSR + kNS <= kColO, "tensor memory");
+};
+
+struct SplitInfo {                           // a unit that starts in a CTA's stretch
+    int s, rt;
+    int cta;                                 // that CTA; the others follow it
+    int slot;                                // its partial; the others' are 2 * cta
+    int pieces;                              // CTAs that share it (1: written out directly)
+    int pad[3];
+};
+
+struct Args {
+    CUtensorMap tm_lat, tm_rope;
+    kvq_mla_tree_problem p;
+    int box_rows;                            // rows a box brings: 128, or what divides the page
+    int by_unit;                             // infos are indexed by unit, else by CTA
+    int n_rt;                                // row tiles a sequence at most
+    float* part_ml;                          // [2 CTAs][NR][2]
+    float* part_o;                           // [2 CTAs][NR][512]
+    SplitInfo* info;
+    __nv_bfloat16* out;
+    float* lse;
+    uint32_t* status;
+    uint64_t wait_ns;
+};
+
+template <int NR>
+struct Shared {
+    using C = Cfg<NR>;
+    uint8_t* base;
+    __device__ uint8_t* box(int st, int b) const { return base + (st * 4 + b) * kBox; }
+    __device__ uint8_t* rope(int i) const { return base + C::kOffRope + i * kRopeBox; }
+    __device__ uint8_t* q() const { return base + C::kOffQ; }
+    __device__ uint8_t* w() const { return base + C::kOffW; }
+    __device__ float* red() const { return reinterpret_cast<float*>(base + C::kOffRed); }
+    __device__ float* m_s() const { return reinterpret_cast<float*>(base + C::kOffM); }
+    __device__ float* m_u() const { return m_s() + NR; }
+    __device__ float* al_s() const { return m_s() + 2 * NR; }
+    __device__ float* al_u() const { return m_s() + 3 * NR; }
+    __device__ float* qs() const { return m_s() + 4 * NR; }
+    __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(base + C::kOffBar) + i; }
+    __device__ uint64_t* full(int st, int b) const { return b < 4 ? bar(st * 4 + b) : bar(16 + st); }
+    __device__ uint64_t* empty(int st, int b) const { return b < 4 ? bar(8 + st * 4 + b) : bar(18 + st); }
+    __device__ uint64_t* s_full() const { return bar(20); }
+    __device__ uint64_t* s_empty() const { return bar(21); }
+    __device__ uint64_t* p_full() const { return bar(22); }
+    __device__ uint64_t* o_done() const { return bar(23); }
+    __device__ uint64_t* q_full() const { return bar(24); }
+    __device__ uint64_t* drain_s() const { return bar(25); }
+    __device__ uint64_t* drain_c() const { return bar(26); }
+    __device__ uint32_t* tmem_base() const { return reinterpret_cast<uint32_t*>(base + C::kOffMisc); }
+    __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(base + C::kOffMisc + 4); }
+    __device__ volatile int64_t* start_off() const { return reinterpret_cast<volatile int64_t*>(base + C::kOffMisc + 8); }
+    __device__ volatile int* start_seq() const { return reinterpret_cast<volatile int*>(base + C::kOffMisc + 16); }
+};
+
+// Wait for a phase, bounded by %globaltimer; kSpin polls, otherwise try_wait may suspend the
+// thread (a limit below 100 us, set only to exercise the failure path, always polls).
+template <bool kSpin, int NR>
+__device__ __forceinline__ bool wait_bar(const Shared<NR>& sh, uint64_t* bar, uint32_t parity, const Args& a)
+{
+    const bool spin = kSpin || a.wait_ns < 100000;
+    if (spin ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+#pragma unroll 1
+        for (int k = 0; k < 4; ++k)
+            if (spin ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
+        if (*sh.abort_flag()) return false;
+        if (globaltimer_ns() - t0 > a.wait_ns) {
+            *sh.abort_flag() = 1;
+            if (a.status) atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
+            return false;
+        }
+    }
 }
+
+__device__ __forceinline__ void smx_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSmx) : "memory"); }
+
+// barrier of the softmax warps; true if `v` holds in any of their threads
+__device__ __forceinline__ bool smx_any(bool v)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "barrier.cta.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r) : "r"((uint32_t)v), "n"(32 * kSmx) : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ int64_t tree_pool_row(const kvq_mla_tree_problem& p, int s, int t)
+{
+    if (!p.block_table) return (int64_t)s * p.seq_stride_rows + t;
+    const int page = t / p.page_size;
+    if (page >= p.max_pages) return -1;
+    const int pid = p.block_table[(int64_t)s * p.max_pages + page];
+    return pid < 0 ? -1 : (int64_t)pid * p.page_size + t % p.page_size;
+}
+
+// ---- the line of tiles --------------------------------------------------------------------
+template <int NR>
+__device__ __forceinline__ int64_t seq_tiles(const kvq_mla_tree_problem& p, int s)
+{
+    const int2 sh = tree_seq_shape(p, s);
+    return (int64_t)((sh.x + kRT - 1) / kRT) * (((int64_t)sh.y * p.n_heads + NR - 1) / NR);
+}
+
+// where the stretch of CTA g of G begins on a line of `total` tiles
+__device__ __forceinline__ int64_t cut(int64_t total, int g, int G) { return total * g / G; }
+
+// the segments of a stretch: row tile rt of sequence s, tiles [tile, end)
+template <int NR>
+struct Walk {
+    int64_t left;
+    int s, rt, tile, end, nt, n_rt, L, n;
+
+    __device__ __forceinline__ void shape(const kvq_mla_tree_problem& p)
+    {
+        const int2 sh = tree_seq_shape(p, s);
+        L = sh.x;
+        n = sh.y;
+        nt = (L + kRT - 1) / kRT;
+        n_rt = (int)(((int64_t)n * p.n_heads + NR - 1) / NR);
+    }
+    __device__ __forceinline__ Walk(const kvq_mla_tree_problem& p, int s0, int64_t off, int64_t count) : left(count), s(s0), end(0)
+    {
+        if (left <= 0) return;
+        shape(p);
+        rt = (int)(off / nt);
+        tile = (int)(off % nt);
+        end = (int)min((int64_t)nt, tile + left);
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    __device__ __forceinline__ void next(const kvq_mla_tree_problem& p)
+    {
+        left -= end - tile;
+        if (left <= 0) return;
+        if (++rt == n_rt) {
+            rt = 0;
+            do {
+                ++s;
+                shape(p);
+            } while (nt == 0 || n_rt == 0);               // (there is a tile left, so a sequence with tiles)
+        }
+        tile = 0;
+        end = (int)min((int64_t)nt, left);
+    }
+};
+
+// ---- queries ------------------------------------------------------------------------------
+__device__ __forceinline__ void bf16x8(const uint4& w, float* v)
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = __uint_as_float(u[i] << 16);
+        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+}
+
+// four values -> their two digits, four codes a word; the second digit in units of 1 / kScale
+template <int kScale>
+__device__ __forceinline__ void digits4(const float* x, uint32_t& d0, uint32_t& d1)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const float2 v = make_float2(x[2 * h], x[2 * h + 1]);
+        const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+        const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+        const __nv_fp8x2_storage_t e = __nv_cvt_float2_to_fp8x2(
+            make_float2((v.x - b.x) * (float)kScale, (v.y - b.y) * (float)kScale), __NV_SATFINITE, __NV_E4M3);
+        d0 = h ? d0 | (uint32_t)c << 16 : c;
+        d1 = h ? d1 | (uint32_t)e << 16 : e;
+    }
+}
+
+// One warp: query row `r` (of the sequence's n * H; zero past them) into rows i and NR + i of
+// the Q image.  sigma puts the row's largest element in [128, 256).
+template <int NR>
+__device__ __forceinline__ void write_query(const Shared<NR>& sh, const kvq_mla_tree_problem& p, int s, int64_t r,
+                                            bool live, int i, int lane)
+{
+    using C = Cfg<NR>;
+    float v[16], x[4];
+    if (live) {
+        const int64_t row = (int64_t)s * p.n_q * p.n_heads + r;
+        const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q_lat) + row * p.ldq_lat) + 2 * lane;
+        bf16x8(ql[0], v);
+        bf16x8(ql[1], v + 8);
+        const uint2 w = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q_rope) + row * p.ldq_rope)[lane & 15];
+        x[0] = __uint_as_float(w.x << 16);
+        x[1] = __uint_as_float(w.x & 0xFFFF0000u);
+        x[2] = __uint_as_float(w.y << 16);
+        x[3] = __uint_as_float(w.y & 0xFFFF0000u);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = 0.0f;
+    }
+    float mx = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fabsf(v[k]));
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fabsf(x[k]));
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
+    int e = 0;
+    (void)frexpf(mx, &e);
+    const int sigma = mx > 0.0f ? min(100, max(-100, 8 - e)) : 0;
+    const float scale = ldexpf(1.0f, sigma);
+    uint32_t d0[4], d1[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        float y[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) y[c] = v[4 * k + c] * scale;
+        digits4<16>(y, d0[k], d1[k]);
+    }
+    uint8_t* img = sh.q() + (lane >> 3) * C::kQBlk;
+    *reinterpret_cast<uint4*>(img + sw128(i, lane & 7)) = make_uint4(d0[0], d0[1], d0[2], d0[3]);
+    *reinterpret_cast<uint4*>(img + sw128(NR + i, lane & 7)) = make_uint4(d1[0], d1[1], d1[2], d1[3]);
+    if (lane < 16) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[c] *= scale;
+        uint32_t r0, r1;
+        digits4<16>(x, r0, r1);
+        uint8_t* rp = sh.q() + C::kQRope;
+        const int at = (((lane >> 2) ^ ((i >> 1) & 3)) << 4) + 4 * (lane & 3);      // (NR + i has the same swizzle)
+        *reinterpret_cast<uint32_t*>(rp + i * 64 + at) = r0;
+        *reinterpret_cast<uint32_t*>(rp + (NR + i) * 64 + at) = r1;
+    }
+    if (lane == 0) sh.qs()[i] = p.sm_scale * kLog2e * ldexpf(1.0f, -sigma);
+}
+
+// ---- codes that no encoder writes -----------------------------------------------------------
+// the 16-byte piece pc of row t: pc < 32 latent block pc / 8, then the rope key's four
+template <int NR>
+__device__ __forceinline__ uint4* row_piece(const Shared<NR>& sh, int st, int rst, int t, int pc)
+{
+    return reinterpret_cast<uint4*>(pc < 32 ? sh.box(st, pc >> 3) + t * 128 + (((pc & 7) ^ (t & 7)) << 4)
+                                            : sh.rope(rst) + t * 64 + (((pc - 32) ^ ((t >> 1) & 3)) << 4));
+}
+
+__device__ __forceinline__ uint32_t clear_unwritten(uint32_t w)
+{
+    return w & ~prmt((w & 0x7F7F7F7Fu) + 0x01010101u, 0u, 0xBA98u);     // bytes S.1111.111 -> 0
+}
+__device__ __forceinline__ uint4 clear_unwritten(const uint4& v)
+{
+    return make_uint4(clear_unwritten(v.x), clear_unwritten(v.y), clear_unwritten(v.z), clear_unwritten(v.w));
+}
+
+// whether row t holds the pattern; the latent's pieces of part hp are cleared of it in place, so
+// that the context reads them as 0 (a thread that still sees them, or no longer, scores the same)
+template <int NR>
+__device__ __noinline__ bool clear_row(const Shared<NR>& sh, int st, int rst, int t, int hp)
+{
+    bool found = false;
+    for (int pc = 0; pc < 36; ++pc) {
+        uint4* ptr = row_piece(sh, st, rst, t, pc);
+        const uint4 v = *ptr, c = clear_unwritten(v);
+        found |= v.x != c.x || v.y != c.y || v.z != c.z || v.w != c.w;
+        if (pc < 32 && pc / kPieces == hp) *ptr = c;
+    }
+    return found;
+}
+
+// q . row from the codes with the pattern read as 0, in fp32: log2-domain score
+template <int NR>
+__device__ __noinline__ float rescore(const Shared<NR>& sh, const kvq_mla_tree_problem& p, int st, int rst, int t,
+                                      int64_t row, float ls, float rs)
+{
+    const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(p.q_lat) + row * p.ldq_lat;
+    const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q_rope) + row * p.ldq_rope;
+    float al = 0.0f, ar = 0.0f;
+    for (int pc = 0; pc < 36; ++pc) {
+        const uint4 v = clear_unwritten(*row_piece(sh, st, rst, t, pc));
+        const uint32_t wd[4] = {v.x, v.y, v.z, v.w};
+        const __nv_bfloat16* q = pc < 32 ? ql + 16 * pc : qr + 16 * (pc - 32);
+        float acc = 0.0f;
+        for (int e = 0; e < 16; ++e) {
+            const float c = __half2float(__half(__nv_cvt_fp8_to_halfraw(
+                (__nv_fp8_storage_t)((wd[e >> 2] >> (8 * (e & 3))) & 0xFFu), __NV_E4M3)));
+            acc = fmaf(__bfloat162float(q[e]), c, acc);
+        }
+        if (pc < 32) al += acc;
+        else ar += acc;
+    }
+    return p.sm_scale * kLog2e * fmaf(ls, al, rs * ar);
+}
+
+// tmem <-> 8 or 16 consecutive columns
+__device__ __forceinline__ void tmem_ld_n(uint32_t c, uint32_t (&r)[8]) { tmem_ld_x8(c, r); }
+__device__ __forceinline__ void tmem_ld_n(uint32_t c, uint32_t (&r)[16]) { tmem_ld_x16(c, r); }
+__device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[8]) { tmem_st_x8(c, r); }
+__device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) { tmem_st_x16(c, r); }
+
+// ====================================================================================
+//  * Warps 0-15: softmax.  Thread = cache row of the tile (lane quarter warp % 4) for the NR / 4
+//    query rows of its part warp / 4; query images, epilogue (thread = output dim).
+//  * Warp 16: TMA loader, five boxes a tile into a two-stage ring.
+//  * Warp 17: tensor memory, score MMAs; warp 18: context MMAs.
+// The loader and the issuers run on into the next unit while the softmax warps finish one.
+// ====================================================================================
+template <int NR>
+__global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_constant__ Args a)
+{
+    using C = Cfg<NR>;
+    constexpr int GR = C::kGR;
+    extern __shared__ __align__(1024) uint8_t dsm[];
+    const Shared<NR> sh{dsm};
+    const kvq_mla_tree_problem& p = a.p;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int g = blockIdx.x;
+    grid_dependents_launch();                    // the combine may start launching
+
+    if (warp == kWarpS) {
+        if (lane == 0) {
+            for (int st = 0; st < kStages; ++st) {
+                for (int b = 0; b < kBoxes; ++b) {
+                    mbar_init(sh.full(st, b), 1);
+                    mbar_init(sh.empty(st, b), b < 4 ? 1 : kSmx);      // the context; the softmax
+                }
+            }
+            mbar_init(sh.s_full(), 1);
+            mbar_init(sh.s_empty(), kSmx);
+            mbar_init(sh.p_full(), kSmx);
+            mbar_init(sh.o_done(), 1);
+            mbar_init(sh.q_full(), kSmx);
+            mbar_init(sh.drain_s(), 1);
+            mbar_init(sh.drain_c(), 1);
+            *sh.abort_flag() = 0;
+            fence_mbar_init();
+        }
+        __syncwarp();
+        tmem_alloc(sh.tmem_base(), 512);
+        tmem_relinquish();
+    }
+    // ---- the length of the line, and where this CTA's stretch begins (scratch: the W image)
+    int64_t total = 0, t0 = 0, t1 = 0;
+    int G = gridDim.x;
+    {
+        int64_t* s_sum = reinterpret_cast<int64_t*>(sh.w());      // [32] sums of the warps
+        constexpr int kW = kThreads / 32;
+        int64_t v = 0;
+        for (int s = tid; s < p.n_seq; s += kThreads) v += seq_tiles<NR>(p, s);
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+        if (lane == 0) s_sum[warp] = v;
+        __syncthreads();
+        for (int w = 0; w < kW; ++w) total += s_sum[w];
+        G = (int)min((int64_t)G, max(total, (int64_t)1));
+        t0 = g < G ? cut(total, g, G) : 0;
+        t1 = g < G ? cut(total, g + 1, G) : 0;
+        int64_t base = 0;
+        for (int c = 0; c < p.n_seq && base <= t0 && t1 > t0; c += kThreads) {
+            const int s = c + tid;
+            const int64_t own = s < p.n_seq ? seq_tiles<NR>(p, s) : 0;
+            int64_t incl = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(kFull, incl, o);
+                if (lane >= o) incl += u;
+            }
+            __syncthreads();
+            if (lane == 31) s_sum[warp] = incl;
+            __syncthreads();
+            int64_t before = base, all = base;
+            for (int w = 0; w < kW; ++w) {
+                if (w < warp) before += s_sum[w];
+                all += s_sum[w];
+            }
+            const int64_t lo = before + incl - own;
+            if (own > 0 && lo <= t0 && t0 < lo + own) {
+                *sh.start_seq() = s;
+                *sh.start_off() = t0 - lo;
+            }
+            base = all;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *sh.tmem_base();
+    Walk<NR> k(p, t1 > t0 ? *sh.start_seq() : 0, t1 > t0 ? *sh.start_off() : 0, t1 - t0);
+
+    if (warp < kSmx) {
+        // ================================ softmax ========================================
+        // Control flow is the same in all 512 threads (the barriers need every one of them);
+        // `ok` only guards work and is kept warp-uniform.
+        const int wq = warp & 3, hp = warp >> 2, hb = GR * hp;
+        const int t = wq * 32 + lane;                 // row within the tile
+        const uint32_t lane_base = (uint32_t)(wq * 32) << 16;
+        // the W image: row t is 64 bytes at (t / 8) 512 + (t % 8) 64, 16-byte chunk c at c ^ ((t / 2) % 4).
+        // NR = 64: an image a digit, this part's rows are chunk hp; NR = 32: digit d is chunks
+        // 2 d, 2 d + 1, this part's rows half a chunk
+        const uint32_t w_row = (t >> 3) * 512 + (t & 7) * 64;
+        const int wx = (t >> 1) & 3;
+        float* m_s = sh.m_s();
+        float* m_u = sh.m_u();
+        bool ok = true;
+        int c = 0;                                    // tiles so far
+        bool first_seg = true;
+        int64_t pos = t0;
+        for (int seg = 0; k.more(); ++seg) {
+            const int s = k.s, L = k.L, n = k.n;
+            const int64_t r0 = (int64_t)k.rt * NR;    // first query row of the tile, of the sequence's n * H
+            const int64_t rows = (int64_t)n * p.n_heads - r0;       // rows there are from r0 on
+            const bool whole = k.tile == 0 && k.end == k.nt;
+            const int slot = 2 * g + (first_seg ? 0 : 1);
+            // a unit that starts here tells the combine who shares it
+            if (tid == 0) {
+                const int64_t u_end = pos + k.nt;     // (meaningful if tile == 0)
+                int last = g;
+                while (k.tile == 0 && cut(total, last + 1, G) < u_end) ++last;
+                const bool starts = k.tile == 0;
+                if (a.by_unit ? starts : k.left == k.end - k.tile) {
+                    SplitInfo* f = a.info + (a.by_unit ? (int64_t)s * a.n_rt + k.rt : (int64_t)g);
+                    f->s = s;
+                    f->rt = k.rt;
+                    f->cta = g;
+                    f->slot = slot;
+                    f->pieces = starts ? last - g + 1 : 0;
+                }
+            }
+            for (int i = warp; i < NR; i += kSmx) write_query(sh, p, s, r0 + i, i < rows, i, lane);
+            if (tid < NR) {
+                m_s[tid] = kNoMax;
+                m_u[tid] = kNoMax;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(sh.q_full());
+            smx_barrier();
+            float l[GR];
+#pragma unroll
+            for (int e = 0; e < GR; ++e) l[e] = 0.0f;
+            auto pool_row = [&](int tl) -> int64_t {
+                if (tl >= L) return -1;
+                const int64_t r = tree_pool_row(p, s, tl);
+                if (r < 0 || r >= p.cache.n_rows) {
+                    if (hp == 0 && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_PAGE);
+                    return -1;
+                }
+                return r;
+            };
+            // the pool row and scales of this thread's row, read one tile ahead
+            int64_t row_n = pool_row(k.tile * kRT + t);
+            float ls_n = row_n >= 0 ? p.cache.lat_scale[row_n] : 0.0f;
+            float rs_n = row_n >= 0 ? p.cache.rope_scale[row_n] : 0.0f;
+            for (int i = k.tile; i < k.end; ++i, ++c) {
+                const int st = c & 1, rst = C::kRS == 2 ? st : 0;
+                const bool have = row_n >= 0;
+                const float ls = ls_n, rs = rs_n;
+                if (i + 1 < k.end) {
+                    row_n = pool_row((i + 1) * kRT + t);
+                    ls_n = row_n >= 0 ? p.cache.lat_scale[row_n] : 0.0f;
+                    rs_n = row_n >= 0 ? p.cache.rope_scale[row_n] : 0.0f;
+                }
+                if (ok) ok = wait_bar<true>(sh, sh.s_full(), (uint32_t)c & 1u, a);
+                ok = __all_sync(kFull, ok);
+                float sv[GR];
+#pragma unroll
+                for (int e = 0; e < GR; ++e) sv[e] = -INFINITY;
+                if (ok) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < GR; h += 8) {
+                        uint32_t x0[8], x1[8], y0[8], y1[8];
+                        tmem_ld_x8(tmem + lane_base + C::kColSL + hb + h, x0);
+                        tmem_ld_x8(tmem + lane_base + C::kColSL + NR + hb + h, x1);
+                        tmem_ld_x8(tmem + lane_base + C::kColSR + hb + h, y0);
+                        tmem_ld_x8(tmem + lane_base + C::kColSR + NR + hb + h, y1);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float al = fmaf(__uint_as_float(x1[e]), 0.0625f, __uint_as_float(x0[e]));
+                            const float ar = fmaf(__uint_as_float(y1[e]), 0.0625f, __uint_as_float(y0[e]));
+                            sv[h + e] = sh.qs()[hb + h + e] * fmaf(ls, al, rs * ar);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sh.s_empty());
+                    if (!have) {
+                        // not a row of the sequence: the context reads it as zeros, whatever the box brought
+                        for (int pc = kPieces * hp; pc < kPieces * hp + kPieces; ++pc)
+                            *row_piece(sh, st, rst, t, pc) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                        for (int e = 0; e < GR; ++e) sv[e] = -INFINITY;
+                    } else {
+                        bool bad = false;
+#pragma unroll
+                        for (int e = 0; e < GR; ++e) bad |= isnan(sv[e]);
+                        if (bad && clear_row(sh, st, rst, t, hp)) {
+#pragma unroll
+                            for (int e = 0; e < GR; ++e)
+                                sv[e] = hb + e < rows ? rescore(sh, p, st, rst, t, (int64_t)s * p.n_q * p.n_heads + r0 + hb + e, ls, rs)
+                                                      : 0.0f;
+                        }
+                        if ((i + 1) * kRT > L - n) {      // the drafted rows: only what the node sees
+                            const int kk = i * kRT + t - (L - n);
+                            if (kk >= 0) {
+                                int node = (int)((r0 + hb) / p.n_heads), head = (int)((r0 + hb) % p.n_heads);
+                                uint64_t see = node < n ? tree_visible(p, s, node, n) : 0;
+#pragma unroll
+                                for (int e = 0; e < GR; ++e) {
+                                    if (!((see >> kk) & 1u)) sv[e] = -INFINITY;
+                                    if (++head == p.n_heads) {
+                                        head = 0;
+                                        ++node;
+                                        see = node < n ? tree_visible(p, s, node, n) : 0;
+                                    }
+                                }
+                            }
+                        }
+                    }
+                }
+                // nothing reads this tile's rope keys from here on
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(sh.empty(rst, 4));
+                const float lg = ls > 0.0f ? log2f(ls) : -INFINITY;
+                auto u_of = [&](float x) { return x == -INFINITY ? -INFINITY : x + lg; };
+                bool exceed = false;
+#pragma unroll
+                for (int e = 0; e < GR; e += 4) {
+                    const float4 ms = *reinterpret_cast<const float4*>(m_s + hb + e);
+                    const float4 mu = *reinterpret_cast<const float4*>(m_u + hb + e);
+                    exceed |= sv[e] > ms.x + kLazy || sv[e + 1] > ms.y + kLazy || sv[e + 2] > ms.z + kLazy ||
+                              sv[e + 3] > ms.w + kLazy || u_of(sv[e]) > mu.x + kLazy || u_of(sv[e + 1]) > mu.y + kLazy ||
+                              u_of(sv[e + 2]) > mu.z + kLazy || u_of(sv[e + 3]) > mu.w + kLazy;
+                }
+                bool rescale_o = false;
+                if (smx_any(exceed)) {
+                    float v[GR];
+                    bool moved = false;
+#pragma unroll 1
+                    for (int which = 0; which < 2; ++which) {         // the scores' maxima, then u's
+                        float* m = which ? m_u : m_s;
+                        float* al = which ? sh.al_u() : sh.al_s();
+#pragma unroll
+                        for (int e = 0; e < GR; ++e) v[e] = which ? u_of(sv[e]) : sv[e];
+                        warp_reduce_transpose<true>(v, lane);
+                        if (lane < GR) sh.red()[wq * NR + hb + lane] = v[0];
+                        smx_barrier();
+                        if (tid < NR) {
+                            const float* r = sh.red() + tid;
+                            const float top = fmaxf(fmaxf(r[0], r[NR]), fmaxf(r[2 * NR], r[3 * NR]));
+                            const float old = m[tid];
+                            const bool up = top > old + kLazy;
+                            al[tid] = up ? ex2(old - top) : 1.0f;
+                            if (up) m[tid] = top;
+                            moved = which == 1 && up;
+                        }
+                        smx_barrier();
+                    }
+                    rescale_o = smx_any(moved && i > k.tile);
+#pragma unroll
+                    for (int e = 0; e < GR; ++e) l[e] *= sh.al_s()[hb + e];
+                }
+                // weights and normalizer terms
+                uint32_t w0[GR / 4], w1[GR / 4];
+#pragma unroll
+                for (int e = 0; e < GR; e += 4) {
+                    const float4 ms = *reinterpret_cast<const float4*>(m_s + hb + e);
+                    const float4 mu = *reinterpret_cast<const float4*>(m_u + hb + e);
+                    const float msv[4] = {ms.x, ms.y, ms.z, ms.w}, muv[4] = {mu.x, mu.y, mu.z, mu.w};
+                    float w[4];
+#pragma unroll
+                    for (int d = 0; d < 4; ++d) {
+                        l[e + d] += ex2(sv[e + d] - msv[d]);
+                        w[d] = ex2(u_of(sv[e + d]) - (muv[d] - kBase));
+                    }
+                    digits4<NR == 64 ? 1 : 16>(w, w0[e / 4], w1[e / 4]);
+                }
+                // the context of tile c - 1 has read the W image, and O may be rescaled
+                if (i > k.tile && ok) ok = wait_bar<true>(sh, sh.o_done(), (uint32_t)(c - 1) & 1u, a);
+                ok = __all_sync(kFull, ok);
+                if (rescale_o && ok) {
+                    tc_fence_after();
+                    float au[GR];
+#pragma unroll
+                    for (int e = 0; e < GR; ++e) au[e] = sh.al_u()[hb + e];
+#pragma unroll 1
+                    for (int m = 0; m < 4 * (64 / NR); ++m) {          // (NR = 32: both digits' columns)
+                        const uint32_t col = tmem + lane_base + kColO + NR * m + hb;
+                        uint32_t x[GR];
+                        tmem_ld_n(col, x);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < GR; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * au[e]);
+                        tmem_st_n(col, x);
+                    }
+                    tmem_st_wait();
+                }
+                if (ok) {
+                    if constexpr (NR == 64) {
+                        uint8_t* img = sh.w() + w_row + ((hp ^ wx) << 4);
+                        *reinterpret_cast<uint4*>(img) = make_uint4(w0[0], w0[1], w0[2], w0[3]);
+                        *reinterpret_cast<uint4*>(img + kRT * 64) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+                    } else {
+                        uint8_t* img = sh.w() + w_row + 8 * (hp & 1);
+                        *reinterpret_cast<uint2*>(img + (((hp >> 1) ^ wx) << 4)) = make_uint2(w0[0], w0[1]);
+                        *reinterpret_cast<uint2*>(img + (((2 + (hp >> 1)) ^ wx) << 4)) = make_uint2(w1[0], w1[1]);
+                    }
+                    tc_fence_before();
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sh.p_full());
+                }
+            }
+            // ---- epilogue: l over the 128 rows, then O^T -> out or the partial ---------------
+            if (ok) ok = wait_bar<true>(sh, sh.o_done(), (uint32_t)(c - 1) & 1u, a);
+            ok = __all_sync(kFull, ok);
+            warp_reduce_transpose<false>(l, lane);
+            if (lane < GR) sh.red()[wq * NR + hb + lane] = l[0];
+            const bool aborted = smx_any(!ok);
+            const int64_t out_row = (int64_t)s * p.n_q * p.n_heads + r0;
+            if (tid < NR) {
+                const float* r = sh.red() + tid;
+                const float lt = (r[0] + r[NR]) + (r[2 * NR] + r[3 * NR]);
+                const float ms = m_s[tid], f = ex2(m_u[tid] - kBase - ms);
+                if (whole) {
+                    sh.al_u()[tid] = aborted ? NAN : lt > 0.0f ? f / lt : 0.0f;
+                    if (tid < rows && a.lse) a.lse[out_row + tid] = aborted ? NAN : lt > 0.0f ? (ms + log2f(lt)) * kLn2 : -INFINITY;
+                } else {
+                    sh.al_u()[tid] = f;
+                    reinterpret_cast<float2*>(a.part_ml)[slot * NR + tid] = aborted ? make_float2(INFINITY, INFINITY) : make_float2(ms, lt);
+                }
+            }
+            smx_barrier();
+            tc_fence_after();
+            float fac[GR];
+#pragma unroll
+            for (int e = 0; e < GR; ++e) fac[e] = sh.al_u()[hb + e];
+#pragma unroll 1
+            for (int m = 0; m < 4; ++m) {
+                const int dim = 128 * m + 32 * wq + lane;
+                float o[GR];
+                if (!aborted) {
+                    uint32_t x[GR];
+                    tmem_ld_n(tmem + lane_base + kColO + 64 * m + hb, x);
+                    if constexpr (NR == 32) {
+                        uint32_t y[GR];
+                        tmem_ld_n(tmem + lane_base + kColO + 64 * m + NR + hb, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < GR; ++e) o[e] = fmaf(__uint_as_float(y[e]), 0.0625f, __uint_as_float(x[e])) * fac[e];
+                    } else {
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < GR; ++e) o[e] = __uint_as_float(x[e]) * fac[e];
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < GR; ++e) o[e] = NAN;
+                }
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < GR; ++e)
+                        if (hb + e < rows) a.out[(out_row + hb + e) * kDLat + dim] = __float2bfloat16_rn(o[e]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < GR; ++e) a.part_o[((int64_t)slot * NR + hb + e) * kDLat + dim] = o[e];
+                }
+            }
+            tc_fence_before();
+            smx_barrier();                            // maxima, factors and query scales may change
+            first_seg = false;
+            pos += k.end - k.tile;
+            k.next(p);
+        }
+        if (tid == 0 && !a.by_unit && t1 <= t0) a.info[g].pieces = 0;
+    } else if (warp == kWarpLoad) {
+        // ================================ TMA loader =====================================
+        const int per = kRT / a.box_rows;             // boxes of a 128-dim block; lane = box
+        bool ok = true;
+        int c = 0, nb = 0;                            // tiles so far, boxes of the ring issued
+        for (; k.more() && ok; k.next(p)) {
+            auto box_row = [&](int i) -> int {
+                const int t = i * kRT + lane * a.box_rows;
+                if (lane >= per || t >= k.L) return -1;
+                const int64_t r = tree_pool_row(p, k.s, t);
+                return r < 0 || r >= p.cache.n_rows ? -1 : (int)r;
+            };
+            int yn = box_row(k.tile);
+            for (int i = k.tile; i < k.end && ok; ++i, ++c) {
+                const int st = c & 1, y = yn;
+                if (i + 1 < k.end) yn = box_row(i + 1);
+                const uint32_t n_in = __popc(__ballot_sync(kFull, y >= 0)) * a.box_rows;    // rows that come
+                for (int b = 0; b < kBoxes && ok; ++b) {
+                    const int slot = b < 4 ? st : C::kRS == 2 ? st : 0;
+                    const int use = b < 4 || C::kRS == 2 ? c >> 1 : c;                       // earlier uses of the slot
+                    ok = __all_sync(kFull, wait_bar<false>(sh, sh.empty(slot, b), ((uint32_t)use & 1u) ^ 1u, a));
+                    if (!ok) break;
+                    uint64_t* bar = sh.full(slot, b);
+                    const uint32_t width = b < 4 ? 128 : 64;
+                    if (lane == 0) mbar_arrive_expect_tx(bar, n_in * width);
+                    __syncwarp();
+                    if (y >= 0) {
+                        uint8_t* dst = (b < 4 ? sh.box(st, b) : sh.rope(slot)) + lane * a.box_rows * width;
+                        tma_load_2d(dst, b < 4 ? &a.tm_lat : &a.tm_rope, b < 4 ? 128 * b : 0, y, bar);
+                    }
+                    __syncwarp();
+                    ++nb;
+                }
+                // the next tile waits for a stage: its rows come as far as L2 meanwhile
+                if (ok && i + 1 < k.end && yn >= 0) {
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) tma_prefetch_2d(&a.tm_lat, 128 * b, yn);
+                    tma_prefetch_2d(&a.tm_rope, 0, yn);
+                }
+                __syncwarp();
+            }
+        }
+        // every box issued has landed before the CTA's shared memory is released
+        if (lane == 0) {
+            for (int j = max(0, nb - kStages * kBoxes); j < nb; ++j) {
+                const int ti = j / kBoxes, b = j % kBoxes, ns = b < 4 ? kStages : C::kRS;
+                if (j + ns * kBoxes < nb) continue;   // a later use of the slot implies that it landed
+                const int slot = b < 4 || C::kRS == 2 ? ti & 1 : 0, use = b < 4 || C::kRS == 2 ? ti >> 1 : ti;
+                if (!mbar_wait(sh.full(slot, b), (uint32_t)use & 1u, kTimeoutNs) && a.status)
+                    atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
+            }
+        }
+        __syncwarp();
+    } else if (warp == kWarpS) {
+        // ================================ score MMAs ======================================
+        const bool leader = elect_one();
+        constexpr uint32_t idesc = idesc_e4m3_f32(kRT, C::kNS, false, false);      // C . Qd^T
+        const uint32_t q_addr = smem_u32(sh.q());
+        bool ok = true;
+        int c = 0;
+        for (int seg = 0; k.more() && ok; ++seg, k.next(p)) {
+            ok = __all_sync(kFull, wait_bar<false>(sh, sh.q_full(), (uint32_t)seg & 1u, a));
+            for (int i = k.tile; i < k.end && ok; ++i, ++c) {
+                const int st = c & 1, rst = C::kRS == 2 ? st : 0;
+                const int ruse = C::kRS == 2 ? c >> 1 : c;
+                // S(c) overwrites S(c - 1): the softmax has read it
+                if (c > 0) ok = __all_sync(kFull, wait_bar<false>(sh, sh.s_empty(), (uint32_t)(c - 1) & 1u, a));
+                for (int b = 0; b < kBoxes && ok; ++b) {
+                    ok = __all_sync(kFull, wait_bar<false>(sh, sh.full(b < 4 ? st : rst, b), (uint32_t)(b < 4 ? c >> 1 : ruse) & 1u, a));
+                    if (!ok) break;
+                    tc_fence_after();
+                    if (leader) {
+                        if (b < 4) {
+                            const uint32_t box = smem_u32(sh.box(st, b));
+#pragma unroll
+                            for (int ks = 0; ks < 4; ++ks) {
+                                const uint64_t ad = desc_smem(box + ks * 32, 16, 1024, kSwizzle128);
+                                const uint64_t bd = desc_smem(q_addr + b * C::kQBlk + ks * 32, 16, 1024, kSwizzle128);
+                                mma_e4m3_ss(tmem + C::kColSL, ad, bd, idesc, (b | ks) ? 1u : 0u);
+                            }
+                        } else {
+                            const uint32_t box = smem_u32(sh.rope(rst));
+#pragma unroll
+                            for (int ks = 0; ks < 2; ++ks) {
+                                const uint64_t ad = desc_smem(box + ks * 32, 16, 512, kSwizzle64);
+                                const uint64_t bd = desc_smem(q_addr + C::kQRope + ks * 32, 16, 512, kSwizzle64);
+                                mma_e4m3_ss(tmem + C::kColSR, ad, bd, idesc, ks > 0 ? 1u : 0u);
+                            }
+                            mma_commit(sh.s_full());
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (leader) {
+            mma_commit(sh.drain_s());
+            if (!mbar_wait(sh.drain_s(), 0, kTimeoutNs) && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
+        }
+        __syncwarp();
+    } else {
+        // ================================ context MMAs ====================================
+        const bool leader = elect_one();
+        constexpr uint32_t idesc = idesc_e4m3_f32(kRT, 64, true, true);            // V^T . Wd^T, both MN-major
+        const uint32_t wb = smem_u32(sh.w());
+        bool ok = true;
+        int c = 0;
+        for (; k.more() && ok; k.next(p)) {
+            for (int i = k.tile; i < k.end && ok; ++i, ++c) {
+                ok = __all_sync(kFull, wait_bar<false>(sh, sh.p_full(), (uint32_t)c & 1u, a));
+                if (!ok) break;
+                tc_fence_after();
+                const int st = c & 1;
+                if (leader) {
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) {
+                        const uint32_t box = smem_u32(sh.box(st, m));
+#pragma unroll
+                        for (int d = 0; d < C::kWImgs; ++d) {
+#pragma unroll
+                            for (int ks = 0; ks < kRT / 32; ++ks) {
+                                const uint64_t ad = desc_smem(box + ks * 4096, 16, 1024, kSwizzle128);
+                                const uint64_t bd = desc_smem(wb + d * kRT * 64 + ks * 2048, 16, 512, kSwizzle64);
+                                mma_e4m3_ss(tmem + kColO + 64 * m, ad, bd, idesc, (i == k.tile && d == 0 && ks == 0) ? 0u : 1u);
+                            }
+                        }
+                        mma_commit(sh.empty(st, m));
+                    }
+                    mma_commit(sh.o_done());
+                }
+                __syncwarp();
+            }
+        }
+        if (leader) {
+            mma_commit(sh.drain_c());
+            if (!mbar_wait(sh.drain_c(), 0, kTimeoutNs) && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
+        }
+        __syncwarp();
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == kWarpS) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ------------------------------------------------------------------------------------
+// Padding rows (zeros), then the units that several CTAs shared: CTA = (unit or CTA, row of
+// the tile); its eight warps take the pieces in turn, lane = 16 dims.
+// ------------------------------------------------------------------------------------
+constexpr int kCombThreads = 256;
+
+template <int NR>
+__global__ void __launch_bounds__(kCombThreads) tree_combine_kernel(const __grid_constant__ Args a)
+{
+    __shared__ __align__(16) float s_o[kCombThreads / 32][kDLat];
+    __shared__ float s_l[kCombThreads / 32];
+    const kvq_mla_tree_problem& p = a.p;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t H = p.n_heads;
+    for (int64_t pr = blockIdx.x + (int64_t)gridDim.x * blockIdx.y; pr < (int64_t)p.n_seq * p.n_q; pr += (int64_t)gridDim.x * gridDim.y) {
+        const int2 sh = tree_seq_shape(p, (int)(pr / p.n_q));
+        if (pr % p.n_q < sh.y) continue;              // a node (there is one only if L > 0)
+        uint4* o = reinterpret_cast<uint4*>(a.out + pr * H * kDLat);
+        for (int64_t i = tid; i < H * kDLat / 8; i += kCombThreads) o[i] = make_uint4(0u, 0u, 0u, 0u);
+        for (int64_t i = tid; i < H && a.lse; i += kCombThreads) a.lse[pr * H + i] = -INFINITY;
+    }
+    grid_dependency_wait();
+    if (a.by_unit) {                                  // a unit without tiles has no info
+        const int2 sh = tree_seq_shape(p, blockIdx.x / a.n_rt);
+        if ((int64_t)(blockIdx.x % a.n_rt) * NR + blockIdx.y >= sh.y * H) return;
+    }
+    const SplitInfo f = a.info[blockIdx.x];
+    if (f.pieces < 2) return;
+    const int64_t r = (int64_t)f.rt * NR + blockIdx.y;
+    if (r >= tree_seq_shape(p, f.s).y * H) return;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
+    auto at = [&](int k) { return (int64_t)(k == 0 ? f.slot : 2 * (f.cta + k)) * NR + blockIdx.y; };
+    float M = kNoMax;
+    bool gave_up = false;
+    for (int k = lane; k < f.pieces; k += 32) {
+        const float2 x = ml[at(k)];
+        gave_up |= x.x == INFINITY;
+        M = fmaxf(M, x.x);
+    }
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
+    gave_up = __any_sync(kFull, gave_up);
+    float4 acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float l = 0.0f;
+#pragma unroll 4
+    for (int k = warp; k < f.pieces; k += kCombThreads / 32) {
+        const int64_t i = at(k);
+        const float2 x = ml[i];
+        const float w = ex2(x.x - M);
+        l = fmaf(x.y, w, l);
+        const float4* o = reinterpret_cast<const float4*>(a.part_o + i * kDLat) + lane;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float4 v = o[32 * j];
+            acc[j].x = fmaf(v.x, w, acc[j].x);
+            acc[j].y = fmaf(v.y, w, acc[j].y);
+            acc[j].z = fmaf(v.z, w, acc[j].z);
+            acc[j].w = fmaf(v.w, w, acc[j].w);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<float4*>(s_o[warp])[32 * j + lane] = acc[j];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    float lt = 0.0f;
+    float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int w = 0; w < kCombThreads / 32; ++w) {
+        lt += s_l[w];
+        const float2 v = reinterpret_cast<const float2*>(s_o[w])[tid];
+        o.x += v.x;
+        o.y += v.y;
+    }
+    const float inv = gave_up ? NAN : lt > 0.0f ? 1.0f / lt : 0.0f;
+    const int64_t row = (int64_t)f.s * p.n_q * H + r;
+    reinterpret_cast<__nv_bfloat162*>(a.out + row * kDLat)[tid] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    if (tid == 0 && a.lse) a.lse[row] = gave_up ? NAN : lt > 0.0f ? (M + log2f(lt)) * kLn2 : -INFINITY;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// 64 query rows a tile feed the tensor core best; few rows run in half tiles, whose softmax and
+// epilogue are half as long
+int tile_rows(const kvq_mla_tree_problem& p) { return (int64_t)p.n_q * p.n_heads <= 32 ? 32 : 64; }
+
+int64_t max_units(const kvq_mla_tree_problem& p)
+{
+    const int nr = tile_rows(p);
+    return (int64_t)p.n_seq * (((int64_t)p.n_q * p.n_heads + nr - 1) / nr);
+}
+
+struct PackedPlan {
+    int ctas;
+    int64_t infos;
+    size_t off_ml, off_o, off_info, bytes;
+};
+
+PackedPlan plan_packed(const kvq_mla_tree_problem& p)
+{
+    PackedPlan t{};
+    t.ctas = sm_count();
+    t.infos = std::max<int64_t>(1, std::min<int64_t>(t.ctas, max_units(p)));
+    const size_t rows = (size_t)2 * t.ctas * tile_rows(p);
+    t.off_ml = 0;
+    t.off_o = align256(rows * 2 * sizeof(float));
+    t.off_info = t.off_o + align256(rows * kDLat * sizeof(float));
+    t.bytes = t.off_info + align256((size_t)t.infos * sizeof(SplitInfo));
+    return t;
+}
+
+template <int NR>
+cudaError_t launch_packed_as(Args& a, const PackedPlan& t, cudaStream_t s)
+{
+    int device = 0;
+    cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    static std::atomic<uint64_t> attr_set{0};
+    const uint64_t bit = 1ull << (device & 63);
+    if (!(attr_set.load() & bit)) {
+        e = cudaFuncSetAttribute(tree_packed_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR>::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set.fetch_or(bit);
+    }
+    tree_packed_kernel<NR><<<t.ctas, kThreads, Cfg<NR>::kSmem, s>>>(a);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    return launch_dependent(tree_combine_kernel<NR>, dim3((unsigned)t.infos, NR), dim3(kCombThreads), 0, s, a);
+}
+
+}  // namespace
+
+bool tree_packed_reads(const kvq_mla_tree_problem& p)
+{
+    return p.cache.n_rows <= INT32_MAX && (!p.block_table || p.page_size % 8 == 0);
+}
+
+size_t tree_packed_workspace(const kvq_mla_tree_problem& p) { return plan_packed(p).bytes; }
+
+cudaError_t launch_tree_packed(const kvq_mla_tree_problem& p, void* out, float* lse, void* ws,
+                               uint32_t* dev_status, cudaStream_t s)
+{
+    const PackedPlan t = plan_packed(p);
+    Args a;
+    memset(&a, 0, sizeof(a));
+    // boxes of the largest power of two up to 128 rows that divides a page: none crosses a page
+    a.box_rows = !p.block_table ? kRT : std::min(kRT, p.page_size & -p.page_size);
+    if (p.cache.n_rows > 0 && (!make_code_map(&a.tm_lat, p.cache.lat, p.cache.n_rows, kDLat, 128, a.box_rows) ||
+                               !make_code_map(&a.tm_rope, p.cache.rope, p.cache.n_rows, kDRope, 64, a.box_rows)))
+        return cudaErrorInvalidValue;
+    a.p = p;
+    char* base = static_cast<char*>(ws);
+    a.part_ml = reinterpret_cast<float*>(base + t.off_ml);
+    a.part_o = reinterpret_cast<float*>(base + t.off_o);
+    a.info = reinterpret_cast<SplitInfo*>(base + t.off_info);
+    a.out = static_cast<__nv_bfloat16*>(out);
+    a.lse = lse;
+    a.status = dev_status;
+    a.wait_ns = wait_limit_ns();
+    const int nr = tile_rows(p);
+    a.n_rt = (int)(((int64_t)p.n_q * p.n_heads + nr - 1) / nr);
+    a.by_unit = max_units(p) <= t.ctas ? 1 : 0;
+    return nr == 32 ? launch_packed_as<32>(a, t, s) : launch_packed_as<64>(a, t, s);
+}
+
+}  // namespace kvq
