@@ -353,19 +353,15 @@ __device__ __forceinline__ uint4 clear_unwritten(const uint4& v)
     return make_uint4(clear_unwritten(v.x), clear_unwritten(v.y), clear_unwritten(v.z), clear_unwritten(v.w));
 }
 
-// whether row t holds the pattern; the latent's pieces of part hp are cleared of it in place, so
-// that the context reads them as 0 (a thread that still sees them, or no longer, scores the same)
+// the latent's pieces of part hp of row t cleared of the pattern in place, so that the context
+// reads it as 0 (whether another part has cleared its pieces yet makes no difference to rescore)
 template <int NR>
-__device__ __noinline__ bool clear_row(const Shared<NR>& sh, int st, int rst, int t, int hp)
+__device__ __noinline__ void clear_row(const Shared<NR>& sh, int st, int t, int hp)
 {
-    bool found = false;
-    for (int pc = 0; pc < 36; ++pc) {
-        uint4* ptr = row_piece(sh, st, rst, t, pc);
-        const uint4 v = *ptr, c = clear_unwritten(v);
-        found |= v.x != c.x || v.y != c.y || v.z != c.z || v.w != c.w;
-        if (pc < 32 && pc / kPieces == hp) *ptr = c;
+    for (int pc = kPieces * hp; pc < kPieces * hp + kPieces; ++pc) {
+        uint4* ptr = row_piece(sh, st, 0, t, pc);
+        *ptr = clear_unwritten(*ptr);
     }
-    return found;
 }
 
 // q . row from the codes with the pattern read as 0, in fp32: log2-domain score
@@ -595,11 +591,13 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                         bool bad = false;
 #pragma unroll
                         for (int e = 0; e < GR; ++e) bad |= isnan(sv[e]);
-                        if (bad && clear_row(sh, st, rst, t, hp)) {
+                        if (bad) {
+                            clear_row(sh, st, t, hp);
 #pragma unroll
                             for (int e = 0; e < GR; ++e)
-                                sv[e] = hb + e < rows ? rescore(sh, p, st, rst, t, (int64_t)s * p.n_q * p.n_heads + r0 + hb + e, ls, rs)
-                                                      : 0.0f;
+                                if (isnan(sv[e]))
+                                    sv[e] = hb + e < rows ? rescore(sh, p, st, rst, t, (int64_t)s * p.n_q * p.n_heads + r0 + hb + e, ls, rs)
+                                                          : 0.0f;
                         }
                         if ((i + 1) * kRT > L - n) {      // the drafted rows: only what the node sees
                             const int kk = i * kRT + t - (L - n);
