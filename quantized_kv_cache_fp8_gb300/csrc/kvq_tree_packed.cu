@@ -12,15 +12,17 @@
 //
 // Digits.  An e4m3 rounding keeps 4 significant bits, so q = 2^-sigma (Qd_0 + Qd_1 / 16) holds
 // the 8 bits of a bfloat16 exactly (down to 2^-21 of the row's largest element), and w = Wd_0 +
-// Wd_1 carries a weight to 2^-8 of its value, or to 2^-10 absolute where the second digit is
+// Wd_1 carries a weight to 2^-9 of its value, or to 2^-10 absolute where the second digit is
 // subnormal, on a scale that keeps the largest weight of a row between 2^kBase and 2^8.  The
 // outputs are rounded to bfloat16 (2^-8), so more digits would not show.  With NR = 32 the digits
 // of a weight have N columns of their own (the second one in units of 2^-4); with NR = 64 tensor
 // memory has no room for that and they are summed along K.
 //
-// Softmax: two running maxima per row, m_s over the scores (for the normalizer) and m_u over
-// u = s + log2(latent scale) (for the weights 2^(u - m_u + kBase)); either moves only when a
-// tile exceeds it by more than 2^kLazy, so that O is rescaled rarely.
+// Softmax: one running maximum m per query row, over u = s + log2(latent scale): the weights are
+// 2^(u - m + kBase), the normalizer sums 2^(s - m).  It moves only when a tile exceeds it by more
+// than 2^kLazy, and for the sixteen (eight) rows of one part of the warps at a time, so O is
+// rescaled rarely.  A latent scale below 2^-kTiny counts as 2^-kTiny in m (so that the normalizer
+// stays finite) and its row as zero in the context.
 //
 // Work: the tiles of every (sequence, row tile) unit laid end to end on one line, cut into
 // equal stretches, one per CTA and SM; the cuts come from the lengths on the device, so ragged
@@ -60,14 +62,15 @@ constexpr int kStages = 2;
 constexpr int kSmx = 16;                     // softmax warps: lane quarter w % 4, query rows NR / 4 (w / 4) ..
 constexpr int kWarpLoad = kSmx;
 constexpr int kWarpS = kSmx + 1;             // score MMAs (and tensor memory)
-constexpr int kWarpC = kSmx + 2;             // context MMAs
+// (and warp kSmx + 2: context MMAs)
 constexpr int kThreads = 32 * (kSmx + 3);
 constexpr int kBoxes = 5;                    // four latent blocks and the rope key
 constexpr int kPieces = 8;                   // 16-byte pieces of a latent that each quarter of the warps clears
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 4.0f, kBase = 4.0f;  // kLazy + kBase <= 8: weights stay below 2^8 < 448
-constexpr float kNoMax = -1e30f;             // a maximum over nothing: finite, below any score
+constexpr float kTiny = 96.0f;
+constexpr float kNoMax = -1e30f;             // the maximum of a partial over nothing: below any other
 constexpr uint64_t kTimeoutNs = kDefaultWaitNs;   // drains
 constexpr uint32_t kColO = 256;              // tensor memory: O^T of dims 128 m .. at 256 + 64 m
 
@@ -85,8 +88,9 @@ struct Cfg {
     static constexpr int kOffQ = kOffRope + kRS * kRopeBox;
     static constexpr int kOffW = kOffQ + kQBytes;
     static constexpr int kOffRed = kOffW + kWImgs * kRT * 64;   // [4][NR] f32
-    static constexpr int kOffM = kOffRed + 4 * NR * 4;          // m_s, m_u, al_s, al_u, query scale: [NR] each
-    static constexpr int kOffBar = kOffM + 5 * NR * 4;
+    // per query row [NR]: gain (sm_scale log2 e 2^-sigma), -m, its last move, 2^move (or the output factor)
+    static constexpr int kOffM = kOffRed + 4 * NR * 4;
+    static constexpr int kOffBar = kOffM + 4 * NR * 4;
     // full[2][4], empty[2][4], rope full[2], empty[2], s_full, s_empty, p_full, o_done, q_full, drain_s, drain_c
     static constexpr int kNumBars = 2 * kStages * 4 + 2 * 2 + 7;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;     // tmem base, abort flag, start of the stretch
@@ -128,11 +132,10 @@ struct Shared {
     __device__ uint8_t* q() const { return base + C::kOffQ; }
     __device__ uint8_t* w() const { return base + C::kOffW; }
     __device__ float* red() const { return reinterpret_cast<float*>(base + C::kOffRed); }
-    __device__ float* m_s() const { return reinterpret_cast<float*>(base + C::kOffM); }
-    __device__ float* m_u() const { return m_s() + NR; }
-    __device__ float* al_s() const { return m_s() + 2 * NR; }
-    __device__ float* al_u() const { return m_s() + 3 * NR; }
-    __device__ float* qs() const { return m_s() + 4 * NR; }
+    __device__ float* gain() const { return reinterpret_cast<float*>(base + C::kOffM); }
+    __device__ float* neg_m() const { return gain() + NR; }
+    __device__ float* move() const { return gain() + 2 * NR; }
+    __device__ float* factor() const { return gain() + 3 * NR; }
     __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(base + C::kOffBar) + i; }
     __device__ uint64_t* full(int st, int b) const { return b < 4 ? bar(st * 4 + b) : bar(16 + st); }
     __device__ uint64_t* empty(int st, int b) const { return b < 4 ? bar(8 + st * 4 + b) : bar(18 + st); }
@@ -151,6 +154,7 @@ struct Shared {
 
 // Wait for a phase, bounded by %globaltimer; kSpin polls, otherwise try_wait may suspend the
 // thread (a limit below 100 us, set only to exercise the failure path, always polls).
+constexpr bool kSmxSpin = true;
 template <bool kSpin, int NR>
 __device__ __forceinline__ bool wait_bar(const Shared<NR>& sh, uint64_t* bar, uint32_t parity, const Args& a)
 {
@@ -172,22 +176,65 @@ __device__ __forceinline__ bool wait_bar(const Shared<NR>& sh, uint64_t* bar, ui
 
 __device__ __forceinline__ void smx_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSmx) : "memory"); }
 
-// barrier of the softmax warps; true if `v` holds in any of their threads
-__device__ __forceinline__ bool smx_any(bool v)
+// barrier `id` of `n` threads; true if `v` holds in any of them
+template <int n>
+__device__ __forceinline__ bool barrier_any(int id, bool v)
 {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "barrier.cta.red.or.pred p, 1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r) : "r"((uint32_t)v), "n"(32 * kSmx) : "memory");
+        "barrier.cta.red.or.pred p, %2, %3, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r) : "r"((uint32_t)v), "r"(id), "n"(n) : "memory");
     return r != 0;
 }
+// the four warps of part hp (every lane quarter of the same query rows)
+__device__ __forceinline__ void part_barrier(int hp) { asm volatile("bar.sync %0, 128;" ::"r"(2 + hp) : "memory"); }
 
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// two floats in one register pair, and the arithmetic that Blackwell does on them at once
+typedef uint64_t f32x2;
+__device__ __forceinline__ f32x2 pack2(float lo, float hi)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 unpack2(f32x2 v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// maximum of three (a NaN is passed over)
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
 
 __device__ __forceinline__ int64_t tree_pool_row(const kvq_mla_tree_problem& p, int s, int t)
@@ -276,6 +323,19 @@ __device__ __forceinline__ void digits4(const float* x, uint32_t& d0, uint32_t& 
     }
 }
 
+// two weights -> their two digits.  The weight passes through binary16 (2^-11 of its value, beside
+// the 2^-9 that two digits keep), where the first digit's remainder is exact.
+template <int kScale>
+__device__ __forceinline__ void weight_digits(float2 w, uint32_t& d0, uint32_t& d1)
+{
+    const __half2 h = __float22half2_rn(w);
+    const __nv_fp8x2_storage_t c = __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
+    __half2 r = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
+    if (kScale != 1) r = __hmul2(r, __half2half2(__ushort_as_half(0x4C00)));       // 16
+    d0 = c;
+    d1 = __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
+}
+
 // One warp: query row `r` (of the sequence's n * H; zero past them) into rows i and NR + i of
 // the Q image.  sigma puts the row's largest element in [128, 256).
 template <int NR>
@@ -332,7 +392,7 @@ __device__ __forceinline__ void write_query(const Shared<NR>& sh, const kvq_mla_
         *reinterpret_cast<uint32_t*>(rp + i * 64 + at) = r0;
         *reinterpret_cast<uint32_t*>(rp + (NR + i) * 64 + at) = r1;
     }
-    if (lane == 0) sh.qs()[i] = p.sm_scale * kLog2e * ldexpf(1.0f, -sigma);
+    if (lane == 0) sh.gain()[i] = p.sm_scale * kLog2e * ldexpf(1.0f, -sigma);
 }
 
 // ---- codes that no encoder writes -----------------------------------------------------------
@@ -364,10 +424,10 @@ __device__ __noinline__ void clear_row(const Shared<NR>& sh, int st, int t, int 
     }
 }
 
-// q . row from the codes with the pattern read as 0, in fp32: log2-domain score
+// q . row from the codes with the pattern read as 0, in fp32, in units of the row's gain
 template <int NR>
 __device__ __noinline__ float rescore(const Shared<NR>& sh, const kvq_mla_tree_problem& p, int st, int rst, int t,
-                                      int64_t row, float ls, float rs)
+                                      int64_t row, float gain, float ls, float rs)
 {
     const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(p.q_lat) + row * p.ldq_lat;
     const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q_rope) + row * p.ldq_rope;
@@ -385,7 +445,7 @@ __device__ __noinline__ float rescore(const Shared<NR>& sh, const kvq_mla_tree_p
         if (pc < 32) al += acc;
         else ar += acc;
     }
-    return p.sm_scale * kLog2e * fmaf(ls, al, rs * ar);
+    return gain != 0.0f ? fmaf(ls, al, rs * ar) * (p.sm_scale * kLog2e / gain) : 0.0f;
 }
 
 // tmem <-> 8 or 16 consecutive columns
@@ -493,10 +553,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         // the W image: row t is 64 bytes at (t / 8) 512 + (t % 8) 64, 16-byte chunk c at c ^ ((t / 2) % 4).
         // NR = 64: an image a digit, this part's rows are chunk hp; NR = 32: digit d is chunks
         // 2 d, 2 d + 1, this part's rows half a chunk
+        constexpr uint32_t kAll = (1u << GR) - 1u;
+        const float tiny = ex2(-kTiny);
         const uint32_t w_row = (t >> 3) * 512 + (t & 7) * 64;
         const int wx = (t >> 1) & 3;
-        float* m_s = sh.m_s();
-        float* m_u = sh.m_u();
         bool ok = true;
         int c = 0;                                    // tiles so far
         bool first_seg = true;
@@ -524,16 +584,20 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
             }
             for (int i = warp; i < NR; i += kSmx) write_query(sh, p, s, r0 + i, i < rows, i, lane);
             if (tid < NR) {
-                m_s[tid] = kNoMax;
-                m_u[tid] = kNoMax;
+                sh.neg_m()[tid] = 0.0f;
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(sh.q_full());
             smx_barrier();
-            float l[GR];
+            f32x2 l2[GR / 2];                         // this thread's part of the normalizers
 #pragma unroll
-            for (int e = 0; e < GR; ++e) l[e] = 0.0f;
+            for (int e = 0; e < GR / 2; ++e) l2[e] = 0;
+            const ulonglong2* gain = reinterpret_cast<const ulonglong2*>(sh.gain() + hb);
+            const ulonglong2* neg_m = reinterpret_cast<const ulonglong2*>(sh.neg_m() + hb);
+            const ulonglong2* move = reinterpret_cast<const ulonglong2*>(sh.move() + hb);
+            bool fresh = true;                        // some row of the part has no maximum yet
+            bool mine_fresh = true;                   // lane < GR: row hb + lane has none
             auto pool_row = [&](int tl) -> int64_t {
                 if (tl >= L) return -1;
                 const int64_t r = tree_pool_row(p, s, tl);
@@ -556,13 +620,18 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                     ls_n = row_n >= 0 ? p.cache.lat_scale[row_n] : 0.0f;
                     rs_n = row_n >= 0 ? p.cache.rope_scale[row_n] : 0.0f;
                 }
-                if (ok) ok = wait_bar<true>(sh, sh.s_full(), (uint32_t)c & 1u, a);
+                if (ok) ok = wait_bar<kSmxSpin>(sh, sh.s_full(), (uint32_t)c & 1u, a);
                 ok = __all_sync(kFull, ok);
-                float sv[GR];
+                // t: the scores before the row's gain, then score - m; vis: the query rows that see this
+                // cache row
+                f32x2 t2[GR / 2];
+                uint32_t vis = have ? kAll : 0u;
 #pragma unroll
-                for (int e = 0; e < GR; ++e) sv[e] = -INFINITY;
+                for (int e = 0; e < GR / 2; ++e) t2[e] = 0;
                 if (ok) {
                     tc_fence_after();
+                    const f32x2 vls = pack2(ls, ls), vrs = pack2(rs, rs);
+                    const f32x2 vls16 = pack2(ls * 0.0625f, ls * 0.0625f), vrs16 = pack2(rs * 0.0625f, rs * 0.0625f);
 #pragma unroll
                     for (int h = 0; h < GR; h += 8) {
                         uint32_t x0[8], x1[8], y0[8], y1[8];
@@ -571,42 +640,42 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                         tmem_ld_x8(tmem + lane_base + C::kColSR + hb + h, y0);
                         tmem_ld_x8(tmem + lane_base + C::kColSR + NR + hb + h, y1);
                         tmem_ld_wait();
+                        auto pair = [](const uint32_t (&r)[8], int e) { return pack2(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1])); };
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float al = fmaf(__uint_as_float(x1[e]), 0.0625f, __uint_as_float(x0[e]));
-                            const float ar = fmaf(__uint_as_float(y1[e]), 0.0625f, __uint_as_float(y0[e]));
-                            sv[h + e] = sh.qs()[hb + h + e] * fmaf(ls, al, rs * ar);
-                        }
+                        for (int e = 0; e < 4; ++e)
+                            t2[h / 2 + e] = fma2(pair(x0, e), vls, fma2(pair(x1, e), vls16, fma2(pair(y0, e), vrs, mul2(pair(y1, e), vrs16))));
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sh.s_empty());
-                    if (!have) {
-                        // not a row of the sequence: the context reads it as zeros, whatever the box brought
+                    if (!(have && ls >= tiny)) {
+                        // not a row of the sequence, or a zero row: the context reads it as zeros, whatever
+                        // the box brought
                         for (int pc = kPieces * hp; pc < kPieces * hp + kPieces; ++pc)
                             *row_piece(sh, st, rst, t, pc) = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                        for (int e = 0; e < GR; ++e) sv[e] = -INFINITY;
-                    } else {
-                        bool bad = false;
-#pragma unroll
-                        for (int e = 0; e < GR; ++e) bad |= isnan(sv[e]);
-                        if (bad) {
+                    }
+                    if (have) {
+                        // a code that no encoder writes makes the scores of every query row NaN
+                        if (isnan(unpack2(t2[0]).x)) {
                             clear_row(sh, st, t, hp);
 #pragma unroll
-                            for (int e = 0; e < GR; ++e)
-                                if (isnan(sv[e]))
-                                    sv[e] = hb + e < rows ? rescore(sh, p, st, rst, t, (int64_t)s * p.n_q * p.n_heads + r0 + hb + e, ls, rs)
-                                                          : 0.0f;
+                            for (int e = 0; e < GR; e += 2) {
+                                float v[2];
+#pragma unroll
+                                for (int d = 0; d < 2; ++d)
+                                    v[d] = hb + e + d < rows ? rescore(sh, p, st, rst, t, (int64_t)s * p.n_q * p.n_heads + r0 + hb + e + d,
+                                                                       sh.gain()[hb + e + d], ls, rs) : 0.0f;
+                                t2[e / 2] = pack2(v[0], v[1]);
+                            }
                         }
                         if ((i + 1) * kRT > L - n) {      // the drafted rows: only what the node sees
                             const int kk = i * kRT + t - (L - n);
                             if (kk >= 0) {
                                 int node = (int)((r0 + hb) / p.n_heads), head = (int)((r0 + hb) % p.n_heads);
                                 uint64_t see = node < n ? tree_visible(p, s, node, n) : 0;
-#pragma unroll
+                                vis = 0;
                                 for (int e = 0; e < GR; ++e) {
-                                    if (!((see >> kk) & 1u)) sv[e] = -INFINITY;
+                                    vis |= (uint32_t)((see >> kk) & 1u) << e;
                                     if (++head == p.n_heads) {
                                         head = 0;
                                         ++node;
@@ -618,78 +687,91 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                     }
                 }
                 // nothing reads this tile's rope keys from here on
-                __syncwarp();
+                const bool some_hidden = __any_sync(kFull, vis != kAll);
                 if (ok && lane == 0) mbar_arrive(sh.empty(rst, 4));
-                const float lg = ls > 0.0f ? log2f(ls) : -INFINITY;
-                auto u_of = [&](float x) { return x == -INFINITY ? -INFINITY : x + lg; };
-                bool exceed = false;
+                const float lg = ls >= tiny ? fminf(log2f(ls), 200.0f) : -kTiny;
+                float top = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < GR; e += 4) {
-                    const float4 ms = *reinterpret_cast<const float4*>(m_s + hb + e);
-                    const float4 mu = *reinterpret_cast<const float4*>(m_u + hb + e);
-                    exceed |= sv[e] > ms.x + kLazy || sv[e + 1] > ms.y + kLazy || sv[e + 2] > ms.z + kLazy ||
-                              sv[e + 3] > ms.w + kLazy || u_of(sv[e]) > mu.x + kLazy || u_of(sv[e + 1]) > mu.y + kLazy ||
-                              u_of(sv[e + 2]) > mu.z + kLazy || u_of(sv[e + 3]) > mu.w + kLazy;
+                    const ulonglong2 ga = gain[e / 4], nm = neg_m[e / 4];
+                    t2[e / 2] = fma2(t2[e / 2], ga.x, nm.x);
+                    t2[e / 2 + 1] = fma2(t2[e / 2 + 1], ga.y, nm.y);
                 }
-                bool rescale_o = false;
-                if (smx_any(exceed)) {
+                if (some_hidden) {
+#pragma unroll
+                    for (int e = 0; e < GR; e += 2) {
+                        const float2 f = unpack2(t2[e / 2]);
+                        t2[e / 2] = pack2((vis >> e) & 1u ? f.x : -INFINITY, (vis >> (e + 1)) & 1u ? f.y : -INFINITY);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < GR / 2; ++e) {
+                    const float2 f = unpack2(t2[e]);
+                    top = max3(top, f.x, f.y);
+                }
+                // the maxima of this part's rows move only if one is exceeded by more than 2^kLazy
+                bool moved = false;
+                if (barrier_any<128>(2 + hp, fresh || top + lg > kLazy)) {
+                    const float old = lane < GR ? sh.neg_m()[hb + lane] : 0.0f;
                     float v[GR];
-                    bool moved = false;
-#pragma unroll 1
-                    for (int which = 0; which < 2; ++which) {         // the scores' maxima, then u's
-                        float* m = which ? m_u : m_s;
-                        float* al = which ? sh.al_u() : sh.al_s();
 #pragma unroll
-                        for (int e = 0; e < GR; ++e) v[e] = which ? u_of(sv[e]) : sv[e];
-                        warp_reduce_transpose<true>(v, lane);
-                        if (lane < GR) sh.red()[wq * NR + hb + lane] = v[0];
-                        smx_barrier();
-                        if (tid < NR) {
-                            const float* r = sh.red() + tid;
-                            const float top = fmaxf(fmaxf(r[0], r[NR]), fmaxf(r[2 * NR], r[3 * NR]));
-                            const float old = m[tid];
-                            const bool up = top > old + kLazy;
-                            al[tid] = up ? ex2(old - top) : 1.0f;
-                            if (up) m[tid] = top;
-                            moved = which == 1 && up;
-                        }
-                        smx_barrier();
+                    for (int e = 0; e < GR; e += 2) {
+                        const float2 f = unpack2(t2[e / 2]);
+                        v[e] = f.x + lg;
+                        v[e + 1] = f.y + lg;
                     }
-                    rescale_o = smx_any(moved && i > k.tile);
+                    warp_reduce_transpose<true>(v, lane);
+                    if (lane < GR) sh.red()[wq * NR + hb + lane] = v[0];
+                    part_barrier(hp);
+                    // (each of the part's warps computes and stores the same)
+                    bool up = false;
+                    if (lane < GR) {
+                        const float* r = sh.red() + hb + lane;
+                        const float by = fmaxf(fmaxf(r[0], r[NR]), fmaxf(r[2 * NR], r[3 * NR]));
+                        up = by > kLazy || (mine_fresh && by > -INFINITY);
+                        sh.neg_m()[hb + lane] = up ? old - by : old;
+                        sh.move()[hb + lane] = up ? -by : 0.0f;
+                        sh.factor()[hb + lane] = up && !mine_fresh ? ex2(-by) : 1.0f;
+                        mine_fresh = mine_fresh && !up;
+                    }
+                    moved = __any_sync(kFull, up) && i > k.tile;      // (also orders the stores)
+                    fresh = __any_sync(kFull, lane < GR && mine_fresh);
 #pragma unroll
-                    for (int e = 0; e < GR; ++e) l[e] *= sh.al_s()[hb + e];
+                    for (int e = 0; e < GR; e += 4) {
+                        const ulonglong2 mv = move[e / 4], f = reinterpret_cast<const ulonglong2*>(sh.factor() + hb)[e / 4];
+                        t2[e / 2] = add2(t2[e / 2], mv.x);
+                        t2[e / 2 + 1] = add2(t2[e / 2 + 1], mv.y);
+                        l2[e / 2] = mul2(l2[e / 2], f.x);
+                        l2[e / 2 + 1] = mul2(l2[e / 2 + 1], f.y);
+                    }
                 }
-                // weights and normalizer terms
                 uint32_t w0[GR / 4], w1[GR / 4];
+                const f32x2 up2 = pack2(lg + kBase, lg + kBase);
 #pragma unroll
                 for (int e = 0; e < GR; e += 4) {
-                    const float4 ms = *reinterpret_cast<const float4*>(m_s + hb + e);
-                    const float4 mu = *reinterpret_cast<const float4*>(m_u + hb + e);
-                    const float msv[4] = {ms.x, ms.y, ms.z, ms.w}, muv[4] = {mu.x, mu.y, mu.z, mu.w};
-                    float w[4];
-#pragma unroll
-                    for (int d = 0; d < 4; ++d) {
-                        l[e + d] += ex2(sv[e + d] - msv[d]);
-                        w[d] = ex2(u_of(sv[e + d]) - (muv[d] - kBase));
-                    }
-                    digits4<NR == 64 ? 1 : 16>(w, w0[e / 4], w1[e / 4]);
+                    const float2 va = unpack2(add2(t2[e / 2], up2)), vb = unpack2(add2(t2[e / 2 + 1], up2));
+                    uint32_t a0, a1, b0, b1;
+                    weight_digits<NR == 64 ? 1 : 16>(make_float2(ex2(va.x), ex2(va.y)), a0, a1);
+                    weight_digits<NR == 64 ? 1 : 16>(make_float2(ex2(vb.x), ex2(vb.y)), b0, b1);
+                    w0[e / 4] = a0 | b0 << 16;
+                    w1[e / 4] = a1 | b1 << 16;
                 }
                 // the context of tile c - 1 has read the W image, and O may be rescaled
-                if (i > k.tile && ok) ok = wait_bar<true>(sh, sh.o_done(), (uint32_t)(c - 1) & 1u, a);
+                if (i > k.tile && ok) ok = wait_bar<kSmxSpin>(sh, sh.o_done(), (uint32_t)(c - 1) & 1u, a);
                 ok = __all_sync(kFull, ok);
-                if (rescale_o && ok) {
+                if (moved && ok) {
                     tc_fence_after();
-                    float au[GR];
+                    float f[GR];
 #pragma unroll
-                    for (int e = 0; e < GR; ++e) au[e] = sh.al_u()[hb + e];
+                    for (int e = 0; e < GR; ++e) f[e] = sh.factor()[hb + e];
 #pragma unroll 1
-                    for (int m = 0; m < 4 * (64 / NR); ++m) {          // (NR = 32: both digits' columns)
+                    for (int m = 0; m < 256 / NR; ++m) {               // (NR = 32: both digits' columns)
                         const uint32_t col = tmem + lane_base + kColO + NR * m + hb;
                         uint32_t x[GR];
                         tmem_ld_n(col, x);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < GR; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * au[e]);
+                        for (int e = 0; e < GR; ++e) x[e] = __float_as_uint(__uint_as_float(x[e]) * f[e]);
                         tmem_st_n(col, x);
                     }
                     tmem_st_wait();
@@ -709,31 +791,45 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sh.p_full());
                 }
+                // the normalizers, while the context runs
+#pragma unroll
+                for (int e = 0; e < GR / 2; ++e) {
+                    const float2 f = unpack2(t2[e]);
+                    l2[e] = add2(l2[e], pack2(ex2(f.x), ex2(f.y)));
+                }
             }
             // ---- epilogue: l over the 128 rows, then O^T -> out or the partial ---------------
-            if (ok) ok = wait_bar<true>(sh, sh.o_done(), (uint32_t)(c - 1) & 1u, a);
+            if (ok) ok = wait_bar<kSmxSpin>(sh, sh.o_done(), (uint32_t)(c - 1) & 1u, a);
             ok = __all_sync(kFull, ok);
+            float l[GR];
+#pragma unroll
+            for (int e = 0; e < GR; e += 2) {
+                l[e] = unpack2(l2[e / 2]).x;
+                l[e + 1] = unpack2(l2[e / 2]).y;
+            }
             warp_reduce_transpose<false>(l, lane);
             if (lane < GR) sh.red()[wq * NR + hb + lane] = l[0];
-            const bool aborted = smx_any(!ok);
+            const bool aborted = barrier_any<32 * kSmx>(1, !ok);
             const int64_t out_row = (int64_t)s * p.n_q * p.n_heads + r0;
             if (tid < NR) {
                 const float* r = sh.red() + tid;
                 const float lt = (r[0] + r[NR]) + (r[2 * NR] + r[3 * NR]);
-                const float ms = m_s[tid], f = ex2(m_u[tid] - kBase - ms);
+                const float m = -sh.neg_m()[tid], unit = ex2(-kBase);
                 if (whole) {
-                    sh.al_u()[tid] = aborted ? NAN : lt > 0.0f ? f / lt : 0.0f;
-                    if (tid < rows && a.lse) a.lse[out_row + tid] = aborted ? NAN : lt > 0.0f ? (ms + log2f(lt)) * kLn2 : -INFINITY;
+                    sh.factor()[tid] = lt > 0.0f ? unit / lt : lt == 0.0f ? 0.0f : NAN;
+                    if (tid < rows && a.lse)
+                        a.lse[out_row + tid] = aborted ? NAN : lt == 0.0f ? -INFINITY : (m + log2f(lt)) * kLn2;
                 } else {
-                    sh.al_u()[tid] = f;
-                    reinterpret_cast<float2*>(a.part_ml)[slot * NR + tid] = aborted ? make_float2(INFINITY, INFINITY) : make_float2(ms, lt);
+                    sh.factor()[tid] = unit;
+                    reinterpret_cast<float2*>(a.part_ml)[slot * NR + tid] =
+                        aborted ? make_float2(INFINITY, INFINITY) : make_float2(lt == 0.0f ? kNoMax : m, lt);
                 }
             }
             smx_barrier();
             tc_fence_after();
             float fac[GR];
 #pragma unroll
-            for (int e = 0; e < GR; ++e) fac[e] = sh.al_u()[hb + e];
+            for (int e = 0; e < GR; ++e) fac[e] = sh.factor()[hb + e];
 #pragma unroll 1
             for (int m = 0; m < 4; ++m) {
                 const int dim = 128 * m + 32 * wq + lane;
@@ -995,10 +1091,10 @@ __global__ void __launch_bounds__(kCombThreads) tree_combine_kernel(const __grid
         o.x += v.x;
         o.y += v.y;
     }
-    const float inv = gave_up ? NAN : lt > 0.0f ? 1.0f / lt : 0.0f;
+    const float inv = gave_up ? NAN : lt == 0.0f ? 0.0f : 1.0f / lt;
     const int64_t row = (int64_t)f.s * p.n_q * H + r;
     reinterpret_cast<__nv_bfloat162*>(a.out + row * kDLat)[tid] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    if (tid == 0 && a.lse) a.lse[row] = gave_up ? NAN : lt > 0.0f ? (M + log2f(lt)) * kLn2 : -INFINITY;
+    if (tid == 0 && a.lse) a.lse[row] = gave_up ? NAN : lt == 0.0f ? -INFINITY : (M + log2f(lt)) * kLn2;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
