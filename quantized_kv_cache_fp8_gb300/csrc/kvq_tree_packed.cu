@@ -62,8 +62,12 @@ constexpr int kStages = 2;
 constexpr int kSmx = 16;                     // softmax warps: lane quarter w % 4, query rows NR / 4 (w / 4) ..
 constexpr int kWarpLoad = kSmx;
 constexpr int kWarpS = kSmx + 1;             // score MMAs (and tensor memory)
-// (and warp kSmx + 2: context MMAs)
-constexpr int kThreads = 32 * (kSmx + 3);
+constexpr int kWarpC = kSmx + 2;             // context MMAs
+constexpr int kThreads = 32 * (kSmx + 4);    // (whole warpgroups: the last warp idles)
+// registers a thread: of the launch's 96 the softmax takes 104 and the rest 64 (with 96 each the
+// softmax spills)
+constexpr int kRegsSmx = 104, kRegsRest = 64;
+constexpr int kRegsNeeded = 32 * kSmx * kRegsSmx + 128 * kRegsRest;
 constexpr int kBoxes = 5;                    // four latent blocks and the rope key
 constexpr int kPieces = 8;                   // 16-byte pieces of a latent that each quarter of the warps clears
 constexpr float kLog2e = 1.4426950408889634f;
@@ -154,7 +158,7 @@ struct Shared {
 
 // Wait for a phase, bounded by %globaltimer; kSpin polls, otherwise try_wait may suspend the
 // thread (a limit below 100 us, set only to exercise the failure path, always polls).
-constexpr bool kSmxSpin = true;
+constexpr bool kSmxSpin = false;
 template <bool kSpin, int NR>
 __device__ __forceinline__ bool wait_bar(const Shared<NR>& sh, uint64_t* bar, uint32_t parity, const Args& a)
 {
@@ -244,6 +248,12 @@ __device__ __forceinline__ int64_t tree_pool_row(const kvq_mla_tree_problem& p, 
     if (page >= p.max_pages) return -1;
     const int pid = p.block_table[(int64_t)s * p.max_pages + page];
     return pid < 0 ? -1 : (int64_t)pid * p.page_size + t % p.page_size;
+}
+
+// the `bytes` at p (both multiples of 16) on their way to L2
+__device__ __forceinline__ void l2_prefetch(const void* p, int bytes)
+{
+    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
 // ---- the line of tiles --------------------------------------------------------------------
@@ -544,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
     Walk<NR> k(p, t1 > t0 ? *sh.start_seq() : 0, t1 > t0 ? *sh.start_off() : 0, t1 - t0);
 
     if (warp < kSmx) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSmx));
         // ================================ softmax ========================================
         // Control flow is the same in all 512 threads (the barriers need every one of them);
         // `ok` only guards work and is kept warp-uniform.
@@ -615,6 +626,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 const int st = c & 1, rst = C::kRS == 2 ? st : 0;
                 const bool have = row_n >= 0;
                 const float ls = ls_n, rs = rs_n;
+                const float lg = ls >= tiny ? fminf(log2f(ls), 200.0f) : -kTiny;
+                const bool zero_row = !(have && ls >= tiny);
                 if (i + 1 < k.end) {
                     row_n = pool_row((i + 1) * kRT + t);
                     ls_n = row_n >= 0 ? p.cache.lat_scale[row_n] : 0.0f;
@@ -648,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(sh.s_empty());
-                    if (!(have && ls >= tiny)) {
+                    if (zero_row) {
                         // not a row of the sequence, or a zero row: the context reads it as zeros, whatever
                         // the box brought
                         for (int pc = kPieces * hp; pc < kPieces * hp + kPieces; ++pc)
@@ -658,14 +671,15 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                         // a code that no encoder writes makes the scores of every query row NaN
                         if (isnan(unpack2(t2[0]).x)) {
                             clear_row(sh, st, t, hp);
+#pragma unroll 1
+                            for (int e = 0; e < GR; ++e) {
+                                const float v = hb + e < rows ? rescore(sh, p, st, rst, t, (int64_t)s * p.n_q * p.n_heads + r0 + hb + e,
+                                                                        sh.gain()[hb + e], ls, rs) : 0.0f;
 #pragma unroll
-                            for (int e = 0; e < GR; e += 2) {
-                                float v[2];
-#pragma unroll
-                                for (int d = 0; d < 2; ++d)
-                                    v[d] = hb + e + d < rows ? rescore(sh, p, st, rst, t, (int64_t)s * p.n_q * p.n_heads + r0 + hb + e + d,
-                                                                       sh.gain()[hb + e + d], ls, rs) : 0.0f;
-                                t2[e / 2] = pack2(v[0], v[1]);
+                                for (int d = 0; d < GR; d += 2) {
+                                    const float2 f = unpack2(t2[d / 2]);
+                                    t2[d / 2] = pack2(d == e ? v : f.x, d + 1 == e ? v : f.y);
+                                }
                             }
                         }
                         if ((i + 1) * kRT > L - n) {      // the drafted rows: only what the node sees
@@ -689,7 +703,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 // nothing reads this tile's rope keys from here on
                 const bool some_hidden = __any_sync(kFull, vis != kAll);
                 if (ok && lane == 0) mbar_arrive(sh.empty(rst, 4));
-                const float lg = ls >= tiny ? fminf(log2f(ls), 200.0f) : -kTiny;
                 float top = -INFINITY;
 #pragma unroll
                 for (int e = 0; e < GR; e += 4) {
@@ -868,22 +881,27 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
             k.next(p);
         }
         if (tid == 0 && !a.by_unit && t1 <= t0) a.info[g].pieces = 0;
-    } else if (warp == kWarpLoad) {
+    } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
+    if (warp == kWarpLoad) {
         // ================================ TMA loader =====================================
-        const int per = kRT / a.box_rows;             // boxes of a 128-dim block; lane = box
+        // (one thread issues the copies: from several lanes they would go out one by one with a loop
+        // around each)
+        const bool leader = elect_one();
+        const int per = kRT / a.box_rows;             // copies a 128-dim block; lane = copy for the lookups
         bool ok = true;
         int c = 0, nb = 0;                            // tiles so far, boxes of the ring issued
         for (; k.more() && ok; k.next(p)) {
-            auto box_row = [&](int i) -> int {
+            auto copy_row = [&](int i) -> int {       // the pool row where copy `lane` of tile i begins
                 const int t = i * kRT + lane * a.box_rows;
                 if (lane >= per || t >= k.L) return -1;
                 const int64_t r = tree_pool_row(p, k.s, t);
                 return r < 0 || r >= p.cache.n_rows ? -1 : (int)r;
             };
-            int yn = box_row(k.tile);
+            int yn = copy_row(k.tile);
             for (int i = k.tile; i < k.end && ok; ++i, ++c) {
                 const int st = c & 1, y = yn;
-                if (i + 1 < k.end) yn = box_row(i + 1);
+                if (i + 1 < k.end) yn = copy_row(i + 1);
                 const uint32_t n_in = __popc(__ballot_sync(kFull, y >= 0)) * a.box_rows;    // rows that come
                 for (int b = 0; b < kBoxes && ok; ++b) {
                     const int slot = b < 4 ? st : C::kRS == 2 ? st : 0;
@@ -891,27 +909,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                     ok = __all_sync(kFull, wait_bar<false>(sh, sh.empty(slot, b), ((uint32_t)use & 1u) ^ 1u, a));
                     if (!ok) break;
                     uint64_t* bar = sh.full(slot, b);
-                    const uint32_t width = b < 4 ? 128 : 64;
-                    if (lane == 0) mbar_arrive_expect_tx(bar, n_in * width);
-                    __syncwarp();
-                    if (y >= 0) {
-                        uint8_t* dst = (b < 4 ? sh.box(st, b) : sh.rope(slot)) + lane * a.box_rows * width;
-                        tma_load_2d(dst, b < 4 ? &a.tm_lat : &a.tm_rope, b < 4 ? 128 * b : 0, y, bar);
+                    const int width = b < 4 ? 128 : 64;
+                    uint8_t* dst = b < 4 ? sh.box(st, b) : sh.rope(slot);
+                    if (leader) mbar_arrive_expect_tx(bar, n_in * width);
+                    for (int h = 0; h < per; ++h) {
+                        const int yh = __shfl_sync(kFull, y, h);
+                        if (leader && yh >= 0)
+                            tma_load_2d(dst + h * a.box_rows * width, b < 4 ? &a.tm_lat : &a.tm_rope, b < 4 ? 128 * b : 0, yh, bar);
                     }
-                    __syncwarp();
                     ++nb;
                 }
                 // the next tile waits for a stage: its rows come as far as L2 meanwhile
-                if (ok && i + 1 < k.end && yn >= 0) {
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) tma_prefetch_2d(&a.tm_lat, 128 * b, yn);
-                    tma_prefetch_2d(&a.tm_rope, 0, yn);
+                for (int h = 0; h < per && ok && i + 1 < k.end; ++h) {
+                    const int yh = __shfl_sync(kFull, yn, h);
+                    const int rows_h = (int)min((int64_t)a.box_rows, p.cache.n_rows - yh);
+                    if (leader && yh >= 0) {
+                        l2_prefetch(p.cache.lat + (int64_t)yh * kDLat, rows_h * kDLat);
+                        l2_prefetch(p.cache.rope + (int64_t)yh * kDRope, rows_h * kDRope);
+                    }
                 }
                 __syncwarp();
             }
         }
         // every box issued has landed before the CTA's shared memory is released
-        if (lane == 0) {
+        if (leader) {
             for (int j = max(0, nb - kStages * kBoxes); j < nb; ++j) {
                 const int ti = j / kBoxes, b = j % kBoxes, ns = b < 4 ? kStages : C::kRS;
                 if (j + ns * kBoxes < nb) continue;   // a later use of the slot implies that it landed
@@ -968,7 +989,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
             if (!mbar_wait(sh.drain_s(), 0, kTimeoutNs) && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
         }
         __syncwarp();
-    } else {
+    } else if (warp == kWarpC) {
         // ================================ context MMAs ====================================
         const bool leader = elect_one();
         constexpr uint32_t idesc = idesc_e4m3_f32(kRT, 64, true, true);            // V^T . Wd^T, both MN-major
@@ -1006,6 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
             if (!mbar_wait(sh.drain_c(), 0, kTimeoutNs) && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
         }
         __syncwarp();
+    }
     }
 
     tc_fence_before();
@@ -1137,6 +1159,11 @@ cudaError_t launch_packed_as(Args& a, const PackedPlan& t, cudaStream_t s)
     static std::atomic<uint64_t> attr_set{0};
     const uint64_t bit = 1ull << (device & 63);
     if (!(attr_set.load() & bit)) {
+        // the split above waits for ever if the launch has fewer registers than it hands out
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, tree_packed_kernel<NR>);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs * kThreads < kRegsNeeded) return cudaErrorLaunchOutOfResources;
         e = cudaFuncSetAttribute(tree_packed_kernel<NR>, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg<NR>::kSmem);
         if (e != cudaSuccess) return e;
         attr_set.fetch_or(bit);
