@@ -60,10 +60,11 @@ constexpr int kBox = kRT * 128;              // [128 rows x 128 dims] codes
 constexpr int kRopeBox = kRT * 64;
 constexpr int kStages = 2;
 constexpr int kSmx = 16;                     // softmax warps: lane quarter w % 4, query rows NR / 4 (w / 4) ..
-constexpr int kWarpLoad = kSmx;
+constexpr int kWarpLoad = kSmx;            // TMA: the first two latent blocks
 constexpr int kWarpS = kSmx + 1;             // score MMAs (and tensor memory)
 constexpr int kWarpC = kSmx + 2;             // context MMAs
-constexpr int kThreads = 32 * (kSmx + 4);    // (whole warpgroups: the last warp idles)
+constexpr int kWarpLoad2 = kSmx + 3;         // TMA: the other two and the rope key
+constexpr int kThreads = 32 * (kSmx + 4);
 // registers a thread: of the launch's 96 the softmax takes 104 and the rest 64 (with 96 each the
 // softmax spills)
 constexpr int kRegsSmx = 104, kRegsRest = 64;
@@ -98,7 +99,8 @@ struct Cfg {
     // full[2][4], empty[2][4], rope full[2], empty[2], s_full, s_empty, p_full, o_done, q_full, drain_s, drain_c
     static constexpr int kNumBars = 2 * kStages * 4 + 2 * 2 + 7;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;     // tmem base, abort flag, start of the stretch
-    static constexpr int kSmem = kOffMisc + 32;
+    static constexpr int kOffRows = kOffMisc + 32;              // [2][2][16] pool rows of a tile's copies
+    static constexpr int kSmem = kOffRows + 4 * 16 * 4;
     static_assert(kSmem <= 227 * 1024, "shared memory");
     static_assert(kOffQ % 1024 == 0 && kQBlk % 1024 == 0 && kOffW % 1024 == 0 && kOffBar % 16 == 0, "swizzle atoms");
     static_assert(kColSR + kNS <= kColO, "tensor memory");
@@ -153,12 +155,14 @@ struct Shared {
     __device__ uint32_t* tmem_base() const { return reinterpret_cast<uint32_t*>(base + C::kOffMisc); }
     __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(base + C::kOffMisc + 4); }
     __device__ volatile int64_t* start_off() const { return reinterpret_cast<volatile int64_t*>(base + C::kOffMisc + 8); }
+    __device__ volatile int* copy_rows(int i) const { return reinterpret_cast<volatile int*>(base + C::kOffRows) + 16 * i; }
     __device__ volatile int* start_seq() const { return reinterpret_cast<volatile int*>(base + C::kOffMisc + 16); }
 };
 
-// Wait for a phase, bounded by %globaltimer; kSpin polls, otherwise try_wait may suspend the
-// thread (a limit below 100 us, set only to exercise the failure path, always polls).
-constexpr bool kSmxSpin = false;
+// Wait for a phase, bounded by %globaltimer.  The one-thread roles poll (kSpin): a thread that
+// sleeps in try_wait was seen to wake 1500 cycles late.  The 512 softmax threads sleep, so that
+// their polls stay out of the shared memory pipe (a limit below 100 us, set only to exercise the
+// failure path, always polls).
 template <bool kSpin, int NR>
 __device__ __forceinline__ bool wait_bar(const Shared<NR>& sh, uint64_t* bar, uint32_t parity, const Args& a)
 {
@@ -167,7 +171,7 @@ __device__ __forceinline__ bool wait_bar(const Shared<NR>& sh, uint64_t* bar, ui
     const uint64_t t0 = globaltimer_ns();
     for (;;) {
 #pragma unroll 1
-        for (int k = 0; k < 4; ++k)
+        for (int k = 0; k < (kSpin ? 32 : 4); ++k)
             if (spin ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity)) return true;
         if (*sh.abort_flag()) return false;
         if (globaltimer_ns() - t0 > a.wait_ns) {
@@ -177,6 +181,7 @@ __device__ __forceinline__ bool wait_bar(const Shared<NR>& sh, uint64_t* bar, ui
         }
     }
 }
+constexpr bool kSmxSpin = false, kRoleSpin = true;
 
 __device__ __forceinline__ void smx_barrier() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kSmx) : "memory"); }
 
@@ -883,62 +888,77 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         if (tid == 0 && !a.by_unit && t1 <= t0) a.info[g].pieces = 0;
     } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
-    if (warp == kWarpLoad) {
+    if (warp == kWarpLoad || warp == kWarpLoad2) {
         // ================================ TMA loader =====================================
-        // (one thread issues the copies: from several lanes they would go out one by one with a loop
-        // around each)
+        // The lanes look up a tile's pool rows one tile ahead, one thread issues its copies.
         const bool leader = elect_one();
-        const int per = kRT / a.box_rows;             // copies a 128-dim block; lane = copy for the lookups
+        const int per = kRT / a.box_rows;             // copies a 128-dim block
+        const int who = warp == kWarpLoad ? 0 : 1, b0 = who ? 2 : 0, b1 = who ? kBoxes : 2;
         bool ok = true;
-        int c = 0, nb = 0;                            // tiles so far, boxes of the ring issued
+        int c = 0;                                    // tiles so far
+        int done[3] = {0, 0, 0};                      // tiles whose box went out: this warp's blocks, the rope key
         for (; k.more() && ok; k.next(p)) {
-            auto copy_row = [&](int i) -> int {       // the pool row where copy `lane` of tile i begins
+            auto look_up = [&](int i, int buf) {      // the pool row where copy `lane` of tile i begins
                 const int t = i * kRT + lane * a.box_rows;
-                if (lane >= per || t >= k.L) return -1;
-                const int64_t r = tree_pool_row(p, k.s, t);
-                return r < 0 || r >= p.cache.n_rows ? -1 : (int)r;
+                if (lane < per) {
+                    const int64_t r = t < k.L ? tree_pool_row(p, k.s, t) : -1;
+                    sh.copy_rows(2 * who + buf)[lane] = r < 0 || r >= p.cache.n_rows ? -1 : (int)r;
+                }
             };
-            int yn = copy_row(k.tile);
+            look_up(k.tile, c & 1);
+            __syncwarp();
             for (int i = k.tile; i < k.end && ok; ++i, ++c) {
-                const int st = c & 1, y = yn;
-                if (i + 1 < k.end) yn = copy_row(i + 1);
-                const uint32_t n_in = __popc(__ballot_sync(kFull, y >= 0)) * a.box_rows;    // rows that come
-                for (int b = 0; b < kBoxes && ok; ++b) {
-                    const int slot = b < 4 ? st : C::kRS == 2 ? st : 0;
-                    const int use = b < 4 || C::kRS == 2 ? c >> 1 : c;                       // earlier uses of the slot
-                    ok = __all_sync(kFull, wait_bar<false>(sh, sh.empty(slot, b), ((uint32_t)use & 1u) ^ 1u, a));
-                    if (!ok) break;
-                    uint64_t* bar = sh.full(slot, b);
-                    const int width = b < 4 ? 128 : 64;
-                    uint8_t* dst = b < 4 ? sh.box(st, b) : sh.rope(slot);
-                    if (leader) mbar_arrive_expect_tx(bar, n_in * width);
-                    for (int h = 0; h < per; ++h) {
-                        const int yh = __shfl_sync(kFull, y, h);
-                        if (leader && yh >= 0)
-                            tma_load_2d(dst + h * a.box_rows * width, b < 4 ? &a.tm_lat : &a.tm_rope, b < 4 ? 128 * b : 0, yh, bar);
-                    }
-                    ++nb;
-                }
-                // the next tile waits for a stage: its rows come as far as L2 meanwhile
-                for (int h = 0; h < per && ok && i + 1 < k.end; ++h) {
-                    const int yh = __shfl_sync(kFull, yn, h);
-                    const int rows_h = (int)min((int64_t)a.box_rows, p.cache.n_rows - yh);
-                    if (leader && yh >= 0) {
-                        l2_prefetch(p.cache.lat + (int64_t)yh * kDLat, rows_h * kDLat);
-                        l2_prefetch(p.cache.rope + (int64_t)yh * kDRope, rows_h * kDRope);
+                if (leader) {
+                    const int st = c & 1;
+                    volatile int* y = sh.copy_rows(2 * who + st);
+                    uint32_t n_in = 0;                // rows that come
+                    for (int h = 0; h < per; ++h) n_in += y[h] >= 0 ? a.box_rows : 0;
+#pragma unroll
+                    for (int b = 0; b < kBoxes; ++b) {
+                        if (b < b0 || b >= b1) continue;
+                        const int slot = b < 4 ? st : C::kRS == 2 ? st : 0;
+                        const int use = b < 4 || C::kRS == 2 ? c >> 1 : c;                   // earlier uses of the slot
+                        ok = ok && wait_bar<kRoleSpin>(sh, sh.empty(slot, b), ((uint32_t)use & 1u) ^ 1u, a);
+                        if (!ok) break;
+                        uint64_t* bar = sh.full(slot, b);
+                        const int width = b < 4 ? 128 : 64;
+                        uint8_t* dst = b < 4 ? sh.box(st, b) : sh.rope(slot);
+                        mbar_arrive_expect_tx(bar, n_in * width);
+                        for (int h = 0; h < per; ++h) {
+                            const int yh = y[h];
+                            if (yh >= 0) {
+                                if (b < 4) tma_load_2d(dst + h * a.box_rows * width, &a.tm_lat, 128 * b, yh, bar);
+                                else tma_load_2d(dst + h * a.box_rows * width, &a.tm_rope, 0, yh, bar);
+                            }
+                        }
+                        done[b < 4 ? b & 1 : 2] = c + 1;
                     }
                 }
-                __syncwarp();
+                if (i + 1 < k.end) {
+                    look_up(i + 1, (c + 1) & 1);
+                    // the next tile waits for a stage: its rows come as far as L2 meanwhile
+                    if (who == 0 && lane < per) {
+                        const int y = sh.copy_rows(2 * who + ((c + 1) & 1))[lane];
+                        if (y >= 0) {
+                            const int n = (int)min((int64_t)a.box_rows, p.cache.n_rows - y);
+                            l2_prefetch(p.cache.lat + (int64_t)y * kDLat, n * kDLat);
+                            l2_prefetch(p.cache.rope + (int64_t)y * kDRope, n * kDRope);
+                        }
+                    }
+                }
+                ok = __any_sync(kFull, leader && ok);
             }
         }
         // every box issued has landed before the CTA's shared memory is released
         if (leader) {
-            for (int j = max(0, nb - kStages * kBoxes); j < nb; ++j) {
-                const int ti = j / kBoxes, b = j % kBoxes, ns = b < 4 ? kStages : C::kRS;
-                if (j + ns * kBoxes < nb) continue;   // a later use of the slot implies that it landed
-                const int slot = b < 4 || C::kRS == 2 ? ti & 1 : 0, use = b < 4 || C::kRS == 2 ? ti >> 1 : ti;
-                if (!mbar_wait(sh.full(slot, b), (uint32_t)use & 1u, kTimeoutNs) && a.status)
-                    atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
+#pragma unroll
+            for (int b = 0; b < kBoxes; ++b) {
+                if (b < b0 || b >= b1) continue;
+                const int n = done[b < 4 ? b & 1 : 2], ns = b < 4 ? kStages : C::kRS;
+                for (int i = max(0, n - ns); i < n; ++i) {        // (an earlier use landed before a later one)
+                    if (!mbar_wait(sh.full(i % ns, b), (uint32_t)(i / ns) & 1u, kTimeoutNs) && a.status)
+                        atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
+                }
             }
         }
         __syncwarp();
@@ -947,40 +967,38 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         const bool leader = elect_one();
         constexpr uint32_t idesc = idesc_e4m3_f32(kRT, C::kNS, false, false);      // C . Qd^T
         const uint32_t q_addr = smem_u32(sh.q());
-        bool ok = true;
+        bool ok = leader;
         int c = 0;
         for (int seg = 0; k.more() && ok; ++seg, k.next(p)) {
-            ok = __all_sync(kFull, wait_bar<false>(sh, sh.q_full(), (uint32_t)seg & 1u, a));
+            ok = wait_bar<kRoleSpin>(sh, sh.q_full(), (uint32_t)seg & 1u, a);
             for (int i = k.tile; i < k.end && ok; ++i, ++c) {
                 const int st = c & 1, rst = C::kRS == 2 ? st : 0;
                 const int ruse = C::kRS == 2 ? c >> 1 : c;
                 // S(c) overwrites S(c - 1): the softmax has read it
-                if (c > 0) ok = __all_sync(kFull, wait_bar<false>(sh, sh.s_empty(), (uint32_t)(c - 1) & 1u, a));
-                for (int b = 0; b < kBoxes && ok; ++b) {
-                    ok = __all_sync(kFull, wait_bar<false>(sh, sh.full(b < 4 ? st : rst, b), (uint32_t)(b < 4 ? c >> 1 : ruse) & 1u, a));
+                if (c > 0) ok = wait_bar<kRoleSpin>(sh, sh.s_empty(), (uint32_t)(c - 1) & 1u, a);
+#pragma unroll
+                for (int b = 0; b < kBoxes; ++b) {
+                    ok = ok && wait_bar<kRoleSpin>(sh, sh.full(b < 4 ? st : rst, b), (uint32_t)(b < 4 ? c >> 1 : ruse) & 1u, a);
                     if (!ok) break;
                     tc_fence_after();
-                    if (leader) {
-                        if (b < 4) {
-                            const uint32_t box = smem_u32(sh.box(st, b));
+                    if (b < 4) {
+                        const uint32_t box = smem_u32(sh.box(st, b));
 #pragma unroll
-                            for (int ks = 0; ks < 4; ++ks) {
-                                const uint64_t ad = desc_smem(box + ks * 32, 16, 1024, kSwizzle128);
-                                const uint64_t bd = desc_smem(q_addr + b * C::kQBlk + ks * 32, 16, 1024, kSwizzle128);
-                                mma_e4m3_ss(tmem + C::kColSL, ad, bd, idesc, (b | ks) ? 1u : 0u);
-                            }
-                        } else {
-                            const uint32_t box = smem_u32(sh.rope(rst));
-#pragma unroll
-                            for (int ks = 0; ks < 2; ++ks) {
-                                const uint64_t ad = desc_smem(box + ks * 32, 16, 512, kSwizzle64);
-                                const uint64_t bd = desc_smem(q_addr + C::kQRope + ks * 32, 16, 512, kSwizzle64);
-                                mma_e4m3_ss(tmem + C::kColSR, ad, bd, idesc, ks > 0 ? 1u : 0u);
-                            }
-                            mma_commit(sh.s_full());
+                        for (int ks = 0; ks < 4; ++ks) {
+                            const uint64_t ad = desc_smem(box + ks * 32, 16, 1024, kSwizzle128);
+                            const uint64_t bd = desc_smem(q_addr + b * C::kQBlk + ks * 32, 16, 1024, kSwizzle128);
+                            mma_e4m3_ss(tmem + C::kColSL, ad, bd, idesc, (b | ks) ? 1u : 0u);
                         }
+                    } else {
+                        const uint32_t box = smem_u32(sh.rope(rst));
+#pragma unroll
+                        for (int ks = 0; ks < 2; ++ks) {
+                            const uint64_t ad = desc_smem(box + ks * 32, 16, 512, kSwizzle64);
+                            const uint64_t bd = desc_smem(q_addr + C::kQRope + ks * 32, 16, 512, kSwizzle64);
+                            mma_e4m3_ss(tmem + C::kColSR, ad, bd, idesc, ks > 0 ? 1u : 0u);
+                        }
+                        mma_commit(sh.s_full());
                     }
-                    __syncwarp();
                 }
             }
         }
@@ -994,32 +1012,29 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         const bool leader = elect_one();
         constexpr uint32_t idesc = idesc_e4m3_f32(kRT, 64, true, true);            // V^T . Wd^T, both MN-major
         const uint32_t wb = smem_u32(sh.w());
-        bool ok = true;
+        bool ok = leader;
         int c = 0;
         for (; k.more() && ok; k.next(p)) {
             for (int i = k.tile; i < k.end && ok; ++i, ++c) {
-                ok = __all_sync(kFull, wait_bar<false>(sh, sh.p_full(), (uint32_t)c & 1u, a));
+                ok = wait_bar<kRoleSpin>(sh, sh.p_full(), (uint32_t)c & 1u, a);
                 if (!ok) break;
                 tc_fence_after();
                 const int st = c & 1;
-                if (leader) {
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        const uint32_t box = smem_u32(sh.box(st, m));
+                for (int m = 0; m < 4; ++m) {
+                    const uint32_t box = smem_u32(sh.box(st, m));
 #pragma unroll
-                        for (int d = 0; d < C::kWImgs; ++d) {
+                    for (int d = 0; d < C::kWImgs; ++d) {
 #pragma unroll
-                            for (int ks = 0; ks < kRT / 32; ++ks) {
-                                const uint64_t ad = desc_smem(box + ks * 4096, 16, 1024, kSwizzle128);
-                                const uint64_t bd = desc_smem(wb + d * kRT * 64 + ks * 2048, 16, 512, kSwizzle64);
-                                mma_e4m3_ss(tmem + kColO + 64 * m, ad, bd, idesc, (i == k.tile && d == 0 && ks == 0) ? 0u : 1u);
-                            }
+                        for (int ks = 0; ks < kRT / 32; ++ks) {
+                            const uint64_t ad = desc_smem(box + ks * 4096, 16, 1024, kSwizzle128);
+                            const uint64_t bd = desc_smem(wb + d * kRT * 64 + ks * 2048, 16, 512, kSwizzle64);
+                            mma_e4m3_ss(tmem + kColO + 64 * m, ad, bd, idesc, (i == k.tile && d == 0 && ks == 0) ? 0u : 1u);
                         }
-                        mma_commit(sh.empty(st, m));
                     }
-                    mma_commit(sh.o_done());
+                    mma_commit(sh.empty(st, m));
                 }
-                __syncwarp();
+                mma_commit(sh.o_done());
             }
         }
         if (leader) {
