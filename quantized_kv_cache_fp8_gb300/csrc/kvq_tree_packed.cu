@@ -255,12 +255,6 @@ __device__ __forceinline__ int64_t tree_pool_row(const kvq_mla_tree_problem& p, 
     return pid < 0 ? -1 : (int64_t)pid * p.page_size + t % p.page_size;
 }
 
-// the `bytes` at p (both multiples of 16) on their way to L2
-__device__ __forceinline__ void l2_prefetch(const void* p, int bytes)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 // ---- the line of tiles --------------------------------------------------------------------
 template <int NR>
 __device__ __forceinline__ int64_t seq_tiles(const kvq_mla_tree_problem& p, int s)
@@ -311,39 +305,14 @@ struct Walk {
     }
 };
 
-// ---- queries ------------------------------------------------------------------------------
-__device__ __forceinline__ void bf16x8(const uint4& w, float* v)
-{
-    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        v[2 * i] = __uint_as_float(u[i] << 16);
-        v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-    }
-}
-
-// four values -> their two digits, four codes a word; the second digit in units of 1 / kScale
+// ---- digits and queries -------------------------------------------------------------------
+// Two values -> their two digits, the second in units of 1 / kScale.  The value passes through
+// binary16 (2^-11 of it beside the 2^-9 that two digits keep; a query's 8 bits exactly), where the
+// first digit's remainder is exact.
 template <int kScale>
-__device__ __forceinline__ void digits4(const float* x, uint32_t& d0, uint32_t& d1)
+__device__ __forceinline__ void digits2(float2 v, uint32_t& d0, uint32_t& d1)
 {
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const float2 v = make_float2(x[2 * h], x[2 * h + 1]);
-        const __nv_fp8x2_storage_t c = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-        const float2 b = __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-        const __nv_fp8x2_storage_t e = __nv_cvt_float2_to_fp8x2(
-            make_float2((v.x - b.x) * (float)kScale, (v.y - b.y) * (float)kScale), __NV_SATFINITE, __NV_E4M3);
-        d0 = h ? d0 | (uint32_t)c << 16 : c;
-        d1 = h ? d1 | (uint32_t)e << 16 : e;
-    }
-}
-
-// two weights -> their two digits.  The weight passes through binary16 (2^-11 of its value, beside
-// the 2^-9 that two digits keep), where the first digit's remainder is exact.
-template <int kScale>
-__device__ __forceinline__ void weight_digits(float2 w, uint32_t& d0, uint32_t& d1)
-{
-    const __half2 h = __float22half2_rn(w);
+    const __half2 h = __float22half2_rn(v);
     const __nv_fp8x2_storage_t c = __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
     __half2 r = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
     if (kScale != 1) r = __hmul2(r, __half2half2(__ushort_as_half(0x4C00)));       // 16
@@ -351,63 +320,64 @@ __device__ __forceinline__ void weight_digits(float2 w, uint32_t& d0, uint32_t& 
     d1 = __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
 }
 
-// One warp: query row `r` (of the sequence's n * H; zero past them) into rows i and NR + i of
-// the Q image.  sigma puts the row's largest element in [128, 256).
+// One warp: query rows r0 + i, i = warp, warp + 16, .. (of the sequence's n * H; zero from `rows` on)
+// into rows i and NR + i of the Q image.  Lane: 16 latent dims, and (lane < 16) 4 rope dims.  sigma
+// puts the row's largest element in [128, 256).
 template <int NR>
-__device__ __forceinline__ void write_query(const Shared<NR>& sh, const kvq_mla_tree_problem& p, int s, int64_t r,
-                                            bool live, int i, int lane)
+__device__ __forceinline__ void write_queries(const Shared<NR>& sh, const kvq_mla_tree_problem& p, int s, int64_t r0,
+                                              int64_t rows, int warp, int lane)
 {
     using C = Cfg<NR>;
-    float v[16], x[4];
-    if (live) {
-        const int64_t row = (int64_t)s * p.n_q * p.n_heads + r;
-        const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q_lat) + row * p.ldq_lat) + 2 * lane;
-        bf16x8(ql[0], v);
-        bf16x8(ql[1], v + 8);
-        const uint2 w = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q_rope) + row * p.ldq_rope)[lane & 15];
-        x[0] = __uint_as_float(w.x << 16);
-        x[1] = __uint_as_float(w.x & 0xFFFF0000u);
-        x[2] = __uint_as_float(w.y << 16);
-        x[3] = __uint_as_float(w.y & 0xFFFF0000u);
-    } else {
+    constexpr int kRows = NR / kSmx;
+    uint32_t w[kRows][10];                       // bf16 pairs, every row's loads in flight at once
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = 0.0f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = 0.0f;
+    for (int n = 0; n < kRows; ++n) {
+        const int i = warp + kSmx * n;
+        uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+        uint2 c = make_uint2(0u, 0u);
+        if (i < rows) {
+            const int64_t row = (int64_t)s * p.n_q * p.n_heads + r0 + i;
+            const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q_lat) + row * p.ldq_lat) + 2 * lane;
+            a = __ldg(ql);
+            b = __ldg(ql + 1);
+            if (lane < 16) c = __ldg(reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(p.q_rope) + row * p.ldq_rope) + lane);
+        }
+        w[n][0] = a.x; w[n][1] = a.y; w[n][2] = a.z; w[n][3] = a.w;
+        w[n][4] = b.x; w[n][5] = b.y; w[n][6] = b.z; w[n][7] = b.w;
+        w[n][8] = c.x; w[n][9] = c.y;
     }
-    float mx = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) mx = fmaxf(mx, fabsf(v[k]));
+    for (int n = 0; n < kRows; ++n) {
+        const int i = warp + kSmx * n;
+        // the largest exponent: of bf16 patterns without sign, the largest pattern's
+        uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) mx = fmaxf(mx, fabsf(x[k]));
+        for (int e = 0; e < 10; ++e) m = __vmaxu2(m, w[n][e] & 0x7FFF7FFFu);
+        m = max(m & 0xFFFFu, m >> 16);
+        m = __reduce_max_sync(kFull, m);
+        const int sigma = m != 0 ? min(100, max(-100, 7 - ((int)(m >> 7) - 127))) : 0;
+        const float scale = __int_as_float((127 + sigma) << 23);
+        uint32_t d0[5], d1[5];
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    int e = 0;
-    (void)frexpf(mx, &e);
-    const int sigma = mx > 0.0f ? min(100, max(-100, 8 - e)) : 0;
-    const float scale = ldexpf(1.0f, sigma);
-    uint32_t d0[4], d1[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        float y[4];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) y[c] = v[4 * k + c] * scale;
-        digits4<16>(y, d0[k], d1[k]);
+        for (int e = 0; e < 5; ++e) {
+            uint32_t a0, a1, b0, b1;
+            const uint32_t x = w[n][2 * e], y = w[n][2 * e + 1];
+            digits2<16>(make_float2(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xFFFF0000u) * scale), a0, a1);
+            digits2<16>(make_float2(__uint_as_float(y << 16) * scale, __uint_as_float(y & 0xFFFF0000u) * scale), b0, b1);
+            d0[e] = a0 | b0 << 16;
+            d1[e] = a1 | b1 << 16;
+        }
+        uint8_t* img = sh.q() + (lane >> 3) * C::kQBlk;
+        *reinterpret_cast<uint4*>(img + sw128(i, lane & 7)) = make_uint4(d0[0], d0[1], d0[2], d0[3]);
+        *reinterpret_cast<uint4*>(img + sw128(NR + i, lane & 7)) = make_uint4(d1[0], d1[1], d1[2], d1[3]);
+        if (lane < 16) {
+            uint8_t* rp = sh.q() + C::kQRope;
+            const int at = (((lane >> 2) ^ ((i >> 1) & 3)) << 4) + 4 * (lane & 3);      // (NR + i has the same swizzle)
+            *reinterpret_cast<uint32_t*>(rp + i * 64 + at) = d0[4];
+            *reinterpret_cast<uint32_t*>(rp + (NR + i) * 64 + at) = d1[4];
+        }
+        if (lane == 0) sh.gain()[i] = p.sm_scale * kLog2e * __int_as_float((127 - sigma) << 23);
     }
-    uint8_t* img = sh.q() + (lane >> 3) * C::kQBlk;
-    *reinterpret_cast<uint4*>(img + sw128(i, lane & 7)) = make_uint4(d0[0], d0[1], d0[2], d0[3]);
-    *reinterpret_cast<uint4*>(img + sw128(NR + i, lane & 7)) = make_uint4(d1[0], d1[1], d1[2], d1[3]);
-    if (lane < 16) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) x[c] *= scale;
-        uint32_t r0, r1;
-        digits4<16>(x, r0, r1);
-        uint8_t* rp = sh.q() + C::kQRope;
-        const int at = (((lane >> 2) ^ ((i >> 1) & 3)) << 4) + 4 * (lane & 3);      // (NR + i has the same swizzle)
-        *reinterpret_cast<uint32_t*>(rp + i * 64 + at) = r0;
-        *reinterpret_cast<uint32_t*>(rp + (NR + i) * 64 + at) = r1;
-    }
-    if (lane == 0) sh.gain()[i] = p.sm_scale * kLog2e * ldexpf(1.0f, -sigma);
 }
 
 // ---- codes that no encoder writes -----------------------------------------------------------
@@ -461,6 +431,22 @@ __device__ __noinline__ float rescore(const Shared<NR>& sh, const kvq_mla_tree_p
         else ar += acc;
     }
     return gain != 0.0f ? fmaf(ls, al, rs * ar) * (p.sm_scale * kLog2e / gain) : 0.0f;
+}
+
+// One stage of a 4 x 4 transposition among four neighbouring lanes, for every group of four values:
+// value index bit B and lane bit B change places.
+template <int B, int N>
+__device__ __forceinline__ void swap_dims(float (&v)[N], int lane)
+{
+    const bool hi = (lane & B) != 0;
+#pragma unroll
+    for (int e = 0; e < N; ++e) {
+        if ((e & B) == 0) {
+            const float got = __shfl_xor_sync(kFull, hi ? v[e] : v[e + B], B);
+            if (hi) v[e] = got;
+            else v[e + B] = got;
+        }
+    }
 }
 
 // tmem <-> 8 or 16 consecutive columns
@@ -598,7 +584,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                     f->pieces = starts ? last - g + 1 : 0;
                 }
             }
-            for (int i = warp; i < NR; i += kSmx) write_query(sh, p, s, r0 + i, i < rows, i, lane);
+            write_queries(sh, p, s, r0, rows, warp, lane);
             if (tid < NR) {
                 sh.neg_m()[tid] = 0.0f;
             }
@@ -769,8 +755,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 for (int e = 0; e < GR; e += 4) {
                     const float2 va = unpack2(add2(t2[e / 2], up2)), vb = unpack2(add2(t2[e / 2 + 1], up2));
                     uint32_t a0, a1, b0, b1;
-                    weight_digits<NR == 64 ? 1 : 16>(make_float2(ex2(va.x), ex2(va.y)), a0, a1);
-                    weight_digits<NR == 64 ? 1 : 16>(make_float2(ex2(vb.x), ex2(vb.y)), b0, b1);
+                    digits2<NR == 64 ? 1 : 16>(make_float2(ex2(va.x), ex2(va.y)), a0, a1);
+                    digits2<NR == 64 ? 1 : 16>(make_float2(ex2(vb.x), ex2(vb.y)), b0, b1);
                     w0[e / 4] = a0 | b0 << 16;
                     w1[e / 4] = a1 | b1 << 16;
                 }
@@ -870,13 +856,21 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
 #pragma unroll
                     for (int e = 0; e < GR; ++e) o[e] = NAN;
                 }
-                if (whole) {
+                // thread = one dim of GR rows -> 4 dims of GR / 4 rows: lane l keeps the rows 4 j + l % 4
+                swap_dims<1>(o, lane);
+                swap_dims<2>(o, lane);
+                const int d0 = dim & ~3, sub = lane & 3;
 #pragma unroll
-                    for (int e = 0; e < GR; ++e)
-                        if (hb + e < rows) a.out[(out_row + hb + e) * kDLat + dim] = __float2bfloat16_rn(o[e]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < GR; ++e) a.part_o[((int64_t)slot * NR + hb + e) * kDLat + dim] = o[e];
+                for (int e = 0; e < GR / 4; ++e) {
+                    const int row = hb + 4 * e + sub;
+                    const float4 v = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    if (!whole) {
+                        *reinterpret_cast<float4*>(a.part_o + ((int64_t)slot * NR + row) * kDLat + d0) = v;
+                    } else if (row < rows) {
+                        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+                        *reinterpret_cast<uint2*>(a.out + (out_row + row) * kDLat + d0) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&x), *reinterpret_cast<const uint32_t*>(&y));
+                    }
                 }
             }
             tc_fence_before();
@@ -936,15 +930,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 }
                 if (i + 1 < k.end) {
                     look_up(i + 1, (c + 1) & 1);
-                    // the next tile waits for a stage: its rows come as far as L2 meanwhile
-                    if (who == 0 && lane < per) {
-                        const int y = sh.copy_rows(2 * who + ((c + 1) & 1))[lane];
-                        if (y >= 0) {
-                            const int n = (int)min((int64_t)a.box_rows, p.cache.n_rows - y);
-                            l2_prefetch(p.cache.lat + (int64_t)y * kDLat, n * kDLat);
-                            l2_prefetch(p.cache.rope + (int64_t)y * kDRope, n * kDRope);
-                        }
-                    }
                 }
                 ok = __any_sync(kFull, leader && ok);
             }
