@@ -60,10 +60,10 @@ constexpr int kBox = kRT * 128;              // [128 rows x 128 dims] codes
 constexpr int kRopeBox = kRT * 64;
 constexpr int kStages = 2;
 constexpr int kSmx = 16;                     // softmax warps: lane quarter w % 4, query rows NR / 4 (w / 4) ..
-constexpr int kWarpLoad = kSmx;            // TMA: the first two latent blocks
+constexpr int kWarpLoad = kSmx;            // TMA: the first two latent blocks and the rope key
 constexpr int kWarpS = kSmx + 1;             // score MMAs (and tensor memory)
 constexpr int kWarpC = kSmx + 2;             // context MMAs
-constexpr int kWarpLoad2 = kSmx + 3;         // TMA: the other two and the rope key
+constexpr int kWarpLoad2 = kSmx + 3;         // TMA: the other two
 constexpr int kThreads = 32 * (kSmx + 4);
 // registers a thread: of the launch's 96 the softmax takes 104 and the rest 64 (with 96 each the
 // softmax spills)
@@ -256,21 +256,27 @@ __device__ __forceinline__ int64_t tree_pool_row(const kvq_mla_tree_problem& p, 
 }
 
 // ---- the line of tiles --------------------------------------------------------------------
+// A unit takes kUnitCost places on the line before its tiles: what a CTA pays to begin another unit
+// (query image, refill of the pipeline, epilogue: about four tiles' time).  Every stretch begins
+// one anyway, so these places even out the stretches with several units.
+constexpr int kUnitCost = 4;
+
 template <int NR>
-__device__ __forceinline__ int64_t seq_tiles(const kvq_mla_tree_problem& p, int s)
+__device__ __forceinline__ int64_t seq_places(const kvq_mla_tree_problem& p, int s)
 {
     const int2 sh = tree_seq_shape(p, s);
-    return (int64_t)((sh.x + kRT - 1) / kRT) * (((int64_t)sh.y * p.n_heads + NR - 1) / NR);
+    const int nt = (sh.x + kRT - 1) / kRT;
+    return nt == 0 ? 0 : (int64_t)(nt + kUnitCost) * (((int64_t)sh.y * p.n_heads + NR - 1) / NR);
 }
 
-// where the stretch of CTA g of G begins on a line of `total` tiles
+// where the stretch of CTA g of G begins on a line of `total` places
 __device__ __forceinline__ int64_t cut(int64_t total, int g, int G) { return total * g / G; }
 
-// the segments of a stretch: row tile rt of sequence s, tiles [tile, end)
+// the segments of a stretch: row tile rt of sequence s, its tiles [tile, end)
 template <int NR>
 struct Walk {
-    int64_t left;
-    int s, rt, tile, end, nt, n_rt, L, n;
+    int left;                                // places of the stretch from this unit's first one in it on
+    int s, rt, at, tile, end, nt, n_rt, L, n;
 
     __device__ __forceinline__ void shape(const kvq_mla_tree_problem& p)
     {
@@ -280,29 +286,43 @@ struct Walk {
         nt = (L + kRT - 1) / kRT;
         n_rt = (int)(((int64_t)n * p.n_heads + NR - 1) / NR);
     }
-    __device__ __forceinline__ Walk(const kvq_mla_tree_problem& p, int s0, int64_t off, int64_t count) : left(count), s(s0), end(0)
+    __device__ __forceinline__ int places() const { return min(nt + kUnitCost - at, left); }
+    __device__ __forceinline__ void tiles()
     {
-        if (left <= 0) return;
-        shape(p);
-        rt = (int)(off / nt);
-        tile = (int)(off % nt);
-        end = (int)min((int64_t)nt, tile + left);
+        tile = max(at - kUnitCost, 0);
+        end = max(at + places() - kUnitCost, 0);
     }
-    __device__ __forceinline__ bool more() const { return left > 0; }
-    __device__ __forceinline__ void next(const kvq_mla_tree_problem& p)
+    __device__ __forceinline__ void step(const kvq_mla_tree_problem& p)
     {
-        left -= end - tile;
+        left -= places();
+        at = 0;
         if (left <= 0) return;
         if (++rt == n_rt) {
             rt = 0;
             do {
                 ++s;
                 shape(p);
-            } while (nt == 0 || n_rt == 0);               // (there is a tile left, so a sequence with tiles)
+            } while (nt == 0 || n_rt == 0);               // (there is a place left, so a sequence with tiles)
         }
-        tile = 0;
-        end = (int)min((int64_t)nt, left);
+        tiles();
     }
+    __device__ __forceinline__ void next(const kvq_mla_tree_problem& p)
+    {
+        do step(p); while (left > 0 && tile == end);      // (a stretch may end among a unit's first places)
+    }
+    __device__ __forceinline__ Walk(const kvq_mla_tree_problem& p, int s0, int64_t off, int64_t count)
+        : left((int)count), s(s0), at(0), tile(0), end(0)
+    {
+        if (left <= 0) return;
+        shape(p);
+        rt = (int)(off / (nt + kUnitCost));
+        at = (int)(off % (nt + kUnitCost));
+        tiles();
+        if (tile == end) next(p);
+    }
+    __device__ __forceinline__ bool more() const { return left > 0; }
+    // the place behind this unit's last one, of a stretch that ends at `stretch_end`
+    __device__ __forceinline__ int64_t unit_end(int64_t stretch_end) const { return stretch_end - left - at + nt + kUnitCost; }
 };
 
 // ---- digits and queries -------------------------------------------------------------------
@@ -503,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         int64_t* s_sum = reinterpret_cast<int64_t*>(sh.w());      // [32] sums of the warps
         constexpr int kW = kThreads / 32;
         int64_t v = 0;
-        for (int s = tid; s < p.n_seq; s += kThreads) v += seq_tiles<NR>(p, s);
+        for (int s = tid; s < p.n_seq; s += kThreads) v += seq_places<NR>(p, s);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
         if (lane == 0) s_sum[warp] = v;
@@ -515,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         int64_t base = 0;
         for (int c = 0; c < p.n_seq && base <= t0 && t1 > t0; c += kThreads) {
             const int s = c + tid;
-            const int64_t own = s < p.n_seq ? seq_tiles<NR>(p, s) : 0;
+            const int64_t own = s < p.n_seq ? seq_places<NR>(p, s) : 0;
             int64_t incl = own;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -562,28 +582,12 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         bool ok = true;
         int c = 0;                                    // tiles so far
         bool first_seg = true;
-        int64_t pos = t0;
         for (int seg = 0; k.more(); ++seg) {
             const int s = k.s, L = k.L, n = k.n;
             const int64_t r0 = (int64_t)k.rt * NR;    // first query row of the tile, of the sequence's n * H
             const int64_t rows = (int64_t)n * p.n_heads - r0;       // rows there are from r0 on
             const bool whole = k.tile == 0 && k.end == k.nt;
             const int slot = 2 * g + (first_seg ? 0 : 1);
-            // a unit that starts here tells the combine who shares it
-            if (tid == 0) {
-                const int64_t u_end = pos + k.nt;     // (meaningful if tile == 0)
-                int last = g;
-                while (k.tile == 0 && cut(total, last + 1, G) < u_end) ++last;
-                const bool starts = k.tile == 0;
-                if (a.by_unit ? starts : k.left == k.end - k.tile) {
-                    SplitInfo* f = a.info + (a.by_unit ? (int64_t)s * a.n_rt + k.rt : (int64_t)g);
-                    f->s = s;
-                    f->rt = k.rt;
-                    f->cta = g;
-                    f->slot = slot;
-                    f->pieces = starts ? last - g + 1 : 0;
-                }
-            }
             write_queries(sh, p, s, r0, rows, warp, lane);
             if (tid < NR) {
                 sh.neg_m()[tid] = 0.0f;
@@ -876,10 +880,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
             tc_fence_before();
             smx_barrier();                            // maxima, factors and query scales may change
             first_seg = false;
-            pos += k.end - k.tile;
             k.next(p);
         }
-        if (tid == 0 && !a.by_unit && t1 <= t0) a.info[g].pieces = 0;
     } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsRest));
     if (warp == kWarpLoad || warp == kWarpLoad2) {
@@ -887,7 +889,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         // The lanes look up a tile's pool rows one tile ahead, one thread issues its copies.
         const bool leader = elect_one();
         const int per = kRT / a.box_rows;             // copies a 128-dim block
-        const int who = warp == kWarpLoad ? 0 : 1, b0 = who ? 2 : 0, b1 = who ? kBoxes : 2;
+        const int who = warp == kWarpLoad ? 0 : 1;
         bool ok = true;
         int c = 0;                                    // tiles so far
         int done[3] = {0, 0, 0};                      // tiles whose box went out: this warp's blocks, the rope key
@@ -909,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                     for (int h = 0; h < per; ++h) n_in += y[h] >= 0 ? a.box_rows : 0;
 #pragma unroll
                     for (int b = 0; b < kBoxes; ++b) {
-                        if (b < b0 || b >= b1) continue;
+                        if ((b == 2 || b == 3) != (who == 1)) continue;
                         const int slot = b < 4 ? st : C::kRS == 2 ? st : 0;
                         const int use = b < 4 || C::kRS == 2 ? c >> 1 : c;                   // earlier uses of the slot
                         ok = ok && wait_bar<kRoleSpin>(sh, sh.empty(slot, b), ((uint32_t)use & 1u) ^ 1u, a);
@@ -938,7 +940,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         if (leader) {
 #pragma unroll
             for (int b = 0; b < kBoxes; ++b) {
-                if (b < b0 || b >= b1) continue;
+                if ((b == 2 || b == 3) != (who == 1)) continue;
                 const int n = done[b < 4 ? b & 1 : 2], ns = b < 4 ? kStages : C::kRS;
                 for (int i = max(0, n - ns); i < n; ++i) {        // (an earlier use landed before a later one)
                     if (!mbar_wait(sh.full(i % ns, b), (uint32_t)(i / ns) & 1u, kTimeoutNs) && a.status)
@@ -996,6 +998,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         // ================================ context MMAs ====================================
         const bool leader = elect_one();
         constexpr uint32_t idesc = idesc_e4m3_f32(kRT, 64, true, true);            // V^T . Wd^T, both MN-major
+        // first, the CTA with a unit's first tile tells the combine who shares it (all units of the
+        // stretch at once, so that nothing is left out if the CTA gives up)
+        if (leader) {
+            bool splits = false, first = true;        // the last unit begun goes on in the next CTA
+            for (Walk<NR> w = k; w.more(); w.next(p), first = false) {
+                if (w.tile != 0) continue;
+                int last = g;
+                while (cut(total, last + 1, G) < w.unit_end(t1)) ++last;
+                SplitInfo* f = a.info + (a.by_unit ? (int64_t)w.s * a.n_rt + w.rt : (int64_t)g);
+                f->s = w.s;
+                f->rt = w.rt;
+                f->cta = g;
+                f->slot = 2 * g + (first ? 0 : 1);
+                f->pieces = last - g + 1;
+                splits = last > g;
+            }
+            if (!a.by_unit && !splits) a.info[g].pieces = 0;
+        }
         const uint32_t wb = smem_u32(sh.w());
         bool ok = leader;
         int c = 0;
