@@ -228,6 +228,9 @@ def _stream(stream):
     if stream is not None:
         return stream
     import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # the handle without a Stream object
+    if raw is not None:
+        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -436,10 +439,11 @@ def _want(name, t, dtype, *shape):
     """A contiguous tensor of `dtype` (a name) and `shape` (None: any size), or None."""
     if t is None:
         return
-    if str(t.dtype) != "torch." + dtype or not t.is_contiguous() or t.dim() != len(shape) or \
-            any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, "
-                         f"is {t.dtype} {list(t.shape)}")
+    import torch
+    got = t.shape
+    if t.dtype is not getattr(torch, dtype) or not t.is_contiguous() or \
+            (got != shape and (len(got) != len(shape) or any(n is not None and n != m for n, m in zip(shape, got)))):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, is {t.dtype} {list(got)}")
 
 
 def make_page_plan(*, keep_len, n_new, block_table, n_held, free_list, n_free, page_size, seq_len,
@@ -468,14 +472,17 @@ def kvq_resize_pages(p: PagePlan, dev_status=None, stream=None) -> None:
     _check(lib().kvq_resize_pages(C.byref(p), _ptr(dev_status), _stream(stream)))
 
 
+_LAT_BYTES = {FMT_FP8: 512, FMT_TQ4: 256, FMT_TQ6: 384, FMT_TQ3: 192}
+
+
 def _mla_planes(planes, fmt):
-    row = {FMT_FP8: 512, FMT_TQ4: 256, FMT_TQ6: 384, FMT_TQ3: 192}.get(int(fmt))
-    n = planes["lat"].shape[0]
-    _want("lat", planes["lat"], "uint8", n, row)
-    _want("lat_scale", planes["lat_scale"], "float32", n)
-    _want("rope", planes["rope"], "uint8", n, 64)
-    _want("rope_scale", planes["rope_scale"], "float32", n)
-    return _cache(planes)
+    lat, ls, rope, rs = planes["lat"], planes["lat_scale"], planes["rope"], planes["rope_scale"]
+    n = lat.shape[0]
+    _want("lat", lat, "uint8", n, _LAT_BYTES.get(fmt))
+    _want("lat_scale", ls, "float32", n)
+    _want("rope", rope, "uint8", n, 64)
+    _want("rope_scale", rs, "float32", n)
+    return MlaCache(lat.data_ptr(), ls.data_ptr(), rope.data_ptr(), rs.data_ptr(), n)
 
 
 def kvq_append_mla(c_lat, k_rope, slot_map, fmt, sign_bits, planes: dict, dev_status=None,
@@ -483,16 +490,20 @@ def kvq_append_mla(c_lat, k_rope, slot_map, fmt, sign_bits, planes: dict, dev_st
     """Encode rows c_lat [rows, 512] and k_rope [rows, 64] (both float32 or both bfloat16, rows
     possibly strided) into the cache planes of tier `fmt` at pool rows slot_map int32 [rows]
     (negative: skipped)."""
-    rows = c_lat.shape[0]
-    kind = {"torch.float32": WEIGHT_F32, "torch.bfloat16": WEIGHT_BF16}.get(str(c_lat.dtype))
-    if kind is None or k_rope.dtype != c_lat.dtype or tuple(c_lat.shape) != (rows, 512) or \
-            tuple(k_rope.shape) != (rows, 64) or (rows and (c_lat.stride(1) != 1 or k_rope.stride(1) != 1)):
+    import torch
+    rows, width = c_lat.shape
+    kind = WEIGHT_F32 if c_lat.dtype is torch.float32 else WEIGHT_BF16 if c_lat.dtype is torch.bfloat16 else None
+    ldx, one = c_lat.stride()
+    ldr, one_r = k_rope.stride()
+    if kind is None or k_rope.dtype is not c_lat.dtype or width != 512 or k_rope.shape != (rows, 64) or \
+            (rows and (one != 1 or one_r != 1)):
         raise ValueError("c_lat, k_rope must be [rows, 512] and [rows, 64], both float32 or both bfloat16")
+    if rows == 1:                                         # (a single row's stride is arbitrary)
+        ldx, ldr = 512, 64
     _want("slot_map", slot_map, "int32", rows)
     c = _mla_planes(planes, fmt)
-    _check(lib().kvq_append_mla(_ptr(c_lat), c_lat.stride(0), _ptr(k_rope), k_rope.stride(0), kind, rows,
-                                _ptr(slot_map), int(fmt), _ptr(sign_bits), C.byref(c), _ptr(dev_status),
-                                _stream(stream)))
+    _check(lib().kvq_append_mla(c_lat.data_ptr(), ldx, k_rope.data_ptr(), ldr, kind, rows, slot_map.data_ptr(),
+                                int(fmt), _ptr(sign_bits), C.byref(c), _ptr(dev_status), _stream(stream)))
 
 
 def _row_stride(name, q, width):
@@ -501,7 +512,7 @@ def _row_stride(name, q, width):
     ld = q.stride(2) if h > 1 else q.stride(1) if nq > 1 else q.stride(0) if n > 1 else w
     even = (w == width and q.stride(3) == 1 and (h == 1 or q.stride(2) == ld)
             and (nq == 1 or q.stride(1) == ld * h) and (n == 1 or q.stride(0) == ld * h * nq))
-    if str(q.dtype) != "torch.bfloat16" or not even:
+    if not str(q.dtype).endswith("bfloat16") or not even:
         raise ValueError(f"{name} must be bfloat16 [n_seq, n_q, heads, {width}] with evenly spaced rows")
     return ld
 

@@ -29,7 +29,9 @@ __device__ __forceinline__ void flag(uint32_t* status, unsigned bit)
 constexpr int kMaxThreads = 1024;
 constexpr int kInlineTokens = 4096;
 constexpr int kSlotThreads = 256;
-constexpr int kSlotTile = 2048;              // tokens per CTA of the second launch
+constexpr int kSlotRun = 4;                  // consecutive tokens per thread of the second launch
+constexpr int kSlotTile = kSlotThreads * kSlotRun;
+constexpr int kMoves = 4;                    // page moves a thread keeps in flight
 constexpr int kSlotShared = 2048;            // sequence offsets searched in shared memory
 
 struct ResizeArgs {
@@ -200,14 +202,28 @@ __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeA
             s_base[tid] = n_free + (give_all - carry - incl) + give - 1;   // of entry q.need, descending
             __syncthreads();
             const int last = min(T, p.n_seq - c) - 1;
-            for (int64_t i = tid; i < sum; i += T) {
-                const int k = last_not_above(s_pre, 0, last, i);
-                const int64_t d = i - s_pre[k];
-                int32_t* e = p.block_table + (int64_t)(c + k) * p.max_pages + s_first[k] + d;
-                const int64_t at = s_base[k] - d;
-                if (at < p.n_pages) p.free_list[at] = *e;
-                else bits |= KVQ_DEV_BAD_PAGE;
-                *e = -1;
+            for (int64_t i0 = tid; i0 < sum; i0 += (int64_t)T * kMoves) {
+                int32_t* e[kMoves];
+                int64_t at[kMoves];
+                int32_t page[kMoves];
+#pragma unroll
+                for (int u = 0; u < kMoves; ++u) {
+                    const int64_t i = i0 + (int64_t)u * T;
+                    e[u] = nullptr;
+                    if (i >= sum) continue;
+                    const int k = last_not_above(s_pre, 0, last, i);
+                    const int64_t d = i - s_pre[k];
+                    e[u] = p.block_table + (int64_t)(c + k) * p.max_pages + s_first[k] + d;
+                    at[u] = s_base[k] - d;
+                    page[u] = *e[u];
+                }
+#pragma unroll
+                for (int u = 0; u < kMoves; ++u) {
+                    if (!e[u]) continue;
+                    if (at[u] < p.n_pages) p.free_list[at[u]] = page[u];
+                    else bits |= KVQ_DEV_BAD_PAGE;
+                    *e[u] = -1;
+                }
             }
             carry += sum;
             __syncthreads();
@@ -231,11 +247,23 @@ __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeA
         if (served && take > 0) atomicMax(&s_used, (unsigned long long)end);
         __syncthreads();
         const int last = min(T, p.n_seq - c) - 1;
-        for (int64_t i = tid; i < sum; i += T) {
-            const int k = last_not_above(s_pre, 0, last, i);
-            if (s_base[k] < 0) break;                    // refused, as is every page wanted after it
-            const int64_t d = i - s_pre[k];
-            p.block_table[(int64_t)(c + k) * p.max_pages + s_first[k] + d] = p.free_list[s_base[k] - d];
+        for (int64_t i0 = tid; i0 < sum; i0 += (int64_t)T * kMoves) {
+            int32_t* e[kMoves];
+            int32_t page[kMoves];
+#pragma unroll
+            for (int u = 0; u < kMoves; ++u) {
+                const int64_t i = i0 + (int64_t)u * T;
+                e[u] = nullptr;
+                if (i >= sum) continue;
+                const int k = last_not_above(s_pre, 0, last, i);
+                if (s_base[k] < 0) continue;             // refused, as is every page wanted after it
+                const int64_t d = i - s_pre[k];
+                e[u] = p.block_table + (int64_t)(c + k) * p.max_pages + s_first[k] + d;
+                page[u] = p.free_list[s_base[k] - d];
+            }
+#pragma unroll
+            for (int u = 0; u < kMoves; ++u)
+                if (e[u]) *e[u] = page[u];
         }
         if (live) {
             p.seq_len[s] = served ? q.keep + q.add : (int)min((int64_t)q.keep, (int64_t)q.held * p.page_size);
@@ -258,26 +286,65 @@ __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeA
     }
 }
 
+// Thread = kSlotRun consecutive tokens: one search for the first one's sequence, then the
+// sequences, and the pages, in passing; 16-byte stores.
 __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const ResizeArgs a)
 {
-    __shared__ int s_start[kSlotShared];
+    __shared__ int s_start[kSlotShared + 1];
     const kvq_page_plan& p = a.p;
     grid_dependency_wait();
     const bool shared = p.n_seq <= kSlotShared;
     if (shared)
-        for (int s = threadIdx.x; s < p.n_seq; s += kSlotThreads) s_start[s] = p.tok_start[s];
-    const int n_tok = p.tok_start[p.n_seq];
+        for (int s = threadIdx.x; s <= p.n_seq; s += kSlotThreads) s_start[s] = p.tok_start[s];
     __syncthreads();
-    const int64_t i0 = (int64_t)blockIdx.x * kSlotTile;
-    for (int64_t i = i0 + threadIdx.x; i < min(i0 + kSlotTile, (int64_t)p.max_tokens); i += kSlotThreads) {
-        const bool inside = i < n_tok;
-        int s = 0, start = 0;
-        if (inside) {
-            s = shared ? last_not_above(s_start, 0, p.n_seq - 1, i) : last_not_above(p.tok_start, 0, p.n_seq - 1, i);
-            start = shared ? s_start[s] : p.tok_start[s];
+    const int* start = shared ? s_start : p.tok_start;
+    const int n_tok = start[p.n_seq];
+    const int64_t first = (int64_t)blockIdx.x * kSlotTile + threadIdx.x * kSlotRun;
+    if (first >= p.max_tokens) return;
+    int slot[kSlotRun], pos[kSlotRun];
+    int s = -1, begin = 0, end = 0;                      // the sequence at hand and its tokens
+    int base = 0, page_at = -1, page = -1;               // its first new position; the page last looked up
+    bool served = false;
+#pragma unroll
+    for (int u = 0; u < kSlotRun; ++u) {
+        const int64_t i = first + u;
+        slot[u] = pos[u] = -1;
+        if (i >= n_tok) continue;
+        if (i >= end) {
+            s = s < 0 ? last_not_above(start, 0, p.n_seq - 1, i) : s + 1;
+            while (start[s + 1] <= i) ++s;               // (sequences without tokens)
+            begin = start[s];
+            end = start[s + 1];
+            const int keep = max(p.keep_len[s], 0), add = max(p.n_new[s], 0);
+            served = (int64_t)p.seq_len[s] == (int64_t)keep + add;
+            base = keep;
+            page_at = -1;
         }
-        write_slot(p, (int)i, s, start, inside, a.status);
+        if (!served) continue;
+        const int t = base + (int)(i - begin), at = t / p.page_size;
+        if (at != page_at) {
+            page_at = at;
+            page = p.block_table[(int64_t)s * p.max_pages + at];
+        }
+        if (page < 0 || page >= p.n_pages) {
+            flag(a.status, KVQ_DEV_BAD_PAGE);
+        } else {
+            slot[u] = page * p.page_size + (t - at * p.page_size);
+            pos[u] = t;
+        }
     }
+    const bool whole = first + kSlotRun <= p.max_tokens;
+    auto store = [&](int32_t* dst, const int (&v)[kSlotRun]) {
+        if (whole && ((uintptr_t)(dst + first) & 15) == 0) {
+            *reinterpret_cast<int4*>(dst + first) = make_int4(v[0], v[1], v[2], v[3]);
+        } else {
+#pragma unroll
+            for (int u = 0; u < kSlotRun; ++u)
+                if (first + u < p.max_tokens) dst[first + u] = v[u];
+        }
+    };
+    store(p.slot_map, slot);
+    if (p.tok_pos) store(p.tok_pos, pos);
 }
 
 // ------------------------------------------------------------------------------------

@@ -101,6 +101,7 @@ __device__ void stage_row(const kvq_mla_tree_problem& p, int64_t row, const floa
         const int bits = rotated_bits(p.fmt), bytes = kDLat * bits / 8;
         const float sig = C.lat_scale[row] * tq4_inv_sqrt(kDLat);
         const uint8_t* src = C.lat + row * bytes;
+#pragma unroll
         for (int k = 0; k < kDLat / 32; ++k) {
             const int b0 = (k * 32 + lane) * bits, at = b0 >> 3;
             const uint32_t w = src[at] | (at + 1 < bytes ? (uint32_t)src[at + 1] << 8 : 0u);
@@ -271,8 +272,10 @@ void plan_tree(const kvq_mla_tree_problem& p, TreePlan& t)
     kvq_mla_problem& d = t.prefix;
     d = kvq_mla_problem{};
     d.n_seq = p.n_seq;
-    d.n_q = p.n_q;
-    d.n_heads = p.n_heads;
+    // every node sees all of the prefix: the (node, head) rows are the heads of one query, so that
+    // the kernels' groups of 16 or 32 heads fill up whatever the number of heads
+    d.n_q = 1;
+    d.n_heads = p.n_q * p.n_heads;
     d.d_lat = kDLat;
     d.d_rope = kDRope;
     d.max_seq_len = p.max_seq_len;
