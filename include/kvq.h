@@ -454,7 +454,7 @@ int kvq_mla_decode_noalloc(const kvq_mla_problem* p, float* out, float* lse,
  */
 typedef struct kvq_page_plan {
     int32_t n_seq;                  /* 0 .. 65535                                       */
-    int32_t max_pages, page_size;
+    int32_t max_pages, page_size;   /* max_pages: 1 .. 2^20                              */
     int32_t n_pages;                /* pages of the pool = entries of free_list          */
     int32_t max_tokens;             /* entries of slot_map and tok_pos                   */
     const int32_t* keep_len;        /* device [n_seq]                                   */

@@ -31,7 +31,8 @@ constexpr int kInlineTokens = 4096;
 constexpr int kSlotThreads = 256;
 constexpr int kSlotRun = 4;                  // consecutive tokens per thread of the second launch
 constexpr int kSlotTile = kSlotThreads * kSlotRun;
-constexpr int kMoves = 4;                    // page moves a thread keeps in flight
+constexpr int kMoves = 4;                    // consecutive page moves per thread, in flight together
+constexpr int kMaxPages = 1 << 20;           // pages of a table row: a chunk's moves fit 31 bits
 constexpr int kSlotShared = 2048;            // sequence offsets searched in shared memory
 
 struct ResizeArgs {
@@ -106,7 +107,7 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_warp, int64_
 
 // the largest i in [lo, hi] with a[i] <= x (a ascending, a[lo] <= x)
 template <typename T>
-__device__ __forceinline__ int last_not_above(const T* a, int lo, int hi, int64_t x)
+__device__ __forceinline__ int last_not_above(const T* a, int lo, int hi, T x)
 {
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -140,7 +141,7 @@ __device__ __forceinline__ void write_slot(const kvq_page_plan& p, int i, int s,
 __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeArgs a)
 {
     __shared__ int64_t s_warp[33];
-    __shared__ int64_t s_pre[kMaxThreads];               // exclusive prefix of the chunk's page moves
+    __shared__ int s_pre[kMaxThreads + 1];               // exclusive prefix of the chunk's page moves, then all
     __shared__ int s_first[kMaxThreads];                 // first table entry of the sequence that moves
     __shared__ int64_t s_base[kMaxThreads];              // list position of that entry's page (-1: refused)
     __shared__ unsigned long long s_used;
@@ -197,22 +198,22 @@ __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeA
             const int64_t give = live ? max(q.held - q.need, 0) : 0;
             int64_t sum;
             const int64_t incl = block_scan(give, s_warp, &sum);
-            s_pre[tid] = incl - give;
+            s_pre[tid] = (int)(incl - give);
             s_first[tid] = q.need;
             s_base[tid] = n_free + (give_all - carry - incl) + give - 1;   // of entry q.need, descending
+            if (tid == 0) s_pre[T] = (int)sum;
             __syncthreads();
-            const int last = min(T, p.n_seq - c) - 1;
-            for (int64_t i0 = tid; i0 < sum; i0 += (int64_t)T * kMoves) {
+            for (int i0 = tid * kMoves; i0 < (int)sum; i0 += T * kMoves) {
                 int32_t* e[kMoves];
                 int64_t at[kMoves];
                 int32_t page[kMoves];
+                int k = last_not_above(s_pre, 0, T - 1, i0);
 #pragma unroll
                 for (int u = 0; u < kMoves; ++u) {
-                    const int64_t i = i0 + (int64_t)u * T;
                     e[u] = nullptr;
-                    if (i >= sum) continue;
-                    const int k = last_not_above(s_pre, 0, last, i);
-                    const int64_t d = i - s_pre[k];
+                    if (i0 + u >= (int)sum) continue;
+                    while (s_pre[k + 1] <= i0 + u) ++k;
+                    const int d = i0 + u - s_pre[k];
                     e[u] = p.block_table + (int64_t)(c + k) * p.max_pages + s_first[k] + d;
                     at[u] = s_base[k] - d;
                     page[u] = *e[u];
@@ -241,23 +242,23 @@ __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeA
         const int64_t end = carry + block_scan(take, s_warp, &sum);
         const bool served = live && q.fits && (take == 0 || end <= have);
         if (live && q.fits && !served) bits |= KVQ_DEV_NO_PAGE;
-        s_pre[tid] = end - take - carry;
+        s_pre[tid] = (int)(end - take - carry);
         s_first[tid] = q.held;
         s_base[tid] = served ? have - 1 - (end - take) : -1;
+        if (tid == 0) s_pre[T] = (int)sum;
         if (served && take > 0) atomicMax(&s_used, (unsigned long long)end);
         __syncthreads();
-        const int last = min(T, p.n_seq - c) - 1;
-        for (int64_t i0 = tid; i0 < sum; i0 += (int64_t)T * kMoves) {
+        for (int i0 = tid * kMoves; i0 < (int)sum; i0 += T * kMoves) {
             int32_t* e[kMoves];
             int32_t page[kMoves];
+            int k = last_not_above(s_pre, 0, T - 1, i0);
 #pragma unroll
             for (int u = 0; u < kMoves; ++u) {
-                const int64_t i = i0 + (int64_t)u * T;
                 e[u] = nullptr;
-                if (i >= sum) continue;
-                const int k = last_not_above(s_pre, 0, last, i);
+                if (i0 + u >= (int)sum) continue;
+                while (s_pre[k + 1] <= i0 + u) ++k;
                 if (s_base[k] < 0) continue;             // refused, as is every page wanted after it
-                const int64_t d = i - s_pre[k];
+                const int d = i0 + u - s_pre[k];
                 e[u] = p.block_table + (int64_t)(c + k) * p.max_pages + s_first[k] + d;
                 page[u] = p.free_list[s_base[k] - d];
             }
@@ -311,7 +312,7 @@ __global__ void __launch_bounds__(kSlotThreads) slot_map_kernel(const ResizeArgs
         slot[u] = pos[u] = -1;
         if (i >= n_tok) continue;
         if (i >= end) {
-            s = s < 0 ? last_not_above(start, 0, p.n_seq - 1, i) : s + 1;
+            s = s < 0 ? last_not_above(start, 0, p.n_seq - 1, (int)i) : s + 1;
             while (start[s + 1] <= i) ++s;               // (sequences without tokens)
             begin = start[s];
             end = start[s + 1];
@@ -464,7 +465,7 @@ int kvq_resize_pages(const kvq_page_plan* p, uint32_t* dev_status, kvq_stream_t 
     if (int st = fault_injected(E)) return st;
     if (!p) return set_last_error(KVQ_EINVAL, "%s: NULL plan", E);
     if (p->n_seq < 0 || p->n_seq > 65535) return set_last_error(KVQ_EINVAL, "%s: n_seq outside [0, 65535]", E);
-    if (p->max_pages < 1 || p->page_size < 1 || p->n_pages < 0 || p->max_tokens < 0)
+    if (p->max_pages < 1 || p->max_pages > kMaxPages || p->page_size < 1 || p->n_pages < 0 || p->max_tokens < 0)
         return set_last_error(KVQ_EINVAL, "%s: bad sizes", E);
     if ((int64_t)p->n_pages * p->page_size > INT32_MAX)
         return set_last_error(KVQ_EINVAL, "%s: a pool of more than INT32_MAX rows", E);

@@ -35,7 +35,7 @@ def plan(kvq, **kw):
 def test_resize_pages_argument_errors(kvq):
     call = lambda **kw: kvq.lib().kvq_resize_pages(C.byref(plan(kvq, **kw)), None, None)
     assert kvq.lib().kvq_resize_pages(None, None, None) == 1
-    for bad in (dict(n_seq=-1), dict(n_seq=65536), dict(max_pages=0), dict(page_size=0), dict(n_pages=-1),
+    for bad in (dict(n_seq=-1), dict(n_seq=65536), dict(max_pages=0), dict(max_pages=(1 << 20) + 1), dict(page_size=0), dict(n_pages=-1),
                 dict(max_tokens=-1), dict(n_pages=1 << 26, page_size=64), dict(keep_len=None), dict(n_new=None),
                 dict(block_table=None), dict(n_held=None), dict(free_list=None), dict(n_free=None),
                 dict(seq_len=None), dict(tok_start=None), dict(slot_map=None), dict(seq_len=FAKE),
