@@ -315,8 +315,13 @@ struct Walk {
     {
         if (left <= 0) return;
         shape(p);
-        rt = (int)(off / (nt + kUnitCost));
-        at = (int)(off % (nt + kUnitCost));
+        if (off <= INT32_MAX) {                           // (a 64-bit division takes microseconds)
+            rt = (int)off / (nt + kUnitCost);
+            at = (int)off % (nt + kUnitCost);
+        } else {
+            rt = (int)(off / (nt + kUnitCost));
+            at = (int)(off % (nt + kUnitCost));
+        }
         tiles();
         if (tile == end) next(p);
     }
@@ -516,24 +521,32 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         tmem_alloc(sh.tmem_base(), 512);
         tmem_relinquish();
     }
-    // ---- the length of the line, and where this CTA's stretch begins (scratch: the W image)
+    // ---- the length of the line, and where this CTA's stretch begins (scratch: the W image) ----
+    // One pass over the sequences if they fit the threads; else a first pass for the length.
     int64_t total = 0, t0 = 0, t1 = 0;
     int G = gridDim.x;
     {
-        int64_t* s_sum = reinterpret_cast<int64_t*>(sh.w());      // [32] sums of the warps
+        int64_t* s_sum = reinterpret_cast<int64_t*>(sh.w());      // sums of the warps
         constexpr int kW = kThreads / 32;
-        int64_t v = 0;
-        for (int s = tid; s < p.n_seq; s += kThreads) v += seq_places<NR>(p, s);
+        const bool one_pass = p.n_seq <= kThreads;
+        auto stretch = [&]() {
+            G = (int)min((int64_t)G, max(total, (int64_t)1));
+            t0 = g < G ? cut(total, g, G) : 0;
+            t1 = g < G ? cut(total, g + 1, G) : 0;
+        };
+        if (!one_pass) {
+            int64_t v = 0;
+            for (int s = tid; s < p.n_seq; s += kThreads) v += seq_places<NR>(p, s);
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
-        if (lane == 0) s_sum[warp] = v;
-        __syncthreads();
-        for (int w = 0; w < kW; ++w) total += s_sum[w];
-        G = (int)min((int64_t)G, max(total, (int64_t)1));
-        t0 = g < G ? cut(total, g, G) : 0;
-        t1 = g < G ? cut(total, g + 1, G) : 0;
+            for (int o = 16; o >= 1; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+            if (lane == 0) s_sum[warp] = v;
+            __syncthreads();
+            for (int w = 0; w < kW; ++w) total += s_sum[w];
+            stretch();
+            __syncthreads();
+        }
         int64_t base = 0;
-        for (int c = 0; c < p.n_seq && base <= t0 && t1 > t0; c += kThreads) {
+        for (int c = 0; c < p.n_seq && base <= t0; c += kThreads) {
             const int s = c + tid;
             const int64_t own = s < p.n_seq ? seq_places<NR>(p, s) : 0;
             int64_t incl = own;
@@ -542,13 +555,17 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 const int64_t u = __shfl_up_sync(kFull, incl, o);
                 if (lane >= o) incl += u;
             }
-            __syncthreads();
             if (lane == 31) s_sum[warp] = incl;
             __syncthreads();
             int64_t before = base, all = base;
+#pragma unroll
             for (int w = 0; w < kW; ++w) {
                 if (w < warp) before += s_sum[w];
                 all += s_sum[w];
+            }
+            if (one_pass) {
+                total = all;
+                stretch();
             }
             const int64_t lo = before + incl - own;
             if (own > 0 && lo <= t0 && t0 < lo + own) {
@@ -556,6 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 *sh.start_off() = t0 - lo;
             }
             base = all;
+            if (!one_pass) __syncthreads();
         }
     }
     tc_fence_before();
@@ -1060,19 +1078,24 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
 
 // ------------------------------------------------------------------------------------
 // Padding rows (zeros), then the units that several CTAs shared: CTA = (unit or CTA, row of
-// the tile); its eight warps take the pieces in turn, lane = 16 dims.
+// the tile, part of the dims); its eight warps take the pieces in turn, lane = 4 V dims.  Few
+// rows have their dims split over four CTAs (V = 1), so that the partials of a long sequence
+// cut into 152 pieces are read by enough SMs.
 // ------------------------------------------------------------------------------------
 constexpr int kCombThreads = 256;
+constexpr int kCombWarps = kCombThreads / 32;
 
-template <int NR>
+template <int NR, int V>
 __global__ void __launch_bounds__(kCombThreads) tree_combine_kernel(const __grid_constant__ Args a)
 {
-    __shared__ __align__(16) float s_o[kCombThreads / 32][kDLat];
-    __shared__ float s_l[kCombThreads / 32];
+    constexpr int kDims = 128 * V;
+    __shared__ __align__(16) float s_o[kCombWarps][kDims];
+    __shared__ float s_l[kCombWarps];
     const kvq_mla_tree_problem& p = a.p;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t H = p.n_heads;
-    for (int64_t pr = blockIdx.x + (int64_t)gridDim.x * blockIdx.y; pr < (int64_t)p.n_seq * p.n_q; pr += (int64_t)gridDim.x * gridDim.y) {
+    const int64_t n_cta = (int64_t)gridDim.x * gridDim.y * gridDim.z;
+    for (int64_t pr = blockIdx.x + gridDim.x * ((int64_t)blockIdx.y + (int64_t)gridDim.y * blockIdx.z); pr < (int64_t)p.n_seq * p.n_q; pr += n_cta) {
         const int2 sh = tree_seq_shape(p, (int)(pr / p.n_q));
         if (pr % p.n_q < sh.y) continue;              // a node (there is one only if L > 0)
         uint4* o = reinterpret_cast<uint4*>(a.out + pr * H * kDLat);
@@ -1100,19 +1123,19 @@ __global__ void __launch_bounds__(kCombThreads) tree_combine_kernel(const __grid
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kFull, M, o));
     gave_up = __any_sync(kFull, gave_up);
-    float4 acc[4];
+    float4 acc[V];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int j = 0; j < V; ++j) acc[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     float l = 0.0f;
-#pragma unroll 4
-    for (int k = warp; k < f.pieces; k += kCombThreads / 32) {
+#pragma unroll (8 / V + 2)
+    for (int k = warp; k < f.pieces; k += kCombWarps) {
         const int64_t i = at(k);
         const float2 x = ml[i];
         const float w = ex2(x.x - M);
         l = fmaf(x.y, w, l);
-        const float4* o = reinterpret_cast<const float4*>(a.part_o + i * kDLat) + lane;
+        const float4* o = reinterpret_cast<const float4*>(a.part_o + i * kDLat + kDims * blockIdx.z) + lane;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int j = 0; j < V; ++j) {
             const float4 v = o[32 * j];
             acc[j].x = fmaf(v.x, w, acc[j].x);
             acc[j].y = fmaf(v.y, w, acc[j].y);
@@ -1121,13 +1144,14 @@ __global__ void __launch_bounds__(kCombThreads) tree_combine_kernel(const __grid
         }
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) reinterpret_cast<float4*>(s_o[warp])[32 * j + lane] = acc[j];
+    for (int j = 0; j < V; ++j) reinterpret_cast<float4*>(s_o[warp])[32 * j + lane] = acc[j];
     if (lane == 0) s_l[warp] = l;
     __syncthreads();
+    if (tid >= kDims / 2) return;
     float lt = 0.0f;
     float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll
-    for (int w = 0; w < kCombThreads / 32; ++w) {
+    for (int w = 0; w < kCombWarps; ++w) {
         lt += s_l[w];
         const float2 v = reinterpret_cast<const float2*>(s_o[w])[tid];
         o.x += v.x;
@@ -1135,15 +1159,21 @@ __global__ void __launch_bounds__(kCombThreads) tree_combine_kernel(const __grid
     }
     const float inv = gave_up ? NAN : lt == 0.0f ? 0.0f : 1.0f / lt;
     const int64_t row = (int64_t)f.s * p.n_q * H + r;
-    reinterpret_cast<__nv_bfloat162*>(a.out + row * kDLat)[tid] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
-    if (tid == 0 && a.lse) a.lse[row] = gave_up ? NAN : lt == 0.0f ? -INFINITY : (M + log2f(lt)) * kLn2;
+    reinterpret_cast<__nv_bfloat162*>(a.out + row * kDLat + kDims * blockIdx.z)[tid] = __floats2bfloat162_rn(o.x * inv, o.y * inv);
+    if (tid == 0 && blockIdx.z == 0 && a.lse) a.lse[row] = gave_up ? NAN : lt == 0.0f ? -INFINITY : (M + log2f(lt)) * kLn2;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// 64 query rows a tile feed the tensor core best; few rows run in half tiles, whose softmax and
-// epilogue are half as long
-int tile_rows(const kvq_mla_tree_problem& p) { return (int64_t)p.n_q * p.n_heads <= 32 ? 32 : 64; }
+// 64 query rows a tile feed the tensor core best.  Up to 32 rows, and problems of at most two such
+// tiles an SM, run in half tiles: more SMs share the work, and the softmax, query image and epilogue
+// of each are half as long (64 rows: T = 1024 20.6 -> 16.5 us, T = 32768 45 -> 31 us; at T = 131072,
+// seven tiles an SM, both take 53 us, and with more the full tiles win).
+int tile_rows(const kvq_mla_tree_problem& p)
+{
+    const int64_t rows = (int64_t)p.n_q * p.n_heads, tiles = ((int64_t)p.max_seq_len + kRT - 1) / kRT;
+    return rows <= 32 || p.n_seq * ((rows + 63) / 64) * tiles <= 2 * sm_count() ? 32 : 64;
+}
 
 int64_t max_units(const kvq_mla_tree_problem& p)
 {
@@ -1191,7 +1221,9 @@ cudaError_t launch_packed_as(Args& a, const PackedPlan& t, cudaStream_t s)
     tree_packed_kernel<NR><<<t.ctas, kThreads, Cfg<NR>::kSmem, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_dependent(tree_combine_kernel<NR>, dim3((unsigned)t.infos, NR), dim3(kCombThreads), 0, s, a);
+    if (t.infos * NR <= 1024)
+        return launch_dependent(tree_combine_kernel<NR, 1>, dim3((unsigned)t.infos, NR, 4), dim3(kCombThreads), 0, s, a);
+    return launch_dependent(tree_combine_kernel<NR, 4>, dim3((unsigned)t.infos, NR), dim3(kCombThreads), 0, s, a);
 }
 
 }  // namespace
