@@ -31,7 +31,7 @@ constexpr int kInlineTokens = 4096;
 constexpr int kSlotThreads = 256;
 constexpr int kSlotRun = 4;                  // consecutive tokens per thread of the second launch
 constexpr int kSlotTile = kSlotThreads * kSlotRun;
-constexpr int kMoves = 4;                    // consecutive page moves per thread, in flight together
+constexpr int kMoves = 8;                    // page moves of a thread in flight together
 constexpr int kMaxPages = 1 << 20;           // pages of a table row: a chunk's moves fit 31 bits
 constexpr int kSlotShared = 2048;            // sequence offsets searched in shared memory
 
@@ -59,14 +59,14 @@ __device__ __forceinline__ Seq load_seq(const kvq_page_plan& p, int s)
 __device__ __forceinline__ void judge_seq(const kvq_page_plan& p, Seq& q, int64_t tok_end, unsigned& bits)
 {
     const int64_t len = (int64_t)q.keep + q.add;
-    const int64_t need = (len + p.page_size - 1) / p.page_size;
+    const uint32_t need = ((uint32_t)len + (uint32_t)p.page_size - 1u) / (uint32_t)p.page_size;   // (if len fits)
     q.fits = false;
     q.need = q.held;
     if (len > INT32_MAX || (q.add > 0 && tok_end > p.max_tokens)) {
         bits |= KVQ_DEV_BAD_INDEX;
     } else if (q.keep > (int64_t)q.held * p.page_size) {
         bits |= KVQ_DEV_BAD_PAGE;
-    } else if (need > p.max_pages) {
+    } else if (need > (uint32_t)p.max_pages) {
         bits |= KVQ_DEV_NO_PAGE;
     } else {
         q.fits = true;
@@ -77,7 +77,8 @@ __device__ __forceinline__ void judge_seq(const kvq_page_plan& p, Seq& q, int64_
 // a packed end as tok_start holds it: INT32_MAX stands for that or more, past any max_tokens
 __device__ __forceinline__ int64_t packed_end(int64_t end) { return end >= INT32_MAX ? (int64_t)INT32_MAX + 1 : end; }
 
-// inclusive prefix sum over the CTA; *total = the CTA's sum.  s_warp: 33 entries.
+// Inclusive prefix sum over the CTA; *total = the CTA's sum.  s_warp: 32 entries that no thread may
+// still be reading from an earlier call (one barrier a call: callers alternate buffers).
 __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_warp, int64_t* total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -88,21 +89,15 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* s_warp, int64_
     }
     if (lane == 31) s_warp[warp] = v;
     __syncthreads();
-    if (warp == 0) {
-        int64_t w = lane < nw ? s_warp[lane] : 0;
+    int64_t w = lane < nw ? s_warp[lane] : 0;            // every warp scans the warps' sums itself
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int64_t u = __shfl_up_sync(kFull, w, o);
-            if (lane >= o) w += u;
-        }
-        if (lane < nw) s_warp[lane] = w;
-        if (lane == 31) s_warp[32] = w;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(kFull, w, o);
+        if (lane >= o) w += u;
     }
-    __syncthreads();
-    if (warp > 0) v += s_warp[warp - 1];
-    *total = s_warp[32];
-    __syncthreads();
-    return v;
+    *total = __shfl_sync(kFull, w, 31);
+    const int64_t before = __shfl_sync(kFull, w, (warp + 31) & 31);
+    return warp > 0 ? v + before : v;
 }
 
 // the largest i in [lo, hi] with a[i] <= x (a ascending, a[lo] <= x)
@@ -138,24 +133,70 @@ __device__ __forceinline__ void write_slot(const kvq_page_plan& p, int i, int s,
     if (p.tok_pos) p.tok_pos[i] = pos;
 }
 
+// The moves of a chunk of sequences: sequence c + k moves the pages of its table entries s_first[k] ..,
+// s_pre[k + 1] - s_pre[k] of them; its first one's place in the list is s_base[k], descending.
+// kBack: table -> list (the entries become -1), else list -> table (s_base -1: none).  Returns whether
+// a page found no place in the list.
+template <bool kBack>
+__device__ __forceinline__ bool move_pages(const kvq_page_plan& p, int c, int sum, const int* s_pre, const int* s_first, const int64_t* s_base)
+{
+    const int T = blockDim.x, lane = threadIdx.x & 31;
+    bool lost = false;
+    // a warp takes 32 kMoves moves in a row, neighbouring lanes neighbouring entries
+    for (int i0 = (threadIdx.x & ~31) * kMoves + lane; i0 < sum; i0 += T * kMoves) {
+        int32_t* e[kMoves];
+        int64_t at[kMoves];
+        int32_t page[kMoves];
+        int k = last_not_above(s_pre, 0, T - 1, i0);
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+            const int i = i0 + 32 * u;
+            e[u] = nullptr;
+            if (i >= sum) continue;
+            while (s_pre[k + 1] <= i) ++k;
+            const int64_t b = s_base[k];
+            if (!kBack && b < 0) continue;
+            const int d = i - s_pre[k];
+            e[u] = p.block_table + (int64_t)(c + k) * p.max_pages + s_first[k] + d;
+            at[u] = b - d;
+            page[u] = kBack ? *e[u] : p.free_list[at[u]];
+        }
+#pragma unroll
+        for (int u = 0; u < kMoves; ++u) {
+            if (!e[u]) continue;
+            if (!kBack) {
+                *e[u] = page[u];
+            } else {
+                if (at[u] < p.n_pages) p.free_list[at[u]] = page[u];
+                else lost = true;
+                *e[u] = -1;
+            }
+        }
+    }
+    return lost;
+}
+
 __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeArgs a)
 {
-    __shared__ int64_t s_warp[33];
+    __shared__ int64_t s_warp[4][32];                    // scan buffers, in turn
     __shared__ int s_pre[kMaxThreads + 1];               // exclusive prefix of the chunk's page moves, then all
     __shared__ int s_first[kMaxThreads];                 // first table entry of the sequence that moves
-    __shared__ int64_t s_base[kMaxThreads];              // list position of that entry's page (-1: refused)
-    __shared__ unsigned long long s_used;
+    __shared__ int64_t s_base[kMaxThreads];              // list place of that entry's page (-1: refused)
+    __shared__ int s_used;
     const kvq_page_plan& p = a.p;
     const int tid = threadIdx.x, T = blockDim.x;
     grid_dependents_launch();                            // the slot launch may get ready
     unsigned bits = 0;
     const int n_free0 = p.n_free[0];
-    const int64_t n_free = min(max(n_free0, 0), p.n_pages);
+    const int n_free = min(max(n_free0, 0), p.n_pages);
     if (n_free0 != n_free && tid == 0) bits |= KVQ_DEV_BAD_INDEX;
     if (tid == 0) s_used = 0;
+    const bool one = p.n_seq <= T;                       // a single chunk stays in registers throughout
 
-    // ---- tokens' packed order, and the pages given back in all
-    int64_t tok = 0, give_all = 0;
+    // ---- tokens' packed order, and the pages given back in all.  Pages given and taken share
+    // one scan: a chunk's counts fit 31 bits each, given in the upper half
+    int64_t tok = 0, both = 0, sum = 0;
+    int64_t give_all = 0;
     Seq q{};
     for (int c = 0; c < p.n_seq; c += T) {
         const int s = c + tid;
@@ -164,117 +205,78 @@ __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeA
             q = load_seq(p, s);
             if (p.keep_len[s] < 0 || p.n_new[s] < 0 || p.n_held[s] != q.held) bits |= KVQ_DEV_BAD_INDEX;
         }
-        int64_t sum;
-        const int64_t end = tok + block_scan(live ? q.add : 0, s_warp, &sum);
-        int64_t give = 0;
+        const int buf = (c / T & 1) * 2;
+        const int64_t end = tok + block_scan(live ? q.add : 0, s_warp[buf], &sum);
+        tok += sum;
+        int64_t v = 0;
         if (live) {
             judge_seq(p, q, packed_end(end), bits);
             p.tok_start[s + 1] = (int)min(end, (int64_t)INT32_MAX);
-            give = max(q.held - q.need, 0);
+            v = ((int64_t)max(q.held - q.need, 0) << 32) + max(q.need - q.held, 0);
         }
-        tok += sum;
-        (void)block_scan(give, s_warp, &sum);
-        give_all += sum;
+        both = block_scan(v, s_warp[buf + 1], &sum);
+        give_all += sum >> 32;
     }
     if (tid == 0) p.tok_start[0] = 0;
-    const int64_t have = min(n_free + give_all, (int64_t)p.n_pages);
+    const int have = (int)min((int64_t)n_free + give_all, (int64_t)p.n_pages);
 
-    // a chunk's sequences again (the only chunk's are still in registers): same-thread reads
-    // of what this thread wrote or of inputs that have not changed yet
-    auto reload = [&](int s) {
-        if (p.n_seq <= T) return;
+    // a chunk's sequences and scan again: same-thread reads of what this thread wrote, or of
+    // inputs that have not changed yet
+    auto reload = [&](int c, int s) {
+        if (one) return;
         unsigned ignore = 0;
-        q = load_seq(p, s);
-        judge_seq(p, q, packed_end(p.tok_start[s + 1]), ignore);
+        int64_t v = 0;
+        if (s < p.n_seq) {
+            q = load_seq(p, s);
+            judge_seq(p, q, packed_end(p.tok_start[s + 1]), ignore);
+            v = ((int64_t)max(q.held - q.need, 0) << 32) + max(q.need - q.held, 0);
+        }
+        both = block_scan(v, s_warp[c / T & 3], &sum);
     };
 
     // ---- pages go back: sequence s's page e (from its last) to n_free + (given by later ones) + e
     if (give_all > 0) {
         int64_t carry = 0;
         for (int c = 0; c < p.n_seq; c += T) {
-            const int s = c + tid;
-            const bool live = s < p.n_seq;
-            if (live) reload(s);
-            const int64_t give = live ? max(q.held - q.need, 0) : 0;
-            int64_t sum;
-            const int64_t incl = block_scan(give, s_warp, &sum);
-            s_pre[tid] = (int)(incl - give);
+            __syncthreads();                             // the last chunk's moves are made
+            reload(c, c + tid);
+            const int give = c + tid < p.n_seq ? max(q.held - q.need, 0) : 0, incl = (int)(both >> 32);
+            s_pre[tid] = incl - give;
             s_first[tid] = q.need;
-            s_base[tid] = n_free + (give_all - carry - incl) + give - 1;   // of entry q.need, descending
-            if (tid == 0) s_pre[T] = (int)sum;
+            s_base[tid] = n_free + (give_all - carry - incl) + give - 1;   // of entry q.need
+            if (tid == 0) s_pre[T] = (int)(sum >> 32);
             __syncthreads();
-            for (int i0 = tid * kMoves; i0 < (int)sum; i0 += T * kMoves) {
-                int32_t* e[kMoves];
-                int64_t at[kMoves];
-                int32_t page[kMoves];
-                int k = last_not_above(s_pre, 0, T - 1, i0);
-#pragma unroll
-                for (int u = 0; u < kMoves; ++u) {
-                    e[u] = nullptr;
-                    if (i0 + u >= (int)sum) continue;
-                    while (s_pre[k + 1] <= i0 + u) ++k;
-                    const int d = i0 + u - s_pre[k];
-                    e[u] = p.block_table + (int64_t)(c + k) * p.max_pages + s_first[k] + d;
-                    at[u] = s_base[k] - d;
-                    page[u] = *e[u];
-                }
-#pragma unroll
-                for (int u = 0; u < kMoves; ++u) {
-                    if (!e[u]) continue;
-                    if (at[u] < p.n_pages) p.free_list[at[u]] = page[u];
-                    else bits |= KVQ_DEV_BAD_PAGE;
-                    *e[u] = -1;
-                }
-            }
-            carry += sum;
-            __syncthreads();
+            if (move_pages<true>(p, c, (int)(sum >> 32), s_pre, s_first, s_base)) bits |= KVQ_DEV_BAD_PAGE;
+            carry += sum >> 32;
         }
     }
 
     // ---- pages are taken: the d-th page wanted is the d-th from the top
     int64_t carry = 0;
     for (int c = 0; c < p.n_seq; c += T) {
+        __syncthreads();
         const int s = c + tid;
         const bool live = s < p.n_seq;
-        if (live) reload(s);
-        const int64_t take = live ? max(q.need - q.held, 0) : 0;
-        int64_t sum;
-        const int64_t end = carry + block_scan(take, s_warp, &sum);
+        reload(c, s);
+        const int take = live ? max(q.need - q.held, 0) : 0, incl = (int)(both & 0x7FFFFFFF);
+        const int64_t end = carry + incl;
         const bool served = live && q.fits && (take == 0 || end <= have);
         if (live && q.fits && !served) bits |= KVQ_DEV_NO_PAGE;
-        s_pre[tid] = (int)(end - take - carry);
+        s_pre[tid] = incl - take;
         s_first[tid] = q.held;
-        s_base[tid] = served ? have - 1 - (end - take) : -1;
-        if (tid == 0) s_pre[T] = (int)sum;
-        if (served && take > 0) atomicMax(&s_used, (unsigned long long)end);
+        s_base[tid] = served ? have - 1 - (int)(end - take) : -1;
+        if (tid == 0) s_pre[T] = (int)(sum & 0x7FFFFFFF);
+        if (served && take > 0) atomicMax(&s_used, (int)end);
         __syncthreads();
-        for (int i0 = tid * kMoves; i0 < (int)sum; i0 += T * kMoves) {
-            int32_t* e[kMoves];
-            int32_t page[kMoves];
-            int k = last_not_above(s_pre, 0, T - 1, i0);
-#pragma unroll
-            for (int u = 0; u < kMoves; ++u) {
-                e[u] = nullptr;
-                if (i0 + u >= (int)sum) continue;
-                while (s_pre[k + 1] <= i0 + u) ++k;
-                if (s_base[k] < 0) continue;             // refused, as is every page wanted after it
-                const int d = i0 + u - s_pre[k];
-                e[u] = p.block_table + (int64_t)(c + k) * p.max_pages + s_first[k] + d;
-                page[u] = p.free_list[s_base[k] - d];
-            }
-#pragma unroll
-            for (int u = 0; u < kMoves; ++u)
-                if (e[u]) *e[u] = page[u];
-        }
+        (void)move_pages<false>(p, c, (int)(sum & 0x7FFFFFFF), s_pre, s_first, s_base);
         if (live) {
             p.seq_len[s] = served ? q.keep + q.add : (int)min((int64_t)q.keep, (int64_t)q.held * p.page_size);
             if (served) p.n_held[s] = q.need;
         }
-        carry += sum;
-        __syncthreads();
+        carry += sum & 0x7FFFFFFF;
     }
     __syncthreads();
-    if (tid == 0) p.n_free[0] = (int)(have - (int64_t)s_used);
+    if (tid == 0) p.n_free[0] = have - s_used;
     if (bits) flag(a.status, bits);
 
     if (a.inline_slots) {
