@@ -242,7 +242,7 @@ int validate_tree(const kvq_mla_tree_problem* p, const char* E)
     }
     if (p->impl == 1 && p->fmt != KVQ_FMT_FP8) return set_last_error(KVQ_EFORMAT, "%s: impl 1 reads FP8 rows only", E);
     if (p->impl == 1 && !tree_packed_reads(*p))
-        return set_last_error(KVQ_EINVAL, "%s: impl 1 reads contiguous rows or pages of a multiple of 8 rows", E);
+        return set_last_error(KVQ_EINVAL, "%s: impl 1 reads contiguous rows or pages of a multiple of 8 rows (and 2^36 tiles at most)", E);
     if (p->n_seq == 0) return KVQ_OK;
     const kvq_mla_cache& c = p->cache;
     if (!p->seq_len || !p->q_lat || !p->q_rope || !c.lat || !c.lat_scale || !c.rope || !c.rope_scale || c.n_rows < 0 ||

@@ -1230,7 +1230,9 @@ cudaError_t launch_packed_as(Args& a, const PackedPlan& t, cudaStream_t s)
 
 bool tree_packed_reads(const kvq_mla_tree_problem& p)
 {
-    return p.cache.n_rows <= INT32_MAX && (!p.block_table || p.page_size % 8 == 0);
+    // (a stretch of the line counts its places in an int)
+    const double places = (double)p.n_seq * ((double)p.n_q * p.n_heads / 32 + 1) * ((double)p.max_seq_len / kRT + 1 + kUnitCost);
+    return p.cache.n_rows <= INT32_MAX && (!p.block_table || p.page_size % 8 == 0) && places < 0x1p36;
 }
 
 size_t tree_packed_workspace(const kvq_mla_tree_problem& p) { return plan_packed(p).bytes; }

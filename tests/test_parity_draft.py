@@ -230,6 +230,23 @@ def test_append_bytes_and_untouched_rows(kvq, orc, fmt, bf16, rows):
     assert st.item() == (BAD_PAGE if rows > 7 else 0)
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_append_extreme_magnitudes(kvq, orc, bf16):
+    """fp8 rows from the smallest normal numbers to 1e35: the quotients by the row's scale are IEEE ones
+    at every scale, codes and scales byte for byte."""
+    g = np.random.default_rng(0)
+    mag = np.concatenate([10.0 ** np.arange(-37, 36, 1.0), [2.0**-81, 2.0**-82, 2.0**99, 2.0**98]]).astype(np.float32)
+    x = (W.normal(g, (len(mag), 576)) * mag[:, None]).astype(np.float32)
+    both = dev(x).bfloat16() if bf16 else dev(x)
+    planes = empty_planes(1, len(mag))
+    kvq.kvq_append_mla(both[:, :512], both[:, 512:], torch.arange(len(mag), dtype=torch.int32, device="cuda"), 1, None, planes)
+    torch.cuda.synchronize()
+    host = both.float().cpu().numpy()
+    ref = encode_ref(orc, 1, np.ascontiguousarray(host[:, :512]), np.ascontiguousarray(host[:, 512:]), None)
+    for key in ref:
+        assert np.array_equal(planes[key].cpu().numpy().view(np.uint8), ref[key].view(np.uint8)), key
+
+
 def test_append_equals_encode_mla(kvq):
     """The bytes of kvq_encode_mla, at the identity and a reversed slot map; zero rows."""
     n = 600
@@ -427,6 +444,55 @@ def test_tree_ragged_pages_padding(kvq, orc, fmt, impl, page, H):
     check_tree(got, ref)
 
 
+@pytest.mark.parametrize("n_seq,n,H,T,page,kind", [(2, 16, 33, 2400, 64, "tree"), (1, 64, 50, 1100, 0, "any"),
+                                                   (40, 4, 64, 700, 16, "tree"), (3, 7, 129, 3001, 128, "chain")])
+def test_tree_full_tiles(kvq, orc, n_seq, n, H, T, page, kind):
+    """Problems large enough for tiles of 64 query rows: units split among CTAs, several units a
+    CTA, more units than CTAs; ragged lengths and nodes; the same bits at a second call."""
+    g = np.random.default_rng(T)
+    signs = W.sign_bits(T)
+    lens = [T] + [int(x) for x in g.integers(1, T + 1, n_seq - 1)]
+    n_node = [min(int(x), L) for x, L in zip([n] + list(g.integers(1, n + 1, n_seq - 1)), lens)]
+    if page:
+        table, rows, rows_of = paged(lens, page, g)
+    else:
+        table, rows, rows_of = None, n_seq * T, contiguous(lens, T)
+    cache = make_cache(orc, 1, rows, T, signs)
+    masks = masks_of(g, n_node, n, kind)
+    ql, qr = queries(n_seq, n, H, T)
+    runs = [run_tree(kvq, fmt=1, cache=cache, signs=signs, lens=lens, n_node=n_node, masks=masks, q_lat=ql, q_rope=qr,
+                     table=table, page=page, stride=T, impl=1) for _ in range(2)]
+    ref = tree_ref(orc, 1, cache, signs, rows_of, lens, n_node, masks, ql.float().cpu().numpy(),
+                   qr.float().cpu().numpy(), float(W.SM_SCALE))
+    assert runs[0][2] == 0
+    check_tree(runs[0], ref)
+    assert np.array_equal(runs[0][0], runs[1][0]) and np.array_equal(runs[0][1], runs[1][1])
+
+
+@pytest.mark.parametrize("impl", [1, 2])
+def test_tree_many_short_sequences(kvq, orc, impl):
+    """More sequences than a CTA has threads, lengths from 0 to 200."""
+    n_seq, n_q, H, cap = 1500, 2, 3, 200
+    g = np.random.default_rng(3)
+    signs = W.sign_bits(1)
+    lens = [int(x) for x in g.integers(0, cap + 1, n_seq)]
+    n_node = [min(int(x), L) for x, L in zip(g.integers(0, n_q + 1, n_seq), lens)]
+    cache = make_cache(orc, 1, 4096, 3, signs)
+    starts = g.integers(0, 4096 // 8, (n_seq, cap // 8)).astype(np.int32)        # pages of 8, shared freely
+    masks = masks_of(g, n_node, n_q, "tree")
+    ql, qr = queries(n_seq, n_q, H, 2)
+
+    def rows_of(s):
+        t = np.arange(lens[s])
+        return starts[s, t // 8].astype(np.int64) * 8 + t % 8, np.ones(lens[s], bool)
+    got = run_tree(kvq, fmt=1, cache=cache, signs=signs, lens=lens, n_node=n_node, masks=masks, q_lat=ql, q_rope=qr,
+                   table=starts, page=8, impl=impl, max_len=cap)
+    ref = tree_ref(orc, 1, cache, signs, rows_of, lens, n_node, masks, ql.float().cpu().numpy(),
+                   qr.float().cpu().numpy(), float(W.SM_SCALE))
+    assert got[2] == 0
+    check_tree(got, ref)
+
+
 @pytest.mark.parametrize("impl", [1, 2])
 def test_tree_missing_pages(kvq, orc, impl):
     """A page id of -1, one past the pool and a table that is too short: those rows are skipped and
@@ -457,11 +523,15 @@ def test_tree_missing_pages(kvq, orc, impl):
     check_tree(got, ref)
 
 
-@pytest.mark.parametrize("impl", [1, 2])
-def test_tree_unused_rows_and_unwritten_codes(kvq, orc, impl):
+# 20 heads run in tiles of 32 query rows, 640 in tiles of 64
+SIZES = pytest.mark.parametrize("impl,H", [(1, 20), (1, 640), (2, 20)])
+
+
+@SIZES
+def test_tree_unused_rows_and_unwritten_codes(kvq, orc, impl, H):
     """Rows behind a sequence, and rows that a node does not see, may hold NaN codes and scales; the code
     S.1111.111 in a row that is seen reads as 0."""
-    T, n_q, H = 333, 10, 7
+    T, n_q = 999, 5
     g = np.random.default_rng(9)
     signs = W.sign_bits(1)
     cache = make_cache(orc, 1, T + 64, 4, signs)
@@ -473,8 +543,8 @@ def test_tree_unused_rows_and_unwritten_codes(kvq, orc, impl):
     for key in ("lat_scale", "rope_scale"):
         cache[key][T:] = np.nan
     masks = masks_of(g, [n_q], n_q, "tree")
-    masks &= ~np.uint64(1 << 4)                           # nobody sees node 4, whose scales are not finite
-    cache["lat_scale"][T - n_q + 4], cache["rope_scale"][T - n_q + 4] = np.inf, np.nan
+    masks &= ~np.uint64(1 << 3)                           # nobody sees node 3, whose scales are not finite
+    cache["lat_scale"][T - n_q + 3], cache["rope_scale"][T - n_q + 3] = np.inf, np.nan
     ql, qr = queries(1, n_q, H, 7)
     got = run_tree(kvq, fmt=1, cache=cache, signs=signs, lens=[T], n_node=[n_q], masks=masks, q_lat=ql, q_rope=qr, impl=impl)
     host = {k: v.copy() for k, v in cache.items()}
@@ -485,12 +555,12 @@ def test_tree_unused_rows_and_unwritten_codes(kvq, orc, impl):
     check_tree(got, ref)
 
 
-@pytest.mark.parametrize("impl", [1, 2])
+@SIZES
 @pytest.mark.parametrize("case", ["large scores", "zero queries", "zero rows", "mixed magnitudes", "one row"])
-def test_tree_score_ranges(kvq, orc, impl, case):
+def test_tree_score_ranges(kvq, orc, impl, H, case):
     """Scores far apart (one row takes everything; running maxima that climb by many powers of
     two), all equal, and rows of zero scale."""
-    T, n_q, H = 900, 4, 20
+    T, n_q = 900, 4
     g = np.random.default_rng(11)
     signs = W.sign_bits(1)
     scale = float(W.SM_SCALE)
@@ -536,6 +606,61 @@ def test_tree_strided_queries_stream_and_no_lse(kvq, orc, impl):
         side.synchronize()
         outs.append(out)
     assert torch.equal(outs[0], outs[1])
+
+
+@pytest.mark.parametrize("n_seq,H", [(1, 16), (3, 200)])
+def test_tree_waits_give_up_then_recover(kvq, orc, n_seq, H):
+    """With the limit of the pipeline's waits cut to 200 ns the call still returns, sets KVQ_DEV_TIMEOUT and
+    leaves rows that are NaN whole or right; with the default limit the next call is right again."""
+    T, n_q = 5000, 4
+    g = np.random.default_rng(6)
+    signs = W.sign_bits(1)
+    host = make_cache(orc, 1, n_seq * T, 7, signs)
+    cache = {k: dev(v) for k, v in host.items()}
+    masks = masks_of(g, [n_q] * n_seq, n_q, "tree")
+    ql, qr = queries(n_seq, n_q, H, 8)
+    kw = dict(fmt=1, cache=cache, signs=signs, lens=[T] * n_seq, n_node=[n_q] * n_seq, masks=masks, q_lat=ql, q_rope=qr,
+              stride=T, impl=1)
+    ref = tree_ref(orc, 1, host, signs, contiguous([T] * n_seq, T), [T] * n_seq, [n_q] * n_seq, masks,
+                   ql.float().cpu().numpy(), qr.float().cpu().numpy(), float(W.SM_SCALE))
+    assert kvq.lib().kvq_set_wait_limit_ns(200) == 0
+    try:
+        out, lse, st = run_tree(kvq, **kw)
+    finally:
+        assert kvq.lib().kvq_set_wait_limit_ns(0) == 0
+    assert st & kvq.DEV_TIMEOUT
+    gone = np.isnan(out).all(-1)
+    assert gone.any() and np.array_equal(gone, np.isnan(lse)) and np.array_equal(gone, np.isnan(out).any(-1))
+    out[gone], lse[gone] = ref[0][gone], ref[1][gone]
+    check_tree((out, lse, st), ref)
+    got = run_tree(kvq, **kw)
+    assert got[2] == 0
+    check_tree(got, ref)
+
+
+def test_tree_two_calls_at_once(kvq, orc):
+    """Calls on two streams with their own workspaces do not touch one another."""
+    T, n_q, H = 3000, 8, 64
+    signs = W.sign_bits(1)
+    cache = {k: dev(v) for k, v in make_cache(orc, 1, T, 9, signs).items()}
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    jobs = []
+    for i in range(2):
+        ql, qr = queries(1, n_q, H, 30 + i)
+        p = kvq.make_tree_problem(seq_len=i32(1, fill=T), q_lat=ql, q_rope=qr, sm_scale=0.07, max_seq_len=T, fmt=1, cache=cache)
+        ws = torch.empty(kvq.kvq_mla_tree_decode_workspace(p), dtype=torch.uint8, device="cuda")
+        outs = [torch.empty(1, n_q, H, 512, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        jobs.append((p, ws, outs))
+    torch.cuda.synchronize()
+    for p, ws, outs in jobs:
+        kvq.kvq_mla_tree_decode(p, outs[0], None, ws)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for (p, ws, outs), s in zip(jobs, streams):
+            kvq.kvq_mla_tree_decode(p, outs[1], None, ws, stream=s.cuda_stream)
+    torch.cuda.synchronize()
+    for _, _, outs in jobs:
+        assert torch.equal(outs[0], outs[1])
 
 
 @pytest.mark.parametrize("fmt,impl", [(1, 1), (1, 2), (2, 2)])
