@@ -500,13 +500,14 @@ int kvq_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t l
  * A node with nothing to see, and every node j >= n (padding), gets out = 0 and lse = -inf;
  * the q rows of padding are not used.  A page that is missing or outside the pool sets
  * KVQ_DEV_BAD_PAGE and its rows are skipped.  The rows of a page past L may hold anything.
- * Queries and outputs are bfloat16; scores, softmax and sums are fp32, and so is lse.
+ * Queries and outputs are bfloat16; scores, softmax and sums are fp32, and so is lse.  A query row
+ * that holds a NaN or an infinity gets NaN (if it sees anything), and touches no other row.
  */
 typedef struct kvq_mla_tree_problem {
     int32_t n_seq, n_q, n_heads;    /* n_q: nodes a sequence at most, 1 .. 64            */
     int32_t d_lat, d_rope;          /* must be 512 and 64                               */
     int32_t fmt;                    /* KVQ_FMT_FP8 / TQ3 / TQ4 / TQ6                     */
-    int32_t max_seq_len;            /* host bound on every seq_len (clamped to it)       */
+    int32_t max_seq_len;            /* host bound on every seq_len (clamped to it), 0 .. 2^30 */
     const int32_t* seq_len;         /* device [n_seq]: rows held, the nodes' included    */
     const int32_t* n_node;          /* device [n_seq] (clamped as above) or NULL: n_q     */
     const uint64_t* mask;           /* device [n_seq][n_q] or NULL                      */
@@ -524,7 +525,7 @@ typedef struct kvq_mla_tree_problem {
 
 /*
  * The form that runs: 1, packed — every (node, head) row of a sequence shares one pass over
- * its cache, 64 rows a tile on the tensor cores (fp8 rows; contiguous sequences, or pages of a
+ * its cache, 64 or 32 rows a tile on the tensor cores (fp8 rows; contiguous sequences, or pages of a
  * multiple of 8 rows); 2 — kvq_mla_decode over the rows before the draft, query by query, then
  * the drafted rows joined to it (every tier and page size).  impl 0 takes 1 where it can read
  * the problem.  A negated status for an invalid problem (-KVQ_EFORMAT for impl 1 on another

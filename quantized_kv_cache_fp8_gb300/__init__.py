@@ -446,6 +446,22 @@ def _want(name, t, dtype, *shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, is {t.dtype} {list(got)}")
 
 
+def _one_device(*tensors):
+    """The index of the device that holds every tensor (-1: the host)."""
+    d = {t.get_device() for t in tensors if t is not None}
+    if len(d) != 1:
+        raise ValueError(f"tensors on different devices: {sorted(d)}")
+    return d.pop()
+
+
+def _on_current(d):
+    """`d` (a device index, -1: the host) must be the current device, which the kernels run on."""
+    if d >= 0:
+        import torch
+        if d != torch.cuda.current_device():
+            raise ValueError(f"tensors on cuda:{d}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
 def make_page_plan(*, keep_len, n_new, block_table, n_held, free_list, n_free, page_size, seq_len,
                    tok_start, slot_map, tok_pos=None) -> PagePlan:
     """Fill a kvq_page_plan from int32 tensors: block_table [n_seq, max_pages], free_list
@@ -465,10 +481,12 @@ def make_page_plan(*, keep_len, n_new, block_table, n_held, free_list, n_free, p
     p.free_list, p.n_free, p.seq_len = _ptr(free_list), _ptr(n_free), _ptr(seq_len)
     p.tok_start, p.slot_map, p.tok_pos = _ptr(tok_start), _ptr(slot_map), _ptr(tok_pos)
     p._keep = [keep_len, n_new, block_table, n_held, free_list, n_free, seq_len, tok_start, slot_map, tok_pos]
+    p._device = _one_device(*p._keep)
     return p
 
 
 def kvq_resize_pages(p: PagePlan, dev_status=None, stream=None) -> None:
+    _on_current(p._device)
     _check(lib().kvq_resize_pages(C.byref(p), _ptr(dev_status), _stream(stream)))
 
 
@@ -502,6 +520,8 @@ def kvq_append_mla(c_lat, k_rope, slot_map, fmt, sign_bits, planes: dict, dev_st
         ldx, ldr = 512, 64
     _want("slot_map", slot_map, "int32", rows)
     c = _mla_planes(planes, fmt)
+    _on_current(_one_device(c_lat, k_rope, slot_map, sign_bits, planes["lat"], planes["lat_scale"], planes["rope"],
+                            planes["rope_scale"]))
     _check(lib().kvq_append_mla(c_lat.data_ptr(), ldx, k_rope.data_ptr(), ldr, kind, rows, slot_map.data_ptr(),
                                 int(fmt), _ptr(sign_bits), C.byref(c), _ptr(dev_status), _stream(stream)))
 
@@ -541,6 +561,8 @@ def make_tree_problem(*, seq_len, q_lat, q_rope, sm_scale, max_seq_len, fmt, cac
     p.ldq_lat, p.ldq_rope = _row_stride("q_lat", q_lat, 512), _row_stride("q_rope", q_rope, 64)
     p.sm_scale, p.impl = float(sm_scale), int(impl)
     p._keep = [seq_len, n_node, mask, block_table, cache, signs, q_lat, q_rope]
+    p._device = _one_device(seq_len, n_node, mask, block_table, signs, q_lat, q_rope, cache["lat"], cache["lat_scale"],
+                            cache["rope"], cache["rope_scale"])
     return p
 
 
@@ -559,6 +581,7 @@ def kvq_mla_tree_decode_kernel(p: TreeProblem) -> int:
 def kvq_mla_tree_decode(p: TreeProblem, out, lse=None, workspace=None, dev_status=None, stream=None) -> None:
     _want("out", out, "bfloat16", p.n_seq, p.n_q, p.n_heads, 512)
     _want("lse", lse, "float32", p.n_seq, p.n_q, p.n_heads)
+    _on_current(_one_device(out, lse, workspace, p._keep[0]))
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().kvq_mla_tree_decode(C.byref(p), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
                                      _ptr(dev_status), _stream(stream)))
@@ -581,10 +604,13 @@ def make_accept(*, seq_len, path, n_acc, new_len, fmt, cache, n_node=None, block
         d.block_table, d.max_pages, d.page_size = _ptr(block_table), block_table.shape[1], int(page_size)
     d.seq_stride_rows, d.cache = int(seq_stride_rows), _mla_planes(cache, fmt)
     d._keep = [seq_len, n_node, path, n_acc, new_len, block_table, cache]
+    d._device = _one_device(seq_len, n_node, path, n_acc, new_len, block_table, cache["lat"], cache["lat_scale"],
+                            cache["rope"], cache["rope_scale"])
     return d
 
 
 def kvq_accept_mla(d: AcceptDesc, dev_status=None, stream=None) -> None:
+    _on_current(d._device)
     _check(lib().kvq_accept_mla(C.byref(d), _ptr(dev_status), _stream(stream)))
 
 

@@ -652,8 +652,20 @@ __device__ __forceinline__ void append_fp8_bf16_rows(const __nv_bfloat16* __rest
         }
 #pragma unroll
         for (int w = 8; w >= 1; w >>= 1) m = __vmaxu2(m, __shfl_xor_sync(kFull, m, w));
+        float amax = __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
+        if (__any_sync(kFull, isnan(amax))) {              // a NaN is passed over, as fmaxf does
+            amax = 0.0f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+            }
+#pragma unroll
+            for (int w = 8; w >= 1; w >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, w));
+        }
         if (o < 0) continue;
-        const float amax = __uint_as_float(max(m & 0xFFFFu, m >> 16) << 16);
         const float s = __fdiv_rn(amax, 448.0f);
         // IEEE quotients from one reciprocal a row: with y = RN(1 / s) and q = RN(x y), which is within
         // an ulp of x / s, RN(q + (x - q s) y) is RN(x / s) (Markstein, 1990), as long as the remainder

@@ -149,6 +149,11 @@ __global__ void __launch_bounds__(kThreads) tree_tail_kernel(const TreeArgs a)
         qr[0] = a.q_rope[r * kDRope + lane];
         qr[1] = a.q_rope[r * kDRope + 32 + lane];
     }
+    bool bad = !isfinite(qr[0]) || !isfinite(qr[1]);     // a NaN or an infinity in the query
+#pragma unroll
+    for (int k = 0; k < 16; ++k) bad |= !isfinite(q[k]);
+    bad = __any_sync(kFull, bad);
+    bool saw = false;
     if (rot) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) neg |= ((p.signs[k] >> lane) & 1u) << k;
@@ -182,6 +187,7 @@ __global__ void __launch_bounds__(kThreads) tree_tail_kernel(const TreeArgs a)
         for (int e = 0; e < kWarps && k0 + e < n; ++e) {
             if (!((see >> (k0 + e)) & 1u) || !s_ok[e]) continue;         // (the same in every lane)
             const float* x = s_row[e];
+            saw = true;
             float sc = fmaf(qr[0], x[kDLat + lane], qr[1] * x[kDLat + 32 + lane]);
 #pragma unroll
             for (int k = 0; k < 16; ++k) sc = fmaf(q[k], x[k * 32 + lane], sc);
@@ -203,9 +209,10 @@ __global__ void __launch_bounds__(kThreads) tree_tail_kernel(const TreeArgs a)
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[k] *= ((neg >> k) & 1u) ? -tq4_inv_sqrt(kDLat) : tq4_inv_sqrt(kDLat);
     }
-    const float lse0 = live ? a.pre_lse[r] : -INFINITY;
+    float lse0 = live ? a.pre_lse[r] : -INFINITY;
+    if (bad && (saw || lse0 != -INFINITY)) lse0 = NAN;
     const float M = fmaxf(lse0, m);
-    // (a prefix that gave up has lse0 = NaN: so have w0 and everything after it)
+    // (a query with a NaN or an infinity, or a prefix that gave up, has lse0 = NaN: so have w0 and everything after it)
     const float w0 = lse0 == -INFINITY ? 0.0f : expf(lse0 - M), w1 = m == -INFINITY ? 0.0f : expf(m - M);
     const float tot = w0 + w1 * l;
     const float inv = tot == 0.0f ? 0.0f : 1.0f / tot;
@@ -228,7 +235,8 @@ int validate_tree(const kvq_mla_tree_problem* p, const char* E)
         return set_last_error(KVQ_EFORMAT, "%s: fmt %d is not FP8, TQ3, TQ4 or TQ6", E, p->fmt);
     if (p->n_seq < 0 || p->n_seq > 65535) return set_last_error(KVQ_EINVAL, "%s: n_seq outside [0, 65535]", E);
     if (p->n_q < 1 || p->n_q > 64) return set_last_error(KVQ_EINVAL, "%s: n_q outside [1, 64]", E);
-    if (p->n_heads < 1 || p->max_seq_len < 0) return set_last_error(KVQ_EINVAL, "%s: bad sizes", E);
+    if (p->n_heads < 1) return set_last_error(KVQ_EINVAL, "%s: n_heads < 1", E);
+    if (p->max_seq_len < 0 || p->max_seq_len > 1 << 30) return set_last_error(KVQ_EINVAL, "%s: max_seq_len outside [0, 2^30]", E);
     if ((int64_t)p->n_q * (((int64_t)p->n_heads + 7) / 8) > 65535 || (int64_t)p->n_seq * p->n_q * p->n_heads > INT32_MAX)
         return set_last_error(KVQ_EINVAL, "%s: n_seq * n_q * n_heads too large", E);
     if (p->impl < 0 || p->impl > 2) return set_last_error(KVQ_EINVAL, "%s: impl must be 0..2", E);

@@ -159,10 +159,9 @@ struct Shared {
     __device__ volatile int* start_seq() const { return reinterpret_cast<volatile int*>(base + C::kOffMisc + 16); }
 };
 
-// Wait for a phase, bounded by %globaltimer.  The one-thread roles poll (kSpin): a thread that
-// sleeps in try_wait was seen to wake 1500 cycles late.  The 512 softmax threads sleep, so that
-// their polls stay out of the shared memory pipe (a limit below 100 us, set only to exercise the
-// failure path, always polls).
+// Wait for a phase, bounded by %globaltimer.  The one-thread roles poll (kSpin); the 512 softmax
+// threads sleep in try_wait, so that their polls stay out of the shared memory pipe (a limit
+// below 100 us, set only to exercise the failure path, always polls).
 template <bool kSpin, int NR>
 __device__ __forceinline__ bool wait_bar(const Shared<NR>& sh, uint64_t* bar, uint32_t parity, const Args& a)
 {
@@ -380,7 +379,8 @@ __device__ __forceinline__ void write_queries(const Shared<NR>& sh, const kvq_ml
         for (int e = 0; e < 10; ++e) m = __vmaxu2(m, w[n][e] & 0x7FFF7FFFu);
         m = max(m & 0xFFFFu, m >> 16);
         m = __reduce_max_sync(kFull, m);
-        const int sigma = m != 0 ? min(100, max(-100, 7 - ((int)(m >> 7) - 127))) : 0;
+        const bool finite = m < 0x7F80u;             // else the row's scores are NaN
+        const int sigma = m != 0 && finite ? min(100, 7 - ((int)(m >> 7) - 127)) : 0;
         const float scale = __int_as_float((127 + sigma) << 23);
         uint32_t d0[5], d1[5];
 #pragma unroll
@@ -401,7 +401,7 @@ __device__ __forceinline__ void write_queries(const Shared<NR>& sh, const kvq_ml
             *reinterpret_cast<uint32_t*>(rp + i * 64 + at) = d0[4];
             *reinterpret_cast<uint32_t*>(rp + (NR + i) * 64 + at) = d1[4];
         }
-        if (lane == 0) sh.gain()[i] = p.sm_scale * kLog2e * __int_as_float((127 - sigma) << 23);
+        if (lane == 0) sh.gain()[i] = finite ? p.sm_scale * kLog2e * __int_as_float((127 - sigma) << 23) : NAN;
     }
 }
 
@@ -483,9 +483,18 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 // ====================================================================================
 //  * Warps 0-15: softmax.  Thread = cache row of the tile (lane quarter warp % 4) for the NR / 4
 //    query rows of its part warp / 4; query images, epilogue (thread = output dim).
-//  * Warp 16: TMA loader, five boxes a tile into a two-stage ring.
+//  * Warps 16 and 19: TMA, five boxes a tile into a two-stage ring (a copy takes its issuing thread
+//    about 60 + 1.9 cycles a 128-byte row, so two share them: 16 the first two latent blocks and
+//    the rope key, 19 the other two).
 //  * Warp 17: tensor memory, score MMAs; warp 18: context MMAs.
-// The loader and the issuers run on into the next unit while the softmax warps finish one.
+// The loaders and the issuers run on into the next unit while the softmax warps finish one.
+//
+// A tile of 128 x 64 costs the tensor core 2974 cycles (N = 128 69 cycles, N = 64 54 cycles each MMA
+// of K = 32, measured) and the loop takes 4250 to 4600: it is bound by the chain context MMAs ->
+// box free -> copy -> score MMAs -> softmax -> context MMAs through a ring that shared memory
+// limits to two stages.  Measured, whole calls with the combine: 4 trees of 16 nodes x 64 heads at
+// T = 16384 314 us = 929 TFLOP/s; one of 32 x 128 heads at T = 20000 205 us = 890; 32 ragged ones up
+// to T = 65536 2395 us = 1037 TFLOP/s.
 // ====================================================================================
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_constant__ Args a)
@@ -607,9 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
             const bool whole = k.tile == 0 && k.end == k.nt;
             const int slot = 2 * g + (first_seg ? 0 : 1);
             write_queries(sh, p, s, r0, rows, warp, lane);
-            if (tid < NR) {
-                sh.neg_m()[tid] = 0.0f;
-            }
+            if (tid < NR) sh.neg_m()[tid] = 0.0f;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(sh.q_full());
@@ -914,10 +921,9 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
         for (; k.more() && ok; k.next(p)) {
             auto look_up = [&](int i, int buf) {      // the pool row where copy `lane` of tile i begins
                 const int t = i * kRT + lane * a.box_rows;
-                if (lane < per) {
-                    const int64_t r = t < k.L ? tree_pool_row(p, k.s, t) : -1;
-                    sh.copy_rows(2 * who + buf)[lane] = r < 0 || r >= p.cache.n_rows ? -1 : (int)r;
-                }
+                if (lane >= per) return;
+                const int64_t r = t < k.L ? tree_pool_row(p, k.s, t) : -1;
+                sh.copy_rows(2 * who + buf)[lane] = r < 0 || r >= p.cache.n_rows ? -1 : (int)r;
             };
             look_up(k.tile, c & 1);
             __syncwarp();
@@ -948,9 +954,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                         done[b < 4 ? b & 1 : 2] = c + 1;
                     }
                 }
-                if (i + 1 < k.end) {
-                    look_up(i + 1, (c + 1) & 1);
-                }
+                if (i + 1 < k.end) look_up(i + 1, (c + 1) & 1);
                 ok = __any_sync(kFull, leader && ok);
             }
         }

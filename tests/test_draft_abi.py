@@ -78,7 +78,7 @@ def test_tree_argument_errors(kvq):
         return L.kvq_mla_tree_decode(C.byref(tree(kvq, **kw)), out, lse, ws, n, None, None)
     assert L.kvq_mla_tree_decode(None, FAKE, None, None, 0, None, None) == 1
     for bad in (dict(d_lat=256), dict(d_rope=32), dict(n_seq=-1), dict(n_seq=65536), dict(n_q=0), dict(n_q=65),
-                dict(n_heads=0), dict(n_heads=1 << 20), dict(n_heads=(1 << 31) - 1), dict(max_seq_len=-1), dict(impl=3),
+                dict(n_heads=0), dict(n_heads=1 << 20), dict(n_heads=(1 << 31) - 1), dict(max_seq_len=-1), dict(max_seq_len=(1 << 30) + 1), dict(impl=3),
                 dict(impl=-1), dict(sm_scale=float("nan")), dict(sm_scale=float("inf")), dict(ldq_lat=504),
                 dict(ldq_rope=56), dict(page_size=0), dict(max_pages=0), dict(block_table=None, seq_stride_rows=4000),
                 dict(impl=1, page_size=20), dict(seq_len=None), dict(q_lat=None), dict(q_rope=None),
@@ -169,6 +169,32 @@ def test_binding_refuses_wrong_tensors(kvq):
         kvq.kvq_append_mla(torch.zeros(4, 512), torch.zeros(4, 64).bfloat16(), i32(4), 1, None, planes)
     with pytest.raises(ValueError):
         kvq.kvq_append_mla(torch.zeros(4, 512), torch.zeros(4, 64), i32(3), 1, None, planes)
+
+
+def test_binding_refuses_tensors_of_several_devices(kvq, monkeypatch):
+    i32 = lambda *s, device="cpu": torch.zeros(*s, dtype=torch.int32, device=device)
+    args = dict(keep_len=i32(3), n_new=i32(3), block_table=i32(3, 4), n_held=i32(3), free_list=i32(9),
+                n_free=i32(1), page_size=16, seq_len=i32(3), tok_start=i32(4), slot_map=i32(8))
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1 if t.shape == (9,) else 0)
+    with pytest.raises(ValueError, match="different devices"):
+        kvq.make_page_plan(**args)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    p = kvq.make_page_plan(**args)
+    with pytest.raises(ValueError, match="current device"):
+        kvq.kvq_resize_pages(p)
+    planes = dict(lat=torch.zeros(8, 512, dtype=torch.uint8), lat_scale=torch.zeros(8),
+                  rope=torch.zeros(8, 64, dtype=torch.uint8), rope_scale=torch.zeros(8))
+    with pytest.raises(ValueError, match="current device"):
+        kvq.kvq_append_mla(torch.zeros(4, 512), torch.zeros(4, 64), i32(4), 1, None, planes)
+    d = kvq.make_accept(seq_len=i32(2), path=i32(2, 3), n_acc=i32(2), new_len=i32(2), fmt=1, cache=planes)
+    with pytest.raises(ValueError, match="current device"):
+        kvq.kvq_accept_mla(d)
+    q = torch.zeros(2, 3, 4, 576, dtype=torch.bfloat16)
+    t = kvq.make_tree_problem(seq_len=i32(2), q_lat=q[..., :512], q_rope=q[..., 512:], sm_scale=1.0, max_seq_len=8, fmt=1,
+                              cache=planes)
+    with pytest.raises(ValueError, match="current device"):
+        kvq.kvq_mla_tree_decode(t, torch.zeros(2, 3, 4, 512, dtype=torch.bfloat16), None, torch.zeros(4096, dtype=torch.uint8))
 
 
 def test_struct_layouts(kvq, tmp_path):

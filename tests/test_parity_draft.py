@@ -247,6 +247,25 @@ def test_append_extreme_magnitudes(kvq, orc, bf16):
         assert np.array_equal(planes[key].cpu().numpy().view(np.uint8), ref[key].view(np.uint8)), key
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_append_non_finite_rows_equal_encode_mla(kvq, bf16):
+    """fp8 rows that hold NaNs, infinities or subnormals: still the bytes of kvq_encode_mla."""
+    x = W.normal(np.random.default_rng(8), (40, 576)).astype(np.float32)
+    for r in range(30):
+        x[r, 17 * r % 512] = (np.nan, np.inf, -np.inf)[r % 3]
+        x[r, 512 + r] = (np.inf, np.nan, -np.nan)[r % 3]
+    x[5, :] = np.nan
+    x[33:36] *= np.float32(1e-39)
+    both = dev(x).bfloat16() if bf16 else dev(x)
+    wide = both.float()
+    a, b = empty_planes(1, 40), empty_planes(1, 40)
+    kvq.kvq_encode_mla(wide[:, :512].contiguous(), wide[:, 512:].contiguous(), 1, None, a["lat"], a["lat_scale"], a["rope"], a["rope_scale"])
+    kvq.kvq_append_mla(both[:, :512], both[:, 512:], torch.arange(40, dtype=torch.int32, device="cuda"), 1, None, b)
+    torch.cuda.synchronize()
+    for key in a:
+        assert torch.equal(a[key].view(torch.uint8), b[key].view(torch.uint8)), key
+
+
 def test_append_equals_encode_mla(kvq):
     """The bytes of kvq_encode_mla, at the identity and a reversed slot map; zero rows."""
     n = 600
@@ -606,6 +625,30 @@ def test_tree_strided_queries_stream_and_no_lse(kvq, orc, impl):
         side.synchronize()
         outs.append(out)
     assert torch.equal(outs[0], outs[1])
+
+
+@SIZES
+def test_tree_non_finite_queries(kvq, orc, impl, H):
+    """A query row with an infinity or a NaN gets NaN and leaves the others alone."""
+    T, n_q = 900, 4
+    signs = W.sign_bits(1)
+    cache = make_cache(orc, 1, T, 2, signs)
+    ql, qr = queries(1, n_q, H, 4)
+    bad = [(0, 0), (0, 5), (1, 3), (2, 18), (3, 7)]
+    for i, (j, h) in enumerate(bad):
+        (qr if i == 3 else ql)[0, j, h, 7 * i] = (float("inf"), float("nan"), float("-inf"))[i % 3]
+    out, lse, st = run_tree(kvq, fmt=1, cache=cache, signs=signs, lens=[T], n_node=[n_q], masks=None, q_lat=ql, q_rope=qr,
+                            stride=T, impl=impl)
+    where = torch.zeros(1, n_q, H, dtype=torch.bool)
+    for j, h in bad:
+        where[0, j, h] = True
+    ql[where.cuda()], qr[where.cuda()] = 0, 0
+    ref = tree_ref(orc, 1, cache, signs, contiguous([T], T), [T], [n_q], None, ql.float().cpu().numpy(),
+                   qr.float().cpu().numpy(), float(W.SM_SCALE))
+    where = where.numpy()
+    assert st == 0 and np.isnan(out[where]).all() and np.isnan(lse[where]).all()
+    out[where], lse[where] = ref[0][where], ref[1][where]
+    check_tree((out, lse, st), ref)
 
 
 @pytest.mark.parametrize("n_seq,H", [(1, 16), (3, 200)])
