@@ -346,7 +346,8 @@ __device__ __forceinline__ void digits2(float2 v, uint32_t& d0, uint32_t& d1)
 
 // One warp: query rows r0 + i, i = warp, warp + 16, .. (of the sequence's n * H; zero from `rows` on)
 // into rows i and NR + i of the Q image.  Lane: 16 latent dims, and (lane < 16) 4 rope dims.  sigma
-// puts the row's largest element in [128, 256).
+// puts the row's largest element in [128, 256); a NaN or an infinity in the row makes its gain, and so
+// its scores, NaN.
 template <int NR>
 __device__ __forceinline__ void write_queries(const Shared<NR>& sh, const kvq_mla_tree_problem& p, int s, int64_t r0,
                                               int64_t rows, int warp, int lane)
@@ -379,8 +380,7 @@ __device__ __forceinline__ void write_queries(const Shared<NR>& sh, const kvq_ml
         for (int e = 0; e < 10; ++e) m = __vmaxu2(m, w[n][e] & 0x7FFF7FFFu);
         m = max(m & 0xFFFFu, m >> 16);
         m = __reduce_max_sync(kFull, m);
-        const bool finite = m < 0x7F80u;             // else the row's scores are NaN
-        const int sigma = m != 0 && finite ? min(100, 7 - ((int)(m >> 7) - 127)) : 0;
+        const int sigma = m != 0 ? min(100, max(-120, 7 - ((int)(m >> 7) - 127))) : 0;
         const float scale = __int_as_float((127 + sigma) << 23);
         uint32_t d0[5], d1[5];
 #pragma unroll
@@ -401,7 +401,7 @@ __device__ __forceinline__ void write_queries(const Shared<NR>& sh, const kvq_ml
             *reinterpret_cast<uint32_t*>(rp + i * 64 + at) = d0[4];
             *reinterpret_cast<uint32_t*>(rp + (NR + i) * 64 + at) = d1[4];
         }
-        if (lane == 0) sh.gain()[i] = finite ? p.sm_scale * kLog2e * __int_as_float((127 - sigma) << 23) : NAN;
+        if (lane == 0) sh.gain()[i] = m < 0x7F80u ? p.sm_scale * kLog2e * __int_as_float((127 - sigma) << 23) : NAN;
     }
 }
 
@@ -490,11 +490,16 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 // The loaders and the issuers run on into the next unit while the softmax warps finish one.
 //
 // A tile of 128 x 64 costs the tensor core 2974 cycles (N = 128 69 cycles, N = 64 54 cycles each MMA
-// of K = 32, measured) and the loop takes 4250 to 4600: it is bound by the chain context MMAs ->
-// box free -> copy -> score MMAs -> softmax -> context MMAs through a ring that shared memory
-// limits to two stages.  Measured, whole calls with the combine: 4 trees of 16 nodes x 64 heads at
-// T = 16384 314 us = 929 TFLOP/s; one of 32 x 128 heads at T = 20000 205 us = 890; 32 ragged ones up
-// to T = 65536 2395 us = 1037 TFLOP/s.
+// of K = 32, measured) and the loop takes 4300 to 4900.  What bounds it is a tile's way through a
+// ring that shared memory limits to two stages: box free -> copy (about 2000 cycles) -> score MMAs
+// (1000 more) -> softmax (2600, 3400 when maxima move) -> context MMAs (2800 beside the next tile's
+// scores), which takes two tiles' time.  Tried and slower: the context in two halves of the rows, so
+// that the next weights need not wait but the boxes are free later (13%); holding back one of the two
+// products while the other runs (9 to 25%); the rope keys' slot freed by the score MMAs and copied
+// first (2 to 5%); copies of their own for scores and context (17%).
+// Measured, whole calls with the combine: 4 trees of 16 nodes x 64 heads at
+// T = 32768 315 us = 926 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 206 us = 885; 32 ragged
+// ones of up to 32 nodes and 65536 rows 2417 us = 1028 TFLOP/s.
 // ====================================================================================
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_constant__ Args a)
