@@ -454,12 +454,18 @@ def _one_device(*tensors):
     return d.pop()
 
 
-def _on_current(d):
-    """`d` (a device index, -1: the host) must be the current device, which the kernels run on."""
+def _stream_on(d, stream):
+    """The stream of a call whose tensors are on device `d` (-1: the host), which must be the current
+    device: the kernels run there."""
     if d >= 0:
         import torch
-        if d != torch.cuda.current_device():
-            raise ValueError(f"tensors on cuda:{d}, but the current device is cuda:{torch.cuda.current_device()}")
+        now = torch.cuda.current_device()
+        if d != now:
+            raise ValueError(f"tensors on cuda:{d}, but the current device is cuda:{now}")
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if stream is None and raw is not None:
+            return raw(d)
+    return _stream(stream)
 
 
 def make_page_plan(*, keep_len, n_new, block_table, n_held, free_list, n_free, page_size, seq_len,
@@ -486,20 +492,24 @@ def make_page_plan(*, keep_len, n_new, block_table, n_held, free_list, n_free, p
 
 
 def kvq_resize_pages(p: PagePlan, dev_status=None, stream=None) -> None:
-    _on_current(p._device)
-    _check(lib().kvq_resize_pages(C.byref(p), _ptr(dev_status), _stream(stream)))
+    _check(lib().kvq_resize_pages(C.byref(p), _ptr(dev_status), _stream_on(p._device, stream)))
 
 
 _LAT_BYTES = {FMT_FP8: 512, FMT_TQ4: 256, FMT_TQ6: 384, FMT_TQ3: 192}
 
 
 def _mla_planes(planes, fmt):
+    import torch
     lat, ls, rope, rs = planes["lat"], planes["lat_scale"], planes["rope"], planes["rope_scale"]
     n = lat.shape[0]
-    _want("lat", lat, "uint8", n, _LAT_BYTES.get(fmt))
-    _want("lat_scale", ls, "float32", n)
-    _want("rope", rope, "uint8", n, 64)
-    _want("rope_scale", rs, "float32", n)
+    one, u8, f32 = (n,), torch.uint8, torch.float32
+    if not (lat.dtype is u8 and rope.dtype is u8 and ls.dtype is f32 and rs.dtype is f32 and
+            lat.shape == (n, _LAT_BYTES.get(fmt)) and rope.shape == (n, 64) and ls.shape == one and rs.shape == one and
+            lat.is_contiguous() and rope.is_contiguous() and ls.is_contiguous() and rs.is_contiguous()):
+        _want("lat", lat, "uint8", n, _LAT_BYTES.get(fmt))            # (names the one at fault)
+        _want("lat_scale", ls, "float32", n)
+        _want("rope", rope, "uint8", n, 64)
+        _want("rope_scale", rs, "float32", n)
     return MlaCache(lat.data_ptr(), ls.data_ptr(), rope.data_ptr(), rs.data_ptr(), n)
 
 
@@ -520,10 +530,10 @@ def kvq_append_mla(c_lat, k_rope, slot_map, fmt, sign_bits, planes: dict, dev_st
         ldx, ldr = 512, 64
     _want("slot_map", slot_map, "int32", rows)
     c = _mla_planes(planes, fmt)
-    _on_current(_one_device(c_lat, k_rope, slot_map, sign_bits, planes["lat"], planes["lat_scale"], planes["rope"],
-                            planes["rope_scale"]))
+    stream = _stream_on(_one_device(c_lat, k_rope, slot_map, sign_bits, planes["lat"], planes["lat_scale"],
+                                    planes["rope"], planes["rope_scale"]), stream)
     _check(lib().kvq_append_mla(c_lat.data_ptr(), ldx, k_rope.data_ptr(), ldr, kind, rows, slot_map.data_ptr(),
-                                int(fmt), _ptr(sign_bits), C.byref(c), _ptr(dev_status), _stream(stream)))
+                                int(fmt), _ptr(sign_bits), C.byref(c), _ptr(dev_status), stream))
 
 
 def _row_stride(name, q, width):
@@ -581,10 +591,10 @@ def kvq_mla_tree_decode_kernel(p: TreeProblem) -> int:
 def kvq_mla_tree_decode(p: TreeProblem, out, lse=None, workspace=None, dev_status=None, stream=None) -> None:
     _want("out", out, "bfloat16", p.n_seq, p.n_q, p.n_heads, 512)
     _want("lse", lse, "float32", p.n_seq, p.n_q, p.n_heads)
-    _on_current(_one_device(out, lse, workspace, p._keep[0]))
+    stream = _stream_on(_one_device(out, lse, workspace, p._keep[0]), stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(lib().kvq_mla_tree_decode(C.byref(p), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
-                                     _ptr(dev_status), _stream(stream)))
+                                     _ptr(dev_status), stream))
 
 
 def make_accept(*, seq_len, path, n_acc, new_len, fmt, cache, n_node=None, block_table=None, page_size=0,
@@ -610,8 +620,7 @@ def make_accept(*, seq_len, path, n_acc, new_len, fmt, cache, n_node=None, block
 
 
 def kvq_accept_mla(d: AcceptDesc, dev_status=None, stream=None) -> None:
-    _on_current(d._device)
-    _check(lib().kvq_accept_mla(C.byref(d), _ptr(dev_status), _stream(stream)))
+    _check(lib().kvq_accept_mla(C.byref(d), _ptr(dev_status), _stream_on(d._device, stream)))
 
 
 # --- cache files ------------------------------------------------------------------------

@@ -27,6 +27,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kLd = kDLat + kDRope + 4;      // floats of a staged row
+constexpr int kStage = 2 * kWarps;           // drafted rows in shared memory at a time
 
 __constant__ float c_cb4[16] = {
     kTq4Centroids[0], kTq4Centroids[1], kTq4Centroids[2], kTq4Centroids[3],
@@ -48,7 +49,8 @@ struct TreeArgs {
     uint32_t* status;
 };
 
-// fp32 copies of the queries (padding reads as 0) and the prefix lengths
+// fp32 copies of the queries (padding reads as 0), which kvq_mla_decode takes, and the prefix lengths:
+// a warp a row, 16-byte loads; bound by HBM, 1152 bytes read and 2304 written a row
 __global__ void __launch_bounds__(kThreads) tree_prepare_kernel(const TreeArgs a)
 {
     const kvq_mla_tree_problem& p = a.p;
@@ -61,16 +63,24 @@ __global__ void __launch_bounds__(kThreads) tree_prepare_kernel(const TreeArgs a
         a.prefix[s] = sh.x - sh.y;
     }
     for (int64_t r = warp; r < rows; r += n_warps) {
+        // (the loads do not wait for the lengths)
+        const uint4* ql = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q_lat) + r * p.ldq_lat);
+        const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q_rope) + r * p.ldq_rope);
+        const uint4 x[2] = {ql[lane], ql[32 + lane]};
+        const uint32_t y = qr[lane];
         const int64_t node = r / p.n_heads;
         const bool live = (int)(node % p.n_q) < tree_seq_shape(p, (int)(node / p.n_q)).y;
-        const __nv_bfloat16* ql = static_cast<const __nv_bfloat16*>(p.q_lat) + r * p.ldq_lat;
-        const __nv_bfloat16* qr = static_cast<const __nv_bfloat16*>(p.q_rope) + r * p.ldq_rope;
+        auto wide = [&](uint32_t w) {
+            return live ? make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)) : make_float2(0.0f, 0.0f);
+        };
 #pragma unroll
-        for (int k = 0; k < kDLat / 32; ++k)
-            a.q_lat[r * kDLat + k * 32 + lane] = live ? __bfloat162float(ql[k * 32 + lane]) : 0.0f;
-#pragma unroll
-        for (int k = 0; k < kDRope / 32; ++k)
-            a.q_rope[r * kDRope + k * 32 + lane] = live ? __bfloat162float(qr[k * 32 + lane]) : 0.0f;
+        for (int k = 0; k < 2; ++k) {
+            const float2 a0 = wide(x[k].x), a1 = wide(x[k].y), a2 = wide(x[k].z), a3 = wide(x[k].w);
+            float4* dst = reinterpret_cast<float4*>(a.q_lat + r * kDLat) + 64 * k + 2 * lane;
+            dst[0] = make_float4(a0.x, a0.y, a1.x, a1.y);
+            dst[1] = make_float4(a2.x, a2.y, a3.x, a3.y);
+        }
+        reinterpret_cast<float2*>(a.q_rope + r * kDRope)[lane] = wide(y);
     }
 }
 
@@ -116,14 +126,17 @@ __device__ void stage_row(const kvq_mla_tree_problem& p, int64_t row, const floa
 
 // ------------------------------------------------------------------------------------
 // The drafted rows, and the join: CTA = eight (node, head) rows of one sequence, a warp each;
-// the drafted rows pass through shared memory eight at a time, one dequantised by each warp.
+// the drafted rows pass through shared memory sixteen at a time, two dequantised by each warp.
 // At most 64 rows a sequence.  Launched to start during the prefix's combine: only the join needs
-// its results (nine nodes of 20 heads at T = 8190, TQ4, two sequences: 62.8 -> 60.1 us a call).
+// its results.  Bound by latency: chains of dependent loads and 64 shuffled dot products a warp, so
+// the loads of sixteen rows are in flight together, beside the query's (nine nodes of 20 heads, TQ4,
+// two sequences of about 4100 rows: 56.6 us a call, of which the prefix's kvq_mla_decode 44.5; waiting
+// for the combine at the start 62.8, eight rows at a time and the queries' copies by 2-byte loads 60.1).
 // ------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kThreads) tree_tail_kernel(const TreeArgs a)
 {
-    __shared__ __align__(16) float s_row[kWarps][kLd];
-    __shared__ int s_ok[kWarps];
+    __shared__ __align__(16) float s_row[kStage][kLd];
+    __shared__ int s_ok[kStage];
     __shared__ float s_cb[64];
     const kvq_mla_tree_problem& p = a.p;
     const int s = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -166,25 +179,30 @@ __global__ void __launch_bounds__(kThreads) tree_tail_kernel(const TreeArgs a)
     float m = -INFINITY, l = 0.0f, o[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) o[k] = 0.0f;
-    for (int k0 = 0; k0 < n; k0 += kWarps) {
+    for (int k0 = 0; k0 < n; k0 += kStage) {
         __syncthreads();
-        const int t = L - n + k0 + warp;
-        int64_t row = -1;
-        if (k0 + warp < n) {
+        int64_t row[2] = {-1, -1};
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int e = k0 + kWarps * i + warp, t = L - n + e;
+            if (e >= n) continue;
             if (!p.block_table) {
-                row = (int64_t)s * p.seq_stride_rows + t;
+                row[i] = (int64_t)s * p.seq_stride_rows + t;
             } else {
                 const int pg = t / p.page_size;
                 const int pid = pg < p.max_pages ? p.block_table[(int64_t)s * p.max_pages + pg] : -1;
-                row = pid < 0 ? -1 : (int64_t)pid * p.page_size + t % p.page_size;
+                row[i] = pid < 0 ? -1 : (int64_t)pid * p.page_size + t % p.page_size;
             }
-            if (row >= p.cache.n_rows) row = -1;
-            if (row < 0 && lane == 0 && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_PAGE);
+            if (row[i] >= p.cache.n_rows) row[i] = -1;
+            if (row[i] < 0 && lane == 0 && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_PAGE);
         }
-        if (row >= 0) stage_row(p, row, s_cb, s_row[warp]);
-        if (lane == 0) s_ok[warp] = row >= 0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            if (row[i] >= 0) stage_row(p, row[i], s_cb, s_row[kWarps * i + warp]);
+            if (lane == 0) s_ok[kWarps * i + warp] = row[i] >= 0;
+        }
         __syncthreads();
-        for (int e = 0; e < kWarps && k0 + e < n; ++e) {
+        for (int e = 0; e < kStage && k0 + e < n; ++e) {
             if (!((see >> (k0 + e)) & 1u) || !s_ok[e]) continue;         // (the same in every lane)
             const float* x = s_row[e];
             saw = true;
@@ -202,13 +220,13 @@ __global__ void __launch_bounds__(kThreads) tree_tail_kernel(const TreeArgs a)
             for (int k = 0; k < 16; ++k) o[k] = fmaf(o[k], keep, w * x[k * 32 + lane]);
         }
     }
-    grid_dependency_wait();                       // the prefix's combine, launched just before
-    if (!there) return;
     if (rot) {
         fwht_warp<16>(o, lane);
 #pragma unroll
         for (int k = 0; k < 16; ++k) o[k] *= ((neg >> k) & 1u) ? -tq4_inv_sqrt(kDLat) : tq4_inv_sqrt(kDLat);
     }
+    grid_dependency_wait();                       // the prefix's combine, launched just before
+    if (!there) return;
     float lse0 = live ? a.pre_lse[r] : -INFINITY;
     if (bad && (saw || lse0 != -INFINITY)) lse0 = NAN;
     const float M = fmaxf(lse0, m);
