@@ -175,7 +175,6 @@ __device__ __forceinline__ bool wait_bar(const Shared<NR>& sh, uint64_t* bar, ui
         if (*sh.abort_flag()) return false;
         if (globaltimer_ns() - t0 > a.wait_ns) {
             *sh.abort_flag() = 1;
-            if (a.status) atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
             return false;
         }
     }
@@ -488,6 +487,8 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 //    the rope key, 19 the other two).
 //  * Warp 17: tensor memory, score MMAs; warp 18: context MMAs.
 // The loaders and the issuers run on into the next unit while the softmax warps finish one.
+// The loops of the roles run side by side, so their code shares the instruction cache: loops over the
+// boxes, and a status set once at the end, took the calls below from 315, 206 and 2418 us to these.
 //
 // A tile of 128 x 64 costs the tensor core 2974 cycles (N = 128 69 cycles, N = 64 54 cycles each MMA
 // of K = 32, measured) and the loop takes 4300 to 4900.  What bounds it is a tile's way through a
@@ -498,8 +499,8 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 // products while the other runs (9 to 25%); the rope keys' slot freed by the score MMAs and copied
 // first (2 to 5%); copies of their own for scores and context (17%).
 // Measured, whole calls with the combine: 4 trees of 16 nodes x 64 heads at
-// T = 32768 315 us = 926 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 206 us = 885; 32 ragged
-// ones of up to 32 nodes and 65536 rows 2417 us = 1028 TFLOP/s.
+// T = 32768 284 us = 1029 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 187 us = 977; 32 ragged
+// ones of up to 32 nodes and 65536 rows 2228 us = 1069 TFLOP/s (17.1 M pairs of node and row, 64 heads).
 // ====================================================================================
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_constant__ Args a)
@@ -713,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                                 int node = (int)((r0 + hb) / p.n_heads), head = (int)((r0 + hb) % p.n_heads);
                                 uint64_t see = node < n ? tree_visible(p, s, node, n) : 0;
                                 vis = 0;
+#pragma unroll 1
                                 for (int e = 0; e < GR; ++e) {
                                     vis |= (uint32_t)((see >> kk) & 1u) << e;
                                     if (++head == p.n_heads) {
@@ -930,10 +932,10 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 const int64_t r = t < k.L ? tree_pool_row(p, k.s, t) : -1;
                 sh.copy_rows(2 * who + buf)[lane] = r < 0 || r >= p.cache.n_rows ? -1 : (int)r;
             };
-            look_up(k.tile, c & 1);
-            __syncwarp();
-            for (int i = k.tile; i < k.end && ok; ++i, ++c) {
-                if (leader) {
+            // (one tile ahead, from the tile before the first: one copy of the code)
+#pragma unroll 1
+            for (int i = k.tile - 1; i < k.end && ok; ++i) {
+                if (leader && i >= k.tile) {
                     const int st = c & 1;
                     volatile int* y = sh.copy_rows(2 * who + st);
                     uint32_t n_in = 0;                // rows that come
@@ -959,7 +961,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                         done[b < 4 ? b & 1 : 2] = c + 1;
                     }
                 }
-                if (i + 1 < k.end) look_up(i + 1, (c + 1) & 1);
+                if (i >= k.tile) ++c;
+                if (i + 1 < k.end) look_up(i + 1, c & 1);
                 ok = __any_sync(kFull, leader && ok);
             }
         }
@@ -990,30 +993,30 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 const int ruse = C::kRS == 2 ? c >> 1 : c;
                 // S(c) overwrites S(c - 1): the softmax has read it
                 if (c > 0) ok = wait_bar<kRoleSpin>(sh, sh.s_empty(), (uint32_t)(c - 1) & 1u, a);
-#pragma unroll
-                for (int b = 0; b < kBoxes; ++b) {
-                    ok = ok && wait_bar<kRoleSpin>(sh, sh.full(b < 4 ? st : rst, b), (uint32_t)(b < 4 ? c >> 1 : ruse) & 1u, a);
+#pragma unroll 1
+                for (int b = 0; b < 4; ++b) {
+                    ok = ok && wait_bar<kRoleSpin>(sh, sh.full(st, b), (uint32_t)(c >> 1) & 1u, a);
                     if (!ok) break;
                     tc_fence_after();
-                    if (b < 4) {
-                        const uint32_t box = smem_u32(sh.box(st, b));
+                    const uint32_t box = smem_u32(sh.box(st, b)), q_at = q_addr + b * C::kQBlk;
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks) {
-                            const uint64_t ad = desc_smem(box + ks * 32, 16, 1024, kSwizzle128);
-                            const uint64_t bd = desc_smem(q_addr + b * C::kQBlk + ks * 32, 16, 1024, kSwizzle128);
-                            mma_e4m3_ss(tmem + C::kColSL, ad, bd, idesc, (b | ks) ? 1u : 0u);
-                        }
-                    } else {
-                        const uint32_t box = smem_u32(sh.rope(rst));
-#pragma unroll
-                        for (int ks = 0; ks < 2; ++ks) {
-                            const uint64_t ad = desc_smem(box + ks * 32, 16, 512, kSwizzle64);
-                            const uint64_t bd = desc_smem(q_addr + C::kQRope + ks * 32, 16, 512, kSwizzle64);
-                            mma_e4m3_ss(tmem + C::kColSR, ad, bd, idesc, ks > 0 ? 1u : 0u);
-                        }
-                        mma_commit(sh.s_full());
+                    for (int ks = 0; ks < 4; ++ks) {
+                        const uint64_t ad = desc_smem(box + ks * 32, 16, 1024, kSwizzle128);
+                        const uint64_t bd = desc_smem(q_at + ks * 32, 16, 1024, kSwizzle128);
+                        mma_e4m3_ss(tmem + C::kColSL, ad, bd, idesc, (b | ks) ? 1u : 0u);
                     }
                 }
+                ok = ok && wait_bar<kRoleSpin>(sh, sh.full(rst, 4), (uint32_t)ruse & 1u, a);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t box = smem_u32(sh.rope(rst));
+#pragma unroll
+                for (int ks = 0; ks < 2; ++ks) {
+                    const uint64_t ad = desc_smem(box + ks * 32, 16, 512, kSwizzle64);
+                    const uint64_t bd = desc_smem(q_addr + C::kQRope + ks * 32, 16, 512, kSwizzle64);
+                    mma_e4m3_ss(tmem + C::kColSR, ad, bd, idesc, ks > 0 ? 1u : 0u);
+                }
+                mma_commit(sh.s_full());
             }
         }
         if (leader) {
@@ -1052,7 +1055,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 if (!ok) break;
                 tc_fence_after();
                 const int st = c & 1;
-#pragma unroll
+#pragma unroll 1
                 for (int m = 0; m < 4; ++m) {
                     const uint32_t box = smem_u32(sh.box(st, m));
 #pragma unroll
@@ -1079,6 +1082,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
 
     tc_fence_before();
     __syncthreads();
+    if (tid == 0 && *sh.abort_flag() && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_TIMEOUT);
     if (warp == kWarpS) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
