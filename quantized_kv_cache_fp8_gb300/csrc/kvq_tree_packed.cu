@@ -499,8 +499,8 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 // products while the other runs (9 to 25%); the rope keys' slot freed by the score MMAs and copied
 // first (2 to 5%); copies of their own for scores and context (17%).
 // Measured, whole calls with the combine: 4 trees of 16 nodes x 64 heads at
-// T = 32768 284 us = 1029 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 187 us = 977; 32 ragged
-// ones of up to 32 nodes and 65536 rows 2228 us = 1069 TFLOP/s (17.1 M pairs of node and row, 64 heads).
+// T = 32768 282 us = 1035 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 186 us = 982; 32 ragged
+// ones of up to 32 nodes and 65536 rows 2213 us = 1076 TFLOP/s (17.1 M pairs of node and row, 64 heads).
 // ====================================================================================
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_constant__ Args a)
@@ -939,6 +939,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                     const int st = c & 1;
                     volatile int* y = sh.copy_rows(2 * who + st);
                     uint32_t n_in = 0;                // rows that come
+#pragma unroll 2
                     for (int h = 0; h < per; ++h) n_in += y[h] >= 0 ? a.box_rows : 0;
 #pragma unroll
                     for (int b = 0; b < kBoxes; ++b) {
@@ -951,6 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                         const int width = b < 4 ? 128 : 64;
                         uint8_t* dst = b < 4 ? sh.box(st, b) : sh.rope(slot);
                         mbar_arrive_expect_tx(bar, n_in * width);
+#pragma unroll 2
                         for (int h = 0; h < per; ++h) {
                             const int yh = y[h];
                             if (yh >= 0) {
