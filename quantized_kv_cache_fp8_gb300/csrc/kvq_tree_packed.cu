@@ -1180,14 +1180,16 @@ __global__ void __launch_bounds__(kCombThreads) tree_combine_kernel(const __grid
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
-// 64 query rows a tile feed the tensor core best.  Up to 32 rows, and problems of at most two such
-// tiles an SM, run in half tiles: more SMs share the work, and the softmax, query image and epilogue
-// of each are half as long (64 rows: T = 1024 20.6 -> 16.5 us, T = 32768 45 -> 31 us; at T = 131072,
-// seven tiles an SM, both take 53 us, and with more the full tiles win).
+// 64 query rows a tile feed the tensor core best.  Up to 32 rows, and problems of few such tiles an
+// SM, run in half tiles: more SMs share the work, the softmax, query image and epilogue of each are
+// half as long, and so are the partials, which cost the more the fewer units the SMs share (us in
+// half and full tiles: one unit of 64 rows, 256 tiles 25.4 / 37.1, 512 31.3 / 40.2, 768 39.6 / 38.3;
+// two units, 512 tiles 29.8 / 29.9, 1024 43.6 / 37.5; 16 units, 256 32.9 / 33.5, 512 39.2 / 36.8).
 int tile_rows(const kvq_mla_tree_problem& p)
 {
     const int64_t rows = (int64_t)p.n_q * p.n_heads, tiles = ((int64_t)p.max_seq_len + kRT - 1) / kRT;
-    return rows <= 32 || p.n_seq * ((rows + 63) / 64) * tiles <= 2 * sm_count() ? 32 : 64;
+    const int64_t units = std::max<int64_t>(1, p.n_seq * ((rows + 63) / 64));
+    return rows <= 32 || units * tiles <= 2 * sm_count() * (units + 1) / units ? 32 : 64;
 }
 
 int64_t max_units(const kvq_mla_tree_problem& p)
