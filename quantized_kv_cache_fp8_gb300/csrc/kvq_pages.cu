@@ -56,7 +56,7 @@ __device__ __forceinline__ Seq load_seq(const kvq_page_plan& p, int s)
 }
 
 // the checks that need no other sequence; `tok_end` = the packed end of its tokens
-__device__ __forceinline__ void judge_seq(const kvq_page_plan& p, Seq& q, int64_t tok_end, unsigned& bits)
+__device__ __forceinline__ void screen_seq(const kvq_page_plan& p, Seq& q, int64_t tok_end, unsigned& bits)
 {
     const int64_t len = (int64_t)q.keep + q.add;
     const uint32_t need = ((uint32_t)len + (uint32_t)p.page_size - 1u) / (uint32_t)p.page_size;   // (if len fits)
@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeA
         tok += sum;
         int64_t v = 0;
         if (live) {
-            judge_seq(p, q, packed_end(end), bits);
+            screen_seq(p, q, packed_end(end), bits);
             p.tok_start[s + 1] = (int)min(end, (int64_t)INT32_MAX);
             v = ((int64_t)max(q.held - q.need, 0) << 32) + max(q.need - q.held, 0);
         }
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kMaxThreads) resize_pages_kernel(const ResizeA
         int64_t v = 0;
         if (s < p.n_seq) {
             q = load_seq(p, s);
-            judge_seq(p, q, packed_end(p.tok_start[s + 1]), ignore);
+            screen_seq(p, q, packed_end(p.tok_start[s + 1]), ignore);
             v = ((int64_t)max(q.held - q.need, 0) << 32) + max(q.need - q.held, 0);
         }
         both = block_scan(v, s_warp[c / T & 3], &sum);

@@ -123,7 +123,7 @@ class Pages:
 
 
 @pytest.mark.parametrize("n_seq,page,grow,tokens", [(1, 64, 1, 1), (1, 8, 5000, 5003), (7, 16, 40, 280), (300, 64, 30, 9000),
-                                                   (1024, 1, 3, 3072), (1500, 48, 100, 150000), (2600, 16, 9, 4096),
+                                                   (1024, 1, 3, 3100), (1500, 48, 100, 150000), (2600, 16, 9, 4096),
                                                    (3000, 100, 2, 6000)])
 def test_resize_grow_shrink_refuse(kvq, n_seq, page, grow, tokens):
     """A run of steps: admission, growth, roll-back, ends of sequences, an empty list."""
