@@ -120,6 +120,7 @@ struct Args {
     int box_rows;                            // rows a box brings: 128, or what divides the page
     int by_unit;                             // infos are indexed by unit, else by CTA
     int n_rt;                                // row tiles a sequence at most
+    int page_shift;                          // log2 of the page size, -1 if it is no power of two
     float* part_ml;                          // [2 CTAs][NR][2]
     float* part_o;                           // [2 CTAs][NR][512]
     SplitInfo* info;
@@ -244,13 +245,15 @@ __device__ __forceinline__ float max3(float a, float b, float c)
     return r;
 }
 
-__device__ __forceinline__ int64_t tree_pool_row(const kvq_mla_tree_problem& p, int s, int t)
+// `shift`: log2 of the page size, -1 if it is no power of two (every softmax thread does this for each of
+// its rows, where a division shows: four trees below, pages of 64: 281 us with it, 273 without)
+__device__ __forceinline__ int64_t tree_pool_row(const kvq_mla_tree_problem& p, int s, int t, int shift)
 {
     if (!p.block_table) return (int64_t)s * p.seq_stride_rows + t;
-    const int page = t / p.page_size;
+    const int page = shift >= 0 ? t >> shift : t / p.page_size;
     if (page >= p.max_pages) return -1;
     const int pid = p.block_table[(int64_t)s * p.max_pages + page];
-    return pid < 0 ? -1 : (int64_t)pid * p.page_size + t % p.page_size;
+    return pid < 0 ? -1 : (int64_t)pid * p.page_size + (t - page * p.page_size);
 }
 
 // ---- the line of tiles --------------------------------------------------------------------
@@ -488,7 +491,8 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 //  * Warp 17: tensor memory, score MMAs; warp 18: context MMAs.
 // The loaders and the issuers run on into the next unit while the softmax warps finish one.
 // The loops of the roles run side by side, so their code shares the instruction cache: loops over the
-// boxes, and a status set once at the end, took the calls below from 315, 206 and 2418 us to these.
+// boxes, and a status set once at the end, took the calls below from 315, 206 and 2418 us to 282, 186
+// and 2213.
 //
 // A tile of 128 x 64 costs the tensor core 2974 cycles (N = 128 69 cycles, N = 64 54 cycles each MMA
 // of K = 32, measured) and the loop takes 4300 to 4900.  What bounds it is a tile's way through a
@@ -499,8 +503,8 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 // products while the other runs (9 to 25%); the rope keys' slot freed by the score MMAs and copied
 // first (2 to 5%); copies of their own for scores and context (17%).
 // Measured, whole calls with the combine: 4 trees of 16 nodes x 64 heads at
-// T = 32768 282 us = 1035 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 186 us = 982; 32 ragged
-// ones of up to 32 nodes and 65536 rows 2213 us = 1076 TFLOP/s (17.1 M pairs of node and row, 64 heads).
+// T = 32768 273 us = 1070 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 181 us = 1009; 32 ragged
+// ones of up to 32 nodes and 65536 rows 2170 us = 1097 TFLOP/s (17.1 M pairs of node and row, 64 heads).
 // ====================================================================================
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_constant__ Args a)
@@ -637,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
             bool mine_fresh = true;                   // lane < GR: row hb + lane has none
             auto pool_row = [&](int tl) -> int64_t {
                 if (tl >= L) return -1;
-                const int64_t r = tree_pool_row(p, s, tl);
+                const int64_t r = tree_pool_row(p, s, tl, a.page_shift);
                 if (r < 0 || r >= p.cache.n_rows) {
                     if (hp == 0 && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_PAGE);
                     return -1;
@@ -652,7 +656,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 const int st = c & 1, rst = C::kRS == 2 ? st : 0;
                 const bool have = row_n >= 0;
                 const float ls = ls_n, rs = rs_n;
-                const float lg = ls >= tiny ? fminf(log2f(ls), 200.0f) : -kTiny;
+                const float lg = ls >= tiny ? fminf(__log2f(ls), 200.0f) : -kTiny;
                 const bool zero_row = !(have && ls >= tiny);
                 if (i + 1 < k.end) {
                     row_n = pool_row((i + 1) * kRT + t);
@@ -929,7 +933,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
             auto look_up = [&](int i, int buf) {      // the pool row where copy `lane` of tile i begins
                 const int t = i * kRT + lane * a.box_rows;
                 if (lane >= per) return;
-                const int64_t r = t < k.L ? tree_pool_row(p, k.s, t) : -1;
+                const int64_t r = t < k.L ? tree_pool_row(p, k.s, t, a.page_shift) : -1;
                 sh.copy_rows(2 * who + buf)[lane] = r < 0 || r >= p.cache.n_rows ? -1 : (int)r;
             };
             // (one tile ahead, from the tile before the first: one copy of the code)
@@ -1266,6 +1270,9 @@ cudaError_t launch_tree_packed(const kvq_mla_tree_problem& p, void* out, float* 
                                !make_code_map(&a.tm_rope, p.cache.rope, p.cache.n_rows, kDRope, 64, a.box_rows)))
         return cudaErrorInvalidValue;
     a.p = p;
+    a.page_shift = -1;
+    for (int k = 0; k < 31; ++k)
+        if (p.block_table && p.page_size == 1 << k) a.page_shift = k;
     char* base = static_cast<char*>(ws);
     a.part_ml = reinterpret_cast<float*>(base + t.off_ml);
     a.part_o = reinterpret_cast<float*>(base + t.off_o);
