@@ -258,16 +258,19 @@ __device__ __forceinline__ int64_t tree_pool_row(const kvq_mla_tree_problem& p, 
 
 // ---- the line of tiles --------------------------------------------------------------------
 // A unit takes kUnitCost places on the line before its tiles: what a CTA pays to begin another unit
-// (query image, refill of the pipeline, epilogue: about four tiles' time).  Every stretch begins
-// one anyway, so these places even out the stretches with several units.
-constexpr int kUnitCost = 4;
+// (epilogue, query image, refill of the pipeline: 25 thousand cycles of a full tile's 4300).  Every
+// stretch begins one anyway, so these places even out the stretches with several units.  Full tiles
+// with 4, 5, 6, 7 places: the ragged batch below 2182, 2127, 2100, 2084 us, 32 units of 32 tiles 44.4, 44.6,
+// 44.4, 46.9; half tiles, two units of 256: 25.0, 24.9, 28.6, 26.8.
+template <int NR>
+constexpr int kUnitCost = NR == 64 ? 6 : 4;
 
 template <int NR>
 __device__ __forceinline__ int64_t seq_places(const kvq_mla_tree_problem& p, int s)
 {
     const int2 sh = tree_seq_shape(p, s);
     const int nt = (sh.x + kRT - 1) / kRT;
-    return nt == 0 ? 0 : (int64_t)(nt + kUnitCost) * (((int64_t)sh.y * p.n_heads + NR - 1) / NR);
+    return nt == 0 ? 0 : (int64_t)(nt + kUnitCost<NR>) * (((int64_t)sh.y * p.n_heads + NR - 1) / NR);
 }
 
 // where the stretch of CTA g of G begins on a line of `total` places
@@ -287,11 +290,11 @@ struct Walk {
         nt = (L + kRT - 1) / kRT;
         n_rt = (int)(((int64_t)n * p.n_heads + NR - 1) / NR);
     }
-    __device__ __forceinline__ int places() const { return min(nt + kUnitCost - at, left); }
+    __device__ __forceinline__ int places() const { return min(nt + kUnitCost<NR> - at, left); }
     __device__ __forceinline__ void tiles()
     {
-        tile = max(at - kUnitCost, 0);
-        end = max(at + places() - kUnitCost, 0);
+        tile = max(at - kUnitCost<NR>, 0);
+        end = max(at + places() - kUnitCost<NR>, 0);
     }
     __device__ __forceinline__ void step(const kvq_mla_tree_problem& p)
     {
@@ -317,18 +320,18 @@ struct Walk {
         if (left <= 0) return;
         shape(p);
         if (off <= INT32_MAX) {                           // (a 64-bit division takes microseconds)
-            rt = (int)off / (nt + kUnitCost);
-            at = (int)off % (nt + kUnitCost);
+            rt = (int)off / (nt + kUnitCost<NR>);
+            at = (int)off % (nt + kUnitCost<NR>);
         } else {
-            rt = (int)(off / (nt + kUnitCost));
-            at = (int)(off % (nt + kUnitCost));
+            rt = (int)(off / (nt + kUnitCost<NR>));
+            at = (int)(off % (nt + kUnitCost<NR>));
         }
         tiles();
         if (tile == end) next(p);
     }
     __device__ __forceinline__ bool more() const { return left > 0; }
     // the place behind this unit's last one, of a stretch that ends at `stretch_end`
-    __device__ __forceinline__ int64_t unit_end(int64_t stretch_end) const { return stretch_end - left - at + nt + kUnitCost; }
+    __device__ __forceinline__ int64_t unit_end(int64_t stretch_end) const { return stretch_end - left - at + nt + kUnitCost<NR>; }
 };
 
 // ---- digits and queries -------------------------------------------------------------------
@@ -495,7 +498,7 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 // and 2213.
 //
 // A tile of 128 x 64 costs the tensor core 2974 cycles (N = 128 69 cycles, N = 64 54 cycles each MMA
-// of K = 32, measured) and the loop takes 4300 to 4900.  What bounds it is a tile's way through a
+// of K = 32, measured) and the loop takes 4100 to 4500.  What bounds it is a tile's way through a
 // ring that shared memory limits to two stages: box free -> copy (about 2000 cycles) -> score MMAs
 // (1000 more) -> softmax (2600, 3400 when maxima move) -> context MMAs (2800 beside the next tile's
 // scores), which takes two tiles' time.  Tried and slower: the context in two halves of the rows, so
@@ -503,8 +506,8 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 // products while the other runs (9 to 25%); the rope keys' slot freed by the score MMAs and copied
 // first (2 to 5%); copies of their own for scores and context (17%).
 // Measured, whole calls with the combine: 4 trees of 16 nodes x 64 heads at
-// T = 32768 273 us = 1070 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 181 us = 1009; 32 ragged
-// ones of up to 32 nodes and 65536 rows 2170 us = 1097 TFLOP/s (17.1 M pairs of node and row, 64 heads).
+// T = 32768 268 us = 1090 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 178 us = 1025; 32 ragged
+// ones of up to 32 nodes and 65536 rows 2100 us = 1133 TFLOP/s (17.1 M pairs of node and row, 64 heads).
 // ====================================================================================
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_constant__ Args a)
@@ -1252,7 +1255,7 @@ cudaError_t launch_packed_as(Args& a, const PackedPlan& t, cudaStream_t s)
 bool tree_packed_reads(const kvq_mla_tree_problem& p)
 {
     // (a stretch of the line counts its places in an int)
-    const double places = (double)p.n_seq * ((double)p.n_q * p.n_heads / 32 + 1) * ((double)p.max_seq_len / kRT + 1 + kUnitCost);
+    const double places = (double)p.n_seq * ((double)p.n_q * p.n_heads / 32 + 1) * ((double)p.max_seq_len / kRT + 1 + kUnitCost<64>);
     return p.cache.n_rows <= INT32_MAX && (!p.block_table || p.page_size % 8 == 0) && places < 0x1p36;
 }
 
