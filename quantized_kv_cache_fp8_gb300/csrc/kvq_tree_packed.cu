@@ -781,7 +781,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                         sh.factor()[hb + lane] = up && !mine_fresh ? ex2(-by) : 1.0f;
                         mine_fresh = mine_fresh && !up;
                     }
-                    moved = __any_sync(kFull, up) && i > k.tile;      // (also orders the stores)
+                    __syncwarp();                     // (every lane reads what these lanes stored; a vote orders no memory)
+                    moved = __any_sync(kFull, up) && i > k.tile;
                     fresh = __any_sync(kFull, lane < GR && mine_fresh);
 #pragma unroll
                     for (int e = 0; e < GR; e += 4) {
@@ -972,6 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 }
                 if (i >= k.tile) ++c;
                 if (i + 1 < k.end) look_up(i + 1, c & 1);
+                __syncwarp();                         // (the leader reads the rows that the lanes stored)
                 ok = __any_sync(kFull, leader && ok);
             }
         }

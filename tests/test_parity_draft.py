@@ -681,6 +681,36 @@ def test_tree_waits_give_up_then_recover(kvq, orc, n_seq, H):
     check_tree(got, ref)
 
 
+@pytest.mark.parametrize("H", [20, 640])
+def test_tree_moving_maxima_and_small_pages_repeat(kvq, orc, H):
+    """Scores that rise tile after tile, so that the running maxima move in each, over pages of 8 rows, whose
+    addresses the lanes of a warp look up for the thread that issues the copies: the formula's values,
+    and the same bits at every call."""
+    T, n_q, page = 2600, 4, 8
+    g = np.random.default_rng(13)
+    signs = W.sign_bits(1)
+    data = W.unit_rows(T, seed=2)
+    data.c *= np.linspace(0.1, 20.0, T, dtype=np.float32)[:, None]
+    table, rows, rows_of = paged([T], page, g)
+    r, _ = rows_of(0)
+    enc = encode_ref(orc, 1, data.c, data.k_rope, signs)
+    cache = {k: np.zeros((rows,) + v.shape[1:], v.dtype) for k, v in enc.items()}
+    for k, v in enc.items():
+        cache[k][r] = v
+    masks = masks_of(g, [n_q], n_q, "tree")
+    ql, qr = queries(1, n_q, H, 9)
+    kw = dict(fmt=1, cache={k: dev(v) for k, v in cache.items()}, signs=signs, lens=[T], n_node=[n_q], masks=masks,
+              q_lat=ql, q_rope=qr, table=table, page=page, impl=1)
+    got = run_tree(kvq, **kw)
+    ref = tree_ref(orc, 1, cache, signs, rows_of, [T], [n_q], masks, ql.float().cpu().numpy(), qr.float().cpu().numpy(),
+                   float(W.SM_SCALE))
+    assert got[2] == 0
+    check_tree(got, ref)
+    for _ in range(10):
+        again = run_tree(kvq, **kw)
+        assert np.array_equal(again[0], got[0]) and np.array_equal(again[1], got[1])
+
+
 def test_tree_two_calls_at_once(kvq, orc):
     """Calls on two streams with their own workspaces do not touch one another."""
     T, n_q, H = 3000, 8, 64
