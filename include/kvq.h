@@ -500,8 +500,12 @@ int kvq_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t l
  * A node with nothing to see, and every node j >= n (padding), gets out = 0 and lse = -inf;
  * the q rows of padding are not used.  A page that is missing or outside the pool sets
  * KVQ_DEV_BAD_PAGE and its rows are skipped.  The rows of a page past L may hold anything.
- * Queries and outputs are bfloat16; scores, softmax and sums are fp32, and so is lse.  A query row
- * that holds a NaN or an infinity gets NaN (if it sees anything), and touches no other row.
+ * Queries and outputs are bfloat16; scores, the softmax's maximum and normalizer, the sums over rows and
+ * lse are fp32.  In the packed form (below) a weight that multiplies a row keeps 8 bits (within
+ * 2^-8 of itself) down to 2^-14 of its query row's largest; smaller ones are within 2^-19 of the
+ * largest, rounded up or down by their row's position so that the errors of many cancel (their sum
+ * is that of exact weights down to 2^-31 of the largest).  A query row that holds a NaN or an
+ * infinity gets NaN (if it sees anything), and touches no other row.
  */
 typedef struct kvq_mla_tree_problem {
     int32_t n_seq, n_q, n_heads;    /* n_q: nodes a sequence at most, 1 .. 64            */

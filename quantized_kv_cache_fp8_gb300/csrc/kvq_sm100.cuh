@@ -188,16 +188,16 @@ __device__ __forceinline__ uint64_t desc_smem(uint32_t saddr, uint32_t lbo, uint
     return d;
 }
 
-// Instruction descriptor of kind::f8f6f4 with e4m3 A and B and fp32 D (the A and B format
-// fields read 0 = e4m3); MN-major operands as in idesc_f16_f32.
+// Instruction descriptor of kind::f8f6f4 with e4m3 A, e4m3 or e5m2 B and fp32 D (the A and B format
+// fields read 0 = e4m3, 1 = e5m2); MN-major operands as in idesc_f16_f32.
 __host__ __device__ constexpr uint32_t idesc_e4m3_f32(int M, int N, bool a_mn = false,
-                                                      bool b_mn = false)
+                                                      bool b_mn = false, bool b_e5m2 = false)
 {
-    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
+    return (1u << 4) | ((b_e5m2 ? 1u : 0u) << 10) | ((a_mn ? 1u : 0u) << 15) | ((b_mn ? 1u : 0u) << 16) |
            ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T with e4m3 operands (K = 32 a step), one thread
+// D[tmem] (+)= A[smem] * B[smem]^T with 8-bit operands (K = 32 a step), one thread
 __device__ __forceinline__ void mma_e4m3_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                             uint32_t idesc, uint32_t accumulate)
 {

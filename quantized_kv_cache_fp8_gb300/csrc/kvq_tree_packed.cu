@@ -2,7 +2,7 @@
 // of a sequence packed into tiles of NR = 64 (or 32) rows that share one pass over the cache
 // (tcgen05 kind::f8f6f4; no code is converted).
 //
-// Per tile of 128 cache rows (M) and NR query rows (N), all operands e4m3:
+// Per tile of 128 cache rows (M) and NR query rows (N), e4m3 operands but for one digit:
 //   S^T[rows x 2 NR] = C_tile[rows x 576] . Qd^T        Qd: two digits of every query row
 //   O^T[dims x NR]  += V_tile^T[dims x rows] . Wd^T      Wd: two digits of every weight
 // Each 128-dim block of the latent codes is one [128 rows x 128 B] box, 128B-swizzled, read
@@ -10,13 +10,27 @@
 // of a row stay outside: the softmax applies them to the scores in fp32 and folds the
 // latent's into the weights.
 //
-// Digits.  An e4m3 rounding keeps 4 significant bits, so q = 2^-sigma (Qd_0 + Qd_1 / 16) holds
-// the 8 bits of a bfloat16 exactly (down to 2^-21 of the row's largest element), and w = Wd_0 +
-// Wd_1 carries a weight to 2^-9 of its value, or to 2^-10 absolute where the second digit is
-// subnormal, on a scale that keeps the largest weight of a row between 2^kBase and 2^8.  The
-// outputs are rounded to bfloat16 (2^-8), so more digits would not show.  With NR = 32 the digits
-// of a weight have N columns of their own (the second one in units of 2^-4); with NR = 64 tensor
-// memory has no room for that and they are summed along K.
+// Digits of a query.  An e4m3 rounding keeps 4 significant bits, so q = 2^-sigma (Qd_0 + Qd_1 / 16) holds
+// the 8 bits of a bfloat16 exactly (down to 2^-21 of the row's largest element).
+//
+// Digits of a weight.  w is on a scale that keeps the largest weight of a row between 2^kBase and 2^8.
+// Wd_0 is its e4m3 rounding, with a remainder of at most 2^-4 w, or 2^-10 where w < 2^-6; Wd_1 is the
+// remainder's:
+//   NR = 64: in e5m2 (an MMA has a type for each operand), an image of its own summed along K, as tensor
+//            memory has no room for more columns: w to 2^-8 of itself from 2^-6 on;
+//   NR = 32: in e4m3, in units of 2^-4, with N columns of its own: w to 2^-9 of itself from 2^-6 on.
+// The outputs are rounded to bfloat16 (2^-8), so more digits would not show in a single weight.  Smaller
+// ones are small alone, but a long context has many: under one heavy row, the tail's weights of 2^-10 and
+// less can be half of the softmax, and if each is rounded to the nearest digit they are off the same
+// way together (with e4m3 digits that end at 2^-9, 32768 equal weights of half of the sum were lost whole: an
+// error of 0.44 of the output).  So a small remainder is rounded up or down by a level that depends on the
+// row's position (dither below): off by 2^-13 at most, which is 2^-19 of the largest weight, right on
+// the average of any 256 neighbouring rows down to 2^-25, and the same at every call.  Errors of the tail
+// then grow with the square root of its rows, 2^-11 of the output for 65536 of them.  Measured against 64
+// bits with a heavy row of 0 to 99.9% of the weight before 1000 to 65536 rows that share a mean: 0.0018 to
+// 0.0024 of the output's norm, the figures of the per-query form, whose weights keep 16 bits.  What it
+// costs: 277.6 -> 282.0 us and 179.0 -> 181.7 us in the first two calls below (kBase 4 and kLazy 4: 280.9 and
+// 180.8, at four times the tail's error).
 //
 // Softmax: one running maximum m per query row, over u = s + log2(latent scale): the weights are
 // 2^(u - m + kBase), the normalizer sums 2^(s - m).  It moves only when a tile exceeds it by more
@@ -73,7 +87,7 @@ constexpr int kBoxes = 5;                    // four latent blocks and the rope 
 constexpr int kPieces = 8;                   // 16-byte pieces of a latent that each quarter of the warps clears
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 4.0f, kBase = 4.0f;  // kLazy + kBase <= 8: weights stay below 2^8 < 448
+constexpr float kLazy = 2.0f, kBase = 6.0f;  // kLazy + kBase <= 8: weights stay up to 2^8 < 448
 constexpr float kTiny = 96.0f;
 constexpr float kNoMax = -1e30f;             // the maximum of a partial over nothing: below any other
 constexpr uint64_t kTimeoutNs = kDefaultWaitNs;   // drains
@@ -335,18 +349,58 @@ struct Walk {
 };
 
 // ---- digits and queries -------------------------------------------------------------------
-// Two values -> their two digits, the second in units of 1 / kScale.  The value passes through
-// binary16 (2^-11 of it beside the 2^-9 that two digits keep; a query's 8 bits exactly), where the
-// first digit's remainder is exact.
-template <int kScale>
-__device__ __forceinline__ void digits2(float2 v, uint32_t& d0, uint32_t& d1)
+// Two values of a query -> their two e4m3 digits, the second in units of 1/16.  The value passes through
+// binary16 (a query's 8 bits exactly), where the first digit's remainder is exact.
+__device__ __forceinline__ void query_digits(float2 v, uint32_t& d0, uint32_t& d1)
 {
     const __half2 h = __float22half2_rn(v);
     const __nv_fp8x2_storage_t c = __nv_cvt_halfraw2_to_fp8x2(h, __NV_SATFINITE, __NV_E4M3);
-    __half2 r = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
-    if (kScale != 1) r = __hmul2(r, __half2half2(__ushort_as_half(0x4C00)));       // 16
+    const __half2 r = __hsub2(h, __half2(__nv_cvt_fp8x2_to_halfraw2(c, __NV_E4M3)));
     d0 = c;
-    d1 = __nv_cvt_halfraw2_to_fp8x2(r, __NV_SATFINITE, __NV_E4M3);
+    d1 = __nv_cvt_halfraw2_to_fp8x2(__hmul2(r, __half2half2(__ushort_as_half(0x4C00))), __NV_SATFINITE, __NV_E4M3);   // 16
+}
+
+// What a cache row's second digits are rounded with (the same bits in both halves): row t of the
+// sequence takes the level 157 t mod 256 of 256 equidistant ones, so that any 256 rows in a row have
+// each level once.  NR = 64: the level, added below the digit's last bit; NR = 32: (2 level - 255) 2^-18
+// as binary16, from -1/2 to 1/2 of the smallest step of e4m3.
+template <int NR>
+__device__ __forceinline__ uint32_t dither(int t)
+{
+    const uint32_t level = (157u * (uint32_t)t) & 255u;
+    if (NR == 64) return level * 0x10001u;
+    const __half2 d = __half2half2(__float2half_rn((float)(2 * (int)level - 255) * 0x1p-18f));
+    uint32_t r;
+    memcpy(&r, &d, 4);
+    return r;
+}
+
+// Four weights -> their two digits, a byte each (0 gives 0).  A weight passes through binary16 (2^-12 of
+// it, or 2^-25), where the first digit's remainder r is exact.
+template <int NR>
+__device__ __forceinline__ void weight_digits(float2 a, float2 b, uint32_t dith, uint32_t& d0, uint32_t& d1)
+{
+    const __half2 v[2] = {__float22half2_rn(a), __float22half2_rn(b)};
+    uint32_t c[2], o[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        c[e] = __nv_cvt_halfraw2_to_fp8x2(v[e], __NV_SATFINITE, __NV_E4M3);
+        const __half2 r = __hsub2(v[e], __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[e], __NV_E4M3)));
+        if constexpr (NR == 64) {
+            // e5m2 is the upper byte of binary16: r rounded to the nearest from 2^-10 on, and by the row's
+            // level below (a NaN's pattern, 0x7FFF, carries no further than its own half)
+            uint32_t bits;
+            memcpy(&bits, &r, 4);
+            const uint32_t small = __hlt2_mask(__habs2(r), __half2half2(__ushort_as_half(0x1400)));      // 2^-10
+            o[e] = bits + ((small & dith) | (~small & 0x00800080u));
+        } else {
+            __half2 off;
+            memcpy(&off, &dith, 4);
+            o[e] = __nv_cvt_halfraw2_to_fp8x2(__hfma2(r, __half2half2(__ushort_as_half(0x4C00)), off), __NV_SATFINITE, __NV_E4M3);   // 16 r
+        }
+    }
+    d0 = c[0] | c[1] << 16;
+    d1 = NR == 64 ? prmt(o[0], o[1], 0x7531u) : o[0] | o[1] << 16;
 }
 
 // One warp: query rows r0 + i, i = warp, warp + 16, .. (of the sequence's n * H; zero from `rows` on)
@@ -392,8 +446,8 @@ __device__ __forceinline__ void write_queries(const Shared<NR>& sh, const kvq_ml
         for (int e = 0; e < 5; ++e) {
             uint32_t a0, a1, b0, b1;
             const uint32_t x = w[n][2 * e], y = w[n][2 * e + 1];
-            digits2<16>(make_float2(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xFFFF0000u) * scale), a0, a1);
-            digits2<16>(make_float2(__uint_as_float(y << 16) * scale, __uint_as_float(y & 0xFFFF0000u) * scale), b0, b1);
+            query_digits(make_float2(__uint_as_float(x << 16) * scale, __uint_as_float(x & 0xFFFF0000u) * scale), a0, a1);
+            query_digits(make_float2(__uint_as_float(y << 16) * scale, __uint_as_float(y & 0xFFFF0000u) * scale), b0, b1);
             d0[e] = a0 | b0 << 16;
             d1[e] = a1 | b1 << 16;
         }
@@ -795,14 +849,11 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 }
                 uint32_t w0[GR / 4], w1[GR / 4];
                 const f32x2 up2 = pack2(lg + kBase, lg + kBase);
+                const uint32_t dith = dither<NR>(i * kRT + t);
 #pragma unroll
                 for (int e = 0; e < GR; e += 4) {
                     const float2 va = unpack2(add2(t2[e / 2], up2)), vb = unpack2(add2(t2[e / 2 + 1], up2));
-                    uint32_t a0, a1, b0, b1;
-                    digits2<NR == 64 ? 1 : 16>(make_float2(ex2(va.x), ex2(va.y)), a0, a1);
-                    digits2<NR == 64 ? 1 : 16>(make_float2(ex2(vb.x), ex2(vb.y)), b0, b1);
-                    w0[e / 4] = a0 | b0 << 16;
-                    w1[e / 4] = a1 | b1 << 16;
+                    weight_digits<NR>(make_float2(ex2(va.x), ex2(va.y)), make_float2(ex2(vb.x), ex2(vb.y)), dith, w0[e / 4], w1[e / 4]);
                 }
                 // the context of tile c - 1 has read the W image, and O may be rescaled
                 if (i > k.tile && ok) ok = wait_bar<kSmxSpin>(sh, sh.o_done(), (uint32_t)(c - 1) & 1u, a);
@@ -1038,7 +1089,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
     } else if (warp == kWarpC) {
         // ================================ context MMAs ====================================
         const bool leader = elect_one();
-        constexpr uint32_t idesc = idesc_e4m3_f32(kRT, 64, true, true);            // V^T . Wd^T, both MN-major
+        // V^T . Wd^T, both MN-major; the second image of NR = 64 is e5m2
+        constexpr uint32_t idesc = idesc_e4m3_f32(kRT, 64, true, true), idesc1 = idesc_e4m3_f32(kRT, 64, true, true, true);
         // first, the CTA with a unit's first tile tells the combine who shares it (all units of the
         // stretch at once, so that nothing is left out if the CTA gives up)
         if (leader) {
@@ -1075,7 +1127,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                         for (int ks = 0; ks < kRT / 32; ++ks) {
                             const uint64_t ad = desc_smem(box + ks * 4096, 16, 1024, kSwizzle128);
                             const uint64_t bd = desc_smem(wb + d * kRT * 64 + ks * 2048, 16, 512, kSwizzle64);
-                            mma_e4m3_ss(tmem + kColO + 64 * m, ad, bd, idesc, (i == k.tile && d == 0 && ks == 0) ? 0u : 1u);
+                            mma_e4m3_ss(tmem + kColO + 64 * m, ad, bd, d ? idesc1 : idesc, (i == k.tile && d == 0 && ks == 0) ? 0u : 1u);
                         }
                     }
                     mma_commit(sh.empty(st, m));

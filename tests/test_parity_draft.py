@@ -711,6 +711,89 @@ def test_tree_moving_maxima_and_small_pages_repeat(kvq, orc, H):
         assert np.array_equal(again[0], got[0]) and np.array_equal(again[1], got[1])
 
 
+def heavy_tail_cache(T, seed):
+    """fp8 rows with a common mean; rope keys whose element 0 is N(0,1) and whose elements 1, 2, 3 single out
+    the first, a middle and the last row but eight (256 there, 0 elsewhere)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    rnd = lambda *s: torch.randn(*s, device="cuda", generator=g)
+    c = rnd(1, 512) + rnd(T, 512)
+    k = torch.zeros(T, 64, device="cuda")
+    k[:, 0] = rnd(T)
+    for i, t in enumerate((0, T // 2 + 5, T - 9)):
+        k[t] = 0
+        k[t, 1 + i] = 256.0
+    ls, rs = c.abs().amax(1) / 448.0, k.abs().amax(1) / 448.0
+    code = lambda x, s: (x / s.clamp(min=1e-30)[:, None]).to(torch.float8_e4m3fn)
+    lat, rope = code(c, ls), code(k, rs)
+    cache = dict(lat=lat.view(torch.uint8), lat_scale=ls, rope=rope.view(torch.uint8), rope_scale=rs)
+    return cache, lat.double() * ls.double()[:, None], rope.double() * rs.double()[:, None]
+
+
+@pytest.mark.parametrize("impl,n_q,many", [(1, 2, True), (1, 4, True), (1, 4, False), (2, 4, False)])
+@pytest.mark.parametrize("T", [1000, 4096, 14001, 32768, 65536])
+def test_tree_heavy_row_and_broad_tail(kvq, impl, n_q, many, T):
+    """A long context as it is met: one row holds 0 to 99.9% of a query's weight, the rest is spread over all
+    others, whose latents share a mean, so that lost or rounded weights of the tail add up instead of
+    averaging out.  In tiles of 32 and 64 query rows, with a unit in one stretch (as many equal sequences as SMs,
+    sharing their pages) and cut into many, and per query.
+
+    Bounds, relative to the output's norm, none of which grows with T.  Rounding of the output: 2^-8 an
+    element at most, so 2^-8 / sqrt(3) in the root mean square.  Weights of the heavy row and of a tail of equal
+    weights may all be off the same way, by 2^-8 of themselves, but one of the two sets the scale and is exact, so the
+    mixture is off by 2^-8 / 4 of the two parts' difference at most, 2^-9 of the output with a tail of at least its
+    norm.  Below 2^-12 of the largest, weights are off by 2^-19 of it at random: sqrt(65536) 2^-19 = 2^-11.
+    Together under 2^-8.  The share along the right direction, where the roundings of 512 elements
+    average to 2^-8 / sqrt(3 512) each, six of them 2^-10.7: 2^-9 + 2^-10."""
+    page, H, n_seq = 64, 16, torch.cuda.get_device_properties(0).multi_processor_count if many else 1
+    cache, c, k = heavy_tail_cache(T, T + n_q)
+    pad = -T % page
+    cache = {key: torch.cat([v, v[:pad]]).contiguous() for key, v in cache.items()}
+    scale = float(W.SM_SCALE)
+    spread = [0.0, 0.3, 1.0, 2.5]                               # standard deviation of the tail's scores, in nats
+    share = [0.0, 0.5, 0.9, 0.99, 0.999]
+    ql = torch.zeros(n_q, H, 512, device="cuda")
+    qr = torch.zeros(n_q, H, 64, device="cuda")
+    for j in range(n_q):
+        for h in range(H):
+            i = H * j + h
+            qr[j, h, 0] = spread[i % 4] / scale
+            p = share[i % 5]
+            tail = torch.logsumexp(scale * qr[j, h, 0].bfloat16().double() * k[:, 0], 0).item()
+            for at in range(3):
+                want = tail + np.log(p / (1 - p)) if p > 0 and at == i % 3 else 0.0
+                qr[j, h, 1 + at] = want / (256.0 * scale)
+    ql, qr = ql.bfloat16()[None].repeat(n_seq, 1, 1, 1), qr.bfloat16()[None].repeat(n_seq, 1, 1, 1)
+    order = torch.randperm((T + pad) // page, generator=torch.Generator().manual_seed(T)).int().cuda()
+    paged_cache = {}
+    for key, v in cache.items():
+        w = torch.empty_like(v).view(-1, page, *v.shape[1:])
+        w[order.long()] = v.view(-1, page, *v.shape[1:])
+        paged_cache[key] = w.view(v.shape)
+    p = kvq.make_tree_problem(seq_len=i32(n_seq, fill=T), q_lat=ql, q_rope=qr, sm_scale=scale, max_seq_len=T, fmt=1,
+                              cache=paged_cache, block_table=order[None].repeat(n_seq, 1), page_size=page, impl=impl)
+    assert kvq.kvq_mla_tree_decode_kernel(p) == impl
+    ws = torch.empty(kvq.kvq_mla_tree_decode_workspace(p), dtype=torch.uint8, device="cuda")
+    out = torch.empty(n_seq, n_q, H, 512, dtype=torch.bfloat16, device="cuda")
+    lse, st = torch.empty(n_seq, n_q, H, device="cuda"), i32(1)
+    kvq.kvq_mla_tree_decode(p, out, lse, ws, st)
+    torch.cuda.synchronize()
+    assert st.item() == 0
+    worst = 0.0
+    for j in range(n_q):
+        L = T - n_q + j + 1
+        sc = scale * (ql[0, j].double() @ c[:L].T + qr[0, j].double() @ k[:L].T)
+        ref = torch.softmax(sc, 1) @ c[:L]
+        got = out[:, j].double()
+        assert torch.allclose(lse[:, j].double(), torch.logsumexp(sc, 1).expand(n_seq, H), rtol=2e-6, atol=1e-4)
+        err = (got - ref).norm(dim=-1) / ref.norm(dim=-1)
+        along = ((got * ref).sum(-1) / (ref * ref).sum(-1) - 1).abs()
+        worst = max(worst, err.max().item())
+        assert err.max() < 2.0**-8, f"node {j}: {err.max(0).values.tolist()}"
+        assert along.max() < 2.0**-9 + 2.0**-10, f"node {j}: {along.max(0).values.tolist()}"
+    print(f"worst |error| / |output| {worst:.5f}")
+
+
 def test_tree_two_calls_at_once(kvq, orc):
     """Calls on two streams with their own workspaces do not touch one another."""
     T, n_q, H = 3000, 8, 64
