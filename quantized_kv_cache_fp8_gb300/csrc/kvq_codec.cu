@@ -667,9 +667,11 @@ __device__ __forceinline__ void append_fp8_bf16_rows(const __nv_bfloat16* __rest
         }
         if (o < 0) continue;
         const float s = __fdiv_rn(amax, 448.0f);
-        // IEEE quotients from one reciprocal a row: with y = RN(1 / s) and q = RN(x y), which is within
-        // an ulp of x / s, RN(q + (x - q s) y) is RN(x / s) (Markstein, 1990), as long as the remainder
-        // is exact: scales far from the ends of the range
+        // IEEE quotients from one reciprocal a row (Markstein, 1990): with y = RN(1 / s) and q = RN(x y), which
+        // is within 1.5 ulp of x / s (half of one each for y and for the product, up to twice that where
+        // significands are near 2), RN(q - (q s - x) y) is RN(x / s): the remainder q s - x is exact for scales far
+        // from the ends of the range, and the test of all pairs of bfloat16 significands finds no code that
+        // differs.  x = 0 keeps its sign: its remainder is +0 and q - 0 is q.
         const bool plain = s >= 0x1p-90f && s <= 0x1p90f;
         const float y = __frcp_rn(plain ? s : 1.0f);
         uint2* cr = reinterpret_cast<uint2*>(codes + o * kDLat);
@@ -688,7 +690,7 @@ __device__ __forceinline__ void append_fp8_bf16_rows(const __nv_bfloat16* __rest
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float q = __fmul_rn(f[e], y);
-                        f[e] = __fmaf_rn(__fmaf_rn(-q, s, f[e]), y, q);
+                        f[e] = __fmaf_rn(-__fmaf_rn(q, s, -f[e]), y, q);
                     }
                 } else {
 #pragma unroll 1

@@ -266,6 +266,37 @@ def test_append_non_finite_rows_equal_encode_mla(kvq, bf16):
         assert torch.equal(a[key].view(torch.uint8), b[key].view(torch.uint8)), key
 
 
+@pytest.mark.parametrize("bf16", [False, True])
+def test_append_every_quotient_equals_encode_mla(kvq, bf16):
+    """fp8 rows whose largest element takes each of the 128 significands of bfloat16, at exponents from -70 to 90, beside
+    elements of every significand, both signs and 18 binades, and beside zeros of both signs: the
+    bytes of kvq_encode_mla, in which a negative zero is the code 0x80."""
+    sig = np.arange(128, 256, dtype=np.float64)
+    small = np.concatenate([sig * 2.0**-e for e in range(1, 19)])             # below the largest's binade
+    small = np.concatenate([small, -small, [0.0, -0.0]])
+    per = 510
+    small = np.concatenate([small, np.full(-len(small) % per, -0.0)]).reshape(-1, per)
+    rows = []
+    for e in (-77, 0, 83):
+        for top in sig:
+            x = np.full((len(small), 576), -0.0)
+            x[:, 0], x[:, 1:1 + per], x[:, 511], x[:, 512] = top, small, 0.0, -top
+            x[:, 513:] = small[:, :63]
+            rows.append(x * 2.0**e)
+    x = np.concatenate(rows).astype(np.float32)
+    n = len(x)
+    wide = dev(x)
+    both = wide.bfloat16() if bf16 else wide
+    assert torch.equal(both.float().view(torch.int32), wide.view(torch.int32))                 # exact, signs of zeros included
+    a, b = empty_planes(1, n), empty_planes(1, n)
+    kvq.kvq_encode_mla(wide[:, :512].contiguous(), wide[:, 512:].contiguous(), 1, None, a["lat"], a["lat_scale"], a["rope"], a["rope_scale"])
+    kvq.kvq_append_mla(both[:, :512], both[:, 512:], torch.arange(n, dtype=torch.int32, device="cuda"), 1, None, b)
+    torch.cuda.synchronize()
+    assert (a["lat"] == 0x80).any() and (a["rope"] == 0x80).any()
+    for key in a:
+        assert torch.equal(a[key].view(torch.uint8), b[key].view(torch.uint8)), key
+
+
 def test_append_equals_encode_mla(kvq):
     """The bytes of kvq_encode_mla, at the identity and a reversed slot map; zero rows."""
     n = 600
