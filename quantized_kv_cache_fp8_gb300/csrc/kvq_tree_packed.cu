@@ -406,7 +406,7 @@ __device__ __forceinline__ void weight_digits(float2 a, float2 b, uint32_t dith,
 // One warp: query rows r0 + i, i = warp, warp + 16, .. (of the sequence's n * H; zero from `rows` on)
 // into rows i and NR + i of the Q image.  Lane: 16 latent dims, and (lane < 16) 4 rope dims.  sigma
 // puts the row's largest element in [128, 256); a NaN or an infinity in the row makes its gain, and so
-// its scores, NaN.
+// its scores, NaN, and its digits zeros.
 template <int NR>
 __device__ __forceinline__ void write_queries(const Shared<NR>& sh, const kvq_mla_tree_problem& p, int s, int64_t r0,
                                               int64_t rows, int warp, int lane)
@@ -439,6 +439,11 @@ __device__ __forceinline__ void write_queries(const Shared<NR>& sh, const kvq_ml
         for (int e = 0; e < 10; ++e) m = __vmaxu2(m, w[n][e] & 0x7FFF7FFFu);
         m = max(m & 0xFFFFu, m >> 16);
         m = __reduce_max_sync(kFull, m);
+        if (m >= 0x7F80u) {
+            // the row's gain says NaN; its digits are zeros, so that the scores of a row tell only of its codes
+#pragma unroll
+            for (int e = 0; e < 10; ++e) w[n][e] = 0;
+        }
         const int sigma = m != 0 ? min(100, max(-120, 7 - ((int)(m >> 7) - 127))) : 0;
         const float scale = __int_as_float((127 + sigma) << 23);
         uint32_t d0[5], d1[5];
@@ -755,7 +760,8 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                             *row_piece(sh, st, rst, t, pc) = make_uint4(0u, 0u, 0u, 0u);
                     }
                     if (have) {
-                        // a code that no encoder writes makes the scores of every query row NaN
+                        // a code that no encoder writes makes the scores of every query row NaN (and a scale that is not
+                        // finite may), a query's digits never
                         if (isnan(unpack2(t2[0]).x)) {
                             clear_row(sh, st, t, hp);
 #pragma unroll 1

@@ -682,6 +682,34 @@ def test_tree_non_finite_queries(kvq, orc, impl, H):
     check_tree((out, lse, st), ref)
 
 
+@pytest.mark.parametrize("H", [20, 640])
+def test_tree_non_finite_queries_touch_no_other_row(kvq, orc, H):
+    """NaNs and infinities in every eighth query row (the first of each group of rows that the packed form's warps
+    share), beside codes that no encoder writes: the other rows have the bits that they have when these
+    rows are zero."""
+    T, n_q = 1300, 4
+    signs = W.sign_bits(1)
+    cache = make_cache(orc, 1, T, 2, signs)
+    for i, key in enumerate(("lat", "rope")):
+        mask, val = W.planted_codes(cache[key].shape, 2e-5, seed=5 + i)
+        cache[key] = np.where(mask, val, cache[key])
+    ql, qr = queries(1, n_q, H, 4)
+    flat_l, flat_r = ql.view(-1, 512), qr.view(-1, 64)
+    bad = torch.arange(0, n_q * H, 8, device="cuda")
+    kw = dict(fmt=1, cache=cache, signs=signs, lens=[T], n_node=[n_q], masks=None, q_lat=ql, q_rope=qr, stride=T, impl=1)
+    flat_l[bad], flat_r[bad] = 0, 0
+    want = run_tree(kvq, **kw)
+    for i, r in enumerate(bad.tolist()):
+        (flat_r if i % 4 == 3 else flat_l)[r, 5 * i % 64] = (float("nan"), float("inf"), float("-inf"))[i % 3]
+    got = run_tree(kvq, **kw)
+    hit = np.zeros(n_q * H, bool)
+    hit[::8] = True
+    hit = hit.reshape(1, n_q, H)
+    assert got[2] == want[2] == 0
+    assert np.isnan(got[0][hit]).all() and np.isnan(got[1][hit]).all()
+    assert np.array_equal(got[0][~hit], want[0][~hit]) and np.array_equal(got[1][~hit], want[1][~hit])
+
+
 @pytest.mark.parametrize("n_seq,H", [(1, 16), (3, 200)])
 def test_tree_waits_give_up_then_recover(kvq, orc, n_seq, H):
     """With the limit of the pipeline's waits cut to 200 ns the call still returns, sets KVQ_DEV_TIMEOUT and
