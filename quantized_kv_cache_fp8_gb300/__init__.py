@@ -446,6 +446,15 @@ def _want(name, t, dtype, *shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)}, is {t.dtype} {list(got)}")
 
 
+def _want_signs(name, t, fmt):
+    """The 512 rotation signs of a rotated tier: 16 words, one bit a dimension (None: left to the library)."""
+    if t is None or fmt == FMT_FP8:
+        return
+    import torch
+    if t.dtype not in (torch.int32, torch.uint32) or t.numel() != 16 or not t.is_contiguous():
+        raise ValueError(f"{name} must be 16 contiguous 32-bit integers, is {t.dtype} {list(t.shape)}")
+
+
 def _one_device(*tensors):
     """The index of the device that holds every tensor (-1: the host)."""
     d = {t.get_device() for t in tensors if t is not None}
@@ -529,6 +538,7 @@ def kvq_append_mla(c_lat, k_rope, slot_map, fmt, sign_bits, planes: dict, dev_st
     if rows == 1:                                         # (a single row's stride is arbitrary)
         ldx, ldr = 512, 64
     _want("slot_map", slot_map, "int32", rows)
+    _want_signs("sign_bits", sign_bits, fmt)
     c = _mla_planes(planes, fmt)
     stream = _stream_on(_one_device(c_lat, k_rope, slot_map, sign_bits, planes["lat"], planes["lat_scale"],
                                     planes["rope"], planes["rope_scale"]), stream)
@@ -559,6 +569,7 @@ def make_tree_problem(*, seq_len, q_lat, q_rope, sm_scale, max_seq_len, fmt, cac
     _want("n_node", n_node, "int32", n_seq)
     _want("mask", mask, "int64", n_seq, n_q)
     _want("block_table", block_table, "int32", n_seq, None)
+    _want_signs("signs", signs, fmt)
     p = TreeProblem()
     p.n_seq, p.n_q, p.n_heads, p.d_lat, p.d_rope = n_seq, n_q, H, DL, q_rope.shape[-1]
     p.fmt, p.max_seq_len = int(fmt), int(max_seq_len)

@@ -197,6 +197,28 @@ def test_binding_refuses_tensors_of_several_devices(kvq, monkeypatch):
         kvq.kvq_mla_tree_decode(t, torch.zeros(2, 3, 4, 512, dtype=torch.bfloat16), None, torch.zeros(4096, dtype=torch.uint8))
 
 
+def host_planes(bytes_a_row):
+    return dict(lat=torch.zeros(8, bytes_a_row, dtype=torch.uint8), lat_scale=torch.zeros(8),
+                rope=torch.zeros(8, 64, dtype=torch.uint8), rope_scale=torch.zeros(8))
+
+
+@pytest.mark.parametrize("bad", [torch.zeros(15, dtype=torch.int32), torch.zeros(16, dtype=torch.int16),
+                                 torch.zeros(16), torch.zeros(32, dtype=torch.int32)[::2], torch.zeros(512, dtype=torch.int32)],
+                         ids=["short", "int16", "float", "strided", "long"])
+def test_binding_refuses_wrong_signs(kvq, bad):
+    """The kernels read 16 words of signs: a tensor of fewer would be read past its end."""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    q = torch.zeros(2, 3, 4, 576, dtype=torch.bfloat16)
+    args = dict(seq_len=i32(2), q_lat=q[..., :512], q_rope=q[..., 512:], sm_scale=1.0, max_seq_len=8)
+    for fmt, width in ((kvq.FMT_TQ4, 256), (kvq.FMT_TQ6, 384), (kvq.FMT_TQ3, 192)):
+        planes = host_planes(width)
+        kvq.make_tree_problem(**args, fmt=fmt, cache=planes, signs=i32(16))
+        with pytest.raises(ValueError, match="signs"):
+            kvq.make_tree_problem(**args, fmt=fmt, cache=planes, signs=bad)
+        with pytest.raises(ValueError, match="sign_bits"):
+            kvq.kvq_append_mla(torch.zeros(4, 512), torch.zeros(4, 64), i32(4), fmt, bad, planes)
+
+
 def test_struct_layouts(kvq, tmp_path):
     structs = dict(kvq_page_plan=kvq.PagePlan, kvq_mla_tree_problem=kvq.TreeProblem, kvq_mla_accept_desc=kvq.AcceptDesc)
     lines = []
