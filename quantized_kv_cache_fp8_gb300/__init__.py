@@ -463,6 +463,18 @@ def _one_device(*tensors):
     return d.pop()
 
 
+def _status_on(d, t):
+    """The address of the dev_status word `t` (or None) of a call whose tensors are on device `d`."""
+    if t is None:
+        return None
+    import torch
+    if t.dtype not in (torch.int32, torch.uint32) or t.numel() < 1:
+        raise ValueError(f"dev_status must be a 32-bit integer tensor, is {t.dtype} {list(t.shape)}")
+    if t.get_device() != d:
+        raise ValueError(f"tensors on different devices: dev_status on {t.device}")
+    return t.data_ptr()
+
+
 def _stream_on(d, stream):
     """The stream of a call whose tensors are on device `d` (-1: the host), which must be the current
     device: the kernels run there."""
@@ -501,7 +513,8 @@ def make_page_plan(*, keep_len, n_new, block_table, n_held, free_list, n_free, p
 
 
 def kvq_resize_pages(p: PagePlan, dev_status=None, stream=None) -> None:
-    _check(lib().kvq_resize_pages(C.byref(p), _ptr(dev_status), _stream_on(p._device, stream)))
+    status = _status_on(p._device, dev_status)
+    _check(lib().kvq_resize_pages(C.byref(p), status, _stream_on(p._device, stream)))
 
 
 _LAT_BYTES = {FMT_FP8: 512, FMT_TQ4: 256, FMT_TQ6: 384, FMT_TQ3: 192}
@@ -540,10 +553,11 @@ def kvq_append_mla(c_lat, k_rope, slot_map, fmt, sign_bits, planes: dict, dev_st
     _want("slot_map", slot_map, "int32", rows)
     _want_signs("sign_bits", sign_bits, fmt)
     c = _mla_planes(planes, fmt)
-    stream = _stream_on(_one_device(c_lat, k_rope, slot_map, sign_bits, planes["lat"], planes["lat_scale"],
-                                    planes["rope"], planes["rope_scale"]), stream)
+    d = _one_device(c_lat, k_rope, slot_map, sign_bits, planes["lat"], planes["lat_scale"], planes["rope"],
+                    planes["rope_scale"])
+    status, stream = _status_on(d, dev_status), _stream_on(d, stream)
     _check(lib().kvq_append_mla(c_lat.data_ptr(), ldx, k_rope.data_ptr(), ldr, kind, rows, slot_map.data_ptr(),
-                                int(fmt), _ptr(sign_bits), C.byref(c), _ptr(dev_status), stream))
+                                int(fmt), _ptr(sign_bits), C.byref(c), status, stream))
 
 
 def _row_stride(name, q, width):
@@ -602,10 +616,10 @@ def kvq_mla_tree_decode_kernel(p: TreeProblem) -> int:
 def kvq_mla_tree_decode(p: TreeProblem, out, lse=None, workspace=None, dev_status=None, stream=None) -> None:
     _want("out", out, "bfloat16", p.n_seq, p.n_q, p.n_heads, 512)
     _want("lse", lse, "float32", p.n_seq, p.n_q, p.n_heads)
-    stream = _stream_on(_one_device(out, lse, workspace, p._keep[0]), stream)
+    d = _one_device(out, lse, workspace, p._keep[0])
+    status, stream = _status_on(d, dev_status), _stream_on(d, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(lib().kvq_mla_tree_decode(C.byref(p), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes,
-                                     _ptr(dev_status), stream))
+    _check(lib().kvq_mla_tree_decode(C.byref(p), _ptr(out), _ptr(lse), _ptr(workspace), ws_bytes, status, stream))
 
 
 def make_accept(*, seq_len, path, n_acc, new_len, fmt, cache, n_node=None, block_table=None, page_size=0,
@@ -631,7 +645,8 @@ def make_accept(*, seq_len, path, n_acc, new_len, fmt, cache, n_node=None, block
 
 
 def kvq_accept_mla(d: AcceptDesc, dev_status=None, stream=None) -> None:
-    _check(lib().kvq_accept_mla(C.byref(d), _ptr(dev_status), _stream_on(d._device, stream)))
+    status = _status_on(d._device, dev_status)
+    _check(lib().kvq_accept_mla(C.byref(d), status, _stream_on(d._device, stream)))
 
 
 # --- cache files ------------------------------------------------------------------------

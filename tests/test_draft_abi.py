@@ -219,6 +219,36 @@ def test_binding_refuses_wrong_signs(kvq, bad):
             kvq.kvq_append_mla(torch.zeros(4, 512), torch.zeros(4, 64), i32(4), fmt, bad, planes)
 
 
+def calls_with_status(kvq):
+    """The entry points on host tensors that pass every other check, as functions of dev_status."""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    planes = host_planes(512)
+    plan = kvq.make_page_plan(keep_len=i32(3), n_new=i32(3), block_table=i32(3, 4), n_held=i32(3), free_list=i32(9),
+                              n_free=i32(1), page_size=16, seq_len=i32(3), tok_start=i32(4), slot_map=i32(8))
+    done = kvq.make_accept(seq_len=i32(2), path=i32(2, 3), n_acc=i32(2), new_len=i32(2), fmt=1, cache=planes)
+    q = torch.zeros(2, 3, 4, 576, dtype=torch.bfloat16)
+    tree = kvq.make_tree_problem(seq_len=i32(2), q_lat=q[..., :512], q_rope=q[..., 512:], sm_scale=1.0, max_seq_len=8, fmt=1,
+                                 cache=planes)
+    out = torch.zeros(2, 3, 4, 512, dtype=torch.bfloat16)
+    return [lambda st: kvq.kvq_resize_pages(plan, st),
+            lambda st: kvq.kvq_append_mla(torch.zeros(4, 512), torch.zeros(4, 64), i32(4), 1, None, planes, st),
+            lambda st: kvq.kvq_mla_tree_decode(tree, out, None, torch.zeros(4096, dtype=torch.uint8), st),
+            lambda st: kvq.kvq_accept_mla(done, st)]
+
+
+def test_binding_refuses_wrong_status(kvq, monkeypatch):
+    for call in calls_with_status(kvq):
+        for bad in (torch.zeros(1, dtype=torch.int16), torch.zeros(1), torch.zeros(0, dtype=torch.int32)):
+            with pytest.raises(ValueError, match="dev_status"):
+                call(bad)
+    there = torch.zeros(1, dtype=torch.int32)
+    real = torch.Tensor.get_device
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 1 if t is there else real(t))
+    for call in calls_with_status(kvq):
+        with pytest.raises(ValueError, match="different devices"):
+            call(there)
+
+
 def test_struct_layouts(kvq, tmp_path):
     structs = dict(kvq_page_plan=kvq.PagePlan, kvq_mla_tree_problem=kvq.TreeProblem, kvq_mla_accept_desc=kvq.AcceptDesc)
     lines = []
