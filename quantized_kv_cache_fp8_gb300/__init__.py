@@ -520,9 +520,13 @@ def kvq_resize_pages(p: PagePlan, dev_status=None, stream=None) -> None:
 _LAT_BYTES = {FMT_FP8: 512, FMT_TQ4: 256, FMT_TQ6: 384, FMT_TQ3: 192}
 
 
+def _planes_of(planes):
+    return planes["lat"], planes["lat_scale"], planes["rope"], planes["rope_scale"]
+
+
 def _mla_planes(planes, fmt):
     import torch
-    lat, ls, rope, rs = planes["lat"], planes["lat_scale"], planes["rope"], planes["rope_scale"]
+    lat, ls, rope, rs = _planes_of(planes)
     n = lat.shape[0]
     one, u8, f32 = (n,), torch.uint8, torch.float32
     if not (lat.dtype is u8 and rope.dtype is u8 and ls.dtype is f32 and rs.dtype is f32 and
@@ -553,8 +557,7 @@ def kvq_append_mla(c_lat, k_rope, slot_map, fmt, sign_bits, planes: dict, dev_st
     _want("slot_map", slot_map, "int32", rows)
     _want_signs("sign_bits", sign_bits, fmt)
     c = _mla_planes(planes, fmt)
-    d = _one_device(c_lat, k_rope, slot_map, sign_bits, planes["lat"], planes["lat_scale"], planes["rope"],
-                    planes["rope_scale"])
+    d = _one_device(c_lat, k_rope, slot_map, sign_bits, *_planes_of(planes))
     status, stream = _status_on(d, dev_status), _stream_on(d, stream)
     _check(lib().kvq_append_mla(c_lat.data_ptr(), ldx, k_rope.data_ptr(), ldr, kind, rows, slot_map.data_ptr(),
                                 int(fmt), _ptr(sign_bits), C.byref(c), status, stream))
@@ -595,9 +598,8 @@ def make_tree_problem(*, seq_len, q_lat, q_rope, sm_scale, max_seq_len, fmt, cac
     p.q_lat, p.q_rope = _ptr(q_lat), _ptr(q_rope)
     p.ldq_lat, p.ldq_rope = _row_stride("q_lat", q_lat, 512), _row_stride("q_rope", q_rope, 64)
     p.sm_scale, p.impl = float(sm_scale), int(impl)
-    p._keep = [seq_len, n_node, mask, block_table, cache, signs, q_lat, q_rope]
-    p._device = _one_device(seq_len, n_node, mask, block_table, signs, q_lat, q_rope, cache["lat"], cache["lat_scale"],
-                            cache["rope"], cache["rope_scale"])
+    p._keep = [seq_len, n_node, mask, block_table, signs, q_lat, q_rope, *_planes_of(cache)]
+    p._device = _one_device(*p._keep)
     return p
 
 
@@ -638,9 +640,8 @@ def make_accept(*, seq_len, path, n_acc, new_len, fmt, cache, n_node=None, block
     if block_table is not None:
         d.block_table, d.max_pages, d.page_size = _ptr(block_table), block_table.shape[1], int(page_size)
     d.seq_stride_rows, d.cache = int(seq_stride_rows), _mla_planes(cache, fmt)
-    d._keep = [seq_len, n_node, path, n_acc, new_len, block_table, cache]
-    d._device = _one_device(seq_len, n_node, path, n_acc, new_len, block_table, cache["lat"], cache["lat_scale"],
-                            cache["rope"], cache["rope_scale"])
+    d._keep = [seq_len, n_node, path, n_acc, new_len, block_table, *_planes_of(cache)]
+    d._device = _one_device(*d._keep)
     return d
 
 

@@ -249,6 +249,26 @@ def test_binding_refuses_wrong_status(kvq, monkeypatch):
             call(there)
 
 
+def test_problems_keep_the_planes(kvq):
+    """A problem holds the tensors whose addresses it carries, not the dictionary they came in."""
+    import gc
+    import weakref
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    q = torch.zeros(2, 3, 4, 576, dtype=torch.bfloat16)
+    for make in (lambda planes: kvq.make_accept(seq_len=i32(2), path=i32(2, 3), n_acc=i32(2), new_len=i32(2), fmt=1, cache=planes),
+                 lambda planes: kvq.make_tree_problem(seq_len=i32(2), q_lat=q[..., :512], q_rope=q[..., 512:], sm_scale=1.0,
+                                                      max_seq_len=8, fmt=1, cache=planes)):
+        planes = host_planes(512)
+        refs = {k: weakref.ref(v) for k, v in planes.items()}
+        p = make(planes)
+        for k in planes:
+            planes[k] = None
+        gc.collect()
+        kept = {"lat": p.cache.lat, "lat_scale": p.cache.lat_scale, "rope": p.cache.rope, "rope_scale": p.cache.rope_scale}
+        for k, ref in refs.items():
+            assert ref() is not None and ref().data_ptr() == kept[k], k
+
+
 def test_struct_layouts(kvq, tmp_path):
     structs = dict(kvq_page_plan=kvq.PagePlan, kvq_mla_tree_problem=kvq.TreeProblem, kvq_mla_accept_desc=kvq.AcceptDesc)
     lines = []
