@@ -476,16 +476,17 @@ def _status_on(d, t):
 
 
 def _stream_on(d, stream):
-    """The stream of a call whose tensors are on device `d` (-1: the host), which must be the current
-    device: the kernels run there."""
-    if d >= 0:
-        import torch
-        now = torch.cuda.current_device()
-        if d != now:
-            raise ValueError(f"tensors on cuda:{d}, but the current device is cuda:{now}")
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if stream is None and raw is not None:
-            return raw(d)
+    """The stream of a call whose tensors are on device `d`, which must be the current device: the kernels
+    run there."""
+    if d < 0:
+        raise ValueError("the tensors are on the host")
+    import torch
+    now = torch.cuda.current_device()
+    if d != now:
+        raise ValueError(f"tensors on cuda:{d}, but the current device is cuda:{now}")
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if stream is None and raw is not None:
+        return raw(d)
     return _stream(stream)
 
 

@@ -249,6 +249,16 @@ def test_binding_refuses_wrong_status(kvq, monkeypatch):
             call(there)
 
 
+def test_binding_refuses_host_tensors(kvq):
+    """Nothing is launched on addresses of the host, whatever the stream."""
+    for call in calls_with_status(kvq):
+        with pytest.raises(ValueError, match="on the host"):
+            call(None)
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    with pytest.raises(ValueError, match="on the host"):
+        kvq.kvq_append_mla(torch.zeros(4, 512), torch.zeros(4, 64), i32(4), 1, None, host_planes(512), i32(1), stream=0)
+
+
 def test_problems_keep_the_planes(kvq):
     """A problem holds the tensors whose addresses it carries, not the dictionary they came in."""
     import gc
