@@ -54,6 +54,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <cfloat>
 #include <climits>
 #include <cstring>
 
@@ -89,7 +90,6 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 2.0f, kBase = 6.0f;  // kLazy + kBase <= 8: weights stay up to 2^8 < 448
 constexpr float kTiny = 96.0f;
-constexpr float kNoMax = -1e30f;             // the maximum of a partial over nothing: below any other
 constexpr uint64_t kTimeoutNs = kDefaultWaitNs;   // drains
 constexpr uint32_t kColO = 256;              // tensor memory: O^T of dims 128 m .. at 256 + 64 m
 
@@ -927,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 } else {
                     sh.factor()[tid] = unit;
                     reinterpret_cast<float2*>(a.part_ml)[slot * NR + tid] =
-                        aborted ? make_float2(INFINITY, INFINITY) : make_float2(lt == 0.0f ? kNoMax : m, lt);
+                        aborted ? make_float2(INFINITY, INFINITY) : make_float2(lt == 0.0f ? -INFINITY : m, lt);
                 }
             }
             smx_barrier();
@@ -1195,7 +1195,7 @@ __global__ void __launch_bounds__(kCombThreads) tree_combine_kernel(const __grid
     if (r >= tree_seq_shape(p, f.s).y * H) return;
     const float2* ml = reinterpret_cast<const float2*>(a.part_ml);
     auto at = [&](int k) { return (int64_t)(k == 0 ? f.slot : 2 * (f.cta + k)) * NR + blockIdx.y; };
-    float M = kNoMax;
+    float M = -FLT_MAX;                               // (finite: a piece that saw nothing has -inf, and so the weight 0)
     bool gave_up = false;
     for (int k = lane; k < f.pieces; k += 32) {
         const float2 x = ml[at(k)];

@@ -606,6 +606,32 @@ def test_tree_unused_rows_and_unwritten_codes(kvq, orc, impl, H):
 
 
 @SIZES
+def test_tree_scores_far_below_zero_beside_missing_pages(kvq, impl, H):
+    """Scores of about -5e31, and every page but the last third missing, so that parts of the sequence have nothing to
+    add: the rows that are there, all equal, are the output."""
+    T, n_q, page = 20000, 4, 16
+    pages = T // page
+    table = torch.full((1, pages), -1, dtype=torch.int32, device="cuda")
+    table[0, 2 * pages // 3:] = torch.arange(pages - 2 * pages // 3, dtype=torch.int32, device="cuda")
+    rows = (pages - 2 * pages // 3) * page
+    planes = dict(lat=torch.full((rows, 512), 0x38, dtype=torch.uint8, device="cuda"),            # 1.0
+                  lat_scale=torch.ones(rows, device="cuda"),
+                  rope=torch.zeros(rows, 64, dtype=torch.uint8, device="cuda"), rope_scale=torch.zeros(rows, device="cuda"))
+    ql = torch.full((1, n_q, H, 512), -(2.0**100), dtype=torch.bfloat16, device="cuda")
+    p = kvq.make_tree_problem(seq_len=i32(1, fill=T), q_lat=ql, q_rope=torch.zeros(1, n_q, H, 64, dtype=torch.bfloat16, device="cuda"),
+                              sm_scale=float(W.SM_SCALE), max_seq_len=T, fmt=1, cache=planes, block_table=table, page_size=page, impl=impl)
+    ws = torch.empty(kvq.kvq_mla_tree_decode_workspace(p), dtype=torch.uint8, device="cuda")
+    out, lse, st = torch.empty(1, n_q, H, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(1, n_q, H, device="cuda"), i32(1)
+    kvq.kvq_mla_tree_decode(p, out, lse, ws, st)
+    torch.cuda.synchronize()
+    score = -512 * 2.0**100 * float(W.SM_SCALE)
+    assert st.item() == BAD_PAGE
+    # the mean of equal rows: off by a step of fp32 a row at most, 2^-24 * 7000, below the rounding's 2^-8
+    assert (out == 1.0).all()
+    assert torch.allclose(lse, torch.full_like(lse, score), rtol=2e-6, atol=0)
+
+
+@SIZES
 @pytest.mark.parametrize("case", ["large scores", "zero queries", "zero rows", "mixed magnitudes", "one row"])
 def test_tree_score_ranges(kvq, orc, impl, H, case):
     """Scores far apart (one row takes everything; running maxima that climb by many powers of
