@@ -501,10 +501,11 @@ int kvq_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t l
  * the q rows of padding are not used.  A page that is missing or outside the pool sets
  * KVQ_DEV_BAD_PAGE and its rows are skipped.  The rows of a page past L may hold anything.
  * Queries and outputs are bfloat16; scores, the softmax's maximum and normalizer, the sums over rows and
- * lse are fp32.  In the packed form (below) a weight that multiplies a row keeps 8 bits (within
- * 2^-8 of itself) down to 2^-14 of its query row's largest; smaller ones are within 2^-19 of the
- * largest, rounded up or down by their row's position so that the errors of many cancel (their sum
- * is that of exact weights down to 2^-31 of the largest).  A query row that holds a NaN or an
+ * lse are fp32, for scores of magnitudes up to 2^22 (beyond, a step of fp32 is no longer small beside
+ * the logarithm of a row's scale).  In the packed form (below) a weight that multiplies a row is within
+ * 2^-8 of itself or, if that is more, 2^-19 of its query row's largest; those below 2^-12 of the
+ * largest are rounded up or down by their row's position, so that the errors of many cancel (their
+ * sum is that of exact weights down to 2^-31 of the largest).  A query row that holds a NaN or an
  * infinity gets NaN (if it sees anything), and touches no other row.
  */
 typedef struct kvq_mla_tree_problem {
@@ -558,7 +559,8 @@ int kvq_mla_tree_decode(const kvq_mla_tree_problem* p, void* out, float* lse, vo
  * n_acc is clamped to [0, n]; a path entry that is not larger than the one before it, or not a
  * node (0 .. n - 1), ends the path before it (KVQ_DEV_BAD_INDEX).  A row on a missing page is
  * not moved (KVQ_DEV_BAD_PAGE).  Rows behind new_len that no row moved to keep their bytes.
- * new_len may be seq_len itself.
+ * new_len may be seq_len itself.  Sequences without a block table must not share rows
+ * (seq_stride_rows >= 1 for more than one, KVQ_EINVAL otherwise, and not below any seq_len).
  */
 typedef struct kvq_mla_accept_desc {
     int32_t n_seq, n_q;             /* n_q: nodes a sequence at most, 1 .. 64            */

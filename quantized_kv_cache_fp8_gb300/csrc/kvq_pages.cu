@@ -499,7 +499,7 @@ int kvq_accept_mla(const kvq_mla_accept_desc* d, uint32_t* dev_status, kvq_strea
     if (d->fmt != KVQ_FMT_FP8 && !rotated_format(d->fmt)) return set_last_error(KVQ_EFORMAT, "%s: fmt %d", E, d->fmt);
     if (d->n_seq < 0) return set_last_error(KVQ_EINVAL, "%s: n_seq < 0", E);
     if (d->n_q < 1 || d->n_q > kAccNodes) return set_last_error(KVQ_EINVAL, "%s: n_q outside [1, 64]", E);
-    if (d->block_table ? d->max_pages < 1 || d->page_size < 1 : d->seq_stride_rows < 0)
+    if (d->block_table ? d->max_pages < 1 || d->page_size < 1 : d->seq_stride_rows < (d->n_seq > 1 ? 1 : 0))
         return set_last_error(KVQ_EINVAL, "%s: bad paging sizes", E);
     if (d->n_seq == 0) return KVQ_OK;
     const kvq_mla_cache& c = d->cache;

@@ -129,6 +129,16 @@ def test_accept_argument_errors(kvq):
     assert call(n_seq=0, seq_len=None) == 0
 
 
+def test_accept_refuses_sequences_on_the_same_rows(kvq):
+    """Without a block table and without a stride every sequence would move the same rows."""
+    i32 = lambda *s: torch.zeros(*s, dtype=torch.int32)
+    for n_seq, stride, reason in ((2, 0, b"bad paging sizes"), (1, 0, b"NULL pointer"), (2, 1, b"NULL pointer")):
+        d = kvq.make_accept(seq_len=i32(n_seq), path=i32(n_seq, 3), n_acc=i32(n_seq), new_len=i32(n_seq), fmt=1,
+                            cache=host_planes(512), seq_stride_rows=stride)
+        d.cache.lat = None                    # the check behind it: nothing is launched
+        assert kvq.lib().kvq_accept_mla(C.byref(d), None, None) == 1 and reason in kvq.lib().kvq_last_error()
+
+
 def test_faults_reach_the_new_entries(kvq):
     L = kvq.lib()
     calls = {"kvq_resize_pages": lambda: L.kvq_resize_pages(None, None, None),
