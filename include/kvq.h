@@ -503,7 +503,7 @@ int kvq_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t l
  * Queries and outputs are bfloat16; scores, the softmax's maximum and normalizer, the sums over rows and
  * lse are fp32, for scores of magnitudes up to 2^22 (beyond, a step of fp32 is no longer small beside
  * the logarithm of a row's scale).  In the packed form (below) a weight that multiplies a row is within
- * 2^-8 of itself or, if that is more, 2^-19 of its query row's largest; those below 2^-12 of the
+ * 2^-8 of itself or, if that is more, 2^-19 of its query row's largest; those below 2^-14 of the
  * largest are rounded up or down by their row's position, so that the errors of many cancel (their
  * sum is that of exact weights down to 2^-31 of the largest).  A query row that holds a NaN or an
  * infinity gets NaN (if it sees anything), and touches no other row.

@@ -17,14 +17,15 @@
 // Wd_0 is its e4m3 rounding, with a remainder of at most 2^-4 w, or 2^-10 where w < 2^-6; Wd_1 is the
 // remainder's:
 //   NR = 64: in e5m2 (an MMA has a type for each operand), an image of its own summed along K, as tensor
-//            memory has no room for more columns: w to 2^-8 of itself from 2^-6 on;
-//   NR = 32: in e4m3, in units of 2^-4, with N columns of its own: w to 2^-9 of itself from 2^-6 on.
+//            memory has no room for more columns;
+//   NR = 32: in e4m3, in units of 2^-4, with N columns of its own.
+// Either way w is within 2^-8 of itself from 2^-5 on.
 // The outputs are rounded to bfloat16 (2^-8), so more digits would not show in a single weight.  Smaller
 // ones are small alone, but a long context has many: under one heavy row, the tail's weights of 2^-10 and
 // less can be half of the softmax, and if each is rounded to the nearest digit they are off the same
 // way together (with e4m3 digits that end at 2^-9, 32768 equal weights of half of the sum were lost whole: an
-// error of 0.44 of the output).  So a small remainder is rounded up or down by a level that depends on the
-// row's position (dither below): off by 2^-13 at most, which is 2^-19 of the largest weight, right on
+// error of 0.44 of the output).  So the remainder is rounded up or down by a level that depends on the row's
+// position (dither below; NR = 64: where w < 2^-6): off by 2^-13 at most, which is 2^-19 of the largest weight, right on
 // the average of any 256 neighbouring rows down to 2^-25, and the same at every call.  Errors of the tail
 // then grow with the square root of its rows, 2^-11 of the output for 65536 of them.  Measured against 64
 // bits with a heavy row of 0 to 99.9% of the weight before 1000 to 65536 rows that share a mean: 0.0018 to
@@ -274,7 +275,7 @@ __device__ __forceinline__ int64_t tree_pool_row(const kvq_mla_tree_problem& p, 
 // A unit takes kUnitCost places on the line before its tiles: what a CTA pays to begin another unit
 // (epilogue, query image, refill of the pipeline: 25 thousand cycles of a full tile's 4300).  Every
 // stretch begins one anyway, so these places even out the stretches with several units.  Full tiles
-// with 4, 5, 6, 7 places: the ragged batch below 2182, 2127, 2100, 2084 us, 32 units of 32 tiles 44.4, 44.6,
+// with 4, 5, 6, 7 places: 32 ragged trees of 17.1 M pairs of node and row 2182, 2127, 2100, 2084 us, 32 units of 32 tiles 44.4, 44.6,
 // 44.4, 46.9; half tiles, two units of 256: 25.0, 24.9, 28.6, 26.8.
 template <int NR>
 constexpr int kUnitCost = NR == 64 ? 6 : 4;
@@ -387,11 +388,11 @@ __device__ __forceinline__ void weight_digits(float2 a, float2 b, uint32_t dith,
         c[e] = __nv_cvt_halfraw2_to_fp8x2(v[e], __NV_SATFINITE, __NV_E4M3);
         const __half2 r = __hsub2(v[e], __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)c[e], __NV_E4M3)));
         if constexpr (NR == 64) {
-            // e5m2 is the upper byte of binary16: r rounded to the nearest from 2^-10 on, and by the row's
-            // level below (a NaN's pattern, 0x7FFF, carries no further than its own half)
+            // e5m2 is the upper byte of binary16: r rounded to the nearest where the weight is 2^-6 or more, else by
+            // the row's level (a NaN's pattern, 0x7FFF, carries no further than its own half)
             uint32_t bits;
             memcpy(&bits, &r, 4);
-            const uint32_t small = __hlt2_mask(__habs2(r), __half2half2(__ushort_as_half(0x1400)));      // 2^-10
+            const uint32_t small = __hlt2_mask(v[e], __half2half2(__ushort_as_half(0x2400)));      // 2^-6
             o[e] = bits + ((small & dith) | (~small & 0x00800080u));
         } else {
             __half2 off;
@@ -565,8 +566,8 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 // products while the other runs (9 to 25%); the rope keys' slot freed by the score MMAs and copied
 // first (2 to 5%); copies of their own for scores and context (17%).
 // Measured, whole calls with the combine: 4 trees of 16 nodes x 64 heads at
-// T = 32768 268 us = 1090 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 178 us = 1025; 32 ragged
-// ones of up to 32 nodes and 65536 rows 2100 us = 1133 TFLOP/s (17.1 M pairs of node and row, 64 heads).
+// T = 32768 282 us = 1034 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 182 us = 1005; 32 ragged
+// ones of up to 32 nodes and 65536 rows 2892 us = 1117 TFLOP/s (23.2 M pairs of node and row, 64 heads).
 // ====================================================================================
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_constant__ Args a)
@@ -1000,6 +1001,7 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
             // (one tile ahead, from the tile before the first: one copy of the code)
 #pragma unroll 1
             for (int i = k.tile - 1; i < k.end && ok; ++i) {
+                __syncwarp();                         // (the leader reads the rows that the lanes stored a tile ago)
                 if (leader && i >= k.tile) {
                     const int st = c & 1;
                     volatile int* y = sh.copy_rows(2 * who + st);
@@ -1030,7 +1032,6 @@ __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_c
                 }
                 if (i >= k.tile) ++c;
                 if (i + 1 < k.end) look_up(i + 1, c & 1);
-                __syncwarp();                         // (the leader reads the rows that the lanes stored)
                 ok = __any_sync(kFull, leader && ok);
             }
         }
