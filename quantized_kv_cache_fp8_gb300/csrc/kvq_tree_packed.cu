@@ -30,8 +30,8 @@
 // then grow with the square root of its rows, 2^-11 of the output for 65536 of them.  Measured against 64
 // bits with a heavy row of 0 to 99.9% of the weight before 1000 to 65536 rows that share a mean: 0.0018 to
 // 0.0024 of the output's norm, the figures of the per-query form, whose weights keep 16 bits.  What it
-// costs: 277.6 -> 282.0 us and 179.0 -> 181.7 us in the first two calls below (kBase 4 and kLazy 4: 280.9 and
-// 180.8, at four times the tail's error).
+// costs: 266.3 -> 270.8 us and 174.1 -> 176.6 us in the first two calls below (kBase 4 and kLazy 4 would take 0.4%
+// off, at four times the tail's error).
 //
 // Softmax: one running maximum m per query row, over u = s + log2(latent scale): the weights are
 // 2^(u - m + kBase), the normalizer sums 2^(s - m).  It moves only when a tile exceeds it by more
@@ -566,8 +566,8 @@ __device__ __forceinline__ void tmem_st_n(uint32_t c, const uint32_t (&r)[16]) {
 // products while the other runs (9 to 25%); the rope keys' slot freed by the score MMAs and copied
 // first (2 to 5%); copies of their own for scores and context (17%).
 // Measured, whole calls with the combine: 4 trees of 16 nodes x 64 heads at
-// T = 32768 282 us = 1034 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 182 us = 1005; 32 ragged
-// ones of up to 32 nodes and 65536 rows 2892 us = 1117 TFLOP/s (23.2 M pairs of node and row, 64 heads).
+// T = 32768 271 us = 1078 TFLOP/s; one of 5 nodes x 128 heads at T = 131072 177 us = 1034; 32 ragged
+// ones of up to 32 nodes and 65536 rows 2830 us = 1141 TFLOP/s (23.2 M pairs of node and row, 64 heads).
 // ====================================================================================
 template <int NR>
 __global__ void __launch_bounds__(kThreads, 1) tree_packed_kernel(const __grid_constant__ Args a)
@@ -1251,13 +1251,15 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // 64 query rows a tile feed the tensor core best.  Up to 32 rows, and problems of few such tiles an
 // SM, run in half tiles: more SMs share the work, the softmax, query image and epilogue of each are
 // half as long, and so are the partials, which cost the more the fewer units the SMs share (us in
-// half and full tiles: one unit of 64 rows, 256 tiles 25.4 / 37.1, 512 31.3 / 40.2, 768 39.6 / 38.3;
-// two units, 512 tiles 29.8 / 29.9, 1024 43.6 / 37.5; 16 units, 256 32.9 / 33.5, 512 39.2 / 36.8).
+// half and full tiles: one unit of 64 rows, 512 tiles 31.0 / 44.0, 896 42.1 / 48.0, 1280 52.3 / 49.1; two
+// units, 512 tiles 28.9 / 32.7, 640 32.9 / 32.2, 1024 42.3 / 40.4; four, 384 28.2 / 27.6, 512 30.1 / 30.1; 16,
+// 256 32.4 / 32.9, 512 38.4 / 36.3; 32, 320 32.0 / 33.1, 448 35.6 / 35.4).  The tiles are those of
+// max_seq_len, the host's bound: shorter sequences under a generous bound run in full tiles.
 int tile_rows(const kvq_mla_tree_problem& p)
 {
     const int64_t rows = (int64_t)p.n_q * p.n_heads, tiles = ((int64_t)p.max_seq_len + kRT - 1) / kRT;
     const int64_t units = std::max<int64_t>(1, p.n_seq * ((rows + 63) / 64));
-    return rows <= 32 || units * tiles <= 2 * sm_count() * (units + 1) / units ? 32 : 64;
+    return rows <= 32 || units * tiles <= 2 * sm_count() * (units + 2) / units ? 32 : 64;
 }
 
 int64_t max_units(const kvq_mla_tree_problem& p)
