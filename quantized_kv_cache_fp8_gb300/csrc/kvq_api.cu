@@ -228,8 +228,8 @@ int kvq_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t l
     if (!aligned(c_lat, 16) || !aligned(k_rope, 16) || ldx % per16 != 0 || ldr % per16 != 0)
         return fail(KVQ_EALIGN, "%s: input rows not 16-byte aligned", E);
     if (!aligned(cache->lat, 16) || !aligned(cache->rope, 16) || !aligned(cache->lat_scale, 4) ||
-        !aligned(cache->rope_scale, 4) || !aligned(slot, 4) || (rot && !aligned(sign_bits, 4)))
-        return fail(KVQ_EALIGN, "%s: cache planes, slots or signs misaligned", E);
+        !aligned(cache->rope_scale, 4) || !aligned(slot, 4) || (rot && !aligned(sign_bits, 4)) || !aligned(dev_status, 4))
+        return fail(KVQ_EALIGN, "%s: cache planes, slots, signs or dev_status misaligned", E);
     return cuda_status(kvq::launch_append_mla(c_lat, ldx, k_rope, ldr, x_type == KVQ_WEIGHT_BF16, rows, slot, fmt,
                                               sign_bits, *cache, dev_status, (cudaStream_t)stream), E);
 }

@@ -508,6 +508,9 @@ int kvq_accept_mla(const kvq_mla_accept_desc* d, uint32_t* dev_status, kvq_strea
         return set_last_error(KVQ_EINVAL, "%s: NULL pointer", E);
     if (!aligned(c.lat, 16) || !aligned(c.rope, 16) || !aligned(c.lat_scale, 4) || !aligned(c.rope_scale, 4))
         return set_last_error(KVQ_EALIGN, "%s: cache planes misaligned", E);
+    for (const void* q : {(const void*)d->seq_len, (const void*)d->n_node, (const void*)d->path, (const void*)d->n_acc,
+                          (const void*)d->new_len, (const void*)d->block_table, (const void*)dev_status})
+        if (!aligned(q, 4)) return set_last_error(KVQ_EALIGN, "%s: an array is not 4-byte aligned", E);
     AcceptArgs a{*d, dev_status, d->fmt == KVQ_FMT_FP8 ? kDLat : kDLat * rotated_bits(d->fmt) / 8};
     accept_mla_kernel<<<d->n_seq, kAccThreads, 0, (cudaStream_t)stream>>>(a);
     return cuda_status(cudaGetLastError(), E);

@@ -279,6 +279,9 @@ int validate_tree(const kvq_mla_tree_problem* p, const char* E)
     if (!aligned(p->q_lat, 16) || !aligned(p->q_rope, 16) || p->ldq_lat % 8 != 0 || p->ldq_rope % 8 != 0)
         return set_last_error(KVQ_EALIGN, "%s: query rows not 16-byte aligned", E);
     if (!aligned(p->mask, 8)) return set_last_error(KVQ_EALIGN, "%s: mask not 8-byte aligned", E);
+    for (const void* q : {(const void*)p->seq_len, (const void*)p->n_node, (const void*)p->block_table,
+                          (const void*)(rotated_format(p->fmt) ? p->signs : nullptr)})
+        if (!aligned(q, 4)) return set_last_error(KVQ_EALIGN, "%s: an array is not 4-byte aligned", E);
     return KVQ_OK;
 }
 
@@ -385,7 +388,8 @@ int kvq_mla_tree_decode(const kvq_mla_tree_problem* p, void* out, float* lse, vo
     if (int st = validate_tree(p, E)) return st;
     if (p->n_seq == 0) return KVQ_OK;
     if (!out) return set_last_error(KVQ_EINVAL, "%s: NULL out", E);
-    if (!aligned(out, 16) || !aligned(lse, 4)) return set_last_error(KVQ_EALIGN, "%s: out/lse misaligned", E);
+    if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(dev_status, 4))
+        return set_last_error(KVQ_EALIGN, "%s: out/lse/dev_status misaligned", E);
     const bool packed = packed_form(*p);
     TreePlan t;
     if (!packed) plan_tree(*p, t);

@@ -139,6 +139,23 @@ def test_accept_refuses_sequences_on_the_same_rows(kvq):
         assert kvq.lib().kvq_accept_mla(C.byref(d), None, None) == 1 and reason in kvq.lib().kvq_last_error()
 
 
+def test_misaligned_arrays_are_refused(kvq):
+    """Every 32-bit array that a kernel would read at a misaligned address."""
+    L = kvq.lib()
+    tree_call = lambda st=None, **kw: L.kvq_mla_tree_decode(C.byref(tree(kvq, **kw)), FAKE, None, None, 0, st, None)
+    for bad in (dict(seq_len=FAKE + 2), dict(n_node=FAKE + 1), dict(block_table=FAKE + 3), dict(fmt=2, signs=FAKE + 2),
+                dict(st=FAKE + 2)):
+        assert tree_call(**bad) == 4, bad
+    assert tree_call(signs=FAKE + 2) == 5                 # fp8: no signs; the workspace is missing
+    base = dict(n_seq=2, n_q=16, fmt=1, seq_len=FAKE, n_node=FAKE, path=FAKE, n_acc=FAKE, new_len=FAKE, block_table=FAKE,
+                max_pages=8, page_size=20, seq_stride_rows=0, cache=kvq.MlaCache(FAKE, FAKE, FAKE, FAKE, 100))
+    for name in ("seq_len", "n_node", "path", "n_acc", "new_len", "block_table"):
+        assert L.kvq_accept_mla(C.byref(fill(kvq.AcceptDesc(), base, {name: FAKE + 2})), None, None) == 4, name
+    assert L.kvq_accept_mla(C.byref(fill(kvq.AcceptDesc(), base, {})), FAKE + 2, None) == 4
+    c = kvq.MlaCache(FAKE, FAKE, FAKE, FAKE, 100)
+    assert L.kvq_append_mla(FAKE, 512, FAKE, 64, 0, 4, FAKE, 1, None, C.byref(c), FAKE + 2, None) == 4
+
+
 def test_faults_reach_the_new_entries(kvq):
     L = kvq.lib()
     calls = {"kvq_resize_pages": lambda: L.kvq_resize_pages(None, None, None),
