@@ -61,7 +61,9 @@ enum {
                                 the pool                                               */
     KVQ_DEV_TIMEOUT = 4u,    /* a bounded device wait expired                          */
     KVQ_DEV_BAD_FORMAT = 8u, /* a per-sequence format the kernel in use cannot read    */
-    KVQ_DEV_NO_PAGE = 16u    /* kvq_resize_pages: no free page, or no room in a table  */
+    KVQ_DEV_NO_PAGE = 16u,   /* kvq_resize_pages: no free page, or no room in a table;
+                                kvq_fork_pages: no free page                            */
+    KVQ_DEV_BAD_VALUE = 32u  /* kvq_beam_select: a NaN or +inf logit or score           */
 };
 
 typedef enum kvq_format {
@@ -72,7 +74,8 @@ typedef enum kvq_format {
     KVQ_FMT_TQ3 = 5          /* rotated tier, 3-bit codes (8 levels) + fp32 radius      */
 } kvq_format;
 
-/* element type of a projection weight matrix, and of the rows that kvq_append_mla takes */
+/* element type of a projection weight matrix, of the rows that kvq_append_mla and kvq_append_kv8
+   take and of the logits that kvq_beam_select takes */
 typedef enum kvq_weight_type {
     KVQ_WEIGHT_F32 = 0,      /* fp32                                                   */
     KVQ_WEIGHT_BF16 = 1      /* bfloat16 (the upper half of an fp32 pattern; widened
@@ -450,7 +453,8 @@ int kvq_mla_decode_noalloc(const kvq_mla_problem* p, float* out, float* lse,
  * pages (KVQ_DEV_BAD_PAGE).  Negative lengths count as 0, *n_free and n_held outside their
  * arrays are clamped (KVQ_DEV_BAD_INDEX); a page id outside [0, n_pages) gets slot -1
  * (KVQ_DEV_BAD_PAGE).  List entries at and above the new top that no page was pushed to stay as
- * they were.  The page ids of list and tables are distinct: the caller sees to that.
+ * they were.  The page ids of list and tables are distinct: the caller sees to that.  (Tables that
+ * share pages, as kvq_fork_pages makes them, may grow; a shared page must not be given back here.)
  */
 typedef struct kvq_page_plan {
     int32_t n_seq;                  /* 0 .. 65535                                       */
@@ -577,6 +581,244 @@ typedef struct kvq_mla_accept_desc {
 } kvq_mla_accept_desc;
 
 int kvq_accept_mla(const kvq_mla_accept_desc* d, uint32_t* dev_status, kvq_stream_t stream);
+
+/* ------------------------------------------------------------------------------------
+ * Beam search and parallel samples over a paged fp8 K/V cache.  One step is
+ *     kvq_resize_pages (the new tokens' pages and pool rows), kvq_append_kv8 (their K/V rows),
+ *     kvq_kv8_decode (attention; these two once a layer), kvq_beam_select (the best
+ *     continuations and their parents), kvq_fork_pages (the block tables follow the parents:
+ *     pages are shared, copied and freed) and kvq_copy_pages (those copies; once for all
+ *     layers, or layer by layer).
+ * Every quantity that varies from step to step is read from device memory, so a captured
+ * graph of the step can be replayed.
+ * ------------------------------------------------------------------------------------ */
+
+/* Planes of a paged fp8 K/V cache of a grouped-query model, KV head by KV head. */
+typedef struct kvq_kv8_cache {
+    uint8_t* k;                     /* device [n_kv][n_rows][head_dim] e4m3 codes         */
+    float*   k_scale;               /* device [n_kv][n_rows]                            */
+    uint8_t* v;                     /* as k                                             */
+    float*   v_scale;
+    int64_t  n_rows;                /* rows in the pool                                  */
+    int32_t  n_kv, head_dim;        /* head_dim: 64, 128 or 256                          */
+} kvq_kv8_cache;
+
+/*
+ * Paged append of K/V rows: for row r and KV head h, k[r][h] and v[r][h] are encoded as
+ * kvq_encode_fp8 encodes a row of head_dim (codes and scale the same bytes) into pool row
+ * slot[r] of head h's planes.  Slots as in kvq_append_mla: a negative one skips the row, one
+ * of n_rows or more skips it and sets KVQ_DEV_BAD_PAGE; the others must differ from one
+ * another.
+ *   k, v   device [rows] x ld_row, heads ld_head apart, of x_type (bfloat16 is widened
+ *          exactly): slices of a fused projection's output are read in place
+ *   slot   device i32 [rows]
+ * k, v and both strides 16-byte aligned, code planes 16-byte (KVQ_EALIGN otherwise).  Errors:
+ * KVQ_EINVAL for rows < 0, n_kv < 1 or > 65535, another head_dim or x_type, a head stride below head_dim, a
+ * negative row stride, or a NULL pointer.  rows == 0 is a no-op.  One kernel launch.
+ */
+int kvq_append_kv8(const void* k, int64_t k_ld_row, int64_t k_ld_head, const void* v, int64_t v_ld_row,
+                   int64_t v_ld_head, int x_type, int64_t rows, const int32_t* slot,
+                   const kvq_kv8_cache* cache, uint32_t* dev_status, kvq_stream_t stream);
+
+/*
+ * Decode attention of one new token a sequence over a paged fp8 K/V cache, grouped-query:
+ * query head h reads KV head g = h / (n_qh / n_kv).  With L = seq_len[s] (clamped to
+ * [0, max_seq_len]) the token sees the rows max(0, L - window) <= t < L (window 0: t < L), and
+ *     s_t = sm_scale * q . (kcode_t * kscale_t),  out = sum_t softmax(s)_t vcode_t * vscale_t,
+ *     lse = log sum_t exp(s_t)
+ * A sequence that sees no row gets out = 0 and lse = -inf.  A page that is missing or outside
+ * the pool sets KVQ_DEV_BAD_PAGE and its rows are skipped; rows of a page past L may hold
+ * anything.  Scores, the softmax's maximum and sum, the sums over rows and lse are fp32; a
+ * query element is exact down to 2^-31 of its head's largest, within 2^-39 of that below; the
+ * weight that multiplies a V row's codes (the row's scale in it) is rounded to binary16 against the largest
+ * of its part of the rows: within 2^-11 of itself or, if that is more, 2^-24 of that largest.  A query head
+ * that holds a NaN or an infinity gets NaN (if it sees anything), and touches no other head.
+ * The rows are read once by a part of the grid each, and the parts' results joined in a fixed
+ * order: the same call gives the same bits.
+ */
+typedef struct kvq_kv8_problem {
+    int32_t n_seq;                  /* 0 .. 65535                                       */
+    int32_t n_qh;                   /* query heads, a multiple of cache.n_kv             */
+    int32_t max_seq_len;            /* host bound on every seq_len, 0 .. 2^30            */
+    int32_t window;                 /* rows seen at most; 0: all                         */
+    const int32_t* seq_len;         /* device [n_seq]: rows held, the new token's included */
+    const int32_t* block_table;     /* device [n_seq][max_pages] pool page ids, or NULL */
+    int32_t max_pages, page_size;
+    int64_t seq_stride_rows;        /* no block table: seq i row t = pool row i*stride+t */
+    kvq_kv8_cache cache;
+    const void* q;                  /* device bf16 [n_seq] x ldq, heads head_dim apart   */
+    int64_t ldq;                    /* elements between sequences: a multiple of 8       */
+    float sm_scale;                 /* finite                                           */
+} kvq_kv8_problem;
+
+/* Bytes of workspace kvq_kv8_decode needs for this problem (0 if invalid, or if none). */
+size_t kvq_kv8_decode_workspace(const kvq_kv8_problem* p);
+
+/*
+ *   out        device bf16 [n_seq][n_qh][head_dim], 16-byte aligned
+ *   lse        device fp32 [n_seq][n_qh] or NULL (natural log)
+ *   workspace  device, >= kvq_kv8_decode_workspace(p) bytes, 256-byte aligned; not shared by
+ *              calls that may overlap (streams, captured graphs)
+ *   dev_status device u32 or NULL
+ */
+int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* workspace, size_t ws_bytes,
+                   uint32_t* dev_status, kvq_stream_t stream);
+
+/*
+ * Beam search's selection.  Request r has n_beam beams; beam b has the running score
+ * score[r][b] and the logits x = logits[r][b][0 .. vocab - 1].  Its candidates are the tokens t
+ * with x_t > -inf, of value
+ *     score[r][b] + x_t - log sum_u exp(x_u),
+ * and, where finished[r][b] is not 0, the token `pad` alone, of value score[r][b].  A beam whose
+ * score is -inf has none; one with a NaN or +inf among its logits (an unfinished beam's) or as its
+ * score has none either, and sets KVQ_DEV_BAD_VALUE.  The n_out candidates of the largest
+ * values are written in descending order, equal ones by ascending (beam, token); values of one beam
+ * are compared by their logits, those of different beams before they are rounded to fp32 (the sums
+ * are kept in 64 bits).  Of each:
+ *     out_score   its value
+ *     out_token   its token
+ *     out_parent  the index r * n_beam + b of its beam (kvq_fork_pages' parent)
+ *     out_finished  1 if finished[r][b] or the token is eos (eos -1: none is), else 0
+ * Places without a candidate get score -inf, token -1, parent -1, finished 0.  Where n_out ==
+ * n_beam, out_score may be score and out_finished may be finished (a step in place).
+ */
+typedef struct kvq_beam_problem {
+    int32_t n_req;                  /* 0 .. 65535                                       */
+    int32_t n_beam;                 /* 1 .. 64                                          */
+    int32_t vocab;                  /* 1 .. 2^24                                        */
+    int32_t n_out;                  /* 1 .. 128                                         */
+    int32_t x_type;                 /* kvq_weight_type of the logits                     */
+    int32_t eos, pad;               /* eos: a token or -1; pad: any                      */
+    const void* logits;             /* device [n_req * n_beam] rows of ld elements        */
+    int64_t ld;                     /* >= vocab                                         */
+    const float* score;             /* device [n_req][n_beam]                           */
+    const int32_t* finished;        /* device [n_req][n_beam] or NULL: none is           */
+    float* out_score;               /* device [n_req][n_out]                            */
+    int32_t* out_token;             /* device [n_req][n_out]                            */
+    int32_t* out_parent;            /* device [n_req][n_out]                            */
+    int32_t* out_finished;          /* device [n_req][n_out] or NULL                    */
+} kvq_beam_problem;
+
+/* Bytes of workspace kvq_beam_select needs for this problem (0 if invalid). */
+size_t kvq_beam_select_workspace(const kvq_beam_problem* p);
+
+/* workspace: as in kvq_kv8_decode. */
+int kvq_beam_select(const kvq_beam_problem* p, void* workspace, size_t ws_bytes, uint32_t* dev_status,
+                    kvq_stream_t stream);
+
+/*
+ * Fork, reorder and release: sequence s becomes the first len_s rows of sequence parent[s] as it
+ * was before the call; parent -1 releases s (len_s = 0).  len_s = seq_len[parent[s]], at most
+ * keep_len[s] if given.  Several sequences may have the same parent, and tables may share
+ * pages already.
+ *   1. A page that len_s covers whole is shared: every sequence that holds it lists it.
+ *   2. A last page that len_s covers in part is written by s next, so it must be its own.  It
+ *      stays with the lowest such s if no sequence holds it as a whole page; each other s gets a
+ *      free page, and copy_* an entry: page copy_src[i] to page copy_dst[i], its first
+ *      copy_rows[i] rows.  Entries are in the order of s, *n_copy of them, -1 behind.
+ *   3. Pages of the tables before the call that no sequence holds after it go back to the free
+ *      list, the highest page id first; then the copies' pages are popped from its top, the
+ *      lowest s first (so a page given back may be one of them).
+ * When the list has no page left, s and every later sequence that needs one loses the rows of its last page
+ * (KVQ_DEV_NO_PAGE).  The copies' sources are pages that some sequence still holds and no destination, so the copies
+ * may run in any order.  Table entries between the new and the old n_held become -1.
+ *   seq_len     in: rows held; out: len_s.  Below 0, or beyond the pages held: clamped
+ *               (KVQ_DEV_BAD_INDEX, KVQ_DEV_BAD_PAGE)
+ *   parent      outside [-1, n_seq): as -1 (KVQ_DEV_BAD_INDEX)
+ *   n_held, *n_free outside their arrays are clamped (KVQ_DEV_BAD_INDEX); a page id outside
+ *   [0, n_pages) becomes -1 in the new table (KVQ_DEV_BAD_PAGE); a push past the end of the list is dropped
+ *   (KVQ_DEV_BAD_PAGE).
+ * Pages shared with tables outside the call must not be released or truncated by it.  A page of the
+ * free list must not be in a table.  While tables share pages, kvq_resize_pages may let
+ * them grow, but rows are given back with this call (keep_len), which knows who else holds a page.
+ */
+typedef struct kvq_fork_plan {
+    int32_t n_seq;                  /* 0 .. 65535                                       */
+    int32_t max_pages, page_size;   /* max_pages: 1 .. 2^20                              */
+    int32_t n_pages;                /* pages of the pool = entries of free_list          */
+    const int32_t* parent;          /* device [n_seq]                                   */
+    const int32_t* keep_len;        /* device [n_seq] (negative: 0) or NULL              */
+    int32_t* block_table;           /* device [n_seq][max_pages], updated                */
+    int32_t* n_held;                /* device [n_seq], updated                          */
+    int32_t* free_list;             /* device [n_pages], updated                        */
+    int32_t* n_free;                /* device [1], updated                              */
+    int32_t* seq_len;               /* device [n_seq], updated                          */
+    int32_t* copy_src;              /* device [n_seq]                                   */
+    int32_t* copy_dst;              /* device [n_seq]                                   */
+    int32_t* copy_rows;             /* device [n_seq]                                   */
+    int32_t* n_copy;                /* device [1]                                       */
+} kvq_fork_plan;
+
+/* Bytes of workspace kvq_fork_pages needs for this plan (0 if invalid). */
+size_t kvq_fork_pages_workspace(const kvq_fork_plan* p);
+
+/* workspace: as in kvq_kv8_decode.  One kernel launch. */
+int kvq_fork_pages(const kvq_fork_plan* p, void* workspace, size_t ws_bytes, uint32_t* dev_status,
+                   kvq_stream_t stream);
+
+/*
+ * Compaction: the U pages that the tables hold move to the page ids 0 .. U - 1.  The i-th
+ * held page of id U or more (ascending) moves to the i-th page below U that no table holds;
+ * pages below U stay.  new_table is the block table with the new ids, -1 behind a sequence's
+ * pages; it may be block_table.  copy_* as in kvq_fork_pages, in ascending order of the sources, every
+ * copy_rows entry page_size; sources and destinations are disjoint.  free_list becomes
+ * n_pages - 1, ..., U + 1, U (U on top), -1 behind; *n_free = n_pages - U, *n_used = U.
+ * The tables of every sequence that holds pages of the pool must be in the call: any other page is
+ * taken to be free.  n_held outside [0, max_pages] is clamped (KVQ_DEV_BAD_INDEX), a page id outside
+ * [0, n_pages) becomes -1 (KVQ_DEV_BAD_PAGE).
+ */
+typedef struct kvq_compact_plan {
+    int32_t n_seq;                  /* 0 .. 65535                                       */
+    int32_t max_pages, page_size;   /* max_pages: 1 .. 2^20                              */
+    int32_t n_pages;                /* pages of the pool = entries of free_list          */
+    int32_t max_copy;               /* entries of copy_*: n_pages / 2 or more            */
+    const int32_t* block_table;     /* device [n_seq][max_pages]                        */
+    const int32_t* n_held;          /* device [n_seq]                                   */
+    int32_t* new_table;             /* device [n_seq][max_pages]                        */
+    int32_t* free_list;             /* device [n_pages]                                 */
+    int32_t* n_free;                /* device [1]                                       */
+    int32_t* n_used;                /* device [1]                                       */
+    int32_t* copy_src;              /* device [max_copy]                                */
+    int32_t* copy_dst;              /* device [max_copy]                                */
+    int32_t* copy_rows;             /* device [max_copy]                                */
+    int32_t* n_copy;                /* device [1]                                       */
+} kvq_compact_plan;
+
+/* Bytes of workspace kvq_compact_pages needs for this plan (0 if invalid). */
+size_t kvq_compact_pages_workspace(const kvq_compact_plan* p);
+
+/* workspace: as in kvq_kv8_decode.  One kernel launch. */
+int kvq_compact_pages(const kvq_compact_plan* p, void* workspace, size_t ws_bytes, uint32_t* dev_status,
+                      kvq_stream_t stream);
+
+/* A plane of a pool: n_outer arrays of n_rows rows of row_bytes bytes, outer_stride bytes apart. */
+typedef struct kvq_plane {
+    void*   base;
+    int64_t row_bytes;              /* >= 1                                             */
+    int64_t n_rows;
+    int64_t n_outer;                /* >= 1 (a plane a KV head: n_kv)                    */
+    int64_t outer_stride;           /* >= n_rows * row_bytes where n_outer > 1           */
+} kvq_plane;
+
+/*
+ * The copies of kvq_fork_pages or kvq_compact_pages: for i < *n_copy (clamped to [0, max_copy]),
+ * the first copy_rows[i] rows (clamped to [0, page_size]) of page copy_src[i] go to page copy_dst[i],
+ * in every plane and outer array, byte for byte.  Negative pages are passed over; a page
+ * that ends behind n_rows is skipped (KVQ_DEV_BAD_PAGE).  No destination may be a
+ * source or another destination.  Rows behind copy_rows keep their bytes.  One kernel launch for all planes.
+ */
+typedef struct kvq_page_copy {
+    const kvq_plane* planes;        /* HOST [n_planes]                                  */
+    int32_t n_planes;               /* 1 .. 64                                          */
+    int32_t page_size;
+    int32_t max_copy;               /* entries of copy_*                                */
+    const int32_t* copy_src;        /* device [max_copy]                                */
+    const int32_t* copy_dst;        /* device [max_copy]                                */
+    const int32_t* copy_rows;       /* device [max_copy]                                */
+    const int32_t* n_copy;          /* device [1]                                       */
+} kvq_page_copy;
+
+int kvq_copy_pages(const kvq_page_copy* d, uint32_t* dev_status, kvq_stream_t stream);
 
 /*
  * q4_0 paged decode attention, grouped-query, head_dim 256 — Strata PR #2533, the qsa

@@ -27,6 +27,11 @@ __all__ = [
     "TreeProblem", "make_tree_problem", "kvq_mla_tree_decode", "kvq_mla_tree_decode_workspace",
     "kvq_mla_tree_decode_kernel", "TREE_PACKED", "TREE_PER_QUERY",
     "AcceptDesc", "make_accept", "kvq_accept_mla",
+    "Kv8Cache", "kvq_append_kv8", "Kv8Problem", "make_kv8_problem", "kvq_kv8_decode", "kvq_kv8_decode_workspace",
+    "BeamProblem", "make_beam_problem", "kvq_beam_select", "kvq_beam_select_workspace", "DEV_BAD_VALUE",
+    "ForkPlan", "make_fork_plan", "kvq_fork_pages", "kvq_fork_pages_workspace",
+    "CompactPlan", "make_compact_plan", "kvq_compact_pages", "kvq_compact_pages_workspace",
+    "PageCopy", "make_page_copy", "kvq_copy_pages",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +44,7 @@ IMPL_AUTO, IMPL_SIMT, IMPL_TC, IMPL_MMA, IMPL_TC16, IMPL_TCF8 = 0, 1, 2, 3, 4, 5
 IMPL_BY_FMT = 6   # kvq_mla_decode_kernel only: fp8 sequences on IMPL_TCF8, TQ4 ones on IMPL_TC
 TREE_PACKED, TREE_PER_QUERY = 1, 2       # forms of kvq_mla_tree_decode
 DEV_BAD_INDEX, DEV_BAD_PAGE, DEV_TIMEOUT, DEV_BAD_FORMAT, DEV_NO_PAGE = 1, 2, 4, 8, 16
+DEV_BAD_VALUE = 32
 STATUS = {0: "KVQ_OK", 1: "KVQ_EINVAL", 2: "KVQ_ENOTPOW2", 3: "KVQ_EFORMAT", 4: "KVQ_EALIGN",
           5: "KVQ_EWORKSPACE", 6: "KVQ_ECUDA", 7: "KVQ_EFAULT_INJECTED", 8: "KVQ_EMISMATCH",
           9: "KVQ_EIO"}
@@ -53,7 +59,10 @@ EXPORTS = ["kvq_version", "kvq_status_string", "kvq_last_error", "kvq_set_fault"
            "kvq_cache_probe", "kvq_cache_save", "kvq_cache_save_f32", "kvq_cache_append",
            "kvq_cache_load_workspace", "kvq_cache_load",
            "kvq_resize_pages", "kvq_append_mla", "kvq_mla_tree_decode_kernel",
-           "kvq_mla_tree_decode_workspace", "kvq_mla_tree_decode", "kvq_accept_mla"]
+           "kvq_mla_tree_decode_workspace", "kvq_mla_tree_decode", "kvq_accept_mla",
+           "kvq_append_kv8", "kvq_kv8_decode_workspace", "kvq_kv8_decode",
+           "kvq_beam_select_workspace", "kvq_beam_select", "kvq_fork_pages_workspace", "kvq_fork_pages",
+           "kvq_compact_pages_workspace", "kvq_compact_pages", "kvq_copy_pages"]
 
 
 class KvqError(RuntimeError):
@@ -121,6 +130,44 @@ class AcceptDesc(C.Structure):
                 ("path", _p), ("n_acc", _p), ("new_len", _p), ("block_table", _p),
                 ("max_pages", _i32), ("page_size", _i32), ("seq_stride_rows", _i64),
                 ("cache", MlaCache)]
+
+
+class Kv8Cache(C.Structure):
+    _fields_ = [("k", _p), ("k_scale", _p), ("v", _p), ("v_scale", _p), ("n_rows", _i64), ("n_kv", _i32),
+                ("head_dim", _i32)]
+
+
+class Kv8Problem(C.Structure):
+    _fields_ = [("n_seq", _i32), ("n_qh", _i32), ("max_seq_len", _i32), ("window", _i32), ("seq_len", _p),
+                ("block_table", _p), ("max_pages", _i32), ("page_size", _i32), ("seq_stride_rows", _i64),
+                ("cache", Kv8Cache), ("q", _p), ("ldq", _i64), ("sm_scale", _f32)]
+
+
+class BeamProblem(C.Structure):
+    _fields_ = [("n_req", _i32), ("n_beam", _i32), ("vocab", _i32), ("n_out", _i32), ("x_type", _i32), ("eos", _i32),
+                ("pad", _i32), ("logits", _p), ("ld", _i64), ("score", _p), ("finished", _p), ("out_score", _p),
+                ("out_token", _p), ("out_parent", _p), ("out_finished", _p)]
+
+
+class ForkPlan(C.Structure):
+    _fields_ = [("n_seq", _i32), ("max_pages", _i32), ("page_size", _i32), ("n_pages", _i32), ("parent", _p),
+                ("keep_len", _p), ("block_table", _p), ("n_held", _p), ("free_list", _p), ("n_free", _p),
+                ("seq_len", _p), ("copy_src", _p), ("copy_dst", _p), ("copy_rows", _p), ("n_copy", _p)]
+
+
+class CompactPlan(C.Structure):
+    _fields_ = [("n_seq", _i32), ("max_pages", _i32), ("page_size", _i32), ("n_pages", _i32), ("max_copy", _i32),
+                ("block_table", _p), ("n_held", _p), ("new_table", _p), ("free_list", _p), ("n_free", _p),
+                ("n_used", _p), ("copy_src", _p), ("copy_dst", _p), ("copy_rows", _p), ("n_copy", _p)]
+
+
+class Plane(C.Structure):
+    _fields_ = [("base", _p), ("row_bytes", _i64), ("n_rows", _i64), ("n_outer", _i64), ("outer_stride", _i64)]
+
+
+class PageCopy(C.Structure):
+    _fields_ = [("planes", C.POINTER(Plane)), ("n_planes", _i32), ("page_size", _i32), ("max_copy", _i32),
+                ("copy_src", _p), ("copy_dst", _p), ("copy_rows", _p), ("n_copy", _p)]
 
 
 class CacheInfo(C.Structure):
@@ -209,6 +256,18 @@ def _declare(L):
     L.kvq_mla_tree_decode.argtypes = [C.POINTER(TreeProblem), _p, _p, _p, C.c_size_t, _p, _p]
     L.kvq_accept_mla.restype = C.c_int
     L.kvq_accept_mla.argtypes = [C.POINTER(AcceptDesc), _p, _p]
+    L.kvq_append_kv8.restype = C.c_int
+    L.kvq_append_kv8.argtypes = [_p, _i64, _i64, _p, _i64, _i64, C.c_int, _i64, _p, C.POINTER(Kv8Cache), _p, _p]
+    L.kvq_kv8_decode_workspace.restype = C.c_size_t
+    L.kvq_kv8_decode_workspace.argtypes = [C.POINTER(Kv8Problem)]
+    L.kvq_kv8_decode.restype = C.c_int
+    L.kvq_kv8_decode.argtypes = [C.POINTER(Kv8Problem), _p, _p, _p, C.c_size_t, _p, _p]
+    for name, plan in (("kvq_beam_select", BeamProblem), ("kvq_fork_pages", ForkPlan), ("kvq_compact_pages", CompactPlan)):
+        f, w = getattr(L, name), getattr(L, name + "_workspace")
+        f.restype, f.argtypes = C.c_int, [C.POINTER(plan), _p, C.c_size_t, _p, _p]
+        w.restype, w.argtypes = C.c_size_t, [C.POINTER(plan)]
+    L.kvq_copy_pages.restype = C.c_int
+    L.kvq_copy_pages.argtypes = [C.POINTER(PageCopy), _p, _p]
     L.kvq_q4_decode_workspace.restype = C.c_size_t
     L.kvq_q4_decode_workspace.argtypes = [C.POINTER(Q4Problem)]
     L.kvq_q4_decode.restype = C.c_int
@@ -649,6 +708,241 @@ def make_accept(*, seq_len, path, n_acc, new_len, fmt, cache, n_node=None, block
 def kvq_accept_mla(d: AcceptDesc, dev_status=None, stream=None) -> None:
     status = _status_on(d._device, dev_status)
     _check(lib().kvq_accept_mla(C.byref(d), status, _stream_on(d._device, stream)))
+
+
+# --- beam search and samples over a paged fp8 K/V cache --------------------------------------
+
+def _kv8_cache(planes):
+    """The planes k, v uint8 [n_kv, rows, head_dim] and k_scale, v_scale float32 [n_kv, rows]."""
+    import torch
+    k, ks, v, vs = planes["k"], planes["k_scale"], planes["v"], planes["v_scale"]
+    kv, n, d = k.shape
+    two, u8, f32 = (kv, n), torch.uint8, torch.float32
+    if not (k.dtype is u8 and v.dtype is u8 and ks.dtype is f32 and vs.dtype is f32 and v.shape == k.shape and
+            ks.shape == two and vs.shape == two and k.is_contiguous() and v.is_contiguous() and
+            ks.is_contiguous() and vs.is_contiguous()):
+        _want("k", k, "uint8", kv, n, d)                       # (names the one at fault)
+        _want("v", v, "uint8", kv, n, d)
+        _want("k_scale", ks, "float32", kv, n)
+        _want("v_scale", vs, "float32", kv, n)
+    return Kv8Cache(k.data_ptr(), ks.data_ptr(), v.data_ptr(), vs.data_ptr(), n, kv, d)
+
+
+def _kv8_planes(planes):
+    return planes["k"], planes["k_scale"], planes["v"], planes["v_scale"]
+
+
+def kvq_append_kv8(k, v, slot_map, planes: dict, dev_status=None, stream=None) -> None:
+    """Encode rows k, v [rows, n_kv, head_dim] (both float32 or both bfloat16; rows and heads possibly
+    strided, as slices of a fused projection are) into the fp8 K/V planes at pool rows slot_map int32
+    [rows] (negative: skipped)."""
+    import torch
+    c = _kv8_cache(planes)
+    rows, kv, d = k.shape
+    kind = WEIGHT_F32 if k.dtype is torch.float32 else WEIGHT_BF16 if k.dtype is torch.bfloat16 else None
+    kr, kh, k1 = k.stride()
+    vr, vh, v1 = v.stride()
+    if kind is None or v.dtype is not k.dtype or v.shape != k.shape or kv != c.n_kv or d != c.head_dim or \
+            (rows and (k1 != 1 or v1 != 1)):
+        raise ValueError(f"k, v must be [rows, {c.n_kv}, {c.head_dim}], both float32 or both bfloat16")
+    if rows <= 1:                                          # (the stride of a single row or head is arbitrary)
+        kr = vr = kv * d
+    if kv == 1:
+        kh = vh = d
+    _want("slot_map", slot_map, "int32", rows)
+    dv = _one_device(k, v, slot_map, *_kv8_planes(planes))
+    status, stream = _status_on(dv, dev_status), _stream_on(dv, stream)
+    _check(lib().kvq_append_kv8(k.data_ptr(), kr, kh, v.data_ptr(), vr, vh, kind, rows, slot_map.data_ptr(), C.byref(c),
+                                status, stream))
+
+
+def make_kv8_problem(*, seq_len, q, sm_scale, max_seq_len, cache, block_table=None, page_size=0, seq_stride_rows=0,
+                     window=0) -> Kv8Problem:
+    """Fill a kvq_kv8_problem from torch tensors: q [n_seq, n_qh, head_dim] bfloat16 (sequences possibly
+    strided), cache the planes k, k_scale, v, v_scale.  The returned object keeps a reference to
+    every tensor it carries."""
+    import torch
+    c = _kv8_cache(cache)
+    n_seq, n_qh, d = q.shape
+    if q.dtype is not torch.bfloat16 or d != c.head_dim or q.stride(2) != 1 or (n_qh > 1 and q.stride(1) != d):
+        raise ValueError(f"q must be bfloat16 [n_seq, n_qh, {c.head_dim}] with contiguous heads")
+    _want("seq_len", seq_len, "int32", n_seq)
+    _want("block_table", block_table, "int32", n_seq, None)
+    p = Kv8Problem()
+    p.n_seq, p.n_qh, p.max_seq_len, p.window = n_seq, n_qh, int(max_seq_len), int(window)
+    p.seq_len = _ptr(seq_len)
+    if block_table is not None:
+        p.block_table, p.max_pages, p.page_size = _ptr(block_table), block_table.shape[1], int(page_size)
+    p.seq_stride_rows, p.cache = int(seq_stride_rows), c
+    p.q, p.ldq, p.sm_scale = _ptr(q), q.stride(0) if n_seq > 1 else n_qh * d, float(sm_scale)
+    p._keep = [seq_len, block_table, q, *_kv8_planes(cache)]
+    p._device = _one_device(*p._keep)
+    return p
+
+
+def kvq_kv8_decode_workspace(p: Kv8Problem) -> int:
+    return lib().kvq_kv8_decode_workspace(C.byref(p))
+
+
+def _scratch(d, t):
+    """The address and the bytes of a call's workspace `t` (or None) on device `d`."""
+    if t is None:
+        return None, 0
+    if t.get_device() != d:
+        raise ValueError(f"tensors on different devices: workspace on {t.device}")
+    if not t.is_contiguous():
+        raise ValueError("the workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
+def kvq_kv8_decode(p: Kv8Problem, out, lse=None, workspace=None, dev_status=None, stream=None) -> None:
+    """out bfloat16 [n_seq, n_qh, head_dim], lse float32 [n_seq, n_qh] or None."""
+    _want("out", out, "bfloat16", p.n_seq, p.n_qh, p.cache.head_dim)
+    _want("lse", lse, "float32", p.n_seq, p.n_qh)
+    d = _one_device(out, lse, p._keep[0])
+    ws, ws_bytes = _scratch(d, workspace)
+    status, stream = _status_on(d, dev_status), _stream_on(d, stream)
+    _check(lib().kvq_kv8_decode(C.byref(p), _ptr(out), _ptr(lse), ws, ws_bytes, status, stream))
+
+
+def make_beam_problem(*, logits, score, out_score, out_token, out_parent, finished=None, out_finished=None, eos=-1,
+                      pad=0) -> BeamProblem:
+    """Fill a kvq_beam_problem from torch tensors: logits [n_req, n_beam, vocab] float32 or bfloat16 (rows
+    evenly spaced), score float32 and finished int32 [n_req, n_beam], out_score float32 and out_token,
+    out_parent, out_finished int32 [n_req, n_out].  The returned object keeps a reference to every tensor it
+    carries."""
+    import torch
+    R, B, V = logits.shape
+    kind = WEIGHT_F32 if logits.dtype is torch.float32 else WEIGHT_BF16 if logits.dtype is torch.bfloat16 else None
+    ld = logits.stride(1) if B > 1 else logits.stride(0) if R > 1 else V
+    if kind is None or (V > 1 and logits.stride(2) != 1) or (R > 1 and logits.stride(0) != ld * B):
+        raise ValueError("logits must be float32 or bfloat16 [n_req, n_beam, vocab] with evenly spaced rows")
+    n_out = out_score.shape[-1]
+    for name, t, dt, w in (("score", score, "float32", B), ("finished", finished, "int32", B),
+                           ("out_score", out_score, "float32", n_out), ("out_token", out_token, "int32", n_out),
+                           ("out_parent", out_parent, "int32", n_out), ("out_finished", out_finished, "int32", n_out)):
+        _want(name, t, dt, R, w)
+    p = BeamProblem()
+    p.n_req, p.n_beam, p.vocab, p.n_out, p.x_type, p.eos, p.pad = R, B, V, n_out, kind, int(eos), int(pad)
+    p.logits, p.ld, p.score, p.finished = _ptr(logits), ld, _ptr(score), _ptr(finished)
+    p.out_score, p.out_token, p.out_parent = _ptr(out_score), _ptr(out_token), _ptr(out_parent)
+    p.out_finished = _ptr(out_finished)
+    p._keep = [logits, score, finished, out_score, out_token, out_parent, out_finished]
+    p._device = _one_device(*p._keep)
+    return p
+
+
+def kvq_beam_select_workspace(p: BeamProblem) -> int:
+    return lib().kvq_beam_select_workspace(C.byref(p))
+
+
+def kvq_beam_select(p: BeamProblem, workspace=None, dev_status=None, stream=None) -> None:
+    ws, ws_bytes = _scratch(p._device, workspace)
+    status, stream = _status_on(p._device, dev_status), _stream_on(p._device, stream)
+    _check(lib().kvq_beam_select(C.byref(p), ws, ws_bytes, status, stream))
+
+
+def make_fork_plan(*, parent, block_table, n_held, free_list, n_free, seq_len, page_size, copy_src, copy_dst, copy_rows,
+                   n_copy, keep_len=None) -> ForkPlan:
+    """Fill a kvq_fork_plan from int32 tensors: block_table [n_seq, max_pages], free_list [n_pages], n_free
+    and n_copy [1], the others [n_seq].  The returned object keeps a reference to every tensor it carries."""
+    n = parent.shape[0]
+    for name, t, shape in (("parent", parent, (n,)), ("keep_len", keep_len, (n,)), ("block_table", block_table, (n, None)),
+                           ("n_held", n_held, (n,)), ("free_list", free_list, (None,)), ("n_free", n_free, (1,)),
+                           ("seq_len", seq_len, (n,)), ("copy_src", copy_src, (n,)), ("copy_dst", copy_dst, (n,)),
+                           ("copy_rows", copy_rows, (n,)), ("n_copy", n_copy, (1,))):
+        _want(name, t, "int32", *shape)
+    p = ForkPlan()
+    p.n_seq, p.max_pages, p.page_size, p.n_pages = n, block_table.shape[1], int(page_size), free_list.shape[0]
+    p.parent, p.keep_len, p.block_table, p.n_held = _ptr(parent), _ptr(keep_len), _ptr(block_table), _ptr(n_held)
+    p.free_list, p.n_free, p.seq_len = _ptr(free_list), _ptr(n_free), _ptr(seq_len)
+    p.copy_src, p.copy_dst, p.copy_rows, p.n_copy = _ptr(copy_src), _ptr(copy_dst), _ptr(copy_rows), _ptr(n_copy)
+    p._keep = [parent, keep_len, block_table, n_held, free_list, n_free, seq_len, copy_src, copy_dst, copy_rows, n_copy]
+    p._device = _one_device(*p._keep)
+    return p
+
+
+def kvq_fork_pages_workspace(p: ForkPlan) -> int:
+    return lib().kvq_fork_pages_workspace(C.byref(p))
+
+
+def kvq_fork_pages(p: ForkPlan, workspace=None, dev_status=None, stream=None) -> None:
+    ws, ws_bytes = _scratch(p._device, workspace)
+    status, stream = _status_on(p._device, dev_status), _stream_on(p._device, stream)
+    _check(lib().kvq_fork_pages(C.byref(p), ws, ws_bytes, status, stream))
+
+
+def make_compact_plan(*, block_table, n_held, new_table, free_list, n_free, n_used, page_size, copy_src, copy_dst,
+                      copy_rows, n_copy) -> CompactPlan:
+    """Fill a kvq_compact_plan from int32 tensors: block_table and new_table [n_seq, max_pages] (possibly the
+    same), n_held [n_seq], free_list [n_pages], copy_* [n_pages / 2 or more], the others [1].  The returned
+    object keeps a reference to every tensor it carries."""
+    n, mp = block_table.shape
+    m = copy_src.shape[0]
+    for name, t, shape in (("block_table", block_table, (n, mp)), ("n_held", n_held, (n,)), ("new_table", new_table, (n, mp)),
+                           ("free_list", free_list, (None,)), ("n_free", n_free, (1,)), ("n_used", n_used, (1,)),
+                           ("copy_src", copy_src, (m,)), ("copy_dst", copy_dst, (m,)), ("copy_rows", copy_rows, (m,)),
+                           ("n_copy", n_copy, (1,))):
+        _want(name, t, "int32", *shape)
+    p = CompactPlan()
+    p.n_seq, p.max_pages, p.page_size, p.n_pages, p.max_copy = n, mp, int(page_size), free_list.shape[0], m
+    p.block_table, p.n_held, p.new_table = _ptr(block_table), _ptr(n_held), _ptr(new_table)
+    p.free_list, p.n_free, p.n_used = _ptr(free_list), _ptr(n_free), _ptr(n_used)
+    p.copy_src, p.copy_dst, p.copy_rows, p.n_copy = _ptr(copy_src), _ptr(copy_dst), _ptr(copy_rows), _ptr(n_copy)
+    p._keep = [block_table, n_held, new_table, free_list, n_free, n_used, copy_src, copy_dst, copy_rows, n_copy]
+    p._device = _one_device(*p._keep)
+    return p
+
+
+def kvq_compact_pages_workspace(p: CompactPlan) -> int:
+    return lib().kvq_compact_pages_workspace(C.byref(p))
+
+
+def kvq_compact_pages(p: CompactPlan, workspace=None, dev_status=None, stream=None) -> None:
+    ws, ws_bytes = _scratch(p._device, workspace)
+    status, stream = _status_on(p._device, dev_status), _stream_on(p._device, stream)
+    _check(lib().kvq_compact_pages(C.byref(p), ws, ws_bytes, status, stream))
+
+
+def _pool_planes(cache):
+    """(tensor, axis of the pool's rows) of every plane of a cache."""
+    if not isinstance(cache, dict):
+        return [(cache, 0)]                                    # a q4_0 pool [n_cells, heads, 144], or any rows
+    if "lat" in cache:
+        return [(t, 0) for t in _planes_of(cache)]
+    return [(t, 1) for t in _kv8_planes(cache)]
+
+
+def make_page_copy(*, caches, page_size, copy_src, copy_dst, copy_rows, n_copy) -> PageCopy:
+    """Fill a kvq_page_copy: `caches` lists what the copies are made in (64 planes at most): dictionaries of
+    MLA planes or of fp8 K/V planes, or pools as tensors with their rows along the first axis; copy_* int32
+    [max_copy] and n_copy int32 [1] as kvq_fork_pages or kvq_compact_pages wrote them.  The
+    returned object keeps a reference to every tensor it carries."""
+    m = copy_src.shape[0]
+    for name, t, shape in (("copy_src", copy_src, (m,)), ("copy_dst", copy_dst, (m,)), ("copy_rows", copy_rows, (m,)),
+                           ("n_copy", n_copy, (1,))):
+        _want(name, t, "int32", *shape)
+    planes = [x for c in caches for x in _pool_planes(c)]
+    d = PageCopy()
+    d._planes = (Plane * max(1, len(planes)))()
+    for at, (t, axis) in zip(d._planes, planes):
+        if not t.is_contiguous():
+            raise ValueError(f"a plane is not contiguous: {list(t.shape)}")
+        rows, size = t.shape[axis], t.element_size()
+        for n in t.shape[axis + 1:]:
+            size *= n
+        at.base, at.row_bytes, at.n_rows = _ptr(t), size, rows
+        at.n_outer, at.outer_stride = t.shape[0] if axis else 1, rows * size
+    d.planes, d.n_planes, d.page_size, d.max_copy = d._planes, len(planes), int(page_size), m
+    d.copy_src, d.copy_dst, d.copy_rows, d.n_copy = _ptr(copy_src), _ptr(copy_dst), _ptr(copy_rows), _ptr(n_copy)
+    d._keep = [copy_src, copy_dst, copy_rows, n_copy, *(t for t, _ in planes)]
+    d._device = _one_device(*d._keep)
+    return d
+
+
+def kvq_copy_pages(d: PageCopy, dev_status=None, stream=None) -> None:
+    status = _status_on(d._device, dev_status)
+    _check(lib().kvq_copy_pages(C.byref(d), status, _stream_on(d._device, stream)))
 
 
 # --- cache files ------------------------------------------------------------------------

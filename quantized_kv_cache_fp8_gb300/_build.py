@@ -32,6 +32,9 @@ UNITS = {
     "kvq_pages.cu": [],
     "kvq_tree.cu": [],
     "kvq_tree_packed.cu": [],
+    "kvq_kv8.cu": [],
+    "kvq_beam.cu": [],
+    "kvq_fork.cu": [],
 }
 
 

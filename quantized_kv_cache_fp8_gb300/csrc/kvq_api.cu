@@ -234,6 +234,33 @@ int kvq_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t l
                                               sign_bits, *cache, dev_status, (cudaStream_t)stream), E);
 }
 
+int kvq_append_kv8(const void* k, int64_t k_ld_row, int64_t k_ld_head, const void* v, int64_t v_ld_row,
+                   int64_t v_ld_head, int x_type, int64_t rows, const int32_t* slot,
+                   const kvq_kv8_cache* cache, uint32_t* dev_status, kvq_stream_t stream)
+{
+    const char* E = "kvq_append_kv8";
+    if (int st = injected(E)) return st;
+    if (rows < 0) return fail(KVQ_EINVAL, "%s: rows < 0", E);
+    if (x_type != KVQ_WEIGHT_F32 && x_type != KVQ_WEIGHT_BF16) return fail(KVQ_EINVAL, "%s: x_type %d", E, x_type);
+    if (!cache) return fail(KVQ_EINVAL, "%s: NULL cache", E);
+    const int d = cache->head_dim;
+    if (d != 64 && d != 128 && d != 256) return fail(KVQ_EINVAL, "%s: head_dim %d not 64, 128 or 256", E, d);
+    if (cache->n_kv < 1 || cache->n_kv > 65535) return fail(KVQ_EINVAL, "%s: n_kv outside [1, 65535]", E);
+    if (k_ld_row < 0 || v_ld_row < 0 || k_ld_head < d || v_ld_head < d)
+        return fail(KVQ_EINVAL, "%s: a head stride is smaller than head_dim, or a row stride negative", E);
+    if (rows == 0) return KVQ_OK;
+    if (!k || !v || !slot || !cache->k || !cache->k_scale || !cache->v || !cache->v_scale || cache->n_rows < 0)
+        return fail(KVQ_EINVAL, "%s: NULL pointer", E);
+    const int64_t per16 = x_type == KVQ_WEIGHT_BF16 ? 8 : 4;      // elements in 16 bytes
+    if (!aligned(k, 16) || !aligned(v, 16) || k_ld_row % per16 || v_ld_row % per16 || k_ld_head % per16 || v_ld_head % per16)
+        return fail(KVQ_EALIGN, "%s: input rows not 16-byte aligned", E);
+    if (!aligned(cache->k, 16) || !aligned(cache->v, 16) || !aligned(cache->k_scale, 4) || !aligned(cache->v_scale, 4) ||
+        !aligned(slot, 4) || !aligned(dev_status, 4))
+        return fail(KVQ_EALIGN, "%s: cache planes, slots or dev_status misaligned", E);
+    return cuda_status(kvq::launch_append_kv8(k, k_ld_row, k_ld_head, v, v_ld_row, v_ld_head, x_type == KVQ_WEIGHT_BF16,
+                                              rows, slot, *cache, dev_status, (cudaStream_t)stream), E);
+}
+
 int kvq_append_q4(const float* k, const float* v, int n_seq, const int32_t* pos0, int n_tok,
                   int n_heads, int head_dim, const int32_t* page_table, int max_pages,
                   int page_size, int64_t n_cells, uint8_t* k_pool, uint8_t* v_pool,

@@ -733,6 +733,101 @@ append_mla_kernel(const X* __restrict__ c_lat, int64_t ldx, const X* __restrict_
     }
 }
 
+// ------------------------------------------------------------------------------------
+// Paged append of a grouped-query model's K/V rows in fp8 (the bytes of encode_fp8_vec_rows): D / 8
+// lanes take the vector of one row, one of K and V and one KV head, 8 elements a lane (one 16-byte load of
+// bfloat16, two of fp32), 8-byte stores.  Vectors in the order of the rows' memory, kKvRun of them a group of
+// lanes at once, loads first.  Bound by the rows' bytes.
+// ------------------------------------------------------------------------------------
+constexpr int kKvRun = 4;
+
+struct AppendKv8Args {
+    const void *k, *v;
+    int64_t k_row, k_head, v_row, v_head;    // strides in elements
+    int64_t rows;
+    RowSlot row_of;
+    kvq_kv8_cache c;
+};
+
+template <int D, typename X>
+__global__ void __launch_bounds__(kCodecThreads) append_kv8_kernel(const AppendKv8Args a)
+{
+    constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes, kWords = sizeof(X) == 2 ? 1 : 2;
+    const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
+    const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+    const int64_t n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
+    const uint32_t per_row = 2u * (uint32_t)a.c.n_kv;
+    const int64_t n = a.rows * per_row;
+    for (int64_t i0 = warp * (kPerWarp * kKvRun); i0 < n; i0 += n_warps * (kPerWarp * kKvRun)) {
+        uint4 w[kKvRun][kWords];
+        int64_t at[kKvRun];                                // row of the planes, -1: none
+        bool is_v[kKvRun];
+#pragma unroll
+        for (int u = 0; u < kKvRun; ++u) {
+            const int64_t i = i0 + u * kPerWarp + sub;
+            at[u] = -1;
+            is_v[u] = false;
+            if (i >= n) continue;
+            const int64_t r = n <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / per_row) : i / per_row;
+            int h = (int)(i - r * per_row);
+            is_v[u] = h >= a.c.n_kv;
+            if (is_v[u]) h -= a.c.n_kv;
+            const int64_t slot = a.row_of(r);
+            if (slot < 0) continue;
+            at[u] = h * a.c.n_rows + slot;
+            const X* src = static_cast<const X*>(is_v[u] ? a.v : a.k) + r * (is_v[u] ? a.v_row : a.k_row) +
+                           h * (is_v[u] ? a.v_head : a.k_head);
+#pragma unroll
+            for (int e = 0; e < kWords; ++e) w[u][e] = __ldcs(reinterpret_cast<const uint4*>(src) + l * kWords + e);
+        }
+#pragma unroll
+        for (int u = 0; u < kKvRun; ++u) {
+            float f[8];
+            float amax = 0.0f;
+            if (at[u] >= 0) {
+#pragma unroll
+                for (int e = 0; e < kWords; ++e) {
+                    const uint32_t x[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (sizeof(X) == 2) {
+                            f[2 * j] = __uint_as_float(x[j] << 16);
+                            f[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                        } else {
+                            f[4 * e + j] = __uint_as_float(x[j]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+            }
+#pragma unroll
+            for (int m = kLanes / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
+            if (at[u] < 0) continue;
+            const float s = __fdiv_rn(amax, 448.0f);
+            uint2 c = make_uint2(0u, 0u);
+            if (amax != 0.0f) {
+                // the quotients of bfloat16 rows as in append_fp8_bf16_rows
+                const bool plain = sizeof(X) == 2 && s >= 0x1p-90f && s <= 0x1p90f;
+                if (plain) {
+                    const float y = __frcp_rn(s);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float q = __fmul_rn(f[j], y);
+                        f[j] = __fmaf_rn(-__fmaf_rn(q, s, -f[j]), y, q);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], s);
+                }
+                c = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+            }
+            reinterpret_cast<uint2*>((is_v[u] ? a.c.v : a.c.k) + at[u] * D)[l] = c;
+            if (l == 0) (is_v[u] ? a.c.v_scale : a.c.k_scale)[at[u]] = s;
+        }
+    }
+}
+
 template <int VPL, int BITS>   // dim = 32 * VPL
 __global__ void __launch_bounds__(kCodecThreads, 4)
 encode_tqb_kernel(const float* __restrict__ x, int64_t rows, int64_t ldx,
@@ -1516,6 +1611,26 @@ cudaError_t launch_append_mla(const void* c_lat, int64_t ldx, const void* k_rope
         default: KVQ_APPEND(3);
     }
 #undef KVQ_APPEND
+}
+
+cudaError_t launch_append_kv8(const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head,
+                              bool bf16, int64_t rows, const int32_t* slot, const kvq_kv8_cache& c,
+                              uint32_t* dev_status, cudaStream_t s)
+{
+    const AppendKv8Args a{k, v, k_row, k_head, v_row, v_head, rows, RowSlot{slot, c.n_rows, dev_status}, c};
+    const int64_t per_cta = (int64_t)kCodecWarps * (256 / c.head_dim) * kKvRun;
+    const int64_t g = std::max<int64_t>(1, std::min<int64_t>((rows * 2 * c.n_kv + per_cta - 1) / per_cta, (int64_t)sm_count() * 64));
+#define KVQ_APPEND_KV8(D)                                                                      \
+    if (bf16) append_kv8_kernel<D, __nv_bfloat16><<<(unsigned)g, kCodecThreads, 0, s>>>(a);    \
+    else append_kv8_kernel<D, float><<<(unsigned)g, kCodecThreads, 0, s>>>(a);                 \
+    break
+    switch (c.head_dim) {
+        case 64: KVQ_APPEND_KV8(64);
+        case 128: KVQ_APPEND_KV8(128);
+        default: KVQ_APPEND_KV8(256);
+    }
+#undef KVQ_APPEND_KV8
+    return cudaGetLastError();
 }
 
 void tq_codebook_values(int bits, float* centroids, float* thresholds)

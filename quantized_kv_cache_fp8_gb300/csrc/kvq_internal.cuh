@@ -189,6 +189,10 @@ cudaError_t launch_encode_mla(const float* c_lat, int64_t ldx, const float* k_ro
 cudaError_t launch_append_mla(const void* c_lat, int64_t ldx, const void* k_rope, int64_t ldr, bool bf16, int64_t rows,
                               const int32_t* slot, int fmt, const uint32_t* sign_bits, const kvq_mla_cache& c,
                               uint32_t* dev_status, cudaStream_t s);
+// K/V rows of a grouped-query model in fp8 at the pool rows slot[r] (kvq_append_kv8)
+cudaError_t launch_append_kv8(const void* k, int64_t k_row, int64_t k_head, const void* v, int64_t v_row, int64_t v_head,
+                              bool bf16, int64_t rows, const int32_t* slot, const kvq_kv8_cache& c,
+                              uint32_t* dev_status, cudaStream_t s);
 // the stored codebook of width b (2^b centroids, 2^b - 1 thresholds), host side
 void tq_codebook_values(int bits, float* centroids, float* thresholds);
 cudaError_t launch_append_q4(const float* k, const float* v, int n_seq, const int32_t* pos0,

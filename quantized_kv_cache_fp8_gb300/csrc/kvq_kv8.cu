@@ -1,0 +1,634 @@
+// kvq_kv8.cu — decode attention of one new token a sequence over a paged fp8 K/V cache,
+// grouped-query (kvq_kv8_decode).
+//
+// Bound by the cache's bytes: 2 (head_dim + 4) a row and KV head, against 4 head_dim operations a query
+// head.  At eight query heads a KV head and the copy's rate that is 105 TFLOP/s, too much for
+// the CUDA cores and little for the tensor cores, so both contractions are mma.sync
+// m16n8k16 with register operands (fp16 in, fp32 out): the codes are exact in fp16, and eight query heads are
+// the n of one instruction, so nothing is padded at the usual group sizes.
+//   score    S[row][head]  = sum_d kcode[row][d] * Q[d][head]       A = K as it lies in memory
+//   context  O[d][head]   += sum_row vcode[row][d] * W[row][head]   A = V transposed: bytes of two
+//                                                                   rows zipped before they widen
+// The k index of a contraction may be permuted freely if both operands are, and so may m: a lane's fragments
+// are whole 16-byte pieces of a row (dims 64 c + 16 t .. of K rows g, g + 8; dims 16 g .. of V rows
+// 2 t, 2 t + 1, 2 t + 8, 2 t + 9, with g = lane / 4, t = lane % 4).  Each lane copies the pieces that it
+// reads itself with cp.async into a ring that only its warp uses: no barrier, no swizzle, no bank conflict.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "kvq_internal.cuh"
+
+namespace kvq {
+
+namespace {
+
+constexpr unsigned kFull = 0xffffffffu;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kTile = 16;                // rows of a warp's tile
+constexpr int kHeads = 8;                // query heads of an n block
+constexpr float kSlack = 10.0f;          // log2 by which a weight may pass 1 before the reference moves
+
+struct Kv8Args {
+    kvq_kv8_problem p;
+    int group, n_hb;                     // query heads a KV head; blocks of heads a KV head
+    int split_rows, n_splits;
+    float* part_ml;                      // [n_seq][n_qh][n_splits][2]: reference (log2), sum
+    float* part_o;                       // [n_seq][n_qh][n_splits][D]: sum of weighted rows
+    __nv_bfloat16* out;
+    float* lse;
+    uint32_t* status;
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// two e4m3 codes (the low or the high half of w) as f16x2: exact
+__device__ __forceinline__ uint32_t wide_lo(uint32_t w)
+{
+    uint32_t r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, l;}" : "=r"(r) : "r"(w));
+    return r;
+}
+__device__ __forceinline__ uint32_t wide_hi(uint32_t w)
+{
+    uint32_t r;
+    asm("{.reg .b16 l, h; mov.b32 {l, h}, %1; cvt.rn.f16x2.e4m3x2 %0, h;}" : "=r"(r) : "r"(w));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// the 8 x 8 matrix of 16-bit elements that a warp holds (lane: row lane / 4, columns 2 (lane % 4) ..), transposed
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float lg2(float x)
+{
+    float r;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+__device__ __forceinline__ float pow2(int k)              // k in [-126, 127]
+{
+    return __int_as_float((k + 127) << 23);
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool valid)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+
+// the rows that sequence s sees: [x, y)
+__device__ __forceinline__ int2 seen_rows(const kvq_kv8_problem& p, int s)
+{
+    const int L = min(max(p.seq_len[s], 0), p.max_seq_len);
+    return make_int2(p.window > 0 ? max(0, L - p.window) : 0, L);
+}
+
+// The ring of a warp: kStages tiles of codes in the order in which the lanes read them, their scales
+// (K rows, then V rows) and the mask of rows that may be read.
+template <int D, int NB, int W, int S>
+struct Kv8Shape {
+    static constexpr int kThreads = 32 * W;
+    static constexpr int kPieces = D / 64;                  // 16-byte pieces a lane holds of a K row
+    static constexpr int kCodes = 2 * kTile * D;
+    static constexpr int kRing = S * (kCodes + 32 * 4 + 16);
+    static constexpr int kHb = NB * kHeads;                 // heads of a CTA
+    // the merge of the warps reuses the ring: weighted rows, then references and sums
+    static constexpr int kMerge = W * kHb * (D + 2) * 4;
+    static constexpr int kSmem = kRing * W > kMerge ? kRing * W : kMerge;
+};
+
+// One CTA: the rows [x, x + split_rows) of one sequence, one KV head, up to 8 NB query heads of it.  Its warps
+// take the 16-row tiles in turn, each with a softmax of its own, and are joined at the end.
+template <int D, int NB, int W, int S>
+__global__ void __launch_bounds__(32 * W)
+kv8_decode_kernel(const Kv8Args a)
+{
+    using Sh = Kv8Shape<D, NB, W, S>;
+    constexpr int kP = Sh::kPieces, kBlocks = D / 16;       // m blocks of the context, k steps of the score
+    extern __shared__ __align__(128) uint8_t smem[];
+    grid_dependents_launch();
+    const kvq_kv8_problem& p = a.p;
+    const int kv = blockIdx.x / a.n_hb, hb = blockIdx.x % a.n_hb;
+    const int split = blockIdx.y, s = blockIdx.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int heads = min(a.group - hb * Sh::kHb, Sh::kHb);           // query heads at hand
+    const int64_t head0 = (int64_t)s * p.n_qh + kv * a.group + hb * Sh::kHb;
+    const int2 seen = seen_rows(p, s);
+    // (a split begins where the window does: nothing ahead of it is read)
+    const int64_t first = seen.x + (int64_t)split * a.split_rows;
+    const int rows = (int)min((int64_t)a.split_rows, seen.y - first);
+    if (rows <= 0) {
+        if (a.n_splits == 1) {
+            for (int i = threadIdx.x; i < heads * D; i += Sh::kThreads) a.out[head0 * D + i] = __float2bfloat16(0.0f);
+            if (a.lse)
+                for (int i = threadIdx.x; i < heads; i += Sh::kThreads) a.lse[head0 + i] = -INFINITY;
+        }
+        return;                                             // (the join goes by the lengths too)
+    }
+    const int n_tiles = (rows + kTile - 1) / kTile;
+    const int my_tiles = warp < n_tiles ? (n_tiles - warp + W - 1) / W : 0;
+
+    uint8_t* ring = smem + warp * Sh::kRing;
+    const uint32_t ring_at = smem_addr(ring);
+    constexpr int kScaleAt = S * Sh::kCodes, kMaskAt = kScaleAt + S * 128;
+    const uint8_t* kc = p.cache.k + (int64_t)kv * p.cache.n_rows * D;
+    const uint8_t* vc = p.cache.v + (int64_t)kv * p.cache.n_rows * D;
+    const float* ks = p.cache.k_scale + (int64_t)kv * p.cache.n_rows;
+    const float* vs = p.cache.v_scale + (int64_t)kv * p.cache.n_rows;
+
+    // pool row of row `tile * 16 + lane % 16` of this split, -1 behind it, -2 where a page is bad
+    auto look_up = [&](int tile) -> int64_t {
+        const int i = tile * kTile + (lane & 15);
+        if (i >= rows) return -1;
+        const int64_t pos = first + i;
+        int64_t r = -2;
+        if (!p.block_table) {
+            r = s * p.seq_stride_rows + pos;
+        } else {
+            const int pg = (int)pos / p.page_size;
+            const int id = pg < p.max_pages ? p.block_table[(int64_t)s * p.max_pages + pg] : -1;
+            if (id >= 0) r = (int64_t)id * p.page_size + ((int)pos - pg * p.page_size);
+        }
+        return r < p.cache.n_rows ? r : -2;
+    };
+    bool bad = false;
+    auto fetch = [&](int stage, int64_t row) {
+        bad |= row == -2;
+        const unsigned mask = __ballot_sync(kFull, row >= 0);
+        const uint32_t at = ring_at + stage * Sh::kCodes;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t r = __shfl_sync(kFull, row, g + 8 * h);
+#pragma unroll
+            for (int c = 0; c < kP; ++c)
+                copy16(at + ((h * kP + c) * 32 + lane) * 16, kc + max(r, (int64_t)0) * D + 64 * c + 16 * t, r >= 0);
+        }
+        const uint32_t vat = at + kTile * D;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t r = __shfl_sync(kFull, row, 2 * t + (i & 1) + 8 * (i >> 1));
+            const uint8_t* src = vc + max(r, (int64_t)0) * D;
+            if constexpr (D == 64) {
+                copy8(vat + (i * 32 + lane) * 8, src + 8 * g, r >= 0);
+            } else {
+#pragma unroll
+                for (int c = 0; c < D / 128; ++c) copy16(vat + ((i * (D / 128) + c) * 32 + lane) * 16, src + 128 * c + 16 * g, r >= 0);
+            }
+        }
+        copy4(ring_at + kScaleAt + stage * 128 + lane * 4, (lane < 16 ? ks : vs) + max(row, (int64_t)0), row >= 0);
+        if (lane == 0) *reinterpret_cast<uint32_t*>(ring + kMaskAt + stage * 16) = mask;
+    };
+
+    // the first tiles start before the queries are read
+    int64_t next_row = -1;
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        if (i < my_tiles) fetch(i, look_up(warp + i * W));
+        copy_commit();
+    }
+    if (S - 1 < my_tiles) next_row = look_up(warp + (S - 1) * W);
+
+    // Queries as the score's B operand.  bf16 has fp32's range, so a head is scaled by a power of two that puts
+    // its largest element into [2^14, 2^15): elements down to 2^-31 of it are exact, the rest within 2^-39 of it.
+    uint32_t qf[NB][kBlocks][2];
+    float hs[NB][2];                                        // what a score of heads 2 t, 2 t + 1 is multiplied by
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int h = nb * kHeads + g;
+        uint4 w[kP][2];
+#pragma unroll
+        for (int c = 0; c < kP; ++c) {
+            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + s * p.ldq +
+                                                              ((int64_t)kv * a.group + hb * Sh::kHb + h) * D + 64 * c + 16 * t);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) w[c][e] = h < heads ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
+        }
+        uint32_t m = 0;                                     // |bfloat16| patterns order like their values
+#pragma unroll
+        for (int c = 0; c < kP; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t x[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) m = max(m, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
+            }
+        m = max(m, __shfl_xor_sync(kFull, m, 1));
+        m = max(m, __shfl_xor_sync(kFull, m, 2));
+        // 14 - exponent; no head is scaled up by more than 2^100 (a largest element below 2^-86: not exact)
+        const int up = min(14 - ((int)(m >> 7) - 127), 100);
+        const float f = pow2(up);
+#pragma unroll
+        for (int c = 0; c < kP; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const uint32_t x[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    qf[nb][4 * c + 2 * e + (j >> 1)][j & 1] =
+                        pack_h2(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xFFFF0000u) * f);
+            }
+        const float back = pow2(-up) * (p.sm_scale * kLog2e);
+        hs[nb][0] = __shfl_sync(kFull, back, 8 * t);
+        hs[nb][1] = __shfl_sync(kFull, back, 8 * t + 4);
+    }
+
+    float o[NB][kBlocks][4];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[nb][b][e] = 0.0f;
+    // Two references a head, in log2: ref of the scores, for the sum of exp2(x - ref), and wref of x +
+    // log2(vscale), for the weights that multiply V's codes, so that the largest of those is near 1 whatever the
+    // scales.  They move only when something passes them by kSlack (top, wtop: the level that makes them).
+    float ref[NB][2], wref[NB][2], top[NB][2], wtop[NB][2], sum[NB][2];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            ref[nb][e] = wref[nb][e] = sum[nb][e] = 0.0f;
+            top[nb][e] = wtop[nb][e] = -INFINITY;
+        }
+
+    int stage = 0;
+    for (int i = 0; i < my_tiles; ++i) {
+        copy_wait<S - 2>();
+        __syncwarp();                // other lanes' scales are here too, and every lane has left tile i - 1: its stage is free
+        const int into = stage == 0 ? S - 1 : stage - 1;
+        if (i + S - 1 < my_tiles) fetch(into, next_row);
+        copy_commit();
+        if (i + S < my_tiles) next_row = look_up(warp + (i + S) * W);
+        const uint8_t* codes = ring + stage * Sh::kCodes;
+        const float* sc = reinterpret_cast<const float*>(ring + kScaleAt + stage * 128);
+        const uint32_t mask = *reinterpret_cast<const uint32_t*>(ring + kMaskAt + stage * 16);
+
+        float x[NB][4];                                     // rows g (0, 1) and g + 8 (2, 3), heads 2 t, 2 t + 1
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[nb][e] = 0.0f;
+#pragma unroll
+        for (int c = 0; c < kP; ++c) {
+            const uint4 lo = *reinterpret_cast<const uint4*>(codes + (c * 32 + lane) * 16);
+            const uint4 hi = *reinterpret_cast<const uint4*>(codes + ((kP + c) * 32 + lane) * 16);
+            const uint32_t u[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t a0 = wide_lo(u[j]), a1 = wide_lo(v[j]), a2 = wide_hi(u[j]), a3 = wide_hi(v[j]);
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) mma16816(x[nb], a0, a1, a2, a3, qf[nb][4 * c + j][0], qf[nb][4 * c + j][1]);
+            }
+        }
+        const float ks0 = sc[g], ks1 = sc[g + 8], lv0 = lg2(sc[16 + g]), lv1 = lg2(sc[24 + g]);
+        const bool in0 = (mask >> g) & 1, in1 = (mask >> (g + 8)) & 1;
+        bool over = false;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in = e < 2 ? in0 : in1;
+                x[nb][e] = in ? x[nb][e] * (e < 2 ? ks0 : ks1) * hs[nb][e & 1] : -INFINITY;
+                over |= x[nb][e] > top[nb][e & 1] || x[nb][e] + (e < 2 ? lv0 : lv1) > wtop[nb][e & 1];
+            }
+        if (__any_sync(kFull, over)) {                      // (rare after the first tile)
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float m = fmaxf(x[nb][e], x[nb][e + 2]), mw = fmaxf(x[nb][e] + lv0, x[nb][e + 2] + lv1);
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+                        mw = fmaxf(mw, __shfl_xor_sync(kFull, mw, d));
+                    }
+                    if (m > top[nb][e] - kSlack) {          // (top is -inf, or the reference and kSlack)
+                        const float f = top[nb][e] == -INFINITY ? 0.0f : ex2(ref[nb][e] - m);
+                        sum[nb][e] *= f;
+                        ref[nb][e] = m;
+                        top[nb][e] = m + kSlack;
+                    }
+                    if (mw > wtop[nb][e] - kSlack) {
+                        const float f = wtop[nb][e] == -INFINITY ? 0.0f : ex2(wref[nb][e] - mw);
+#pragma unroll
+                        for (int b = 0; b < kBlocks; ++b) {
+                            o[nb][b][e] *= f;
+                            o[nb][b][e + 2] *= f;
+                        }
+                        wref[nb][e] = mw;
+                        wtop[nb][e] = mw + kSlack;
+                    }
+                }
+            }
+        }
+        uint32_t w[NB][2];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[nb][e & 1] += ex2(x[nb][e] - ref[nb][e & 1]);
+            w[nb][0] = transpose8(pack_h2(ex2(x[nb][0] + lv0 - wref[nb][0]), ex2(x[nb][1] + lv0 - wref[nb][1])));
+            w[nb][1] = transpose8(pack_h2(ex2(x[nb][2] + lv1 - wref[nb][0]), ex2(x[nb][3] + lv1 - wref[nb][1])));
+        }
+        // context: block b of a lane is its dims 2 b and 2 b + 1 of the pieces
+        const uint8_t* vcodes = codes + kTile * D;
+        if constexpr (D == 64) {
+            uint2 v[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] = *reinterpret_cast<const uint2*>(vcodes + (r * 32 + lane) * 8);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint32_t x0 = j ? v[0].y : v[0].x, x1 = j ? v[1].y : v[1].x, x2 = j ? v[2].y : v[2].x, x3 = j ? v[3].y : v[3].x;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t z0 = __byte_perm(x0, x1, h ? 0x7362 : 0x5140), z1 = __byte_perm(x2, x3, h ? 0x7362 : 0x5140);
+                    const uint32_t a0 = wide_lo(z0), a1 = wide_hi(z0), a2 = wide_lo(z1), a3 = wide_hi(z1);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][2 * j + h], a0, a1, a2, a3, w[nb][0], w[nb][1]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int c = 0; c < D / 128; ++c) {
+                uint32_t v[4][4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint4 y = *reinterpret_cast<const uint4*>(vcodes + ((r * (D / 128) + c) * 32 + lane) * 16);
+                    v[r][0] = y.x;
+                    v[r][1] = y.y;
+                    v[r][2] = y.z;
+                    v[r][3] = y.w;
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t z0 = __byte_perm(v[0][j], v[1][j], h ? 0x7362 : 0x5140);
+                        const uint32_t z1 = __byte_perm(v[2][j], v[3][j], h ? 0x7362 : 0x5140);
+                        const uint32_t a0 = wide_lo(z0), a1 = wide_hi(z0), a2 = wide_lo(z1), a3 = wide_hi(z1);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][8 * c + 2 * j + h], a0, a1, a2, a3, w[nb][0], w[nb][1]);
+                    }
+            }
+        }
+        stage = stage + 1 == S ? 0 : stage + 1;
+    }
+    copy_wait<0>();
+    if (__any_sync(kFull, bad) && lane == 0 && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_PAGE);
+
+    // ---- the warps are joined: weighted rows relative to ref, then references and sums
+    __syncthreads();
+    float* mo = reinterpret_cast<float*>(smem);             // [warp][head][D]
+    float* ml = mo + W * Sh::kHb * D;                       // [warp][head][2]
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = nb * kHeads + 2 * t + e;
+            float l = sum[nb][e];
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
+            // (exp2f: with scales below 2^-126 the factor may be subnormal)
+            const float f = wtop[nb][e] == -INFINITY ? (l != l ? l : 0.0f) : exp2f(wref[nb][e] - ref[nb][e]);
+            float* dst = mo + (warp * Sh::kHb + h) * D;
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+                const int d = D == 64 ? 8 * g + 2 * b : 128 * (b / 8) + 16 * g + 2 * (b % 8);
+                *reinterpret_cast<float2*>(dst + d) = make_float2(o[nb][b][e] * f, o[nb][b][e + 2] * f);
+            }
+            if (g == 0) {
+                // a head without a row: reference -inf, sum 0; one that holds a NaN keeps it in the sum
+                ml[(warp * Sh::kHb + h) * 2] = top[nb][e] == -INFINITY ? -INFINITY : ref[nb][e];
+                ml[(warp * Sh::kHb + h) * 2 + 1] = l;
+            }
+        }
+    __syncthreads();
+    for (int i = threadIdx.x; i < heads * (D / 4); i += Sh::kThreads) {
+        const int h = i / (D / 4), d = i % (D / 4) * 4;
+        float m = -INFINITY, l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) m = fmaxf(m, ml[(w * Sh::kHb + h) * 2]);
+        const float base = m == -INFINITY ? 0.0f : m;
+        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float wl = ml[(w * Sh::kHb + h) * 2 + 1];
+            // (a NaN query: no reference was ever set, the sum says it)
+            const float f = wl != wl ? wl : ex2(ml[(w * Sh::kHb + h) * 2] - base);
+            const float4 y = *reinterpret_cast<const float4*>(mo + (w * Sh::kHb + h) * D + d);
+            l += wl * f;
+            acc.x = fmaf(y.x, f, acc.x);
+            acc.y = fmaf(y.y, f, acc.y);
+            acc.z = fmaf(y.z, f, acc.z);
+            acc.w = fmaf(y.w, f, acc.w);
+        }
+        const int64_t row = head0 + h;
+        if (a.n_splits == 1) {
+            const float r = l == 0.0f ? 0.0f : 1.0f / l;
+            __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
+            dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
+            dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+            if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
+        } else {
+            const int64_t at = row * a.n_splits + split;
+            *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
+            if (d == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m, l);
+        }
+    }
+}
+
+// The splits of a (sequence, query head) joined: D / 4 threads, splits in ascending order.
+template <int D>
+__global__ void __launch_bounds__(D / 4) kv8_combine_kernel(const Kv8Args a)
+{
+    const kvq_kv8_problem& p = a.p;
+    const int64_t row = (int64_t)blockIdx.y * p.n_qh + blockIdx.x;
+    const int2 seen = seen_rows(p, blockIdx.y);
+    const int n = (int)(((int64_t)seen.y - seen.x + a.split_rows - 1) / a.split_rows);
+    const int d = threadIdx.x * 4;
+    grid_dependency_wait();
+    const float* ml = a.part_ml + row * a.n_splits * 2;
+    const float* po = a.part_o + row * a.n_splits * D + d;
+    float m = -INFINITY;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, ml[2 * i]);
+    const float base = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+        const float wl = ml[2 * i + 1];
+        const float f = wl != wl ? wl : ex2(ml[2 * i] - base);
+        const float4 y = *reinterpret_cast<const float4*>(po + (int64_t)i * D);
+        l += wl * f;
+        acc.x = fmaf(y.x, f, acc.x);
+        acc.y = fmaf(y.y, f, acc.y);
+        acc.z = fmaf(y.z, f, acc.z);
+        acc.w = fmaf(y.w, f, acc.w);
+    }
+    const float r = l == 0.0f ? 0.0f : 1.0f / l;
+    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
+    dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
+    dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+    if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
+}
+
+struct Kv8Plan {
+    int nb = 1, n_hb = 1, split_rows = 0, n_splits = 0;
+    size_t off_o = 0, bytes = 0;
+};
+
+Kv8Plan plan_kv8(const kvq_kv8_problem& p)
+{
+    Kv8Plan q;
+    const int group = p.n_qh / p.cache.n_kv;
+    // two blocks of eight heads share the rows' conversion; at 256 dims their accumulators do not fit
+    q.nb = group > kHeads && p.cache.head_dim <= 128 ? 2 : 1;
+    q.n_hb = (group + q.nb * kHeads - 1) / (q.nb * kHeads);
+    const int64_t most = p.window > 0 ? std::min(p.window, p.max_seq_len) : p.max_seq_len;
+    const int64_t units = (int64_t)p.n_seq * p.cache.n_kv * q.n_hb;
+    const int64_t slots = 2 * (int64_t)sm_count();
+    int64_t split = 4096;
+    if (p.n_seq == 1) split = (most * units + slots - 1) / slots;
+    else split = most * units / (slots * 8);
+    split = std::min<int64_t>(std::max<int64_t>(split, 128), 4096);
+    split = std::max<int64_t>(split, (most + 65534) / 65535);
+    split = (split + 127) / 128 * 128;
+    q.split_rows = (int)split;
+    q.n_splits = (int)std::max<int64_t>(1, (most + split - 1) / split);
+    if (q.n_splits > 1) {
+        const size_t rows = (size_t)p.n_seq * p.n_qh * q.n_splits;
+        q.off_o = (rows * 8 + 255) / 256 * 256;
+        q.bytes = q.off_o + rows * p.cache.head_dim * 4;
+    }
+    return q;
+}
+
+template <int D, int NB, int W, int S>
+cudaError_t launch_kv8_as(const Kv8Args& a, cudaStream_t s)
+{
+    constexpr int smem = Kv8Shape<D, NB, W, S>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<D, NB, W, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    const dim3 grid((unsigned)(a.p.cache.n_kv * a.n_hb), (unsigned)a.n_splits, (unsigned)a.p.n_seq);
+    kv8_decode_kernel<D, NB, W, S><<<grid, 32 * W, smem, s>>>(a);
+    e = cudaGetLastError();
+    if (e == cudaSuccess && a.n_splits > 1)
+        e = launch_dependent(kv8_combine_kernel<D>, dim3((unsigned)a.p.n_qh, (unsigned)a.p.n_seq), dim3(D / 4), 0, s, a);
+    return e;
+}
+
+bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+int check_problem(const kvq_kv8_problem* p, const char* E)
+{
+    if (!p) return set_last_error(KVQ_EINVAL, "%s: NULL problem", E);
+    const kvq_kv8_cache& c = p->cache;
+    if (c.head_dim != 64 && c.head_dim != 128 && c.head_dim != 256)
+        return set_last_error(KVQ_EINVAL, "%s: head_dim %d not 64, 128 or 256", E, c.head_dim);
+    if (p->n_seq < 0 || p->n_seq > 65535) return set_last_error(KVQ_EINVAL, "%s: n_seq outside [0, 65535]", E);
+    if (c.n_kv < 1 || p->n_qh < 1 || p->n_qh % c.n_kv || p->n_qh > 65536)
+        return set_last_error(KVQ_EINVAL, "%s: n_qh must be a multiple of n_kv, at most 65536", E);
+    if (p->max_seq_len < 0 || p->max_seq_len > 1 << 30 || p->window < 0)
+        return set_last_error(KVQ_EINVAL, "%s: max_seq_len outside [0, 2^30] or window < 0", E);
+    if (!std::isfinite(p->sm_scale)) return set_last_error(KVQ_EINVAL, "%s: sm_scale is not finite", E);
+    if (p->block_table ? p->max_pages < 1 || p->page_size < 1 : p->seq_stride_rows < 0)
+        return set_last_error(KVQ_EINVAL, "%s: bad paging sizes", E);
+    if (c.n_rows < 0) return set_last_error(KVQ_EINVAL, "%s: n_rows < 0", E);
+    if (p->ldq < 0) return set_last_error(KVQ_EINVAL, "%s: ldq < 0", E);
+    if (p->n_seq == 0) return KVQ_OK;
+    if (!p->seq_len || !p->q || !c.k || !c.k_scale || !c.v || !c.v_scale)
+        return set_last_error(KVQ_EINVAL, "%s: NULL pointer", E);
+    if (p->n_seq > 1 && p->ldq < (int64_t)p->n_qh * c.head_dim)
+        return set_last_error(KVQ_EINVAL, "%s: ldq smaller than the heads", E);
+    if (!aligned(p->q, 16) || p->ldq % 8) return set_last_error(KVQ_EALIGN, "%s: queries not 16-byte aligned", E);
+    if (!aligned(c.k, 16) || !aligned(c.v, 16)) return set_last_error(KVQ_EALIGN, "%s: code planes not 16-byte aligned", E);
+    if (!aligned(c.k_scale, 4) || !aligned(c.v_scale, 4) || !aligned(p->seq_len, 4) || !aligned(p->block_table, 4))
+        return set_last_error(KVQ_EALIGN, "%s: an array is not 4-byte aligned", E);
+    return KVQ_OK;
+}
+
+}  // namespace
+
+}  // namespace kvq
+
+extern "C" {
+
+size_t kvq_kv8_decode_workspace(const kvq_kv8_problem* p)
+{
+    using namespace kvq;
+    if (check_problem(p, "kvq_kv8_decode_workspace") != KVQ_OK || p->n_seq == 0) return 0;
+    return plan_kv8(*p).bytes;
+}
+
+int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* workspace, size_t ws_bytes,
+                   uint32_t* dev_status, kvq_stream_t stream)
+{
+    using namespace kvq;
+    const char* E = "kvq_kv8_decode";
+    if (int st = fault_injected(E)) return st;
+    if (int st = check_problem(p, E)) return st;
+    if (p->n_seq == 0) return KVQ_OK;
+    if (!out) return set_last_error(KVQ_EINVAL, "%s: NULL out", E);
+    if (!aligned(out, 16) || !aligned(lse, 4) || !aligned(dev_status, 4))
+        return set_last_error(KVQ_EALIGN, "%s: out, lse or dev_status misaligned", E);
+    const Kv8Plan q = plan_kv8(*p);
+    if (q.bytes && (!workspace || ws_bytes < q.bytes))
+        return set_last_error(KVQ_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", E, workspace ? ws_bytes : (size_t)0, q.bytes);
+    if (q.bytes && !aligned(workspace, 256)) return set_last_error(KVQ_EALIGN, "%s: workspace not 256-byte aligned", E);
+    Kv8Args a{*p, p->n_qh / p->cache.n_kv, q.n_hb, q.split_rows, q.n_splits, nullptr, nullptr,
+              static_cast<__nv_bfloat16*>(out), lse, dev_status};
+    if (q.bytes) {
+        a.part_ml = static_cast<float*>(workspace);
+        a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + q.off_o);
+    }
+    const cudaStream_t s = (cudaStream_t)stream;
+    cudaError_t e;
+    switch (p->cache.head_dim) {
+        case 64: e = q.nb == 2 ? launch_kv8_as<64, 2, 8, 4>(a, s) : launch_kv8_as<64, 1, 8, 4>(a, s); break;
+        case 128: e = q.nb == 2 ? launch_kv8_as<128, 2, 8, 3>(a, s) : launch_kv8_as<128, 1, 8, 3>(a, s); break;
+        default: e = launch_kv8_as<256, 1, 4, 3>(a, s);
+    }
+    return e == cudaSuccess ? KVQ_OK : set_last_error(KVQ_ECUDA, "%s: %s", E, cudaGetErrorString(e));
+}
+
+}  // extern "C"
