@@ -599,7 +599,7 @@ typedef struct kvq_kv8_cache {
     float*   k_scale;               /* device [n_kv][n_rows]                            */
     uint8_t* v;                     /* as k                                             */
     float*   v_scale;
-    int64_t  n_rows;                /* rows in the pool                                  */
+    int64_t  n_rows;                /* rows in the pool (kvq_kv8_decode: below 2^31)      */
     int32_t  n_kv, head_dim;        /* head_dim: 64, 128 or 256                          */
 } kvq_kv8_cache;
 

@@ -28,8 +28,9 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kTile = 16;                // rows of a warp's tile
+constexpr int kGroup = 16;               // rows of an instruction's tile
 constexpr int kHeads = 8;                // query heads of an n block
+constexpr int kCtas = 3;                 // CTAs an SM
 constexpr float kSlack = 10.0f;          // log2 by which a weight may pass 1 before the reference moves
 
 struct Kv8Args {
@@ -99,23 +100,30 @@ __device__ __forceinline__ float pow2(int k)              // k in [-126, 127]
     return __int_as_float((k + 127) << 23);
 }
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid)
+// bytes of the cache, read once
+__device__ __forceinline__ uint4 load16(const uint8_t* p)
 {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0) : "memory");
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+    return r;
 }
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src, bool valid)
+template <int BYTES, int N>
+__device__ __forceinline__ void load_piece(uint32_t (&w)[N], const uint8_t* p, bool on)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(valid ? 8 : 0) : "memory");
+    static_assert(BYTES == 4 * N, "a piece is its words");
+    if constexpr (N == 4) {
+        const uint4 r = on ? load16(p) : make_uint4(0u, 0u, 0u, 0u);
+        w[0] = r.x;
+        w[1] = r.y;
+        w[2] = r.z;
+        w[3] = r.w;
+    } else {
+        uint2 r = make_uint2(0u, 0u);
+        if (on) asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+        w[0] = r.x;
+        w[1] = r.y;
+    }
 }
-__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool valid)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(valid ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
 // the rows that sequence s sees: [x, y)
 __device__ __forceinline__ int2 seen_rows(const kvq_kv8_problem& p, int s)
@@ -124,28 +132,32 @@ __device__ __forceinline__ int2 seen_rows(const kvq_kv8_problem& p, int s)
     return make_int2(p.window > 0 ? max(0, L - p.window) : 0, L);
 }
 
-// The ring of a warp: kStages tiles of codes in the order in which the lanes read them, their scales
-// (K rows, then V rows) and the mask of rows that may be read.
-template <int D, int NB, int W, int S>
+// splits begin at a multiple of a group's rows: the first at or ahead of the first row that is seen
+__device__ __forceinline__ int first_group(const int2& seen) { return seen.x & ~(kGroup - 1); }
+
+// What the kernel is built from: D dims, NB blocks of eight heads, R rows a warp's tile, W warps, C CTAs an SM.
+template <int D, int NB, int R, int W, int C>
 struct Kv8Shape {
     static constexpr int kThreads = 32 * W;
-    static constexpr int kPieces = D / 64;                  // 16-byte pieces a lane holds of a K row
-    static constexpr int kCodes = 2 * kTile * D;
-    static constexpr int kRing = S * (kCodes + 32 * 4 + 16);
+    static constexpr int kKp = D / 64;                      // 16-byte pieces a lane holds of a K row
+    static constexpr int kVp = D == 64 ? 1 : D / 128;       // and of a V row (8 bytes at 64 dims)
+    static constexpr int kVw = D == 64 ? 2 : 4;             // words of such a piece
     static constexpr int kHb = NB * kHeads;                 // heads of a CTA
-    // the merge of the warps reuses the ring: weighted rows, then references and sums
-    static constexpr int kMerge = W * kHb * (D + 2) * 4;
-    static constexpr int kSmem = kRing * W > kMerge ? kRing * W : kMerge;
+    // the merge of the warps: weighted rows, then references and sums
+    static constexpr int kSmem = W * kHb * (D + 2) * 4;
 };
 
 // One CTA: the rows [x, x + split_rows) of one sequence, one KV head, up to 8 NB query heads of it.  Its warps
-// take the 16-row tiles in turn, each with a softmax of its own, and are joined at the end.
-template <int D, int NB, int W, int S>
-__global__ void __launch_bounds__(32 * W)
+// take the tiles in turn, each with a softmax of its own, and are joined at the end.  GROUPED: 16 rows from a
+// multiple of 16 are neighbours in the pool (pages of a multiple of 16 rows, or no table), so that a group has one
+// address; otherwise every row has its own.
+template <int D, int NB, int R, int W, int C, bool GROUPED>
+__global__ void __launch_bounds__(32 * W, C)
 kv8_decode_kernel(const Kv8Args a)
 {
-    using Sh = Kv8Shape<D, NB, W, S>;
-    constexpr int kP = Sh::kPieces, kBlocks = D / 16;       // m blocks of the context, k steps of the score
+    using Sh = Kv8Shape<D, NB, R, W, C>;
+    constexpr int kP = Sh::kKp, kBlocks = D / 16;       // m blocks of the context, k steps of the score
+    constexpr int kGroups = R / kGroup;
     extern __shared__ __align__(128) uint8_t smem[];
     grid_dependents_launch();
     const kvq_kv8_problem& p = a.p;
@@ -155,10 +167,8 @@ kv8_decode_kernel(const Kv8Args a)
     const int heads = min(a.group - hb * Sh::kHb, Sh::kHb);           // query heads at hand
     const int64_t head0 = (int64_t)s * p.n_qh + kv * a.group + hb * Sh::kHb;
     const int2 seen = seen_rows(p, s);
-    // (a split begins where the window does: nothing ahead of it is read)
-    const int64_t first = seen.x + (int64_t)split * a.split_rows;
-    const int rows = (int)min((int64_t)a.split_rows, seen.y - first);
-    if (rows <= 0) {
+    const int64_t first64 = first_group(seen) + (int64_t)split * a.split_rows;
+    if (first64 >= seen.y) {
         if (a.n_splits == 1) {
             for (int i = threadIdx.x; i < heads * D; i += Sh::kThreads) a.out[head0 * D + i] = __float2bfloat16(0.0f);
             if (a.lse)
@@ -166,68 +176,124 @@ kv8_decode_kernel(const Kv8Args a)
         }
         return;                                             // (the join goes by the lengths too)
     }
-    const int n_tiles = (rows + kTile - 1) / kTile;
+    const int first = (int)first64, end = (int)min((int64_t)seen.y, first64 + a.split_rows);
+    const int n_tiles = (end - first + R - 1) / R;
     const int my_tiles = warp < n_tiles ? (n_tiles - warp + W - 1) / W : 0;
 
-    uint8_t* ring = smem + warp * Sh::kRing;
-    const uint32_t ring_at = smem_addr(ring);
-    constexpr int kScaleAt = S * Sh::kCodes, kMaskAt = kScaleAt + S * 128;
-    const uint8_t* kc = p.cache.k + (int64_t)kv * p.cache.n_rows * D;
-    const uint8_t* vc = p.cache.v + (int64_t)kv * p.cache.n_rows * D;
+    // where this lane's pieces of row 0 begin
+    const uint8_t* kc = p.cache.k + (int64_t)kv * p.cache.n_rows * D + 16 * t;
+    const uint8_t* vc = p.cache.v + (int64_t)kv * p.cache.n_rows * D + (D == 64 ? 8 : 16) * g;
     const float* ks = p.cache.k_scale + (int64_t)kv * p.cache.n_rows;
     const float* vs = p.cache.v_scale + (int64_t)kv * p.cache.n_rows;
 
-    // pool row of row `tile * 16 + lane % 16` of this split, -1 behind it, -2 where a page is bad
-    auto look_up = [&](int tile) -> int64_t {
-        const int i = tile * kTile + (lane & 15);
-        if (i >= rows) return -1;
-        const int64_t pos = first + i;
-        int64_t r = -2;
+    // Pool row of a position, or of a group's first (a pool holds fewer than 2^31): -2 where there is none
+    const int pool = (int)p.cache.n_rows;
+    auto pool_row = [&](int pos) -> int {
         if (!p.block_table) {
-            r = s * p.seq_stride_rows + pos;
-        } else {
-            const int pg = (int)pos / p.page_size;
-            const int id = pg < p.max_pages ? p.block_table[(int64_t)s * p.max_pages + pg] : -1;
-            if (id >= 0) r = (int64_t)id * p.page_size + ((int)pos - pg * p.page_size);
+            const int64_t r = s * p.seq_stride_rows + pos;
+            return r < pool ? (int)r : -2;
         }
-        return r < p.cache.n_rows ? r : -2;
+        const int pg = pos / p.page_size;
+        const int id = pg < p.max_pages ? p.block_table[(int64_t)s * p.max_pages + pg] : -1;
+        return id >= 0 && ((int64_t)id + 1) * p.page_size <= pool ? id * p.page_size + (pos - pg * p.page_size) : -2;
     };
-    bool bad = false;
-    auto fetch = [&](int stage, int64_t row) {
-        bad |= row == -2;
-        const unsigned mask = __ballot_sync(kFull, row >= 0);
-        const uint32_t at = ring_at + stage * Sh::kCodes;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t r = __shfl_sync(kFull, row, g + 8 * h);
-#pragma unroll
-            for (int c = 0; c < kP; ++c)
-                copy16(at + ((h * kP + c) * 32 + lane) * 16, kc + max(r, (int64_t)0) * D + 64 * c + 16 * t, r >= 0);
+    // what a lane finds for tile i: GROUPED: the row of group lane % kGroups, else the row of lane % R; -1: none
+    auto look_up = [&](int i) -> int {
+        if constexpr (GROUPED) {
+            const int pos = first + (warp + i * W) * R + (lane % kGroups) * kGroup;
+            return pos < end ? pool_row(pos) : -1;
+        } else {
+            const int pos = first + (warp + i * W) * R + lane % R;
+            return pos >= seen.x && pos < end ? pool_row(pos) : -1;
         }
-        const uint32_t vat = at + kTile * D;
+    };
+    // The tile at hand, in registers: the lane's pieces of K rows 8 e + g and of V rows 16 (e / 4) + 8 (e / 2 % 2) +
+    // 2 t + e % 2, the scales of row lane % R, and the mask of the rows that may be read (zeros stand for the others).
+    // Each part is loaded for tile i + 1 as soon as tile i is done with it.
+    uint4 kr[2 * kGroups][kP];
+    uint32_t vr[4 * kGroups][Sh::kVp][Sh::kVw];
+    float k_scale, v_scale;
+    uint32_t mask = 0;
+    bool bad = false;
+    int base[GROUPED ? kGroups : 1];                        // pool rows of the groups (GROUPED: of all lanes alike)
+    bool whole = false;
+    int lo = 0, hi = 0;                                     // GROUPED: rows of the tile to be read, where not whole
+    // K and the scales of tile i, found by look_up(i)
+    auto load_k = [&](int i, int found) {
+        bad |= found == -2;
+        int64_t row;
+        bool in;
+        if constexpr (GROUPED) {
+            const int pos0 = first + (warp + i * W) * R;
+            whole = pos0 >= seen.x && pos0 + R <= end;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t r = __shfl_sync(kFull, row, 2 * t + (i & 1) + 8 * (i >> 1));
-            const uint8_t* src = vc + max(r, (int64_t)0) * D;
-            if constexpr (D == 64) {
-                copy8(vat + (i * 32 + lane) * 8, src + 8 * g, r >= 0);
+            for (int j = 0; j < kGroups; ++j) {
+                base[j] = __shfl_sync(kFull, found, j);
+                whole = whole && base[j] >= 0 && base[j] <= pool - kGroup;
+            }
+            row = (lane & (kGroup - 1)) + (kGroups == 2 && lane >= kGroup ? base[kGroups - 1] : base[0]);
+            if (whole) {
+                mask = ~0u;
+                in = true;
+#pragma unroll
+                for (int e = 0; e < 2 * kGroups; ++e)
+#pragma unroll
+                    for (int c = 0; c < kP; ++c) kr[e][c] = load16(kc + ((int64_t)base[e / 2] + g) * D + (e % 2 * 8 * D + 64 * c));
             } else {
+                lo = seen.x - pos0;
+                hi = end - pos0;
+                const int r = lane % R, b = kGroups == 2 && r >= kGroup ? base[kGroups - 1] : base[0];
+                in = r >= lo && r < hi && b >= 0 && b + (r & (kGroup - 1)) < pool;
+                bad |= r >= lo && r < hi && b >= 0 && b + (r & (kGroup - 1)) >= pool;       // (no table: the pool may end anywhere)
+                mask = __ballot_sync(kFull, in);
 #pragma unroll
-                for (int c = 0; c < D / 128; ++c) copy16(vat + ((i * (D / 128) + c) * 32 + lane) * 16, src + 128 * c + 16 * g, r >= 0);
+                for (int e = 0; e < 2 * kGroups; ++e) {
+                    const bool on = mask >> (8 * e + g) & 1;
+#pragma unroll
+                    for (int c = 0; c < kP; ++c)
+                        kr[e][c] = on ? load16(kc + ((int64_t)base[e / 2] + g) * D + (e % 2 * 8 * D + 64 * c)) : make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        } else {
+            base[0] = found;
+            row = found;
+            in = found >= 0;
+            mask = __ballot_sync(kFull, in);
+#pragma unroll
+            for (int e = 0; e < 2 * kGroups; ++e) {
+                const int r = __shfl_sync(kFull, found, 8 * e + g);
+#pragma unroll
+                for (int c = 0; c < kP; ++c) kr[e][c] = r >= 0 ? load16(kc + (int64_t)r * D + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        copy4(ring_at + kScaleAt + stage * 128 + lane * 4, (lane < 16 ? ks : vs) + max(row, (int64_t)0), row >= 0);
-        if (lane == 0) *reinterpret_cast<uint32_t*>(ring + kMaskAt + stage * 16) = mask;
+        k_scale = in ? __ldg(ks + row) : 0.0f;
+        v_scale = in ? __ldg(vs + row) : 0.0f;
     };
-
-    // the first tiles start before the queries are read
-    int64_t next_row = -1;
+    // V of the tile whose K was loaded last
+    auto load_v = [&]() {
 #pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-        if (i < my_tiles) fetch(i, look_up(warp + i * W));
-        copy_commit();
+        for (int e = 0; e < 4 * kGroups; ++e) {
+            constexpr int kStep = D == 64 ? 8 : 16;
+            const int in_group = 8 * (e / 2 % 2) + e % 2;
+            const uint8_t* src;
+            bool on = true;
+            if constexpr (GROUPED) {
+                src = vc + ((int64_t)base[e / 4] + 2 * t) * D + in_group * D;
+                if (!whole) on = mask >> (kGroup * (e / 4) + in_group + 2 * t) & 1;
+            } else {
+                const int r = __shfl_sync(kFull, base[0], kGroup * (e / 4) + in_group + 2 * t);
+                src = vc + (int64_t)r * D;
+                on = r >= 0;
+            }
+#pragma unroll
+            for (int c = 0; c < Sh::kVp; ++c) load_piece<kStep>(vr[e][c], src + 128 * c, on);
+        }
+    };
+    int next = my_tiles > 1 ? look_up(1) : -1;
+    if (my_tiles > 0) {                                     // the first tile starts before the queries are read
+        load_k(0, look_up(0));
+        load_v();
     }
-    if (S - 1 < my_tiles) next_row = look_up(warp + (S - 1) * W);
 
     // Queries as the score's B operand.  bf16 has fp32's range, so a head is scaled by a power of two that puts
     // its largest element into [2^14, 2^15): elements down to 2^-31 of it are exact, the rest within 2^-39 of it.
@@ -292,52 +358,83 @@ kv8_decode_kernel(const Kv8Args a)
             top[nb][e] = wtop[nb][e] = -INFINITY;
         }
 
-    int stage = 0;
     for (int i = 0; i < my_tiles; ++i) {
-        copy_wait<S - 2>();
-        __syncwarp();                // other lanes' scales are here too, and every lane has left tile i - 1: its stage is free
-        const int into = stage == 0 ? S - 1 : stage - 1;
-        if (i + S - 1 < my_tiles) fetch(into, next_row);
-        copy_commit();
-        if (i + S < my_tiles) next_row = look_up(warp + (i + S) * W);
-        const uint8_t* codes = ring + stage * Sh::kCodes;
-        const float* sc = reinterpret_cast<const float*>(ring + kScaleAt + stage * 128);
-        const uint32_t mask = *reinterpret_cast<const uint32_t*>(ring + kMaskAt + stage * 16);
-
-        float x[NB][4];                                     // rows g (0, 1) and g + 8 (2, 3), heads 2 t, 2 t + 1
+        const int after = i + 2 < my_tiles ? look_up(i + 2) : -1;
+        // rows 16 j + g (0, 1) and 16 j + g + 8 (2, 3), heads 2 t, 2 t + 1
+        float x[kGroups][NB][4];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
+        for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[nb][e] = 0.0f;
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int c = 0; c < kP; ++c) {
-            const uint4 lo = *reinterpret_cast<const uint4*>(codes + (c * 32 + lane) * 16);
-            const uint4 hi = *reinterpret_cast<const uint4*>(codes + ((kP + c) * 32 + lane) * 16);
-            const uint32_t u[4] = {lo.x, lo.y, lo.z, lo.w}, v[4] = {hi.x, hi.y, hi.z, hi.w};
+                for (int e = 0; e < 4; ++e) x[j][nb][e] = 0.0f;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const uint32_t a0 = wide_lo(u[j]), a1 = wide_lo(v[j]), a2 = wide_hi(u[j]), a3 = wide_hi(v[j]);
+        for (int c = 0; c < kP; ++c)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) mma16816(x[nb], a0, a1, a2, a3, qf[nb][4 * c + j][0], qf[nb][4 * c + j][1]);
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    const uint4 &l = kr[2 * j][c], &u = kr[2 * j + 1][c];
+                    const uint32_t wl = k == 0 ? l.x : k == 1 ? l.y : k == 2 ? l.z : l.w;
+                    const uint32_t wu = k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
+                    const uint32_t a0 = wide_lo(wl), a1 = wide_lo(wu), a2 = wide_hi(wl), a3 = wide_hi(wu);
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        mma16816(x[j][nb], a0, a1, a2, a3, qf[nb][4 * c + k][0], qf[nb][4 * c + k][1]);
+                }
+        float kf[kGroups][2], lv[kGroups][2];
+        const float my_lv = lg2(v_scale);
+#pragma unroll
+        for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                kf[j][e] = __shfl_sync(kFull, k_scale, 16 * j + 8 * e + g);
+                lv[j][e] = __shfl_sync(kFull, my_lv, 16 * j + 8 * e + g);
             }
-        }
-        const float ks0 = sc[g], ks1 = sc[g + 8], lv0 = lg2(sc[16 + g]), lv1 = lg2(sc[24 + g]);
-        const bool in0 = (mask >> g) & 1, in1 = (mask >> (g + 8)) & 1;
+        const uint32_t now = mask;
+        if (i + 1 < my_tiles) load_k(i + 1, next);
         bool over = false;
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool in = e < 2 ? in0 : in1;
-                x[nb][e] = in ? x[nb][e] * (e < 2 ? ks0 : ks1) * hs[nb][e & 1] : -INFINITY;
-                over |= x[nb][e] > top[nb][e & 1] || x[nb][e] + (e < 2 ? lv0 : lv1) > wtop[nb][e & 1];
+            for (int e = 0; e < 2; ++e) {
+                float m = -INFINITY, mw = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        float& y = x[j][nb][2 * h + e];
+                        y = y * kf[j][h] * hs[nb][e];
+                        m = fmaxf(m, y);
+                        mw = fmaxf(mw, y + lv[j][h]);
+                    }
+                over |= m > top[nb][e] || mw > wtop[nb][e];
             }
-        if (__any_sync(kFull, over)) {                      // (rare after the first tile)
+        const bool part = now != ~0u;
+        if (__any_sync(kFull, over) || part) {              // (rare after the first tile)
+            if (part) {
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        if (!(now >> (16 * j + 8 * h + g) & 1)) {
+                            lv[j][h] = 0.0f;
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb) x[j][nb][2 * h] = x[j][nb][2 * h + 1] = -INFINITY;
+                        }
+            }
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float m = fmaxf(x[nb][e], x[nb][e + 2]), mw = fmaxf(x[nb][e] + lv0, x[nb][e + 2] + lv1);
+                    float m = -INFINITY, mw = -INFINITY;
+#pragma unroll
+                    for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            m = fmaxf(m, x[j][nb][2 * h + e]);
+                            mw = fmaxf(mw, x[j][nb][2 * h + e] + lv[j][h]);
+                        }
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) {
                         m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
@@ -362,58 +459,37 @@ kv8_decode_kernel(const Kv8Args a)
                 }
             }
         }
-        uint32_t w[NB][2];
+        uint32_t w[kGroups][NB][2];
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
+        for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) sum[nb][e & 1] += ex2(x[nb][e] - ref[nb][e & 1]);
-            w[nb][0] = transpose8(pack_h2(ex2(x[nb][0] + lv0 - wref[nb][0]), ex2(x[nb][1] + lv0 - wref[nb][1])));
-            w[nb][1] = transpose8(pack_h2(ex2(x[nb][2] + lv1 - wref[nb][0]), ex2(x[nb][3] + lv1 - wref[nb][1])));
-        }
-        // context: block b of a lane is its dims 2 b and 2 b + 1 of the pieces
-        const uint8_t* vcodes = codes + kTile * D;
-        if constexpr (D == 64) {
-            uint2 v[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = *reinterpret_cast<const uint2*>(vcodes + (r * 32 + lane) * 8);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint32_t x0 = j ? v[0].y : v[0].x, x1 = j ? v[1].y : v[1].x, x2 = j ? v[2].y : v[2].x, x3 = j ? v[3].y : v[3].x;
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const uint32_t z0 = __byte_perm(x0, x1, h ? 0x7362 : 0x5140), z1 = __byte_perm(x2, x3, h ? 0x7362 : 0x5140);
-                    const uint32_t a0 = wide_lo(z0), a1 = wide_hi(z0), a2 = wide_lo(z1), a3 = wide_hi(z1);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][2 * j + h], a0, a1, a2, a3, w[nb][0], w[nb][1]);
+                    const float x0 = x[j][nb][2 * h], x1 = x[j][nb][2 * h + 1];
+                    sum[nb][0] += ex2(x0 - ref[nb][0]);
+                    sum[nb][1] += ex2(x1 - ref[nb][1]);
+                    w[j][nb][h] = transpose8(pack_h2(ex2(x0 + lv[j][h] - wref[nb][0]), ex2(x1 + lv[j][h] - wref[nb][1])));
                 }
-            }
-        } else {
+        // context: block b of a lane is its dims 2 b and 2 b + 1 of the pieces
 #pragma unroll
-            for (int c = 0; c < D / 128; ++c) {
-                uint32_t v[4][4];
+        for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint4 y = *reinterpret_cast<const uint4*>(vcodes + ((r * (D / 128) + c) * 32 + lane) * 16);
-                    v[r][0] = y.x;
-                    v[r][1] = y.y;
-                    v[r][2] = y.z;
-                    v[r][3] = y.w;
-                }
+            for (int c = 0; c < Sh::kVp; ++c)
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+                for (int k = 0; k < Sh::kVw; ++k)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t z0 = __byte_perm(v[0][j], v[1][j], h ? 0x7362 : 0x5140);
-                        const uint32_t z1 = __byte_perm(v[2][j], v[3][j], h ? 0x7362 : 0x5140);
+                        const uint32_t z0 = __byte_perm(vr[4 * j][c][k], vr[4 * j + 1][c][k], h ? 0x7362 : 0x5140);
+                        const uint32_t z1 = __byte_perm(vr[4 * j + 2][c][k], vr[4 * j + 3][c][k], h ? 0x7362 : 0x5140);
                         const uint32_t a0 = wide_lo(z0), a1 = wide_hi(z0), a2 = wide_lo(z1), a3 = wide_hi(z1);
 #pragma unroll
-                        for (int nb = 0; nb < NB; ++nb) mma16816(o[nb][8 * c + 2 * j + h], a0, a1, a2, a3, w[nb][0], w[nb][1]);
+                        for (int nb = 0; nb < NB; ++nb)
+                            mma16816(o[nb][8 * c + 2 * k + h], a0, a1, a2, a3, w[j][nb][0], w[j][nb][1]);
                     }
-            }
-        }
-        stage = stage + 1 == S ? 0 : stage + 1;
+        if (i + 1 < my_tiles) load_v();
+        next = after;
     }
-    copy_wait<0>();
     if (__any_sync(kFull, bad) && lane == 0 && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_PAGE);
 
     // ---- the warps are joined: weighted rows relative to ref, then references and sums
@@ -477,33 +553,59 @@ kv8_decode_kernel(const Kv8Args a)
     }
 }
 
-// The splits of a (sequence, query head) joined: D / 4 threads, splits in ascending order.
+// The splits of a (sequence, query head) joined: groups of D / 4 threads take the splits in turn, and are joined in
+// their order.
+constexpr int kJoinThreads = 128;
+
 template <int D>
-__global__ void __launch_bounds__(D / 4) kv8_combine_kernel(const Kv8Args a)
+__global__ void __launch_bounds__(kJoinThreads) kv8_combine_kernel(const Kv8Args a)
 {
+    constexpr int kLanes = D / 4, kJoin = kJoinThreads / kLanes;
+    __shared__ float s_m[kJoinThreads / 32];
+    __shared__ float s_l[kJoin];
+    __shared__ __align__(16) float s_o[kJoin][D];
     const kvq_kv8_problem& p = a.p;
     const int64_t row = (int64_t)blockIdx.y * p.n_qh + blockIdx.x;
     const int2 seen = seen_rows(p, blockIdx.y);
-    const int n = (int)(((int64_t)seen.y - seen.x + a.split_rows - 1) / a.split_rows);
-    const int d = threadIdx.x * 4;
+    const int n = (int)(((int64_t)seen.y - first_group(seen) + a.split_rows - 1) / a.split_rows);
+    const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
     grid_dependency_wait();
-    const float* ml = a.part_ml + row * a.n_splits * 2;
+    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.n_splits;
     const float* po = a.part_o + row * a.n_splits * D + d;
     float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, ml[2 * i]);
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) m = fmaxf(m, ml[i].x);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, s_m[w]);
     const float base = m == -INFINITY ? 0.0f : m;
     float l = 0.0f;
     float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-        const float wl = ml[2 * i + 1];
-        const float f = wl != wl ? wl : ex2(ml[2 * i] - base);
+    for (int i = grp; i < n; i += kJoin) {
+        const float2 x = ml[i];
+        const float f = x.y != x.y ? x.y : ex2(x.x - base);
         const float4 y = *reinterpret_cast<const float4*>(po + (int64_t)i * D);
-        l += wl * f;
+        l += x.y * f;
         acc.x = fmaf(y.x, f, acc.x);
         acc.y = fmaf(y.y, f, acc.y);
         acc.z = fmaf(y.z, f, acc.z);
         acc.w = fmaf(y.w, f, acc.w);
+    }
+    *reinterpret_cast<float4*>(&s_o[grp][d]) = acc;
+    if (d == 0) s_l[grp] = l;
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll
+    for (int k = 1; k < kJoin; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(&s_o[k][d]);
+        l += s_l[k];
+        acc.x += y.x;
+        acc.y += y.y;
+        acc.z += y.z;
+        acc.w += y.w;
     }
     const float r = l == 0.0f ? 0.0f : 1.0f / l;
     __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
@@ -524,12 +626,12 @@ Kv8Plan plan_kv8(const kvq_kv8_problem& p)
     // two blocks of eight heads share the rows' conversion; at 256 dims their accumulators do not fit
     q.nb = group > kHeads && p.cache.head_dim <= 128 ? 2 : 1;
     q.n_hb = (group + q.nb * kHeads - 1) / (q.nb * kHeads);
-    const int64_t most = p.window > 0 ? std::min(p.window, p.max_seq_len) : p.max_seq_len;
+    // rows from the first split's begin (a group ahead of the window's at most)
+    const int64_t most = p.window > 0 ? std::min<int64_t>((int64_t)p.window + kGroup - 1, p.max_seq_len) : p.max_seq_len;
     const int64_t units = (int64_t)p.n_seq * p.cache.n_kv * q.n_hb;
-    const int64_t slots = 2 * (int64_t)sm_count();
-    int64_t split = 4096;
-    if (p.n_seq == 1) split = (most * units + slots - 1) / slots;
-    else split = most * units / (slots * 8);
+    const int64_t slots = kCtas * (int64_t)sm_count();
+    // one sequence: a CTA for every slot; several, whose lengths are not known here: smaller ones, in turn
+    int64_t split = p.n_seq == 1 ? (most * units + slots - 1) / slots : most * units / (slots * 8);
     split = std::min<int64_t>(std::max<int64_t>(split, 128), 4096);
     split = std::max<int64_t>(split, (most + 65534) / 65535);
     split = (split + 127) / 128 * 128;
@@ -543,18 +645,26 @@ Kv8Plan plan_kv8(const kvq_kv8_problem& p)
     return q;
 }
 
-template <int D, int NB, int W, int S>
+template <int D, int NB, int R, int W, int C, bool GROUPED>
 cudaError_t launch_kv8_as(const Kv8Args& a, cudaStream_t s)
 {
-    constexpr int smem = Kv8Shape<D, NB, W, S>::kSmem;
-    cudaError_t e = cudaFuncSetAttribute(kv8_decode_kernel<D, NB, W, S>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    constexpr int smem = Kv8Shape<D, NB, R, W, C>::kSmem;
+    const auto kernel = kv8_decode_kernel<D, NB, R, W, C, GROUPED>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     const dim3 grid((unsigned)(a.p.cache.n_kv * a.n_hb), (unsigned)a.n_splits, (unsigned)a.p.n_seq);
-    kv8_decode_kernel<D, NB, W, S><<<grid, 32 * W, smem, s>>>(a);
+    kernel<<<grid, 32 * W, smem, s>>>(a);
     e = cudaGetLastError();
     if (e == cudaSuccess && a.n_splits > 1)
-        e = launch_dependent(kv8_combine_kernel<D>, dim3((unsigned)a.p.n_qh, (unsigned)a.p.n_seq), dim3(D / 4), 0, s, a);
+        e = launch_dependent(kv8_combine_kernel<D>, dim3((unsigned)a.p.n_qh, (unsigned)a.p.n_seq), dim3(kJoinThreads), 0, s, a);
     return e;
+}
+
+template <int D, int NB, int R, int W, int C>
+cudaError_t launch_kv8(const Kv8Args& a, cudaStream_t s)
+{
+    const bool grouped = !a.p.block_table || a.p.page_size % kGroup == 0;
+    return grouped ? launch_kv8_as<D, NB, R, W, C, true>(a, s) : launch_kv8_as<D, NB, R, W, C, false>(a, s);
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -573,7 +683,7 @@ int check_problem(const kvq_kv8_problem* p, const char* E)
     if (!std::isfinite(p->sm_scale)) return set_last_error(KVQ_EINVAL, "%s: sm_scale is not finite", E);
     if (p->block_table ? p->max_pages < 1 || p->page_size < 1 : p->seq_stride_rows < 0)
         return set_last_error(KVQ_EINVAL, "%s: bad paging sizes", E);
-    if (c.n_rows < 0) return set_last_error(KVQ_EINVAL, "%s: n_rows < 0", E);
+    if (c.n_rows < 0 || c.n_rows > INT32_MAX) return set_last_error(KVQ_EINVAL, "%s: n_rows outside [0, 2^31)", E);
     if (p->ldq < 0) return set_last_error(KVQ_EINVAL, "%s: ldq < 0", E);
     if (p->n_seq == 0) return KVQ_OK;
     if (!p->seq_len || !p->q || !c.k || !c.k_scale || !c.v || !c.v_scale)
@@ -624,9 +734,9 @@ int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* worksp
     const cudaStream_t s = (cudaStream_t)stream;
     cudaError_t e;
     switch (p->cache.head_dim) {
-        case 64: e = q.nb == 2 ? launch_kv8_as<64, 2, 8, 4>(a, s) : launch_kv8_as<64, 1, 8, 4>(a, s); break;
-        case 128: e = q.nb == 2 ? launch_kv8_as<128, 2, 8, 3>(a, s) : launch_kv8_as<128, 1, 8, 3>(a, s); break;
-        default: e = launch_kv8_as<256, 1, 4, 3>(a, s);
+        case 64: e = q.nb == 2 ? launch_kv8<64, 2, 32, 4, 3>(a, s) : launch_kv8<64, 1, 32, 4, 5>(a, s); break;
+        case 128: e = q.nb == 2 ? launch_kv8<128, 2, 16, 4, 2>(a, s) : launch_kv8<128, 1, 32, 4, 3>(a, s); break;
+        default: e = launch_kv8<256, 1, 16, 4, 2>(a, s);
     }
     return e == cudaSuccess ? KVQ_OK : set_last_error(KVQ_ECUDA, "%s: %s", E, cudaGetErrorString(e));
 }

@@ -1024,3 +1024,24 @@ def test_beam_search(kvq, orc, as_graph):
         free = host(f.d["free_list"])[:f.d["n_free"].item()].tolist()
         assert len(pages) + len(free) == n_pages and not pages & set(free)
     assert len({tuple(h) for h in history}) > R              # beams of a request differ
+
+
+@pytest.mark.parametrize("d,page", [(64, 0), (128, 0), (256, 16), (128, 48), (64, 20)])
+def test_decode_rows_behind_the_pool(kvq, d, page):
+    """A pool cut short: rows (without a table) or whole pages that it no longer holds are skipped, and flagged."""
+    c = Cache([400, 300], 2, d, page, 95)
+    cut = c.pool - 37
+    pl = {k: t[:, :cut].contiguous() for k, t in c.pl.items()}
+    q = queries(2, 8, d, 96)
+    p = kvq.make_kv8_problem(seq_len=dev(c.lens), q=q, sm_scale=1 / math.sqrt(d), max_seq_len=400, cache=pl, page_size=page,
+                             block_table=None if c.table is None else dev(c.table), seq_stride_rows=0 if page else c.stride)
+    st = i32(1)
+    out, lse = decode(kvq, p, st)
+
+    def rows_of(s, pos):
+        r = c.rows_of(s, pos)
+        last = (r // page + 1) * page - 1 if page else r
+        return np.where(last < cut, r, -1)
+    lost = any((rows_of(s, np.arange(int(n))) < 0).any() for s, n in enumerate(c.lens))
+    assert st.item() == (BAD_PAGE if lost else 0)
+    check_decode(out, lse, decode_ref(pl, q, c.lens, rows_of, 0, 1 / math.sqrt(d)), d, 400)
