@@ -30,15 +30,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr int kGroup = 16;               // rows of an instruction's tile
 constexpr int kHeads = 8;                // query heads of an n block
-constexpr int kCtas = 3;                 // CTAs an SM
+constexpr int kIdle = 1;                 // see unit_steps
 constexpr float kSlack = 10.0f;          // log2 by which a weight may pass 1 before the reference moves
 
 struct Kv8Args {
     kvq_kv8_problem p;
     int group, n_hb;                     // query heads a KV head; blocks of heads a KV head
-    int split_rows, n_splits;
-    float* part_ml;                      // [n_seq][n_qh][n_splits][2]: reference (log2), sum
-    float* part_o;                       // [n_seq][n_qh][n_splits][D]: sum of weighted rows
+    int line;                            // CTAs of a block of heads: what the line is cut into
+    int idle;                            // places of the line that stand for a unit's beginning
+    int4* info;                          // [line * n_hb]: sequence (-1: none), KV head and last CTA of the unit that the
+                                         // CTA began and did not end
+    float2* part_ml;                     // [line * n_hb][2][heads of a block]: reference (log2), sum of a unit's part: of
+                                         // the one that the CTA found begun, of the one that it left
+    float* part_o;                       // [line * n_hb][2][heads of a block][D]: sum of weighted rows
     __nv_bfloat16* out;
     float* lse;
     uint32_t* status;
@@ -100,6 +104,9 @@ __device__ __forceinline__ float pow2(int k)              // k in [-126, 127]
     return __int_as_float((k + 127) << 23);
 }
 
+// what a part of reference x.x and sum x.y counts against the reference `base` (a NaN head: no reference, its sum says it)
+__device__ __forceinline__ float part_weight(float2 x, float base) { return x.y != x.y ? x.y : ex2(x.x - base); }
+
 // bytes of the cache, read once
 __device__ __forceinline__ uint4 load16(const uint8_t* p)
 {
@@ -132,8 +139,32 @@ __device__ __forceinline__ int2 seen_rows(const kvq_kv8_problem& p, int s)
     return make_int2(p.window > 0 ? max(0, L - p.window) : 0, L);
 }
 
-// splits begin at a multiple of a group's rows: the first at or ahead of the first row that is seen
-__device__ __forceinline__ int first_group(const int2& seen) { return seen.x & ~(kGroup - 1); }
+// a unit's rows begin at a multiple of 16: the last at or ahead of the first row that is seen
+__host__ __device__ constexpr int first_group(int x) { return x & ~(kGroup - 1); }
+
+// The line.  A unit (a sequence and KV head) takes a place for every STEP rows and, where there are more places
+// than CTAs, kIdle places for what it costs to begin one; units follow one another, the KV heads of a sequence side by side.  CTA c of n has total / n
+// places, the first total % n one more: the same work for all, whatever the lengths, and a partial result only where a
+// cut falls into a unit (64 ragged sequences, 512 to 32768 rows: 198 us with splits of one size, which pay for their
+// beginnings, 186 us on the line).
+template <int STEP>
+__device__ __forceinline__ int unit_steps(const int2& seen) { return (seen.y - first_group(seen.x) + STEP - 1) / STEP; }
+template <int STEP>
+__device__ __forceinline__ int seq_places(const kvq_kv8_problem& p, int s, int idle)
+{
+    const int n = unit_steps<STEP>(seen_rows(p, s));
+    return n > 0 ? (n + idle) * p.cache.n_kv : 0;
+}
+
+struct Line {
+    int each, more;                      // places of a CTA; CTAs with one more
+    __device__ int begin(int c) const { return c * each + min(c, more); }
+    __device__ int cta(int place) const
+    {
+        const int wide = more * (each + 1);
+        return place < wide ? place / (each + 1) : more + (place - wide) / each;
+    }
+};
 
 // What the kernel is built from: D dims, NB blocks of eight heads, R rows a warp's tile, W warps, C CTAs an SM.
 template <int D, int NB, int R, int W, int C>
@@ -143,12 +174,13 @@ struct Kv8Shape {
     static constexpr int kVp = D == 64 ? 1 : D / 128;       // and of a V row (8 bytes at 64 dims)
     static constexpr int kVw = D == 64 ? 2 : 4;             // words of such a piece
     static constexpr int kHb = NB * kHeads;                 // heads of a CTA
+    static constexpr int kStep = W * R;                     // rows of a place of the line
     // the merge of the warps: weighted rows, then references and sums
     static constexpr int kSmem = W * kHb * (D + 2) * 4;
 };
 
-// One CTA: the rows [x, x + split_rows) of one sequence, one KV head, up to 8 NB query heads of it.  Its warps
-// take the tiles in turn, each with a softmax of its own, and are joined at the end.  GROUPED: 16 rows from a
+// One CTA: a stretch of the line for one block of up to 8 NB query heads of the KV heads on it.  In each unit its
+// warps take the tiles in turn, each with a softmax of its own, and are joined at the end.  GROUPED: 16 rows from a
 // multiple of 16 are neighbours in the pool (pages of a multiple of 16 rows, or no table), so that a group has one
 // address; otherwise every row has its own.
 template <int D, int NB, int R, int W, int C, bool GROUPED>
@@ -156,35 +188,143 @@ __global__ void __launch_bounds__(32 * W, C)
 kv8_decode_kernel(const Kv8Args a)
 {
     using Sh = Kv8Shape<D, NB, R, W, C>;
-    constexpr int kP = Sh::kKp, kBlocks = D / 16;       // m blocks of the context, k steps of the score
-    constexpr int kGroups = R / kGroup;
+    constexpr int kP = Sh::kKp, kBlocks = D / 16;           // m blocks of the context, k steps of the score
+    constexpr int kGroups = R / kGroup, kStep = Sh::kStep, kScan = 8;
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_sum[W];
+    __shared__ Line s_line;
+    __shared__ int4 s_at[W];                                // of a warp: place, end of the stretch, sequence, place in it
     grid_dependents_launch();
     const kvq_kv8_problem& p = a.p;
-    const int kv = blockIdx.x / a.n_hb, hb = blockIdx.x % a.n_hb;
-    const int split = blockIdx.y, s = blockIdx.z;
+    const int c = blockIdx.x / a.n_hb, hb = blockIdx.x % a.n_hb;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int heads = min(a.group - hb * Sh::kHb, Sh::kHb);           // query heads at hand
-    const int64_t head0 = (int64_t)s * p.n_qh + kv * a.group + hb * Sh::kHb;
-    const int2 seen = seen_rows(p, s);
-    const int64_t first64 = first_group(seen) + (int64_t)split * a.split_rows;
-    if (first64 >= seen.y) {
-        if (a.n_splits == 1) {
-            for (int i = threadIdx.x; i < heads * D; i += Sh::kThreads) a.out[head0 * D + i] = __float2bfloat16(0.0f);
-            if (a.lse)
-                for (int i = threadIdx.x; i < heads; i += Sh::kThreads) a.lse[head0 + i] = -INFINITY;
-        }
-        return;                                             // (the join goes by the lengths too)
-    }
-    const int first = (int)first64, end = (int)min((int64_t)seen.y, first64 + a.split_rows);
-    const int n_tiles = (end - first + R - 1) / R;
-    const int my_tiles = warp < n_tiles ? (n_tiles - warp + W - 1) / W : 0;
 
-    // where this lane's pieces of row 0 begin
-    const uint8_t* kc = p.cache.k + (int64_t)kv * p.cache.n_rows * D + 16 * t;
-    const uint8_t* vc = p.cache.v + (int64_t)kv * p.cache.n_rows * D + (D == 64 ? 8 : 16) * g;
-    const float* ks = p.cache.k_scale + (int64_t)kv * p.cache.n_rows;
-    const float* vs = p.cache.v_scale + (int64_t)kv * p.cache.n_rows;
+    // ---- this CTA's stretch of the line, and the sequence and place in it where it begins
+    {
+        int total = 0;
+        auto chunk_places = [&](int s0, int (&v)[kScan]) {  // of the sequences from s0 + kScan * threadIdx.x on
+            int sum = 0;
+#pragma unroll
+            for (int u = 0; u < kScan; ++u) {
+                const int q = s0 + (int)threadIdx.x * kScan + u;
+                v[u] = q < p.n_seq ? seq_places<kStep>(p, q, a.idle) : 0;
+                sum += v[u];
+            }
+            return sum;
+        };
+        // inclusive prefix sum over the CTA, and the CTA's sum
+        auto scan = [&](int v, int& all) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int u = __shfl_up_sync(kFull, v, o);
+                if (lane >= o) v += u;
+            }
+            __syncthreads();
+            if (lane == 31) s_sum[warp] = v;
+            __syncthreads();
+            all = 0;
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                if (w < warp) v += s_sum[w];
+                all += s_sum[w];
+            }
+            return v;
+        };
+        constexpr int kChunk = Sh::kThreads * kScan;
+        int v[kScan], mine = 0, incl = 0;
+        if (p.n_seq == 1) {
+            total = seq_places<kStep>(p, 0, a.idle);
+        } else {
+            for (int s0 = 0; s0 < p.n_seq; s0 += kChunk) {
+                int all;
+                mine = chunk_places(s0, v);
+                incl = scan(mine, all);
+                total += all;
+            }
+        }
+        const int n_line = max(1, min(a.line, total));      // (short lengths: fewer stretches, none of them empty)
+        const Line line{total / n_line, total % n_line};
+        const int at = c < n_line ? line.begin(c) : 0, stop = c < n_line ? line.begin(c + 1) : 0;
+        if (p.n_seq == 1) {
+            if (threadIdx.x < W) s_at[threadIdx.x] = make_int4(at, stop, 0, at);
+        } else if (at < stop) {
+            int before = 0;
+            for (int s0 = 0; s0 < p.n_seq; s0 += kChunk) {
+                int all = total;
+                if (p.n_seq > kChunk) {                     // (a single chunk's sums are still at hand)
+                    mine = chunk_places(s0, v);
+                    incl = scan(mine, all);
+                }
+                int from = before + incl - mine;
+                if (at >= from && at < from + mine) {
+#pragma unroll
+                    for (int u = 0; u < kScan; ++u) {
+                        if (at >= from && at < from + v[u])
+#pragma unroll
+                            for (int w = 0; w < W; ++w)
+                                s_at[w] = make_int4(at, stop, s0 + (int)threadIdx.x * kScan + u, at - from);
+                        from += v[u];
+                    }
+                }
+                before += all;
+                if (at < before) break;
+            }
+        } else if (threadIdx.x < W) {
+            s_at[threadIdx.x] = make_int4(0, 0, 0, 0);
+        }
+        if (threadIdx.x == 0) {
+            s_line = line;
+            if (a.info) a.info[blockIdx.x] = make_int4(-1, 0, 0, 0);
+        }
+        __syncthreads();
+    }
+
+    // ---- the piece of a unit at hand: rows [first, end) of sequence s, KV head kv
+    int s = 0, kv = 0, first = 0, end = 0, my_tiles = 0, part = 0;   // part: -1 a whole unit, 0 found begun, 1 begun here
+    int2 seen = make_int2(0, 0);
+    auto next_piece = [&]() -> bool {
+        int4 q = s_at[warp];                                // place, end of the stretch, sequence, place in it
+        bool found = false;
+        while (q.x < q.y && !found) {
+            seen = seen_rows(p, q.z);
+            const int n = unit_steps<kStep>(seen), per = n + a.idle;
+            if (n <= 0 || q.w >= per * p.cache.n_kv) {
+                q.w = 0;
+                // the next sequence that sees anything (there is one: the line goes on)
+                for (++q.z;; q.z += 32) {
+                    const bool some = q.z + lane >= p.n_seq || seen_rows(p, q.z + lane).y > 0;
+                    const unsigned who = __ballot_sync(kFull, some);
+                    if (who) {
+                        q.z += __ffs(who) - 1;
+                        break;
+                    }
+                }
+                continue;
+            }
+            kv = q.w / per;
+            const int inside = q.w - kv * per, take = min(per - inside, q.y - q.x);
+            const int g0 = max(inside - a.idle, 0), g1 = max(inside + take - a.idle, 0);
+            found = g1 > g0;
+            if (found) {
+                const int row0 = first_group(seen.x);
+                s = q.z;
+                first = row0 + g0 * kStep;
+                end = g1 == n ? seen.y : row0 + g1 * kStep;
+                const int n_tiles = (end - first + R - 1) / R;
+                my_tiles = warp < n_tiles ? (n_tiles - warp + W - 1) / W : 0;
+                part = g0 > 0 ? 0 : g1 < n ? 1 : -1;
+                // (the CTA of the unit's last place)
+                if (part == 1 && threadIdx.x == 0) a.info[blockIdx.x] = make_int4(s, kv, s_line.cta(q.x - inside + per - 1), 0);
+            }
+            q.x += take;
+            q.w += take;
+        }
+        __syncwarp();
+        if (lane == 0) s_at[warp] = q;
+        __syncwarp();
+        return found;
+    };
 
     // Pool row of a position, or of a group's first (a pool holds fewer than 2^31): -2 where there is none
     const int pool = (int)p.cache.n_rows;
@@ -217,11 +357,14 @@ kv8_decode_kernel(const Kv8Args a)
     bool bad = false;
     int base[GROUPED ? kGroups : 1];                        // pool rows of the groups (GROUPED: of all lanes alike)
     bool whole = false;
-    int lo = 0, hi = 0;                                     // GROUPED: rows of the tile to be read, where not whole
+    int64_t head_row = 0;                                   // the KV head's row 0 in the planes
+    // where this lane's pieces of a pool row begin
+    auto k_at = [&](int row) { return p.cache.k + (head_row + row) * D + 16 * t; };
+    auto v_at = [&](int row) { return p.cache.v + (head_row + row) * D + (D == 64 ? 8 : 16) * g; };
     // K and the scales of tile i, found by look_up(i)
     auto load_k = [&](int i, int found) {
         bad |= found == -2;
-        int64_t row;
+        int row;
         bool in;
         if constexpr (GROUPED) {
             const int pos0 = first + (warp + i * W) * R;
@@ -238,10 +381,9 @@ kv8_decode_kernel(const Kv8Args a)
 #pragma unroll
                 for (int e = 0; e < 2 * kGroups; ++e)
 #pragma unroll
-                    for (int c = 0; c < kP; ++c) kr[e][c] = load16(kc + ((int64_t)base[e / 2] + g) * D + (e % 2 * 8 * D + 64 * c));
+                    for (int c = 0; c < kP; ++c) kr[e][c] = load16(k_at(base[e / 2] + g) + (e % 2 * 8 * D + 64 * c));
             } else {
-                lo = seen.x - pos0;
-                hi = end - pos0;
+                const int lo = seen.x - pos0, hi = end - pos0;
                 const int r = lane % R, b = kGroups == 2 && r >= kGroup ? base[kGroups - 1] : base[0];
                 in = r >= lo && r < hi && b >= 0 && b + (r & (kGroup - 1)) < pool;
                 bad |= r >= lo && r < hi && b >= 0 && b + (r & (kGroup - 1)) >= pool;       // (no table: the pool may end anywhere)
@@ -251,7 +393,7 @@ kv8_decode_kernel(const Kv8Args a)
                     const bool on = mask >> (8 * e + g) & 1;
 #pragma unroll
                     for (int c = 0; c < kP; ++c)
-                        kr[e][c] = on ? load16(kc + ((int64_t)base[e / 2] + g) * D + (e % 2 * 8 * D + 64 * c)) : make_uint4(0u, 0u, 0u, 0u);
+                        kr[e][c] = on ? load16(k_at(base[e / 2] + g) + (e % 2 * 8 * D + 64 * c)) : make_uint4(0u, 0u, 0u, 0u);
                 }
             }
         } else {
@@ -263,11 +405,11 @@ kv8_decode_kernel(const Kv8Args a)
             for (int e = 0; e < 2 * kGroups; ++e) {
                 const int r = __shfl_sync(kFull, found, 8 * e + g);
 #pragma unroll
-                for (int c = 0; c < kP; ++c) kr[e][c] = r >= 0 ? load16(kc + (int64_t)r * D + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
+                for (int c = 0; c < kP; ++c) kr[e][c] = r >= 0 ? load16(k_at(r) + 64 * c) : make_uint4(0u, 0u, 0u, 0u);
             }
         }
-        k_scale = in ? __ldg(ks + row) : 0.0f;
-        v_scale = in ? __ldg(vs + row) : 0.0f;
+        k_scale = in ? __ldg(p.cache.k_scale + head_row + row) : 0.0f;
+        v_scale = in ? __ldg(p.cache.v_scale + head_row + row) : 0.0f;
     };
     // V of the tile whose K was loaded last
     auto load_v = [&]() {
@@ -278,23 +420,32 @@ kv8_decode_kernel(const Kv8Args a)
             const uint8_t* src;
             bool on = true;
             if constexpr (GROUPED) {
-                src = vc + ((int64_t)base[e / 4] + 2 * t) * D + in_group * D;
+                src = v_at(base[e / 4] + 2 * t) + in_group * D;
                 if (!whole) on = mask >> (kGroup * (e / 4) + in_group + 2 * t) & 1;
             } else {
                 const int r = __shfl_sync(kFull, base[0], kGroup * (e / 4) + in_group + 2 * t);
-                src = vc + (int64_t)r * D;
+                src = v_at(r);
                 on = r >= 0;
             }
 #pragma unroll
             for (int c = 0; c < Sh::kVp; ++c) load_piece<kStep>(vr[e][c], src + 128 * c, on);
         }
     };
-    int next = my_tiles > 1 ? look_up(1) : -1;
-    if (my_tiles > 0) {                                     // the first tile starts before the queries are read
-        load_k(0, look_up(0));
-        load_v();
-    }
+    int next = -1;
+    auto begin = [&]() {                                    // the piece's first tile is on its way
+        head_row = (int64_t)kv * p.cache.n_rows;
+        if (my_tiles > 0) {
+            load_k(0, look_up(0));
+            load_v();
+        }
+        next = my_tiles > 1 ? look_up(1) : -1;
+    };
 
+    bool more = next_piece();
+    if (more) begin();
+    while (more) {
+    const int64_t head0 = (int64_t)s * p.n_qh + kv * a.group + hb * Sh::kHb;
+    const int this_part = part;
     // Queries as the score's B operand.  bf16 has fp32's range, so a head is scaled by a power of two that puts
     // its largest element into [2^14, 2^15): elements down to 2^-31 of it are exact, the rest within 2^-39 of it.
     uint32_t qf[NB][kBlocks][2];
@@ -410,9 +561,9 @@ kv8_decode_kernel(const Kv8Args a)
                     }
                 over |= m > top[nb][e] || mw > wtop[nb][e];
             }
-        const bool part = now != ~0u;
-        if (__any_sync(kFull, over) || part) {              // (rare after the first tile)
-            if (part) {
+        const bool some = now != ~0u;
+        if (__any_sync(kFull, over) || some) {              // (rare after the first tile)
+            if (some) {
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j)
 #pragma unroll
@@ -490,7 +641,8 @@ kv8_decode_kernel(const Kv8Args a)
         if (i + 1 < my_tiles) load_v();
         next = after;
     }
-    if (__any_sync(kFull, bad) && lane == 0 && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_PAGE);
+    more = next_piece();
+    if (more) begin();
 
     // ---- the warps are joined: weighted rows relative to ref, then references and sums
     __syncthreads();
@@ -529,8 +681,7 @@ kv8_decode_kernel(const Kv8Args a)
 #pragma unroll
         for (int w = 0; w < W; ++w) {
             const float wl = ml[(w * Sh::kHb + h) * 2 + 1];
-            // (a NaN query: no reference was ever set, the sum says it)
-            const float f = wl != wl ? wl : ex2(ml[(w * Sh::kHb + h) * 2] - base);
+            const float f = part_weight(make_float2(ml[(w * Sh::kHb + h) * 2], wl), base);
             const float4 y = *reinterpret_cast<const float4*>(mo + (w * Sh::kHb + h) * D + d);
             l += wl * f;
             acc.x = fmaf(y.x, f, acc.x);
@@ -539,132 +690,198 @@ kv8_decode_kernel(const Kv8Args a)
             acc.w = fmaf(y.w, f, acc.w);
         }
         const int64_t row = head0 + h;
-        if (a.n_splits == 1) {
+        if (this_part < 0) {
             const float r = l == 0.0f ? 0.0f : 1.0f / l;
             __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
             dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
             dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
             if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
         } else {
-            const int64_t at = row * a.n_splits + split;
-            *reinterpret_cast<float4*>(a.part_o + at * D + d) = acc;
-            if (d == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m, l);
+            const int64_t to = ((int64_t)blockIdx.x * 2 + this_part) * Sh::kHb + h;
+            *reinterpret_cast<float4*>(a.part_o + to * D + d) = acc;
+            if (d == 0) a.part_ml[to] = make_float2(m, l);
+        }
+    }
+    }
+    if (__any_sync(kFull, bad) && lane == 0 && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_PAGE);
+
+    // ---- sequences that see nothing
+    for (int q = c; q < p.n_seq; q += a.line) {
+        if (seen_rows(p, q).y > 0) continue;
+        for (int i = threadIdx.x; i < p.cache.n_kv * heads * (D / 2); i += Sh::kThreads) {
+            const int h = i / (D / 2);
+            const int64_t row = (int64_t)q * p.n_qh + h / heads * a.group + hb * Sh::kHb + h % heads;
+            reinterpret_cast<uint32_t*>(a.out)[row * (D / 2) + i % (D / 2)] = 0u;
+            if (i % (D / 2) == 0 && a.lse) a.lse[row] = -INFINITY;
         }
     }
 }
 
-// The splits of a (sequence, query head) joined: groups of D / 4 threads take the splits in turn, and are joined in
-// their order.
-constexpr int kJoinThreads = 128;
-
-template <int D>
-__global__ void __launch_bounds__(kJoinThreads) kv8_combine_kernel(const Kv8Args a)
+// The parts of a unit joined, a CTA a query head: groups of D / 4 threads take the parts in turn, four of them in
+// flight, with a softmax each, and are joined in their order.  T threads: 512 where units have many parts (131072 rows
+// in 57 parts: the call 55.8 us, with 128 threads 61.4), 128 where they have few (64 ragged sequences: 186 us, 201).  The first part is what CTA c left, the others are
+// what the CTAs behind it found begun.
+template <int D, int T>
+__global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_heads)
 {
-    constexpr int kLanes = D / 4, kJoin = kJoinThreads / kLanes;
-    __shared__ float s_m[kJoinThreads / 32];
-    __shared__ float s_l[kJoin];
+    constexpr int kJoinThreads = T, kLanes = D / 4, kJoin = kJoinThreads / kLanes, kFlight = 4;
+    __shared__ float2 s_ml[kJoin];
     __shared__ __align__(16) float s_o[kJoin][D];
+    __shared__ int4 s_unit[kJoinThreads];
+    __shared__ unsigned s_some[kJoinThreads / 32];
     const kvq_kv8_problem& p = a.p;
-    const int64_t row = (int64_t)blockIdx.y * p.n_qh + blockIdx.x;
-    const int2 seen = seen_rows(p, blockIdx.y);
-    const int n = (int)(((int64_t)seen.y - first_group(seen) + a.split_rows - 1) / a.split_rows);
+    const int hb = blockIdx.x % a.n_hb, h = blockIdx.y;
     const int grp = threadIdx.x / kLanes, d = threadIdx.x % kLanes * 4;
+    if (hb * n_heads + h >= a.group) return;
+    // the units that one of some neighbouring CTAs of the line began and did not end, a CTA a thread
+    const int joins = gridDim.x / a.n_hb, mine = blockIdx.x / a.n_hb;
+    const int stop = (int)((mine + 1) * (int64_t)a.line / joins);
     grid_dependency_wait();
-    const float2* ml = reinterpret_cast<const float2*>(a.part_ml) + row * a.n_splits;
-    const float* po = a.part_o + row * a.n_splits * D + d;
-    float m = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) m = fmaxf(m, ml[i].x);
+    for (int first = (int)(mine * (int64_t)a.line / joins); first < stop; first += kJoinThreads) {
+        const int look = first + threadIdx.x;
+        const int4 found = look < stop ? a.info[look * a.n_hb + hb] : make_int4(-1, 0, 0, 0);
+        const unsigned some = __ballot_sync(kFull, found.x >= 0);
+        __syncthreads();                                    // (the last round's units are done with)
+        if (found.x >= 0) s_unit[threadIdx.x] = found;
+        if ((threadIdx.x & 31) == 0) s_some[threadIdx.x >> 5] = some;
+        __syncthreads();
+        for (int k = 0; k < kJoinThreads / 32; ++k) {
+            for (unsigned left = s_some[k]; left; left &= left - 1) {
+                const int at = 32 * k + __ffs(left) - 1;
+                const int4 unit = s_unit[at];
+                const int c = first + at, n = unit.z - c + 1;
+                float m = -INFINITY, l = 0.0f;
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                for (int i = grp; i < n; i += kJoin * kFlight) {
+                    float2 x[kFlight];
+                    float4 y[kFlight];
+                    float top = m;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-    if ((threadIdx.x & 31) == 0) s_m[threadIdx.x >> 5] = m;
-    __syncthreads();
+                    for (int u = 0; u < kFlight; ++u) {
+                        const int q = i + u * kJoin;
+                        const int64_t place = (((int64_t)(c + q) * a.n_hb + hb) * 2 + (q == 0)) * n_heads + h;
+                        x[u] = q < n ? a.part_ml[place] : make_float2(-INFINITY, 0.0f);
+                        y[u] = q < n ? *reinterpret_cast<const float4*>(a.part_o + place * D + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                    }
 #pragma unroll
-    for (int w = 0; w < kJoinThreads / 32; ++w) m = fmaxf(m, s_m[w]);
-    const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
-    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = grp; i < n; i += kJoin) {
-        const float2 x = ml[i];
-        const float f = x.y != x.y ? x.y : ex2(x.x - base);
-        const float4 y = *reinterpret_cast<const float4*>(po + (int64_t)i * D);
-        l += x.y * f;
-        acc.x = fmaf(y.x, f, acc.x);
-        acc.y = fmaf(y.y, f, acc.y);
-        acc.z = fmaf(y.z, f, acc.z);
-        acc.w = fmaf(y.w, f, acc.w);
+                    for (int u = 0; u < kFlight; ++u) top = fmaxf(top, x[u].x);
+                    const float base = top == -INFINITY ? 0.0f : top, f0 = ex2(m - base);
+                    m = top;
+                    l *= f0;
+                    acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
+#pragma unroll
+                    for (int u = 0; u < kFlight; ++u) {
+                        const float f = part_weight(x[u], base);
+                        l = fmaf(x[u].y, f, l);
+                        acc.x = fmaf(y[u].x, f, acc.x);
+                        acc.y = fmaf(y[u].y, f, acc.y);
+                        acc.z = fmaf(y[u].z, f, acc.z);
+                        acc.w = fmaf(y[u].w, f, acc.w);
+                    }
+                }
+                __syncthreads();                            // (the last unit is written)
+                *reinterpret_cast<float4*>(&s_o[grp][d]) = acc;
+                if (d == 0) s_ml[grp] = make_float2(m, l);
+                __syncthreads();
+                if (grp != 0) continue;
+#pragma unroll
+                for (int g = 1; g < kJoin; ++g) m = fmaxf(m, s_ml[g].x);
+                const float base = m == -INFINITY ? 0.0f : m;
+                l = 0.0f;
+                acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int g = 0; g < kJoin; ++g) {
+                    const float f = part_weight(s_ml[g], base);
+                    const float4 y = *reinterpret_cast<const float4*>(&s_o[g][d]);
+                    l = fmaf(s_ml[g].y, f, l);
+                    acc.x = fmaf(y.x, f, acc.x);
+                    acc.y = fmaf(y.y, f, acc.y);
+                    acc.z = fmaf(y.z, f, acc.z);
+                    acc.w = fmaf(y.w, f, acc.w);
+                }
+                const float r = l == 0.0f ? 0.0f : 1.0f / l;
+                const int64_t row = (int64_t)unit.x * p.n_qh + unit.y * a.group + hb * n_heads + h;
+                __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
+                dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
+                dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+                if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
+            }
+        }
     }
-    *reinterpret_cast<float4*>(&s_o[grp][d]) = acc;
-    if (d == 0) s_l[grp] = l;
-    __syncthreads();
-    if (grp != 0) return;
-#pragma unroll
-    for (int k = 1; k < kJoin; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>(&s_o[k][d]);
-        l += s_l[k];
-        acc.x += y.x;
-        acc.y += y.y;
-        acc.z += y.z;
-        acc.w += y.w;
-    }
-    const float r = l == 0.0f ? 0.0f : 1.0f / l;
-    __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
-    dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
-    dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
-    if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
 }
 
+// The kernel of a problem: blocks of eight heads a CTA (two share the rows' conversion; at 256 dims their
+// accumulators do not fit), rows a tile, warps, CTAs an SM (what the registers allow).
 struct Kv8Plan {
-    int nb = 1, n_hb = 1, split_rows = 0, n_splits = 0;
-    size_t off_o = 0, bytes = 0;
+    int nb = 1, n_hb = 1, line = 1;
+    bool cuts = false;                   // whether a unit can be cut
+    int joins = 1;                       // CTAs of the join, in all blocks of heads
+    int idle = 0;
+    size_t off_ml = 0, off_o = 0, bytes = 0;
 };
+
+template <int D, int NB, int R, int W, int C>
+struct Kv8Kind {
+    static constexpr int kStep = W * R, kHb = NB * kHeads;
+    using Shape = Kv8Shape<D, NB, R, W, C>;
+    static void plan(const kvq_kv8_problem& p, Kv8Plan& q)
+    {
+        const int group = p.n_qh / p.cache.n_kv;
+        q.nb = NB;
+        q.n_hb = (group + kHb - 1) / kHb;
+        // places of the longest unit (a window begins a group ahead of its first row at most)
+        const int64_t most = p.window > 0 ? std::min<int64_t>((int64_t)p.window + kGroup - 1, p.max_seq_len) : p.max_seq_len;
+        const int64_t steps = (most + kStep - 1) / kStep, units = (int64_t)p.n_seq * p.cache.n_kv;
+        q.cuts = steps > 1;
+        q.idle = units * steps > (int64_t)C * sm_count() / q.n_hb ? kIdle : 0;
+        q.line = (int)std::max<int64_t>(1, std::min<int64_t>(units * steps, (int64_t)C * sm_count() / q.n_hb));
+        q.joins = (int)std::min<int64_t>(units, q.line) * q.n_hb;
+        if (!q.cuts) return;
+        const size_t ctas = (size_t)q.line * q.n_hb;
+        q.off_ml = (ctas * sizeof(int4) + 255) / 256 * 256;
+        q.off_o = (q.off_ml + ctas * 2 * kHb * sizeof(float2) + 255) / 256 * 256;
+        q.bytes = q.off_o + ctas * 2 * kHb * D * sizeof(float);
+    }
+    template <bool GROUPED>
+    static cudaError_t launch_as(const Kv8Args& a, const Kv8Plan& q, cudaStream_t s)
+    {
+        const auto kernel = kv8_decode_kernel<D, NB, R, W, C, GROUPED>;
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
+        if (e != cudaSuccess) return e;
+        const unsigned ctas = (unsigned)(a.line * a.n_hb);
+        kernel<<<ctas, 32 * W, Shape::kSmem, s>>>(a);
+        e = cudaGetLastError();
+        if (e == cudaSuccess && q.cuts) {
+            const dim3 grid((unsigned)q.joins, (unsigned)std::min(a.group, kHb));
+            e = q.line >= 16 * (q.joins / q.n_hb) ? launch_dependent(kv8_combine_kernel<D, 512>, grid, dim3(512), 0, s, a, kHb)
+                                                  : launch_dependent(kv8_combine_kernel<D, 128>, grid, dim3(128), 0, s, a, kHb);
+        }
+        return e;
+    }
+    static cudaError_t launch(const Kv8Args& a, const Kv8Plan& q, cudaStream_t s)
+    {
+        const bool grouped = !a.p.block_table || a.p.page_size % kGroup == 0;
+        return grouped ? launch_as<true>(a, q, s) : launch_as<false>(a, q, s);
+    }
+};
+
+// f(kind) for the kind of a problem
+template <typename F>
+auto of_kind(const kvq_kv8_problem& p, F f)
+{
+    const bool two = p.n_qh / p.cache.n_kv > kHeads;
+    switch (p.cache.head_dim) {
+        case 64: return two ? f(Kv8Kind<64, 2, 32, 4, 3>()) : f(Kv8Kind<64, 1, 32, 4, 4>());
+        case 128: return two ? f(Kv8Kind<128, 2, 16, 4, 2>()) : f(Kv8Kind<128, 1, 32, 4, 3>());
+        default: return f(Kv8Kind<256, 1, 16, 4, 2>());
+    }
+}
 
 Kv8Plan plan_kv8(const kvq_kv8_problem& p)
 {
     Kv8Plan q;
-    const int group = p.n_qh / p.cache.n_kv;
-    // two blocks of eight heads share the rows' conversion; at 256 dims their accumulators do not fit
-    q.nb = group > kHeads && p.cache.head_dim <= 128 ? 2 : 1;
-    q.n_hb = (group + q.nb * kHeads - 1) / (q.nb * kHeads);
-    // rows from the first split's begin (a group ahead of the window's at most)
-    const int64_t most = p.window > 0 ? std::min<int64_t>((int64_t)p.window + kGroup - 1, p.max_seq_len) : p.max_seq_len;
-    const int64_t units = (int64_t)p.n_seq * p.cache.n_kv * q.n_hb;
-    const int64_t slots = kCtas * (int64_t)sm_count();
-    // one sequence: a CTA for every slot; several, whose lengths are not known here: smaller ones, in turn
-    int64_t split = p.n_seq == 1 ? (most * units + slots - 1) / slots : most * units / (slots * 8);
-    split = std::min<int64_t>(std::max<int64_t>(split, 128), 4096);
-    split = std::max<int64_t>(split, (most + 65534) / 65535);
-    split = (split + 127) / 128 * 128;
-    q.split_rows = (int)split;
-    q.n_splits = (int)std::max<int64_t>(1, (most + split - 1) / split);
-    if (q.n_splits > 1) {
-        const size_t rows = (size_t)p.n_seq * p.n_qh * q.n_splits;
-        q.off_o = (rows * 8 + 255) / 256 * 256;
-        q.bytes = q.off_o + rows * p.cache.head_dim * 4;
-    }
+    of_kind(p, [&](auto kind) { kind.plan(p, q); return 0; });
     return q;
-}
-
-template <int D, int NB, int R, int W, int C, bool GROUPED>
-cudaError_t launch_kv8_as(const Kv8Args& a, cudaStream_t s)
-{
-    constexpr int smem = Kv8Shape<D, NB, R, W, C>::kSmem;
-    const auto kernel = kv8_decode_kernel<D, NB, R, W, C, GROUPED>;
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
-    const dim3 grid((unsigned)(a.p.cache.n_kv * a.n_hb), (unsigned)a.n_splits, (unsigned)a.p.n_seq);
-    kernel<<<grid, 32 * W, smem, s>>>(a);
-    e = cudaGetLastError();
-    if (e == cudaSuccess && a.n_splits > 1)
-        e = launch_dependent(kv8_combine_kernel<D>, dim3((unsigned)a.p.n_qh, (unsigned)a.p.n_seq), dim3(kJoinThreads), 0, s, a);
-    return e;
-}
-
-template <int D, int NB, int R, int W, int C>
-cudaError_t launch_kv8(const Kv8Args& a, cudaStream_t s)
-{
-    const bool grouped = !a.p.block_table || a.p.page_size % kGroup == 0;
-    return grouped ? launch_kv8_as<D, NB, R, W, C, true>(a, s) : launch_kv8_as<D, NB, R, W, C, false>(a, s);
 }
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -685,6 +902,9 @@ int check_problem(const kvq_kv8_problem* p, const char* E)
         return set_last_error(KVQ_EINVAL, "%s: bad paging sizes", E);
     if (c.n_rows < 0 || c.n_rows > INT32_MAX) return set_last_error(KVQ_EINVAL, "%s: n_rows outside [0, 2^31)", E);
     if (p->ldq < 0) return set_last_error(KVQ_EINVAL, "%s: ldq < 0", E);
+    // (the line counts places of 64 rows or more in 32 bits)
+    if ((int64_t)p->n_seq * c.n_kv * (p->max_seq_len / 64 + 2) > INT32_MAX)
+        return set_last_error(KVQ_EINVAL, "%s: n_seq * n_kv * max_seq_len beyond 2^37", E);
     if (p->n_seq == 0) return KVQ_OK;
     if (!p->seq_len || !p->q || !c.k || !c.k_scale || !c.v || !c.v_scale)
         return set_last_error(KVQ_EINVAL, "%s: NULL pointer", E);
@@ -725,19 +945,14 @@ int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* worksp
     if (q.bytes && (!workspace || ws_bytes < q.bytes))
         return set_last_error(KVQ_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", E, workspace ? ws_bytes : (size_t)0, q.bytes);
     if (q.bytes && !aligned(workspace, 256)) return set_last_error(KVQ_EALIGN, "%s: workspace not 256-byte aligned", E);
-    Kv8Args a{*p, p->n_qh / p->cache.n_kv, q.n_hb, q.split_rows, q.n_splits, nullptr, nullptr,
-              static_cast<__nv_bfloat16*>(out), lse, dev_status};
+    Kv8Args a{*p, p->n_qh / p->cache.n_kv, q.n_hb, q.line, q.idle, nullptr, nullptr, nullptr, static_cast<__nv_bfloat16*>(out), lse, dev_status};
     if (q.bytes) {
-        a.part_ml = static_cast<float*>(workspace);
-        a.part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + q.off_o);
+        uint8_t* ws = static_cast<uint8_t*>(workspace);
+        a.info = reinterpret_cast<int4*>(ws);
+        a.part_ml = reinterpret_cast<float2*>(ws + q.off_ml);
+        a.part_o = reinterpret_cast<float*>(ws + q.off_o);
     }
-    const cudaStream_t s = (cudaStream_t)stream;
-    cudaError_t e;
-    switch (p->cache.head_dim) {
-        case 64: e = q.nb == 2 ? launch_kv8<64, 2, 32, 4, 3>(a, s) : launch_kv8<64, 1, 32, 4, 5>(a, s); break;
-        case 128: e = q.nb == 2 ? launch_kv8<128, 2, 16, 4, 2>(a, s) : launch_kv8<128, 1, 32, 4, 3>(a, s); break;
-        default: e = launch_kv8<256, 1, 16, 4, 2>(a, s);
-    }
+    const cudaError_t e = of_kind(*p, [&](auto kind) { return kind.launch(a, q, (cudaStream_t)stream); });
     return e == cudaSuccess ? KVQ_OK : set_last_error(KVQ_ECUDA, "%s: %s", E, cudaGetErrorString(e));
 }
 
