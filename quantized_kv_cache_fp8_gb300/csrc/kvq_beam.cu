@@ -6,10 +6,9 @@
 // logarithm and picks the n_out best of all chunks' candidates.  Bound by the logits' bytes, with an exponential an
 // element not far behind (two bytes at the copy's rate take as long as 0.6 of a MUFU operation).
 //
-// Best k of the values that a CTA holds: each warp finds the r-th largest of its threads' maxima,
-// r = ceil(k / warps); at least k values reach the least of these, so that nothing below it can be among the best k.
-// What reaches it (a few times k, unless many values are equal) is gathered and ranked by counting.  Where it does
-// not fit the buffer, the best are taken one by one instead.
+// Best k of the values that a CTA holds: k of its threads' maxima reach some level, so that nothing below it can be
+// among the best k (floor_of).  What reaches it (little more than k, unless many values are equal) is gathered and
+// ranked by counting.  Where it does not fit the buffer, the best are taken one by one instead.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -25,6 +24,7 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kMaxBeam = 64, kMaxOut = 128, kMaxVocab = 1 << 24;
 constexpr int kBuffer = 1024;            // gathered candidates
+constexpr int kVectors = 512;            // gathered vectors
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLarge = 1e30f;          // logits from here on are subtracted before they are scaled
 
@@ -32,7 +32,7 @@ struct BeamArgs {
     kvq_beam_problem p;
     int n_chunk;
     float* part_m;                       // [n_req * n_beam][n_chunk]: the chunk's largest logit
-    double* part_s;                      // [n_req * n_beam][n_chunk]: sum of exp(x - that), up to the rounding of that times log2 e; NaN: not finite
+    float2* part_s;                      // [n_req * n_beam][n_chunk]: sum of exp(x - that) in two floats; NaN: not finite
     uint64_t* part_key;                  // [n_req * n_beam][n_chunk][n_out]: candidates, 0: none
     uint32_t* status;
 };
@@ -44,16 +44,6 @@ __device__ __forceinline__ uint32_t ordered(float x)
     return b ^ ((int32_t)b < 0 ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k ^ ((int32_t)k < 0 ? 0x80000000u : 0xffffffffu)); }
-__device__ __forceinline__ uint64_t ordered(double x)
-{
-    const uint64_t b = (uint64_t)__double_as_longlong(x + 0.0);
-    return b ^ ((int64_t)b < 0 ? ~0ull : 1ull << 63);
-}
-__device__ __forceinline__ double unordered(uint64_t k)
-{
-    return __longlong_as_double((long long)(k ^ ((int64_t)k < 0 ? 1ull << 63 : ~0ull)));
-}
-
 __device__ __forceinline__ float ex2(float x)
 {
     float r;
@@ -61,16 +51,67 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
-// the r-th largest of the warp's keys, counted with their multiplicity (0 if fewer are not 0)
-__device__ __forceinline__ uint32_t rth_largest(uint32_t key, int r)
+// the r-th largest of the warp's keys, counted with their multiplicity (0 if fewer are not 0), and the first `keep`
+// of them into `to`
+__device__ __forceinline__ uint32_t rth_largest(uint32_t key, int r, uint32_t* to = nullptr)
 {
     uint32_t m = 0;
     for (int i = 0; i < r; ++i) {
         m = __reduce_max_sync(kFull, key);
         const unsigned who = __ballot_sync(kFull, key == m);
         if ((threadIdx.x & 31) == __ffs(who) - 1) key = 0;
+        if (to && (threadIdx.x & 31) == 0) to[i] = m;
     }
     return m;
+}
+
+// A level that k of the CTA's keys reach, one a thread (0, if fewer than k are not 0).  Up to 16: the k-th largest of
+// each warp's four largest, which is the k-th largest of all but where one warp holds more than four of those.
+// More: the least of the warps' (k / warps)-th largest.  put_floor, a barrier, get_floor; s: 32 entries.
+__device__ __forceinline__ void put_floor(uint32_t key, int k, uint32_t* s)
+{
+    const int warp = threadIdx.x >> 5;
+    if (k <= 16) {
+        (void)rth_largest(key, 4, s + 4 * warp);
+    } else {
+        const uint32_t m = rth_largest(key, (k + kWarps - 1) / kWarps);
+        if ((threadIdx.x & 31) == 0) s[warp] = m;
+    }
+}
+__device__ __forceinline__ uint32_t get_floor(int k, const uint32_t* s)
+{
+    if (k <= 16) return rth_largest(s[threadIdx.x & 31], k);
+    uint32_t least = s[0];
+#pragma unroll
+    for (int w = 1; w < kWarps; ++w) least = min(least, s[w]);
+    return least;
+}
+
+// s += x, what the addition rounds off gathered in lo (exact whichever is the larger: Knuth, 1969)
+__device__ __forceinline__ void add_exact(float& s, float& lo, float x)
+{
+    const float t = __fadd_rn(s, x), z = __fsub_rn(t, s);
+    lo += __fadd_rn(__fsub_rn(s, __fsub_rn(t, z)), __fsub_rn(x, z));
+    s = t;
+}
+
+// sum += (x + lo_x) f, in two floats
+__device__ __forceinline__ void add_scaled(float& sum, float& lo, float2 x, float f)
+{
+    const float y = x.x * f;
+    lo += fmaf(x.x, f, -y) + x.y * f;
+    add_exact(sum, lo, y);
+}
+
+// the warp's sum of (sum + lo), in two floats
+__device__ __forceinline__ void warp_sum(float& sum, float& lo)
+{
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) {
+        const float s2 = __shfl_xor_sync(kFull, sum, o), l2 = __shfl_xor_sync(kFull, lo, o);
+        add_exact(sum, lo, s2);
+        lo += l2;
+    }
 }
 
 // whether beam b of request r has candidates of its own logits
@@ -80,118 +121,192 @@ __device__ __forceinline__ bool reads_logits(const kvq_beam_problem& p, int64_t 
     return s > -INFINITY && s < INFINITY && !(p.finished && p.finished[row]);
 }
 
+// 16 bytes of a row as values
 template <typename X>
-__device__ __forceinline__ float widen(X x);
+struct Vec;
 template <>
-__device__ __forceinline__ float widen(float x) { return x; }
+struct __align__(16) Vec<float> {
+    static constexpr int kN = 4;
+    uint32_t w[4];
+    __device__ float get(int i) const { return __uint_as_float(w[i]); }
+    __device__ void set(int i, float x) { w[i] = __float_as_uint(x); }
+    __device__ float largest() const { return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3))); }
+    static __device__ float load(const float* p) { return *p; }
+};
 template <>
-__device__ __forceinline__ float widen(__nv_bfloat16 x) { return __bfloat162float(x); }
+struct __align__(16) Vec<__nv_bfloat16> {
+    static constexpr int kN = 8;
+    uint32_t w[4];
+    __device__ float get(int i) const { return __uint_as_float(i % 2 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16); }
+    __device__ void set(int i, float x)                     // (a bfloat16's value)
+    {
+        const uint32_t b = __float_as_uint(x);
+        w[i / 2] = i % 2 ? (w[i / 2] & 0xFFFFu) | (b & 0xFFFF0000u) : (w[i / 2] & 0xFFFF0000u) | b >> 16;
+    }
+    __device__ float largest() const                        // packed maxima pass over NaNs, as fmaxf does
+    {
+        uint32_t a, b;
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(w[0]), "r"(w[1]));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(b) : "r"(w[2]), "r"(w[3]));
+        asm("max.bf16x2 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(b));
+        return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
+    }
+    static __device__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+};
 
-// VPT values a thread; VEC: rows are 16-byte aligned
-template <typename X, int VPT, bool VEC>
-__global__ void __launch_bounds__(kThreads) beam_chunk_kernel(const BeamArgs a)
+// sum of 2^(x l - c) over a vector, two values at a time
+template <typename V>
+__device__ __forceinline__ float exp_sum(const V& v, float c)
 {
-    constexpr int kE = VEC ? 16 / (int)sizeof(X) : 1;       // consecutive elements a load
-    constexpr int kChunk = kThreads * VPT;
-    __shared__ uint32_t s_t[kWarps];
+    uint64_t acc = 0, l2, c2;
+    asm("mov.b64 %0, {%1, %1};" : "=l"(l2) : "f"(kLog2e));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(c2) : "f"(-c));
+#pragma unroll
+    for (int i = 0; i < V::kN; i += 2) {
+        uint64_t x;
+        float a, b;
+        asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(v.get(i)), "f"(v.get(i + 1)));
+        asm("fma.rn.f32x2 %0, %0, %1, %2;" : "+l"(x) : "l"(l2), "l"(c2));
+        asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+        asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(ex2(a)), "f"(ex2(b)));
+        if (i == 0) acc = x;
+        else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(acc) : "l"(x));
+    }
+    float a, b;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(acc));
+    return a + b;
+}
+
+// NV vectors a thread.  Vectors begin at multiples of 16 bytes: `lead` elements of the first lie ahead of the row.
+template <typename X, int NV>
+__global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs a)
+{
+    using V = Vec<X>;
+    constexpr int kE = V::kN, kChunk = kThreads * NV * kE;
+    __shared__ uint32_t s_floor[32];
     __shared__ float s_m[kWarps];
-    __shared__ double s_sum[kWarps];
+    __shared__ float2 s_sum[kWarps];
     __shared__ int s_n;
+    __shared__ int s_vecs;
     __shared__ uint64_t s_best[kWarps];
     __shared__ uint64_t s_key[kBuffer];
+    __shared__ V s_vec[kVectors];
+    __shared__ int s_at[kVectors];
     const kvq_beam_problem& p = a.p;
     const int64_t row = blockIdx.x;
     grid_dependents_launch();
     if (!reads_logits(p, row)) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int c0 = blockIdx.y * kChunk;
     const X* src = static_cast<const X*>(p.logits) + row * p.ld;
+    const int lead = (int)((uintptr_t)src % 16 / sizeof(X));
+    const int c0 = (int)blockIdx.y * kChunk - lead;
     const int k = p.n_out;
 
-    float x[VPT];
+    V x[NV];
 #pragma unroll
-    for (int j = 0; j < VPT / kE; ++j) {
+    for (int j = 0; j < NV; ++j) {
         const int at = c0 + (j * kThreads + tid) * kE;
-        if constexpr (VEC) {
-            if (at + kE <= p.vocab) {
-                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src + at));
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        if (at >= 0 && at + kE <= p.vocab) {
+            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src + at));
+            x[j].w[0] = w.x;
+            x[j].w[1] = w.y;
+            x[j].w[2] = w.z;
+            x[j].w[3] = w.w;
+        } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    if constexpr (sizeof(X) == 2) {
-                        x[j * kE + 2 * e] = __uint_as_float(u[e] << 16);
-                        x[j * kE + 2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
-                    } else {
-                        x[j * kE + e] = __uint_as_float(u[e]);
-                    }
-                }
-                continue;
-            }
+            for (int e = 0; e < kE; ++e) x[j].set(e, at + e >= 0 && at + e < p.vocab ? V::load(src + at + e) : -INFINITY);
         }
-#pragma unroll
-        for (int e = 0; e < kE; ++e) x[j * kE + e] = at + e < p.vocab ? widen(src[at + e]) : -INFINITY;
     }
-    auto index_of = [&](int v) { return c0 + ((v / kE) * kThreads + tid) * kE + v % kE; };
-
-    float mine = -INFINITY;
+    float most[NV], mine = -INFINITY;
 #pragma unroll
-    for (int v = 0; v < VPT; ++v) mine = fmaxf(mine, x[v]);
+    for (int j = 0; j < NV; ++j) {
+        most[j] = x[j].largest();
+        mine = fmaxf(mine, most[j]);
+    }
     const uint32_t my_key = mine > -INFINITY ? ordered(mine) : 0u;
-    const uint32_t wt = rth_largest(my_key, (k + kWarps - 1) / kWarps);
     const uint32_t wm = __reduce_max_sync(kFull, my_key);
-    if (lane == 0) {
-        s_t[warp] = wt;
-        s_m[warp] = wm ? unordered(wm) : -INFINITY;
-    }
-    if (tid == 0) s_n = 0;
-    __syncthreads();
-    uint32_t floor_key = s_t[0];
-    float m = s_m[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) {
-        floor_key = min(floor_key, s_t[w]);
-        m = fmaxf(m, s_m[w]);
-    }
+    if (tid == 0) s_n = s_vecs = 0;
+    put_floor(my_key, k, s_floor);
 
-    // exp(x - m) as 2^(x l - c), one fused multiply-add: l = log2 e in fp32, c = m l rounded; what the
-    // rounding of c took is the same factor for all and is put back by the merge
-    float sum = 0.0f;
+    // exp(y - m), m the warp's largest, as 2^(y l - c), one fused multiply-add: l = log2 e in fp32, c = m l rounded.
+    // What the rounding of c took is the same factor for all and is put back below.
+    const float m = wm ? unordered(wm) : -INFINITY;
+    float sum = 0.0f, low = 0.0f;
     if (fabsf(m) < kLarge) {
         const float c = __fmul_rn(m, kLog2e);
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) sum += ex2(fmaf(x[v], kLog2e, -c));
-    } else if (m != -INFINITY) {                            // (m l may not be finite)
-#pragma unroll
-        for (int v = 0; v < VPT; ++v) sum += ex2((x[v] - m) * kLog2e);
+        for (int j = 0; j < NV; ++j) add_exact(sum, low, exp_sum(x[j], c));
     } else {
 #pragma unroll
-        for (int v = 0; v < VPT; ++v) sum += x[v] == -INFINITY ? 0.0f : x[v];      // nothing, or NaN
-    }
-    double ds = sum;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) ds += __shfl_xor_sync(kFull, ds, o);
-    if (lane == 0) s_sum[warp] = ds;
-
-    if (my_key != 0 && my_key >= floor_key) {
-        const float low = floor_key ? unordered(floor_key) : -INFINITY;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-            if (x[v] >= low && x[v] > -INFINITY) {
-                const int i = atomicAdd(&s_n, 1);
-                if (i < kBuffer) s_key[i] = (uint64_t)ordered(x[v]) << 32 | (uint32_t)~index_of(v);
+        for (int j = 0; j < NV; ++j)
+#pragma unroll 1
+            for (int e = 0; e < kE; ++e) {
+                const uint32_t w = sizeof(X) == 2 ? e / 2 : e;
+                const uint32_t b = w == 0 ? x[j].w[0] : w == 1 ? x[j].w[1] : w == 2 ? x[j].w[2] : x[j].w[3];
+                const float y = __uint_as_float(sizeof(X) == 4 ? b : e % 2 ? b & 0xFFFF0000u : b << 16);
+                // m l may not be finite; without a maximum there is nothing, or a NaN
+                sum += m != -INFINITY ? ex2((y - m) * kLog2e) : y == -INFINITY ? 0.0f : y;
             }
+    }
+    warp_sum(sum, low);
+    if (lane == 0) {
+        s_m[warp] = m;
+        s_sum[warp] = make_float2(sum, low);
+    }
+    __syncthreads();
+
+    // vectors with something at or above the floor (few): their elements are looked at together, further down
+    const uint32_t floor_key = get_floor(k, s_floor);
+    const float least = floor_key ? unordered(floor_key) : -INFINITY;
+    if (my_key != 0 && my_key >= floor_key) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (most[j] >= least && most[j] > -INFINITY) {
+                const int i = atomicAdd(&s_vecs, 1);
+                if (i < kVectors) {
+                    s_vec[i] = x[j];
+                    s_at[i] = c0 + (j * kThreads + tid) * kE;
+                }
+            }
+    }
+    const int64_t at = row * a.n_chunk + blockIdx.y;
+    if (warp == kWarps - 1) {                               // the chunk's sum, a warp's a lane
+        const float mw = lane < kWarps ? s_m[lane] : -INFINITY;
+        float2 sw = lane < kWarps ? s_sum[lane] : make_float2(0.0f, 0.0f);
+        float all = mw;
+#pragma unroll
+        for (int o = 16; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, o));
+        // The rounding of c in nats is exact as a fused multiply-add but for its last factor.  Its exponential is its
+        // series (to 2^-32) but for logits beyond 2^13.
+        const float off = fabsf(mw) < kLarge ? -0.6931471805599453f * fmaf(mw, kLog2e, -__fmul_rn(mw, kLog2e)) : 0.0f;
+        if (fabsf(off) < 0x1p-10f) {
+            sw.y = fmaf(sw.x, off * fmaf(0.5f, off, 1.0f), sw.y);
+        } else {
+            const float f = expf(off);
+            sw = make_float2(sw.x * f, sw.y * f);
+        }
+        float t = 0.0f, lo = 0.0f;
+        // (a sum of 0 has no maximum; that of the maximum's warp stays as it is)
+        if (sw.x != 0.0f) add_scaled(t, lo, sw, mw == all ? 1.0f : expf(mw - all));
+        warp_sum(t, lo);
+        if (lane == 0) {
+            a.part_m[at] = all;
+            a.part_s[at] = make_float2(t, lo);
+        }
+    }
+    __syncthreads();
+    const int vecs = s_vecs;
+    for (int i = tid; i < min(vecs, kVectors) * kE; i += kThreads) {
+        const float y = s_vec[i / kE].get(i % kE);
+        if (y >= least && y > -INFINITY) {
+            const int at = atomicAdd(&s_n, 1);
+            if (at < kBuffer) s_key[at] = (uint64_t)ordered(y) << 32 | (uint32_t)~(s_at[i / kE] + i % kE);
+        }
     }
     __syncthreads();
     const int n = s_n;
-    const int64_t at = row * a.n_chunk + blockIdx.y;
-    if (tid == 0) {
-        double t = 0.0;
-        for (int w = 0; w < kWarps; ++w) t += s_sum[w];
-        a.part_m[at] = m;
-        a.part_s[at] = t;
-    }
     uint64_t* out = a.part_key + at * k;
-    if (n <= kBuffer) {
+    if (vecs <= kVectors && n <= kBuffer) {
         for (int i = tid; i < n; i += kThreads) {
             const uint64_t key = s_key[i];
             int rank = 0;
@@ -201,15 +316,15 @@ __global__ void __launch_bounds__(kThreads) beam_chunk_kernel(const BeamArgs a)
         for (int i = n + tid; i < k; i += kThreads) out[i] = 0;
         return;
     }
-    // too many equal values: the best one by one
+    // too many equal values: the best one by one, of a thread's elements read again
     uint64_t last = ~0ull, best = 0;
     bool stale = true;
     for (int i = 0; i < k; ++i) {
         if (stale) {
             best = 0;
-#pragma unroll
-            for (int v = 0; v < VPT; ++v) {
-                const uint64_t key = x[v] > -INFINITY ? (uint64_t)ordered(x[v]) << 32 | (uint32_t)~index_of(v) : 0;
+            for (int t = max(c0, 0) + tid; t < min(c0 + kChunk, p.vocab); t += kThreads) {
+                const float y = V::load(src + t);
+                const uint64_t key = y > -INFINITY ? (uint64_t)ordered(y) << 32 | (uint32_t)~t : 0;
                 if (key < last && key > best) best = key;
             }
         }
@@ -227,7 +342,7 @@ __global__ void __launch_bounds__(kThreads) beam_chunk_kernel(const BeamArgs a)
     }
 }
 
-// A candidate of any beam: value, then beam (ascending), logit (descending), token (ascending)
+// A candidate of any beam: value (as two floats, ordered), then beam (ascending), logit (descending), token (ascending)
 struct Cand {
     uint64_t v, t;
 };
@@ -235,9 +350,10 @@ __device__ __forceinline__ bool above(const Cand& a, const Cand& b) { return a.v
 
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
 {
-    __shared__ double s_base[kMaxBeam];                     // score - log sum exp
+    __shared__ float2 s_base[kMaxBeam];                     // sum of exponentials, then score - its logarithm, in two floats
+    __shared__ float s_max[kMaxBeam];
     __shared__ uint8_t s_live[kMaxBeam];                    // 0: no candidates; 1: its tokens; 2: finished
-    __shared__ uint32_t s_t[kWarps];
+    __shared__ uint32_t s_floor[32];
     __shared__ int s_n;
     __shared__ Cand s_best[kWarps];
     __shared__ Cand s_c[kBuffer];
@@ -246,78 +362,88 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     const int64_t row0 = (int64_t)blockIdx.x * p.n_beam;
     const int k = p.n_out, per_beam = a.n_chunk * k;
     if (tid == 0) s_n = 0;
+    float score = 0.0f;                                     // of beam `tid` (inputs: read ahead of the wait)
+    int live = 0;
+    if (tid < p.n_beam) {
+        score = p.score[row0 + tid];
+        if (score > -INFINITY && score < INFINITY) live = p.finished && p.finished[row0 + tid] ? 2 : 1;
+        s_base[tid] = make_float2(score, 0.0f);
+        s_live[tid] = (uint8_t)live;
+        if (!(score < INFINITY) && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_VALUE);      // NaN or +inf
+    }
+    __syncthreads();
     grid_dependency_wait();
     for (int b = warp; b < p.n_beam; b += kWarps) {
-        const int64_t row = row0 + b;
-        const float score = p.score[row];
-        bool bad = !(score < INFINITY);                     // NaN or +inf
-        int live = 0;
-        double base = score;
-        if (!bad && score > -INFINITY) {
-            if (p.finished && p.finished[row]) {
-                live = 2;
-            } else {
-                float m = -INFINITY;
-                for (int c = lane; c < a.n_chunk; c += 32) m = fmaxf(m, a.part_m[row * a.n_chunk + c]);
+        if (s_live[b] != 1) continue;
+        const int64_t at = (row0 + b) * a.n_chunk;
+        float m = -INFINITY;
+        for (int c = lane; c < a.n_chunk; c += 32) m = fmaxf(m, a.part_m[at + c]);
 #pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-                double s = 0.0;
-                for (int c = lane; c < a.n_chunk; c += 32) {
-                    const double sc = a.part_s[row * a.n_chunk + c];
-                    const float mc = a.part_m[row * a.n_chunk + c];
-                    // (the product of two floats is exact in 64 bits, and so is the rounding that it shows)
-                    const double off = fabsf(mc) < kLarge ? (double)__fmul_rn(mc, kLog2e) - (double)mc * (double)kLog2e : 0.0;
-                    s += sc == 0.0 ? 0.0 : sc * exp(((double)mc - (double)m) + off * 0.6931471805599453);
-                }
-#pragma unroll
-                for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
-                bad = s != s;
-                live = !bad && s > 0.0;
-                if (live) base = (double)score - ((double)m + log(s));
-            }
+        for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+        float s = 0.0f, lo = 0.0f;
+        for (int c = lane; c < a.n_chunk; c += 32) {
+            const float2 sc = a.part_s[at + c];
+            const float mc = a.part_m[at + c];
+            // (the chunk of the maximum as it is, the others by an fp32 exponential as all terms are)
+            if (sc.x != 0.0f) add_scaled(s, lo, sc, mc == m ? 1.0f : expf(mc - m));
         }
+        warp_sum(s, lo);
         if (lane == 0) {
-            s_base[b] = base;
-            s_live[b] = (uint8_t)live;
-            if (bad && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_VALUE);
+            s_max[b] = m;
+            s_base[b] = make_float2(s, lo);
+        }
+    }
+    __syncthreads();
+    // (64-bit arithmetic is slow here: one warp does it for all beams, a lane each)
+    if (tid < p.n_beam && s_live[tid] == 1) {
+        const float2 s = s_base[tid];
+        if (s.x > 0.0f) {
+            const double base = (double)score - ((double)s_max[tid] + log((double)s.x + (double)s.y));
+            s_base[tid] = make_float2((float)base, (float)(base - (double)(float)base));
+        } else {
+            s_live[tid] = 0;
+            if (s.x != s.x && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_VALUE);
         }
     }
     __syncthreads();
 
-    // candidate i: the chunks' of beam i / per_beam; a finished beam's first place is its one candidate
-    const int total = p.n_beam * per_beam;
-    auto candidate = [&](int i) {
-        const int b = i / per_beam;
+    // A list is what a chunk left, descending; `share` threads (a power of two) take its places in turn, so that each
+    // one's first is its largest.  A finished beam's one candidate is the first of its first list.
+    const int lists = p.n_beam * a.n_chunk;
+    int share = 1;
+    while (share < 32 && 2 * share * lists <= kThreads) share *= 2;
+    auto candidate = [&](int list, int b, int place) {
         Cand c{0, 0};
         const int live = s_live[b];
         const uint64_t beam = (uint64_t)(kMaxBeam - 1 - b) << 56;
-        if (live == 1) {
-            const uint64_t key = a.part_key[row0 * per_beam + i];
+        if (live == 1 && place < k) {
+            const uint64_t key = a.part_key[row0 * per_beam + (int64_t)list * k + place];
             if (key) {
-                c.v = ordered((double)unordered((uint32_t)(key >> 32)) + s_base[b]);
+                float v = unordered((uint32_t)(key >> 32)), lo = s_base[b].y;
+                add_exact(v, lo, s_base[b].x);
+                const float hi = v + lo;                    // (both normalised: their pairs order as their sums)
+                lo = (v - hi) + lo;
+                c.v = (uint64_t)ordered(hi) << 32 | ordered(lo);
                 c.t = beam | (key >> 32) << 24 | ((uint32_t)key & (kMaxVocab - 1));
             }
-        } else if (live == 2 && i == b * per_beam) {
-            c.v = ordered(s_base[b]);
+        } else if (live == 2 && place == 0 && list == b * a.n_chunk) {
+            c.v = (uint64_t)ordered(s_base[b].x) << 32 | ordered(0.0f);
             c.t = beam;
         }
         return c;
     };
-    Cand mine{0, 0};
-    for (int i = tid; i < total; i += kThreads) {
-        const Cand c = candidate(i);
-        if (above(c, mine)) mine = c;
-    }
-    const uint32_t wt = rth_largest((uint32_t)(mine.v >> 32), (k + kWarps - 1) / kWarps);
-    if (lane == 0) s_t[warp] = wt;
+    const int list0 = tid / share, place0 = tid % share, list_step = kThreads / share;
+    uint32_t mine = 0;                                      // the upper half of this thread's largest value
+    for (int l = list0; l < lists; l += list_step) mine = max(mine, (uint32_t)(candidate(l, l / a.n_chunk, place0).v >> 32));
+    put_floor(mine, k, s_floor);
     __syncthreads();
-    uint32_t floor_key = s_t[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) floor_key = min(floor_key, s_t[w]);
-    if ((uint32_t)(mine.v >> 32) >= floor_key && mine.v) {
-        for (int i = tid; i < total; i += kThreads) {
-            const Cand c = candidate(i);
-            if (c.v && (uint32_t)(c.v >> 32) >= floor_key) {
+    const uint32_t floor_key = get_floor(k, s_floor);
+    if (mine != 0 && mine >= floor_key) {
+        for (int l = list0; l < lists; l += list_step) {
+            const int b = l / a.n_chunk;
+            for (int i = place0; i < k; i += share) {
+                const Cand c = candidate(l, b, i);
+                if (!c.v || (uint32_t)(c.v >> 32) < floor_key) break;
                 const int at = atomicAdd(&s_n, 1);
                 if (at < kBuffer) s_c[at] = c;
             }
@@ -337,7 +463,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
         const int b = kMaxBeam - 1 - (int)(c.t >> 56);
         const bool done = s_live[b] == 2;
         const int token = done ? p.pad : (int)(~(uint32_t)c.t & (kMaxVocab - 1));
-        p.out_score[at] = (float)unordered(c.v);
+        p.out_score[at] = unordered((uint32_t)(c.v >> 32));
         p.out_token[at] = token;
         p.out_parent[at] = (int)(row0 + b);
         if (p.out_finished) p.out_finished[at] = done || (p.eos >= 0 && token == p.eos);
@@ -358,10 +484,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     for (int i = 0; i < k; ++i) {
         if (stale) {
             best = Cand{0, 0};
-            for (int j = tid; j < total; j += kThreads) {
-                const Cand c = candidate(j);
-                if (above(last, c) && above(c, best)) best = c;
-            }
+            for (int l = list0; l < lists; l += list_step)
+                for (int i = place0; i < k; i += share) {
+                    const Cand c = candidate(l, l / a.n_chunk, i);
+                    if (above(last, c) && above(c, best)) best = c;
+                }
         }
         Cand b = best;
 #pragma unroll
@@ -382,7 +509,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
 }
 
 struct BeamPlan {
-    int vpt = 8, n_chunk = 1;
+    int nv = 1, n_chunk = 1;
     size_t off_s = 0, off_key = 0, bytes = 0;
 };
 
@@ -390,9 +517,11 @@ BeamPlan plan_beam(const kvq_beam_problem& p)
 {
     BeamPlan q;
     const int64_t rows = (int64_t)p.n_req * p.n_beam;
-    const int64_t big = (p.vocab + kThreads * 32 - 1) / (kThreads * 32);
-    if (rows * big >= 2 * (int64_t)sm_count()) q.vpt = 32;
-    q.n_chunk = (p.vocab + kThreads * q.vpt - 1) / (kThreads * q.vpt);
+    const int e = p.x_type == KVQ_WEIGHT_BF16 ? 8 : 4;
+    // large chunks where they fill the GPU, else small ones
+    const auto chunks = [&](int nv) { return ((int64_t)p.vocab + e - 1 + kThreads * nv * e - 1) / (kThreads * nv * e); };
+    q.nv = rows * chunks(8) >= 2 * (int64_t)sm_count() ? 8 : 2;
+    q.n_chunk = (int)chunks(q.nv);
     const size_t n = (size_t)rows * q.n_chunk;
     q.off_s = (n * 4 + 255) / 256 * 256;
     q.off_key = (q.off_s + n * 8 + 255) / 256 * 256;
@@ -423,12 +552,12 @@ int check_problem(const kvq_beam_problem* p, const char* E)
     return KVQ_OK;
 }
 
-template <typename X, bool VEC>
-void launch_chunks(const BeamArgs& a, int vpt, cudaStream_t s)
+template <typename X>
+void launch_chunks(const BeamArgs& a, int nv, cudaStream_t s)
 {
-    const dim3 grid((unsigned)(a.p.n_req * a.p.n_beam), (unsigned)a.n_chunk);     // (chunks: at most 2^24 / 2048)
-    if (vpt == 32) beam_chunk_kernel<X, 32, VEC><<<grid, kThreads, 0, s>>>(a);
-    else beam_chunk_kernel<X, 8, VEC><<<grid, kThreads, 0, s>>>(a);
+    const dim3 grid((unsigned)(a.p.n_req * a.p.n_beam), (unsigned)a.n_chunk);     // (chunks: at most 2^24 / 2048 and one)
+    if (nv == 8) beam_chunk_kernel<X, 8><<<grid, kThreads, 0, s>>>(a);
+    else beam_chunk_kernel<X, 2><<<grid, kThreads, 0, s>>>(a);
 }
 
 }  // namespace
@@ -458,13 +587,11 @@ int kvq_beam_select(const kvq_beam_problem* p, void* workspace, size_t ws_bytes,
         return set_last_error(KVQ_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", E, workspace ? ws_bytes : (size_t)0, q.bytes);
     if (!aligned(workspace, 256)) return set_last_error(KVQ_EALIGN, "%s: workspace not 256-byte aligned", E);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    BeamArgs a{*p, q.n_chunk, reinterpret_cast<float*>(ws), reinterpret_cast<double*>(ws + q.off_s),
+    BeamArgs a{*p, q.n_chunk, reinterpret_cast<float*>(ws), reinterpret_cast<float2*>(ws + q.off_s),
                reinterpret_cast<uint64_t*>(ws + q.off_key), dev_status};
     const cudaStream_t s = (cudaStream_t)stream;
-    const bool bf16 = p->x_type == KVQ_WEIGHT_BF16;
-    const bool vec = aligned(p->logits, 16) && p->ld % (bf16 ? 8 : 4) == 0;
-    if (bf16) vec ? launch_chunks<__nv_bfloat16, true>(a, q.vpt, s) : launch_chunks<__nv_bfloat16, false>(a, q.vpt, s);
-    else vec ? launch_chunks<float, true>(a, q.vpt, s) : launch_chunks<float, false>(a, q.vpt, s);
+    if (p->x_type == KVQ_WEIGHT_BF16) launch_chunks<__nv_bfloat16>(a, q.nv, s);
+    else launch_chunks<float>(a, q.nv, s);
     cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) e = launch_dependent(beam_merge_kernel, dim3((unsigned)p->n_req), dim3(kThreads), 0, s, a);
     return e == cudaSuccess ? KVQ_OK : set_last_error(KVQ_ECUDA, "%s: %s", E, cudaGetErrorString(e));
