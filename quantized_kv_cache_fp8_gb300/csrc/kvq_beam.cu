@@ -80,7 +80,17 @@ __device__ __forceinline__ void put_floor(uint32_t key, int k, uint32_t* s)
 }
 __device__ __forceinline__ uint32_t get_floor(int k, const uint32_t* s)
 {
-    if (k <= 16) return rth_largest(s[threadIdx.x & 31], k);
+    if (k <= 16) {
+        // the least of the values with fewer than k above them
+        const uint32_t v = s[threadIdx.x & 31];
+        int above = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint4 q = reinterpret_cast<const uint4*>(s)[i];
+            above += (q.x > v) + (q.y > v) + (q.z > v) + (q.w > v);
+        }
+        return __reduce_min_sync(kFull, above < k ? v : ~0u);
+    }
     uint32_t least = s[0];
 #pragma unroll
     for (int w = 1; w < kWarps; ++w) least = min(least, s[w]);
@@ -114,6 +124,34 @@ __device__ __forceinline__ void warp_sum(float& sum, float& lo)
     }
 }
 
+// score - m - log(s.x + s.y) in two floats, s.x > 0 finite.  The logarithm is e log 2 + 2 atanh u, u = (f - 1) / (f + 1),
+// for s = 2^e f, f in [1/sqrt 2, sqrt 2): u to two floats, then 2 (u + u^3 / 3 + u^5 / 5 + ...) with the powers from the
+// third on in one (|u| < 0.172: they are below 2^-8 of u, and seven terms leave 2^-37).  64-bit arithmetic takes 16
+// times as long here.
+__device__ __forceinline__ float2 less_log(float score, float m, float2 s)
+{
+    int e = (int)(__float_as_uint(s.x) >> 23) - 127;
+    float f = __uint_as_float((__float_as_uint(s.x) & 0x7FFFFFu) | 0x3F800000u);       // (sums are 1 or more, not subnormal)
+    if (f > 1.41421354f) {
+        f *= 0.5f;
+        ++e;
+    }
+    const float fl = s.y * __uint_as_float((uint32_t)(127 - e) << 23);
+    const float num = f - 1.0f, den = f + 1.0f;             // num is exact
+    const float den_lo = (f - (den - 1.0f)) + fl;
+    const float u = __fdividef(num, den);
+    const float ul = __fdividef(fmaf(-u, den, num) + fl - u * den_lo, den);
+    const float q = u * u;
+    const float tail = u * q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.0f / 13.0f, 1.0f / 11.0f), 1.0f / 9.0f), 1.0f / 7.0f), 0.2f), 1.0f / 3.0f);
+    float hi = score, lo = 0.0f;
+    add_exact(hi, lo, -m);
+    add_exact(hi, lo, (float)-e * 0x1.62e4p-1f);            // log 2 = 0x1.62e4p-1 (15 bits: the product is exact) + the rest
+    add_exact(hi, lo, -2.0f * u);
+    lo -= fmaf((float)e, 0x1.7f7d1cp-20f, 2.0f * (fmaf(ul, q, ul) + tail));
+    const float r = hi + lo;
+    return make_float2(r, (hi - r) + lo);
+}
+
 // whether beam b of request r has candidates of its own logits
 __device__ __forceinline__ bool reads_logits(const kvq_beam_problem& p, int64_t row)
 {
@@ -132,6 +170,12 @@ struct __align__(16) Vec<float> {
     __device__ void set(int i, float x) { w[i] = __float_as_uint(x); }
     __device__ float largest() const { return fmaxf(fmaxf(get(0), get(1)), fmaxf(get(2), get(3))); }
     static __device__ float load(const float* p) { return *p; }
+    // elements at .. of a row of n, -inf for those outside
+    __device__ void fill(const float* row, int at, int n)
+    {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) set(e, at + e >= 0 && at + e < n ? row[at + e] : -INFINITY);
+    }
 };
 template <>
 struct __align__(16) Vec<__nv_bfloat16> {
@@ -152,6 +196,11 @@ struct __align__(16) Vec<__nv_bfloat16> {
         return fmaxf(__uint_as_float(a << 16), __uint_as_float(a & 0xFFFF0000u));
     }
     static __device__ float load(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+    __device__ void fill(const __nv_bfloat16* row, int at, int n)
+    {
+#pragma unroll
+        for (int e = 0; e < kN; ++e) set(e, at + e >= 0 && at + e < n ? load(row + at + e) : -INFINITY);
+    }
 };
 
 // sum of 2^(x l - c) over a vector, two values at a time
@@ -178,45 +227,73 @@ __device__ __forceinline__ float exp_sum(const V& v, float c)
 }
 
 // NV vectors a thread.  Vectors begin at multiples of 16 bytes: `lead` elements of the first lie ahead of the row.
+// The CTAs go over the rows' chunks in turn; the next chunk's vectors are on their way while this one's best are ranked.
 template <typename X, int NV>
 __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs a)
 {
     using V = Vec<X>;
     constexpr int kE = V::kN, kChunk = kThreads * NV * kE;
-    __shared__ uint32_t s_floor[32];
+    __shared__ __align__(16) uint32_t s_floor[32];
     __shared__ float s_m[kWarps];
     __shared__ float2 s_sum[kWarps];
-    __shared__ int s_n;
-    __shared__ int s_vecs;
+    __shared__ int2 s_count[2];                             // vectors and elements gathered, of this chunk and the next
     __shared__ uint64_t s_best[kWarps];
     __shared__ uint64_t s_key[kBuffer];
     __shared__ V s_vec[kVectors];
     __shared__ int s_at[kVectors];
     const kvq_beam_problem& p = a.p;
-    const int64_t row = blockIdx.x;
     grid_dependents_launch();
-    if (!reads_logits(p, row)) return;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const X* src = static_cast<const X*>(p.logits) + row * p.ld;
-    const int lead = (int)((uintptr_t)src % 16 / sizeof(X));
-    const int c0 = (int)blockIdx.y * kChunk - lead;
     const int k = p.n_out;
+    const int64_t items = (int64_t)p.n_req * p.n_beam * a.n_chunk;
 
+    // the chunk at hand: of row `row`, whose elements c0 + (j * kThreads + tid) * kE .. are vector j of thread tid
     V x[NV];
-#pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        const int at = c0 + (j * kThreads + tid) * kE;
-        if (at >= 0 && at + kE <= p.vocab) {
-            const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src + at));
-            x[j].w[0] = w.x;
-            x[j].w[1] = w.y;
-            x[j].w[2] = w.z;
-            x[j].w[3] = w.w;
-        } else {
-#pragma unroll
-            for (int e = 0; e < kE; ++e) x[j].set(e, at + e >= 0 && at + e < p.vocab ? V::load(src + at + e) : -INFINITY);
+    int64_t item = blockIdx.x, row = 0;
+    const X* src = nullptr;
+    int c0 = 0;
+    // the next chunk with logits to be read, from `item` on; its vectors
+    auto fetch = [&]() {
+        for (; item < items; item += gridDim.x) {
+            row = item / a.n_chunk;
+            if (reads_logits(p, row)) break;
         }
-    }
+        if (item >= items) return;
+        src = static_cast<const X*>(p.logits) + row * p.ld;
+        const int lead = (int)((uintptr_t)src % 16 / sizeof(X));
+        c0 = (int)(item - row * a.n_chunk) * kChunk - lead;
+        if (c0 >= 0 && c0 + kChunk <= p.vocab) {
+            const uint4* from = reinterpret_cast<const uint4*>(src + c0) + tid;
+#pragma unroll
+            for (int j = 0; j < NV; ++j) {
+                const uint4 w = __ldcs(from + j * kThreads);
+                x[j].w[0] = w.x;
+                x[j].w[1] = w.y;
+                x[j].w[2] = w.z;
+                x[j].w[3] = w.w;
+            }
+            return;
+        }
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            const int at = c0 + (j * kThreads + tid) * kE;
+            if (at >= 0 && at + kE <= p.vocab) {
+                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src + at));
+                x[j].w[0] = w.x;
+                x[j].w[1] = w.y;
+                x[j].w[2] = w.z;
+                x[j].w[3] = w.w;
+            } else {
+                x[j].fill(src, at, p.vocab);
+            }
+        }
+    };
+    if (tid == 0) s_count[0] = make_int2(0, 0);
+    fetch();
+    for (int turn = 0; item < items; turn ^= 1) {
+    const X* const this_src = src;
+    const int this_c0 = c0;
+    const int64_t this_at = item;                           // (row * n_chunk + chunk)
     float most[NV], mine = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -225,7 +302,6 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
     }
     const uint32_t my_key = mine > -INFINITY ? ordered(mine) : 0u;
     const uint32_t wm = __reduce_max_sync(kFull, my_key);
-    if (tid == 0) s_n = s_vecs = 0;
     put_floor(my_key, k, s_floor);
 
     // exp(y - m), m the warp's largest, as 2^(y l - c), one fused multiply-add: l = log2 e in fp32, c = m l rounded.
@@ -235,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
     if (fabsf(m) < kLarge) {
         const float c = __fmul_rn(m, kLog2e);
 #pragma unroll
-        for (int j = 0; j < NV; ++j) add_exact(sum, low, exp_sum(x[j], c));
+        for (int j = 0; j < NV; j += 2) add_exact(sum, low, exp_sum(x[j], c) + exp_sum(x[j + 1], c));
     } else {
 #pragma unroll
         for (int j = 0; j < NV; ++j)
@@ -262,14 +338,16 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
 #pragma unroll
         for (int j = 0; j < NV; ++j)
             if (most[j] >= least && most[j] > -INFINITY) {
-                const int i = atomicAdd(&s_vecs, 1);
+                const int i = atomicAdd(&s_count[turn].x, 1);
                 if (i < kVectors) {
                     s_vec[i] = x[j];
-                    s_at[i] = c0 + (j * kThreads + tid) * kE;
+                    s_at[i] = this_c0 + (j * kThreads + tid) * kE;
                 }
             }
     }
-    const int64_t at = row * a.n_chunk + blockIdx.y;
+    if (tid == 0) s_count[turn ^ 1] = make_int2(0, 0);      // (nobody counts for the next chunk yet)
+    item += gridDim.x;
+    fetch();
     if (warp == kWarps - 1) {                               // the chunk's sum, a warp's a lane
         const float mw = lane < kWarps ? s_m[lane] : -INFINITY;
         float2 sw = lane < kWarps ? s_sum[lane] : make_float2(0.0f, 0.0f);
@@ -290,22 +368,22 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
         if (sw.x != 0.0f) add_scaled(t, lo, sw, mw == all ? 1.0f : expf(mw - all));
         warp_sum(t, lo);
         if (lane == 0) {
-            a.part_m[at] = all;
-            a.part_s[at] = make_float2(t, lo);
+            a.part_m[this_at] = all;
+            a.part_s[this_at] = make_float2(t, lo);
         }
     }
     __syncthreads();
-    const int vecs = s_vecs;
+    const int vecs = s_count[turn].x;
     for (int i = tid; i < min(vecs, kVectors) * kE; i += kThreads) {
         const float y = s_vec[i / kE].get(i % kE);
         if (y >= least && y > -INFINITY) {
-            const int at = atomicAdd(&s_n, 1);
+            const int at = atomicAdd(&s_count[turn].y, 1);
             if (at < kBuffer) s_key[at] = (uint64_t)ordered(y) << 32 | (uint32_t)~(s_at[i / kE] + i % kE);
         }
     }
     __syncthreads();
-    const int n = s_n;
-    uint64_t* out = a.part_key + at * k;
+    const int n = s_count[turn].y;
+    uint64_t* out = a.part_key + this_at * k;
     if (vecs <= kVectors && n <= kBuffer) {
         for (int i = tid; i < n; i += kThreads) {
             const uint64_t key = s_key[i];
@@ -314,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
             if (rank < k) out[rank] = key;
         }
         for (int i = n + tid; i < k; i += kThreads) out[i] = 0;
-        return;
+        continue;
     }
     // too many equal values: the best one by one, of a thread's elements read again
     uint64_t last = ~0ull, best = 0;
@@ -322,8 +400,8 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
     for (int i = 0; i < k; ++i) {
         if (stale) {
             best = 0;
-            for (int t = max(c0, 0) + tid; t < min(c0 + kChunk, p.vocab); t += kThreads) {
-                const float y = V::load(src + t);
+            for (int t = max(this_c0, 0) + tid; t < min(this_c0 + kChunk, p.vocab); t += kThreads) {
+                const float y = V::load(this_src + t);
                 const uint64_t key = y > -INFINITY ? (uint64_t)ordered(y) << 32 | (uint32_t)~t : 0;
                 if (key < last && key > best) best = key;
             }
@@ -340,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
         last = b;
         stale = best == b;
     }
+    }
 }
 
 // A candidate of any beam: value (as two floats, ordered), then beam (ascending), logit (descending), token (ascending)
@@ -353,7 +432,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     __shared__ float2 s_base[kMaxBeam];                     // sum of exponentials, then score - its logarithm, in two floats
     __shared__ float s_max[kMaxBeam];
     __shared__ uint8_t s_live[kMaxBeam];                    // 0: no candidates; 1: its tokens; 2: finished
-    __shared__ uint32_t s_floor[32];
+    __shared__ __align__(16) uint32_t s_floor[32];
     __shared__ int s_n;
     __shared__ Cand s_best[kWarps];
     __shared__ Cand s_c[kBuffer];
@@ -394,12 +473,10 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
         }
     }
     __syncthreads();
-    // (64-bit arithmetic is slow here: one warp does it for all beams, a lane each)
     if (tid < p.n_beam && s_live[tid] == 1) {
         const float2 s = s_base[tid];
         if (s.x > 0.0f) {
-            const double base = (double)score - ((double)s_max[tid] + log((double)s.x + (double)s.y));
-            s_base[tid] = make_float2((float)base, (float)(base - (double)(float)base));
+            s_base[tid] = less_log(score, s_max[tid], s);
         } else {
             s_live[tid] = 0;
             if (s.x != s.x && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_VALUE);
@@ -432,7 +509,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
         }
         return c;
     };
-    const int list0 = tid / share, place0 = tid % share, list_step = kThreads / share;
+    const int list_step = kThreads / share, list0 = tid % list_step, place0 = tid / list_step;
     uint32_t mine = 0;                                      // the upper half of this thread's largest value
     for (int l = list0; l < lists; l += list_step) mine = max(mine, (uint32_t)(candidate(l, l / a.n_chunk, place0).v >> 32));
     put_floor(mine, k, s_floor);
@@ -555,7 +632,8 @@ int check_problem(const kvq_beam_problem* p, const char* E)
 template <typename X>
 void launch_chunks(const BeamArgs& a, int nv, cudaStream_t s)
 {
-    const dim3 grid((unsigned)(a.p.n_req * a.p.n_beam), (unsigned)a.n_chunk);     // (chunks: at most 2^24 / 2048 and one)
+    const int64_t items = (int64_t)a.p.n_req * a.p.n_beam * a.n_chunk;
+    const unsigned grid = (unsigned)std::min<int64_t>(items, 4 * (int64_t)sm_count());
     if (nv == 8) beam_chunk_kernel<X, 8><<<grid, kThreads, 0, s>>>(a);
     else beam_chunk_kernel<X, 2><<<grid, kThreads, 0, s>>>(a);
 }

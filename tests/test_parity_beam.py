@@ -426,9 +426,10 @@ def beam_ref(x, score, fin, n_out, eos, pad):
             t = np.flatnonzero(row > -np.inf)
             if len(t) == 0:
                 continue
-            m = row[t].max()
-            lse = m + math.log(np.exp(row[t] - m).sum())
-            val.append(row[t] + (np.float64(s) - lse)), logit.append(row[t] + 0.0), token.append(t)
+            # the differences first: m + log(sum) of logits near 3e38 rounds to m even in 64 bits, and a constant row's
+            # values, score - log(vocab), would come out as 0
+            d = row[t] - row[t].max()
+            val.append(d + (np.float64(s) - math.log(np.exp(d).sum()))), logit.append(row[t] + 0.0), token.append(t)
             beam.append(np.full(len(t), b)), done.append(np.zeros(len(t), int))
         if not val:
             continue
