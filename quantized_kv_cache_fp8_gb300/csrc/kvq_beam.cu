@@ -51,50 +51,52 @@ __device__ __forceinline__ float ex2(float x)
     return r;
 }
 
-// the r-th largest of the warp's keys, counted with their multiplicity (0 if fewer are not 0), and the first `keep`
-// of them into `to`
-__device__ __forceinline__ uint32_t rth_largest(uint32_t key, int r, uint32_t* to = nullptr)
+// the r-th largest of the warp's keys, counted with their multiplicity (0 if fewer are not 0)
+__device__ __forceinline__ uint32_t rth_largest(uint32_t key, int r)
 {
     uint32_t m = 0;
     for (int i = 0; i < r; ++i) {
         m = __reduce_max_sync(kFull, key);
         const unsigned who = __ballot_sync(kFull, key == m);
         if ((threadIdx.x & 31) == __ffs(who) - 1) key = 0;
-        if (to && (threadIdx.x & 31) == 0) to[i] = m;
     }
     return m;
 }
 
-// A level that k of the CTA's keys reach, one a thread (0, if fewer than k are not 0).  Up to 16: the k-th largest of
-// each warp's four largest, which is the k-th largest of all but where one warp holds more than four of those.
-// More: the least of the warps' (k / warps)-th largest.  put_floor, a barrier, get_floor; s: 32 entries.
+// A level that k of the CTA's keys reach, one a thread (0, if fewer than k are not 0).  Up to 16: the k-th largest of the
+// maxima of 32 groups of eight lanes, which little more than k keys reach.  More: the least of the warps' (k / warps)-th
+// largest.  s: 32 entries, 16-byte aligned.  put_floor, a barrier, make_floor, a barrier: s[0].
 __device__ __forceinline__ void put_floor(uint32_t key, int k, uint32_t* s)
 {
     const int warp = threadIdx.x >> 5;
     if (k <= 16) {
-        (void)rth_largest(key, 4, s + 4 * warp);
+#pragma unroll
+        for (int o = 4; o >= 1; o >>= 1) key = max(key, __shfl_xor_sync(kFull, key, o));
+        if (threadIdx.x % 8 == 0) s[threadIdx.x / 8] = key;
     } else {
         const uint32_t m = rth_largest(key, (k + kWarps - 1) / kWarps);
         if ((threadIdx.x & 31) == 0) s[warp] = m;
     }
 }
-__device__ __forceinline__ uint32_t get_floor(int k, const uint32_t* s)
+__device__ __forceinline__ void make_floor(int k, uint32_t* s)
 {
+    if (threadIdx.x >= 32) return;                          // (the others' issue slots are for other CTAs)
+    uint32_t least;
     if (k <= 16) {
         // the least of the values with fewer than k above them
-        const uint32_t v = s[threadIdx.x & 31];
+        const uint32_t v = s[threadIdx.x];
         int above = 0;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const uint4 q = reinterpret_cast<const uint4*>(s)[i];
             above += (q.x > v) + (q.y > v) + (q.z > v) + (q.w > v);
         }
-        return __reduce_min_sync(kFull, above < k ? v : ~0u);
+        least = __reduce_min_sync(kFull, above < k ? v : ~0u);
+    } else {
+        least = __reduce_min_sync(kFull, threadIdx.x < kWarps ? s[threadIdx.x] : ~0u);
     }
-    uint32_t least = s[0];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) least = min(least, s[w]);
-    return least;
+    __syncwarp();
+    if (threadIdx.x == 0) s[0] = least;
 }
 
 // s += x, what the addition rounds off gathered in lo (exact whichever is the larger: Knuth, 1969)
@@ -227,7 +229,7 @@ __device__ __forceinline__ float exp_sum(const V& v, float c)
 }
 
 // NV vectors a thread.  Vectors begin at multiples of 16 bytes: `lead` elements of the first lie ahead of the row.
-// The CTAs go over the rows' chunks in turn; the next chunk's vectors are on their way while this one's best are ranked.
+// The CTAs go over the rows' chunks in turn; a next chunk's vectors are on their way while this one's best are ranked.
 template <typename X, int NV>
 __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs a)
 {
@@ -245,23 +247,29 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
     grid_dependents_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int k = p.n_out;
-    const int64_t items = (int64_t)p.n_req * p.n_beam * a.n_chunk;
+    const int rows = p.n_req * p.n_beam;
 
-    // the chunk at hand: of row `row`, whose elements c0 + (j * kThreads + tid) * kE .. are vector j of thread tid
+    // the chunk at hand, chunk `chunk` of row `row`: elements c0 + (j * kThreads + tid) * kE .. are vector j of thread tid
     V x[NV];
-    int64_t item = blockIdx.x, row = 0;
+    int row = blockIdx.x / a.n_chunk, chunk = blockIdx.x - row * a.n_chunk;
+    const int row_step = gridDim.x / a.n_chunk, chunk_step = gridDim.x - row_step * a.n_chunk;
     const X* src = nullptr;
     int c0 = 0;
-    // the next chunk with logits to be read, from `item` on; its vectors
-    auto fetch = [&]() {
-        for (; item < items; item += gridDim.x) {
-            row = item / a.n_chunk;
-            if (reads_logits(p, row)) break;
+    auto advance = [&]() {
+        row += row_step;
+        chunk += chunk_step;
+        if (chunk >= a.n_chunk) {
+            chunk -= a.n_chunk;
+            ++row;
         }
-        if (item >= items) return;
-        src = static_cast<const X*>(p.logits) + row * p.ld;
+    };
+    // the next chunk with logits to be read, from this one on; its vectors
+    auto fetch = [&]() {
+        while (row < rows && !reads_logits(p, row)) advance();
+        if (row >= rows) return;
+        src = static_cast<const X*>(p.logits) + (int64_t)row * p.ld;
         const int lead = (int)((uintptr_t)src % 16 / sizeof(X));
-        c0 = (int)(item - row * a.n_chunk) * kChunk - lead;
+        c0 = chunk * kChunk - lead;
         if (c0 >= 0 && c0 + kChunk <= p.vocab) {
             const uint4* from = reinterpret_cast<const uint4*>(src + c0) + tid;
 #pragma unroll
@@ -290,10 +298,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
     };
     if (tid == 0) s_count[0] = make_int2(0, 0);
     fetch();
-    for (int turn = 0; item < items; turn ^= 1) {
+    for (int turn = 0; row < rows; turn ^= 1) {
     const X* const this_src = src;
     const int this_c0 = c0;
-    const int64_t this_at = item;                           // (row * n_chunk + chunk)
+    const int64_t this_at = (int64_t)row * a.n_chunk + chunk;
     float most[NV], mine = -INFINITY;
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
@@ -331,23 +339,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
     }
     __syncthreads();
 
-    // vectors with something at or above the floor (few): their elements are looked at together, further down
-    const uint32_t floor_key = get_floor(k, s_floor);
-    const float least = floor_key ? unordered(floor_key) : -INFINITY;
-    if (my_key != 0 && my_key >= floor_key) {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (most[j] >= least && most[j] > -INFINITY) {
-                const int i = atomicAdd(&s_count[turn].x, 1);
-                if (i < kVectors) {
-                    s_vec[i] = x[j];
-                    s_at[i] = this_c0 + (j * kThreads + tid) * kE;
-                }
-            }
-    }
-    if (tid == 0) s_count[turn ^ 1] = make_int2(0, 0);      // (nobody counts for the next chunk yet)
-    item += gridDim.x;
-    fetch();
+    make_floor(k, s_floor);
     if (warp == kWarps - 1) {                               // the chunk's sum, a warp's a lane
         const float mw = lane < kWarps ? s_m[lane] : -INFINITY;
         float2 sw = lane < kWarps ? s_sum[lane] : make_float2(0.0f, 0.0f);
@@ -373,10 +365,29 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
         }
     }
     __syncthreads();
+
+    // vectors with something at or above the floor (few): their elements are looked at together, further down
+    const uint32_t floor_key = s_floor[0];
+    const float least = floor_key ? unordered(floor_key) : -0x1.fffffep127f;       // (all but -inf)
+    if (mine >= least) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+            if (most[j] >= least) {
+                const int i = atomicAdd(&s_count[turn].x, 1);
+                if (i < kVectors) {
+                    s_vec[i] = x[j];
+                    s_at[i] = this_c0 + (j * kThreads + tid) * kE;
+                }
+            }
+    }
+    if (tid == 0) s_count[turn ^ 1] = make_int2(0, 0);      // (nobody counts for the next chunk yet)
+    advance();
+    fetch();
+    __syncthreads();
     const int vecs = s_count[turn].x;
     for (int i = tid; i < min(vecs, kVectors) * kE; i += kThreads) {
         const float y = s_vec[i / kE].get(i % kE);
-        if (y >= least && y > -INFINITY) {
+        if (y >= least) {
             const int at = atomicAdd(&s_count[turn].y, 1);
             if (at < kBuffer) s_key[at] = (uint64_t)ordered(y) << 32 | (uint32_t)~(s_at[i / kE] + i % kE);
         }
@@ -385,11 +396,11 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
     const int n = s_count[turn].y;
     uint64_t* out = a.part_key + this_at * k;
     if (vecs <= kVectors && n <= kBuffer) {
-        for (int i = tid; i < n; i += kThreads) {
+        for (int i = warp; i < n; i += kWarps) {            // a warp counts what is above
             const uint64_t key = s_key[i];
             int rank = 0;
-            for (int j = 0; j < n; ++j) rank += s_key[j] > key;
-            if (rank < k) out[rank] = key;
+            for (int j = 0; j < n; j += 32) rank += __popc(__ballot_sync(kFull, j + lane < n && s_key[min(j + lane, n - 1)] > key));
+            if (rank < k && lane == 0) out[rank] = key;
         }
         for (int i = n + tid; i < k; i += kThreads) out[i] = 0;
         continue;
@@ -452,18 +463,32 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     }
     __syncthreads();
     grid_dependency_wait();
+    // A list is what a chunk left, descending; `share` threads (a power of two) take its places in turn, so that each
+    // one's first is its largest.  That one is read here already (of a dead beam it is not used, and may be anything).
+    // List l is chunk l / n_beam of beam l % n_beam: where one beam has all the best, they are in many groups of lanes.
+    const int lists = p.n_beam * a.n_chunk;
+    int share = 1;
+    while (share < 32 && 2 * share * lists <= kThreads) share *= 2;
+    const int list_step = kThreads / share, first = tid % list_step, place0 = tid / list_step;
+    const int b_first = first % p.n_beam;
+    auto key_at = [&](int l, int b, int place) { return a.part_key + (row0 + b) * per_beam + (int64_t)(l / p.n_beam) * k + place; };
+    const uint64_t head_key = first < lists && place0 < k ? *key_at(first, b_first, place0) : 0;
     for (int b = warp; b < p.n_beam; b += kWarps) {
         if (s_live[b] != 1) continue;
         const int64_t at = (row0 + b) * a.n_chunk;
-        float m = -INFINITY;
-        for (int c = lane; c < a.n_chunk; c += 32) m = fmaxf(m, a.part_m[at + c]);
+        const bool one = lane < a.n_chunk;                  // the lane's first chunk, loaded at once
+        const float m0 = one ? a.part_m[at + lane] : -INFINITY;
+        const float2 sc0 = one ? a.part_s[at + lane] : make_float2(0.0f, 0.0f);
+        float m = m0;
+        for (int c = lane + 32; c < a.n_chunk; c += 32) m = fmaxf(m, a.part_m[at + c]);
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
         float s = 0.0f, lo = 0.0f;
-        for (int c = lane; c < a.n_chunk; c += 32) {
+        // (the chunk of the maximum as it is, the others by an fp32 exponential as all terms are)
+        if (sc0.x != 0.0f) add_scaled(s, lo, sc0, m0 == m ? 1.0f : expf(m0 - m));
+        for (int c = lane + 32; c < a.n_chunk; c += 32) {
             const float2 sc = a.part_s[at + c];
             const float mc = a.part_m[at + c];
-            // (the chunk of the maximum as it is, the others by an fp32 exponential as all terms are)
             if (sc.x != 0.0f) add_scaled(s, lo, sc, mc == m ? 1.0f : expf(mc - m));
         }
         warp_sum(s, lo);
@@ -484,42 +509,42 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     }
     __syncthreads();
 
-    // A list is what a chunk left, descending; `share` threads (a power of two) take its places in turn, so that each
-    // one's first is its largest.  A finished beam's one candidate is the first of its first list.
-    const int lists = p.n_beam * a.n_chunk;
-    int share = 1;
-    while (share < 32 && 2 * share * lists <= kThreads) share *= 2;
-    auto candidate = [&](int list, int b, int place) {
+    // a candidate of beam b from the key that its chunk left (a finished beam's, whatever the key: its one)
+    auto candidate = [&](int b, uint64_t key) {
         Cand c{0, 0};
-        const int live = s_live[b];
         const uint64_t beam = (uint64_t)(kMaxBeam - 1 - b) << 56;
-        if (live == 1 && place < k) {
-            const uint64_t key = a.part_key[row0 * per_beam + (int64_t)list * k + place];
-            if (key) {
-                float v = unordered((uint32_t)(key >> 32)), lo = s_base[b].y;
-                add_exact(v, lo, s_base[b].x);
-                const float hi = v + lo;                    // (both normalised: their pairs order as their sums)
-                lo = (v - hi) + lo;
-                c.v = (uint64_t)ordered(hi) << 32 | ordered(lo);
-                c.t = beam | (key >> 32) << 24 | ((uint32_t)key & (kMaxVocab - 1));
-            }
-        } else if (live == 2 && place == 0 && list == b * a.n_chunk) {
+        if (s_live[b] == 2) {
             c.v = (uint64_t)ordered(s_base[b].x) << 32 | ordered(0.0f);
             c.t = beam;
+        } else if (key) {
+            float v = unordered((uint32_t)(key >> 32)), lo = s_base[b].y;
+            add_exact(v, lo, s_base[b].x);
+            const float hi = v + lo;                        // (both normalised: their pairs order as their sums)
+            lo = (v - hi) + lo;
+            c.v = (uint64_t)ordered(hi) << 32 | ordered(lo);
+            c.t = beam | (key >> 32) << 24 | ((uint32_t)key & (kMaxVocab - 1));
         }
         return c;
     };
-    const int list_step = kThreads / share, list0 = tid % list_step, place0 = tid / list_step;
-    uint32_t mine = 0;                                      // the upper half of this thread's largest value
-    for (int l = list0; l < lists; l += list_step) mine = max(mine, (uint32_t)(candidate(l, l / a.n_chunk, place0).v >> 32));
+    auto item = [&](int l, int b, int place) {
+        if (s_live[b] == 2) return place == 0 && l == b ? candidate(b, 0) : Cand{0, 0};
+        return candidate(b, s_live[b] == 1 && place < k ? *key_at(l, b, place) : 0);
+    };
+    const Cand head = first >= lists ? Cand{0, 0}
+                      : s_live[b_first] == 2 ? item(first, b_first, place0)
+                                             : candidate(b_first, s_live[b_first] == 1 ? head_key : 0);
+    uint32_t mine = (uint32_t)(head.v >> 32);               // the upper half of this thread's largest value
+    for (int l = first + list_step; l < lists; l += list_step) mine = max(mine, (uint32_t)(item(l, l % p.n_beam, place0).v >> 32));
     put_floor(mine, k, s_floor);
     __syncthreads();
-    const uint32_t floor_key = get_floor(k, s_floor);
+    make_floor(k, s_floor);
+    __syncthreads();
+    const uint32_t floor_key = s_floor[0];
     if (mine != 0 && mine >= floor_key) {
-        for (int l = list0; l < lists; l += list_step) {
-            const int b = l / a.n_chunk;
+        for (int l = first; l < lists; l += list_step) {
+            const int b = l == first ? b_first : l % p.n_beam;
             for (int i = place0; i < k; i += share) {
-                const Cand c = candidate(l, b, i);
+                const Cand c = l == first && i == place0 ? head : item(l, b, i);
                 if (!c.v || (uint32_t)(c.v >> 32) < floor_key) break;
                 const int at = atomicAdd(&s_n, 1);
                 if (at < kBuffer) s_c[at] = c;
@@ -547,11 +572,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     };
     const int n = s_n;
     if (n <= kBuffer) {
-        for (int i = tid; i < n; i += kThreads) {
+        for (int i = warp; i < n; i += kWarps) {            // a warp counts what is above
             const Cand c = s_c[i];
             int rank = 0;
-            for (int j = 0; j < n; ++j) rank += above(s_c[j], c);
-            if (rank < k) write(rank, c);
+            for (int j = 0; j < n; j += 32) rank += __popc(__ballot_sync(kFull, j + lane < n && above(s_c[min(j + lane, n - 1)], c)));
+            if (rank < k && lane == 0) write(rank, c);
         }
         for (int i = n + tid; i < k; i += kThreads) write(i, Cand{0, 0});
         return;
@@ -561,9 +586,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     for (int i = 0; i < k; ++i) {
         if (stale) {
             best = Cand{0, 0};
-            for (int l = list0; l < lists; l += list_step)
+            for (int l = first; l < lists; l += list_step)
                 for (int i = place0; i < k; i += share) {
-                    const Cand c = candidate(l, l / a.n_chunk, i);
+                    const Cand c = item(l, l % p.n_beam, i);
                     if (above(last, c) && above(c, best)) best = c;
                 }
         }
@@ -633,7 +658,8 @@ template <typename X>
 void launch_chunks(const BeamArgs& a, int nv, cudaStream_t s)
 {
     const int64_t items = (int64_t)a.p.n_req * a.p.n_beam * a.n_chunk;
-    const unsigned grid = (unsigned)std::min<int64_t>(items, 4 * (int64_t)sm_count());
+    // (a CTA a chunk up to many: the finished beams' make the work uneven, and the GPU levels it)
+    const unsigned grid = (unsigned)std::min<int64_t>(items, 64 * (int64_t)sm_count());
     if (nv == 8) beam_chunk_kernel<X, 8><<<grid, kThreads, 0, s>>>(a);
     else beam_chunk_kernel<X, 2><<<grid, kThreads, 0, s>>>(a);
 }
