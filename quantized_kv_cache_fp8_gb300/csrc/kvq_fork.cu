@@ -15,20 +15,24 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kMaxPages = 1 << 20;
-constexpr int kCluster = 8;              // CTAs of the planning kernels where there is work for them
-constexpr int kRun = 16;                 // page marks a thread scans at once (one 16-byte load)
+constexpr int kCluster = 8;              // CTAs of a planning kernel where one is not enough
+constexpr int kThreads = 1024;           // of each; of a single one:
+constexpr int kThreadsOne = 512;
+constexpr int kSeqShared = 512;          // sequences of a CTA whose lengths are kept in shared memory
+constexpr int kRowsShared = 8192;        // table entries of a single CTA that are
+constexpr int kPagesOne = 8192;          // pages that a single CTA goes over (5 bytes of shared memory each)
+constexpr int kPagesShared = 65536;      // pages whose marks fit the CTAs' shared memory
 
 __device__ __forceinline__ void flag(uint32_t* status, unsigned bit)
 {
     if (status) atomicOr(status, bit);
 }
 
-// Inclusive prefix sum over the CTA; *total = the CTA's sum.  s_warp: kWarps entries.
+// Inclusive prefix sum over the CTA; *total = the CTA's sum.  s_warp: 32 entries.
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(kFull, v, o);
@@ -37,7 +41,7 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total)
     __syncthreads();                                     // an earlier call's readers are done
     if (lane == 31) s_warp[warp] = v;
     __syncthreads();
-    int w = s_warp[lane];
+    int w = lane < nw ? s_warp[lane] : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
         const int u = __shfl_up_sync(kFull, w, o);
@@ -48,57 +52,135 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total)
     return warp > 0 ? v + before : v;
 }
 
-// The planning kernels are one cluster of CTAs, whose barrier orders their accesses to the workspace and to
-// the tables: a launch for what would be five.  Loads of what another CTA of the cluster wrote go past the L1.
-template <typename T>
-__device__ __forceinline__ T fresh(const T* p) { return __ldcg(p); }
+// ------------------------------------------------------------------------------------
+// The planning kernels.  Small problems run as one CTA, larger ones as a cluster of kCluster; either way one launch,
+// whose phases are parted by the CTA's or the cluster's barrier.  A CTA goes over the table rows of its share of the
+// sequences and leaves marks, a byte a page, in its own set; each CTA then owns a range of the pages, and reads that
+// range of all the sets.  Marks are plain stores of one value, so that no order changes them; lists of pages come from
+// prefix sums over the marks, in the order of the ids.  The sets are in shared memory, read across the cluster, up to
+// kPagesShared pages, else in the workspace.  Bound by latency: a handful of dependent accesses between barriers
+// (4 beams: 12.5 us with the marks in global memory and a barrier of a cluster, 5.6 as one CTA).
+// ------------------------------------------------------------------------------------
+template <bool ONE, bool SHARED>
+struct Team {
+    uint8_t* shared;                     // this CTA's dynamic shared memory
+    uint8_t* global;                     // the workspace that stands for it, `stride` bytes a CTA
+    size_t stride;
+    int n_cta, cta;
+
+    __device__ Team(uint8_t* sh, uint8_t* gl, size_t st) : shared(sh), global(gl), stride(st), n_cta(1), cta(0)
+    {
+        if constexpr (!ONE) {
+            n_cta = (int)cg::this_cluster().num_blocks();
+            cta = (int)cg::this_cluster().block_rank();
+        }
+    }
+    __device__ void sync() const
+    {
+        if constexpr (ONE) __syncthreads();
+        else cg::this_cluster().sync();
+    }
+    // CTA c's part of the storage, from byte `at` on
+    template <typename T>
+    __device__ T* part(int c, size_t at) const
+    {
+        if constexpr (!SHARED) return reinterpret_cast<T*>(global + c * stride + at);
+        else if constexpr (ONE) return reinterpret_cast<T*>(shared + at);
+        else return reinterpret_cast<T*>(cg::this_cluster().map_shared_rank(shared, c) + at);
+    }
+    template <typename T>
+    __device__ T* mine(size_t at) const
+    {
+        if constexpr (!SHARED) return reinterpret_cast<T*>(global + cta * stride + at);
+        else return reinterpret_cast<T*>(shared + at);
+    }
+    // a static shared variable of CTA c
+    template <typename T>
+    __device__ T* of(int c, T* v) const
+    {
+        if constexpr (ONE) return v;
+        else return cg::this_cluster().map_shared_rank(v, c);
+    }
+};
+
+// Marks come in words of four pages; the words' ranges of the CTAs, and where a page's owner has what it keeps of it
+struct Words {
+    int n, each;
+    __host__ __device__ Words(int n_pages, int n_cta) : n((n_pages + 3) / 4), each(((n_pages + 3) / 4 + n_cta - 1) / n_cta) {}
+    __host__ __device__ size_t bytes() const { return ((size_t)n * 4 + 15) / 16 * 16; }       // of a set of marks
+};
+
+__device__ __forceinline__ void clear(uint8_t* p, size_t bytes)
+{
+    for (size_t i = threadIdx.x; i < bytes / 16; i += blockDim.x) reinterpret_cast<uint4*>(p)[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+// f(s, e) for the entries e of the rows s = s0 .. s1 - 1, as far as length(s): warps take rows, several a row where
+// there are few, and lanes entries, four of a lane together
+template <typename L, typename F>
+__device__ __forceinline__ void over_rows(int s0, int s1, L length, F f)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
+    const int per_row = max(1, n_warps / max(1, s1 - s0)), rows = n_warps / per_row;
+    if (warp >= rows * per_row) return;
+    for (int s = s0 + warp / per_row; s < s1; s += rows) {
+        const int n = length(s);
+        for (int e0 = warp % per_row * 128; e0 < n; e0 += per_row * 128) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) f(s, e0 + 32 * u + lane, n);
+        }
+    }
+}
 
 // ------------------------------------------------------------------------------------
-// kvq_fork_pages.  Which pages stay held, and who keeps a shared last page, are marks a page: a byte where a
-// sequence holds it as a whole page or keeps it (stays), one where the old tables hold it (was), and the
-// lowest sequence that has it as a last page (keeper).  Marks are set by plain stores of one value or by a
-// minimum, so that no order changes them; free pages come from a scan of the marks in the order of the ids.
-// Latency bound: a handful of dependent accesses between cluster barriers.
+// kvq_fork_pages.  Two sets of marks, the pages that the tables held (was) and those that the new ones hold (stays), and
+// for a page that is some sequence's last, in part, the lowest such sequence (keeper, with the page's owner).
 // ------------------------------------------------------------------------------------
 struct ForkArgs {
     kvq_fork_plan p;
     uint32_t* status;
-    uint8_t* was;                        // [n_pages, padded to kRun]
-    uint8_t* stays;                      // [n_pages, padded]
-    int32_t* keeper;                     // [n_pages], set where some sequence's last page is
+    uint8_t* store;                      // the CTAs' marks and keepers, where they are not in shared memory
+    size_t stride;
     int32_t* row;                        // [n_seq][max_pages]: the new tables
-    int4* seq;                           // [n_seq]: parent (-1: none), len, last page (-1: none), old n_held
-    int32_t* rank;                       // [n_seq]: number among the copies, -1: none
-    int32_t* count;                      // [kCluster]: pages given back by a CTA's range; [kCluster]: copies wanted
+    int4* seq;                           // [n_seq], see below
+    int rows_shared;                     // whether the new tables are in shared memory
 };
 
-__global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkArgs a)
+template <bool ONE, bool SHARED>
+__global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kernel(const ForkArgs a)
 {
-    __shared__ int s_warp[kWarps];
-    const cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ __align__(16) uint8_t s_store[];
+    __shared__ int s_warp[32];
+    __shared__ int4 s_seq[kSeqShared];
+    __shared__ int s_copies, s_given;
     const kvq_fork_plan& p = a.p;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int n_cta = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
-    const int all = n_cta * kThreads, me = cta * kThreads + tid;
-    const int ps = p.page_size;
+    const Team<ONE, SHARED> team(s_store, a.store, a.stride);
+    const Words words(p.n_pages, team.n_cta);
+    const size_t set = words.bytes();
+    const int tid = threadIdx.x, T = blockDim.x, ps = p.page_size;
+    uint8_t *was = team.template mine<uint8_t>(0), *stays = team.template mine<uint8_t>(set);
+    auto keeper = [&](int page) { return team.template part<int32_t>(page / 4 / words.each, 2 * set) + (page - page / 4 / words.each * words.each * 4); };
+    const int seqs = (p.n_seq + team.n_cta - 1) / team.n_cta;
+    const int s0 = min(team.cta * seqs, p.n_seq), s1 = min(s0 + seqs, p.n_seq);
+    // of a sequence: parent (-1: none), later its number among the copies (-1: none); rows; last page if held in
+    // part (-1: none); pages held before
+    int4* const seq = seqs <= kSeqShared ? s_seq - s0 : a.seq;
+    int32_t* const row = ONE && a.rows_shared ? reinterpret_cast<int32_t*>(s_store + 2 * set + (size_t)words.each * 16) : a.row;
     unsigned bits = 0;
-
     const int n_free0 = p.n_free[0], n_free = min(max(n_free0, 0), p.n_pages);
     if (n_free != n_free0) bits |= KVQ_DEV_BAD_INDEX;
 
     // ---- marks cleared; every sequence's parent, rows and last page
-    const int n_marks = (p.n_pages + kRun - 1) / kRun;      // 16-byte words of marks
-    for (int i = me; i < n_marks; i += all) {
-        reinterpret_cast<uint4*>(a.was)[i] = make_uint4(0u, 0u, 0u, 0u);
-        reinterpret_cast<uint4*>(a.stays)[i] = make_uint4(0u, 0u, 0u, 0u);
-    }
-    for (int s = me; s < p.n_seq; s += all) {
+    clear(was, set);
+    clear(stays, set);
+    for (int i = tid; i < words.each * 4; i += T) team.template mine<int32_t>(2 * set)[i] = INT_MAX;
+    for (int s = s0 + tid; s < s1; s += T) {
         int par = p.parent[s];
+        const int held = p.n_held[s], own = min(max(held, 0), p.max_pages);
         if (par < -1 || par >= p.n_seq) {
             bits |= KVQ_DEV_BAD_INDEX;
             par = -1;
         }
-        const int held = p.n_held[s], own = min(max(held, 0), p.max_pages);
         if (held != own) bits |= KVQ_DEV_BAD_INDEX;
         int len = 0, last = -1;
         if (par >= 0) {
@@ -115,157 +197,141 @@ __global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkArgs a)
             if (p.keep_len) len = min(len, max(p.keep_len[s], 0));
             if (len % ps) {
                 const int page = p.block_table[(int64_t)par * p.max_pages + len / ps];
-                if (page >= 0 && page < p.n_pages) {
-                    last = page;
-                    a.keeper[page] = INT_MAX;
-                }
+                if (page >= 0 && page < p.n_pages) last = page;
             }
         }
-        a.seq[s] = make_int4(par, len, last, own);
+        seq[s] = make_int4(par, len, last, own);
     }
-    cluster.sync();
+    team.sync();
 
-    // ---- the pages that the tables held, and that the new ones hold whole.  A warp takes 128 entries.
-    const int warp = me >> 5, n_warps = all >> 5;
-    const int per_row = (p.max_pages + 127) / 128;
-    for (int64_t i = warp; i < (int64_t)p.n_seq * per_row; i += n_warps) {
-        const int s = (int)(i / per_row), e0 = (int)(i - (int64_t)s * per_row) * 128;
-        const int4 q = fresh(a.seq + s);
-        const int32_t* mine = p.block_table + (int64_t)s * p.max_pages;
-        const int32_t* from = p.block_table + (int64_t)q.x * p.max_pages;
-        int32_t* to = a.row + (int64_t)s * p.max_pages;
-        const int whole = q.y / ps, need = (q.y + ps - 1) / ps;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int e = e0 + 32 * u + lane;
+    // ---- the pages that the tables held, those that the new ones hold whole, and the new rows
+    for (int s = s0 + tid; s < s1; s += T) {
+        const int last = seq[s].z;
+        if (last >= 0) atomicMin(keeper(last), s);
+    }
+    over_rows(
+        s0, s1, [&](int s) { return max(seq[s].w, (seq[s].y + ps - 1) / ps); },
+        [&](int s, int e, int n) {
+            const int4 q = seq[s];
             if (e < q.w) {
-                const int page = mine[e];
-                if (page >= 0 && page < p.n_pages) a.was[page] = 1;
+                const int page = p.block_table[(int64_t)s * p.max_pages + e];
+                if (page >= 0 && page < p.n_pages) was[page] = 1;
                 else bits |= KVQ_DEV_BAD_PAGE;
             }
-            if (e < need) {
-                int page = from[e];
+            if (e < (q.y + ps - 1) / ps) {
+                int page = p.block_table[(int64_t)q.x * p.max_pages + e];
                 if (page < 0 || page >= p.n_pages) {
                     bits |= KVQ_DEV_BAD_PAGE;
                     page = -1;
-                } else if (e < whole) {
-                    a.stays[page] = 1;
+                } else if (e < q.y / ps) {
+                    stays[page] = 1;
                 }
-                to[e] = page;
+                row[(int64_t)s * p.max_pages + e] = page;
             }
+        });
+    team.sync();
+
+    // ---- who copies, in the order of the sequences; who keeps its last page
+    int copies = 0;
+    for (int c = s0; c < s1; c += T) {
+        const int s = c + tid;
+        bool copy = false;
+        int last = -1;
+        if (s < s1) {
+            last = seq[s].z;
+            // (a mark that another thread sets here is for a keeper that is not s: s copies either way)
+            copy = last >= 0 && *keeper(last) != s;
+            if (last >= 0 && !copy)
+                for (int k = 0; k < team.n_cta; ++k) copy |= team.template part<uint8_t>(k, set)[last] != 0;
+            if (last >= 0 && !copy) stays[last] = 1;
         }
-        if (e0 == 0 && lane == 0 && q.z >= 0) atomicMin(a.keeper + q.z, s);
+        int sum;
+        const int r = block_scan(copy ? 1 : 0, s_warp, &sum);
+        if (s < s1) seq[s].x = copy ? copies + r - 1 : -1;
+        copies += sum;
     }
-    cluster.sync();
+    if (tid == 0) s_copies = copies;
+    team.sync();
 
-    // ---- who copies, in the order of the sequences (one CTA); who keeps its last page
-    if (cta == 0) {
-        int carry = 0;
-        for (int c = 0; c < p.n_seq; c += kThreads) {
-            const int s = c + tid;
-            bool copy = false;
-            int last = -1;
-            if (s < p.n_seq) {
-                last = fresh(a.seq + s).z;
-                // (a mark that another thread sets here is for a keeper that is not s: s copies either way)
-                copy = last >= 0 && (fresh(a.keeper + last) != s || fresh(a.stays + last) != 0);
-            }
-            int sum;
-            const int r = block_scan(copy ? 1 : 0, s_warp, &sum);
-            if (s < p.n_seq) {
-                a.rank[s] = copy ? carry + r - 1 : -1;
-                if (last >= 0 && !copy) a.stays[last] = 1;
-            }
-            carry += sum;
+    // ---- pages given back, in this CTA's range: its own marks become theirs
+    const int w0 = min(team.cta * words.each, words.n), w1 = min(w0 + words.each, words.n);
+    uint32_t* const given = reinterpret_cast<uint32_t*>(was);
+    int mine = 0, here;
+    for (int i = w0 + tid; i < w1; i += T) {
+        uint32_t held = 0, kept = 0;
+        for (int k = 0; k < team.n_cta; ++k) {
+            held |= team.template part<uint32_t>(k, 0)[i];
+            kept |= team.template part<uint32_t>(k, set)[i];
         }
-        if (tid == 0) a.count[kCluster] = carry;
+        given[i] = held & ~kept;
+        mine += __popc(held & ~kept);
     }
-    cluster.sync();
-
-    // ---- pages given back: each CTA a range of ids
-    const int per_cta = (n_marks + n_cta - 1) / n_cta;
-    const int m0 = min(cta * per_cta, n_marks), m1 = min(m0 + per_cta, n_marks);
-    auto given = [&](int i) {                               // a byte of 1 for each page of word i that goes back
-        const uint4 w = fresh(reinterpret_cast<const uint4*>(a.was) + i), st = fresh(reinterpret_cast<const uint4*>(a.stays) + i);
-        return make_uint4(w.x & ~st.x, w.y & ~st.y, w.z & ~st.z, w.w & ~st.w);
-    };
-    auto ones = [](uint4 g) { return __popc(g.x) + __popc(g.y) + __popc(g.z) + __popc(g.w); };
-    int mine = 0;
-    for (int i = m0 + tid; i < m1; i += kThreads) mine += ones(given(i));
-    int sum;
-    (void)block_scan(mine, s_warp, &sum);
-    if (tid == 0) a.count[cta] = sum;
-    cluster.sync();
-
-    int above = 0, total = 0;                               // given back by ranges of higher ids; by all
-    for (int c = 0; c < n_cta; ++c) {
-        const int v = fresh(a.count + c);
-        total += v;
-        if (c > cta) above += v;
+    (void)block_scan(mine, s_warp, &here);
+    int above = 0, total = here, want = s_copies, copies0 = 0;
+    if constexpr (!ONE) {
+        if (tid == 0) s_given = here;
+        team.sync();
+        total = want = 0;
+        for (int k = 0; k < team.n_cta; ++k) {
+            const int v = *team.of(k, &s_given), w = *team.of(k, &s_copies);
+            total += v;
+            want += w;
+            if (k > team.cta) above += v;
+            if (k < team.cta) copies0 += w;
+        }
     }
-    // the highest id first: chunks of words from the top
-    for (int top = m1; sum > 0 && top > m0; top -= kThreads) {
+    // the highest id first
+    for (int top = w1; here > 0 && top > w0; top -= T) {
         const int i = top - 1 - tid;
-        const uint4 g = i >= m0 ? given(i) : make_uint4(0u, 0u, 0u, 0u);
-        const int n = ones(g);
-        int in_chunk;
-        int at = n_free + above + block_scan(n, s_warp, &in_chunk) - n;
-        const uint32_t w[4] = {g.x, g.y, g.z, g.w};
-        if (n > 0) {
+        const uint32_t g = i >= w0 ? given[i] : 0;
+        int sum;
+        int at = n_free + above + block_scan(__popc(g), s_warp, &sum) - __popc(g);
 #pragma unroll
-            for (int b = kRun - 1; b >= 0; --b)
-                if (w[b / 4] >> (8 * (b % 4)) & 1) {
-                    if (at < p.n_pages) p.free_list[at] = i * kRun + b;
-                    else bits |= KVQ_DEV_BAD_PAGE;
-                    ++at;
-                }
-        }
-        above += in_chunk;
+        for (int b = 3; b >= 0; --b)
+            if (g >> (8 * b) & 1) {
+                if (at < p.n_pages) p.free_list[at] = i * 4 + b;
+                else bits |= KVQ_DEV_BAD_PAGE;
+                ++at;
+            }
+        above += sum;
     }
-    cluster.sync();
+    team.sync();
 
     // ---- pages for the copies, and the tables
-    const int have = min(n_free + total, p.n_pages);
-    const int want = fresh(a.count + kCluster), used = min(want, have);
-    for (int s = me; s < p.n_seq; s += all) {
-        const int4 q = fresh(a.seq + s);
-        const int r = fresh(a.rank + s);
+    const int have = min(n_free + total, p.n_pages), used = min(want, have);
+    for (int s = s0 + tid; s < s1; s += T) {
+        const int4 q = seq[s];
         int len = q.y;
-        if (r >= 0) {
+        if (q.x >= 0) {
+            const int r = copies0 + q.x;
+            int page = -1;
             if (r < have) {
-                const int page = fresh(p.free_list + have - 1 - r);
-                a.row[(int64_t)s * p.max_pages + len / ps] = page;
+                page = p.free_list[have - 1 - r];
                 p.copy_src[r] = q.z;
                 p.copy_dst[r] = page;
                 p.copy_rows[r] = len % ps;
             } else {
                 bits |= KVQ_DEV_NO_PAGE;
                 len -= len % ps;
-                a.row[(int64_t)s * p.max_pages + len / ps] = -1;
             }
+            p.block_table[(int64_t)s * p.max_pages + q.y / ps] = page;
         }
         if (s >= used) p.copy_src[s] = p.copy_dst[s] = p.copy_rows[s] = -1;
         p.seq_len[s] = len;
         p.n_held[s] = (len + ps - 1) / ps;
     }
-    if (me == 0) {
+    if (team.cta == 0 && tid == 0) {
         p.n_free[0] = have - used;
         p.n_copy[0] = used;
     }
-    cluster.sync();
-    for (int64_t i = warp; i < (int64_t)p.n_seq * per_row; i += n_warps) {
-        const int s = (int)(i / per_row), e0 = (int)(i - (int64_t)s * per_row) * 128;
-        const int4 q = fresh(a.seq + s);
-        const int need = (q.y + ps - 1) / ps;               // (a refused last page is -1 in the row)
-        int32_t* to = p.block_table + (int64_t)s * p.max_pages;
-        const int32_t* from = a.row + (int64_t)s * p.max_pages;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int e = e0 + 32 * u + lane;
-            if (e < need) to[e] = fresh(from + e);
-            else if (e < q.w) to[e] = -1;
-        }
-    }
+    over_rows(
+        s0, s1, [&](int s) { return max(seq[s].w, (seq[s].y + ps - 1) / ps); },
+        [&](int s, int e, int n) {
+            const int4 q = seq[s];
+            const int need = (q.y + ps - 1) / ps;
+            if (e >= n || (q.x >= 0 && e == need - 1)) return;          // (a copy's last page: above)
+            p.block_table[(int64_t)s * p.max_pages + e] = e < need ? row[(int64_t)s * p.max_pages + e] : -1;
+        });
     if (bits) flag(a.status, bits);
 }
 
@@ -276,101 +342,107 @@ __global__ void __launch_bounds__(kThreads) fork_pages_kernel(const ForkArgs a)
 struct CompactArgs {
     kvq_compact_plan p;
     uint32_t* status;
-    uint8_t* used;                       // [n_pages, padded to kRun]
+    uint8_t* store;                      // as in ForkArgs
+    size_t stride;
     int32_t* rank;                       // [n_pages]: number of a page among those that move
-    int32_t* count;                      // [kCluster] held pages of a CTA's range, [kCluster] unheld ones below U,
-                                         // [kCluster] held ones from U on
 };
 
-__global__ void __launch_bounds__(kThreads) compact_pages_kernel(const CompactArgs a)
+template <bool ONE, bool SHARED>
+__global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) compact_pages_kernel(const CompactArgs a)
 {
-    __shared__ int s_warp[kWarps];
-    const cg::cluster_group cluster = cg::this_cluster();
+    extern __shared__ __align__(16) uint8_t s_store[];
+    __shared__ int s_warp[32];
+    __shared__ int s_used, s_holes, s_moves;
     const kvq_compact_plan& p = a.p;
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int n_cta = (int)cluster.num_blocks(), cta = (int)cluster.block_rank();
-    const int all = n_cta * kThreads, me = cta * kThreads + tid;
+    const Team<ONE, SHARED> team(s_store, a.store, a.stride);
+    const Words words(p.n_pages, team.n_cta);
+    const int tid = threadIdx.x, T = blockDim.x, all = team.n_cta * T, me = team.cta * T + tid;
+    uint8_t* const used = team.template mine<uint8_t>(0);
+    const int seqs = (p.n_seq + team.n_cta - 1) / team.n_cta;
+    const int s0 = min(team.cta * seqs, p.n_seq), s1 = min(s0 + seqs, p.n_seq);
     unsigned bits = 0;
 
-    const int n_marks = (p.n_pages + kRun - 1) / kRun;
-    for (int i = me; i < n_marks; i += all) reinterpret_cast<uint4*>(a.used)[i] = make_uint4(0u, 0u, 0u, 0u);
-    cluster.sync();
-
-    const int warp = me >> 5, n_warps = all >> 5;
-    const int per_row = (p.max_pages + 127) / 128;
-    for (int64_t i = warp; i < (int64_t)p.n_seq * per_row; i += n_warps) {
-        const int s = (int)(i / per_row), e0 = (int)(i - (int64_t)s * per_row) * 128;
-        const int held0 = p.n_held[s], held = min(max(held0, 0), p.max_pages);
-        if (held != held0) bits |= KVQ_DEV_BAD_INDEX;
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int e = e0 + 32 * u + lane;
-            if (e >= held) continue;
+    clear(used, words.bytes());
+    __syncthreads();
+    over_rows(
+        s0, s1,
+        [&](int s) {
+            const int held = p.n_held[s], n = min(max(held, 0), p.max_pages);
+            if (held != n) bits |= KVQ_DEV_BAD_INDEX;
+            return n;
+        },
+        [&](int s, int e, int n) {
+            if (e >= n) return;
             const int page = p.block_table[(int64_t)s * p.max_pages + e];
-            if (page >= 0 && page < p.n_pages) a.used[page] = 1;
+            if (page >= 0 && page < p.n_pages) used[page] = 1;
             else bits |= KVQ_DEV_BAD_PAGE;
-        }
-    }
-    cluster.sync();
+        });
+    team.sync();
 
-    const int per_cta = (n_marks + n_cta - 1) / n_cta;
-    const int m0 = min(cta * per_cta, n_marks), m1 = min(m0 + per_cta, n_marks);
-    auto marks = [&](int i) { return fresh(reinterpret_cast<const uint4*>(a.used) + i); };
-    auto ones = [](uint4 g) { return __popc(g.x) + __popc(g.y) + __popc(g.z) + __popc(g.w); };
+    // ---- held pages of this CTA's range: its own marks become all CTAs'
+    const int w0 = min(team.cta * words.each, words.n), w1 = min(w0 + words.each, words.n);
+    uint32_t* const marks = reinterpret_cast<uint32_t*>(used);
     int mine = 0, sum;
-    for (int i = m0 + tid; i < m1; i += kThreads) mine += ones(marks(i));
+    for (int i = w0 + tid; i < w1; i += T) {
+        uint32_t held = 0;
+        for (int k = 0; k < team.n_cta; ++k) held |= team.template part<uint32_t>(k, 0)[i];
+        marks[i] = held;
+        mine += __popc(held);
+    }
     (void)block_scan(mine, s_warp, &sum);
-    if (tid == 0) a.count[cta] = sum;
-    cluster.sync();
-    int n_used = 0;
-    for (int c = 0; c < n_cta; ++c) n_used += fresh(a.count + c);
-
-    // pages that move (held, from U on) or are moved to (not held, below U): a bit each of the run
-    auto places = [&](int i) {
-        const uint4 g = marks(i);
-        const uint32_t w[4] = {g.x, g.y, g.z, g.w};
-        unsigned hole = 0, move = 0;
-#pragma unroll
-        for (int b = 0; b < kRun; ++b) {
-            const int page = i * kRun + b;
-            const bool on = w[b / 4] >> (8 * (b % 4)) & 1;
-            if (page < n_used && !on) hole |= 1u << b;
-            if (page >= n_used && on) move |= 1u << b;
-        }
-        return make_uint2(hole, move);
+    int n_used = sum;
+    if constexpr (!ONE) {
+        if (tid == 0) s_used = sum;
+        team.sync();
+        n_used = 0;
+        for (int k = 0; k < team.n_cta; ++k) n_used += *team.of(k, &s_used);
+    }
+    // pages that are moved to (not held, below U) and that move (held, from U on), a byte of 1 each
+    auto below = [&](int i) {
+        const int n = min(max(n_used - 4 * i, 0), 4);
+        return n == 4 ? 0x01010101u : 0x01010101u & ((1u << 8 * n) - 1u);
     };
-    int holes = 0, moves = 0;
-    for (int i = m0 + tid; i < m1; i += kThreads) {
-        const uint2 q = places(i);
-        holes += __popc(q.x);
-        moves += __popc(q.y);
-    }
-    (void)block_scan(holes, s_warp, &sum);
-    if (tid == 0) a.count[kCluster + cta] = sum;
-    (void)block_scan(moves, s_warp, &sum);
-    if (tid == 0) a.count[2 * kCluster + cta] = sum;
-    cluster.sync();
-    int hole_at = 0, move_at = 0, total = 0;
-    for (int c = 0; c < n_cta; ++c) {
-        const int h = fresh(a.count + kCluster + c), m = fresh(a.count + 2 * kCluster + c);
-        total += m;
-        if (c < cta) {
-            hole_at += h;
-            move_at += m;
+    auto holes_of = [&](int i) { return ~marks[i] & below(i); };
+    auto moves_of = [&](int i) { return marks[i] & ~below(i); };
+    int hole_at = 0, move_at = 0, total;
+    {
+        int holes = 0, moves = 0, sum_h, sum_m;
+        for (int i = w0 + tid; i < w1; i += T) {
+            holes += __popc(holes_of(i));
+            moves += __popc(moves_of(i));
+        }
+        (void)block_scan(holes, s_warp, &sum_h);
+        (void)block_scan(moves, s_warp, &sum_m);
+        total = sum_m;
+        if constexpr (!ONE) {
+            if (tid == 0) {
+                s_holes = sum_h;
+                s_moves = sum_m;
+            }
+            team.sync();
+            total = 0;
+            for (int k = 0; k < team.n_cta; ++k) {
+                const int m = *team.of(k, &s_moves);
+                total += m;
+                if (k < team.cta) {
+                    hole_at += *team.of(k, &s_holes);
+                    move_at += m;
+                }
+            }
         }
     }
-    for (int low = m0; low < m1; low += kThreads) {
+    for (int low = w0; low < w1; low += T) {
         const int i = low + tid;
-        const uint2 q = i < m1 ? places(i) : make_uint2(0u, 0u);
+        const uint32_t hole = i < w1 ? holes_of(i) : 0, move = i < w1 ? moves_of(i) : 0;
         int sum_h, sum_m;
-        int h = hole_at + block_scan(__popc(q.x), s_warp, &sum_h) - __popc(q.x);
-        int m = move_at + block_scan(__popc(q.y), s_warp, &sum_m) - __popc(q.y);
+        int h = hole_at + block_scan(__popc(hole), s_warp, &sum_h) - __popc(hole);
+        int m = move_at + block_scan(__popc(move), s_warp, &sum_m) - __popc(move);
 #pragma unroll
-        for (int b = 0; b < kRun; ++b) {
-            if (q.x >> b & 1) p.copy_dst[h++] = i * kRun + b;
-            if (q.y >> b & 1) {
-                p.copy_src[m] = i * kRun + b;
-                a.rank[i * kRun + b] = m++;
+        for (int b = 0; b < 4; ++b) {
+            if (hole >> (8 * b) & 1) p.copy_dst[h++] = i * 4 + b;
+            if (move >> (8 * b) & 1) {
+                p.copy_src[m] = i * 4 + b;
+                a.rank[i * 4 + b] = m++;
             }
         }
         hole_at += sum_h;
@@ -386,25 +458,21 @@ __global__ void __launch_bounds__(kThreads) compact_pages_kernel(const CompactAr
         p.n_used[0] = n_used;
         p.n_copy[0] = total;
     }
-    cluster.sync();
+    team.sync();
 
-    for (int64_t i = warp; i < (int64_t)p.n_seq * per_row; i += n_warps) {
-        const int s = (int)(i / per_row), e0 = (int)(i - (int64_t)s * per_row) * 128;
-        const int held = min(max(p.n_held[s], 0), p.max_pages);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-            const int e = e0 + 32 * u + lane;
-            if (e >= p.max_pages) continue;
+    over_rows(
+        s0, s1, [&](int) { return p.max_pages; },
+        [&](int s, int e, int n) {
+            if (e >= n) return;
             const int64_t at = (int64_t)s * p.max_pages + e;
             int page = -1;
-            if (e < held) {
+            if (e < p.n_held[s]) {
                 page = p.block_table[at];
                 if (page < 0 || page >= p.n_pages) page = -1;
-                else if (page >= n_used) page = fresh(p.copy_dst + fresh(a.rank + page));
+                else if (page >= n_used) page = p.copy_dst[a.rank[page]];
             }
             p.new_table[at] = page;
-        }
-    }
+        });
     if (bits) flag(a.status, bits);
 }
 
@@ -498,18 +566,47 @@ int cuda_status(cudaError_t e, const char* entry)
 
 size_t up(size_t n) { return (n + 255) / 256 * 256; }
 
-// one CTA where its threads can go over the tables and the marks in a few rounds, else a cluster
-template <typename Args>
-cudaError_t launch_plan(void (*kernel)(Args), const Args& a, int64_t entries, int64_t pages, cudaStream_t s)
+// How a planning kernel runs: one CTA where that is enough, else a cluster; its marks in shared memory where they fit
+struct TeamPlan {
+    bool one = false, shared = false;
+    size_t bytes = 0;                    // of a CTA's marks and keepers
+};
+
+TeamPlan plan_team(int n_seq, int max_pages, int n_pages, int sets, bool keepers)
 {
-    const int n_cta = entries <= 8 * kThreads && pages <= 8 * kThreads * kRun ? 1 : kCluster;
+    TeamPlan t;
+    t.one = n_pages <= kPagesOne && n_seq <= kSeqShared && (int64_t)n_seq * max_pages <= kRowsShared;
+    t.shared = n_pages <= kPagesShared;
+    const Words w(n_pages, t.one ? 1 : kCluster);
+    t.bytes = sets * w.bytes() + (keepers ? (size_t)w.each * 16 : 0);
+    t.bytes = (t.bytes + 15) / 16 * 16;
+    return t;
+}
+
+template <typename Args>
+cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(Args), const TeamPlan& t, size_t rows,
+                        const Args& a, cudaStream_t s)
+{
+    if (t.one) {
+        const size_t smem = t.bytes + rows;
+        cudaError_t e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        one<<<1, kThreadsOne, smem, s>>>(a);
+        return cudaGetLastError();
+    }
+    const auto kernel = t.shared ? shared : global;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)n_cta);
+    cfg.gridDim = dim3(kCluster);
     cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = t.shared ? t.bytes : 0;
     cfg.stream = s;
+    if (t.shared) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)t.bytes);
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = (unsigned)n_cta;
+    attr[0].val.clusterDim.x = kCluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
@@ -580,21 +677,22 @@ int check_workspace(const char* E, const void* workspace, size_t ws_bytes, size_
     return KVQ_OK;
 }
 
+TeamPlan plan_team(const kvq_fork_plan& p) { return plan_team(p.n_seq, p.max_pages, p.n_pages, 2, true); }
+TeamPlan plan_team(const kvq_compact_plan& p) { return plan_team(p.n_seq, p.max_pages, p.n_pages, 1, false); }
+
 size_t lay_out(const kvq_fork_plan& p, uint8_t* ws, ForkArgs* a)
 {
     Layout l;
-    const size_t marks = ((size_t)p.n_pages + kRun - 1) / kRun * kRun, n = (size_t)p.n_seq;
-    const size_t was = l.take(marks), stays = l.take(marks), keeper = l.take((size_t)p.n_pages * 4);
-    const size_t row = l.take(n * p.max_pages * 4), seq = l.take(n * 16), rank = l.take(n * 4);
-    const size_t count = l.take((kCluster + 1) * 4);
+    const TeamPlan t = plan_team(p);
+    const size_t n = (size_t)p.n_seq;
+    const size_t row = l.take(t.one ? 16 : n * p.max_pages * 4), seq = l.take(t.one ? 16 : n * 16);
+    const size_t store = l.take(t.shared ? 0 : t.bytes * kCluster);
     if (a) {
-        a->was = ws + was;
-        a->stays = ws + stays;
-        a->keeper = reinterpret_cast<int32_t*>(ws + keeper);
         a->row = reinterpret_cast<int32_t*>(ws + row);
         a->seq = reinterpret_cast<int4*>(ws + seq);
-        a->rank = reinterpret_cast<int32_t*>(ws + rank);
-        a->count = reinterpret_cast<int32_t*>(ws + count);
+        a->store = ws + store;
+        a->stride = t.bytes;
+        a->rows_shared = t.one;
     }
     return l.bytes;
 }
@@ -602,12 +700,12 @@ size_t lay_out(const kvq_fork_plan& p, uint8_t* ws, ForkArgs* a)
 size_t lay_out(const kvq_compact_plan& p, uint8_t* ws, CompactArgs* a)
 {
     Layout l;
-    const size_t used = l.take(((size_t)p.n_pages + kRun - 1) / kRun * kRun), rank = l.take((size_t)p.n_pages * 4);
-    const size_t count = l.take(3 * kCluster * 4);
+    const TeamPlan t = plan_team(p);
+    const size_t rank = l.take((size_t)p.n_pages * 4 + 16), store = l.take(t.shared ? 0 : t.bytes * kCluster);
     if (a) {
-        a->used = ws + used;
         a->rank = reinterpret_cast<int32_t*>(ws + rank);
-        a->count = reinterpret_cast<int32_t*>(ws + count);
+        a->store = ws + store;
+        a->stride = t.bytes;
     }
     return l.bytes;
 }
@@ -637,7 +735,8 @@ int kvq_fork_pages(const kvq_fork_plan* p, void* workspace, size_t ws_bytes, uin
     a.p = *p;
     a.status = dev_status;
     lay_out(*p, static_cast<uint8_t*>(workspace), &a);
-    return cuda_status(launch_plan(fork_pages_kernel, a, (int64_t)p->n_seq * p->max_pages, p->n_pages, (cudaStream_t)stream), E);
+    return cuda_status(launch_team(fork_pages_kernel<true, true>, fork_pages_kernel<false, true>, fork_pages_kernel<false, false>,
+                                   plan_team(*p), (size_t)p->n_seq * p->max_pages * 4, a, (cudaStream_t)stream), E);
 }
 
 size_t kvq_compact_pages_workspace(const kvq_compact_plan* p)
@@ -659,7 +758,8 @@ int kvq_compact_pages(const kvq_compact_plan* p, void* workspace, size_t ws_byte
     a.p = *p;
     a.status = dev_status;
     lay_out(*p, static_cast<uint8_t*>(workspace), &a);
-    return cuda_status(launch_plan(compact_pages_kernel, a, (int64_t)p->n_seq * p->max_pages, p->n_pages, (cudaStream_t)stream), E);
+    return cuda_status(launch_team(compact_pages_kernel<true, true>, compact_pages_kernel<false, true>,
+                                   compact_pages_kernel<false, false>, plan_team(*p), 0, a, (cudaStream_t)stream), E);
 }
 
 int kvq_copy_pages(const kvq_page_copy* d, uint32_t* dev_status, kvq_stream_t stream)
