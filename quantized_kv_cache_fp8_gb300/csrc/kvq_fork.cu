@@ -66,14 +66,12 @@ struct Team {
     uint8_t* shared;                     // this CTA's dynamic shared memory
     uint8_t* global;                     // the workspace that stands for it, `stride` bytes a CTA
     size_t stride;
-    int n_cta, cta;
+    int cta;
+    static constexpr int n_cta = ONE ? 1 : kCluster;
 
-    __device__ Team(uint8_t* sh, uint8_t* gl, size_t st) : shared(sh), global(gl), stride(st), n_cta(1), cta(0)
+    __device__ Team(uint8_t* sh, uint8_t* gl, size_t st) : shared(sh), global(gl), stride(st), cta(0)
     {
-        if constexpr (!ONE) {
-            n_cta = (int)cg::this_cluster().num_blocks();
-            cta = (int)cg::this_cluster().block_rank();
-        }
+        if constexpr (!ONE) cta = (int)cg::this_cluster().block_rank();
     }
     __device__ void sync() const
     {
@@ -115,19 +113,24 @@ __device__ __forceinline__ void clear(uint8_t* p, size_t bytes)
     for (size_t i = threadIdx.x; i < bytes / 16; i += blockDim.x) reinterpret_cast<uint4*>(p)[i] = make_uint4(0u, 0u, 0u, 0u);
 }
 
-// f(s, e) for the entries e of the rows s = s0 .. s1 - 1, as far as length(s): warps take rows, several a row where
-// there are few, and lanes entries, four of a lane together
-template <typename L, typename F>
-__device__ __forceinline__ void over_rows(int s0, int s1, L length, F f)
+// use(r, e, v) for the entries e < r.n of the rows r = row(s), s = s0 .. s1 - 1, with v = load(r, e): warps take rows,
+// several a row where there are few, and lanes entries, four of a lane loaded together
+template <typename R, typename G, typename F>
+__device__ __forceinline__ void over_rows(int s0, int s1, R row, G load, F use)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_warps = blockDim.x >> 5;
     const int per_row = max(1, n_warps / max(1, s1 - s0)), rows = n_warps / per_row;
     if (warp >= rows * per_row) return;
     for (int s = s0 + warp / per_row; s < s1; s += rows) {
-        const int n = length(s);
-        for (int e0 = warp % per_row * 128; e0 < n; e0 += per_row * 128) {
+        const auto r = row(s);
+        for (int e0 = warp % per_row * 128 + lane; e0 < r.n; e0 += per_row * 128) {
+            decltype(load(r, e0)) v[4];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) f(s, e0 + 32 * u + lane, n);
+            for (int u = 0; u < 4; ++u)
+                if (e0 + 32 * u < r.n) v[u] = load(r, e0 + 32 * u);
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (e0 + 32 * u < r.n) use(r, e0 + 32 * u, v[u]);
         }
     }
 }
@@ -171,11 +174,12 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
     if (n_free != n_free0) bits |= KVQ_DEV_BAD_INDEX;
 
     // ---- marks cleared; every sequence's parent, rows and last page
+    const int par0 = s0 + tid < s1 ? p.parent[s0 + tid] : -1;           // (on its way while the marks are cleared)
     clear(was, set);
     clear(stays, set);
     for (int i = tid; i < words.each * 4; i += T) team.template mine<int32_t>(2 * set)[i] = INT_MAX;
     for (int s = s0 + tid; s < s1; s += T) {
-        int par = p.parent[s];
+        int par = s == s0 + tid ? par0 : p.parent[s];
         const int held = p.n_held[s], own = min(max(held, 0), p.max_pages);
         if (par < -1 || par >= p.n_seq) {
             bits |= KVQ_DEV_BAD_INDEX;
@@ -209,24 +213,34 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
         const int last = seq[s].z;
         if (last >= 0) atomicMin(keeper(last), s);
     }
+    struct Row {
+        int n, own, need, whole;                            // entries in all, before, after, after and whole
+        int64_t at, parent;                                 // where the row begins, and its parent's
+    };
     over_rows(
-        s0, s1, [&](int s) { return max(seq[s].w, (seq[s].y + ps - 1) / ps); },
-        [&](int s, int e, int n) {
+        s0, s1,
+        [&](int s) {
             const int4 q = seq[s];
-            if (e < q.w) {
-                const int page = p.block_table[(int64_t)s * p.max_pages + e];
-                if (page >= 0 && page < p.n_pages) was[page] = 1;
+            const int need = (q.y + ps - 1) / ps;
+            return Row{max(q.w, need), q.w, need, q.y / ps, (int64_t)s * p.max_pages, (int64_t)q.x * p.max_pages};
+        },
+        [&](const Row& r, int e) {                          // its entry before, its parent's
+            return make_int2(e < r.own ? p.block_table[r.at + e] : -1, e < r.need ? p.block_table[r.parent + e] : -1);
+        },
+        [&](const Row& r, int e, int2 v) {
+            if (e < r.own) {
+                if (v.x >= 0 && v.x < p.n_pages) was[v.x] = 1;
                 else bits |= KVQ_DEV_BAD_PAGE;
             }
-            if (e < (q.y + ps - 1) / ps) {
-                int page = p.block_table[(int64_t)q.x * p.max_pages + e];
+            if (e < r.need) {
+                int page = v.y;
                 if (page < 0 || page >= p.n_pages) {
                     bits |= KVQ_DEV_BAD_PAGE;
                     page = -1;
-                } else if (e < q.y / ps) {
+                } else if (e < r.whole) {
                     stays[page] = 1;
                 }
-                row[(int64_t)s * p.max_pages + e] = page;
+                row[r.at + e] = page;
             }
         });
     team.sync();
@@ -242,6 +256,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
             // (a mark that another thread sets here is for a keeper that is not s: s copies either way)
             copy = last >= 0 && *keeper(last) != s;
             if (last >= 0 && !copy)
+#pragma unroll
                 for (int k = 0; k < team.n_cta; ++k) copy |= team.template part<uint8_t>(k, set)[last] != 0;
             if (last >= 0 && !copy) stays[last] = 1;
         }
@@ -259,6 +274,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
     int mine = 0, here;
     for (int i = w0 + tid; i < w1; i += T) {
         uint32_t held = 0, kept = 0;
+#pragma unroll
         for (int k = 0; k < team.n_cta; ++k) {
             held |= team.template part<uint32_t>(k, 0)[i];
             kept |= team.template part<uint32_t>(k, set)[i];
@@ -272,6 +288,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
         if (tid == 0) s_given = here;
         team.sync();
         total = want = 0;
+#pragma unroll
         for (int k = 0; k < team.n_cta; ++k) {
             const int v = *team.of(k, &s_given), w = *team.of(k, &s_copies);
             total += v;
@@ -325,12 +342,16 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
         p.n_copy[0] = used;
     }
     over_rows(
-        s0, s1, [&](int s) { return max(seq[s].w, (seq[s].y + ps - 1) / ps); },
-        [&](int s, int e, int n) {
+        s0, s1,
+        [&](int s) {
             const int4 q = seq[s];
             const int need = (q.y + ps - 1) / ps;
-            if (e >= n || (q.x >= 0 && e == need - 1)) return;          // (a copy's last page: above)
-            p.block_table[(int64_t)s * p.max_pages + e] = e < need ? row[(int64_t)s * p.max_pages + e] : -1;
+            // (whole: a copy's last page is written above)
+            return Row{max(q.w, need), q.w, need, q.x >= 0 ? q.y / ps : -1, (int64_t)s * p.max_pages, 0};
+        },
+        [&](const Row& r, int e) { return e < r.need ? row[r.at + e] : -1; },
+        [&](const Row& r, int e, int page) {
+            if (e != r.whole) p.block_table[r.at + e] = page;
         });
     if (bits) flag(a.status, bits);
 }
@@ -364,16 +385,19 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) compact_pages_ke
 
     clear(used, words.bytes());
     __syncthreads();
+    struct Row {
+        int n, held;                                        // entries in all, held
+        int64_t at;                                         // where the row begins
+    };
     over_rows(
         s0, s1,
         [&](int s) {
             const int held = p.n_held[s], n = min(max(held, 0), p.max_pages);
             if (held != n) bits |= KVQ_DEV_BAD_INDEX;
-            return n;
+            return Row{n, n, (int64_t)s * p.max_pages};
         },
-        [&](int s, int e, int n) {
-            if (e >= n) return;
-            const int page = p.block_table[(int64_t)s * p.max_pages + e];
+        [&](const Row& r, int e) { return p.block_table[r.at + e]; },
+        [&](const Row&, int, int page) {
             if (page >= 0 && page < p.n_pages) used[page] = 1;
             else bits |= KVQ_DEV_BAD_PAGE;
         });
@@ -385,6 +409,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) compact_pages_ke
     int mine = 0, sum;
     for (int i = w0 + tid; i < w1; i += T) {
         uint32_t held = 0;
+#pragma unroll
         for (int k = 0; k < team.n_cta; ++k) held |= team.template part<uint32_t>(k, 0)[i];
         marks[i] = held;
         mine += __popc(held);
@@ -461,18 +486,13 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) compact_pages_ke
     team.sync();
 
     over_rows(
-        s0, s1, [&](int) { return p.max_pages; },
-        [&](int s, int e, int n) {
-            if (e >= n) return;
-            const int64_t at = (int64_t)s * p.max_pages + e;
-            int page = -1;
-            if (e < p.n_held[s]) {
-                page = p.block_table[at];
-                if (page < 0 || page >= p.n_pages) page = -1;
-                else if (page >= n_used) page = p.copy_dst[a.rank[page]];
-            }
-            p.new_table[at] = page;
-        });
+        s0, s1, [&](int s) { return Row{p.max_pages, p.n_held[s], (int64_t)s * p.max_pages}; },
+        [&](const Row& r, int e) {
+            const int page = e < r.held ? p.block_table[r.at + e] : -1;
+            if (page < 0 || page >= p.n_pages) return -1;
+            return page < n_used ? page : p.copy_dst[a.rank[page]];
+        },
+        [&](const Row& r, int e, int page) { p.new_table[r.at + e] = page; });
     if (bits) flag(a.status, bits);
 }
 
