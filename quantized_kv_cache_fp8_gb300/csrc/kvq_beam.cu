@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
     __shared__ V s_vec[kVectors];
     __shared__ int s_at[kVectors];
     const kvq_beam_problem& p = a.p;
+    grid_dependency_wait();
     grid_dependents_launch();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int k = p.n_out;
@@ -452,7 +453,9 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     const int64_t row0 = (int64_t)blockIdx.x * p.n_beam;
     const int k = p.n_out, per_beam = a.n_chunk * k;
     if (tid == 0) s_n = 0;
-    float score = 0.0f;                                     // of beam `tid` (inputs: read ahead of the wait)
+    // (the chunks' kernel lets this one start when all before it has ended, and writes no input: those are read ahead
+    // of the wait)
+    float score = 0.0f;                                     // of beam `tid`
     int live = 0;
     if (tid < p.n_beam) {
         score = p.score[row0 + tid];
@@ -463,6 +466,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     }
     __syncthreads();
     grid_dependency_wait();
+    grid_dependents_launch();
     // A list is what a chunk left, descending; `share` threads (a power of two) take its places in turn, so that each
     // one's first is its largest.  That one is read here already (of a dead beam it is not used, and may be anything).
     // List l is chunk l / n_beam of beam l % n_beam: where one beam has all the best, they are in many groups of lanes.
@@ -655,13 +659,12 @@ int check_problem(const kvq_beam_problem* p, const char* E)
 }
 
 template <typename X>
-void launch_chunks(const BeamArgs& a, int nv, cudaStream_t s)
+cudaError_t launch_chunks(const BeamArgs& a, int nv, cudaStream_t s)
 {
     const int64_t items = (int64_t)a.p.n_req * a.p.n_beam * a.n_chunk;
     // (a CTA a chunk up to many: the finished beams' make the work uneven, and the GPU levels it)
     const unsigned grid = (unsigned)std::min<int64_t>(items, 64 * (int64_t)sm_count());
-    if (nv == 8) beam_chunk_kernel<X, 8><<<grid, kThreads, 0, s>>>(a);
-    else beam_chunk_kernel<X, 2><<<grid, kThreads, 0, s>>>(a);
+    return launch_dependent(nv == 8 ? beam_chunk_kernel<X, 8> : beam_chunk_kernel<X, 2>, dim3(grid), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace
@@ -694,9 +697,7 @@ int kvq_beam_select(const kvq_beam_problem* p, void* workspace, size_t ws_bytes,
     BeamArgs a{*p, q.n_chunk, reinterpret_cast<float*>(ws), reinterpret_cast<float2*>(ws + q.off_s),
                reinterpret_cast<uint64_t*>(ws + q.off_key), dev_status};
     const cudaStream_t s = (cudaStream_t)stream;
-    if (p->x_type == KVQ_WEIGHT_BF16) launch_chunks<__nv_bfloat16>(a, q.nv, s);
-    else launch_chunks<float>(a, q.nv, s);
-    cudaError_t e = cudaGetLastError();
+    cudaError_t e = p->x_type == KVQ_WEIGHT_BF16 ? launch_chunks<__nv_bfloat16>(a, q.nv, s) : launch_chunks<float>(a, q.nv, s);
     if (e == cudaSuccess) e = launch_dependent(beam_merge_kernel, dim3((unsigned)p->n_req), dim3(kThreads), 0, s, a);
     return e == cudaSuccess ? KVQ_OK : set_last_error(KVQ_ECUDA, "%s: %s", E, cudaGetErrorString(e));
 }

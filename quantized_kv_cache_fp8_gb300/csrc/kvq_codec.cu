@@ -758,6 +758,8 @@ __global__ void __launch_bounds__(kCodecThreads) append_kv8_kernel(const AppendK
     const int64_t n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const uint32_t per_row = 2u * (uint32_t)a.c.n_kv;
     const int64_t n = a.rows * per_row;
+    grid_dependency_wait();
+    grid_dependents_launch();
     for (int64_t i0 = warp * (kPerWarp * kKvRun); i0 < n; i0 += n_warps * (kPerWarp * kKvRun)) {
         uint4 w[kKvRun][kWords];
         int64_t at[kKvRun];                                // row of the planes, -1: none
@@ -1620,17 +1622,10 @@ cudaError_t launch_append_kv8(const void* k, int64_t k_row, int64_t k_head, cons
     const AppendKv8Args a{k, v, k_row, k_head, v_row, v_head, rows, RowSlot{slot, c.n_rows, dev_status}, c};
     const int64_t per_cta = (int64_t)kCodecWarps * (256 / c.head_dim) * kKvRun;
     const int64_t g = std::max<int64_t>(1, std::min<int64_t>((rows * 2 * c.n_kv + per_cta - 1) / per_cta, (int64_t)sm_count() * 64));
-#define KVQ_APPEND_KV8(D)                                                                      \
-    if (bf16) append_kv8_kernel<D, __nv_bfloat16><<<(unsigned)g, kCodecThreads, 0, s>>>(a);    \
-    else append_kv8_kernel<D, float><<<(unsigned)g, kCodecThreads, 0, s>>>(a);                 \
-    break
-    switch (c.head_dim) {
-        case 64: KVQ_APPEND_KV8(64);
-        case 128: KVQ_APPEND_KV8(128);
-        default: KVQ_APPEND_KV8(256);
-    }
-#undef KVQ_APPEND_KV8
-    return cudaGetLastError();
+    const auto kernel = c.head_dim == 64    ? bf16 ? append_kv8_kernel<64, __nv_bfloat16> : append_kv8_kernel<64, float>
+                        : c.head_dim == 128 ? bf16 ? append_kv8_kernel<128, __nv_bfloat16> : append_kv8_kernel<128, float>
+                                            : bf16 ? append_kv8_kernel<256, __nv_bfloat16> : append_kv8_kernel<256, float>;
+    return launch_dependent(kernel, dim3((unsigned)g), dim3(kCodecThreads), 0, s, a);
 }
 
 void tq_codebook_values(int bits, float* centroids, float* thresholds)

@@ -160,6 +160,8 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
     const Team<ONE, SHARED> team(s_store, a.store, a.stride);
     const Words words(p.n_pages, team.n_cta);
     const size_t set = words.bytes();
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int tid = threadIdx.x, T = blockDim.x, ps = p.page_size;
     uint8_t *was = team.template mine<uint8_t>(0), *stays = team.template mine<uint8_t>(set);
     auto keeper = [&](int page) { return team.template part<int32_t>(page / 4 / words.each, 2 * set) + (page - page / 4 / words.each * words.each * 4); };
@@ -377,6 +379,8 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) compact_pages_ke
     const kvq_compact_plan& p = a.p;
     const Team<ONE, SHARED> team(s_store, a.store, a.stride);
     const Words words(p.n_pages, team.n_cta);
+    grid_dependency_wait();
+    grid_dependents_launch();
     const int tid = threadIdx.x, T = blockDim.x, all = team.n_cta * T, me = team.cta * T + tid;
     uint8_t* const used = team.template mine<uint8_t>(0);
     const int seqs = (p.n_seq + team.n_cta - 1) / team.n_cta;
@@ -541,6 +545,8 @@ __device__ __forceinline__ void copy_piece(uint8_t* dst, const uint8_t* src, int
 __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a)
 {
     const int lane = threadIdx.x & 31;
+    grid_dependency_wait();                                 // (of the plan, as a rule)
+    grid_dependents_launch();
     const int n_copy = min(max(a.n_copy[0], 0), a.max_copy);
     const int per = a.plane[a.n_planes - 1].piece_end;
     const int64_t n = (int64_t)n_copy * per;
@@ -611,8 +617,7 @@ cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(
         const size_t smem = t.bytes + rows;
         cudaError_t e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
         if (e != cudaSuccess) return e;
-        one<<<1, kThreadsOne, smem, s>>>(a);
-        return cudaGetLastError();
+        return launch_dependent(one, dim3(1), dim3(kThreadsOne), smem, s, a);
     }
     const auto kernel = t.shared ? shared : global;
     cudaLaunchConfig_t cfg = {};
@@ -624,12 +629,14 @@ cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)t.bytes);
         if (e != cudaSuccess) return e;
     }
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = kCluster;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -829,8 +836,7 @@ int kvq_copy_pages(const kvq_page_copy* d, uint32_t* dev_status, kvq_stream_t st
     a.status = dev_status;
     const int64_t warps = (int64_t)d->max_copy * end;
     const int64_t grid = std::min<int64_t>((warps * 32 + kCopyThreads - 1) / kCopyThreads, (int64_t)sm_count() * 8);
-    copy_pages_kernel<<<(unsigned)grid, kCopyThreads, 0, (cudaStream_t)stream>>>(a);
-    return cuda_status(cudaGetLastError(), E);
+    return cuda_status(launch_dependent(copy_pages_kernel, dim3((unsigned)grid), dim3(kCopyThreads), 0, (cudaStream_t)stream, a), E);
 }
 
 }  // extern "C"

@@ -194,6 +194,7 @@ kv8_decode_kernel(const Kv8Args a)
     __shared__ int s_sum[W];
     __shared__ Line s_line;
     __shared__ int4 s_at[W];                                // of a warp: place, end of the stretch, sequence, place in it
+    grid_dependency_wait();
     grid_dependents_launch();
     const kvq_kv8_problem& p = a.p;
     const int c = blockIdx.x / a.n_hb, hb = blockIdx.x % a.n_hb;
@@ -737,6 +738,7 @@ __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_h
     const int joins = gridDim.x / a.n_hb, mine = blockIdx.x / a.n_hb;
     const int stop = (int)((mine + 1) * (int64_t)a.line / joins);
     grid_dependency_wait();
+    grid_dependents_launch();
     for (int first = (int)(mine * (int64_t)a.line / joins); first < stop; first += kJoinThreads) {
         const int look = first + threadIdx.x;
         const int4 found = look < stop ? a.info[look * a.n_hb + hb] : make_int4(-1, 0, 0, 0);
@@ -849,8 +851,7 @@ struct Kv8Kind {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
         if (e != cudaSuccess) return e;
         const unsigned ctas = (unsigned)(a.line * a.n_hb);
-        kernel<<<ctas, 32 * W, Shape::kSmem, s>>>(a);
-        e = cudaGetLastError();
+        e = launch_dependent(kernel, dim3(ctas), dim3(32 * W), Shape::kSmem, s, a);
         if (e == cudaSuccess && q.cuts) {
             const dim3 grid((unsigned)q.joins, (unsigned)std::min(a.group, kHb));
             e = q.line >= 16 * (q.joins / q.n_hb) ? launch_dependent(kv8_combine_kernel<D, 512>, grid, dim3(512), 0, s, a, kHb)
