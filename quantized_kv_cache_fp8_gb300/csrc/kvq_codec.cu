@@ -736,96 +736,114 @@ append_mla_kernel(const X* __restrict__ c_lat, int64_t ldx, const X* __restrict_
 // ------------------------------------------------------------------------------------
 // Paged append of a grouped-query model's K/V rows in fp8 (the bytes of encode_fp8_vec_rows): D / 8
 // lanes take the vector of one row, one of K and V and one KV head, 8 elements a lane (one 16-byte load of
-// bfloat16, two of fp32), 8-byte stores.  Vectors in the order of the rows' memory, kKvRun of them a group of
-// lanes at once, loads first.  Bound by the rows' bytes.
+// bfloat16, two of fp32), 8-byte stores.  A warp takes RUN 256 / D of a row's 2 n_kv vectors (K's heads, then V's),
+// loads first: the row and its slot are looked up once.  Bound by the rows' bytes, with the arithmetic not far behind
+// (a division a vector and a correction a quotient, two quotients at a time): 32768 rows of 8 heads of 128 64 us with a
+// row and a division for every vector, 37 so.
 // ------------------------------------------------------------------------------------
-constexpr int kKvRun = 4;
-
 struct AppendKv8Args {
     const void *k, *v;
     int64_t k_row, k_head, v_row, v_head;    // strides in elements
     int64_t rows;
+    int units;                               // warps' shares of a row
     RowSlot row_of;
     kvq_kv8_cache c;
 };
 
-template <int D, typename X>
+// x / 448, correctly rounded: with c = RN(1 / 448) and q = RN(x c), which is within 1 ulp of x / 448 (half of one
+// for c's rounding, half for its own), RN(q + (x - 448 q) c) is RN(x / 448) (Markstein, 1990); the remainder is exact but
+// for the smallest x
+__device__ __forceinline__ float over_448(float x)
+{
+    if (x < 0x1p-90f) return __fdiv_rn(x, 448.0f);
+    constexpr float c = 1.0f / 448.0f;
+    const float q = __fmul_rn(x, c);
+    return __fmaf_rn(__fmaf_rn(-448.0f, q, x), c, q);
+}
+
+// the quotients of a pair by s, y = RN(1 / s), as in append_fp8_bf16_rows
+__device__ __forceinline__ void divide_pair(float& a, float& b, float s, float y)
+{
+    uint64_t x, q, r, s2, ny2;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(-a), "f"(-b));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+    asm("mov.b64 %0, {%1, %1};" : "=l"(ny2) : "f"(-y));
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(ny2));         // q = a y
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(q), "l"(s2), "l"(x));      // q s - a
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(r), "l"(ny2), "l"(q));     // q - (q s - a) y
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
+}
+
+template <int D, typename X, int RUN>
 __global__ void __launch_bounds__(kCodecThreads) append_kv8_kernel(const AppendKv8Args a)
 {
     constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes, kWords = sizeof(X) == 2 ? 1 : 2;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
     const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
     const int64_t n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    const uint32_t per_row = 2u * (uint32_t)a.c.n_kv;
-    const int64_t n = a.rows * per_row;
+    const int n_kv = a.c.n_kv;
+    const int64_t n = a.rows * a.units;
     grid_dependency_wait();
     grid_dependents_launch();
-    for (int64_t i0 = warp * (kPerWarp * kKvRun); i0 < n; i0 += n_warps * (kPerWarp * kKvRun)) {
-        uint4 w[kKvRun][kWords];
-        int64_t at[kKvRun];                                // row of the planes, -1: none
-        bool is_v[kKvRun];
+    for (int64_t i = warp; i < n; i += n_warps) {
+        const int64_t r = n <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / (uint32_t)a.units) : i / a.units;
+        const int first = (int)(i - r * a.units) * (RUN * kPerWarp) + sub;
+        const int64_t slot = a.row_of(r);
+        if (slot < 0) continue;
+        const X* const k = static_cast<const X*>(a.k) + r * a.k_row + l * 8;
+        const X* const v = static_cast<const X*>(a.v) + r * a.v_row + l * 8;
+        uint4 w[RUN][kWords];
 #pragma unroll
-        for (int u = 0; u < kKvRun; ++u) {
-            const int64_t i = i0 + u * kPerWarp + sub;
-            at[u] = -1;
-            is_v[u] = false;
-            if (i >= n) continue;
-            const int64_t r = n <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / per_row) : i / per_row;
-            int h = (int)(i - r * per_row);
-            is_v[u] = h >= a.c.n_kv;
-            if (is_v[u]) h -= a.c.n_kv;
-            const int64_t slot = a.row_of(r);
-            if (slot < 0) continue;
-            at[u] = h * a.c.n_rows + slot;
-            const X* src = static_cast<const X*>(is_v[u] ? a.v : a.k) + r * (is_v[u] ? a.v_row : a.k_row) +
-                           h * (is_v[u] ? a.v_head : a.k_head);
+        for (int u = 0; u < RUN; ++u) {
+            const int vec = first + u * kPerWarp;
+            const bool is_v = vec >= n_kv;
+            const int h = is_v ? vec - n_kv : vec;
+            const X* src = (is_v ? v : k) + h * (is_v ? a.v_head : a.k_head);
 #pragma unroll
-            for (int e = 0; e < kWords; ++e) w[u][e] = __ldcs(reinterpret_cast<const uint4*>(src) + l * kWords + e);
+            for (int e = 0; e < kWords; ++e)
+                w[u][e] = vec < 2 * n_kv ? __ldcs(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
-        for (int u = 0; u < kKvRun; ++u) {
+        for (int u = 0; u < RUN; ++u) {
+            const int vec = first + u * kPerWarp;
             float f[8];
             float amax = 0.0f;
-            if (at[u] >= 0) {
 #pragma unroll
-                for (int e = 0; e < kWords; ++e) {
-                    const uint32_t x[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
+            for (int e = 0; e < kWords; ++e) {
+                const uint32_t x[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if constexpr (sizeof(X) == 2) {
-                            f[2 * j] = __uint_as_float(x[j] << 16);
-                            f[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
-                        } else {
-                            f[4 * e + j] = __uint_as_float(x[j]);
-                        }
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(X) == 2) {
+                        f[2 * j] = __uint_as_float(x[j] << 16);
+                        f[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                    } else {
+                        f[4 * e + j] = __uint_as_float(x[j]);
                     }
                 }
-#pragma unroll
-                for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
             }
 #pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
+#pragma unroll
             for (int m = kLanes / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
-            if (at[u] < 0) continue;
-            const float s = __fdiv_rn(amax, 448.0f);
+            const float s = over_448(amax);
             uint2 c = make_uint2(0u, 0u);
             if (amax != 0.0f) {
                 // the quotients of bfloat16 rows as in append_fp8_bf16_rows
-                const bool plain = sizeof(X) == 2 && s >= 0x1p-90f && s <= 0x1p90f;
-                if (plain) {
+                if (sizeof(X) == 2 && s >= 0x1p-90f && s <= 0x1p90f) {
                     const float y = __frcp_rn(s);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float q = __fmul_rn(f[j], y);
-                        f[j] = __fmaf_rn(-__fmaf_rn(q, s, -f[j]), y, q);
-                    }
+                    for (int j = 0; j < 8; j += 2) divide_pair(f[j], f[j + 1], s, y);
                 } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], s);
                 }
                 c = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
             }
-            reinterpret_cast<uint2*>((is_v[u] ? a.c.v : a.c.k) + at[u] * D)[l] = c;
-            if (l == 0) (is_v[u] ? a.c.v_scale : a.c.k_scale)[at[u]] = s;
+            if (vec >= 2 * n_kv) continue;
+            const bool is_v = vec >= n_kv;
+            const int64_t at = (is_v ? vec - n_kv : vec) * a.c.n_rows + slot;
+            reinterpret_cast<uint2*>((is_v ? a.c.v : a.c.k) + at * D)[l] = c;
+            if (l == 0) (is_v ? a.c.v_scale : a.c.k_scale)[at] = s;
         }
     }
 }
@@ -1619,12 +1637,16 @@ cudaError_t launch_append_kv8(const void* k, int64_t k_row, int64_t k_head, cons
                               bool bf16, int64_t rows, const int32_t* slot, const kvq_kv8_cache& c,
                               uint32_t* dev_status, cudaStream_t s)
 {
-    const AppendKv8Args a{k, v, k_row, k_head, v_row, v_head, rows, RowSlot{slot, c.n_rows, dev_status}, c};
-    const int64_t per_cta = (int64_t)kCodecWarps * (256 / c.head_dim) * kKvRun;
-    const int64_t g = std::max<int64_t>(1, std::min<int64_t>((rows * 2 * c.n_kv + per_cta - 1) / per_cta, (int64_t)sm_count() * 64));
-    const auto kernel = c.head_dim == 64    ? bf16 ? append_kv8_kernel<64, __nv_bfloat16> : append_kv8_kernel<64, float>
-                        : c.head_dim == 128 ? bf16 ? append_kv8_kernel<128, __nv_bfloat16> : append_kv8_kernel<128, float>
-                                            : bf16 ? append_kv8_kernel<256, __nv_bfloat16> : append_kv8_kernel<256, float>;
+    // vectors of a row that a warp takes at once: as many as the row has, up to four loads a lane
+    const int per = 256 / c.head_dim, vecs = 2 * c.n_kv, run = vecs >= 4 * per ? 4 : vecs >= 2 * per ? 2 : 1;
+    const AppendKv8Args a{k, v, k_row, k_head, v_row, v_head, rows, (vecs + run * per - 1) / (run * per),
+                          RowSlot{slot, c.n_rows, dev_status}, c};
+    const int64_t g = std::max<int64_t>(1, std::min<int64_t>((rows * a.units + kCodecWarps - 1) / kCodecWarps, (int64_t)sm_count() * 64));
+#define KVQ_RUNS(D, X) (run == 4 ? append_kv8_kernel<D, X, 4> : run == 2 ? append_kv8_kernel<D, X, 2> : append_kv8_kernel<D, X, 1>)
+#define KVQ_TYPES(D) (bf16 ? KVQ_RUNS(D, __nv_bfloat16) : KVQ_RUNS(D, float))
+    const auto kernel = c.head_dim == 64 ? KVQ_TYPES(64) : c.head_dim == 128 ? KVQ_TYPES(128) : KVQ_TYPES(256);
+#undef KVQ_TYPES
+#undef KVQ_RUNS
     return launch_dependent(kernel, dim3((unsigned)g), dim3(kCodecThreads), 0, s, a);
 }
 

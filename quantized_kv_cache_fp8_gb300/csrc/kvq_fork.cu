@@ -22,6 +22,7 @@ constexpr int kThreadsOne = 512;
 constexpr int kSeqShared = 512;          // sequences of a CTA whose lengths are kept in shared memory
 constexpr int kRowsShared = 8192;        // table entries of a single CTA that are
 constexpr int kPagesOne = 8192;          // pages that a single CTA goes over (5 bytes of shared memory each)
+constexpr size_t kPlainSmem = 39 * 1024; // dynamic shared memory that needs no attribute, beside the kernels' own
 constexpr int kPagesShared = 65536;      // pages whose marks fit the CTAs' shared memory
 
 __device__ __forceinline__ void flag(uint32_t* status, unsigned bit)
@@ -505,7 +506,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) compact_pages_ke
 // plane, for every entry of the list; as many warps as the machine holds go over them.  Bound by the
 // bytes, read and written once.
 // ------------------------------------------------------------------------------------
-constexpr int kMaxPlanes = 64;
+constexpr int kMaxPlanes = 64, kFewPlanes = 4;
 constexpr int kCopyThreads = 256;
 constexpr int kPiece = 4096;
 
@@ -517,11 +518,12 @@ struct CopyPlane {
     int32_t width;                       // bytes at a time: 16, 4 or 1
 };
 
+template <int N>                         // planes at most (the arguments travel with every launch)
 struct CopyArgs {
     int32_t n_planes, page_size, max_copy;
     const int32_t *src, *dst, *rows, *n_copy;
     uint32_t* status;
-    CopyPlane plane[kMaxPlanes];
+    CopyPlane plane[N];
 };
 
 template <typename T>
@@ -542,7 +544,8 @@ __device__ __forceinline__ void copy_piece(uint8_t* dst, const uint8_t* src, int
     }
 }
 
-__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a)
+template <int N>
+__global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_constant__ CopyArgs<N> a)
 {
     const int lane = threadIdx.x & 31;
     grid_dependency_wait();                                 // (of the plan, as a rule)
@@ -615,8 +618,10 @@ cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(
 {
     if (t.one) {
         const size_t smem = t.bytes + rows;
-        cudaError_t e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return e;
+        if (smem > kPlainSmem) {
+            cudaError_t e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+        }
         return launch_dependent(one, dim3(1), dim3(kThreadsOne), smem, s, a);
     }
     const auto kernel = t.shared ? shared : global;
@@ -625,7 +630,7 @@ cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = t.shared ? t.bytes : 0;
     cfg.stream = s;
-    if (t.shared) {
+    if (cfg.dynamicSmemBytes > kPlainSmem) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)t.bytes);
         if (e != cudaSuccess) return e;
     }
@@ -798,7 +803,7 @@ int kvq_copy_pages(const kvq_page_copy* d, uint32_t* dev_status, kvq_stream_t st
     if (d->n_planes < 1 || d->n_planes > kMaxPlanes || !d->planes)
         return set_last_error(KVQ_EINVAL, "%s: n_planes outside [1, 64] or NULL planes", E);
     if (d->page_size < 1 || d->max_copy < 0) return set_last_error(KVQ_EINVAL, "%s: bad sizes", E);
-    CopyArgs a{};
+    CopyArgs<kMaxPlanes> a;
     a.n_planes = d->n_planes;
     a.page_size = d->page_size;
     a.max_copy = d->max_copy;
@@ -836,7 +841,11 @@ int kvq_copy_pages(const kvq_page_copy* d, uint32_t* dev_status, kvq_stream_t st
     a.status = dev_status;
     const int64_t warps = (int64_t)d->max_copy * end;
     const int64_t grid = std::min<int64_t>((warps * 32 + kCopyThreads - 1) / kCopyThreads, (int64_t)sm_count() * 8);
-    return cuda_status(launch_dependent(copy_pages_kernel, dim3((unsigned)grid), dim3(kCopyThreads), 0, (cudaStream_t)stream, a), E);
+    if (d->n_planes > kFewPlanes)
+        return cuda_status(launch_dependent(copy_pages_kernel<kMaxPlanes>, dim3((unsigned)grid), dim3(kCopyThreads), 0, (cudaStream_t)stream, a), E);
+    CopyArgs<kFewPlanes> few{a.n_planes, a.page_size, a.max_copy, a.src, a.dst, a.rows, a.n_copy, a.status, {}};
+    std::copy(a.plane, a.plane + d->n_planes, few.plane);
+    return cuda_status(launch_dependent(copy_pages_kernel<kFewPlanes>, dim3((unsigned)grid), dim3(kCopyThreads), 0, (cudaStream_t)stream, few), E);
 }
 
 }  // extern "C"

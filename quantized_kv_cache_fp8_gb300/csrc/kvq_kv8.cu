@@ -848,10 +848,9 @@ struct Kv8Kind {
     static cudaError_t launch_as(const Kv8Args& a, const Kv8Plan& q, cudaStream_t s)
     {
         const auto kernel = kv8_decode_kernel<D, NB, R, W, C, GROUPED>;
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Shape::kSmem);
-        if (e != cudaSuccess) return e;
+        static_assert(Shape::kSmem <= 48 * 1024, "more needs an attribute of the kernel");
         const unsigned ctas = (unsigned)(a.line * a.n_hb);
-        e = launch_dependent(kernel, dim3(ctas), dim3(32 * W), Shape::kSmem, s, a);
+        cudaError_t e = launch_dependent(kernel, dim3(ctas), dim3(32 * W), Shape::kSmem, s, a);
         if (e == cudaSuccess && q.cuts) {
             const dim3 grid((unsigned)q.joins, (unsigned)std::min(a.group, kHb));
             e = q.line >= 16 * (q.joins / q.n_hb) ? launch_dependent(kv8_combine_kernel<D, 512>, grid, dim3(512), 0, s, a, kHb)
