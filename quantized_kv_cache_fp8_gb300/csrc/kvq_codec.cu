@@ -734,12 +734,12 @@ append_mla_kernel(const X* __restrict__ c_lat, int64_t ldx, const X* __restrict_
 }
 
 // ------------------------------------------------------------------------------------
-// Paged append of a grouped-query model's K/V rows in fp8 (the bytes of encode_fp8_vec_rows): D / 8
-// lanes take the vector of one row, one of K and V and one KV head, 8 elements a lane (one 16-byte load of
-// bfloat16, two of fp32), 8-byte stores.  A warp takes RUN 256 / D of a row's 2 n_kv vectors (K's heads, then V's),
-// loads first: the row and its slot are looked up once.  Bound by the rows' bytes, with the arithmetic not far behind
-// (a division a vector and a correction a quotient, two quotients at a time): 32768 rows of 8 heads of 128 64 us with a
-// row and a division for every vector, 37 so.
+// Paged append of a grouped-query model's K/V rows in fp8 (the bytes of encode_fp8_vec_rows): D / 16
+// lanes take the vector of one row, one of K and V and one KV head, 16 elements a lane (16-byte loads).  A warp takes
+// 512 / D of a row's 2 n_kv vectors (K's heads, then V's) at once, with the next ones on their way.
+// Bound by the rows' bytes, with the arithmetic not far behind (a division a vector and a correction a quotient, two
+// quotients at a time; what is done once a lane is shared by its 16 elements): 32768 rows of 8 heads of 128 take 64 us
+// with a row and a division for every vector, 52 with 8 elements a lane, APPEND_US so.
 // ------------------------------------------------------------------------------------
 struct AppendKv8Args {
     const void *k, *v;
@@ -774,77 +774,86 @@ __device__ __forceinline__ void divide_pair(float& a, float& b, float s, float y
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
 }
 
-template <int D, typename X, int RUN>
+template <int D, typename X>
 __global__ void __launch_bounds__(kCodecThreads) append_kv8_kernel(const AppendKv8Args a)
 {
-    constexpr int kLanes = D / 8, kPerWarp = 32 / kLanes, kWords = sizeof(X) == 2 ? 1 : 2;
+    constexpr int kLanes = D / 16, kPerWarp = 32 / kLanes;
+    constexpr int kElems = 16 / (int)sizeof(X), kPieces = 16 / kElems;      // a piece: 16 bytes of a row
     const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
-    const int64_t warp = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
     const int64_t n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int n_kv = a.c.n_kv;
     const int64_t n = a.rows * a.units;
     grid_dependency_wait();
     grid_dependents_launch();
-    for (int64_t i = warp; i < n; i += n_warps) {
+    // the vector at hand: its row of the planes (-1: none) and elements; the next one's are on their way meanwhile
+    uint4 next[kPieces];
+    int64_t next_at = -1;
+    bool next_v = false;
+    auto fetch = [&](int64_t i) {
+        next_at = -1;
+        if (i >= n) return;
         const int64_t r = n <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / (uint32_t)a.units) : i / a.units;
-        const int first = (int)(i - r * a.units) * (RUN * kPerWarp) + sub;
+        const int vec = (int)(i - r * a.units) * kPerWarp + sub;
         const int64_t slot = a.row_of(r);
-        if (slot < 0) continue;
-        const X* const k = static_cast<const X*>(a.k) + r * a.k_row + l * 8;
-        const X* const v = static_cast<const X*>(a.v) + r * a.v_row + l * 8;
-        uint4 w[RUN][kWords];
+        if (slot < 0 || vec >= 2 * n_kv) return;
+        next_v = vec >= n_kv;
+        const int h = next_v ? vec - n_kv : vec;
+        next_at = h * a.c.n_rows + slot;
+        const X* src = next_v ? static_cast<const X*>(a.v) + r * a.v_row + h * a.v_head
+                              : static_cast<const X*>(a.k) + r * a.k_row + h * a.k_head;
 #pragma unroll
-        for (int u = 0; u < RUN; ++u) {
-            const int vec = first + u * kPerWarp;
-            const bool is_v = vec >= n_kv;
-            const int h = is_v ? vec - n_kv : vec;
-            const X* src = (is_v ? v : k) + h * (is_v ? a.v_head : a.k_head);
+        for (int e = 0; e < kPieces; ++e) next[e] = __ldcs(reinterpret_cast<const uint4*>(src) + l + e * kLanes);
+    };
+    int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+    fetch(i);
+    for (; i < n; i += n_warps) {
+        const int64_t at = next_at;
+        const bool is_v = next_v;
+        float f[16];
+        float amax = 0.0f;
 #pragma unroll
-            for (int e = 0; e < kWords; ++e)
-                w[u][e] = vec < 2 * n_kv ? __ldcs(reinterpret_cast<const uint4*>(src) + e) : make_uint4(0u, 0u, 0u, 0u);
-        }
+        for (int e = 0; e < kPieces; ++e) {
+            const uint32_t x[4] = {next[e].x, next[e].y, next[e].z, next[e].w};
 #pragma unroll
-        for (int u = 0; u < RUN; ++u) {
-            const int vec = first + u * kPerWarp;
-            float f[8];
-            float amax = 0.0f;
-#pragma unroll
-            for (int e = 0; e < kWords; ++e) {
-                const uint32_t x[4] = {w[u][e].x, w[u][e].y, w[u][e].z, w[u][e].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (sizeof(X) == 2) {
-                        f[2 * j] = __uint_as_float(x[j] << 16);
-                        f[2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
-                    } else {
-                        f[4 * e + j] = __uint_as_float(x[j]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(f[j]));
-#pragma unroll
-            for (int m = kLanes / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
-            const float s = over_448(amax);
-            uint2 c = make_uint2(0u, 0u);
-            if (amax != 0.0f) {
-                // the quotients of bfloat16 rows as in append_fp8_bf16_rows
-                if (sizeof(X) == 2 && s >= 0x1p-90f && s <= 0x1p90f) {
-                    const float y = __frcp_rn(s);
-#pragma unroll
-                    for (int j = 0; j < 8; j += 2) divide_pair(f[j], f[j + 1], s, y);
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (sizeof(X) == 2) {
+                    f[8 * e + 2 * j] = __uint_as_float(x[j] << 16);
+                    f[8 * e + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
                 } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) f[j] = __fdiv_rn(f[j], s);
+                    f[4 * e + j] = __uint_as_float(x[j]);
                 }
-                c = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
             }
-            if (vec >= 2 * n_kv) continue;
-            const bool is_v = vec >= n_kv;
-            const int64_t at = (is_v ? vec - n_kv : vec) * a.c.n_rows + slot;
-            reinterpret_cast<uint2*>((is_v ? a.c.v : a.c.k) + at * D)[l] = c;
-            if (l == 0) (is_v ? a.c.v_scale : a.c.k_scale)[at] = s;
         }
+        fetch(i + n_warps);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(f[j]));
+#pragma unroll
+        for (int m = kLanes / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
+        if (at < 0) continue;                               // (its elements are anything)
+        const float s = over_448(amax);
+        uint32_t c[4] = {0u, 0u, 0u, 0u};
+        if (amax != 0.0f) {
+            // the quotients of bfloat16 rows as in append_fp8_bf16_rows
+            if (sizeof(X) == 2 && s >= 0x1p-90f && s <= 0x1p90f) {
+                const float y = __frcp_rn(s);
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) divide_pair(f[j], f[j + 1], s, y);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) f[j] = __fdiv_rn(f[j], s);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) c[j] = e4m3x4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+        }
+        uint8_t* const dst = (is_v ? a.c.v : a.c.k) + at * D;
+        if constexpr (sizeof(X) == 2) {
+            reinterpret_cast<uint2*>(dst)[l] = make_uint2(c[0], c[1]);
+            reinterpret_cast<uint2*>(dst)[kLanes + l] = make_uint2(c[2], c[3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) reinterpret_cast<uint32_t*>(dst)[e * kLanes + l] = c[e];
+        }
+        if (l == 0) (is_v ? a.c.v_scale : a.c.k_scale)[at] = s;
     }
 }
 
@@ -1637,16 +1646,12 @@ cudaError_t launch_append_kv8(const void* k, int64_t k_row, int64_t k_head, cons
                               bool bf16, int64_t rows, const int32_t* slot, const kvq_kv8_cache& c,
                               uint32_t* dev_status, cudaStream_t s)
 {
-    // vectors of a row that a warp takes at once: as many as the row has, up to four loads a lane
-    const int per = 256 / c.head_dim, vecs = 2 * c.n_kv, run = vecs >= 4 * per ? 4 : vecs >= 2 * per ? 2 : 1;
-    const AppendKv8Args a{k, v, k_row, k_head, v_row, v_head, rows, (vecs + run * per - 1) / (run * per),
-                          RowSlot{slot, c.n_rows, dev_status}, c};
-    const int64_t g = std::max<int64_t>(1, std::min<int64_t>((rows * a.units + kCodecWarps - 1) / kCodecWarps, (int64_t)sm_count() * 64));
-#define KVQ_RUNS(D, X) (run == 4 ? append_kv8_kernel<D, X, 4> : run == 2 ? append_kv8_kernel<D, X, 2> : append_kv8_kernel<D, X, 1>)
-#define KVQ_TYPES(D) (bf16 ? KVQ_RUNS(D, __nv_bfloat16) : KVQ_RUNS(D, float))
-    const auto kernel = c.head_dim == 64 ? KVQ_TYPES(64) : c.head_dim == 128 ? KVQ_TYPES(128) : KVQ_TYPES(256);
-#undef KVQ_TYPES
-#undef KVQ_RUNS
+    const int per = 512 / c.head_dim, vecs = 2 * c.n_kv;              // vectors of a row that a warp takes at once
+    const AppendKv8Args a{k, v, k_row, k_head, v_row, v_head, rows, (vecs + per - 1) / per, RowSlot{slot, c.n_rows, dev_status}, c};
+    const int64_t g = std::max<int64_t>(1, std::min<int64_t>((rows * a.units + kCodecWarps - 1) / kCodecWarps, (int64_t)sm_count() * 4));
+    const auto kernel = c.head_dim == 64    ? bf16 ? append_kv8_kernel<64, __nv_bfloat16> : append_kv8_kernel<64, float>
+                        : c.head_dim == 128 ? bf16 ? append_kv8_kernel<128, __nv_bfloat16> : append_kv8_kernel<128, float>
+                                            : bf16 ? append_kv8_kernel<256, __nv_bfloat16> : append_kv8_kernel<256, float>;
     return launch_dependent(kernel, dim3((unsigned)g), dim3(kCodecThreads), 0, s, a);
 }
 
