@@ -739,7 +739,7 @@ append_mla_kernel(const X* __restrict__ c_lat, int64_t ldx, const X* __restrict_
 // 512 / D of a row's 2 n_kv vectors (K's heads, then V's) at once, with the next ones on their way.
 // Bound by the rows' bytes, with the arithmetic not far behind (a division a vector and a correction a quotient, two
 // quotients at a time; what is done once a lane is shared by its 16 elements): 32768 rows of 8 heads of 128 take 64 us
-// with a row and a division for every vector, 52 with 8 elements a lane, APPEND_US so.
+// with a row and a division for every vector, 52 with 8 elements a lane, 43 so.
 // ------------------------------------------------------------------------------------
 struct AppendKv8Args {
     const void *k, *v;

@@ -53,7 +53,7 @@ def test_append_kv8_argument_errors(kvq):
 
 
 def kv8(kvq, c=None, **kw):
-    base = dict(n_seq=3, n_qh=32, max_seq_len=4096, window=0, seq_len=FAKE, block_table=FAKE, max_pages=64, page_size=64,
+    base = dict(n_seq=3, n_qh=32, max_seq_len=65536, window=0, seq_len=FAKE, block_table=FAKE, max_pages=64, page_size=64,
                 seq_stride_rows=0, cache=c or cache(kvq), q=FAKE, ldq=4096, sm_scale=0.1)
     return fill(kvq.Kv8Problem(), base, kw)
 
@@ -78,6 +78,7 @@ def test_kv8_decode_argument_errors(kvq):
     assert call() == 5 and call(ws=FAKE, n=need - 1) == 5 and call(ws=FAKE + 128, n=need) == 4
     assert call(n_seq=0, seq_len=None, q=None, out=None) == 0
     assert L.kvq_kv8_decode_workspace(C.byref(kv8(kvq, n_seq=0))) == 0
+    assert L.kvq_kv8_decode_workspace(C.byref(kv8(kvq, max_seq_len=1024))) == 0        # short units need none
     assert L.kvq_kv8_decode_workspace(C.byref(kv8(kvq, n_qh=30))) == 0
 
 
