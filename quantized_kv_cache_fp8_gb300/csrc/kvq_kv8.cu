@@ -972,7 +972,7 @@ auto of_kind(const kvq_kv8_problem& p, F f)
     const bool two = p.n_qh / p.cache.n_kv > kHeads;
     switch (p.cache.head_dim) {
         case 64: return two ? f(Kv8Kind<64, 2, 32, 4, 3>()) : f(Kv8Kind<64, 1, 32, 4, 4>());
-        case 128: return two ? f(Kv8Kind<128, 2, 16, 4, 2>()) : f(Kv8Kind<128, 1, 32, 4, 3>());
+        case 128: return two ? f(Kv8Kind<128, 2, 32, 4, 2>()) : f(Kv8Kind<128, 1, 32, 4, 3>());
         default: return f(Kv8Kind<256, 1, 16, 4, 2>());
     }
 }
