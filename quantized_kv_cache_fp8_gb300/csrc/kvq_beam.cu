@@ -228,9 +228,27 @@ __device__ __forceinline__ float exp_sum(const V& v, float c)
     return a + b;
 }
 
-// NV vectors a thread.  Vectors begin at multiples of 16 bytes: `lead` elements of the first lie ahead of the row.
+// 16 bytes from byte `lead` of a on, which b continues
+template <typename V>
+__device__ __forceinline__ V shifted(const V& a, const uint32_t (&b)[4], int lead)
+{
+    const bool two = lead & 8, one = lead & 4;
+    uint32_t c[6], d[5];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) c[i] = two ? (i < 2 ? a.w[i + 2] : b[i - 2 < 4 ? i - 2 : 3]) : i < 4 ? a.w[i] : b[i - 4];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) d[i] = one ? c[i + 1] : c[i];
+    V r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.w[i] = __funnelshift_r(d[i], d[i + 1], (lead & 3) * 8);
+    return r;
+}
+
+// NV vectors of 16 bytes a thread, counted from the row's beginning wherever that lies, so that equal rows have equal
+// sums to the last bit.  ODD: of a row that does not begin at a multiple of 16 bytes the pieces that do are loaded, and
+// a vector put together from a lane's piece and the next lane's.
 // The CTAs go over the rows' chunks in turn; a next chunk's vectors are on their way while this one's best are ranked.
-template <typename X, int NV>
+template <typename X, int NV, bool ODD>
 __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs a)
 {
     using V = Vec<X>;
@@ -250,8 +268,12 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
     const int k = p.n_out;
     const int rows = p.n_req * p.n_beam;
 
-    // the chunk at hand, chunk `chunk` of row `row`: elements c0 + (j * kThreads + tid) * kE .. are vector j of thread tid
+    // the chunk at hand, chunk `chunk` of row `row`: element c0 + at_of(j) begins vector j of a thread, which lies `lead`
+    // bytes behind x[j] where lead is not 0 (then `after` is lane 0's piece behind the warp's last)
     V x[NV];
+    uint32_t after[4];
+    int lead = 0;
+    auto at_of = [&](int j) { return (ODD ? (warp * NV + j) * 32 + lane : j * kThreads + tid) * kE; };
     int row = blockIdx.x / a.n_chunk, chunk = blockIdx.x - row * a.n_chunk;
     const int row_step = gridDim.x / a.n_chunk, chunk_step = gridDim.x - row_step * a.n_chunk;
     const X* src = nullptr;
@@ -269,167 +291,179 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
         while (row < rows && !reads_logits(p, row)) advance();
         if (row >= rows) return;
         src = static_cast<const X*>(p.logits) + (int64_t)row * p.ld;
-        const int lead = (int)((uintptr_t)src % 16 / sizeof(X));
-        c0 = chunk * kChunk - lead;
-        if (c0 >= 0 && c0 + kChunk <= p.vocab) {
-            const uint4* from = reinterpret_cast<const uint4*>(src + c0) + tid;
+        if constexpr (ODD) lead = (int)((uintptr_t)src % 16);
+        c0 = chunk * kChunk;
+        const uint4* const from = reinterpret_cast<const uint4*>(reinterpret_cast<const uint8_t*>(src) - lead);
+        auto take = [](uint32_t (&w)[4], const uint4* q) {
+            const uint4 v = __ldcs(q);
+            w[0] = v.x;
+            w[1] = v.y;
+            w[2] = v.z;
+            w[3] = v.w;
+        };
+        if (c0 + kChunk <= p.vocab && lead == 0) {
 #pragma unroll
-            for (int j = 0; j < NV; ++j) {
-                const uint4 w = __ldcs(from + j * kThreads);
-                x[j].w[0] = w.x;
-                x[j].w[1] = w.y;
-                x[j].w[2] = w.z;
-                x[j].w[3] = w.w;
-            }
+            for (int j = 0; j < NV; ++j) take(x[j].w, from + (c0 + at_of(j)) / kE);
             return;
         }
+        // (pieces that lie in the row as a whole)
+        auto inside = [&](int piece) { return (piece > 0 || lead == 0) && (piece + 1) * kE - lead / (int)sizeof(X) <= p.vocab; };
 #pragma unroll
         for (int j = 0; j < NV; ++j) {
-            const int at = c0 + (j * kThreads + tid) * kE;
-            if (at >= 0 && at + kE <= p.vocab) {
-                const uint4 w = __ldcs(reinterpret_cast<const uint4*>(src + at));
-                x[j].w[0] = w.x;
-                x[j].w[1] = w.y;
-                x[j].w[2] = w.z;
-                x[j].w[3] = w.w;
-            } else {
-                x[j].fill(src, at, p.vocab);
-            }
+            const int piece = (c0 + at_of(j)) / kE;
+            if (inside(piece)) take(x[j].w, from + piece);
+            else if (lead == 0) x[j].fill(src, c0 + at_of(j), p.vocab);
+        }
+        const int behind = (c0 + at_of(NV - 1)) / kE + 32;
+        if (ODD && lead != 0 && lane == 0 && inside(behind)) take(after, from + behind);
+    };
+    auto put_together = [&](const X* row_at, int from) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+            uint32_t next[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                next[i] = __shfl_sync(kFull, lane > 0 ? x[j].w[i] : j + 1 < NV ? x[j + 1 < NV ? j + 1 : j].w[i] : after[i], (lane + 1) & 31);
+            // (whole, and of pieces that are)
+            const int at = from + at_of(j);
+            if (at > 0 && at + 2 * kE - lead / (int)sizeof(X) <= p.vocab) x[j] = shifted(x[j], next, lead);
+            else x[j].fill(row_at, at, p.vocab);
         }
     };
     if (tid == 0) s_count[0] = make_int2(0, 0);
     fetch();
     for (int turn = 0; row < rows; turn ^= 1) {
-    const X* const this_src = src;
-    const int this_c0 = c0;
-    const int64_t this_at = (int64_t)row * a.n_chunk + chunk;
-    float most[NV], mine = -INFINITY;
+        const X* const this_src = src;
+        const int this_c0 = c0;
+        const int64_t this_at = (int64_t)row * a.n_chunk + chunk;
+        if (ODD && lead != 0) put_together(src, c0);
+        float most[NV], mine = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < NV; ++j) {
-        most[j] = x[j].largest();
-        mine = fmaxf(mine, most[j]);
-    }
-    const uint32_t my_key = mine > -INFINITY ? ordered(mine) : 0u;
-    const uint32_t wm = __reduce_max_sync(kFull, my_key);
-    put_floor(my_key, k, s_floor);
+        for (int j = 0; j < NV; ++j) {
+            most[j] = x[j].largest();
+            mine = fmaxf(mine, most[j]);
+        }
+        const uint32_t my_key = mine > -INFINITY ? ordered(mine) : 0u;
+        const uint32_t wm = __reduce_max_sync(kFull, my_key);
+        put_floor(my_key, k, s_floor);
 
-    // exp(y - m), m the warp's largest, as 2^(y l - c), one fused multiply-add: l = log2 e in fp32, c = m l rounded.
-    // What the rounding of c took is the same factor for all and is put back below.
-    const float m = wm ? unordered(wm) : -INFINITY;
-    float sum = 0.0f, low = 0.0f;
-    if (fabsf(m) < kLarge) {
-        const float c = __fmul_rn(m, kLog2e);
+        // exp(y - m), m the warp's largest, as 2^(y l - c), one fused multiply-add: l = log2 e in fp32, c = m l rounded.
+        // What the rounding of c took is the same factor for all and is put back below.
+        const float m = wm ? unordered(wm) : -INFINITY;
+        float sum = 0.0f, low = 0.0f;
+        if (fabsf(m) < kLarge) {
+            const float c = __fmul_rn(m, kLog2e);
 #pragma unroll
-        for (int j = 0; j < NV; j += 2) add_exact(sum, low, exp_sum(x[j], c) + exp_sum(x[j + 1], c));
-    } else {
-#pragma unroll
-        for (int j = 0; j < NV; ++j)
-#pragma unroll 1
-            for (int e = 0; e < kE; ++e) {
-                const uint32_t w = sizeof(X) == 2 ? e / 2 : e;
-                const uint32_t b = w == 0 ? x[j].w[0] : w == 1 ? x[j].w[1] : w == 2 ? x[j].w[2] : x[j].w[3];
-                const float y = __uint_as_float(sizeof(X) == 4 ? b : e % 2 ? b & 0xFFFF0000u : b << 16);
-                // m l may not be finite; without a maximum there is nothing, or a NaN
-                sum += m != -INFINITY ? ex2((y - m) * kLog2e) : y == -INFINITY ? 0.0f : y;
-            }
-    }
-    warp_sum(sum, low);
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_sum[warp] = make_float2(sum, low);
-    }
-    __syncthreads();
-
-    make_floor(k, s_floor);
-    if (warp == kWarps - 1) {                               // the chunk's sum, a warp's a lane
-        const float mw = lane < kWarps ? s_m[lane] : -INFINITY;
-        float2 sw = lane < kWarps ? s_sum[lane] : make_float2(0.0f, 0.0f);
-        float all = mw;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, o));
-        // The rounding of c in nats is exact as a fused multiply-add but for its last factor.  Its exponential is its
-        // series (to 2^-32) but for logits beyond 2^13.
-        const float off = fabsf(mw) < kLarge ? -0.6931471805599453f * fmaf(mw, kLog2e, -__fmul_rn(mw, kLog2e)) : 0.0f;
-        if (fabsf(off) < 0x1p-10f) {
-            sw.y = fmaf(sw.x, off * fmaf(0.5f, off, 1.0f), sw.y);
+            for (int j = 0; j < NV; j += 2) add_exact(sum, low, exp_sum(x[j], c) + exp_sum(x[j + 1], c));
         } else {
-            const float f = expf(off);
-            sw = make_float2(sw.x * f, sw.y * f);
-        }
-        float t = 0.0f, lo = 0.0f;
-        // (a sum of 0 has no maximum; that of the maximum's warp stays as it is)
-        if (sw.x != 0.0f) add_scaled(t, lo, sw, mw == all ? 1.0f : expf(mw - all));
-        warp_sum(t, lo);
-        if (lane == 0) {
-            a.part_m[this_at] = all;
-            a.part_s[this_at] = make_float2(t, lo);
-        }
-    }
-    __syncthreads();
-
-    // vectors with something at or above the floor (few): their elements are looked at together, further down
-    const uint32_t floor_key = s_floor[0];
-    const float least = floor_key ? unordered(floor_key) : -0x1.fffffep127f;       // (all but -inf)
-    if (mine >= least) {
 #pragma unroll
-        for (int j = 0; j < NV; ++j)
-            if (most[j] >= least) {
-                const int i = atomicAdd(&s_count[turn].x, 1);
-                if (i < kVectors) {
-                    s_vec[i] = x[j];
-                    s_at[i] = this_c0 + (j * kThreads + tid) * kE;
+            for (int j = 0; j < NV; ++j)
+#pragma unroll 1
+                for (int e = 0; e < kE; ++e) {
+                    const uint32_t w = sizeof(X) == 2 ? e / 2 : e;
+                    const uint32_t b = w == 0 ? x[j].w[0] : w == 1 ? x[j].w[1] : w == 2 ? x[j].w[2] : x[j].w[3];
+                    const float y = __uint_as_float(sizeof(X) == 4 ? b : e % 2 ? b & 0xFFFF0000u : b << 16);
+                    // m l may not be finite; without a maximum there is nothing, or a NaN
+                    sum += m != -INFINITY ? ex2((y - m) * kLog2e) : y == -INFINITY ? 0.0f : y;
+                }
+        }
+        warp_sum(sum, low);
+        if (lane == 0) {
+            s_m[warp] = m;
+            s_sum[warp] = make_float2(sum, low);
+        }
+        __syncthreads();
+
+        make_floor(k, s_floor);
+        if (warp == kWarps - 1) {                               // the chunk's sum, a warp's a lane
+            const float mw = lane < kWarps ? s_m[lane] : -INFINITY;
+            float2 sw = lane < kWarps ? s_sum[lane] : make_float2(0.0f, 0.0f);
+            float all = mw;
+#pragma unroll
+            for (int o = 16; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, o));
+            // The rounding of c in nats is exact as a fused multiply-add but for its last factor.  Its exponential is its
+            // series (to 2^-32) but for logits beyond 2^13.
+            const float off = fabsf(mw) < kLarge ? -0.6931471805599453f * fmaf(mw, kLog2e, -__fmul_rn(mw, kLog2e)) : 0.0f;
+            if (fabsf(off) < 0x1p-10f) {
+                sw.y = fmaf(sw.x, off * fmaf(0.5f, off, 1.0f), sw.y);
+            } else {
+                const float f = expf(off);
+                sw = make_float2(sw.x * f, sw.y * f);
+            }
+            float t = 0.0f, lo = 0.0f;
+            // (a sum of 0 has no maximum; that of the maximum's warp stays as it is)
+            if (sw.x != 0.0f) add_scaled(t, lo, sw, mw == all ? 1.0f : expf(mw - all));
+            warp_sum(t, lo);
+            if (lane == 0) {
+                a.part_m[this_at] = all;
+                a.part_s[this_at] = make_float2(t, lo);
+            }
+        }
+        __syncthreads();
+
+        // vectors with something at or above the floor (few): their elements are looked at together, further down
+        const uint32_t floor_key = s_floor[0];
+        const float least = floor_key ? unordered(floor_key) : -0x1.fffffep127f;       // (all but -inf)
+        if (mine >= least) {
+#pragma unroll
+            for (int j = 0; j < NV; ++j)
+                if (most[j] >= least) {
+                    const int i = atomicAdd(&s_count[turn].x, 1);
+                    if (i < kVectors) {
+                        s_vec[i] = x[j];
+                        s_at[i] = this_c0 + at_of(j);
+                    }
+                }
+        }
+        if (tid == 0) s_count[turn ^ 1] = make_int2(0, 0);      // (nobody counts for the next chunk yet)
+        advance();
+        fetch();
+        __syncthreads();
+        const int vecs = s_count[turn].x;
+        for (int i = tid; i < min(vecs, kVectors) * kE; i += kThreads) {
+            const float y = s_vec[i / kE].get(i % kE);
+            if (y >= least) {
+                const int at = atomicAdd(&s_count[turn].y, 1);
+                if (at < kBuffer) s_key[at] = (uint64_t)ordered(y) << 32 | (uint32_t)~(s_at[i / kE] + i % kE);
+            }
+        }
+        __syncthreads();
+        const int n = s_count[turn].y;
+        uint64_t* out = a.part_key + this_at * k;
+        if (vecs <= kVectors && n <= kBuffer) {
+            for (int i = warp; i < n; i += kWarps) {            // a warp counts what is above
+                const uint64_t key = s_key[i];
+                int rank = 0;
+                for (int j = 0; j < n; j += 32) rank += __popc(__ballot_sync(kFull, j + lane < n && s_key[min(j + lane, n - 1)] > key));
+                if (rank < k && lane == 0) out[rank] = key;
+            }
+            for (int i = n + tid; i < k; i += kThreads) out[i] = 0;
+            continue;
+        }
+        // too many equal values: the best one by one, of a thread's elements read again
+        uint64_t last = ~0ull, best = 0;
+        bool stale = true;
+        for (int i = 0; i < k; ++i) {
+            if (stale) {
+                best = 0;
+                for (int t = this_c0 + tid; t < min(this_c0 + kChunk, p.vocab); t += kThreads) {
+                    const float y = V::load(this_src + t);
+                    const uint64_t key = y > -INFINITY ? (uint64_t)ordered(y) << 32 | (uint32_t)~t : 0;
+                    if (key < last && key > best) best = key;
                 }
             }
-    }
-    if (tid == 0) s_count[turn ^ 1] = make_int2(0, 0);      // (nobody counts for the next chunk yet)
-    advance();
-    fetch();
-    __syncthreads();
-    const int vecs = s_count[turn].x;
-    for (int i = tid; i < min(vecs, kVectors) * kE; i += kThreads) {
-        const float y = s_vec[i / kE].get(i % kE);
-        if (y >= least) {
-            const int at = atomicAdd(&s_count[turn].y, 1);
-            if (at < kBuffer) s_key[at] = (uint64_t)ordered(y) << 32 | (uint32_t)~(s_at[i / kE] + i % kE);
-        }
-    }
-    __syncthreads();
-    const int n = s_count[turn].y;
-    uint64_t* out = a.part_key + this_at * k;
-    if (vecs <= kVectors && n <= kBuffer) {
-        for (int i = warp; i < n; i += kWarps) {            // a warp counts what is above
-            const uint64_t key = s_key[i];
-            int rank = 0;
-            for (int j = 0; j < n; j += 32) rank += __popc(__ballot_sync(kFull, j + lane < n && s_key[min(j + lane, n - 1)] > key));
-            if (rank < k && lane == 0) out[rank] = key;
-        }
-        for (int i = n + tid; i < k; i += kThreads) out[i] = 0;
-        continue;
-    }
-    // too many equal values: the best one by one, of a thread's elements read again
-    uint64_t last = ~0ull, best = 0;
-    bool stale = true;
-    for (int i = 0; i < k; ++i) {
-        if (stale) {
-            best = 0;
-            for (int t = max(this_c0, 0) + tid; t < min(this_c0 + kChunk, p.vocab); t += kThreads) {
-                const float y = V::load(this_src + t);
-                const uint64_t key = y > -INFINITY ? (uint64_t)ordered(y) << 32 | (uint32_t)~t : 0;
-                if (key < last && key > best) best = key;
-            }
-        }
-        uint64_t b = best;
+            uint64_t b = best;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) b = max(b, (uint64_t)__shfl_xor_sync(kFull, (unsigned long long)b, o));
-        __syncthreads();
-        if (lane == 0) s_best[warp] = b;
-        __syncthreads();
+            for (int o = 16; o >= 1; o >>= 1) b = max(b, (uint64_t)__shfl_xor_sync(kFull, (unsigned long long)b, o));
+            __syncthreads();
+            if (lane == 0) s_best[warp] = b;
+            __syncthreads();
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) b = max(b, s_best[w]);
-        if (tid == 0) out[i] = b;
-        last = b;
-        stale = best == b;
-    }
+            for (int w = 0; w < kWarps; ++w) b = max(b, s_best[w]);
+            if (tid == 0) out[i] = b;
+            last = b;
+            stale = best == b;
+        }
     }
 }
 
@@ -625,7 +659,7 @@ BeamPlan plan_beam(const kvq_beam_problem& p)
     const int64_t rows = (int64_t)p.n_req * p.n_beam;
     const int e = p.x_type == KVQ_WEIGHT_BF16 ? 8 : 4;
     // large chunks where they fill the GPU, else small ones
-    const auto chunks = [&](int nv) { return ((int64_t)p.vocab + e - 1 + kThreads * nv * e - 1) / (kThreads * nv * e); };
+    const auto chunks = [&](int nv) { return ((int64_t)p.vocab + kThreads * nv * e - 1) / (kThreads * nv * e); };
     q.nv = rows * chunks(8) >= 2 * (int64_t)sm_count() ? 8 : 2;
     q.n_chunk = (int)chunks(q.nv);
     const size_t n = (size_t)rows * q.n_chunk;
@@ -664,7 +698,10 @@ cudaError_t launch_chunks(const BeamArgs& a, int nv, cudaStream_t s)
     const int64_t items = (int64_t)a.p.n_req * a.p.n_beam * a.n_chunk;
     // (a CTA a chunk up to many: the finished beams' make the work uneven, and the GPU levels it)
     const unsigned grid = (unsigned)std::min<int64_t>(items, 64 * (int64_t)sm_count());
-    return launch_dependent(nv == 8 ? beam_chunk_kernel<X, 8> : beam_chunk_kernel<X, 2>, dim3(grid), dim3(kThreads), 0, s, a);
+    const bool odd = !aligned(a.p.logits, 16) || a.p.ld * (int64_t)sizeof(X) % 16 != 0;
+    const auto kernel = nv == 8 ? odd ? beam_chunk_kernel<X, 8, true> : beam_chunk_kernel<X, 8, false>
+                                : odd ? beam_chunk_kernel<X, 2, true> : beam_chunk_kernel<X, 2, false>;
+    return launch_dependent(kernel, dim3(grid), dim3(kThreads), 0, s, a);
 }
 
 }  // namespace

@@ -11,8 +11,10 @@
 //                                                                   rows zipped before they widen
 // The k index of a contraction may be permuted freely if both operands are, and so may m: a lane's fragments
 // are whole 16-byte pieces of a row (dims 64 c + 16 t .. of K rows g, g + 8; dims 16 g .. of V rows
-// 2 t, 2 t + 1, 2 t + 8, 2 t + 9, with g = lane / 4, t = lane % 4).  Each lane copies the pieces that it
-// reads itself with cp.async into a ring that only its warp uses: no barrier, no swizzle, no bank conflict.
+// 2 t, 2 t + 1, 2 t + 8, 2 t + 9, with g = lane / 4, t = lane % 4).  Each lane loads the pieces that it reads itself
+// straight into registers, the next tile's as soon as this one's are used: 8 KB in flight a warp, 12 warps an SM, no
+// shared memory and no barrier in the loop.  (A ring in shared memory filled by cp.async cost its reads and
+// the queue in front of them: 131072 rows, 8 KV heads x 8, 73 us against 53.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -148,11 +150,11 @@ __device__ __forceinline__ int2 seen_rows(const kvq_kv8_problem& p, int s)
 // a unit's rows begin at a multiple of 16: the last at or ahead of the first row that is seen
 __host__ __device__ constexpr int first_group(int x) { return x & ~(kGroup - 1); }
 
-// The line.  A unit (a sequence and KV head) takes a place for every STEP rows and, where there are more places
-// than CTAs, kIdle places for what it costs to begin one; units follow one another, the KV heads of a sequence side by side.  CTA c of n has total / n
-// places, the first total % n one more: the same work for all, whatever the lengths, and a partial result only where a
-// cut falls into a unit (64 ragged sequences, 512 to 32768 rows: 198 us with splits of one size, which pay for their
-// beginnings, 186 us on the line).
+// The line.  A unit (a sequence and KV head) takes a place for every STEP rows and, where there are more places than
+// CTAs, kIdle places for what it costs to begin one; units follow one another, the KV heads of a sequence side by
+// side.  CTA c of n has total / n places, the first total % n one more: the same work for all, whatever the lengths,
+// and a partial result only where a cut falls into a unit (64 ragged sequences, 512 to 32768 rows: 198 us with splits
+// of one size, which pay for their beginnings, 186 us on the line).
 template <int STEP>
 __device__ __forceinline__ int unit_steps(const int2& seen) { return (seen.y - first_group(seen.x) + STEP - 1) / STEP; }
 template <int STEP>
@@ -468,138 +470,109 @@ kv8_decode_kernel(const Kv8Args a)
     }
     if (more) begin();
     while (more) {
-    const int64_t head0 = (int64_t)s * p.n_qh + kv * a.group + hb * Sh::kHb;
-    const int this_part = part;
-    // Queries as the score's B operand.  bf16 has fp32's range, so a head is scaled by a power of two that puts
-    // its largest element into [2^14, 2^15): elements down to 2^-31 of it are exact, the rest within 2^-39 of it.
-    uint32_t qf[NB][kBlocks][2];
-    float hs[NB][2];                                        // what a score of heads 2 t, 2 t + 1 is multiplied by
+        const int64_t head0 = (int64_t)s * p.n_qh + kv * a.group + hb * Sh::kHb;
+        const int this_part = part;
+        // Queries as the score's B operand.  bf16 has fp32's range, so a head is scaled by a power of two that puts
+        // its largest element into [2^14, 2^15): elements down to 2^-31 of it are exact, the rest within 2^-39 of it.
+        uint32_t qf[NB][kBlocks][2];
+        float hs[NB][2];                                        // what a score of heads 2 t, 2 t + 1 is multiplied by
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        const int h = nb * kHeads + g;
-        uint4 w[kP][2];
+        for (int nb = 0; nb < NB; ++nb) {
+            const int h = nb * kHeads + g;
+            uint4 w[kP][2];
 #pragma unroll
-        for (int c = 0; c < kP; ++c) {
-            const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + s * p.ldq +
-                                                              ((int64_t)kv * a.group + hb * Sh::kHb + h) * D + 64 * c + 16 * t);
+            for (int c = 0; c < kP; ++c) {
+                const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + s * p.ldq +
+                                                                  ((int64_t)kv * a.group + hb * Sh::kHb + h) * D + 64 * c + 16 * t);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) w[c][e] = h < heads ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        uint32_t m = 0;                                     // |bfloat16| patterns order like their values
-#pragma unroll
-        for (int c = 0; c < kP; ++c)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t x[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
-#pragma unroll
-                for (int j = 0; j < 4; ++j) m = max(m, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
+                for (int e = 0; e < 2; ++e) w[c][e] = h < heads ? __ldg(src + e) : make_uint4(0u, 0u, 0u, 0u);
             }
-        m = max(m, __shfl_xor_sync(kFull, m, 1));
-        m = max(m, __shfl_xor_sync(kFull, m, 2));
-        // 14 - exponent; no head is scaled up by more than 2^100 (a largest element below 2^-86: not exact)
-        const int up = min(14 - ((int)(m >> 7) - 127), 100);
-        const float f = pow2(up);
+            uint32_t m = 0;                                     // |bfloat16| patterns order like their values
 #pragma unroll
-        for (int c = 0; c < kP; ++c)
+            for (int c = 0; c < kP; ++c)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const uint32_t x[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t x[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    qf[nb][4 * c + 2 * e + (j >> 1)][j & 1] =
-                        pack_h2(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xFFFF0000u) * f);
-            }
-        const float back = pow2(-up) * (p.sm_scale * kLog2e);
-        hs[nb][0] = __shfl_sync(kFull, back, 8 * t);
-        hs[nb][1] = __shfl_sync(kFull, back, 8 * t + 4);
-    }
-
-    float o[NB][kBlocks][4];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[nb][b][e] = 0.0f;
-    // Two references a head, in log2: ref of the scores, for the sum of exp2(x - ref), and wref of x +
-    // log2(vscale), for the weights that multiply V's codes, so that the largest of those is near 1 whatever the
-    // scales.  They move only when something passes them by kSlack (top, wtop: the level that makes them).
-    float ref[NB][2], wref[NB][2], top[NB][2], wtop[NB][2], sum[NB][2];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            ref[nb][e] = wref[nb][e] = sum[nb][e] = 0.0f;
-            top[nb][e] = wtop[nb][e] = -INFINITY;
-        }
-
-    for (int i = 0; i < my_tiles; ++i) {
-        const int after = i + 2 < my_tiles ? look_up(i + 2) : -1;
-        // rows 16 j + g (0, 1) and 16 j + g + 8 (2, 3), heads 2 t, 2 t + 1
-        float x[kGroups][NB][4];
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) x[j][nb][e] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < kP; ++c)
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    const uint4 &l = kr[2 * j][c], &u = kr[2 * j + 1][c];
-                    const uint32_t wl = k == 0 ? l.x : k == 1 ? l.y : k == 2 ? l.z : l.w;
-                    const uint32_t wu = k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
-                    const uint32_t a0 = wide_lo(wl), a1 = wide_lo(wu), a2 = wide_hi(wl), a3 = wide_hi(wu);
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                        mma16816(x[j][nb], a0, a1, a2, a3, qf[nb][4 * c + k][0], qf[nb][4 * c + k][1]);
+                    for (int j = 0; j < 4; ++j) m = max(m, max(x[j] & 0x7FFFu, (x[j] >> 16) & 0x7FFFu));
                 }
-        float kf[kGroups][2], lv[kGroups][2];
-        const float my_lv = lg2(v_scale);
+            m = max(m, __shfl_xor_sync(kFull, m, 1));
+            m = max(m, __shfl_xor_sync(kFull, m, 2));
+            // 14 - exponent; no head is scaled up by more than 2^100 (a largest element below 2^-86: not exact)
+            const int up = min(14 - ((int)(m >> 7) - 127), 100);
+            const float f = pow2(up);
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j)
+            for (int c = 0; c < kP; ++c)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                kf[j][e] = __shfl_sync(kFull, k_scale, 16 * j + 8 * e + g);
-                lv[j][e] = __shfl_sync(kFull, my_lv, 16 * j + 8 * e + g);
-            }
-        const uint32_t now = mask;
-        if (i + 1 < my_tiles) load_k(i + 1, next);
-        bool over = false;
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t x[4] = {w[c][e].x, w[c][e].y, w[c][e].z, w[c][e].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        qf[nb][4 * c + 2 * e + (j >> 1)][j & 1] =
+                            pack_h2(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xFFFF0000u) * f);
+                }
+            const float back = pow2(-up) * (p.sm_scale * kLog2e);
+            hs[nb][0] = __shfl_sync(kFull, back, 8 * t);
+            hs[nb][1] = __shfl_sync(kFull, back, 8 * t + 4);
+        }
+
+        float o[NB][kBlocks][4];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[nb][b][e] = 0.0f;
+        // Two references a head, in log2: ref of the scores, for the sum of exp2(x - ref), and wref of x +
+        // log2(vscale), for the weights that multiply V's codes, so that the largest of those is near 1 whatever the
+        // scales.  They move only when something passes them by kSlack (top, wtop: the level that makes them).
+        float ref[NB][2], wref[NB][2], top[NB][2], wtop[NB][2], sum[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float m = -INFINITY, mw = -INFINITY;
+                ref[nb][e] = wref[nb][e] = sum[nb][e] = 0.0f;
+                top[nb][e] = wtop[nb][e] = -INFINITY;
+            }
+
+        for (int i = 0; i < my_tiles; ++i) {
+            const int after = i + 2 < my_tiles ? look_up(i + 2) : -1;
+            // rows 16 j + g (0, 1) and 16 j + g + 8 (2, 3), heads 2 t, 2 t + 1
+            float x[kGroups][NB][4];
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j)
+            for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        float& y = x[j][nb][2 * h + e];
-                        y = y * kf[j][h] * hs[nb][e];
-                        m = fmaxf(m, y);
-                        mw = fmaxf(mw, y + lv[j][h]);
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[j][nb][e] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < kP; ++c)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+#pragma unroll
+                    for (int j = 0; j < kGroups; ++j) {
+                        const uint4 &l = kr[2 * j][c], &u = kr[2 * j + 1][c];
+                        const uint32_t wl = k == 0 ? l.x : k == 1 ? l.y : k == 2 ? l.z : l.w;
+                        const uint32_t wu = k == 0 ? u.x : k == 1 ? u.y : k == 2 ? u.z : u.w;
+                        const uint32_t a0 = wide_lo(wl), a1 = wide_lo(wu), a2 = wide_hi(wl), a3 = wide_hi(wu);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+                            mma16816(x[j][nb], a0, a1, a2, a3, qf[nb][4 * c + k][0], qf[nb][4 * c + k][1]);
                     }
-                over |= m > top[nb][e] || mw > wtop[nb][e];
-            }
-        const bool some = now != ~0u;
-        if (__any_sync(kFull, over) || some) {              // (rare after the first tile)
-            if (some) {
+            float kf[kGroups][2], lv[kGroups][2];
+            const float my_lv = lg2(v_scale);
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j)
+            for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        if (!(now >> (16 * j + 8 * h + g) & 1)) {
-                            lv[j][h] = 0.0f;
+                for (int e = 0; e < 2; ++e) {
+                    kf[j][e] = __shfl_sync(kFull, k_scale, 16 * j + 8 * e + g);
+                    lv[j][e] = __shfl_sync(kFull, my_lv, 16 * j + 8 * e + g);
+                }
+            const uint32_t now = mask;
+            if (i + 1 < my_tiles) load_k(i + 1, next);
+            bool over = false;
 #pragma unroll
-                            for (int nb = 0; nb < NB; ++nb) x[j][nb][2 * h] = x[j][nb][2 * h + 1] = -INFINITY;
-                        }
-            }
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) {
+            for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     float m = -INFINITY, mw = -INFINITY;
@@ -607,130 +580,159 @@ kv8_decode_kernel(const Kv8Args a)
                     for (int j = 0; j < kGroups; ++j)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            m = fmaxf(m, x[j][nb][2 * h + e]);
-                            mw = fmaxf(mw, x[j][nb][2 * h + e] + lv[j][h]);
+                            float& y = x[j][nb][2 * h + e];
+                            y = y * kf[j][h] * hs[nb][e];
+                            m = fmaxf(m, y);
+                            mw = fmaxf(mw, y + lv[j][h]);
                         }
+                    over |= m > top[nb][e] || mw > wtop[nb][e];
+                }
+            const bool some = now != ~0u;
+            if (__any_sync(kFull, over) || some) {              // (rare after the first tile)
+                if (some) {
 #pragma unroll
-                    for (int d = 4; d < 32; d <<= 1) {
-                        m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-                        mw = fmaxf(mw, __shfl_xor_sync(kFull, mw, d));
-                    }
-                    if (m > top[nb][e] - kSlack) {          // (top is -inf, or the reference and kSlack)
-                        const float f = top[nb][e] == -INFINITY ? 0.0f : ex2(ref[nb][e] - m);
-                        sum[nb][e] *= f;
-                        ref[nb][e] = m;
-                        top[nb][e] = m + kSlack;
-                    }
-                    if (mw > wtop[nb][e] - kSlack) {
-                        const float f = wtop[nb][e] == -INFINITY ? 0.0f : ex2(wref[nb][e] - mw);
+                    for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-                        for (int b = 0; b < kBlocks; ++b) {
-                            o[nb][b][e] *= f;
-                            o[nb][b][e + 2] *= f;
+                        for (int h = 0; h < 2; ++h)
+                            if (!(now >> (16 * j + 8 * h + g) & 1)) {
+                                lv[j][h] = 0.0f;
+#pragma unroll
+                                for (int nb = 0; nb < NB; ++nb) x[j][nb][2 * h] = x[j][nb][2 * h + 1] = -INFINITY;
+                            }
+                }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float m = -INFINITY, mw = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                m = fmaxf(m, x[j][nb][2 * h + e]);
+                                mw = fmaxf(mw, x[j][nb][2 * h + e] + lv[j][h]);
+                            }
+#pragma unroll
+                        for (int d = 4; d < 32; d <<= 1) {
+                            m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
+                            mw = fmaxf(mw, __shfl_xor_sync(kFull, mw, d));
                         }
-                        wref[nb][e] = mw;
-                        wtop[nb][e] = mw + kSlack;
+                        if (m > top[nb][e] - kSlack) {          // (top is -inf, or the reference and kSlack)
+                            const float f = top[nb][e] == -INFINITY ? 0.0f : ex2(ref[nb][e] - m);
+                            sum[nb][e] *= f;
+                            ref[nb][e] = m;
+                            top[nb][e] = m + kSlack;
+                        }
+                        if (mw > wtop[nb][e] - kSlack) {
+                            const float f = wtop[nb][e] == -INFINITY ? 0.0f : ex2(wref[nb][e] - mw);
+#pragma unroll
+                            for (int b = 0; b < kBlocks; ++b) {
+                                o[nb][b][e] *= f;
+                                o[nb][b][e + 2] *= f;
+                            }
+                            wref[nb][e] = mw;
+                            wtop[nb][e] = mw + kSlack;
+                        }
                     }
                 }
             }
-        }
-        uint32_t w[kGroups][NB][2];
+            uint32_t w[kGroups][NB][2];
 #pragma unroll
-        for (int j = 0; j < kGroups; ++j)
+            for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float x0 = x[j][nb][2 * h], x1 = x[j][nb][2 * h + 1];
-                    sum[nb][0] += ex2(x0 - ref[nb][0]);
-                    sum[nb][1] += ex2(x1 - ref[nb][1]);
-                    w[j][nb][h] = transpose8(pack_h2(ex2(x0 + lv[j][h] - wref[nb][0]), ex2(x1 + lv[j][h] - wref[nb][1])));
-                }
-        // context: block b of a lane is its dims 2 b and 2 b + 1 of the pieces
-#pragma unroll
-        for (int j = 0; j < kGroups; ++j)
-#pragma unroll
-            for (int c = 0; c < Sh::kVp; ++c)
-#pragma unroll
-                for (int k = 0; k < Sh::kVw; ++k)
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t z0 = __byte_perm(vr[4 * j][c][k], vr[4 * j + 1][c][k], h ? 0x7362 : 0x5140);
-                        const uint32_t z1 = __byte_perm(vr[4 * j + 2][c][k], vr[4 * j + 3][c][k], h ? 0x7362 : 0x5140);
-                        const uint32_t a0 = wide_lo(z0), a1 = wide_hi(z0), a2 = wide_lo(z1), a3 = wide_hi(z1);
-#pragma unroll
-                        for (int nb = 0; nb < NB; ++nb)
-                            mma16816(o[nb][8 * c + 2 * k + h], a0, a1, a2, a3, w[j][nb][0], w[j][nb][1]);
+                        const float x0 = x[j][nb][2 * h], x1 = x[j][nb][2 * h + 1];
+                        sum[nb][0] += ex2(x0 - ref[nb][0]);
+                        sum[nb][1] += ex2(x1 - ref[nb][1]);
+                        w[j][nb][h] = transpose8(pack_h2(ex2(x0 + lv[j][h] - wref[nb][0]), ex2(x1 + lv[j][h] - wref[nb][1])));
                     }
-        if (i + 1 < my_tiles) load_v();
-        next = after;
-    }
-    more = next_piece();
-    if (more) begin();
+            // context: block b of a lane is its dims 2 b and 2 b + 1 of the pieces
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j)
+#pragma unroll
+                for (int c = 0; c < Sh::kVp; ++c)
+#pragma unroll
+                    for (int k = 0; k < Sh::kVw; ++k)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const uint32_t z0 = __byte_perm(vr[4 * j][c][k], vr[4 * j + 1][c][k], h ? 0x7362 : 0x5140);
+                            const uint32_t z1 = __byte_perm(vr[4 * j + 2][c][k], vr[4 * j + 3][c][k], h ? 0x7362 : 0x5140);
+                            const uint32_t a0 = wide_lo(z0), a1 = wide_hi(z0), a2 = wide_lo(z1), a3 = wide_hi(z1);
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+                                mma16816(o[nb][8 * c + 2 * k + h], a0, a1, a2, a3, w[j][nb][0], w[j][nb][1]);
+                        }
+            if (i + 1 < my_tiles) load_v();
+            next = after;
+        }
+        more = next_piece();
+        if (more) begin();
 
-    // ---- the warps are joined: weighted rows relative to ref, then references and sums
-    __syncthreads();
-    float* mo = reinterpret_cast<float*>(smem);             // [warp][head][D]
-    float* ml = mo + W * Sh::kHb * D;                       // [warp][head][2]
-    float* to = ml + W * Sh::kHb * 2;                       // [head][D], of the CTA
-    float* tl = to + Sh::kHb * D;                           // [head][2]
+        // ---- the warps are joined: weighted rows relative to ref, then references and sums
+        __syncthreads();
+        float* mo = reinterpret_cast<float*>(smem);             // [warp][head][D]
+        float* ml = mo + W * Sh::kHb * D;                       // [warp][head][2]
+        float* to = ml + W * Sh::kHb * 2;                       // [head][D], of the CTA
+        float* tl = to + Sh::kHb * D;                           // [head][2]
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int h = nb * kHeads + 2 * t + e;
-            float l = sum[nb][e];
+            for (int e = 0; e < 2; ++e) {
+                const int h = nb * kHeads + 2 * t + e;
+                float l = sum[nb][e];
 #pragma unroll
-            for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
-            // (exp2f: with scales below 2^-126 the factor may be subnormal)
-            const float f = wtop[nb][e] == -INFINITY ? (l != l ? l : 0.0f) : exp2f(wref[nb][e] - ref[nb][e]);
-            float* dst = mo + (warp * Sh::kHb + h) * D;
+                for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
+                // (exp2f: with scales below 2^-126 the factor may be subnormal)
+                const float f = wtop[nb][e] == -INFINITY ? (l != l ? l : 0.0f) : exp2f(wref[nb][e] - ref[nb][e]);
+                float* dst = mo + (warp * Sh::kHb + h) * D;
 #pragma unroll
-            for (int b = 0; b < kBlocks; ++b) {
-                const int d = D == 64 ? 8 * g + 2 * b : 128 * (b / 8) + 16 * g + 2 * (b % 8);
-                *reinterpret_cast<float2*>(dst + d) = make_float2(o[nb][b][e] * f, o[nb][b][e + 2] * f);
+                for (int b = 0; b < kBlocks; ++b) {
+                    const int d = D == 64 ? 8 * g + 2 * b : 128 * (b / 8) + 16 * g + 2 * (b % 8);
+                    *reinterpret_cast<float2*>(dst + d) = make_float2(o[nb][b][e] * f, o[nb][b][e + 2] * f);
+                }
+                if (g == 0) {
+                    // a head without a row: reference -inf, sum 0; one that holds a NaN keeps it in the sum
+                    ml[(warp * Sh::kHb + h) * 2] = top[nb][e] == -INFINITY ? -INFINITY : ref[nb][e];
+                    ml[(warp * Sh::kHb + h) * 2 + 1] = l;
+                }
             }
-            if (g == 0) {
-                // a head without a row: reference -inf, sum 0; one that holds a NaN keeps it in the sum
-                ml[(warp * Sh::kHb + h) * 2] = top[nb][e] == -INFINITY ? -INFINITY : ref[nb][e];
-                ml[(warp * Sh::kHb + h) * 2 + 1] = l;
+        __syncthreads();
+        for (int i = threadIdx.x; i < heads * (D / 4); i += Sh::kThreads) {
+            const int h = i / (D / 4), d = i % (D / 4) * 4;
+            float m = -INFINITY, l = 0.0f;
+#pragma unroll
+            for (int w = 0; w < W; ++w) m = fmaxf(m, ml[(w * Sh::kHb + h) * 2]);
+            const float base = m == -INFINITY ? 0.0f : m;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float wl = ml[(w * Sh::kHb + h) * 2 + 1];
+                const float f = part_weight(make_float2(ml[(w * Sh::kHb + h) * 2], wl), base);
+                const float4 y = *reinterpret_cast<const float4*>(mo + (w * Sh::kHb + h) * D + d);
+                l += wl * f;
+                acc.x = fmaf(y.x, f, acc.x);
+                acc.y = fmaf(y.y, f, acc.y);
+                acc.z = fmaf(y.z, f, acc.z);
+                acc.w = fmaf(y.w, f, acc.w);
+            }
+            const int64_t row = head0 + h;
+            if constexpr (TEAM) {
+                *reinterpret_cast<float4*>(to + h * D + d) = acc;
+                if (d == 0) *reinterpret_cast<float2*>(tl + 2 * h) = make_float2(m, l);
+            } else if (this_part < 0) {
+                const float r = l == 0.0f ? 0.0f : 1.0f / l;
+                __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
+                dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
+                dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
+                if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
+            } else {
+                const int64_t place = ((int64_t)blockIdx.x * 2 + this_part) * Sh::kHb + h;
+                *reinterpret_cast<float4*>(a.part_o + place * D + d) = acc;
+                if (d == 0) a.part_ml[place] = make_float2(m, l);
             }
         }
-    __syncthreads();
-    for (int i = threadIdx.x; i < heads * (D / 4); i += Sh::kThreads) {
-        const int h = i / (D / 4), d = i % (D / 4) * 4;
-        float m = -INFINITY, l = 0.0f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) m = fmaxf(m, ml[(w * Sh::kHb + h) * 2]);
-        const float base = m == -INFINITY ? 0.0f : m;
-        float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-            const float wl = ml[(w * Sh::kHb + h) * 2 + 1];
-            const float f = part_weight(make_float2(ml[(w * Sh::kHb + h) * 2], wl), base);
-            const float4 y = *reinterpret_cast<const float4*>(mo + (w * Sh::kHb + h) * D + d);
-            l += wl * f;
-            acc.x = fmaf(y.x, f, acc.x);
-            acc.y = fmaf(y.y, f, acc.y);
-            acc.z = fmaf(y.z, f, acc.z);
-            acc.w = fmaf(y.w, f, acc.w);
-        }
-        const int64_t row = head0 + h;
-        if constexpr (TEAM) {
-            *reinterpret_cast<float4*>(to + h * D + d) = acc;
-            if (d == 0) *reinterpret_cast<float2*>(tl + 2 * h) = make_float2(m, l);
-        } else if (this_part < 0) {
-            const float r = l == 0.0f ? 0.0f : 1.0f / l;
-            __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
-            dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
-            dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
-            if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
-        } else {
-            const int64_t place = ((int64_t)blockIdx.x * 2 + this_part) * Sh::kHb + h;
-            *reinterpret_cast<float4*>(a.part_o + place * D + d) = acc;
-            if (d == 0) a.part_ml[place] = make_float2(m, l);
-        }
-    }
     }
     if (__any_sync(kFull, bad) && lane == 0 && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_PAGE);
 
@@ -789,9 +791,9 @@ kv8_decode_kernel(const Kv8Args a)
 }
 
 // The parts of a unit joined, a CTA a query head: groups of D / 4 threads take the parts in turn, four of them in
-// flight, with a softmax each, and are joined in their order.  T threads: 512 where units have many parts (131072 rows
-// in 57 parts: the call 55.8 us, with 128 threads 61.4), 128 where they have few (64 ragged sequences: 186 us, 201).  The first part is what CTA c left, the others are
-// what the CTAs behind it found begun.
+// flight, with a softmax each, and are joined in their order.  The first part is what CTA c left, the others are
+// what the CTAs behind it found begun.  T threads: 512 where units have many parts (131072 rows in 57 parts: the call
+// 55.8 us, with 128 threads 61.4), 128 where they have few (64 ragged sequences: 186 us, with 512 threads 201).
 template <int D, int T>
 __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_heads)
 {
@@ -833,7 +835,8 @@ __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_h
                         const int q = i + u * kJoin;
                         const int64_t place = (((int64_t)(c + q) * a.n_hb + hb) * 2 + (q == 0)) * n_heads + h;
                         x[u] = q < n ? a.part_ml[place] : make_float2(-INFINITY, 0.0f);
-                        y[u] = q < n ? *reinterpret_cast<const float4*>(a.part_o + place * D + d) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                        y[u] = q < n ? *reinterpret_cast<const float4*>(a.part_o + place * D + d)
+                                     : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     }
 #pragma unroll
                     for (int u = 0; u < kFlight; ++u) top = fmaxf(top, x[u].x);
@@ -1045,7 +1048,8 @@ int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* worksp
     if (q.bytes && (!workspace || ws_bytes < q.bytes))
         return set_last_error(KVQ_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", E, workspace ? ws_bytes : (size_t)0, q.bytes);
     if (q.bytes && !aligned(workspace, 256)) return set_last_error(KVQ_EALIGN, "%s: workspace not 256-byte aligned", E);
-    Kv8Args a{*p, p->n_qh / p->cache.n_kv, q.n_hb, q.line, q.idle, q.team, q.team_rows, nullptr, nullptr, nullptr, static_cast<__nv_bfloat16*>(out), lse, dev_status};
+    Kv8Args a{*p,      p->n_qh / p->cache.n_kv, q.n_hb, q.line, q.idle, q.team, q.team_rows, nullptr, nullptr,
+              nullptr, static_cast<__nv_bfloat16*>(out), lse, dev_status};
     if (q.bytes) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         a.info = reinterpret_cast<int4*>(ws);

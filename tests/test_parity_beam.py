@@ -508,6 +508,18 @@ def test_select_ties(kvq, V, K, R):
     check_select(kvq, ramp[..., ::-1].copy(), zero, None, K)
 
 
+@pytest.mark.parametrize("V,ld", [(101, None), (4099, None), (50257, None), (50257, 50264), (20000, 20003), (7, None), (33001, 33006)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_select_equal_beams(kvq, V, ld, bf16):
+    """Beams of equal scores and logits, their rows beginning at any place: the lowest beam's candidate stands first."""
+    g = np.random.default_rng(V)
+    R, B = 3, 8
+    x = dev(np.repeat((g.standard_normal((R, 1, V)) * 3).astype(np.float32), B, 1))
+    x = x.bfloat16() if bf16 else x
+    score = np.repeat(-7 * g.random((R, 1)), B, 1).astype(np.float32)
+    check_select(kvq, x, score, None, min(V, 20), ld=ld)
+
+
 def test_select_edges(kvq):
     g = np.random.default_rng(4)
     R, B, V = 6, 4, 3000
