@@ -673,8 +673,8 @@ int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* worksp
  * score is -inf has none; one with a NaN or +inf among its logits (an unfinished beam's) or as its
  * score has none either, and sets KVQ_DEV_BAD_VALUE.  The n_out candidates of the largest
  * values are written in descending order, equal ones by ascending (beam, token); values of one beam
- * are compared by their logits, those of different beams before they are rounded to fp32 (the sums
- * are kept in 64 bits).  Of each:
+ * are compared by their logits, those of different beams before they are rounded to fp32 (as two
+ * floats; the terms of a sum are fp32 exponentials, within 2^-22 of themselves).  Of each:
  *     out_score   its value
  *     out_token   its token
  *     out_parent  the index r * n_beam + b of its beam (kvq_fork_pages' parent)
@@ -729,7 +729,7 @@ int kvq_beam_select(const kvq_beam_problem* p, void* workspace, size_t ws_bytes,
  *   [0, n_pages) becomes -1 in the new table (KVQ_DEV_BAD_PAGE); a push past the end of the list is dropped
  *   (KVQ_DEV_BAD_PAGE).
  * Pages shared with tables outside the call must not be released or truncated by it.  A page of the
- * free list must not be in a table.  While tables share pages, kvq_resize_pages may let
+ * free list must not be in a table.  n_seq == 0 is a no-op (*n_copy too is left).  While tables share pages, kvq_resize_pages may let
  * them grow, but rows are given back with this call (keep_len), which knows who else holds a page.
  */
 typedef struct kvq_fork_plan {

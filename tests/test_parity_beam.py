@@ -248,6 +248,19 @@ def test_decode(kvq, d, lens, kv, group, page, window):
     assert torch.equal(out.view(torch.int16), again.view(torch.int16)) and torch.equal(lse, lse2)      # the same bits
 
 
+@pytest.mark.parametrize("n,kv,most,d,page", [(3, 8, 1000, 128, 16), (9, 8, 700, 64, 24), (16, 8, 1020, 128, 64), (30, 8, 512, 256, 16),
+                                              (60, 7, 150, 64, 0), (2, 1, 4000, 128, 16), (50, 8, 130, 128, 32), (100, 8, 3000, 64, 16)])
+def test_decode_batches_of_short_sequences(kvq, n, kv, most, d, page):
+    """Units of one to a few places: clusters of every size, and more units than CTAs."""
+    g = np.random.default_rng(n + most)
+    lens = g.integers(0, most + 1, n)
+    lens[0], lens[-1] = most, 0
+    c = Cache(lens, kv, d, page, n + d)
+    q = queries(n, 3 * kv, d, n)
+    out, lse = decode(kvq, c.problem(kvq, q))
+    check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, 0, 1 / math.sqrt(d)), d, most)
+
+
 def test_decode_many_sequences(kvq):
     g = np.random.default_rng(0)
     lens = g.integers(0, 90, 1500)
@@ -278,21 +291,21 @@ def test_decode_strided_queries_without_lse(kvq):
     check_decode(out, ref[1].float(), ref, 128, 1700)
 
 
-def test_decode_bad_pages(kvq):
-    lens = [200, 333]
-    c = Cache(lens, 2, 128, 16, 8)
+@pytest.mark.parametrize("lens,page", [([200, 333], 16), ([200, 333], 12), ([9000, 7333], 16), ([9000, 7333], 20)])
+def test_decode_bad_pages(kvq, lens, page):
+    c = Cache(lens, 2, 128, page, 8)
     q = queries(2, 8, 128, 9)
     table = c.table.copy()
-    table[0, 3], table[1, 0], table[1, 20] = -1, c.pool // 16, 2**31 - 1
+    table[0, 3], table[1, 0], table[1, -4] = -1, c.pool // page, 2**31 - 1
     st = i32(1)
     out, lse = decode(kvq, c.problem(kvq, q, table=table), st)
     assert st.item() == BAD_PAGE
-    bad = {(0, 3), (1, 0), (1, 20)}
-    rows_of = lambda s, pos: np.array([-1 if (s, int(t) // 16) in bad else int(c.rows_of(s, t)) for t in pos], np.int64)
-    check_decode(out, lse, decode_ref(c.pl, q, lens, rows_of, 0, 1 / math.sqrt(128)), 128, 333)
+    bad = {(0, 3), (1, 0), (1, table.shape[1] - 4)}
+    rows_of = lambda s, pos: np.array([-1 if (s, int(t) // page) in bad else int(c.rows_of(s, t)) for t in pos], np.int64)
+    check_decode(out, lse, decode_ref(c.pl, q, lens, rows_of, 0, 1 / math.sqrt(128)), 128, max(lens))
     # a table too short for the lengths, and one without any page
     out, lse = decode(kvq, c.problem(kvq, q, table=np.ascontiguousarray(c.table[:, :5])), st)
-    check_decode(out, lse, decode_ref(c.pl, q, [80, 80], c.rows_of, 0, 1 / math.sqrt(128)), 128, 80)
+    check_decode(out, lse, decode_ref(c.pl, q, [5 * page] * 2, c.rows_of, 0, 1 / math.sqrt(128)), 128, 5 * page)
     out, lse = decode(kvq, c.problem(kvq, q, table=np.full_like(c.table, -1)), st)
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
 
@@ -343,8 +356,9 @@ def test_decode_many_small_weights(kvq):
         check_decode(out, lse, decode_ref(c.pl, q, [L], c.rows_of, 0, 1.0), d, 4096)
 
 
-def test_decode_nan_queries_stay_in_their_head(kvq):
-    c = Cache([700, 20], 2, 128, 64, 60)
+@pytest.mark.parametrize("lens", [[700, 20], [9000, 5001]])
+def test_decode_nan_queries_stay_in_their_head(kvq, lens):
+    c = Cache(lens, 2, 128, 64, 60)
     q = queries(2, 16, 128, 61)
     clean, lse0 = decode(kvq, c.problem(kvq, q))
     bad = q.clone()
@@ -374,9 +388,10 @@ def test_decode_far_rows(kvq):
     check_decode(out, lse, decode_ref(pl, q, [L], lambda s, t: slot[t], 0, 1 / 16), d, L)
 
 
-def test_decode_streams_and_graph(kvq):
+@pytest.mark.parametrize("long", [3000, 20000])
+def test_decode_streams_and_graph(kvq, long):
     """Two problems on two streams at once, and a replayed graph after the lengths have changed."""
-    cs = [Cache([3000, 100], 2, 128, 64, 70), Cache([2500, 1, 9], 4, 64, 16, 71)]
+    cs = [Cache([long, 100], 2, 128, 64, 70), Cache([long - 500, 1, 9], 4, 64, 16, 71)]
     qs = [queries(2, 16, 128, 72), queries(3, 4, 64, 73)]
     ps = [c.problem(kvq, q) for c, q in zip(cs, qs)]
     want = [decode(kvq, p) for p in ps]
@@ -698,6 +713,7 @@ class Forks:
 @pytest.mark.parametrize("n,max_pages,n_pages,page,tokens", [
     (1, 1, 1, 1, 1), (4, 8, 64, 16, 60), (8, 40, 400, 16, 500), (64, 9, 900, 5, 30), (300, 30, 20000, 64, 1500),
     (1030, 5, 9000, 3, 9), (2, 3000, 7000, 4, 9000), (40, 600, 200000, 8, 4000),
+    (5000, 3, 20000, 4, 9), (512, 16, 8192, 2, 20), (513, 16, 8192, 2, 20), (4097, 2, 8193, 3, 5),
 ])
 def test_fork_steps(kvq, n, max_pages, n_pages, page, tokens):
     f = Forks(kvq, n, max_pages, n_pages, page, n + page)
