@@ -639,7 +639,8 @@ int kvq_append_kv8(const void* k, int64_t k_ld_row, int64_t k_ld_head, const voi
 typedef struct kvq_kv8_problem {
     int32_t n_seq;                  /* 0 .. 65535                                       */
     int32_t n_qh;                   /* query heads, a multiple of cache.n_kv             */
-    int32_t max_seq_len;            /* host bound on every seq_len, 0 .. 2^30            */
+    int32_t max_seq_len;            /* host bound on every seq_len, 0 .. 2^30; n_seq *
+                                       cache.n_kv * (max_seq_len / 64 + 2) < 2^31        */
     int32_t window;                 /* rows seen at most; 0: all                         */
     const int32_t* seq_len;         /* device [n_seq]: rows held, the new token's included */
     const int32_t* block_table;     /* device [n_seq][max_pages] pool page ids, or NULL */
@@ -673,8 +674,10 @@ int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* worksp
  * score is -inf has none; one with a NaN or +inf among its logits (an unfinished beam's) or as its
  * score has none either, and sets KVQ_DEV_BAD_VALUE.  The n_out candidates of the largest
  * values are written in descending order, equal ones by ascending (beam, token); values of one beam
- * are compared by their logits, those of different beams before they are rounded to fp32 (as two
- * floats; the terms of a sum are fp32 exponentials, within 2^-22 of themselves).  Of each:
+ * are compared by their logits, those of different beams before they are rounded to fp32: as two
+ * floats, within 2^-45 of the largest of score, value and the logarithm but for the sum's terms, which
+ * are fp32 exponentials, within 2^-22 of themselves (logits of a beam nearer to one another than that may change places).
+ * A value below fp32's range is -inf.  Of each:
  *     out_score   its value
  *     out_token   its token
  *     out_parent  the index r * n_beam + b of its beam (kvq_fork_pages' parent)
@@ -729,8 +732,9 @@ int kvq_beam_select(const kvq_beam_problem* p, void* workspace, size_t ws_bytes,
  *   [0, n_pages) becomes -1 in the new table (KVQ_DEV_BAD_PAGE); a push past the end of the list is dropped
  *   (KVQ_DEV_BAD_PAGE).
  * Pages shared with tables outside the call must not be released or truncated by it.  A page of the
- * free list must not be in a table.  n_seq == 0 is a no-op (*n_copy too is left).  While tables share pages, kvq_resize_pages may let
- * them grow, but rows are given back with this call (keep_len), which knows who else holds a page.
+ * free list must not be in a table.  n_seq == 0 is a no-op (*n_copy too is left).  While tables share
+ * pages, kvq_resize_pages may let them grow, but rows are given back with this call (keep_len), which
+ * knows who else holds a page.
  */
 typedef struct kvq_fork_plan {
     int32_t n_seq;                  /* 0 .. 65535                                       */

@@ -127,11 +127,11 @@ __device__ __forceinline__ void warp_sum(float& sum, float& lo)
     }
 }
 
-// score - m - log(s.x + s.y) in two floats, s.x > 0 finite.  The logarithm is e log 2 + 2 atanh u, u = (f - 1) / (f + 1),
+// score - log(s.x + s.y) in two floats, s.x > 0 finite.  The logarithm is e log 2 + 2 atanh u, u = (f - 1) / (f + 1),
 // for s = 2^e f, f in [1/sqrt 2, sqrt 2): u to two floats, then 2 (u + u^3 / 3 + u^5 / 5 + ...) with the powers from the
 // third on in one (|u| < 0.172: they are below 2^-8 of u, and seven terms leave 2^-37).  64-bit arithmetic takes 16
 // times as long here.
-__device__ __forceinline__ float2 less_log(float score, float m, float2 s)
+__device__ __forceinline__ float2 less_log(float score, float2 s)
 {
     int e = (int)(__float_as_uint(s.x) >> 23) - 127;
     float f = __uint_as_float((__float_as_uint(s.x) & 0x7FFFFFu) | 0x3F800000u);       // (sums are 1 or more, not subnormal)
@@ -147,7 +147,6 @@ __device__ __forceinline__ float2 less_log(float score, float m, float2 s)
     const float q = u * u;
     const float tail = u * q * fmaf(q, fmaf(q, fmaf(q, fmaf(q, fmaf(q, 1.0f / 13.0f, 1.0f / 11.0f), 1.0f / 9.0f), 1.0f / 7.0f), 0.2f), 1.0f / 3.0f);
     float hi = score, lo = 0.0f;
-    add_exact(hi, lo, -m);
     add_exact(hi, lo, (float)-e * 0x1.62e4p-1f);            // log 2 = 0x1.62e4p-1 (15 bits: the product is exact) + the rest
     add_exact(hi, lo, -2.0f * u);
     lo -= fmaf((float)e, 0x1.7f7d1cp-20f, 2.0f * (fmaf(ul, q, ul) + tail));
@@ -466,8 +465,8 @@ __device__ __forceinline__ bool above(const Cand& a, const Cand& b) { return a.v
 
 __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
 {
-    __shared__ float2 s_base[kMaxBeam];                     // sum of exponentials, then score - its logarithm, in two floats
-    __shared__ float s_max[kMaxBeam];
+    __shared__ float2 s_base[kMaxBeam];                     // sum of exp(x - the largest logit), then score - its logarithm
+    __shared__ float s_max[kMaxBeam];                       // the largest logit
     __shared__ uint8_t s_live[kMaxBeam];                    // 0: no candidates; 1: its tokens; 2: finished
     __shared__ __align__(16) uint32_t s_floor[32];
     __shared__ int s_n;
@@ -530,7 +529,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     if (tid < p.n_beam && s_live[tid] == 1) {
         const float2 s = s_base[tid];
         if (s.x > 0.0f) {
-            s_base[tid] = less_log(score, s_max[tid], s);
+            s_base[tid] = less_log(score, s);
         } else {
             s_live[tid] = 0;
             if (s.x != s.x && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_VALUE);
@@ -547,9 +546,14 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
             c.t = beam;
         } else if (key) {
             float v = unordered((uint32_t)(key >> 32)), lo = s_base[b].y;
+            add_exact(v, lo, -s_max[b]);                    // (first: the largest ones' difference is small, wherever they lie)
             add_exact(v, lo, s_base[b].x);
-            const float hi = v + lo;                        // (both normalised: their pairs order as their sums)
+            float hi = v + lo;                              // (both normalised: their pairs order as their sums)
             lo = (v - hi) + lo;
+            if (!(hi > -INFINITY)) {                        // (beyond fp32: its parts may be NaN)
+                hi = -INFINITY;
+                lo = 0.0f;
+            }
             c.v = (uint64_t)ordered(hi) << 32 | ordered(lo);
             c.t = beam | (key >> 32) << 24 | ((uint32_t)key & (kMaxVocab - 1));
         }

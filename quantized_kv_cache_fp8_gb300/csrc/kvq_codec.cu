@@ -752,10 +752,10 @@ struct AppendKv8Args {
 
 // x / 448, correctly rounded: with c = RN(1 / 448) and q = RN(x c), which is within 1 ulp of x / 448 (half of one
 // for c's rounding, half for its own), RN(q + (x - 448 q) c) is RN(x / 448) (Markstein, 1990); the remainder is exact but
-// for the smallest x
+// for the smallest x, and no number for an infinite one
 __device__ __forceinline__ float over_448(float x)
 {
-    if (x < 0x1p-90f) return __fdiv_rn(x, 448.0f);
+    if (!(x >= 0x1p-90f && x < INFINITY)) return __fdiv_rn(x, 448.0f);
     constexpr float c = 1.0f / 448.0f;
     const float q = __fmul_rn(x, c);
     return __fmaf_rn(__fmaf_rn(-448.0f, q, x), c, q);

@@ -24,11 +24,17 @@ constexpr int kRowsShared = 8192;        // table entries of a single CTA that a
 constexpr int kPagesOne = 8192;          // pages that a single CTA goes over (5 bytes of shared memory each)
 constexpr size_t kPlainSmem = 39 * 1024; // dynamic shared memory that needs no attribute, beside the kernels' own
 constexpr int kPagesShared = 65536;      // pages whose marks fit the CTAs' shared memory
+// the most that a single CTA and one of a cluster ask for (2 bytes of marks a page, 4 of keepers an own page, a single
+// one's table rows); always this much is allowed, so that calls of several threads do not lower each other's limit
+constexpr int kMostSmemOne = 6 * kPagesOne + 4 * kRowsShared, kMostSmem = 2 * kPagesShared + 4 * kPagesShared / kCluster;
 
 __device__ __forceinline__ void flag(uint32_t* status, unsigned bit)
 {
     if (status) atomicOr(status, bit);
 }
+
+// pages of n rows (n + page - 1 may pass 2^31)
+__device__ __forceinline__ int pages_of(int n, int page) { return n / page + (n % page != 0); }
 
 // Inclusive prefix sum over the CTA; *total = the CTA's sum.  s_warp: 32 entries.
 __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total)
@@ -228,7 +234,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
         s0, s1,
         [&](int s) {
             const int4 q = seq[s];
-            const int need = (q.y + ps - 1) / ps;
+            const int need = pages_of(q.y, ps);
             return Row{max(q.w, need), q.w, need, q.y / ps, (int64_t)s * p.max_pages, (int64_t)q.x * p.max_pages};
         },
         [&](const Row& r, int e) {                          // its entry before, its parent's
@@ -342,7 +348,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
         }
         if (s >= used) p.copy_src[s] = p.copy_dst[s] = p.copy_rows[s] = -1;
         p.seq_len[s] = len;
-        p.n_held[s] = (len + ps - 1) / ps;
+        p.n_held[s] = pages_of(len, ps);
     }
     if (team.cta == 0 && tid == 0) {
         p.n_free[0] = have - used;
@@ -352,7 +358,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
         s0, s1,
         [&](int s) {
             const int4 q = seq[s];
-            const int need = (q.y + ps - 1) / ps;
+            const int need = pages_of(q.y, ps);
             // (whole: a copy's last page is written above)
             return Row{max(q.w, need), q.w, need, q.x >= 0 ? q.y / ps : -1, (int64_t)s * p.max_pages, 0};
         },
@@ -623,7 +629,7 @@ cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(
     if (t.one) {
         const size_t smem = t.bytes + rows;
         if (smem > kPlainSmem) {
-            cudaError_t e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            cudaError_t e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmemOne);
             if (e != cudaSuccess) return e;
         }
         return launch_dependent(one, dim3(1), dim3(kThreadsOne), smem, s, a);
@@ -635,7 +641,7 @@ cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(
     cfg.dynamicSmemBytes = t.shared ? t.bytes : 0;
     cfg.stream = s;
     if (cfg.dynamicSmemBytes > kPlainSmem) {
-        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)t.bytes);
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute attr[2];
@@ -844,7 +850,7 @@ int kvq_copy_pages(const kvq_page_copy* d, uint32_t* dev_status, kvq_stream_t st
     a.n_copy = d->n_copy;
     a.status = dev_status;
     const int64_t warps = (int64_t)d->max_copy * end;
-    const int64_t grid = std::min<int64_t>((warps * 32 + kCopyThreads - 1) / kCopyThreads, (int64_t)sm_count() * 8);
+    const int64_t grid = std::min<int64_t>((warps - 1) / (kCopyThreads / 32) + 1, (int64_t)sm_count() * 8);
     if (d->n_planes > kFewPlanes)
         return cuda_status(launch_dependent(copy_pages_kernel<kMaxPlanes>, dim3((unsigned)grid), dim3(kCopyThreads), 0,
                                             (cudaStream_t)stream, a), E);

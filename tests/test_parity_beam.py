@@ -107,6 +107,38 @@ def test_append_bytes(kvq, orc, d, bf16, rows, kv, layout):
         assert np.array_equal(host(pl[name + "_scale"]).view(np.uint32), want[1].view(np.uint32))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_append_what_is_no_number(kvq, d, bf16):
+    """Rows with infinities and NaNs, rows near the type's largest and smallest: the bytes of kvq_encode_fp8."""
+    rows, kv = 24, 2
+    x = np.random.default_rng(d).standard_normal((2, rows, kv, d)).astype(np.float32)
+    x[:, 0, :, 3] = np.inf
+    x[:, 1, :, d - 1] = -np.inf
+    x[:, 2, :, 0], x[:, 2, :, 9] = np.inf, -np.inf
+    x[:, 3, :, 5] = np.nan
+    x[:, 4] = np.nan
+    x[:, 5, :, 5], x[:, 5, :, 6] = np.nan, np.inf
+    x[:, 6, :, 7] = 3.3e38
+    x[:, 7] *= np.float32(1e-38)
+    x[:, 8] = 0.0
+    x[:, 8, :, 1] = np.float32(2.0**-133)
+    x[:, 9] = 0.0
+    x[:, 9, :, 1] = np.nan
+    t = dev(x)
+    t = t.bfloat16() if bf16 else t
+    pl, slot = new_planes(kv, rows, d), torch.arange(rows, dtype=torch.int32, device="cuda")
+    kvq.kvq_append_kv8(t[0], t[1], slot, pl)
+    for i, name in enumerate(("k", "v")):
+        flat = t[i].float().reshape(rows * kv, d).contiguous()
+        codes, scales = torch.zeros(rows * kv, d, dtype=torch.uint8, device="cuda"), torch.zeros(rows * kv, device="cuda")
+        kvq.kvq_encode_fp8(flat, codes, scales)
+        torch.cuda.synchronize()
+        assert np.array_equal(host(pl[name]), host(codes).reshape(rows, kv, d).transpose(1, 0, 2))
+        got, want = host(pl[name + "_scale"]), host(scales).reshape(rows, kv).T
+        assert np.array_equal(got, want, equal_nan=True) and np.isposinf(got[:, 0]).all()
+
+
 def test_append_nothing(kvq):
     pl = new_planes(2, 16, 64)
     x = torch.zeros(0, 2, 64, device="cuda")
@@ -561,6 +593,23 @@ def test_select_edges(kvq):
     check_select(kvq, x, score, fin, 3, eos=0, pad=0)
 
 
+def test_select_far_apart(kvq):
+    """Logits and scores whose plain sums or differences pass fp32's largest, while the values do not."""
+    g = np.random.default_rng(6)
+    R, B, V = 4, 3, 2500
+    x = (g.standard_normal((R, B, V)) * 2).astype(np.float32)
+    score = np.zeros((R, B), np.float32)
+    x[0] += np.float32(3.0e38) * np.array([1, -1, 1], np.float32)[:, None]
+    score[0] = -3.0e38, -2.9e38, -3.3e38
+    x[1] = -3.0e38                                           # (further from the largest than fp32 reaches)
+    x[1, :, :6] = np.array([3.0, 2.99, 2.98, 2.97, 2.96, 2.95], np.float32) * np.float32(1e38)
+    score[1] = -1, -2, -3
+    x[2, 0] *= 1e-30
+    score[2] = -1000
+    score[3] = 3.0e38, -3.0e38, 1e30
+    check_select(kvq, x, score, None, 8, eos=-1)
+
+
 def test_select_in_place_and_graph(kvq):
     """A loop of steps in a graph whose scores and finished flags are the step's own outputs."""
     g = np.random.default_rng(5)
@@ -766,6 +815,48 @@ def test_fork_bad_inputs(kvq):
     f.held[0], f.held[2], f.n_free = -1, 9, 31
     f.push()
     f.fork([1, 1, 1], status=BAD_INDEX | BAD_PAGE)           # (no room in the list for what is given back)
+
+
+def test_fork_longest(kvq):
+    """A length of 2^31 - 1 rows, of a table that lists its pages many times."""
+    page, n_pages = 1 << 20, 100
+    f = Forks(kvq, 2, 2100, n_pages, page, 6)
+    f.table[0] = np.arange(2100) % 90
+    f.held[0], f.lens[0] = 2100, 2**31 - 1
+    f.free[:10], f.n_free = np.arange(90, 100), 10
+    f.push()
+    assert len(f.fork([0, 0], status=0)) == 2 and f.held.tolist() == [2048, 2048] and f.lens.tolist() == [2**31 - 1] * 2
+
+
+def test_forks_of_several_threads(kvq):
+    """Plans of several sizes (and amounts of shared memory) called at once by threads with a stream each."""
+    import threading
+    sizes = [(8, 1000, 8000, 4), (8, 400, 5000, 4), (600, 20, 60000, 4), (600, 20, 20000, 4)]
+    errors = []
+
+    def run(size, seed):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                n, most, pages, page = size
+                f = Forks(kvq, n, most, pages, page, seed)
+                f.grow(f.g.integers(0, 60, n))
+                parent = dev(np.arange(n, dtype=np.int32))
+                p = kvq.make_fork_plan(parent=parent, page_size=page, **f.d, **f.lists)
+                ws = scratch(kvq.kvq_fork_pages_workspace(p))
+                torch.cuda.current_stream().synchronize()
+                for _ in range(300):
+                    kvq.kvq_fork_pages(p, ws)
+                torch.cuda.current_stream().synchronize()
+                assert np.array_equal(host(f.d["block_table"]), f.table) and np.array_equal(host(f.d["seq_len"]), f.lens)
+        except BaseException as e:                           # noqa: B036 (raised below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(s, i)) for i, s in enumerate(sizes)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
 
 
 def test_fork_in_a_graph(kvq):
