@@ -27,7 +27,7 @@ constexpr int kMaxBeam = 64, kMaxOut = 128, kMaxVocab = 1 << 24;
 constexpr int kBuffer = 1024;            // gathered candidates
 constexpr int kVectors = 512;            // gathered vectors
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLarge = 1e30f;          // logits from here on are subtracted before they are scaled
+constexpr float kLarge = 0x1p13f;        // logits from here on are subtracted before they are scaled
 
 struct BeamArgs {
     kvq_beam_problem p;
@@ -205,14 +205,14 @@ struct __align__(16) Vec<__nv_bfloat16> {
     }
 };
 
-// sum of 2^(x l - c) over a vector, in two chains (packed pairs of fp32 are no faster here)
-template <typename V>
+// sum over a vector, in two chains (packed pairs of fp32 are no faster here): of 2^(x l - c), or of 2^((x - c) l)
+template <bool LARGE, typename V>
 __device__ __forceinline__ float exp_sum(const V& v, float c)
 {
     float acc[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int i = 0; i < V::kN; ++i) {
-        const float t = ex2(fmaf(v.get(i), kLog2e, -c));
+        const float t = ex2(LARGE ? (v.get(i) - c) * kLog2e : fmaf(v.get(i), kLog2e, -c));
         acc[i & 1] = i < 2 ? t : acc[i & 1] + t;
     }
     return acc[0] + acc[1];
@@ -344,18 +344,12 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
         if (fabsf(m) < kLarge) {
             const float c = __fmul_rn(m, kLog2e);
 #pragma unroll
-            for (int j = 0; j < NV; j += 2) add_exact(sum, low, exp_sum(x[j], c) + exp_sum(x[j + 1], c));
+            for (int j = 0; j < NV; j += 2) add_exact(sum, low, exp_sum<false>(x[j], c) + exp_sum<false>(x[j + 1], c));
         } else {
+            // (without a maximum there is nothing, or a NaN)
+            const float c = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-            for (int j = 0; j < NV; ++j)
-#pragma unroll 1
-                for (int e = 0; e < kE; ++e) {
-                    const uint32_t w = sizeof(X) == 2 ? e / 2 : e;
-                    const uint32_t b = w == 0 ? x[j].w[0] : w == 1 ? x[j].w[1] : w == 2 ? x[j].w[2] : x[j].w[3];
-                    const float y = __uint_as_float(sizeof(X) == 4 ? b : e % 2 ? b & 0xFFFF0000u : b << 16);
-                    // m l may not be finite; without a maximum there is nothing, or a NaN
-                    sum += m != -INFINITY ? ex2((y - m) * kLog2e) : y == -INFINITY ? 0.0f : y;
-                }
+            for (int j = 0; j < NV; j += 2) add_exact(sum, low, exp_sum<true>(x[j], c) + exp_sum<true>(x[j + 1], c));
         }
         warp_sum(sum, low);
         if (lane == 0) {
@@ -371,15 +365,10 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
             float all = mw;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, o));
-            // The rounding of c in nats is exact as a fused multiply-add but for its last factor.  Its exponential is its
-            // series (to 2^-32) but for logits beyond 2^13.
+            // The rounding of c in nats is exact as a fused multiply-add but for its last factor.  It is below 2^-11, so its
+            // exponential is its series (to 2^-35).
             const float off = fabsf(mw) < kLarge ? -0.6931471805599453f * fmaf(mw, kLog2e, -__fmul_rn(mw, kLog2e)) : 0.0f;
-            if (fabsf(off) < 0x1p-10f) {
-                sw.y = fmaf(sw.x, off * fmaf(0.5f, off, 1.0f), sw.y);
-            } else {
-                const float f = expf(off);
-                sw = make_float2(sw.x * f, sw.y * f);
-            }
+            sw.y = fmaf(sw.x, off * fmaf(0.5f, off, 1.0f), sw.y);
             float t = 0.0f, lo = 0.0f;
             // (a sum of 0 has no maximum; that of the maximum's warp stays as it is)
             if (sw.x != 0.0f) add_scaled(t, lo, sw, mw == all ? 1.0f : expf(mw - all));

@@ -610,6 +610,22 @@ def test_select_far_apart(kvq):
     check_select(kvq, x, score, None, 8, eos=-1)
 
 
+@pytest.mark.parametrize("V", [3000, 40000])
+@pytest.mark.parametrize("R", [1, 30])
+def test_select_large_logits(kvq, V, R):
+    """Rows around levels of any size and sign, a mask's filler among them: sums are of differences.  (A request a row: values
+    of rows of different levels that would tie exactly differ by the exponentials' 2^-22.)"""
+    g = np.random.default_rng(V)
+    for levels in ([3e4, -3e4, 1e6, -1e6], [2e6, -2e6, 1e9, -1e9], [1e10, -1e10, 1e13, -1e13], [1e25, -1e25, 9e29, -3.4028235e38]):
+        at = np.array(levels, np.float32).repeat(R)[:, None, None]
+        x = np.broadcast_to(at, (4 * R, 1, V)).copy()         # nothing but the level
+        check_select(kvq, x, np.zeros((4 * R, 1), np.float32), None, 6, eos=-1)
+        far = np.abs(at) < 1e30
+        step = np.maximum(np.spacing(np.where(far, np.abs(at), 1)), np.float32(0.125))
+        x = np.where(far, at + step * g.integers(-9, 1, x.shape).astype(np.float32), at).astype(np.float32)
+        check_select(kvq, x, (-5 * g.random((4 * R, 1))).astype(np.float32), None, 6, eos=-1)
+
+
 def test_select_in_place_and_graph(kvq):
     """A loop of steps in a graph whose scores and finished flags are the step's own outputs."""
     g = np.random.default_rng(5)
