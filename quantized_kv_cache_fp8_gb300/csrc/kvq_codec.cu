@@ -56,9 +56,9 @@ struct RowSlot {
     const int32_t* slot;
     int64_t n_rows;
     uint32_t* status;
-    __device__ __forceinline__ int64_t operator()(int64_t r) const
+    __device__ __forceinline__ int64_t operator()(int64_t r) const { return checked(__ldg(slot + r)); }
+    __device__ __forceinline__ int64_t checked(int64_t o) const
     {
-        const int64_t o = __ldg(slot + r);
         if (o < n_rows) return o < 0 ? -1 : o;
         if (status) atomicOr(status, (unsigned)KVQ_DEV_BAD_PAGE);
         return -1;
@@ -737,9 +737,11 @@ append_mla_kernel(const X* __restrict__ c_lat, int64_t ldx, const X* __restrict_
 // Paged append of a grouped-query model's K/V rows in fp8 (the bytes of encode_fp8_vec_rows): D / 16
 // lanes take the vector of one row, one of K and V and one KV head, 16 elements a lane (16-byte loads).  A warp takes
 // 512 / D of a row's 2 n_kv vectors (K's heads, then V's) at once, with the next ones on their way.
-// Bound by the rows' bytes, with the arithmetic not far behind (a division a vector and a correction a quotient, two
-// quotients at a time; what is done once a lane is shared by its 16 elements): 32768 rows of 8 heads of 128 take 64 us
-// with a row and a division for every vector, 52 with 8 elements a lane, 43 so.
+// Bound by the rows' bytes (a division a vector and a correction a quotient, two quotients at a time; what is done once a
+// lane is shared by its 16 elements): 32768 rows of 8 heads of 128 take 64 us with a row and a division for every vector, 52 with
+// 8 elements a lane, 42 so (4.8 TB/s), and 41 without the quotients, 37 without the codes' stores, so that it is the mix of
+// reads a row apart and writes to 16 planes that bounds it.  A ring of four vectors a warp in shared memory takes 39.7, but 37 rows 4.8
+// instead of 4.4.
 // ------------------------------------------------------------------------------------
 struct AppendKv8Args {
     const void *k, *v;
@@ -761,16 +763,16 @@ __device__ __forceinline__ float over_448(float x)
     return __fmaf_rn(__fmaf_rn(-448.0f, q, x), c, q);
 }
 
-// the quotients of a pair by s, y = RN(1 / s), as in append_fp8_bf16_rows
+// the quotients of a pair by -s, y = RN(1 / s), as in append_fp8_bf16_rows (of -a by s: -a is what its steps take)
 __device__ __forceinline__ void divide_pair(float& a, float& b, float s, float y)
 {
     uint64_t x, q, r, s2, ny2;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(-a), "f"(-b));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
     asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
     asm("mov.b64 %0, {%1, %1};" : "=l"(ny2) : "f"(-y));
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(ny2));         // q = a y
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(q), "l"(s2), "l"(x));      // q s - a
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(r), "l"(ny2), "l"(q));     // q - (q s - a) y
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(q) : "l"(x), "l"(ny2));         // q = -a y
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(q), "l"(s2), "l"(x));      // q s + a
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(q) : "l"(r), "l"(ny2), "l"(q));     // q - (q s + a) y
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
 }
 
@@ -782,54 +784,71 @@ __global__ void __launch_bounds__(kCodecThreads) append_kv8_kernel(const AppendK
     const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
     const int64_t n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int n_kv = a.c.n_kv;
-    const int64_t n = a.rows * a.units;
     grid_dependency_wait();
     grid_dependents_launch();
-    // the vector at hand: its row of the planes (-1: none) and elements; the next one's are on their way meanwhile
+    // the vector at hand: its number among its row's, its slot and elements.  The next one's are on their way meanwhile, the
+    // elements without waiting for the slot (32768 rows of 8 heads of 128: 43.4 us, 42.4 so)
     uint4 next[kPieces];
-    int64_t next_at = -1;
-    bool next_v = false;
-    auto fetch = [&](int64_t i) {
-        next_at = -1;
-        if (i >= n) return;
-        const int64_t r = n <= 0xFFFFFFFFll ? (int64_t)((uint32_t)i / (uint32_t)a.units) : i / a.units;
-        const int vec = (int)(i - r * a.units) * kPerWarp + sub;
-        const int64_t slot = a.row_of(r);
-        if (slot < 0 || vec >= 2 * n_kv) return;
-        next_v = vec >= n_kv;
-        const int h = next_v ? vec - n_kv : vec;
-        next_at = h * a.c.n_rows + slot;
-        const X* src = next_v ? static_cast<const X*>(a.v) + r * a.v_row + h * a.v_head
+    int next_vec = 0, next_slot = -1;
+    auto fetch = [&](int64_t r, int unit) {
+        next_slot = -1;
+        next_vec = unit * kPerWarp + sub;
+        if (r >= a.rows || next_vec >= 2 * n_kv) return;
+        next_slot = __ldg(a.row_of.slot + r);
+        const bool is_v = next_vec >= n_kv;
+        const int h = is_v ? next_vec - n_kv : next_vec;
+        const X* src = is_v ? static_cast<const X*>(a.v) + r * a.v_row + h * a.v_head
                               : static_cast<const X*>(a.k) + r * a.k_row + h * a.k_head;
 #pragma unroll
         for (int e = 0; e < kPieces; ++e) next[e] = __ldcs(reinterpret_cast<const uint4*>(src) + l + e * kLanes);
     };
-    int64_t i = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-    fetch(i);
-    for (; i < n; i += n_warps) {
-        const int64_t at = next_at;
-        const bool is_v = next_v;
-        float f[16];
+    // the warp's row and share of it, and the step to its next ones
+    const int64_t first = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
+    int64_t r = first / a.units;
+    int unit = (int)(first - r * a.units);
+    const int64_t r_step = n_warps / a.units;
+    const int unit_step = (int)(n_warps - r_step * a.units);
+    fetch(r, unit);
+    while (r < a.rows) {
+        const int slot_now = next_slot;
+        const bool is_v = next_vec >= n_kv;
+        const int h = is_v ? next_vec - n_kv : next_vec;
+        float f[16];                                        // the elements (bfloat16: less them, see divide_pair)
         float amax = 0.0f;
+        uint32_t most = 0;                                  // bfloat16: largest magnitudes of the even and odd elements, signed
 #pragma unroll
         for (int e = 0; e < kPieces; ++e) {
             const uint32_t x[4] = {next[e].x, next[e].y, next[e].z, next[e].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if constexpr (sizeof(X) == 2) {
-                    f[8 * e + 2 * j] = __uint_as_float(x[j] << 16);
-                    f[8 * e + 2 * j + 1] = __uint_as_float(x[j] & 0xFFFF0000u);
+                    asm("max.xorsign.abs.bf16x2 %0, %0, %1;" : "+r"(most) : "r"(x[j]));
+                    const uint32_t less = x[j] ^ 0x80008000u;
+                    f[8 * e + 2 * j] = __uint_as_float(less << 16);
+                    f[8 * e + 2 * j + 1] = __uint_as_float(less & 0xFFFF0000u);
                 } else {
                     f[4 * e + j] = __uint_as_float(x[j]);
                 }
             }
         }
-        fetch(i + n_warps);
+        r += r_step;
+        unit += unit_step;
+        if (unit >= a.units) {
+            unit -= a.units;
+            ++r;
+        }
+        fetch(r, unit);
+        if constexpr (sizeof(X) == 2) {
+            amax = fmaxf(fabsf(__uint_as_float(most << 16)), fabsf(__uint_as_float(most & 0xFFFF0000u)));
+        } else {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(f[j]));
+            for (int j = 0; j < 16; ++j) amax = fmaxf(amax, fabsf(f[j]));
+        }
 #pragma unroll
         for (int m = kLanes / 2; m >= 1; m >>= 1) amax = fmaxf(amax, __shfl_xor_sync(kFull, amax, m));
-        if (at < 0) continue;                               // (its elements are anything)
+        const int64_t o = a.row_of.checked(slot_now);
+        if (o < 0) continue;                                // (its elements may be anything)
+        const int64_t at = h * a.c.n_rows + o;
         const float s = over_448(amax);
         uint32_t c[4] = {0u, 0u, 0u, 0u};
         if (amax != 0.0f) {
@@ -840,7 +859,7 @@ __global__ void __launch_bounds__(kCodecThreads) append_kv8_kernel(const AppendK
                 for (int j = 0; j < 16; j += 2) divide_pair(f[j], f[j + 1], s, y);
             } else {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) f[j] = __fdiv_rn(f[j], s);
+                for (int j = 0; j < 16; ++j) f[j] = __fdiv_rn(f[j], sizeof(X) == 2 ? -s : s);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) c[j] = e4m3x4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);

@@ -557,14 +557,43 @@ def test_select_ties(kvq, V, K, R):
 
 @pytest.mark.parametrize("V,ld", [(101, None), (4099, None), (50257, None), (50257, 50264), (20000, 20003), (7, None), (33001, 33006)])
 @pytest.mark.parametrize("bf16", [False, True])
-def test_select_equal_beams(kvq, V, ld, bf16):
+@pytest.mark.parametrize("R", [3, 60])
+def test_select_equal_beams(kvq, R, V, ld, bf16):
     """Beams of equal scores and logits, their rows beginning at any place: the lowest beam's candidate stands first."""
     g = np.random.default_rng(V)
-    R, B = 3, 8
+    B = 8
     x = dev(np.repeat((g.standard_normal((R, 1, V)) * 3).astype(np.float32), B, 1))
     x = x.bfloat16() if bf16 else x
     score = np.repeat(-7 * g.random((R, 1)), B, 1).astype(np.float32)
-    check_select(kvq, x, score, None, min(V, 20), ld=ld)
+    check_select(kvq, x, score, None, min(V, 20 if R == 3 else 16), ld=ld)
+
+
+@pytest.mark.parametrize("bf16,ld,K", [(False, 20000, 16), (False, 20001, 7), (True, 20000, 3), (True, 20003, 16), (True, 20008, 13)])
+def test_select_long_rows(kvq, bf16, ld, K):
+    """Many rows of several pieces a warp: random, sorted both ways, few levels, empty stretches, and values of no use."""
+    g = np.random.default_rng(ld + K)
+    B, V = 5, 20000
+    kinds = [(g.standard_normal((B, V)) * 3) for _ in range(60)]
+    kinds[1:13:3] = [np.sort(k, 1) for k in kinds[1:13:3]]
+    kinds[2:14:3] = [np.sort(k, 1)[:, ::-1] for k in kinds[2:14:3]]
+    kinds[15] = np.zeros((B, V))
+    kinds[16] = g.integers(0, 3, (B, V))
+    kinds[17] = np.where(np.arange(V) < 19000, -np.inf, kinds[17])
+    kinds[18] = np.where(np.arange(V) > 50, -np.inf, kinds[18])
+    kinds[19] = np.where(g.random((B, V)) < 0.9997, -np.inf, kinds[19])     # (fewer than K, some of them)
+    kinds[20] = np.full((B, V), -np.inf)
+    kinds[21][2, 19999] = np.nan
+    kinds[22][1, 4100] = np.inf
+    kinds[23] = np.where(g.random((B, V)) < 0.9, -1e9, kinds[23])           # a mask's filler
+    kinds[24] = np.where(np.arange(V) // 4096 % 2 == 0, -3.0e38, kinds[24])
+    kinds[25] = kinds[25] + np.arange(V) * 2.0                              # from below 2^13 to above it
+    kinds[26] = np.cumsum(np.ones((B, V)), 1) * 0.01
+    x = dev(np.stack(kinds).astype(np.float32))
+    x = x.bfloat16() if bf16 else x
+    score = (-10 * g.random((60, B))).astype(np.float32)
+    fin = (g.random((60, B)) < 0.2).astype(int)
+    score[g.random((60, B)) < 0.1] = -np.inf
+    check_select(kvq, x, score, fin, K, ld=ld)
 
 
 def test_select_edges(kvq):
