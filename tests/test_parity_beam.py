@@ -293,6 +293,40 @@ def test_decode_batches_of_short_sequences(kvq, n, kv, most, d, page):
     check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, 0, 1 / math.sqrt(d)), d, most)
 
 
+@pytest.mark.parametrize("lens,page,window", [([700, 90, 1300], 16, 300), ([700, 90, 1300], 20, 300), ([30000, 5], 64, 5000), ([5000, 4100], 48, 1)])
+def test_decode_window_over_freed_pages(kvq, lens, page, window):
+    """Pages that lie ahead of the window as a whole may be gone; nothing is flagged."""
+    c = Cache(lens, 2, 128, page, window)
+    q = queries(len(lens), 6, 128, page)
+    table = c.table.copy()
+    for s, L in enumerate(lens):
+        table[s, :max(0, L - window) // page] = -1
+    st = i32(1)
+    out, lse = decode(kvq, c.problem(kvq, q, window, table=table), st)
+    assert st.item() == 0
+    check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, window, 1 / math.sqrt(128)), 128, max(lens))
+
+
+@pytest.mark.parametrize("most", [2000, 100000, 1 << 30])
+def test_decode_generous_bound(kvq, most):
+    """A bound far above every length: the outcome is that of a close one, up to the parts' order."""
+    lens = [1500, 0, 3, 700]
+    c = Cache(lens, 2, 64, 16, 5)
+    q = queries(4, 10, 64, 6)
+    out, lse = decode(kvq, c.problem(kvq, q, max_seq_len=most))
+    check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, 0, 1 / 8), 64, 1500)
+
+
+@pytest.mark.parametrize("d,heads,L", [(64, 4096, 100), (128, 1000, 700), (256, 333, 50), (64, 24, 5000)])
+def test_decode_many_heads_of_one(kvq, d, heads, L):
+    """One KV head for all query heads: more blocks of heads than CTAs."""
+    lens = [L, L // 2]
+    c = Cache(lens, 1, d, 16, heads)
+    q = queries(2, heads, d, L)
+    out, lse = decode(kvq, c.problem(kvq, q))
+    check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, 0, 1 / math.sqrt(d)), d, L)
+
+
 def test_decode_many_sequences(kvq):
     g = np.random.default_rng(0)
     lens = g.integers(0, 90, 1500)
@@ -1039,6 +1073,19 @@ def test_compact(kvq, n, n_pages, used, in_place):
         k = min(held[s], held[s - 1]) // 2
         table[s, :k] = table[s - 1, :k]
     check_compact(kvq, table, held, n_pages, 16, most=None if n % 2 else n_pages // 2 + 5, in_place=in_place)
+
+
+def test_plans_of_nothing(kvq):
+    """No sequences, no pages, or neither."""
+    check_compact(kvq, np.zeros((0, 4), np.int32), np.zeros(0, np.int32), 20, 16)
+    check_compact(kvq, np.full((3, 4), -1, np.int32), np.zeros(3, np.int32), 0, 16)
+    check_compact(kvq, np.zeros((0, 4), np.int32), np.zeros(0, np.int32), 0, 16)
+    f = Forks(kvq, 3, 4, 0, 16, 1)
+    assert f.fork([2, 0, -1], status=0) == []
+    f = Forks(kvq, 0, 4, 5, 16, 1)
+    kvq.kvq_fork_pages(kvq.make_fork_plan(parent=i32(0), page_size=16, **f.d, **f.lists))
+    torch.cuda.synchronize()
+    assert f.d["n_free"].item() == 5 and np.array_equal(host(f.d["free_list"]), f.free) and f.lists["n_copy"].item() == -7
 
 
 def test_compact_bad_inputs(kvq):
