@@ -183,6 +183,8 @@ _lib = None
 def lib() -> C.CDLL:
     """Load libkvq.so (built by ``__graft_entry__.build()``); raise if it is absent."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -716,9 +718,9 @@ def _kv8_cache(planes):
     """The planes k, v uint8 [n_kv, rows, head_dim] and k_scale, v_scale float32 [n_kv, rows]."""
     import torch
     k, ks, v, vs = planes["k"], planes["k_scale"], planes["v"], planes["v_scale"]
-    kv, n, d = k.shape
+    kv, n, d = shape = k.shape
     two, u8, f32 = (kv, n), torch.uint8, torch.float32
-    if not (k.dtype is u8 and v.dtype is u8 and ks.dtype is f32 and vs.dtype is f32 and v.shape == k.shape and
+    if not (k.dtype is u8 and v.dtype is u8 and ks.dtype is f32 and vs.dtype is f32 and v.shape == shape and
             ks.shape == two and vs.shape == two and k.is_contiguous() and v.is_contiguous() and
             ks.is_contiguous() and vs.is_contiguous()):
         _want("k", k, "uint8", kv, n, d)                       # (names the one at fault)
@@ -738,11 +740,12 @@ def kvq_append_kv8(k, v, slot_map, planes: dict, dev_status=None, stream=None) -
     [rows] (negative: skipped)."""
     import torch
     c = _kv8_cache(planes)
-    rows, kv, d = k.shape
-    kind = WEIGHT_F32 if k.dtype is torch.float32 else WEIGHT_BF16 if k.dtype is torch.bfloat16 else None
+    rows, kv, d = shape = k.shape
+    dtype = k.dtype
+    kind = WEIGHT_BF16 if dtype is torch.bfloat16 else WEIGHT_F32 if dtype is torch.float32 else None
     kr, kh, k1 = k.stride()
     vr, vh, v1 = v.stride()
-    if kind is None or v.dtype is not k.dtype or v.shape != k.shape or kv != c.n_kv or d != c.head_dim or \
+    if kind is None or v.dtype is not dtype or v.shape != shape or kv != c.n_kv or d != c.head_dim or \
             (rows and (k1 != 1 or v1 != 1)):
         raise ValueError(f"k, v must be [rows, {c.n_kv}, {c.head_dim}], both float32 or both bfloat16")
     if rows <= 1:                                          # (the stride of a single row or head is arbitrary)
