@@ -1088,6 +1088,65 @@ def test_plans_of_nothing(kvq):
     assert f.d["n_free"].item() == 5 and np.array_equal(host(f.d["free_list"]), f.free) and f.lists["n_copy"].item() == -7
 
 
+def test_two_streams(kvq):
+    """Appends, selections and compactions of two problems at once, each over and over on a stream of its own."""
+    def append(i):
+        pl, rows = new_planes(4, 5000, 128), 3000 + 1000 * i
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(i)
+        k, v = (torch.randn(rows, 4, 128, device="cuda", generator=gen).bfloat16() for _ in range(2))
+        slot = torch.randperm(5000, device="cuda", generator=gen)[:rows].int()
+        return lambda: kvq.kvq_append_kv8(k, v, slot, pl), list(pl.values())
+
+    def select(i):
+        R, B, V, K = 20, 4, 30000 + 77 * i, 8
+        gen = torch.Generator(device="cuda")
+        gen.manual_seed(i)
+        x = torch.randn(R, B, V, device="cuda", generator=gen)
+        out = [torch.zeros(R, K, device="cuda"), i32(R, K), i32(R, K)]
+        p = kvq.make_beam_problem(logits=x, score=torch.randn(R, B, device="cuda", generator=gen), out_score=out[0], out_token=out[1],
+                                  out_parent=out[2])
+        ws = scratch(kvq.kvq_beam_select_workspace(p))
+        return lambda: kvq.kvq_beam_select(p, ws), out
+
+    def compact(i):
+        n, n_pages = 50, 9000 + 60000 * i
+        g = np.random.default_rng(i)
+        table = g.permutation(n_pages)[:n * 60].reshape(n, 60).astype(np.int32)
+        out = [i32(n, 60), i32(n_pages), i32(1), i32(1), *(i32(n_pages // 2) for _ in range(3)), i32(1)]
+        p = kvq.make_compact_plan(block_table=dev(table), n_held=dev(g.integers(0, 61, n).astype(np.int32)), new_table=out[0], free_list=out[1],
+                                  n_free=out[2], n_used=out[3], page_size=16, copy_src=out[4], copy_dst=out[5], copy_rows=out[6],
+                                  n_copy=out[7])
+        ws = scratch(kvq.kvq_compact_pages_workspace(p))
+        return lambda: kvq.kvq_compact_pages(p, ws), out
+
+    for make in (append, select, compact):
+        calls, outs = zip(*(make(i) for i in range(2)))
+        want = []
+        for call, out in zip(calls, outs):
+            call()
+            torch.cuda.synchronize()
+            want.append([t.clone() for t in out])
+            for t in out:
+                t.zero_()
+        streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+        torch.cuda.synchronize()
+        for _ in range(40):
+            for call, s in zip(calls, streams):
+                with torch.cuda.stream(s):
+                    call()
+        torch.cuda.synchronize()
+        for out, ref in zip(outs, want):
+            for t, r in zip(out, ref):
+                same = t.view(torch.int32) if t.dtype == torch.float32 else t
+                assert torch.equal(same, r.view(torch.int32) if r.dtype == torch.float32 else r) or make is append
+        if make is append:                                   # (rows without a slot keep what was there)
+            for out, ref in zip(outs, want):
+                for t, r in zip(out, ref):
+                    written = (r != 0x7F) if r.dtype == torch.uint8 else ~r.isnan()
+                    assert bool((t == r)[written].all())
+
+
 def test_compact_bad_inputs(kvq):
     table = np.array([[5, -1, 9, 3], [7, 10, 2**31 - 1, 0], [1, 2, 4, 6]], np.int32)
     check_compact(kvq, table, np.array([4, 3, 9], np.int32), 10, 4)
