@@ -37,7 +37,8 @@ constexpr int kGroup = 16;               // rows of an instruction's tile
 constexpr int kHeads = 8;                // query heads of an n block
 constexpr int kIdle = 1;                 // see unit_steps
 constexpr int kTeam = 8;                 // CTAs of a short unit at most (what any cluster may have)
-constexpr int kTeamSteps = 4;            // places that each takes at most
+constexpr int kTeamSteps = 4;            // places that each takes at most, or where the line's CTAs take nearly as many:
+constexpr int kTeamMost = 8, kTeamMore = 5;      // at most, and more than those
 constexpr float kSlack = 10.0f;          // log2 by which a weight may pass 1 before the reference moves
 
 struct Kv8Args {
@@ -154,7 +155,7 @@ __host__ __device__ constexpr int first_group(int x) { return x & ~(kGroup - 1);
 // CTAs, kIdle places for what it costs to begin one; units follow one another, the KV heads of a sequence side by
 // side.  CTA c of n has total / n places, the first total % n one more: the same work for all, whatever the lengths,
 // and a partial result only where a cut falls into a unit (64 ragged sequences, 512 to 32768 rows: 198 us with splits
-// of one size, which pay for their beginnings, 186 us on the line).
+// of one size, which pay for their beginnings, 182 us on the line).
 template <int STEP>
 __device__ __forceinline__ int unit_steps(const int2& seen) { return (seen.y - first_group(seen.x) + STEP - 1) / STEP; }
 template <int STEP>
@@ -190,9 +191,9 @@ struct Kv8Shape {
 // One CTA: a stretch of the line for one block of up to 8 NB query heads of the KV heads on it.  In each unit its
 // warps take the tiles in turn, each with a softmax of its own, and are joined at the end.  TEAM: units are short; each
 // one has a cluster of a.team CTAs, which take team_rows of its rows each and join their results through shared
-// memory, so that there is no second launch (1024 rows, 8 KV heads x 4: 10.3 us on the line, 8.3 so).  GROUPED: 16 rows from a
-// multiple of 16 are neighbours in the pool (pages of a multiple of 16 rows, or no table), so that a group has one
-// address; otherwise every row has its own.
+// memory, so that there is no second launch (8 KV heads x 4, 1024 rows: 8.3 us on the line, 6.1 so; 7 sequences of 3000: 19.5
+// and 15.3; 16 of 2048: 23.8 and 19.2).  GROUPED: 16 rows from a multiple of 16 are neighbours in the pool (pages of a
+// multiple of 16 rows, or no table), so that a group has one address; otherwise every row has its own.
 template <int D, int NB, int R, int W, int C, bool GROUPED, bool TEAM>
 __global__ void __launch_bounds__(32 * W, C)
 kv8_decode_kernel(const Kv8Args a)
@@ -793,7 +794,8 @@ kv8_decode_kernel(const Kv8Args a)
 // The parts of a unit joined, a CTA a query head: groups of D / 4 threads take the parts in turn, four of them in
 // flight, with a softmax each, and are joined in their order.  The first part is what CTA c left, the others are
 // what the CTAs behind it found begun.  T threads: 512 where units have many parts (131072 rows in 57 parts: the call
-// 55.8 us, with 128 threads 61.4), 128 where they have few (64 ragged sequences: 186 us, with 512 threads 201).
+// 52.4 us, with 256 threads 52.8, with 128 threads 5 more), 128 where they have few (64 ragged sequences: 182 us, with 512
+// threads 8% more).
 template <int D, int T>
 __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_heads)
 {
@@ -909,10 +911,12 @@ struct Kv8Kind {
         const int64_t most = p.window > 0 ? std::min<int64_t>((int64_t)p.window + kGroup - 1, p.max_seq_len) : p.max_seq_len;
         const int64_t steps = (most + kStep - 1) / kStep, units = (int64_t)p.n_seq * p.cache.n_kv;
         const int64_t slots = (int64_t)C * sm_count();
-        // units that a cluster each can take in a few places, all of them at once
-        q.team = (int)std::min<int64_t>(std::min<int64_t>(kTeam, steps), units > 0 ? slots / (units * q.n_hb) : 0);
-        if (q.team > 0 && steps <= q.team * kTeamSteps) {
-            const int64_t each = (steps + q.team - 1) / q.team;
+        // units that a cluster each can take in a few places, all of them at once (clusters of any size find room for
+        // 17 CTAs of 20: 64 clusters of 7 took 29 us where 448 CTAs of the line took 23)
+        const int64_t room = slots * 17 / 20;
+        q.team = (int)std::min<int64_t>(std::min<int64_t>(kTeam, steps), units > 0 ? room / (units * q.n_hb) : 0);
+        const int64_t each = q.team > 0 ? (steps + q.team - 1) / q.team : 0;
+        if (q.team > 0 && (each <= kTeamSteps || (each <= kTeamMost && each <= units * q.n_hb * steps / slots + kTeamMore))) {
             q.team = (int)((steps + each - 1) / each);
             q.team_rows = (int)each * kStep;
             return;
