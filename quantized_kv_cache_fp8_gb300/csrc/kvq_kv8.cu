@@ -185,14 +185,22 @@ struct Kv8Shape {
     static constexpr int kHb = NB * kHeads;                 // heads of a CTA
     static constexpr int kStep = W * R;                     // rows of a place of the line
     // the merge of the warps: weighted rows, then references and sums; then the same of the CTA, for its cluster
-    static constexpr int kSmem = (W + 1) * kHb * (D + 2) * 4;
+    static constexpr int kStride = D == 64 ? D : D + 4;     // of a head's weighted rows
+    static constexpr int kSmem = (W * (kStride + 2) + D + 2) * kHb * 4;
+    // Where dims d, d + 1 of head h are in those: pairs turn within 16 dims by the 16's number, or (64 dims) within 8 by the
+    // head's, so that the lanes that write together meet no bank twice (16 sequences of 1024 rows: 13.2 us with the rows as
+    // they are, 12.7 so)
+    static __device__ __forceinline__ int place(int h, int d)
+    {
+        return D == 64 ? h * kStride + (d & ~7) + 2 * ((d / 2 + h / 2) & 3) : h * kStride + (d & ~15) + 2 * ((d / 2 + d / 16) & 7);
+    }
 };
 
 // One CTA: a stretch of the line for one block of up to 8 NB query heads of the KV heads on it.  In each unit its
 // warps take the tiles in turn, each with a softmax of its own, and are joined at the end.  TEAM: units are short; each
 // one has a cluster of a.team CTAs, which take team_rows of its rows each and join their results through shared
-// memory, so that there is no second launch (8 KV heads x 4, 1024 rows: 8.3 us on the line, 6.1 so; 7 sequences of 3000: 19.5
-// and 15.3; 16 of 2048: 23.8 and 19.2).  GROUPED: 16 rows from a multiple of 16 are neighbours in the pool (pages of a
+// memory, so that there is no second launch (8 KV heads x 4, 1024 rows: 8.3 us on the line, 6.0 so; 7 sequences of 3000: 19.5
+// and 14.9; 16 of 2048: 23.8 and 18.8).  GROUPED: 16 rows from a multiple of 16 are neighbours in the pool (pages of a
 // multiple of 16 rows, or no table), so that a group has one address; otherwise every row has its own.
 template <int D, int NB, int R, int W, int C, bool GROUPED, bool TEAM>
 __global__ void __launch_bounds__(32 * W, C)
@@ -673,8 +681,8 @@ kv8_decode_kernel(const Kv8Args a)
 
         // ---- the warps are joined: weighted rows relative to ref, then references and sums
         __syncthreads();
-        float* mo = reinterpret_cast<float*>(smem);             // [warp][head][D]
-        float* ml = mo + W * Sh::kHb * D;                       // [warp][head][2]
+        float* mo = reinterpret_cast<float*>(smem);             // [warp][head][kStride]
+        float* ml = mo + W * Sh::kHb * Sh::kStride;             // [warp][head][2]
         float* to = ml + W * Sh::kHb * 2;                       // [head][D], of the CTA
         float* tl = to + Sh::kHb * D;                           // [head][2]
 #pragma unroll
@@ -687,11 +695,11 @@ kv8_decode_kernel(const Kv8Args a)
                 for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
                 // (exp2f: with scales below 2^-126 the factor may be subnormal)
                 const float f = wtop[nb][e] == -INFINITY ? (l != l ? l : 0.0f) : exp2f(wref[nb][e] - ref[nb][e]);
-                float* dst = mo + (warp * Sh::kHb + h) * D;
+                float* dst = mo + warp * Sh::kHb * Sh::kStride;
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                     const int d = D == 64 ? 8 * g + 2 * b : 128 * (b / 8) + 16 * g + 2 * (b % 8);
-                    *reinterpret_cast<float2*>(dst + d) = make_float2(o[nb][b][e] * f, o[nb][b][e + 2] * f);
+                    *reinterpret_cast<float2*>(dst + Sh::place(h, d)) = make_float2(o[nb][b][e] * f, o[nb][b][e + 2] * f);
                 }
                 if (g == 0) {
                     // a head without a row: reference -inf, sum 0; one that holds a NaN keeps it in the sum
@@ -711,12 +719,13 @@ kv8_decode_kernel(const Kv8Args a)
             for (int w = 0; w < W; ++w) {
                 const float wl = ml[(w * Sh::kHb + h) * 2 + 1];
                 const float f = part_weight(make_float2(ml[(w * Sh::kHb + h) * 2], wl), base);
-                const float4 y = *reinterpret_cast<const float4*>(mo + (w * Sh::kHb + h) * D + d);
+                const float2 y0 = *reinterpret_cast<const float2*>(mo + w * Sh::kHb * Sh::kStride + Sh::place(h, d));
+                const float2 y1 = *reinterpret_cast<const float2*>(mo + w * Sh::kHb * Sh::kStride + Sh::place(h, d + 2));
                 l += wl * f;
-                acc.x = fmaf(y.x, f, acc.x);
-                acc.y = fmaf(y.y, f, acc.y);
-                acc.z = fmaf(y.z, f, acc.z);
-                acc.w = fmaf(y.w, f, acc.w);
+                acc.x = fmaf(y0.x, f, acc.x);
+                acc.y = fmaf(y0.y, f, acc.y);
+                acc.z = fmaf(y1.x, f, acc.z);
+                acc.w = fmaf(y1.y, f, acc.w);
             }
             const int64_t row = head0 + h;
             if constexpr (TEAM) {
@@ -740,7 +749,7 @@ kv8_decode_kernel(const Kv8Args a)
     if constexpr (TEAM) {
         // ---- the CTAs are joined, in their order: each one a share of the elements
         const cg::cluster_group team = cg::this_cluster();
-        const float *to = reinterpret_cast<const float*>(smem) + W * Sh::kHb * (D + 2), *tl = to + Sh::kHb * D;
+        const float *to = reinterpret_cast<const float*>(smem) + W * Sh::kHb * (Sh::kStride + 2), *tl = to + Sh::kHb * D;
         const int64_t head0 = (int64_t)s * p.n_qh + kv * a.group + hb * Sh::kHb;
         team.sync();
         for (int i = (int)team.block_rank() * Sh::kThreads + threadIdx.x; i < heads * (D / 4); i += a.team * Sh::kThreads) {
