@@ -14,6 +14,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "kvq_internal.cuh"
 
@@ -739,10 +740,12 @@ append_mla_kernel(const X* __restrict__ c_lat, int64_t ldx, const X* __restrict_
 // 512 / D of a row's 2 n_kv vectors (K's heads, then V's) at once, with the next ones on their way.
 // Bound by the rows' bytes (a division a vector and a correction a quotient, two quotients at a time; what is done once a
 // lane is shared by its 16 elements): 32768 rows of 8 heads of 128 take 64 us with a row and a division for every vector, 52 with
-// 8 elements a lane, 42 so (4.8 TB/s), and 41 without the quotients, 37 without the codes' stores, so that it is the mix of
-// reads a row apart and writes to 16 planes that bounds it.  A ring of four vectors a warp in shared memory takes 39.7, but 37 rows 4.8
-// instead of 4.4.
+// 8 elements a lane, 39 with 16 and the next vector in registers, 36 with a ring of them (5.6 TB/s).  Without the
+// quotients it is 1 us less, without the codes' stores 5: reads a row apart, mixed with writes to 16 planes.
 // ------------------------------------------------------------------------------------
+// A warp's shares from which on append_kv8_kernel has a ring (rows of 8 heads of 128, without and with: 8000 bfloat16 rows,
+// 6.6 shares, 11.2 and 11.8 us; 16000 rows 20.1 and 19.7; 32768 rows 39.2 and 36.0; float32 14.5 and 15.8, 29.5 and 27.3)
+constexpr int kRingShares = 12;
 struct AppendKv8Args {
     const void *k, *v;
     int64_t k_row, k_head, v_row, v_head;    // strides in elements
@@ -776,43 +779,74 @@ __device__ __forceinline__ void divide_pair(float& a, float& b, float s, float y
     asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(q));
 }
 
-template <int D, typename X>
-__global__ void __launch_bounds__(kCodecThreads) append_kv8_kernel(const AppendKv8Args a)
+// RING: a warp's vectors come through a ring in shared memory, each lane's own pieces of them, some vectors ahead; else in
+// registers, one ahead.  Either way the elements are fetched without waiting for their slots, which come one ahead.
+template <int D, typename X, bool RING>
+__global__ void __launch_bounds__(kCodecThreads, 4) append_kv8_kernel(const AppendKv8Args a)
 {
     constexpr int kLanes = D / 16, kPerWarp = 32 / kLanes;
     constexpr int kElems = 16 / (int)sizeof(X), kPieces = 16 / kElems;      // a piece: 16 bytes of a row
+    constexpr int kStages = RING ? 8 / kPieces : 1;
+    __shared__ uint4 s_ring[RING ? kCodecWarps : 1][kStages][kPieces][32];
+    auto* const ring = s_ring[RING ? threadIdx.x >> 5 : 0];
     const int lane = threadIdx.x & 31, sub = lane / kLanes, l = lane % kLanes;
-    const int64_t n_warps = ((int64_t)gridDim.x * blockDim.x) >> 5;
     const int n_kv = a.c.n_kv;
     grid_dependency_wait();
     grid_dependents_launch();
-    // the vector at hand: its number among its row's, its slot and elements.  The next one's are on their way meanwhile, the
-    // elements without waiting for the slot (32768 rows of 8 heads of 128: 43.4 us, 42.4 so)
-    uint4 next[kPieces];
-    int next_vec = 0, next_slot = -1;
-    auto fetch = [&](int64_t r, int unit) {
-        next_slot = -1;
-        next_vec = unit * kPerWarp + sub;
-        if (r >= a.rows || next_vec >= 2 * n_kv) return;
-        next_slot = __ldg(a.row_of.slot + r);
-        const bool is_v = next_vec >= n_kv;
-        const int h = is_v ? next_vec - n_kv : next_vec;
-        const X* src = is_v ? static_cast<const X*>(a.v) + r * a.v_row + h * a.v_head
-                              : static_cast<const X*>(a.k) + r * a.k_row + h * a.k_head;
-#pragma unroll
-        for (int e = 0; e < kPieces; ++e) next[e] = __ldcs(reinterpret_cast<const uint4*>(src) + l + e * kLanes);
+    // a row and a warp's share of it: the warp's first, and the step to its next ones
+    struct Share {
+        int64_t r;
+        int unit;
     };
-    // the warp's row and share of it, and the step to its next ones
-    const int64_t first = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
-    int64_t r = first / a.units;
-    int unit = (int)(first - r * a.units);
-    const int64_t r_step = n_warps / a.units;
-    const int unit_step = (int)(n_warps - r_step * a.units);
-    fetch(r, unit);
-    while (r < a.rows) {
-        const int slot_now = next_slot;
-        const bool is_v = next_vec >= n_kv;
-        const int h = is_v ? next_vec - n_kv : next_vec;
+    const int first = blockIdx.x * kCodecWarps + (threadIdx.x >> 5), first_r = first / a.units;
+    const int n_warps = gridDim.x * kCodecWarps, r_step = n_warps / a.units, unit_step = n_warps - r_step * a.units;
+    auto advance = [&](Share& t) {
+        t.r += r_step;
+        t.unit += unit_step;
+        if (t.unit >= a.units) {
+            t.unit -= a.units;
+            ++t.r;
+        }
+    };
+    auto vec_of = [&](const Share& t) { return t.unit * kPerWarp + sub; };      // of the row's 2 n_kv vectors
+    auto there = [&](const Share& t) { return t.r < a.rows && vec_of(t) < 2 * n_kv; };
+    Share now{first_r, first - first_r * a.units}, ahead = now;
+    uint4 next[kPieces];
+    auto fetch = [&](int stage) {
+        if (there(ahead)) {
+            const int vec = vec_of(ahead);
+            const bool is_v = vec >= n_kv;
+            const int h = is_v ? vec - n_kv : vec;
+            const X* src = is_v ? static_cast<const X*>(a.v) + ahead.r * a.v_row + h * a.v_head
+                                : static_cast<const X*>(a.k) + ahead.r * a.k_row + h * a.k_head;
+#pragma unroll
+            for (int e = 0; e < kPieces; ++e) {
+                const uint4* const from = reinterpret_cast<const uint4*>(src) + l + e * kLanes;
+                if constexpr (RING)
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(&ring[stage][e][lane])),
+                                 "l"(from)
+                                 : "memory");
+                else
+                    next[e] = __ldcs(from);
+            }
+        }
+        if constexpr (RING) asm volatile("cp.async.commit_group;" ::: "memory");
+        advance(ahead);
+    };
+    auto slot_at = [&](const Share& t) { return there(t) ? __ldg(a.row_of.slot + t.r) : -1; };
+    int next_slot = slot_at(now);
+#pragma unroll
+    for (int st = 0; st < (RING ? kStages - 1 : 1); ++st) fetch(st);
+    for (int stage = 0; now.r < a.rows; stage = stage + 1 == kStages ? 0 : stage + 1) {
+        if constexpr (RING) {
+            fetch(stage == 0 ? kStages - 1 : stage - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+#pragma unroll
+            for (int e = 0; e < kPieces; ++e) next[e] = ring[stage][e][lane];
+        }
+        const int vec = vec_of(now), slot_now = next_slot;
+        const bool is_v = vec >= n_kv;
+        const int h = is_v ? vec - n_kv : vec;
         float f[16];                                        // the elements (bfloat16: less them, see divide_pair)
         float amax = 0.0f;
         uint32_t most = 0;                                  // bfloat16: largest magnitudes of the even and odd elements, signed
@@ -831,13 +865,9 @@ __global__ void __launch_bounds__(kCodecThreads) append_kv8_kernel(const AppendK
                 }
             }
         }
-        r += r_step;
-        unit += unit_step;
-        if (unit >= a.units) {
-            unit -= a.units;
-            ++r;
-        }
-        fetch(r, unit);
+        if constexpr (!RING) fetch(0);
+        advance(now);
+        next_slot = slot_at(now);
         if constexpr (sizeof(X) == 2) {
             amax = fmaxf(fabsf(__uint_as_float(most << 16)), fabsf(__uint_as_float(most & 0xFFFF0000u)));
         } else {
@@ -1668,9 +1698,13 @@ cudaError_t launch_append_kv8(const void* k, int64_t k_row, int64_t k_head, cons
     const int per = 512 / c.head_dim, vecs = 2 * c.n_kv;              // vectors of a row that a warp takes at once
     const AppendKv8Args a{k, v, k_row, k_head, v_row, v_head, rows, (vecs + per - 1) / per, RowSlot{slot, c.n_rows, dev_status}, c};
     const int64_t g = std::max<int64_t>(1, std::min<int64_t>((rows * a.units + kCodecWarps - 1) / kCodecWarps, (int64_t)sm_count() * 4));
-    const auto kernel = c.head_dim == 64    ? bf16 ? append_kv8_kernel<64, __nv_bfloat16> : append_kv8_kernel<64, float>
-                        : c.head_dim == 128 ? bf16 ? append_kv8_kernel<128, __nv_bfloat16> : append_kv8_kernel<128, float>
-                                            : bf16 ? append_kv8_kernel<256, __nv_bfloat16> : append_kv8_kernel<256, float>;
+    auto kernel_of = [&](auto ring) {
+        constexpr bool R = decltype(ring)::value;
+        return c.head_dim == 64    ? bf16 ? append_kv8_kernel<64, __nv_bfloat16, R> : append_kv8_kernel<64, float, R>
+               : c.head_dim == 128 ? bf16 ? append_kv8_kernel<128, __nv_bfloat16, R> : append_kv8_kernel<128, float, R>
+                                   : bf16 ? append_kv8_kernel<256, __nv_bfloat16, R> : append_kv8_kernel<256, float, R>;
+    };
+    const auto kernel = rows * a.units >= kRingShares * g * kCodecWarps ? kernel_of(std::true_type()) : kernel_of(std::false_type());
     return launch_dependent(kernel, dim3((unsigned)g), dim3(kCodecThreads), 0, s, a);
 }
 

@@ -107,6 +107,13 @@ def test_append_bytes(kvq, orc, d, bf16, rows, kv, layout):
         assert np.array_equal(host(pl[name + "_scale"]).view(np.uint32), want[1].view(np.uint32))
 
 
+@pytest.mark.parametrize("d,rows,kv,layout", [(64, 15001, 13, "fused"), (128, 12003, 9, "plain"), (256, 19990, 3, "fused")])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_append_bytes_of_many_rows(kvq, orc, d, bf16, rows, kv, layout):
+    """As many that a warp takes a dozen vectors or more in turn."""
+    test_append_bytes(kvq, orc, d, bf16, rows, kv, layout)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("bf16", [False, True])
 def test_append_what_is_no_number(kvq, d, bf16):
