@@ -26,7 +26,8 @@ constexpr size_t kPlainSmem = 39 * 1024; // dynamic shared memory that needs no 
 constexpr int kPagesShared = 65536;      // pages whose marks fit the CTAs' shared memory
 // the most that a single CTA and one of a cluster ask for (2 bytes of marks a page, 4 of keepers an own page, a single
 // one's table rows); always this much is allowed, so that calls of several threads do not lower each other's limit
-constexpr int kMostSmemOne = 6 * kPagesOne + 4 * kRowsShared, kMostSmem = 2 * kPagesShared + 4 * kPagesShared / kCluster;
+constexpr int kMostSmemOne = 6 * kPagesOne + 4 * kRowsShared, kMostSmem = 200 * 1024;
+static_assert(2 * kPagesShared + 4 * kPagesShared / kCluster <= kMostSmem, "marks and keepers fit");
 
 __device__ __forceinline__ void flag(uint32_t* status, unsigned bit)
 {
@@ -154,7 +155,7 @@ struct ForkArgs {
     size_t stride;
     int32_t* row;                        // [n_seq][max_pages]: the new tables
     int4* seq;                           // [n_seq], see below
-    int rows_shared;                     // whether the new tables are in shared memory
+    int rows_shared;                     // whether the new tables are in shared memory, a CTA's in its own
 };
 
 template <bool ONE, bool SHARED>
@@ -181,7 +182,9 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
     // of a sequence: parent (-1: none), later its number among the copies (-1: none); rows; last page if held in
     // part (-1: none); pages held before
     int4* const seq = seqs <= kSeqShared ? s_seq - s0 : a.seq;
-    int32_t* const row = ONE && a.rows_shared ? reinterpret_cast<int32_t*>(s_store + 2 * set + (size_t)words.each * 16) : a.row;
+    int32_t* const row = SHARED && a.rows_shared
+                             ? reinterpret_cast<int32_t*>(s_store + 2 * set + (size_t)words.each * 16) - (int64_t)s0 * p.max_pages
+                             : a.row;
     unsigned bits = 0;
     const int n_free0 = p.n_free[0], n_free = min(max(n_free0, 0), p.n_pages);
     if (n_free != n_free0) bits |= KVQ_DEV_BAD_INDEX;
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
         given[i] = held & ~kept;
         mine += __popc(held & ~kept);
     }
-    (void)block_scan(mine, s_warp, &here);
+    const int mine_to = block_scan(mine, s_warp, &here);
     int above = 0, total = here, want = s_copies, copies0 = 0;
     if constexpr (!ONE) {
         if (tid == 0) s_given = here;
@@ -311,11 +314,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
         }
     }
     // the highest id first
-    for (int top = w1; here > 0 && top > w0; top -= T) {
-        const int i = top - 1 - tid;
-        const uint32_t g = i >= w0 ? given[i] : 0;
-        int sum;
-        int at = n_free + above + block_scan(__popc(g), s_warp, &sum) - __popc(g);
+    auto push = [&](int i, uint32_t g, int at) {
 #pragma unroll
         for (int b = 3; b >= 0; --b)
             if (g >> (8 * b) & 1) {
@@ -323,7 +322,17 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) fork_pages_kerne
                 else bits |= KVQ_DEV_BAD_PAGE;
                 ++at;
             }
-        above += sum;
+    };
+    if (w1 - w0 <= T) {                                     // (a word a thread: the scan is done)
+        if (mine > 0) push(w0 + tid, given[w0 + tid], n_free + above + here - mine_to);
+    } else {
+        for (int top = w1; here > 0 && top > w0; top -= T) {
+            const int i = top - 1 - tid;
+            const uint32_t g = i >= w0 ? given[i] : 0;
+            int sum;
+            push(i, g, n_free + above + block_scan(__popc(g), s_warp, &sum) - __popc(g));
+            above += sum;
+        }
     }
     team.sync();
 
@@ -444,15 +453,15 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) compact_pages_ke
     };
     auto holes_of = [&](int i) { return ~marks[i] & below(i); };
     auto moves_of = [&](int i) { return marks[i] & ~below(i); };
-    int hole_at = 0, move_at = 0, total;
+    int hole_at = 0, move_at = 0, total, my_hole, my_move;
     {
         int holes = 0, moves = 0, sum_h, sum_m;
         for (int i = w0 + tid; i < w1; i += T) {
             holes += __popc(holes_of(i));
             moves += __popc(moves_of(i));
         }
-        (void)block_scan(holes, s_warp, &sum_h);
-        (void)block_scan(moves, s_warp, &sum_m);
+        my_hole = block_scan(holes, s_warp, &sum_h) - holes;
+        my_move = block_scan(moves, s_warp, &sum_m) - moves;
         total = sum_m;
         if constexpr (!ONE) {
             if (tid == 0) {
@@ -471,12 +480,7 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) compact_pages_ke
             }
         }
     }
-    for (int low = w0; low < w1; low += T) {
-        const int i = low + tid;
-        const uint32_t hole = i < w1 ? holes_of(i) : 0, move = i < w1 ? moves_of(i) : 0;
-        int sum_h, sum_m;
-        int h = hole_at + block_scan(__popc(hole), s_warp, &sum_h) - __popc(hole);
-        int m = move_at + block_scan(__popc(move), s_warp, &sum_m) - __popc(move);
+    auto list = [&](int i, uint32_t hole, uint32_t move, int h, int m) {
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             if (hole >> (8 * b) & 1) p.copy_dst[h++] = i * 4 + b;
@@ -485,8 +489,19 @@ __global__ void __launch_bounds__(ONE ? kThreadsOne : kThreads) compact_pages_ke
                 a.rank[i * 4 + b] = m++;
             }
         }
-        hole_at += sum_h;
-        move_at += sum_m;
+    };
+    if (w1 - w0 <= T) {                                     // (a word a thread: the scans are done)
+        if (w0 + tid < w1) list(w0 + tid, holes_of(w0 + tid), moves_of(w0 + tid), hole_at + my_hole, move_at + my_move);
+    } else {
+        for (int low = w0; low < w1; low += T) {
+            const int i = low + tid;
+            const uint32_t hole = i < w1 ? holes_of(i) : 0, move = i < w1 ? moves_of(i) : 0;
+            int sum_h, sum_m;
+            const int h = hole_at + block_scan(__popc(hole), s_warp, &sum_h) - __popc(hole);
+            list(i, hole, move, h, move_at + block_scan(__popc(move), s_warp, &sum_m) - __popc(move));
+            hole_at += sum_h;
+            move_at += sum_m;
+        }
     }
     for (int i = me; i < p.max_copy; i += all) {
         p.copy_rows[i] = i < total ? p.page_size : -1;
@@ -609,6 +624,7 @@ size_t up(size_t n) { return (n + 255) / 256 * 256; }
 struct TeamPlan {
     bool one = false, shared = false;
     size_t bytes = 0;                    // of a CTA's marks and keepers
+    size_t rows = 0;                     // of its sequences' new tables, where they are in shared memory
 };
 
 TeamPlan plan_team(int n_seq, int max_pages, int n_pages, int sets, bool keepers)
@@ -619,15 +635,19 @@ TeamPlan plan_team(int n_seq, int max_pages, int n_pages, int sets, bool keepers
     const Words w(n_pages, t.one ? 1 : kCluster);
     t.bytes = sets * w.bytes() + (keepers ? (size_t)w.each * 16 : 0);
     t.bytes = (t.bytes + 15) / 16 * 16;
+    if (keepers && t.shared) {
+        const size_t rows = (size_t)(t.one ? n_seq : (n_seq + kCluster - 1) / kCluster) * max_pages * 4;
+        t.rows = t.one || t.bytes + rows <= (size_t)kMostSmem ? rows : 0;
+    }
     return t;
 }
 
 template <typename Args>
-cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(Args), const TeamPlan& t, size_t rows,
-                        const Args& a, cudaStream_t s)
+cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(Args), const TeamPlan& t, const Args& a,
+                        cudaStream_t s)
 {
+    const size_t smem = t.shared ? t.bytes + t.rows : 0;
     if (t.one) {
-        const size_t smem = t.bytes + rows;
         if (smem > kPlainSmem) {
             cudaError_t e = cudaFuncSetAttribute(one, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmemOne);
             if (e != cudaSuccess) return e;
@@ -638,9 +658,9 @@ cudaError_t launch_team(void (*one)(Args), void (*shared)(Args), void (*global)(
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(kCluster);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = t.shared ? t.bytes : 0;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
-    if (cfg.dynamicSmemBytes > kPlainSmem) {
+    if (smem > kPlainSmem) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem);
         if (e != cudaSuccess) return e;
     }
@@ -727,14 +747,14 @@ size_t lay_out(const kvq_fork_plan& p, uint8_t* ws, ForkArgs* a)
     Layout l;
     const TeamPlan t = plan_team(p);
     const size_t n = (size_t)p.n_seq;
-    const size_t row = l.take(t.one ? 16 : n * p.max_pages * 4), seq = l.take(t.one ? 16 : n * 16);
+    const size_t row = l.take(t.rows ? 16 : n * p.max_pages * 4), seq = l.take(t.one ? 16 : n * 16);
     const size_t store = l.take(t.shared ? 0 : t.bytes * kCluster);
     if (a) {
         a->row = reinterpret_cast<int32_t*>(ws + row);
         a->seq = reinterpret_cast<int4*>(ws + seq);
         a->store = ws + store;
         a->stride = t.bytes;
-        a->rows_shared = t.one;
+        a->rows_shared = t.rows > 0;
     }
     return l.bytes;
 }
@@ -778,7 +798,7 @@ int kvq_fork_pages(const kvq_fork_plan* p, void* workspace, size_t ws_bytes, uin
     a.status = dev_status;
     lay_out(*p, static_cast<uint8_t*>(workspace), &a);
     return cuda_status(launch_team(fork_pages_kernel<true, true>, fork_pages_kernel<false, true>, fork_pages_kernel<false, false>,
-                                   plan_team(*p), (size_t)p->n_seq * p->max_pages * 4, a, (cudaStream_t)stream), E);
+                                   plan_team(*p), a, (cudaStream_t)stream), E);
 }
 
 size_t kvq_compact_pages_workspace(const kvq_compact_plan* p)
@@ -801,7 +821,7 @@ int kvq_compact_pages(const kvq_compact_plan* p, void* workspace, size_t ws_byte
     a.status = dev_status;
     lay_out(*p, static_cast<uint8_t*>(workspace), &a);
     return cuda_status(launch_team(compact_pages_kernel<true, true>, compact_pages_kernel<false, true>,
-                                   compact_pages_kernel<false, false>, plan_team(*p), 0, a, (cudaStream_t)stream), E);
+                                   compact_pages_kernel<false, false>, plan_team(*p), a, (cudaStream_t)stream), E);
 }
 
 int kvq_copy_pages(const kvq_page_copy* d, uint32_t* dev_status, kvq_stream_t stream)
