@@ -626,13 +626,14 @@ kv8_decode_kernel(const Kv8Args a)
                             m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
                             mw = fmaxf(mw, __shfl_xor_sync(kFull, mw, d));
                         }
-                        if (m > top[nb][e] - kSlack) {          // (top is -inf, or the reference and kSlack)
+                        // (a head's own top only: what else brought the warp here must not change the head's bits)
+                        if (m > top[nb][e]) {
                             const float f = top[nb][e] == -INFINITY ? 0.0f : ex2(ref[nb][e] - m);
                             sum[nb][e] *= f;
                             ref[nb][e] = m;
                             top[nb][e] = m + kSlack;
                         }
-                        if (mw > wtop[nb][e] - kSlack) {
+                        if (mw > wtop[nb][e]) {
                             const float f = wtop[nb][e] == -INFINITY ? 0.0f : ex2(wref[nb][e] - mw);
 #pragma unroll
                             for (int b = 0; b < kBlocks; ++b) {

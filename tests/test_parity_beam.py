@@ -443,6 +443,23 @@ def test_decode_nan_queries_stay_in_their_head(kvq, lens):
     assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], lse0[~hit])
 
 
+@pytest.mark.parametrize("lens,kv,page", [([900, 300], 2, 16), ([40000, 0, 1], 2, 64), ([9000, 5001, 77], 1, 20)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_heads_do_not_touch_each_other(kvq, d, lens, kv, page):
+    """A head's bits are the same whatever the others hold: zeros, large queries, a NaN."""
+    c = Cache(lens, kv, d, page, 100 + d)
+    n, H = len(lens), 6 * kv
+    q = queries(n, H, d, 101)
+    clean, lse0 = decode(kvq, c.problem(kvq, q))
+    keep = torch.ones(H, dtype=torch.bool, device="cuda")
+    keep[1] = keep[H - 1] = False
+    for x in (0.0, 30.0, float("nan")):
+        other = q.clone()
+        other[:, ~keep] = queries(n, 2, d, 102) * x
+        out, lse = decode(kvq, c.problem(kvq, other))
+        assert torch.equal(out[:, keep], clean[:, keep]) and torch.equal(lse[:, keep], lse0[:, keep]), x
+
+
 def test_decode_far_rows(kvq):
     """A pool whose rows lie behind 2^32 bytes."""
     d, page = 256, 64
