@@ -520,7 +520,8 @@ kv8_decode_kernel(const Kv8Args a)
                         qf[nb][4 * c + 2 * e + (j >> 1)][j & 1] =
                             pack_h2(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xFFFF0000u) * f);
                 }
-            const float back = pow2(-up) * (p.sm_scale * kLog2e);
+            // (a NaN or an infinity: every score is a NaN, as all of them might be -inf, like those of rows that are not seen)
+            const float back = m >= 0x7F80u ? __int_as_float(0x7FFFFFFF) : pow2(-up) * (p.sm_scale * kLog2e);
             hs[nb][0] = __shfl_sync(kFull, back, 8 * t);
             hs[nb][1] = __shfl_sync(kFull, back, 8 * t + 4);
         }

@@ -460,6 +460,28 @@ def test_decode_heads_do_not_touch_each_other(kvq, d, lens, kv, page):
         assert torch.equal(out[:, keep], clean[:, keep]) and torch.equal(lse[:, keep], lse0[:, keep]), x
 
 
+@pytest.mark.parametrize("lens,kv,page,window", [([1, 0, 2], 2, 16, 0), ([1, 1], 3, 0, 0), ([300, 0, 200], 2, 16, 1), ([700, 90], 1, 20, 3),
+                                                 ([1] * 700, 2, 16, 0), ([40000, 0, 1], 2, 64, 0)])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_decode_infinite_queries(kvq, d, lens, kv, page, window):
+    """A head that holds an infinity gets NaN also where every visible row's score is -inf (one element's codes of one
+    sign), on a cluster and on the line; its neighbours keep their bits."""
+    c = Cache(lens, kv, d, page, 80 + d)
+    c.pl["k"][:, :, 5] = 0x38                                # 1.0, in every row
+    n, H = len(lens), 6 * kv
+    q = queries(n, H, d, 81)
+    clean, lse0 = decode(kvq, c.problem(kvq, q, window))
+    bad, hit = q.clone(), torch.zeros(n, H, dtype=torch.bool, device="cuda")
+    for s in {0, n // 2, n - 1}:
+        bad[s, 1, 5], bad[s, H - 1, 5] = -math.inf, math.inf
+        hit[s, 1] = hit[s, H - 1] = True
+    out, lse = decode(kvq, c.problem(kvq, bad, window))
+    sees = dev(np.asarray(lens) > 0)[:, None].expand(n, H)
+    assert bool(out[hit & sees].isnan().all()) and bool(lse[hit & sees].isnan().all())
+    assert bool((out[~sees] == 0).all()) and bool((lse[~sees] == -math.inf).all())
+    assert torch.equal(out[~hit], clean[~hit]) and torch.equal(lse[~hit], lse0[~hit])
+
+
 def test_decode_far_rows(kvq):
     """A pool whose rows lie behind 2^32 bytes."""
     d, page = 256, 64
