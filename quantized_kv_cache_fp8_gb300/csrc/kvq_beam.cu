@@ -478,18 +478,7 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     const int64_t row0 = (int64_t)blockIdx.x * p.n_beam;
     const int k = p.n_out, per_beam = a.n_chunk * k;
     if (tid == 0) s_n = 0;
-    // (the chunks' kernel lets this one start when all before it has ended, and writes no input: those are read ahead
-    // of the wait)
-    float score = 0.0f;                                     // of beam `tid`
-    int live = 0;
-    if (tid < p.n_beam) {
-        score = p.score[row0 + tid];
-        if (score > -INFINITY && score < INFINITY) live = p.finished && p.finished[row0 + tid] ? 2 : 1;
-        s_base[tid] = make_float2(score, 0.0f);
-        s_live[tid] = (uint8_t)live;
-        if (!(score < INFINITY) && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_VALUE);      // NaN or +inf
-    }
-    __syncthreads();
+    // (the scores and flags too: the step before this one may have written them in place)
     grid_dependency_wait();
     grid_dependents_launch();
     // A list is what a chunk left, descending; `share` threads (a power of two) take its places in turn, so that each
@@ -502,6 +491,17 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     const int b_first = first % p.n_beam;
     auto key_at = [&](int l, int b, int place) { return a.part_key + (row0 + b) * per_beam + (int64_t)(l / p.n_beam) * k + place; };
     const uint64_t head_key = first < lists && place0 < k ? *key_at(first, b_first, place0) : 0;
+    float score = 0.0f;                                     // of beam `tid`
+    int live = 0;
+    if (tid < p.n_beam) {
+        score = p.score[row0 + tid];
+        const bool done = p.finished && p.finished[row0 + tid] != 0;
+        if (score > -INFINITY && score < INFINITY) live = done ? 2 : 1;
+        s_base[tid] = make_float2(score, 0.0f);
+        s_live[tid] = (uint8_t)live;
+        if (!(score < INFINITY) && a.status) atomicOr(a.status, (unsigned)KVQ_DEV_BAD_VALUE);      // NaN or +inf
+    }
+    __syncthreads();
     for (int b = warp; b < p.n_beam; b += kWarps) {
         if (s_live[b] != 1) continue;
         const int64_t at = (row0 + b) * a.n_chunk;

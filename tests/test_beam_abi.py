@@ -2,6 +2,7 @@
 (nothing is launched), the workspaces, the struct layouts and the checks of the binding."""
 import ctypes as C
 import os
+import re
 import subprocess
 
 import pytest
@@ -187,6 +188,18 @@ def test_injected_faults(kvq):
             assert call() == 6, name
     finally:
         kvq.kvq_set_fault(None)
+
+
+@pytest.mark.parametrize("source", ["kvq_kv8.cu", "kvq_beam.cu", "kvq_fork.cu"])
+def test_kernels_read_behind_the_wait(source):
+    """A kernel that may start under the one before it reads no array ahead of its own wait: what earlier kernels wrote is
+    visible to the threads that wait."""
+    text = open(os.path.join(ROOT, "quantized_kv_cache_fp8_gb300", "csrc", source)).read()
+    kernels = re.findall(r"__global__.*?(\w+_kernel)\((.*?)grid_dependency_wait\(\);", text, re.S)
+    assert len(kernels) == text.count("__global__") > 0
+    for name, ahead in kernels:
+        assert "__global__" not in ahead, name               # (its own wait)
+        assert not re.search(r"\b[ap]\.\w+(\.\w+)*\[|__ld\w+\(|atomic", ahead), name
 
 
 def test_struct_layouts(kvq, tmp_path):

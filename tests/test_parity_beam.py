@@ -764,6 +764,30 @@ def test_select_in_place_and_graph(kvq):
     assert fin.any()
 
 
+@pytest.mark.parametrize("R,B,V", [(1, 4, 900), (24, 8, 20000)])
+def test_select_queued_steps_in_place(kvq, R, B, V):
+    """Steps in place, one behind the other without a wait of the host, give the bits of steps one by one."""
+    gen = torch.Generator(device="cuda").manual_seed(R)
+    steps = 50
+    x = torch.randn(steps, R, B, V, device="cuda", generator=gen).bfloat16()
+    x[..., 2] += 3.0
+    runs = []
+    for one_by_one in (True, False, False):
+        score, fin, token, parent = torch.zeros(R, B, device="cuda"), i32(R, B), i32(steps, R, B), i32(steps, R, B)
+        ps = [kvq.make_beam_problem(logits=x[k], score=score, finished=fin, out_score=score, out_token=token[k], out_parent=parent[k],
+                                    out_finished=fin, eos=2, pad=1) for k in range(steps)]
+        ws = scratch(kvq.kvq_beam_select_workspace(ps[0]))
+        torch.cuda.synchronize()
+        for p in ps:
+            kvq.kvq_beam_select(p, ws)
+            if one_by_one:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        runs.append((score, fin, token, parent))
+    for run in runs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(runs[0], run))
+
+
 # --- page forks ----------------------------------------------------------------------------------
 
 def fork_ref(parent, keep, table, held, free, n_free, lens, page, n_pages):
