@@ -739,7 +739,8 @@ int kvq_beam_select(const kvq_beam_problem* p, void* workspace, size_t ws_bytes,
 typedef struct kvq_fork_plan {
     int32_t n_seq;                  /* 0 .. 65535                                       */
     int32_t max_pages, page_size;   /* max_pages: 1 .. 2^20                              */
-    int32_t n_pages;                /* pages of the pool = entries of free_list          */
+    int32_t n_pages;                /* pages of the pool = entries of free_list; 0 .. 2^29, at
+                                       most INT32_MAX rows in all                       */
     const int32_t* parent;          /* device [n_seq]                                   */
     const int32_t* keep_len;        /* device [n_seq] (negative: 0) or NULL              */
     int32_t* block_table;           /* device [n_seq][max_pages], updated                */
@@ -774,8 +775,9 @@ int kvq_fork_pages(const kvq_fork_plan* p, void* workspace, size_t ws_bytes, uin
 typedef struct kvq_compact_plan {
     int32_t n_seq;                  /* 0 .. 65535                                       */
     int32_t max_pages, page_size;   /* max_pages: 1 .. 2^20                              */
-    int32_t n_pages;                /* pages of the pool = entries of free_list          */
-    int32_t max_copy;               /* entries of copy_*: n_pages / 2 or more            */
+    int32_t n_pages;                /* pages of the pool = entries of free_list; 0 .. 2^29, at
+                                       most INT32_MAX rows in all                       */
+    int32_t max_copy;               /* entries of copy_*: n_pages / 2 .. 2^30            */
     const int32_t* block_table;     /* device [n_seq][max_pages]                        */
     const int32_t* n_held;          /* device [n_seq]                                   */
     int32_t* new_table;             /* device [n_seq][max_pages]                        */

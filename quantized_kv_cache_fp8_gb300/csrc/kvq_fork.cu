@@ -15,7 +15,9 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kMaxPages = 1 << 20;
+constexpr int kMaxPages = 1 << 20;       // of a sequence
+// pages of a pool: what a list holds and what is pushed to it, one after the other, is counted in 32 bits; entries of a copy list
+constexpr int kMaxPool = 1 << 29, kMaxCopies = 1 << 30;
 constexpr int kCluster = 8;              // CTAs of a planning kernel where one is not enough
 constexpr int kThreads = 1024;           // of each; of a single one:
 constexpr int kThreadsOne = 512;
@@ -680,6 +682,7 @@ int check_pool(const char* E, int n_seq, int max_pages, int page_size, int n_pag
     if (n_seq < 0 || n_seq > 65535) return set_last_error(KVQ_EINVAL, "%s: n_seq outside [0, 65535]", E);
     if (max_pages < 1 || max_pages > kMaxPages || page_size < 1 || n_pages < 0)
         return set_last_error(KVQ_EINVAL, "%s: bad sizes", E);
+    if (n_pages > kMaxPool) return set_last_error(KVQ_EINVAL, "%s: a pool of more than 2^29 pages", E);
     if ((int64_t)n_pages * page_size > INT32_MAX)
         return set_last_error(KVQ_EINVAL, "%s: a pool of more than INT32_MAX rows", E);
     return KVQ_OK;
@@ -707,7 +710,8 @@ int check_compact(const kvq_compact_plan* p, const char* E)
 {
     if (!p) return set_last_error(KVQ_EINVAL, "%s: NULL plan", E);
     if (int st = check_pool(E, p->n_seq, p->max_pages, p->page_size, p->n_pages)) return st;
-    if (p->max_copy < p->n_pages / 2) return set_last_error(KVQ_EINVAL, "%s: max_copy below n_pages / 2", E);
+    if (p->max_copy < p->n_pages / 2 || p->max_copy > kMaxCopies)
+        return set_last_error(KVQ_EINVAL, "%s: max_copy outside [n_pages / 2, 2^30]", E);
     if (!p->n_free || !p->n_used || !p->n_copy || (p->n_pages > 0 && !p->free_list) ||
         (p->max_copy > 0 && (!p->copy_src || !p->copy_dst || !p->copy_rows)) ||
         (p->n_seq > 0 && (!p->block_table || !p->n_held || !p->new_table)))

@@ -146,6 +146,23 @@ def test_page_plan_argument_errors(kvq, make, entry, arrays, own):
     assert need > 0 and call() == 5 and call(ws=FAKE, n=need - 1) == 5 and call(ws=FAKE + 32, n=need) == 4
 
 
+@pytest.mark.parametrize("make,entry", [(fork, "kvq_fork_pages"), (compact, "kvq_compact_pages")])
+def test_page_plans_of_the_largest_pools(kvq, make, entry):
+    """The plans count pages in 32 bits, a list's pushes past its end among them: a pool of more than 2^29 pages, or a copy
+    list of more than 2^30 entries, is refused."""
+    L = kvq.lib()
+    run, size = getattr(L, entry), getattr(L, entry + "_workspace")
+    big = dict(page_size=1, **(dict(max_copy=1 << 30) if make is compact else {}))
+    for pages in ((1 << 29) + 1, 1 << 30, (1 << 31) - 9000, (1 << 31) - 3, (1 << 31) - 1):
+        p = make(kvq, n_pages=pages, **big)
+        assert run(C.byref(p), None, 0, None, None) == 1 and size(C.byref(p)) == 0, pages
+    p = make(kvq, n_pages=1 << 29, **big)
+    # a byte of marks a page in the tables before and after, for each of 8 CTAs; or the pages' new numbers
+    assert size(C.byref(p)) >= (16 << 29 if make is fork else 4 << 29) and run(C.byref(p), None, 0, None, None) == 5
+    if make is compact:
+        assert run(C.byref(make(kvq, max_copy=(1 << 30) + 1)), None, 0, None, None) == 1
+
+
 def test_fork_of_nothing(kvq):
     none = dict(n_seq=0, parent=None, block_table=None, n_held=None, seq_len=None, copy_src=None, copy_dst=None, copy_rows=None)
     assert kvq.lib().kvq_fork_pages(C.byref(fork(kvq, **none)), None, 0, None, None) == 0
