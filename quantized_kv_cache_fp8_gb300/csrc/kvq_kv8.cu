@@ -40,6 +40,7 @@ constexpr int kTeam = 8;                 // CTAs of a short unit at most (what a
 constexpr int kTeamSteps = 4;            // places that each takes at most, or where the line's CTAs take nearly as many:
 constexpr int kTeamMost = 8, kTeamMore = 5;      // at most, and more than those
 constexpr float kSlack = 10.0f;          // log2 by which a weight may pass 1 before the reference moves
+constexpr float kNone = -0x1.fffffep127f;        // no reference
 
 struct Kv8Args {
     kvq_kv8_problem p;
@@ -47,6 +48,8 @@ struct Kv8Args {
     int line;                            // CTAs of a block of heads: what the line is cut into
     int idle;                            // places of the line that stand for a unit's beginning
     int team, team_rows;                 // short units: CTAs of a unit, rows of each
+    float scale;                         // sm_scale log2 e = scale 2^scale_exp, |scale| in [1, 2) or 0
+    int scale_exp;
     int4* info;                          // [line * n_hb]: sequence (-1: none), KV head and last CTA of the unit that the
                                          // CTA began and did not end
     float2* part_ml;                     // [line * n_hb][2][heads of a block]: reference (log2), sum of a unit's part: of
@@ -213,6 +216,7 @@ kv8_decode_kernel(const Kv8Args a)
     __shared__ int s_sum[W];
     __shared__ Line s_line;
     __shared__ int4 s_at[W];                                // of a warp: place, end of the stretch, sequence, place in it
+    __shared__ float s_rest[W][Sh::kHb];                    // of a warp's heads: the powers of two that their scores still lack
     grid_dependency_wait();
     grid_dependents_launch();
     const kvq_kv8_problem& p = a.p;
@@ -485,6 +489,8 @@ kv8_decode_kernel(const Kv8Args a)
         // its largest element into [2^14, 2^15): elements down to 2^-31 of it are exact, the rest within 2^-39 of it.
         uint32_t qf[NB][kBlocks][2];
         float hs[NB][2];                                        // what a score of heads 2 t, 2 t + 1 is multiplied by
+        bool wild = false;                                      // whether, for a head of the warp, that and s_rest
+        int rest[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) {
             const int h = nb * kHeads + g;
@@ -507,8 +513,8 @@ kv8_decode_kernel(const Kv8Args a)
                 }
             m = max(m, __shfl_xor_sync(kFull, m, 1));
             m = max(m, __shfl_xor_sync(kFull, m, 2));
-            // 14 - exponent; no head is scaled up by more than 2^100 (a largest element below 2^-86: not exact)
-            const int up = min(14 - ((int)(m >> 7) - 127), 100);
+            // 14 - exponent; 126 is enough for the smallest heads, whose elements, multiples of 2^-133, are exact so
+            const int up = min(14 - ((int)(m >> 7) - 127), 126);
             const float f = pow2(up);
 #pragma unroll
             for (int c = 0; c < kP; ++c)
@@ -520,10 +526,23 @@ kv8_decode_kernel(const Kv8Args a)
                         qf[nb][4 * c + 2 * e + (j >> 1)][j & 1] =
                             pack_h2(__uint_as_float(x[j] << 16) * f, __uint_as_float(x[j] & 0xFFFF0000u) * f);
                 }
+            // A score is y scale 2^e kf, |y| < 2^32 the product of query and codes, kf the row's scale, up to 2^120.  Multiplied in
+            // this order it does not overflow on the way where e <= 90, and what underflows counts less than 2^-29 in
+            // the score where e >= -100; what e has beyond those (queries near the ends of fp32) comes last.
+            const int e = m > 0u ? a.scale_exp - up : 0, near = min(max(e, -100), 90);
+            rest[nb] = e - near;
+            wild |= rest[nb] != 0;
             // (a NaN or an infinity: every score is a NaN, as all of them might be -inf, like those of rows that are not seen)
-            const float back = m >= 0x7F80u ? __int_as_float(0x7FFFFFFF) : pow2(-up) * (p.sm_scale * kLog2e);
+            const float back = m >= 0x7F80u ? __int_as_float(0x7FFFFFFF) : a.scale * pow2(near);
             hs[nb][0] = __shfl_sync(kFull, back, 8 * t);
             hs[nb][1] = __shfl_sync(kFull, back, 8 * t + 4);
+        }
+        wild = __any_sync(kFull, wild);
+        if (wild) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb)
+                if (t == 0) s_rest[warp][nb * kHeads + g] = pow2(min(max(rest[nb], -126), 127));
+            __syncwarp();
         }
 
         float o[NB][kBlocks][4];
@@ -535,14 +554,14 @@ kv8_decode_kernel(const Kv8Args a)
                 for (int e = 0; e < 4; ++e) o[nb][b][e] = 0.0f;
         // Two references a head, in log2: ref of the scores, for the sum of exp2(x - ref), and wref of x +
         // log2(vscale), for the weights that multiply V's codes, so that the largest of those is near 1 whatever the
-        // scales.  They move only when something passes them by kSlack (top, wtop: the level that makes them).
-        float ref[NB][2], wref[NB][2], top[NB][2], wtop[NB][2], sum[NB][2];
+        // scales.  They move only when something passes them by kSlack; kNone: nothing has yet.
+        float ref[NB][2], wref[NB][2], sum[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                ref[nb][e] = wref[nb][e] = sum[nb][e] = 0.0f;
-                top[nb][e] = wtop[nb][e] = -INFINITY;
+                ref[nb][e] = wref[nb][e] = kNone;
+                sum[nb][e] = 0.0f;
             }
 
         for (int i = 0; i < my_tiles; ++i) {
@@ -591,14 +610,27 @@ kv8_decode_kernel(const Kv8Args a)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             float& y = x[j][nb][2 * h + e];
-                            y = y * kf[j][h] * hs[nb][e];
+                            y = y * hs[nb][e] * kf[j][h];
                             m = fmaxf(m, y);
                             mw = fmaxf(mw, y + lv[j][h]);
                         }
-                    over |= m > top[nb][e] || mw > wtop[nb][e];
+                    over |= m - kSlack > ref[nb][e] || mw - kSlack > wref[nb][e];
                 }
             const bool some = now != ~0u;
-            if (__any_sync(kFull, over) || some) {              // (rare after the first tile)
+            if (__any_sync(kFull, over) || some || wild) {      // (rare after the first tile)
+                if (wild) {
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const float rest = s_rest[warp][nb * kHeads + 2 * t + e];
+#pragma unroll
+                            for (int j = 0; j < kGroups; ++j) {
+                                x[j][nb][e] *= rest;
+                                x[j][nb][2 + e] *= rest;
+                            }
+                        }
+                }
                 if (some) {
 #pragma unroll
                     for (int j = 0; j < kGroups; ++j)
@@ -627,22 +659,19 @@ kv8_decode_kernel(const Kv8Args a)
                             m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
                             mw = fmaxf(mw, __shfl_xor_sync(kFull, mw, d));
                         }
-                        // (a head's own top only: what else brought the warp here must not change the head's bits)
-                        if (m > top[nb][e]) {
-                            const float f = top[nb][e] == -INFINITY ? 0.0f : ex2(ref[nb][e] - m);
-                            sum[nb][e] *= f;
+                        // (a head's own scores only: what else brought the warp here must not change the head's bits)
+                        if (m - kSlack > ref[nb][e]) {
+                            sum[nb][e] *= ex2(ref[nb][e] - m);
                             ref[nb][e] = m;
-                            top[nb][e] = m + kSlack;
                         }
-                        if (mw > wtop[nb][e]) {
-                            const float f = wtop[nb][e] == -INFINITY ? 0.0f : ex2(wref[nb][e] - mw);
+                        if (mw - kSlack > wref[nb][e]) {
+                            const float f = ex2(wref[nb][e] - mw);
 #pragma unroll
                             for (int b = 0; b < kBlocks; ++b) {
                                 o[nb][b][e] *= f;
                                 o[nb][b][e + 2] *= f;
                             }
                             wref[nb][e] = mw;
-                            wtop[nb][e] = mw + kSlack;
                         }
                     }
                 }
@@ -696,7 +725,7 @@ kv8_decode_kernel(const Kv8Args a)
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
                 // (exp2f: with scales below 2^-126 the factor may be subnormal)
-                const float f = wtop[nb][e] == -INFINITY ? (l != l ? l : 0.0f) : exp2f(wref[nb][e] - ref[nb][e]);
+                const float f = wref[nb][e] == kNone ? (l != l ? l : 0.0f) : exp2f(wref[nb][e] - ref[nb][e]);
                 float* dst = mo + warp * Sh::kHb * Sh::kStride;
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
@@ -705,7 +734,7 @@ kv8_decode_kernel(const Kv8Args a)
                 }
                 if (g == 0) {
                     // a head without a row: reference -inf, sum 0; one that holds a NaN keeps it in the sum
-                    ml[(warp * Sh::kHb + h) * 2] = top[nb][e] == -INFINITY ? -INFINITY : ref[nb][e];
+                    ml[(warp * Sh::kHb + h) * 2] = ref[nb][e] == kNone ? -INFINITY : ref[nb][e];
                     ml[(warp * Sh::kHb + h) * 2 + 1] = l;
                 }
             }
@@ -1063,7 +1092,9 @@ int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* worksp
     if (q.bytes && (!workspace || ws_bytes < q.bytes))
         return set_last_error(KVQ_EWORKSPACE, "%s: workspace of %zu bytes, need %zu", E, workspace ? ws_bytes : (size_t)0, q.bytes);
     if (q.bytes && !aligned(workspace, 256)) return set_last_error(KVQ_EALIGN, "%s: workspace not 256-byte aligned", E);
-    Kv8Args a{*p,      p->n_qh / p->cache.n_kv, q.n_hb, q.line, q.idle, q.team, q.team_rows, nullptr, nullptr,
+    int scale_exp = 0;
+    const float scale = (float)(2.0 * std::frexp((double)p->sm_scale * 1.4426950408889634, &scale_exp));
+    Kv8Args a{*p,      p->n_qh / p->cache.n_kv, q.n_hb, q.line, q.idle, q.team, q.team_rows, scale, scale_exp - 1, nullptr, nullptr,
               nullptr, static_cast<__nv_bfloat16*>(out), lse, dev_status};
     if (q.bytes) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);

@@ -410,6 +410,33 @@ def test_decode_ranges(kvq):
     assert bool((out[0, 4:] == 0).all())
 
 
+@pytest.mark.parametrize("lens", [[900, 17], [20000, 300]])
+@pytest.mark.parametrize("ks,qs,scale", [(1e34, 1e-34, 0.09), (1e-34, 1e34, 0.09), (1e36, 1e-37, 0.5), (1e36, 1e-39, 50.0), (1e-37, 1e37, 0.09),
+                                         (1e30, 1e-19, 1e-12), (1e-30, 3e37, 1e-9), (1e-36, 1e19, 1e16), (1.0, 1e-36, 1e19)])
+def test_decode_score_ranges(kvq, lens, ks, qs, scale):
+    """Scores of ordinary size whose factors are near the ends of fp32, queries that are subnormal among them."""
+    d = 128
+    c = Cache(lens, 2, d, 64, 90, spread=0.5)
+    c.pl["k_scale"] *= ks
+    q = queries(2, 12, d, 91, qs)
+    out, lse = decode(kvq, c.problem(kvq, q, scale=scale))
+    check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, 0, scale), d, 32)
+
+
+@pytest.mark.parametrize("d,lens", [(64, [900, 17]), (128, [900, 17]), (128, [20000, 300]), (256, [5000, 1])])
+def test_decode_heads_of_every_size(kvq, d, lens):
+    """Heads of one KV head whose queries are 2^250 apart, one of them zero."""
+    c = Cache(lens, 2, d, 64, 110, spread=0.5)
+    size = torch.tensor([1.0, 1e-39, 1e20, 0.0, 1e37, 1e-30, 1.0], device="cuda").repeat(2)
+    q = (queries(2, 14, d, 111).float() * size[:, None]).bfloat16()
+    out, lse = decode(kvq, c.problem(kvq, q))
+    check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, 0, 1 / math.sqrt(d)), d, 32)
+    one = size == 1.0
+    q[:, ~one] = 0.0
+    out2, lse2 = decode(kvq, c.problem(kvq, q))
+    assert torch.equal(out[:, one], out2[:, one]) and torch.equal(lse[:, one], lse2[:, one])
+
+
 def test_decode_many_small_weights(kvq):
     """One row takes most of the softmax, and 50000 rows far below it hold the rest together."""
     L, d = 50001, 64
