@@ -52,8 +52,8 @@ struct Kv8Args {
     int scale_exp;
     int4* info;                          // [line * n_hb]: sequence (-1: none), KV head and last CTA of the unit that the
                                          // CTA began and did not end
-    float2* part_ml;                     // [line * n_hb][2][heads of a block]: reference (log2), sum of a unit's part: of
-                                         // the one that the CTA found begun, of the one that it left
+    float4* part_ml;                     // [line * n_hb][2][heads of a block]: a unit's part's Level: of the one that the CTA
+                                         // found begun, of the one that it left
     float* part_o;                       // [line * n_hb][2][heads of a block][D]: sum of weighted rows
     __nv_bfloat16* out;
     float* lse;
@@ -116,8 +116,35 @@ __device__ __forceinline__ float pow2(int k)              // k in [-126, 127]
     return __int_as_float((k + 127) << 23);
 }
 
-// what a part of reference x.x and sum x.y counts against the reference `base` (a NaN head: no reference, its sum says it)
-__device__ __forceinline__ float part_weight(float2 x, float base) { return x.y != x.y ? x.y : ex2(x.x - base); }
+// What a part of a unit's rows leaves beside its weighted rows: x the reference of its sum, y that sum, z the reference of the
+// weighted rows, references in log2, -inf where there is none.  The rows are joined against their own reference, so that V
+// rows near the ends of fp32 pass no sum, and come to the sum's with the quotient.
+using Level = float4;
+__device__ __forceinline__ float top_of(float m) { return m == -INFINITY ? 0.0f : m; }
+// what a part counts against the reference `base` of sums (a NaN head: no reference, its sum says it)
+__device__ __forceinline__ float part_weight(const Level& x, float base) { return x.y != x.y ? x.y : ex2(x.x - base); }
+// Weighted rows to outputs: 1 / sum, and 2^(z - x), which may pass 2^128 where a reference lags, as two halves.
+struct Finish {
+    float r, half;
+    __device__ __forceinline__ Finish(const Level& x)
+        : r(x.y == 0.0f ? 0.0f : 1.0f / x.y), half(x.z == -INFINITY ? 0.0f : ex2(0.5f * (x.z - top_of(x.x))))
+    {
+    }
+    __device__ __forceinline__ float operator()(float o) const { return o * r * half * half; }
+    __device__ __forceinline__ void store(__nv_bfloat16* out, const float4& o) const
+    {
+        reinterpret_cast<__nv_bfloat162*>(out)[0] = __floats2bfloat162_rn((*this)(o.x), (*this)(o.y));
+        reinterpret_cast<__nv_bfloat162*>(out)[1] = __floats2bfloat162_rn((*this)(o.z), (*this)(o.w));
+    }
+};
+__device__ __forceinline__ float lse_of(const Level& x) { return x.y == 0.0f ? -INFINITY : (top_of(x.x) + log2f(x.y)) * kLn2; }
+__device__ __forceinline__ void add_rows(float4& acc, const float4& y, float f)
+{
+    acc.x = fmaf(y.x, f, acc.x);
+    acc.y = fmaf(y.y, f, acc.y);
+    acc.z = fmaf(y.z, f, acc.z);
+    acc.w = fmaf(y.w, f, acc.w);
+}
 
 // bytes of the cache, read once
 __device__ __forceinline__ uint4 load16(const uint8_t* p)
@@ -187,9 +214,9 @@ struct Kv8Shape {
     static constexpr int kVw = D == 64 ? 2 : 4;             // words of such a piece
     static constexpr int kHb = NB * kHeads;                 // heads of a CTA
     static constexpr int kStep = W * R;                     // rows of a place of the line
-    // the merge of the warps: weighted rows, then references and sums; then the same of the CTA, for its cluster
+    // the merge of the warps: weighted rows, then levels; then the same of the CTA, for its cluster
     static constexpr int kStride = D == 64 ? D : D + 4;     // of a head's weighted rows
-    static constexpr int kSmem = (W * (kStride + 2) + D + 2) * kHb * 4;
+    static constexpr int kSmem = (W * (kStride + 4) + D + 4) * kHb * 4;
     // Where dims d, d + 1 of head h are in those: pairs turn within 16 dims by the 16's number, or (64 dims) within 8 by the
     // head's, so that the lanes that write together meet no bank twice (16 sequences of 1024 rows: 13.2 us with the rows as
     // they are, 12.7 so)
@@ -710,12 +737,12 @@ kv8_decode_kernel(const Kv8Args a)
         more = next_piece();
         if (more) begin();
 
-        // ---- the warps are joined: weighted rows relative to ref, then references and sums
+        // ---- the warps are joined: weighted rows, then levels
         __syncthreads();
         float* mo = reinterpret_cast<float*>(smem);             // [warp][head][kStride]
-        float* ml = mo + W * Sh::kHb * Sh::kStride;             // [warp][head][2]
-        float* to = ml + W * Sh::kHb * 2;                       // [head][D], of the CTA
-        float* tl = to + Sh::kHb * D;                           // [head][2]
+        Level* ml = reinterpret_cast<Level*>(mo + W * Sh::kHb * Sh::kStride);       // [warp][head]
+        float* to = reinterpret_cast<float*>(ml + W * Sh::kHb); // [head][D], of the CTA
+        Level* tl = reinterpret_cast<Level*>(to + Sh::kHb * D); // [head]
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -724,54 +751,47 @@ kv8_decode_kernel(const Kv8Args a)
                 float l = sum[nb][e];
 #pragma unroll
                 for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(kFull, l, d);
-                // (exp2f: with scales below 2^-126 the factor may be subnormal)
-                const float f = wref[nb][e] == kNone ? (l != l ? l : 0.0f) : exp2f(wref[nb][e] - ref[nb][e]);
                 float* dst = mo + warp * Sh::kHb * Sh::kStride;
 #pragma unroll
                 for (int b = 0; b < kBlocks; ++b) {
                     const int d = D == 64 ? 8 * g + 2 * b : 128 * (b / 8) + 16 * g + 2 * (b % 8);
-                    *reinterpret_cast<float2*>(dst + Sh::place(h, d)) = make_float2(o[nb][b][e] * f, o[nb][b][e + 2] * f);
+                    *reinterpret_cast<float2*>(dst + Sh::place(h, d)) = make_float2(o[nb][b][e], o[nb][b][e + 2]);
                 }
-                if (g == 0) {
-                    // a head without a row: reference -inf, sum 0; one that holds a NaN keeps it in the sum
-                    ml[(warp * Sh::kHb + h) * 2] = ref[nb][e] == kNone ? -INFINITY : ref[nb][e];
-                    ml[(warp * Sh::kHb + h) * 2 + 1] = l;
-                }
+                // a head without a row: reference -inf, sum 0; one that holds a NaN keeps it in the sum
+                if (g == 0)
+                    ml[warp * Sh::kHb + h] = make_float4(ref[nb][e] == kNone ? -INFINITY : ref[nb][e], l,
+                                                         wref[nb][e] == kNone ? -INFINITY : wref[nb][e], 0.0f);
             }
         __syncthreads();
         for (int i = threadIdx.x; i < heads * (D / 4); i += Sh::kThreads) {
             const int h = i / (D / 4), d = i % (D / 4) * 4;
-            float m = -INFINITY, l = 0.0f;
+            Level all = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
 #pragma unroll
-            for (int w = 0; w < W; ++w) m = fmaxf(m, ml[(w * Sh::kHb + h) * 2]);
-            const float base = m == -INFINITY ? 0.0f : m;
+            for (int w = 0; w < W; ++w) {
+                all.x = fmaxf(all.x, ml[w * Sh::kHb + h].x);
+                all.z = fmaxf(all.z, ml[w * Sh::kHb + h].z);
+            }
+            const float base = top_of(all.x), rows_base = top_of(all.z);
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
-                const float wl = ml[(w * Sh::kHb + h) * 2 + 1];
-                const float f = part_weight(make_float2(ml[(w * Sh::kHb + h) * 2], wl), base);
+                const Level x = ml[w * Sh::kHb + h];
                 const float2 y0 = *reinterpret_cast<const float2*>(mo + w * Sh::kHb * Sh::kStride + Sh::place(h, d));
                 const float2 y1 = *reinterpret_cast<const float2*>(mo + w * Sh::kHb * Sh::kStride + Sh::place(h, d + 2));
-                l += wl * f;
-                acc.x = fmaf(y0.x, f, acc.x);
-                acc.y = fmaf(y0.y, f, acc.y);
-                acc.z = fmaf(y1.x, f, acc.z);
-                acc.w = fmaf(y1.y, f, acc.w);
+                all.y = fmaf(x.y, part_weight(x, base), all.y);
+                add_rows(acc, make_float4(y0.x, y0.y, y1.x, y1.y), ex2(x.z - rows_base));
             }
             const int64_t row = head0 + h;
             if constexpr (TEAM) {
                 *reinterpret_cast<float4*>(to + h * D + d) = acc;
-                if (d == 0) *reinterpret_cast<float2*>(tl + 2 * h) = make_float2(m, l);
+                if (d == 0) tl[h] = all;
             } else if (this_part < 0) {
-                const float r = l == 0.0f ? 0.0f : 1.0f / l;
-                __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
-                dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
-                dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
-                if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
+                Finish(all).store(a.out + row * D + d, acc);
+                if (d == 0 && a.lse) a.lse[row] = lse_of(all);
             } else {
                 const int64_t place = ((int64_t)blockIdx.x * 2 + this_part) * Sh::kHb + h;
                 *reinterpret_cast<float4*>(a.part_o + place * D + d) = acc;
-                if (d == 0) a.part_ml[place] = make_float2(m, l);
+                if (d == 0) a.part_ml[place] = all;
             }
         }
     }
@@ -780,40 +800,34 @@ kv8_decode_kernel(const Kv8Args a)
     if constexpr (TEAM) {
         // ---- the CTAs are joined, in their order: each one a share of the elements
         const cg::cluster_group team = cg::this_cluster();
-        const float *to = reinterpret_cast<const float*>(smem) + W * Sh::kHb * (Sh::kStride + 2), *tl = to + Sh::kHb * D;
+        const float* to = reinterpret_cast<const float*>(smem) + W * Sh::kHb * (Sh::kStride + 4);
+        const Level* tl = reinterpret_cast<const Level*>(to + Sh::kHb * D);
         const int64_t head0 = (int64_t)s * p.n_qh + kv * a.group + hb * Sh::kHb;
         team.sync();
         for (int i = (int)team.block_rank() * Sh::kThreads + threadIdx.x; i < heads * (D / 4); i += a.team * Sh::kThreads) {
             const int h = i / (D / 4), d = i % (D / 4) * 4;
-            float2 x[kTeam];
+            Level x[kTeam], all = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
             float4 y[kTeam];
-            float m = -INFINITY, l = 0.0f;
 #pragma unroll
             for (int k = 0; k < kTeam; ++k) {
                 if (k < a.team) {
-                    x[k] = *reinterpret_cast<const float2*>(team.map_shared_rank(tl, k) + 2 * h);
+                    x[k] = *team.map_shared_rank(tl + h, k);
                     y[k] = *reinterpret_cast<const float4*>(team.map_shared_rank(to, k) + h * D + d);
-                    m = fmaxf(m, x[k].x);
+                    all.x = fmaxf(all.x, x[k].x);
+                    all.z = fmaxf(all.z, x[k].z);
                 }
             }
-            const float base = m == -INFINITY ? 0.0f : m;
+            const float base = top_of(all.x), rows_base = top_of(all.z);
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < kTeam; ++k) {
                 if (k < a.team) {
-                    const float f = part_weight(x[k], base);
-                    l = fmaf(x[k].y, f, l);
-                    acc.x = fmaf(y[k].x, f, acc.x);
-                    acc.y = fmaf(y[k].y, f, acc.y);
-                    acc.z = fmaf(y[k].z, f, acc.z);
-                    acc.w = fmaf(y[k].w, f, acc.w);
+                    all.y = fmaf(x[k].y, part_weight(x[k], base), all.y);
+                    add_rows(acc, y[k], ex2(x[k].z - rows_base));
                 }
             }
-            const float r = l == 0.0f ? 0.0f : 1.0f / l;
-            __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + (head0 + h) * D + d);
-            dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
-            dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
-            if (d == 0 && a.lse) a.lse[head0 + h] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
+            Finish(all).store(a.out + (head0 + h) * D + d, acc);
+            if (d == 0 && a.lse) a.lse[head0 + h] = lse_of(all);
         }
         team.sync();                                        // (nobody's shared memory goes before all have read it)
         return;
@@ -840,7 +854,7 @@ template <int D, int T>
 __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_heads)
 {
     constexpr int kJoinThreads = T, kLanes = D / 4, kJoin = kJoinThreads / kLanes, kFlight = 4;
-    __shared__ float2 s_ml[kJoin];
+    __shared__ Level s_ml[kJoin];
     __shared__ __align__(16) float s_o[kJoin][D];
     __shared__ int4 s_unit[kJoinThreads];
     __shared__ unsigned s_some[kJoinThreads / 32];
@@ -866,62 +880,56 @@ __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_h
                 const int at = 32 * k + __ffs(left) - 1;
                 const int4 unit = s_unit[at];
                 const int c = first + at, n = unit.z - c + 1;
-                float m = -INFINITY, l = 0.0f;
+                Level all = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
                 float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                 for (int i = grp; i < n; i += kJoin * kFlight) {
-                    float2 x[kFlight];
+                    Level x[kFlight];
                     float4 y[kFlight];
-                    float top = m;
+                    const Level was = all;
 #pragma unroll
                     for (int u = 0; u < kFlight; ++u) {
                         const int q = i + u * kJoin;
                         const int64_t place = (((int64_t)(c + q) * a.n_hb + hb) * 2 + (q == 0)) * n_heads + h;
-                        x[u] = q < n ? a.part_ml[place] : make_float2(-INFINITY, 0.0f);
+                        x[u] = q < n ? a.part_ml[place] : make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
                         y[u] = q < n ? *reinterpret_cast<const float4*>(a.part_o + place * D + d)
                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     }
 #pragma unroll
-                    for (int u = 0; u < kFlight; ++u) top = fmaxf(top, x[u].x);
-                    const float base = top == -INFINITY ? 0.0f : top, f0 = ex2(m - base);
-                    m = top;
-                    l *= f0;
+                    for (int u = 0; u < kFlight; ++u) {
+                        all.x = fmaxf(all.x, x[u].x);
+                        all.z = fmaxf(all.z, x[u].z);
+                    }
+                    const float base = top_of(all.x), rows_base = top_of(all.z), f0 = ex2(was.z - rows_base);
+                    all.y *= ex2(was.x - base);
                     acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
 #pragma unroll
                     for (int u = 0; u < kFlight; ++u) {
-                        const float f = part_weight(x[u], base);
-                        l = fmaf(x[u].y, f, l);
-                        acc.x = fmaf(y[u].x, f, acc.x);
-                        acc.y = fmaf(y[u].y, f, acc.y);
-                        acc.z = fmaf(y[u].z, f, acc.z);
-                        acc.w = fmaf(y[u].w, f, acc.w);
+                        all.y = fmaf(x[u].y, part_weight(x[u], base), all.y);
+                        add_rows(acc, y[u], ex2(x[u].z - rows_base));
                     }
                 }
                 __syncthreads();                            // (the last unit is written)
                 *reinterpret_cast<float4*>(&s_o[grp][d]) = acc;
-                if (d == 0) s_ml[grp] = make_float2(m, l);
+                if (d == 0) s_ml[grp] = all;
                 __syncthreads();
                 if (grp != 0) continue;
 #pragma unroll
-                for (int g = 1; g < kJoin; ++g) m = fmaxf(m, s_ml[g].x);
-                const float base = m == -INFINITY ? 0.0f : m;
-                l = 0.0f;
+                for (int g = 1; g < kJoin; ++g) {
+                    all.x = fmaxf(all.x, s_ml[g].x);
+                    all.z = fmaxf(all.z, s_ml[g].z);
+                }
+                const float base = top_of(all.x), rows_base = top_of(all.z);
+                all.y = 0.0f;
                 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int g = 0; g < kJoin; ++g) {
-                    const float f = part_weight(s_ml[g], base);
-                    const float4 y = *reinterpret_cast<const float4*>(&s_o[g][d]);
-                    l = fmaf(s_ml[g].y, f, l);
-                    acc.x = fmaf(y.x, f, acc.x);
-                    acc.y = fmaf(y.y, f, acc.y);
-                    acc.z = fmaf(y.z, f, acc.z);
-                    acc.w = fmaf(y.w, f, acc.w);
+                    const Level x = s_ml[g];
+                    all.y = fmaf(x.y, part_weight(x, base), all.y);
+                    add_rows(acc, *reinterpret_cast<const float4*>(&s_o[g][d]), ex2(x.z - rows_base));
                 }
-                const float r = l == 0.0f ? 0.0f : 1.0f / l;
                 const int64_t row = (int64_t)unit.x * p.n_qh + unit.y * a.group + hb * n_heads + h;
-                __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + d);
-                dst[0] = __floats2bfloat162_rn(acc.x * r, acc.y * r);
-                dst[1] = __floats2bfloat162_rn(acc.z * r, acc.w * r);
-                if (d == 0 && a.lse) a.lse[row] = l == 0.0f ? -INFINITY : (base + log2f(l)) * kLn2;
+                Finish(all).store(a.out + row * D + d, acc);
+                if (d == 0 && a.lse) a.lse[row] = lse_of(all);
             }
         }
     }
@@ -969,7 +977,7 @@ struct Kv8Kind {
         if (!q.cuts) return;
         const size_t ctas = (size_t)q.line * q.n_hb;
         q.off_ml = (ctas * sizeof(int4) + 255) / 256 * 256;
-        q.off_o = (q.off_ml + ctas * 2 * kHb * sizeof(float2) + 255) / 256 * 256;
+        q.off_o = (q.off_ml + ctas * 2 * kHb * sizeof(Level) + 255) / 256 * 256;
         q.bytes = q.off_o + ctas * 2 * kHb * D * sizeof(float);
     }
     template <bool GROUPED>
@@ -1099,7 +1107,7 @@ int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* worksp
     if (q.bytes) {
         uint8_t* ws = static_cast<uint8_t*>(workspace);
         a.info = reinterpret_cast<int4*>(ws);
-        a.part_ml = reinterpret_cast<float2*>(ws + q.off_ml);
+        a.part_ml = reinterpret_cast<Level*>(ws + q.off_ml);
         a.part_o = reinterpret_cast<float*>(ws + q.off_o);
     }
     const cudaError_t e = of_kind(*p, [&](auto kind) { return kind.launch(a, q, (cudaStream_t)stream); });

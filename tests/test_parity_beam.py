@@ -423,6 +423,19 @@ def test_decode_score_ranges(kvq, lens, ks, qs, scale):
     check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, 0, scale), d, 32)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[900, 17], [40000, 300], [3, 1]])
+@pytest.mark.parametrize("vs", [1e37, 1e-36])
+def test_decode_value_ranges(kvq, d, lens, vs):
+    """V rows near the ends of fp32: sums over the rows pass its largest, the weighted means do not."""
+    c = Cache(lens, 2, d, 64, 95, spread=0.5)
+    c.pl["v_scale"] *= vs
+    q = queries(2, 12, d, 96)
+    out, lse = decode(kvq, c.problem(kvq, q))
+    assert bool(out.isfinite().all())
+    check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, 0, 1 / math.sqrt(d)), d, 32)
+
+
 @pytest.mark.parametrize("d,lens", [(64, [900, 17]), (128, [900, 17]), (128, [20000, 300]), (256, [5000, 1])])
 def test_decode_heads_of_every_size(kvq, d, lens):
     """Heads of one KV head whose queries are 2^250 apart, one of them zero."""
