@@ -469,6 +469,59 @@ def test_decode_many_small_weights(kvq):
         check_decode(out, lse, decode_ref(c.pl, q, [L], c.rows_of, 0, 1.0), d, 4096)
 
 
+@pytest.mark.parametrize("code,gap", [(0x54, 12.0), (0x56, 14.0), (0x58, 16.0)])
+def test_decode_small_weights_of_a_part(kvq, code, gap):
+    """A row of V = 0 takes most of the softmax, so that the output is what the rows far below it hold together; parts of many
+    rows (64 sequences over the same pages: a warp has about 900 rows of a unit)."""
+    n, kv, L, d, page = 64, 8, 4096, 64, 64
+    pl = new_planes(kv, L, d)
+    pl["k"].zero_()
+    pl["v"].fill_(0x7E)                                      # 448
+    pl["k_scale"].fill_(1.0)
+    pl["v_scale"].fill_(1.0 / 448)
+    at = 1234
+    pl["k"][:, at, 0] = code
+    pl["v"][:, at] = 0
+    q = torch.zeros(n, kv, d, dtype=torch.bfloat16, device="cuda")
+    q[:, :, 0] = 1.0
+    table = torch.arange(L // page, dtype=torch.int32, device="cuda").repeat(n, 1)
+    p = kvq.make_kv8_problem(seq_len=i32(n, fill=L), q=q, sm_scale=1.0, max_seq_len=L, cache=pl, block_table=table, page_size=page)
+    out, lse = decode(kvq, p)
+    total = 1.0 + (L - 1) * math.exp(-gap)
+    want = (L - 1) * math.exp(-gap) / total
+    # the rows of the heavy row's part: a warp's quarter of the unit at most.  Their weights are within 2^-25 of the heavy one
+    # (half a step of binary16's subnormals) or 2^-11 of themselves; scores, in log2 at most 24, are rounded three times (the
+    # scale, two products), on both sides of the quotient: 6 24 2^-24 ln 2 < 2^-17, with the exponentials and sums; then the
+    # output's bfloat16
+    part = L // 4
+    bar = want * (2.0**-11 + 2.0**-17) + part * 2.0**-25 / total
+    bar += 2.0**-8 * (want + bar)
+    # (without the small weights of the heavy row's part: some head's has three quarters of that at least, as a cut falls every 27
+    # places of 128 rows and a unit has 32)
+    assert 0.75 * part * math.exp(-gap) / total > bar
+    assert float((out.double() - want).abs().max()) <= bar
+    # log2 of the sum is added to the score and the whole scaled by ln 2: five roundings of 2^-24 and the constant's 2^-25; the
+    # sum itself within 2^-20
+    assert float((lse.double() - gap - math.log(total)).abs().max()) <= 5.5 * 2.0**-24 * (gap + 1) + 2.0**-20
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,kv,group,page,window", [([300, 5, 0, 1000], 3, 9, 40, 0), ([4097], 1, 16, 64, 0), ([9000], 2, 4, 1, 0),
+                                                       ([777, 2000, 31], 4, 2, 7, 1500), ([40000], 1, 8, 128, 0), ([4000] * 70, 4, 3, 64, 0)])
+def test_decode_rounding_of_weights(kvq, d, lens, kv, group, page, window):
+    """Outputs against what the roundings allow and no more: a weight's 2^-11, or 2^-25 of the largest of its part."""
+    c = Cache(lens, kv, d, page, seed=d)
+    q = queries(len(lens), kv * group, d, 120 + d)
+    out, _ = decode(kvq, c.problem(kvq, q, window))
+    o, _, size, mass = decode_ref(c.pl, q, lens, c.rows_of, window, 1 / math.sqrt(d))
+    # As in check_decode, but for the small weights: each is within 2^-25 of the largest of its part, and that one's row, whose
+    # largest code is 448, has its share in `mass`, so that the part's rows lose 2^-25 of the largest over the dims each
+    dp = torch.expm1(2 * (d + 8) * 2.0**-23 * size) + 2.0**-21
+    bar = (dp[..., None] + 2.0**-11) * mass + min(4096, max(lens)) * 2.0**-25 * mass.amax(2, keepdim=True)
+    bar = bar + 2.0**-8 * (o.abs() + bar) + 1e-38
+    assert bool(((out.double() - o).abs() <= bar).all()), float(((out.double() - o).abs() / bar).max())
+
+
 @pytest.mark.parametrize("lens", [[700, 20], [9000, 5001]])
 def test_decode_nan_queries_stay_in_their_head(kvq, lens):
     c = Cache(lens, 2, 128, 64, 60)
@@ -773,6 +826,22 @@ def test_select_large_logits(kvq, V, R):
         step = np.maximum(np.spacing(np.where(far, np.abs(at), 1)), np.float32(0.125))
         x = np.where(far, at + step * g.integers(-9, 1, x.shape).astype(np.float32), at).astype(np.float32)
         check_select(kvq, x, (-5 * g.random((4 * R, 1))).astype(np.float32), None, 6, eos=-1)
+
+
+def test_select_beams_at_different_levels(kvq):
+    """Constant rows at levels far apart, whose values tie exactly: beams in either order (their sums are of fp32
+    exponentials), each beam's tokens from its lowest on."""
+    for V in (3000, 40000):
+        for levels in ([3e4, -3e4, 1e6, -1e6], [0.0, 1.5, -7.25, 1e13], [1e25, -1e25, 9e29, -3.4e38]):
+            x = np.broadcast_to(np.array(levels, np.float32)[None, :, None], (1, 4, V)).copy()
+            (out, token, parent, _), st = select(kvq, dev(x), dev(np.zeros((1, 4), np.float32)), None, 10, eos=-1)
+            assert st == 0
+            assert np.abs(host(out).astype(np.float64) + math.log(V)).max() <= 2.0**-22 + 2.0**-24 * math.log(V)
+            token, parent = host(token)[0], host(parent)[0]
+            for b in range(4):
+                mine = token[parent == b]
+                assert np.array_equal(mine, np.arange(len(mine)))
+            assert sum((parent == b).sum() for b in range(4)) == 10
 
 
 def test_select_in_place_and_graph(kvq):
