@@ -828,6 +828,24 @@ def test_select_large_logits(kvq, V, R):
         check_select(kvq, x, (-5 * g.random((4 * R, 1))).astype(np.float32), None, 6, eos=-1)
 
 
+@pytest.mark.parametrize("V", [4000, 128000])
+@pytest.mark.parametrize("level", [0.0, 5.3, -300.7, 9000.0, 3e6])
+def test_select_sum_of_a_far_tail(kvq, V, level):
+    """One token above all others, which lie at one distance, so that their exponentials' errors add up."""
+    for far in (0.7, 3.3, 5.01, 7.77, 9.7, 11.1, 12.3, 13.9):
+        x = np.full((1, 1, V), np.float32(level - far), np.float32)
+        x[0, 0, 77] = level
+        (out, token, _, _), st = select(kvq, dev(x), dev(np.zeros((1, 1), np.float32)), None, 1, eos=-1)
+        D = float(x[0, 0, 77]) - float(x[0, 0, 0])
+        tail = (V - 1) * math.exp(-D)
+        # A term: its argument in log2, and the rest of the factor log2 e, are rounded to 2^-24 of the distance each, twice more
+        # where warps and chunks are brought to one maximum, whose exponentials are within 2^-22; the instruction's 2^-22 and
+        # some additions within 2^-24 besides.  Then the value's fp32.
+        bar = 2.0**-20 + tail / (1 + tail) * D * 2.0**-22 + 2.0**-24 * math.log1p(tail)
+        assert st == 0 and token.item() == 77
+        assert abs(out.item() + math.log1p(tail)) <= bar, far
+
+
 def test_select_beams_at_different_levels(kvq):
     """Constant rows at levels far apart, whose values tie exactly: beams in either order (their sums are of fp32
     exponentials), each beam's tokens from its lowest on."""
