@@ -4,13 +4,15 @@
 // over the logits: a CTA takes a chunk of one beam's row into registers and leaves its maximum, its sum of
 // exponentials and its n_out best tokens; a second kernel, a CTA a request, joins the chunks' sums to each beam's
 // logarithm and picks the n_out best of all chunks' candidates.  The logits' bytes are the floor, and an exponential
-// takes 0.7 of the time of a bfloat16's two; what bounds it are instructions: 512 rows of 128000 bfloat16, 16 of
-// each request's 8 beams kept, take 39.8 us (34 the chunks, at 60% of the issue slots, the join the rest) against 19 for the
-// bytes.
+// takes 0.7 of the time of a bfloat16's two.  512 rows of 128000 bfloat16, 16 of each request's 8 beams kept, take
+// 40.0 us (34 the chunks, the join the rest) against 19 for the bytes: a warp spends 835 instructions on a chunk, 65% of the
+// issue slots; the rest goes to waits for a chunk's loads and between its barriers, with half of the SM's warps (64
+// registers) to fill them.
 //
 // Best k of the values that a CTA holds: k of its threads' maxima reach some level, so that nothing below it can be
 // among the best k (put_floor).  What reaches it (little more than k, unless many values are equal) is gathered and
-// ranked by counting.  Where it does not fit the buffer, the best are taken one by one instead.
+// ranked by counting.  Where it does not fit the buffer, the best are taken one by one instead (constant rows: 645 us
+// for the same; maxima that many share, logits rounded to integers, 48; 300 tokens that are not -inf, side by side, 57).
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -491,6 +493,11 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     const int b_first = first % p.n_beam;
     auto key_at = [&](int l, int b, int place) { return a.part_key + (row0 + b) * per_beam + (int64_t)(l / p.n_beam) * k + place; };
     const uint64_t head_key = first < lists && place0 < k ? *key_at(first, b_first, place0) : 0;
+    // the lane's first chunk of the warp's first beam likewise
+    const bool one = lane < a.n_chunk;
+    const int64_t at_warp = (row0 + warp) * a.n_chunk + lane;
+    const float m_warp = one && warp < p.n_beam ? a.part_m[at_warp] : -INFINITY;
+    const float2 s_warp = one && warp < p.n_beam ? a.part_s[at_warp] : make_float2(0.0f, 0.0f);
     float score = 0.0f;                                     // of beam `tid`
     int live = 0;
     if (tid < p.n_beam) {
@@ -505,9 +512,12 @@ __global__ void __launch_bounds__(kThreads) beam_merge_kernel(const BeamArgs a)
     for (int b = warp; b < p.n_beam; b += kWarps) {
         if (s_live[b] != 1) continue;
         const int64_t at = (row0 + b) * a.n_chunk;
-        const bool one = lane < a.n_chunk;                  // the lane's first chunk, loaded at once
-        const float m0 = one ? a.part_m[at + lane] : -INFINITY;
-        const float2 sc0 = one ? a.part_s[at + lane] : make_float2(0.0f, 0.0f);
+        float m0 = m_warp;
+        float2 sc0 = s_warp;
+        if (b != warp) {
+            m0 = one ? a.part_m[at + lane] : -INFINITY;
+            sc0 = one ? a.part_s[at + lane] : make_float2(0.0f, 0.0f);
+        }
         float m = m0;
         for (int c = lane + 32; c < a.n_chunk; c += 32) m = fmaxf(m, a.part_m[at + c]);
 #pragma unroll
