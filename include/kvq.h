@@ -587,8 +587,8 @@ int kvq_accept_mla(const kvq_mla_accept_desc* d, uint32_t* dev_status, kvq_strea
  *     kvq_resize_pages (the new tokens' pages and pool rows), kvq_append_kv8 (their K/V rows),
  *     kvq_kv8_decode (attention; these two once a layer), kvq_beam_select (the best
  *     continuations and their parents), kvq_fork_pages (the block tables follow the parents:
- *     pages are shared, copied and freed) and kvq_copy_pages (those copies; once for all
- *     layers, or layer by layer).
+ *     pages are shared, copied and freed) and kvq_copy_pages (those copies; 64 planes, which
+ *     are 16 layers of this cache, a call).
  * Every quantity that varies from step to step is read from device memory, so a captured
  * graph of the step can be replayed.
  * ------------------------------------------------------------------------------------ */

@@ -5,7 +5,7 @@
 // exponentials and its n_out best tokens; a second kernel, a CTA a request, joins the chunks' sums to each beam's
 // logarithm and picks the n_out best of all chunks' candidates.  The logits' bytes are the floor, and an exponential
 // takes 0.7 of the time of a bfloat16's two.  512 rows of 128000 bfloat16, 16 of each request's 8 beams kept, take
-// 40.0 us (34 the chunks, the join the rest) against 19 for the bytes: a warp spends 835 instructions on a chunk, 65% of the
+// 40.0 us (34 the chunks, the join the rest) against 19 for the bytes: a warp spends 940 instructions on a chunk, 65% of the
 // issue slots; the rest goes to waits for a chunk's loads and between its barriers, with half of the SM's warps (64
 // registers) to fill them.
 //

@@ -185,7 +185,7 @@ __host__ __device__ constexpr int first_group(int x) { return x & ~(kGroup - 1);
 // CTAs, kIdle places for what it costs to begin one; units follow one another, the KV heads of a sequence side by
 // side.  CTA c of n has total / n places, the first total % n one more: the same work for all, whatever the lengths,
 // and a partial result only where a cut falls into a unit (64 ragged sequences, 512 to 32768 rows: 198 us with splits
-// of one size, which pay for their beginnings, 182 us on the line).
+// of one size, which pay for their beginnings, 182 on the line, when it took their place).
 template <int STEP>
 __device__ __forceinline__ int unit_steps(const int2& seen) { return (seen.y - first_group(seen.x) + STEP - 1) / STEP; }
 template <int STEP>
@@ -218,8 +218,8 @@ struct Kv8Shape {
     static constexpr int kStride = D == 64 ? D : D + 4;     // of a head's weighted rows
     static constexpr int kSmem = (W * (kStride + 4) + D + 4) * kHb * 4;
     // Where dims d, d + 1 of head h are in those: pairs turn within 16 dims by the 16's number, or (64 dims) within 8 by the
-    // head's, so that the lanes that write together meet no bank twice (16 sequences of 1024 rows: 13.2 us with the rows as
-    // they are, 12.7 so)
+    // head's, so that the lanes that write together meet no bank twice (131072 rows: 53.3 us with the rows as they are, 51.9
+    // so; 64 ragged sequences 184.2 and 180.8)
     static __device__ __forceinline__ int place(int h, int d)
     {
         return D == 64 ? h * kStride + (d & ~7) + 2 * ((d / 2 + h / 2) & 3) : h * kStride + (d & ~15) + 2 * ((d / 2 + d / 16) & 7);
@@ -229,8 +229,8 @@ struct Kv8Shape {
 // One CTA: a stretch of the line for one block of up to 8 NB query heads of the KV heads on it.  In each unit its
 // warps take the tiles in turn, each with a softmax of its own, and are joined at the end.  TEAM: units are short; each
 // one has a cluster of a.team CTAs, which take team_rows of its rows each and join their results through shared
-// memory, so that there is no second launch (8 KV heads x 4, 1024 rows: 8.3 us on the line, 6.0 so; 7 sequences of 3000: 19.5
-// and 14.9; 16 of 2048: 23.8 and 18.8).  GROUPED: 16 rows from a multiple of 16 are neighbours in the pool (pages of a
+// memory, so that there is no second launch (8 KV heads x 4, 1024 rows: 7.7 us on the line, 5.9 so; 7 sequences of 3000: 18.4
+// and 15.1; 16 of 2048: 22.9 and 19.0).  GROUPED: 16 rows from a multiple of 16 are neighbours in the pool (pages of a
 // multiple of 16 rows, or no table), so that a group has one address; otherwise every row has its own.
 template <int D, int NB, int R, int W, int C, bool GROUPED, bool TEAM>
 __global__ void __launch_bounds__(32 * W, C)
@@ -848,8 +848,7 @@ kv8_decode_kernel(const Kv8Args a)
 // The parts of a unit joined, a CTA a query head: groups of D / 4 threads take the parts in turn, four of them in
 // flight, with a softmax each, and are joined in their order.  The first part is what CTA c left, the others are
 // what the CTAs behind it found begun.  T threads: 512 where units have many parts (131072 rows in 57 parts: the call
-// 52.4 us, with 256 threads 52.8, with 128 threads 5 more), 128 where they have few (64 ragged sequences: 182 us, with 512
-// threads 8% more).
+// 51.9 us, with 256 threads 52.3, with 128 52.9), 128 where they have few (64 ragged sequences: 181 us, with 512 threads 210).
 template <int D, int T>
 __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_heads)
 {
@@ -936,9 +935,10 @@ __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_h
 }
 
 // The kernel of a problem: blocks of eight heads a CTA (two share the rows' conversion; at 256 dims their
-// accumulators do not fit), rows a tile, warps, CTAs an SM (what the registers allow).
+// accumulators do not fit), rows a tile, warps, CTAs an SM (what the registers allow: at 128 dims 168 a thread, of which the
+// line's kernel spills 36 bytes, the clusters' 12; 131072 rows take 51.6 us with those 36 bytes, 52.0 with 100 and 51.2 with 8).
 struct Kv8Plan {
-    int nb = 1, n_hb = 1, line = 1;
+    int n_hb = 1, line = 1;
     bool cuts = false;                   // whether a unit can be cut
     int joins = 1;                       // CTAs of the join, in all blocks of heads
     int idle = 0;
@@ -953,7 +953,6 @@ struct Kv8Kind {
     static void plan(const kvq_kv8_problem& p, Kv8Plan& q)
     {
         const int group = p.n_qh / p.cache.n_kv;
-        q.nb = NB;
         q.n_hb = (group + kHb - 1) / kHb;
         // places of the longest unit (a window begins a group ahead of its first row at most)
         const int64_t most = p.window > 0 ? std::min<int64_t>((int64_t)p.window + kGroup - 1, p.max_seq_len) : p.max_seq_len;
