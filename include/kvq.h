@@ -679,7 +679,8 @@ int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* worksp
  * are compared by their logits, those of different beams before they are rounded to fp32: as two
  * floats, within 2^-45 of the largest of score, value and the logarithm (logits of a beam nearer to one
  * another than that may change places).  The logarithm's terms are fp32 exponentials: exp(x_u) is within
- * 2^-20 + 2^-22 (max x - x_u) of itself, so that beams whose values tie may come in either order.
+ * 2^-20 + 2^-22 (max x - x_u) of itself, so that beams whose values tie may come in either order, and a
+ * value may pass its beam's score by as much where a token has all the probability.
  * A value below fp32's range is -inf.  Of each:
  *     out_score   its value
  *     out_token   its token
