@@ -633,8 +633,8 @@ int kvq_append_kv8(const void* k, int64_t k_ld_row, int64_t k_ld_head, const voi
  * weight that multiplies a V row's codes (the row's scale in it) is rounded to binary16 against the largest
  * of its part of the rows: within 2^-11 of itself or, if that is more, 2^-24 of that largest.  A query head
  * that holds a NaN or an infinity gets NaN (if it sees anything), and touches no other head.
- * Nothing on the way to a score or an output overflows unless that does (|sm_scale| up to 2^64); a score above fp32's
- * range makes its head NaN, one below it counts as a row that is not seen.
+ * Nothing on the way to a score or an output overflows unless that does (|sm_scale| up to 2^64).  Scores are meant to
+ * lie within 2^127; one further up makes its head NaN, one further down counts as a row that is not seen.
  * The rows are read once by a part of the grid each, and the parts' results joined in a fixed
  * order: the same call gives the same bits.
  */

@@ -117,17 +117,20 @@ __device__ __forceinline__ float pow2(int k)              // k in [-126, 127]
 }
 
 // What a part of a unit's rows leaves beside its weighted rows: x the reference of its sum, y that sum, z the reference of the
-// weighted rows, references in log2, -inf where there is none.  The rows are joined against their own reference, so that V
-// rows near the ends of fp32 pass no sum, and come to the sum's with the quotient.
+// weighted rows above x, in log2, -inf where there is none.  The rows are joined against their own reference, so that V
+// rows near the ends of fp32 pass no sum, and come to the sum's with the quotient.  z is kept apart from x, whose rounding,
+// where scores are large, would be the outputs'.
 using Level = float4;
 __device__ __forceinline__ float top_of(float m) { return m == -INFINITY ? 0.0f : m; }
 // what a part counts against the reference `base` of sums (a NaN head: no reference, its sum says it)
 __device__ __forceinline__ float part_weight(const Level& x, float base) { return x.y != x.y ? x.y : ex2(x.x - base); }
-// Weighted rows to outputs: 1 / sum, and 2^(z - x), which may pass 2^128 where a reference lags, as two halves.
+// the reference of a part's weighted rows against that base
+__device__ __forceinline__ float rows_level(const Level& x, float base) { return (x.x - base) + x.z; }
+// Weighted rows to outputs: 1 / sum, and 2^z, which may pass 2^128 where a reference lags, as two halves.
 struct Finish {
     float r, half;
     __device__ __forceinline__ Finish(const Level& x)
-        : r(x.y == 0.0f ? 0.0f : 1.0f / x.y), half(x.z == -INFINITY ? 0.0f : ex2(0.5f * (x.z - top_of(x.x))))
+        : r(x.y == 0.0f ? 0.0f : 1.0f / x.y), half(ex2(0.5f * x.z))
     {
     }
     __device__ __forceinline__ float operator()(float o) const { return o * r * half * half; }
@@ -579,9 +582,10 @@ kv8_decode_kernel(const Kv8Args a)
             for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[nb][b][e] = 0.0f;
-        // Two references a head, in log2: ref of the scores, for the sum of exp2(x - ref), and wref of x +
+        // Two references a head, in log2: ref of the scores, for the sum of exp2(x - ref), and above it wref of (x - ref) +
         // log2(vscale), for the weights that multiply V's codes, so that the largest of those is near 1 whatever the
-        // scales.  They move only when something passes them by kSlack; kNone: nothing has yet.
+        // scales, and no rounding of a large score is in a weight.  They move only when something passes them by kSlack;
+        // kNone: nothing has yet.
         float ref[NB][2], wref[NB][2], sum[NB][2];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
@@ -626,12 +630,16 @@ kv8_decode_kernel(const Kv8Args a)
                 }
             const uint32_t now = mask;
             if (i + 1 < my_tiles) load_k(i + 1, next);
+            // whether a reference may have to move: the largest score with the largest V scale stands for all rows
             bool over = false;
+            float top_lv = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kGroups; ++j) top_lv = fmaxf(top_lv, fmaxf(lv[j][0], lv[j][1]));
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    float m = -INFINITY, mw = -INFINITY;
+                    float m = -INFINITY;
 #pragma unroll
                     for (int j = 0; j < kGroups; ++j)
 #pragma unroll
@@ -639,9 +647,9 @@ kv8_decode_kernel(const Kv8Args a)
                             float& y = x[j][nb][2 * h + e];
                             y = y * hs[nb][e] * kf[j][h];
                             m = fmaxf(m, y);
-                            mw = fmaxf(mw, y + lv[j][h]);
                         }
-                    over |= m - kSlack > ref[nb][e] || mw - kSlack > wref[nb][e];
+                    const float u = m - ref[nb][e];
+                    over |= u > kSlack || u + top_lv - wref[nb][e] > kSlack;
                 }
             const bool some = now != ~0u;
             if (__any_sync(kFull, over) || some || wild) {      // (rare after the first tile)
@@ -669,39 +677,55 @@ kv8_decode_kernel(const Kv8Args a)
                                 for (int nb = 0; nb < NB; ++nb) x[j][nb][2 * h] = x[j][nb][2 * h + 1] = -INFINITY;
                             }
                 }
+                // (a head's own scores only: what else brought the warp here must not change the head's bits)
+                float m[NB][2];
+                auto largest = [&]() {                          // over the warp's rows
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) {
+                    for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) m[nb][e] = fmaxf(m[nb][e], __shfl_xor_sync(kFull, m[nb][e], d));
+                };
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float m = -INFINITY, mw = -INFINITY;
+                        m[nb][e] = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < kGroups; ++j) m[nb][e] = fmaxf(m[nb][e], fmaxf(x[j][nb][e], x[j][nb][2 + e]));
+                    }
+                largest();
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float rise = m[nb][e] - ref[nb][e];
+                        if (rise > kSlack) {
+                            sum[nb][e] *= ex2(-rise);
+                            wref[nb][e] = fmaxf(wref[nb][e] - rise, kNone);
+                            ref[nb][e] = m[nb][e];
+                        }
+                        m[nb][e] = -INFINITY;
 #pragma unroll
                         for (int j = 0; j < kGroups; ++j)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                m = fmaxf(m, x[j][nb][2 * h + e]);
-                                mw = fmaxf(mw, x[j][nb][2 * h + e] + lv[j][h]);
-                            }
+                            for (int h = 0; h < 2; ++h) m[nb][e] = fmaxf(m[nb][e], (x[j][nb][2 * h + e] - ref[nb][e]) + lv[j][h]);
+                    }
+                largest();
 #pragma unroll
-                        for (int d = 4; d < 32; d <<= 1) {
-                            m = fmaxf(m, __shfl_xor_sync(kFull, m, d));
-                            mw = fmaxf(mw, __shfl_xor_sync(kFull, mw, d));
-                        }
-                        // (a head's own scores only: what else brought the warp here must not change the head's bits)
-                        if (m - kSlack > ref[nb][e]) {
-                            sum[nb][e] *= ex2(ref[nb][e] - m);
-                            ref[nb][e] = m;
-                        }
-                        if (mw - kSlack > wref[nb][e]) {
-                            const float f = ex2(wref[nb][e] - mw);
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        if (m[nb][e] - wref[nb][e] > kSlack) {
+                            const float f = ex2(wref[nb][e] - m[nb][e]);
 #pragma unroll
                             for (int b = 0; b < kBlocks; ++b) {
                                 o[nb][b][e] *= f;
                                 o[nb][b][e + 2] *= f;
                             }
-                            wref[nb][e] = mw;
+                            wref[nb][e] = m[nb][e];
                         }
-                    }
-                }
             }
             uint32_t w[kGroups][NB][2];
 #pragma unroll
@@ -710,10 +734,10 @@ kv8_decode_kernel(const Kv8Args a)
                 for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float x0 = x[j][nb][2 * h], x1 = x[j][nb][2 * h + 1];
-                        sum[nb][0] += ex2(x0 - ref[nb][0]);
-                        sum[nb][1] += ex2(x1 - ref[nb][1]);
-                        w[j][nb][h] = transpose8(pack_h2(ex2(x0 + lv[j][h] - wref[nb][0]), ex2(x1 + lv[j][h] - wref[nb][1])));
+                        const float u0 = x[j][nb][2 * h] - ref[nb][0], u1 = x[j][nb][2 * h + 1] - ref[nb][1];
+                        sum[nb][0] += ex2(u0);
+                        sum[nb][1] += ex2(u1);
+                        w[j][nb][h] = transpose8(pack_h2(ex2(u0 + lv[j][h] - wref[nb][0]), ex2(u1 + lv[j][h] - wref[nb][1])));
                     }
             // context: block b of a lane is its dims 2 b and 2 b + 1 of the pieces
 #pragma unroll
@@ -767,11 +791,11 @@ kv8_decode_kernel(const Kv8Args a)
             const int h = i / (D / 4), d = i % (D / 4) * 4;
             Level all = make_float4(-INFINITY, 0.0f, -INFINITY, 0.0f);
 #pragma unroll
-            for (int w = 0; w < W; ++w) {
-                all.x = fmaxf(all.x, ml[w * Sh::kHb + h].x);
-                all.z = fmaxf(all.z, ml[w * Sh::kHb + h].z);
-            }
-            const float base = top_of(all.x), rows_base = top_of(all.z);
+            for (int w = 0; w < W; ++w) all.x = fmaxf(all.x, ml[w * Sh::kHb + h].x);
+            const float base = top_of(all.x);
+#pragma unroll
+            for (int w = 0; w < W; ++w) all.z = fmaxf(all.z, rows_level(ml[w * Sh::kHb + h], base));
+            const float rows_base = top_of(all.z);
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int w = 0; w < W; ++w) {
@@ -779,7 +803,7 @@ kv8_decode_kernel(const Kv8Args a)
                 const float2 y0 = *reinterpret_cast<const float2*>(mo + w * Sh::kHb * Sh::kStride + Sh::place(h, d));
                 const float2 y1 = *reinterpret_cast<const float2*>(mo + w * Sh::kHb * Sh::kStride + Sh::place(h, d + 2));
                 all.y = fmaf(x.y, part_weight(x, base), all.y);
-                add_rows(acc, make_float4(y0.x, y0.y, y1.x, y1.y), ex2(x.z - rows_base));
+                add_rows(acc, make_float4(y0.x, y0.y, y1.x, y1.y), ex2(rows_level(x, base) - rows_base));
             }
             const int64_t row = head0 + h;
             if constexpr (TEAM) {
@@ -814,16 +838,19 @@ kv8_decode_kernel(const Kv8Args a)
                     x[k] = *team.map_shared_rank(tl + h, k);
                     y[k] = *reinterpret_cast<const float4*>(team.map_shared_rank(to, k) + h * D + d);
                     all.x = fmaxf(all.x, x[k].x);
-                    all.z = fmaxf(all.z, x[k].z);
                 }
             }
-            const float base = top_of(all.x), rows_base = top_of(all.z);
+            const float base = top_of(all.x);
+#pragma unroll
+            for (int k = 0; k < kTeam; ++k)
+                if (k < a.team) all.z = fmaxf(all.z, rows_level(x[k], base));
+            const float rows_base = top_of(all.z);
             float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
             for (int k = 0; k < kTeam; ++k) {
                 if (k < a.team) {
                     all.y = fmaf(x[k].y, part_weight(x[k], base), all.y);
-                    add_rows(acc, y[k], ex2(x[k].z - rows_base));
+                    add_rows(acc, y[k], ex2(rows_level(x[k], base) - rows_base));
                 }
             }
             Finish(all).store(a.out + (head0 + h) * D + d, acc);
@@ -894,17 +921,18 @@ __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_h
                                      : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
                     }
 #pragma unroll
-                    for (int u = 0; u < kFlight; ++u) {
-                        all.x = fmaxf(all.x, x[u].x);
-                        all.z = fmaxf(all.z, x[u].z);
-                    }
-                    const float base = top_of(all.x), rows_base = top_of(all.z), f0 = ex2(was.z - rows_base);
+                    for (int u = 0; u < kFlight; ++u) all.x = fmaxf(all.x, x[u].x);
+                    const float base = top_of(all.x);
+                    all.z = rows_level(was, base);
+#pragma unroll
+                    for (int u = 0; u < kFlight; ++u) all.z = fmaxf(all.z, rows_level(x[u], base));
+                    const float rows_base = top_of(all.z), f0 = ex2(rows_level(was, base) - rows_base);
                     all.y *= ex2(was.x - base);
                     acc = make_float4(acc.x * f0, acc.y * f0, acc.z * f0, acc.w * f0);
 #pragma unroll
                     for (int u = 0; u < kFlight; ++u) {
                         all.y = fmaf(x[u].y, part_weight(x[u], base), all.y);
-                        add_rows(acc, y[u], ex2(x[u].z - rows_base));
+                        add_rows(acc, y[u], ex2(rows_level(x[u], base) - rows_base));
                     }
                 }
                 __syncthreads();                            // (the last unit is written)
@@ -913,18 +941,19 @@ __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_h
                 __syncthreads();
                 if (grp != 0) continue;
 #pragma unroll
-                for (int g = 1; g < kJoin; ++g) {
-                    all.x = fmaxf(all.x, s_ml[g].x);
-                    all.z = fmaxf(all.z, s_ml[g].z);
-                }
-                const float base = top_of(all.x), rows_base = top_of(all.z);
+                for (int g = 1; g < kJoin; ++g) all.x = fmaxf(all.x, s_ml[g].x);
+                const float base = top_of(all.x);
+                all.z = -INFINITY;
+#pragma unroll
+                for (int g = 0; g < kJoin; ++g) all.z = fmaxf(all.z, rows_level(s_ml[g], base));
+                const float rows_base = top_of(all.z);
                 all.y = 0.0f;
                 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int g = 0; g < kJoin; ++g) {
                     const Level x = s_ml[g];
                     all.y = fmaf(x.y, part_weight(x, base), all.y);
-                    add_rows(acc, *reinterpret_cast<const float4*>(&s_o[g][d]), ex2(x.z - rows_base));
+                    add_rows(acc, *reinterpret_cast<const float4*>(&s_o[g][d]), ex2(rows_level(x, base) - rows_base));
                 }
                 const int64_t row = (int64_t)unit.x * p.n_qh + unit.y * a.group + hb * n_heads + h;
                 Finish(all).store(a.out + row * D + d, acc);

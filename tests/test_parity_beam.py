@@ -436,6 +436,28 @@ def test_decode_value_ranges(kvq, d, lens, vs):
     check_decode(out, lse, decode_ref(c.pl, q, lens, c.rows_of, 0, 1 / math.sqrt(d)), d, 32)
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens", [[1, 3], [900, 17], [40000, 300]])
+def test_decode_equal_scores_of_any_size(kvq, d, lens):
+    """Rows of one K, whose scores are equal to the last bit: the output is the mean of V however large the scores are."""
+    c = Cache(lens, 2, d, 64, 130, spread=2.0)
+    rows = torch.from_numpy(np.concatenate([c.rows_of(s, np.arange(L)) for s, L in enumerate(lens)])).cuda()
+    for name in ("k", "k_scale"):
+        c.pl[name][:, rows] = c.pl[name][:, rows[:1]]
+    for size in (1.0, 1e3, 1e5, 1e7, 1e10, 1e20, 1e30, 1e36):
+        q = queries(2, 6, d, 131, size)
+        out, lse = decode(kvq, c.problem(kvq, q))
+        o, l, _, mass = decode_ref(c.pl, torch.zeros_like(q), lens, c.rows_of, 0, 1.0)
+        # weights: 2^-11 of each, or 2^-25 of the largest; 2^-20 for exponentials, sums and scales; the output's bfloat16
+        bar = (2.0**-11 + 2.0**-20) * mass + 4096 * 2.0**-25 * mass.amax(2, keepdim=True)
+        bar = bar + 2.0**-8 * (o.abs() + bar)
+        assert bool(((out.double() - o).abs() <= bar).all()), (size, float(((out.double() - o).abs() / bar).max()))
+        x = (q.double().view(2, 2, 3, d) * values(c.pl, "k", rows[:1]).view(1, 2, 1, d)).sum(3).view(2, 6) / math.sqrt(d)
+        n = torch.tensor(lens, dtype=torch.float64, device="cuda").log()[:, None]
+        size_of = (q.double().abs().view(2, 2, 3, d) * values(c.pl, "k", rows[:1]).abs().view(1, 2, 1, d)).sum(3).view(2, 6) / math.sqrt(d)
+        assert bool(((lse.double() - x - n).abs() <= (d + 8) * 2.0**-23 * size_of + 2.0**-22 * (x + n).abs() + 2.0**-20).all()), size
+
+
 @pytest.mark.parametrize("d,lens", [(64, [900, 17]), (128, [900, 17]), (128, [20000, 300]), (256, [5000, 1])])
 def test_decode_heads_of_every_size(kvq, d, lens):
     """Heads of one KV head whose queries are 2^250 apart, one of them zero."""
