@@ -221,8 +221,8 @@ struct Kv8Shape {
     static constexpr int kStride = D == 64 ? D : D + 4;     // of a head's weighted rows
     static constexpr int kSmem = (W * (kStride + 4) + D + 4) * kHb * 4;
     // Where dims d, d + 1 of head h are in those: pairs turn within 16 dims by the 16's number, or (64 dims) within 8 by the
-    // head's, so that the lanes that write together meet no bank twice (131072 rows: 53.3 us with the rows as they are, 51.9
-    // so; 64 ragged sequences 184.2 and 180.8)
+    // head's, so that the lanes that write together meet no bank twice (16 sequences of 1024 rows: 13.1 us with the rows as
+    // they are, 12.9 so; 7 of 3000 15.2 and 14.9)
     static __device__ __forceinline__ int place(int h, int d)
     {
         return D == 64 ? h * kStride + (d & ~7) + 2 * ((d / 2 + h / 2) & 3) : h * kStride + (d & ~15) + 2 * ((d / 2 + d / 16) & 7);
@@ -232,8 +232,8 @@ struct Kv8Shape {
 // One CTA: a stretch of the line for one block of up to 8 NB query heads of the KV heads on it.  In each unit its
 // warps take the tiles in turn, each with a softmax of its own, and are joined at the end.  TEAM: units are short; each
 // one has a cluster of a.team CTAs, which take team_rows of its rows each and join their results through shared
-// memory, so that there is no second launch (8 KV heads x 4, 1024 rows: 7.7 us on the line, 5.9 so; 7 sequences of 3000: 18.4
-// and 15.1; 16 of 2048: 22.9 and 19.0).  GROUPED: 16 rows from a multiple of 16 are neighbours in the pool (pages of a
+// memory, so that there is no second launch (8 KV heads x 4, 1024 rows: 7.6 us on the line, 5.9 so; 7 sequences of 3000: 18.3
+// and 14.9; 16 of 2048: 22.4 and 18.9).  GROUPED: 16 rows from a multiple of 16 are neighbours in the pool (pages of a
 // multiple of 16 rows, or no table), so that a group has one address; otherwise every row has its own.
 template <int D, int NB, int R, int W, int C, bool GROUPED, bool TEAM>
 __global__ void __launch_bounds__(32 * W, C)
@@ -875,7 +875,7 @@ kv8_decode_kernel(const Kv8Args a)
 // The parts of a unit joined, a CTA a query head: groups of D / 4 threads take the parts in turn, four of them in
 // flight, with a softmax each, and are joined in their order.  The first part is what CTA c left, the others are
 // what the CTAs behind it found begun.  T threads: 512 where units have many parts (131072 rows in 57 parts: the call
-// 51.9 us, with 256 threads 52.3, with 128 52.9), 128 where they have few (64 ragged sequences: 181 us, with 512 threads 210).
+// 51.6 us, with 256 threads 51.5, with 128 52.8), 128 where they have few (64 ragged sequences: 182 us, with 512 threads 211).
 template <int D, int T>
 __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_heads)
 {
@@ -964,8 +964,8 @@ __global__ void __launch_bounds__(T) kv8_combine_kernel(const Kv8Args a, int n_h
 }
 
 // The kernel of a problem: blocks of eight heads a CTA (two share the rows' conversion; at 256 dims their
-// accumulators do not fit), rows a tile, warps, CTAs an SM (what the registers allow: at 128 dims 168 a thread, of which the
-// line's kernel spills 36 bytes, the clusters' 12; 131072 rows take 51.6 us with those 36 bytes, 52.0 with 100 and 51.2 with 8).
+// accumulators do not fit), rows a tile, warps, CTAs an SM (what the registers allow: at 128 dims 168 a thread, and 16
+// bytes spilled by the line's kernel; when that spilled 100, 131072 rows took 0.8 us more).
 struct Kv8Plan {
     int n_hb = 1, line = 1;
     bool cuts = false;                   // whether a unit can be cut

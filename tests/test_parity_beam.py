@@ -472,6 +472,29 @@ def test_decode_heads_of_every_size(kvq, d, lens):
     assert torch.equal(out[:, one], out2[:, one]) and torch.equal(lse[:, one], lse2[:, one])
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("lens,page", [([900, 0, 17], 16), ([20000, 300, 1], 64), ([3000, 2], 20)])
+def test_decode_extremes_of_many_heads(kvq, d, lens, page):
+    """Twelve heads a KV head (two blocks of eight): queries of every size, infinities and NaNs, V rows near fp32's largest."""
+    c = Cache(lens, 2, d, page, 140, spread=0.5)
+    c.pl["v_scale"] *= 1e36
+    n = len(lens)
+    size = torch.tensor([1.0, 1e-39, 1e20, 0.0, 1.0, 1e37, 1e-30, 1.0, 1e-38, 1.0, 1e37, 1.0], device="cuda").repeat(2)
+    q = (queries(n, 24, d, 141).float() * size[:, None]).bfloat16()
+    clean, lse0 = decode(kvq, c.problem(kvq, q))
+    assert bool(clean.isfinite().all())
+    check_decode(clean, lse0, decode_ref(c.pl, q, lens, c.rows_of, 0, 1 / math.sqrt(d)), d, 32)
+    bad = q.clone()
+    bad[:, 4, 3], bad[:, 11, 0], bad[:, 21, d - 1] = math.inf, -math.inf, float("nan")
+    hit = torch.zeros(24, dtype=torch.bool, device="cuda")
+    hit[[4, 11, 21]] = True
+    out, lse = decode(kvq, c.problem(kvq, bad))
+    sees = dev(np.asarray(lens) > 0)
+    assert bool(out[sees][:, hit].isnan().all()) and bool(lse[sees][:, hit].isnan().all())
+    assert bool((out[~sees] == 0).all()) and bool((lse[~sees] == -math.inf).all())
+    assert torch.equal(out[:, ~hit], clean[:, ~hit]) and torch.equal(lse[:, ~hit], lse0[:, ~hit])
+
+
 def test_decode_many_small_weights(kvq):
     """One row takes most of the softmax, and 50000 rows far below it hold the rest together."""
     L, d = 50001, 64
