@@ -678,9 +678,9 @@ int kvq_kv8_decode(const kvq_kv8_problem* p, void* out, float* lse, void* worksp
  * values are written in descending order, equal ones by ascending (beam, token); values of one beam
  * are compared by their logits, those of different beams before they are rounded to fp32: as two
  * floats, within 2^-45 of the largest of score, value and the logarithm (logits of a beam nearer to one
- * another than that may change places).  The logarithm's terms are fp32 exponentials: exp(x_u) is within
- * 2^-20 + 2^-22 (max x - x_u) of itself, so that beams whose values tie may come in either order, and a
- * value may pass its beam's score by as much where a token has all the probability.
+ * another than that may change places).  The logarithm's terms but for the largest are fp32 exponentials:
+ * exp(x_u) is within 2^-20 + 2^-22 (max x - x_u) of itself, so that beams of different logits whose values tie
+ * may come in either order.  A beam with one token left keeps its score.
  * A value below fp32's range is -inf.  Of each:
  *     out_score   its value
  *     out_token   its token

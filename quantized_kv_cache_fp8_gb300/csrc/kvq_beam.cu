@@ -5,7 +5,7 @@
 // exponentials and its n_out best tokens; a second kernel, a CTA a request, joins the chunks' sums to each beam's
 // logarithm and picks the n_out best of all chunks' candidates.  The logits' bytes are the floor, and an exponential
 // takes 0.7 of the time of a bfloat16's two.  512 rows of 128000 bfloat16, 16 of each request's 8 beams kept, take
-// 40.0 us (34 the chunks, the join the rest) against 19 for the bytes: a warp spends 940 instructions on a chunk, 65% of the
+// 40.2 us (35 the chunks, the join the rest) against 19 for the bytes: a warp spends 940 instructions on a chunk, 65% of the
 // issue slots; the rest goes to waits for a chunk's loads and between its barriers, with half of the SM's warps (64
 // registers) to fill them.
 //
@@ -379,10 +379,15 @@ __global__ void __launch_bounds__(kThreads, 4) beam_chunk_kernel(const BeamArgs 
             float all = mw;
 #pragma unroll
             for (int o = 16; o >= 1; o >>= 1) all = fmaxf(all, __shfl_xor_sync(kFull, all, o));
-            // The rounding of c in nats is exact as a fused multiply-add but for its last factor.  It is below 2^-11, so its
-            // exponential is its series (to 2^-35).
-            const float off = fabsf(mw) < kLarge ? -0.6931471805599453f * fmaf(mw, kLog2e, -__fmul_rn(mw, kLog2e)) : 0.0f;
-            sw.y = fmaf(sw.x, off * fmaf(0.5f, off, 1.0f), sw.y);
+            // What the rounding of c took is exact as a fused multiply-add.  It is below 2^-11 in nats, so its exponential is its
+            // series (to 2^-35).  The largest term is 1: it is taken out as the instruction gave it and put back, so that
+            // a beam with one token left has a sum of 1.
+            if (fabsf(mw) < kLarge) {
+                const float r = fmaf(mw, kLog2e, -__fmul_rn(mw, kLog2e)), off = -0.6931471805599453f * r;
+                add_exact(sw.x, sw.y, -ex2(r));
+                sw.y = fmaf(sw.x, off * fmaf(0.5f, off, 1.0f), sw.y);
+                add_exact(sw.x, sw.y, 1.0f);
+            }
             float t = 0.0f, lo = 0.0f;
             // (a sum of 0 has no maximum; that of the maximum's warp stays as it is)
             if (sw.x != 0.0f) add_scaled(t, lo, sw, mw == all ? 1.0f : expf(mw - all));

@@ -891,6 +891,26 @@ def test_select_sum_of_a_far_tail(kvq, V, level):
         assert abs(out.item() + math.log1p(tail)) <= bar, far
 
 
+@pytest.mark.parametrize("V", [1, 3000, 70000])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_select_forced_tokens(kvq, V, bf16):
+    """Beams with one token left: its value is the score, to the last bit, and equal ones come in the order of the beams."""
+    g = np.random.default_rng(V)
+    R, B = 40, 8
+    x = torch.full((R, B, V), -math.inf, device="cuda")
+    token = torch.from_numpy(g.integers(0, V, (R, B, 1))).cuda()
+    level = torch.from_numpy((g.standard_normal((R, B, 1)) * np.exp(g.uniform(-5, 12, (R, B, 1)))).astype(np.float32)).cuda()
+    x.scatter_(2, token, level)
+    x = x.bfloat16() if bf16 else x
+    score = (-20 * g.random((R, B))).astype(np.float32)
+    score[:R // 2] = score[:R // 2, :1]
+    (out, tok, parent, _), st = select(kvq, x, dev(score), None, B, eos=-1)
+    order = np.argsort(-score, axis=1, kind="stable")
+    assert st == 0 and np.array_equal(host(out), np.take_along_axis(score, order, 1))
+    assert np.array_equal(host(parent), order + np.arange(R)[:, None] * B)
+    assert np.array_equal(host(tok), np.take_along_axis(host(token)[..., 0], order, 1))
+
+
 def test_select_beams_at_different_levels(kvq):
     """Constant rows at levels far apart, whose values tie exactly: beams in either order (their sums are of fp32
     exponentials), each beam's tokens from its lowest on."""
